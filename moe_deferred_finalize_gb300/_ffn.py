@@ -1,0 +1,333 @@
+"""Binding of include/moe_ffn.h: the matrix products around the finalize.
+
+Argument marshalling only, as in ``_abi``: shape and dtype checks, output and
+workspace allocation through torch, the current CUDA stream, status ->
+exception.  Every step runs in the library's CUDA kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _abi
+from ._abi import MoefError, _check, _on, _ptr, _stream
+
+ACTIVATION = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
+
+_BF16 = (torch.bfloat16,)
+_I32 = (torch.int32,)
+_OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+_LIB = None
+
+
+def _lib():
+    global _LIB
+    if _LIB is None:
+        lib = _abi._lib()
+        vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+        signatures = {
+            "moe_linear": (i32, [vp] * 4 + [i32, vp, i32, vp, i32, i32, i32, vp]),
+            "moe_linear_backward": (i32, [vp] * 3 + [i32] + [vp] * 4 + [i32] * 3 + [vp, sz, vp]),
+            "moe_linear_backward_workspace_bytes": (sz, [i32, i32]),
+            "moe_gated_ffn": (i32, [vp] * 3 + [i32, vp, vp, i32, i32, i32, vp]),
+            "moe_gated_ffn_backward": (i32,
+                                       [vp] * 3 + [i32] + [vp] * 4 + [i32] * 3 + [vp, sz, vp]),
+            "moe_gated_ffn_backward_workspace_bytes": (sz, [i32, i32]),
+            "moe_permute_rows": (i64, [i32] * 4),
+            "moe_permute_workspace_bytes": (sz, [i32] * 3),
+            "moe_permute": (i32, [vp] + [i32] * 4 + [vp, vp, i64, vp, vp, vp, sz, vp]),
+            "moe_expert_gated_ffn": (i32, [vp, i64] + [vp] * 5 + [i32, vp, i64, i32, i32, i32,
+                                                                  vp]),
+            "moe_expert_linear": (i32, [vp, i64] + [vp] * 5 + [i32, vp, i64, i32, i32, i32, vp]),
+        }
+        for name, (restype, argtypes) in signatures.items():
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = restype, argtypes
+        _LIB = lib
+    return _LIB
+
+
+def _activation(name):
+    if name not in ACTIVATION:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATION)}")
+    return ACTIVATION[name]
+
+
+def _matrix(t, name, what):
+    """The shape of a 2-D CUDA tensor argument that fixes a call's device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda" or t.dim() != 2:
+        raise ValueError(f"{name} is a CUDA {what} tensor")
+    return t.shape
+
+
+def _output(t, name, dtype, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, (dtype,), shape, device)
+    return t
+
+
+def _optional(t, name, shape, device):
+    if t is not None:
+        _check(t, name, _BF16, shape, device)
+
+
+def _raise(status, where):
+    if status != 0:
+        raise MoefError(status, where)
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+           residual: Optional[torch.Tensor] = None, activation: str = "none",
+           out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+           save_preact: bool = False, preact: Optional[torch.Tensor] = None,
+           stream=None) -> dict:
+    """act(x weight^T + bias) + residual in one kernel (include/moe_ffn.h).
+
+    x bf16 [T, K]; weight bf16 [N, K]; bias bf16 [N]; residual bf16 [T, N].
+    ``activation``: "none", "silu", "gelu", "gelu_tanh" or "relu".  Returns a
+    dict with "out" [T, N] (``out_dtype`` bfloat16 or float32; a given bf16
+    ``out`` may be the residual) and, with ``save_preact`` or a given
+    ``preact``, "preact" bf16 [T, N] (x weight^T + bias, for
+    ``linear_backward``).  Enqueued on the current stream (or ``stream``)."""
+    T, K = _matrix(x, "x", "[T, K]")
+    N = _matrix(weight, "weight", "[N, K]")[0]
+    dev = x.device
+    act = _activation(activation)
+    _check(x, "x", _BF16, (T, K), dev)
+    _check(weight, "weight", _BF16, (N, K), dev)
+    _optional(bias, "bias", (N,), dev)
+    _optional(residual, "residual", (T, N), dev)
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _OUT_TYPE:
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    out = _output(out, "out", out_dtype, (T, N), dev)
+    res = {"out": out}
+    if save_preact or preact is not None:
+        res["preact"] = preact = _output(preact, "preact", torch.bfloat16, (T, N), dev)
+    with _on(dev):
+        st = _lib().moe_linear(_ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), act, _ptr(out),
+                               _OUT_TYPE[out_dtype], _ptr(preact), T, N, K, _stream(stream, dev))
+    _raise(st, "moe_linear")
+    return res
+
+
+def _backward(where, gated, dout, x, weight, preact, activation, want_dx, want_dweight,
+              want_dbias, dx, dweight, dbias, workspace, stream):
+    T, n = _matrix(dout, "dout", "[T, features]")
+    dev = dout.device
+    K = _matrix(x, "x", "[T, inputs]")[1]
+    act = _activation(activation)
+    cols = 2 * n if gated else n
+    _check(dout, "dout", _BF16, (T, n), dev)
+    _check(x, "x", _BF16, (T, K), dev)
+    _check(weight, "weight", _BF16, (cols, K), dev)
+    if preact is None:
+        if gated or act != 0:
+            raise ValueError("preact is needed for the activation's derivative")
+    else:
+        _check(preact, "preact", _BF16, (T, cols), dev)
+        if not gated and act == 0:
+            preact = None       # the derivative is 1
+    res = {}
+    for name, want, t, shape in (("dx", want_dx, dx, (T, K)),
+                                 ("dweight", want_dweight, dweight, (cols, K)),
+                                 ("dbias", want_dbias, dbias, (cols,))):
+        if want or t is not None:
+            res[name] = _output(t, name, torch.bfloat16, shape, dev)
+    if not res:
+        raise ValueError("no gradient is wanted")
+    lib = _lib()
+    size = lib.moe_gated_ffn_backward_workspace_bytes if gated \
+        else lib.moe_linear_backward_workspace_bytes
+    need = int(size(T, n))
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same device")
+    nbytes = workspace.numel() * workspace.element_size()
+    fn = lib.moe_gated_ffn_backward if gated else lib.moe_linear_backward
+    with _on(dev):
+        st = fn(_ptr(dout), _ptr(x), _ptr(weight), act, _ptr(preact), _ptr(res.get("dx")),
+                _ptr(res.get("dweight")), _ptr(res.get("dbias")), T, n, K, _ptr(workspace),
+                nbytes, _stream(stream, dev))
+    _raise(st, where)
+    return res
+
+
+def linear_backward_workspace_bytes(T: int, N: int) -> int:
+    """Bytes of workspace linear_backward needs for T rows of N features."""
+    return int(_lib().moe_linear_backward_workspace_bytes(int(T), int(N)))
+
+
+def linear_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *,
+                    activation: str = "none", preact: Optional[torch.Tensor] = None,
+                    want_dx: bool = True, want_dweight: bool = True, want_dbias: bool = False,
+                    dx: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+                    dbias: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of ``linear`` for dout bf16 [T, N]: the requested of "dx"
+    bf16 [T, K], "dweight" bf16 [N, K] and "dbias" bf16 [N].  ``preact``:
+    what the forward call saved, needed unless the activation is "none".
+    The gradient of the residual is ``dout`` itself.  ``workspace``: at least
+    ``linear_backward_workspace_bytes`` bytes, allocated when not given."""
+    return _backward("moe_linear_backward", False, dout, x, weight, preact, activation, want_dx,
+                     want_dweight, want_dbias, dx, dweight, dbias, workspace, stream)
+
+
+def gated_ffn(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+              activation: str = "silu", out: Optional[torch.Tensor] = None,
+              save_preact: bool = False, preact: Optional[torch.Tensor] = None,
+              stream=None) -> dict:
+    """act(x Wg^T + bg) * (x Wu^T + bu) in one kernel (include/moe_ffn.h).
+
+    x bf16 [T, H]; weight bf16 [2I, H], the I gate rows and then the I up
+    rows; bias bf16 [2I].  Returns a dict with "out" bf16 [T, I] and, with
+    ``save_preact`` or a given ``preact``, "preact" bf16 [T, 2I] (both
+    projections with their bias, for ``gated_ffn_backward``)."""
+    T, H = _matrix(x, "x", "[T, H]")
+    rows = _matrix(weight, "weight", "[2I, H]")[0]
+    if rows % 2:
+        raise ValueError("weight is [2I, H]: the gate rows, then the up rows")
+    I = rows // 2
+    dev = x.device
+    act = _activation(activation)
+    _check(x, "x", _BF16, (T, H), dev)
+    _check(weight, "weight", _BF16, (rows, H), dev)
+    _optional(bias, "bias", (rows,), dev)
+    out = _output(out, "out", torch.bfloat16, (T, I), dev)
+    res = {"out": out}
+    if save_preact or preact is not None:
+        res["preact"] = preact = _output(preact, "preact", torch.bfloat16, (T, rows), dev)
+    with _on(dev):
+        st = _lib().moe_gated_ffn(_ptr(x), _ptr(weight), _ptr(bias), act, _ptr(out),
+                                  _ptr(preact), T, I, H, _stream(stream, dev))
+    _raise(st, "moe_gated_ffn")
+    return res
+
+
+def gated_ffn_backward_workspace_bytes(T: int, I: int) -> int:
+    """Bytes of workspace gated_ffn_backward needs for T rows of I features."""
+    return int(_lib().moe_gated_ffn_backward_workspace_bytes(int(T), int(I)))
+
+
+def gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                       preact: torch.Tensor, *, activation: str = "silu", want_dx: bool = True,
+                       want_dweight: bool = True, want_dbias: bool = False,
+                       dx: Optional[torch.Tensor] = None,
+                       dweight: Optional[torch.Tensor] = None,
+                       dbias: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of ``gated_ffn`` for dout bf16 [T, I] and the saved preact
+    bf16 [T, 2I]: the requested of "dx" bf16 [T, H], "dweight" bf16 [2I, H]
+    and "dbias" bf16 [2I].  ``workspace``: at least
+    ``gated_ffn_backward_workspace_bytes`` bytes, allocated when not given."""
+    return _backward("moe_gated_ffn_backward", True, dout, x, weight, preact, activation,
+                     want_dx, want_dweight, want_dbias, dx, dweight, dbias, workspace, stream)
+
+
+def permute_rows(T: int, K: int, E: int, tile: int) -> int:
+    """The most rows the grouped layout of T x K slots over E experts can need."""
+    return int(_lib().moe_permute_rows(int(T), int(K), int(E), int(tile)))
+
+
+def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
+                   row_token: Optional[torch.Tensor] = None,
+                   idx_map: Optional[torch.Tensor] = None,
+                   offsets: Optional[torch.Tensor] = None,
+                   counts: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """The padded, expert-grouped layout of expert ids int32 [T, K]
+    (include/moe_ffn.h): "idx_map" int32 [T, K] for ``moe_finalize``,
+    "row_token" int32 [P] (-1 on padding; P = ``permute_rows`` unless given),
+    "offsets" int32 [E + 1] and "counts" int32 [E].  Ids outside [0, E) get
+    no row (idx_map -1)."""
+    T, K = _matrix(expert_ids, "expert_ids", "[T, K]")
+    dev = expert_ids.device
+    E, tile = int(E), int(tile)
+    _check(expert_ids, "expert_ids", _I32, (T, K), dev)
+    lib = _lib()
+    if row_token is None:
+        P = int(lib.moe_permute_rows(T, K, E, tile))
+        row_token = torch.empty(P, dtype=torch.int32, device=dev)
+    else:
+        P = row_token.numel()
+    _check(row_token, "row_token", _I32, (P,), dev)
+    res = {"idx_map": _output(idx_map, "idx_map", torch.int32, (T, K), dev),
+           "row_token": row_token,
+           "offsets": _output(offsets, "offsets", torch.int32, (max(E, 0) + 1,), dev),
+           "counts": _output(counts, "counts", torch.int32, (max(E, 0),), dev)}
+    if workspace is None:
+        need = int(lib.moe_permute_workspace_bytes(T, K, E))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same device")
+    nbytes = workspace.numel() * workspace.element_size()
+    with _on(dev):
+        st = lib.moe_permute(_ptr(expert_ids), T, K, E, tile, _ptr(res["idx_map"]),
+                             _ptr(row_token), P, _ptr(res["offsets"]), _ptr(res["counts"]),
+                             _ptr(workspace), nbytes, _stream(stream, dev))
+    _raise(st, "moe_permute")
+    return res
+
+
+def _expert(where, gated, x, row_token, offsets, counts, weight, bias, activation, out, stream):
+    T, K = _matrix(x, "x", "[T, inputs]")
+    dev = x.device
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 3:
+        raise ValueError("weight is a CUDA [E, features, inputs] tensor")
+    E, rows = weight.shape[:2]
+    if gated and rows % 2:
+        raise ValueError("weight is [E, 2I, H]: the gate rows, then the up rows")
+    M = rows // 2 if gated else rows
+    act = _activation(activation)
+    _check(x, "x", _BF16, (T, K), dev)
+    _check(weight, "weight", _BF16, (E, rows, K), dev)
+    _check(offsets, "offsets", _I32, (E + 1,), dev)
+    _check(counts, "counts", _I32, (E,), dev)
+    _optional(bias, "bias", (E, rows), dev)
+    P = T
+    if row_token is not None:
+        P = row_token.numel()
+        _check(row_token, "row_token", _I32, (P,), dev)
+    out = _output(out, "out", torch.bfloat16, (P, M), dev)
+    fn = _lib().moe_expert_gated_ffn if gated else _lib().moe_expert_linear
+    with _on(dev):
+        st = fn(_ptr(x), T, _ptr(row_token), _ptr(offsets), _ptr(counts), _ptr(weight),
+                _ptr(bias), act, _ptr(out), P, E, M, K, _stream(stream, dev))
+    _raise(st, where)
+    return out
+
+
+def expert_gated_ffn(x: torch.Tensor, row_token: Optional[torch.Tensor], offsets: torch.Tensor,
+                     counts: torch.Tensor, weight: torch.Tensor, *,
+                     bias: Optional[torch.Tensor] = None, activation: str = "silu",
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``gated_ffn`` over rows grouped by expert (include/moe_ffn.h): out
+    bf16 [P, I], row r of expert e from x row ``row_token[r]`` (row r itself
+    with ``row_token=None``) and weight[e].
+
+    x bf16 [T, H]; row_token int32 [P], offsets int32 [E + 1] and counts int32
+    [E] as from ``permute_tokens``; weight bf16 [E, 2I, H]; bias bf16 [E, 2I].
+    Rows of no expert are left as they were (unset when ``out`` is allocated
+    here)."""
+    return _expert("moe_expert_gated_ffn", True, x, row_token, offsets, counts, weight, bias,
+                   activation, out, stream)
+
+
+def expert_linear(x: torch.Tensor, offsets: torch.Tensor, counts: torch.Tensor,
+                  weight: torch.Tensor, *, row_token: Optional[torch.Tensor] = None,
+                  bias: Optional[torch.Tensor] = None, activation: str = "none",
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """act(x weight[e]^T + bias[e]) over rows grouped by expert: out bf16
+    [P, N], the ``permuted_out`` of ``moe_finalize``.  x bf16 [P, K] in the
+    layout itself, or [T, K] with ``row_token``; weight bf16 [E, N, K]; bias
+    bf16 [E, N].  Otherwise as ``expert_gated_ffn``."""
+    return _expert("moe_expert_linear", False, x, row_token, offsets, counts, weight, bias,
+                   activation, out, stream)

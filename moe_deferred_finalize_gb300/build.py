@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_finalize.so")
-SOURCES = ["finalize.cu", "allreduce.cu", "unfused.cu", "routing.cu", "api.cu", "noalloc.cu"]
+SOURCES = ["finalize.cu", "allreduce.cu", "unfused.cu", "routing.cu", "api.cu", "noalloc.cu",
+           "ffn_simple.cu", "ffn_backward.cu", "permute.cu", "ffn_api.cu"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3",
               "-std=c++17", "-Xcompiler", "-fPIC,-O2,-Wall", "-I", INCLUDE, "-I", CSRC]
@@ -29,7 +30,7 @@ def _nvcc():
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "moe_finalize.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

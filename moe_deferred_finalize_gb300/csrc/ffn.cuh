@@ -1,0 +1,106 @@
+// Declarations shared by the translation units of the matrix products around
+// the finalize (moe_ffn.h): the description of one product, the activations
+// and the launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_ffn.h"
+
+namespace moef {
+
+// One product out[n, m] = epilogue(sum_k A[m, k] B[n, k]), m along the
+// output's rows (contiguous), so the three products of a layer read their
+// operands as they lie:
+//   forward   A = weight [M, K],   B = x [N, K]         (both k-contiguous)
+//   dx        A = weight [K, M],   B = dz [N, K]        (A m-contiguous)
+//   dweight   A = x [K, M],        B = dz [K, N]        (both transposed)
+// Gated: A has 2M rows, the gate rows then the up rows, and
+// out = act(gate) * up.  Grouped (E > 0): A is [E, M or 2M, K], the rows n of
+// expert e are offsets[e] .. offsets[e] + counts[e], row n read from row
+// row_token[n] of B.
+struct Gemm {
+    const uint16_t *a, *b;
+    int a_mn, b_mn;             // 1: the operand is contiguous along m (n), not k
+    int M, N, K;
+    int gated;
+    const uint16_t *bias;       // [M] or [2M] (per expert), or null
+    const uint16_t *residual;   // bf16 [N, M] or null
+    void *out;                  // [N, M]
+    int out_f32;
+    uint16_t *preact;           // bf16 [N, M] or [N, 2M], or null
+    int act;
+    int E;                      // 0: not grouped
+    const int32_t *offsets, *counts, *row_token;
+    int64_t b_rows;             // rows of B
+};
+
+// Plain tiled kernel of fp32 multiply-adds: any size, alignment and layout.
+cudaError_t launch_gemm_simple(const Gemm &g, cudaStream_t stream);
+
+// dz of the backward passes, its bf16 rounding into dz [T, cols] (null:
+// none), and the column sums into dbias (bf16 [cols], null: none).  Linear:
+// cols = n, dz = dout * act'(preact), or dout without preact.  Gated: cols =
+// 2n, dout [T, n], preact [T, 2n].  partial: fp32 [ceil(T / kBiasRows), cols]
+// scratch, used with dbias.
+constexpr int kBiasRows = 32;
+cudaError_t launch_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
+                      uint16_t *dz, float *partial, uint16_t *dbias, int T, int n,
+                      cudaStream_t stream);
+
+// The grouped layout (moe_permute); chunks = permute_chunks(T * K).
+int permute_chunks(int64_t slots);
+cudaError_t launch_permute(const int32_t *ids, int T, int K, int E, int tile, int32_t *idx_map,
+                           int32_t *row_token, int64_t P, int32_t *offsets, int32_t *counts,
+                           int32_t *workspace, cudaStream_t stream);
+
+#ifdef __CUDACC__
+namespace {
+
+// The activations in the forms that lose nothing to cancellation: z / (1 +
+// exp(-q)) stays accurate relative to its size where 1 + tanh or 1 + erf
+// would cancel.  __fdividef gives 0 for denominators above 2^126, where the
+// quotient has left the normal range of bf16 and fp32 or is about to.
+__device__ __forceinline__ float act_value(float z, int act) {
+    switch (act) {
+        case MOEF_ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
+        case MOEF_ACT_GELU: return 0.5f * z * erfcf(-0.70710678f * z);
+        case MOEF_ACT_GELU_TANH:
+            return __fdividef(z, 1.f + __expf(-1.59576912f * (z + 0.044715f * z * z * z)));
+        case MOEF_ACT_RELU: return z > 0.f || z != z ? z : 0.f;
+        default: return z;
+    }
+}
+
+// act'(z), and act(z) in *value.
+__device__ __forceinline__ float act_grad(float z, int act, float *value) {
+    switch (act) {
+        case MOEF_ACT_SILU: {
+            const float s = __fdividef(1.f, 1.f + __expf(-z));
+            *value = z * s;
+            return s * (1.f + z * (1.f - s));
+        }
+        case MOEF_ACT_GELU: {
+            const float phi = 0.5f * erfcf(-0.70710678f * z);
+            *value = z * phi;
+            return phi + 0.39894228f * z * __expf(-0.5f * z * z);
+        }
+        case MOEF_ACT_GELU_TANH: {
+            const float s = __fdividef(1.f, 1.f + __expf(-1.59576912f *
+                                                         (z + 0.044715f * z * z * z)));
+            *value = z * s;
+            const float d = s * (1.f - s);      // 0 far out, where z * z may overflow
+            return d == 0.f ? s : s + d * z * 1.59576912f * (1.f + 0.134145f * z * z);
+        }
+        case MOEF_ACT_RELU:
+            *value = z > 0.f || z != z ? z : 0.f;
+            return z > 0.f ? 1.f : 0.f;
+        default: *value = z; return 1.f;
+    }
+}
+
+}  // namespace
+#endif
+
+}  // namespace moef

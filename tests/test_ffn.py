@@ -1,0 +1,470 @@
+"""The products around the finalize on the GPU, against plain 64-bit
+implementations with bounds derived from their roundings (ffn_ref)."""
+import pytest
+import torch
+
+import ffn_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def rand(seed, *shape, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.empty(shape, dtype=BF16, device="cuda").normal_(0.0, scale, generator=g)
+
+
+def misaligned(t):
+    """The same values at an address that is only 2-byte aligned."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    v = buf[1:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+# T, N, K: one token and one value, sizes off and on every tile, odd sizes
+LINEAR_SHAPES = [(1, 1, 1), (1, 256, 512), (3, 8, 64), (7, 40, 72), (16, 128, 64), (17, 136, 200),
+                 (64, 300, 128), (100, 1000, 24), (129, 257, 136), (255, 512, 512),
+                 (256, 264, 1024), (300, 384, 4096), (513, 520, 328), (1100, 640, 256),
+                 (5, 13, 77), (130, 67, 333)]
+
+
+@pytest.mark.parametrize("T,N,K", LINEAR_SHAPES)
+def test_linear_shapes(cuda_lib, T, N, K):
+    x, w = rand(1, T, K), rand(2, N, K, scale=K ** -0.5)
+    R.check(cuda_lib.linear(x, w), R.linear(x, w), f"{T}x{N}x{K}")
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+@pytest.mark.parametrize("T,N,K", [(1, 264, 512), (37, 200, 136), (300, 520, 264), (9, 35, 51)])
+def test_linear_epilogue(cuda_lib, name, T, N, K):
+    x, w, b, r = rand(3, T, K), rand(4, N, K, scale=K ** -0.5), rand(5, N), rand(6, T, N, scale=2)
+    for bias in (None, b):
+        for res in (None, r):
+            for dt in (BF16, torch.float32):
+                got = cuda_lib.linear(x, w, bias=bias, residual=res, activation=name,
+                                      out_dtype=dt, save_preact=True)
+                assert got["out"].dtype == dt
+                R.check(got, R.linear(x, w, bias, res, name, dt == torch.float32),
+                        f"{name} bias={bias is not None} res={res is not None} {dt}")
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 31, 33, 63, 65, 127, 128, 129, 192, 257, 1025])
+def test_linear_every_row_count_class(cuda_lib, T):
+    x, w = rand(7, T, 320), rand(8, 392, 320, scale=0.05)
+    R.check(cuda_lib.linear(x, w), R.linear(x, w), f"T={T}")
+
+
+def test_linear_in_place_residual_and_given_outputs(cuda_lib):
+    x, w, r = rand(9, 70, 256), rand(10, 264, 256, scale=0.06), rand(11, 70, 264)
+    ref = R.linear(x, w, None, r, "silu")
+    pre = torch.empty(70, 264, dtype=BF16, device="cuda")
+    got = cuda_lib.linear(x, w, residual=r, activation="silu", out=r, preact=pre)
+    assert got["out"] is r and got["preact"] is pre
+    R.check(got, ref)
+
+
+def test_linear_misaligned_operands(cuda_lib):
+    x, w, b, r = rand(12, 33, 128), rand(13, 72, 128, scale=0.1), rand(14, 72), rand(15, 33, 72)
+    ref = R.linear(x, w, b, r, "gelu")
+    for k in range(4):
+        a = [misaligned(t) if i == k else t for i, t in enumerate((x, w, b, r))]
+        out = misaligned(torch.zeros(33, 72, dtype=BF16, device="cuda"))
+        R.check(cuda_lib.linear(a[0], a[1], bias=a[2], residual=a[3], activation="gelu", out=out),
+                ref, f"operand {k}")
+
+
+def test_non_finite_rows_stay_in_their_rows(cuda_lib):
+    x, w = rand(16, 40, 192), rand(17, 200, 192, scale=0.1)
+    clean = cuda_lib.linear(x, w)["out"]
+    x2 = x.clone()
+    x2[5, 3] = float("nan")
+    x2[11, 100] = float("inf")
+    got = cuda_lib.linear(x2, w)["out"]
+    keep = torch.ones(40, dtype=torch.bool, device="cuda")
+    keep[5] = keep[11] = False
+    assert torch.equal(got[keep], clean[keep])
+    assert got[5].isnan().all() and not got[11].isfinite().any()
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+@pytest.mark.parametrize("T,I,H", [(1, 64, 256), (1, 8, 64), (5, 200, 136), (33, 136, 512),
+                                   (300, 264, 264), (700, 72, 128), (6, 21, 35)])
+def test_gated_ffn(cuda_lib, name, T, I, H):
+    x, w, b = rand(20, T, H), rand(21, 2 * I, H, scale=H ** -0.5), rand(22, 2 * I)
+    for bias in (None, b):
+        for save in (False, True):
+            got = cuda_lib.gated_ffn(x, w, bias=bias, activation=name, save_preact=save)
+            assert set(got) == ({"out", "preact"} if save else {"out"})
+            R.check(got, R.gated(x, w, bias, name), f"{name} bias={bias is not None}")
+
+
+@pytest.mark.parametrize("T,I,H", [(1, 1, 1), (2, 2048, 1024), (64, 320, 2048), (200, 1024, 520),
+                                   (1030, 264, 136)])
+def test_gated_ffn_shapes(cuda_lib, T, I, H):
+    x, w = rand(23, T, H), rand(24, 2 * I, H, scale=H ** -0.5)
+    R.check(cuda_lib.gated_ffn(x, w, save_preact=True), R.gated(x, w), f"{T}x{I}x{H}")
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+@pytest.mark.parametrize("T,N,K", [(1, 64, 128), (40, 72, 136), (300, 264, 520), (777, 128, 256),
+                                   (33, 35, 51)])
+def test_linear_backward(cuda_lib, name, T, N, K):
+    x, w, d = rand(30, T, K), rand(31, N, K, scale=K ** -0.5), rand(32, T, N, scale=0.1)
+    pre = None if name == "none" else cuda_lib.linear(x, w, save_preact=True)["preact"]
+    got = cuda_lib.linear_backward(d, x, w, activation=name, preact=pre, want_dbias=True)
+    R.check(got, R.backward(d, x, w, pre, name, False), name)
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+@pytest.mark.parametrize("T,I,H", [(1, 64, 128), (40, 72, 136), (300, 264, 520), (777, 64, 256),
+                                   (33, 19, 51)])
+def test_gated_ffn_backward(cuda_lib, name, T, I, H):
+    x, w, d = rand(33, T, H), rand(34, 2 * I, H, scale=H ** -0.5), rand(35, T, I, scale=0.1)
+    pre = cuda_lib.gated_ffn(x, w, activation=name, save_preact=True)["preact"]
+    got = cuda_lib.gated_ffn_backward(d, x, w, pre, activation=name, want_dbias=True)
+    R.check(got, R.backward(d, x, w, pre, name, True), name)
+
+
+def test_backward_gives_what_is_wanted(cuda_lib):
+    x, w, d = rand(36, 40, 64), rand(37, 48, 64), rand(38, 40, 48)
+    full = cuda_lib.linear_backward(d, x, w, want_dbias=True)
+    for key in ("dx", "dweight", "dbias"):
+        want = {f"want_{k}": k == key for k in ("dx", "dweight", "dbias")}
+        got = cuda_lib.linear_backward(d, x, w, **want)
+        assert set(got) == {key} and torch.equal(got[key], full[key])
+    ws = torch.empty(cuda_lib.linear_backward_workspace_bytes(40, 48), dtype=torch.uint8,
+                     device="cuda")
+    given = torch.empty(48, 64, dtype=BF16, device="cuda")
+    got = cuda_lib.linear_backward(d, x, w, want_dx=False, dweight=given, workspace=ws)
+    assert got["dweight"] is given and torch.equal(given, full["dweight"])
+
+
+def test_backward_of_no_rows_is_zero(cuda_lib):
+    x = torch.empty(0, 64, dtype=BF16, device="cuda")
+    for gated, n in ((False, 48), (True, 24)):
+        w = rand(39, 48, 64)
+        d = torch.empty(0, n, dtype=BF16, device="cuda")
+        if gated:
+            got = cuda_lib.gated_ffn_backward(d, x, w, torch.empty(0, 48, dtype=BF16, device="cuda"),
+                                              want_dbias=True)
+        else:
+            got = cuda_lib.linear_backward(d, x, w, want_dbias=True)
+        assert got["dx"].shape == (0, 64)
+        assert not got["dweight"].any() and got["dweight"].shape == (48, 64)
+        assert not got["dbias"].any()
+    assert cuda_lib.linear(x, rand(1, 8, 64))["out"].shape == (0, 8)
+    assert cuda_lib.gated_ffn(x, rand(1, 8, 64))["out"].shape == (0, 4)
+
+
+def test_gradient_against_differences(cuda_lib):
+    """dx and dweight of a linear GELU layer against central differences of
+    the fp32 forward.  x, the weights and the steps are multiples of 2^-6 below
+    4, so x +- step is exact in bf16.  L = sum(dout * out): a central
+    difference with step e is off by e^2 / 6 |L'''| from curvature and by the
+    forward's own error over e."""
+    g = torch.Generator().manual_seed(5)
+    T, N, K, e = 24, 40, 64, 2.0 ** -5
+    x = (torch.randint(-32, 33, (T, K), generator=g).double() / 32)
+    w = (torch.randint(-16, 17, (N, K), generator=g).double() / 64)
+    d = (torch.randint(-8, 9, (T, N), generator=g).double() / 8)
+    vx = torch.randint(0, 2, (T, K), generator=g).double() * 2 - 1
+    vw = torch.randint(0, 2, (N, K), generator=g).double() * 2 - 1
+
+    def dev(t):
+        b = t.to(BF16)
+        assert torch.equal(b.double(), t)
+        return b.cuda()
+
+    def loss(xx, ww):
+        out = cuda_lib.linear(dev(xx), dev(ww), activation="gelu",
+                              out_dtype=torch.float32)["out"].cpu().double()
+        return (d * out).sum().item()
+
+    pre = cuda_lib.linear(dev(x), dev(w), activation="gelu", save_preact=True)["preact"]
+    grads = cuda_lib.linear_backward(dev(d), dev(x), dev(w), activation="gelu", preact=pre)
+    for key, (xx, ww), v in (("dx", (vx, 0 * w), vx), ("dweight", (0 * x, vw), vw)):
+        diff = (loss(x + e * xx, w + e * ww) - loss(x - e * xx, w - e * ww)) / (2 * e)
+        slope = (grads[key].cpu().double() * v).sum().item()
+        dz = (xx @ w.mT + x @ ww.mT).abs()              # dz / de of each element
+        curvature = (d.abs() * dz ** 3 * 2.0).sum().item() * e * e / 6   # |gelu'''| < 2
+        zmag = x.abs() @ w.abs().mT
+        forward = (d.abs() * (1.13 * (K + 2) * R.ADD * zmag * 2 + R.ACT * zmag)).sum().item() / e
+        # dz's rounding, the saved preactivation's and the gradient's own
+        ref = grads[key].cpu().double().abs().sum().item()
+        path = (d.abs() @ w.abs()).sum().item() if key == "dx" else (d.abs().mT @ x.abs()).sum().item()
+        rounding = R.BF16 * (ref + 1.13 * path) + 0.8 * R.BF16 * (
+            (d.abs() * zmag) @ w.abs()).sum().item() * (key == "dx") + 0.8 * R.BF16 * (
+            (d.abs() * zmag).mT @ x.abs()).sum().item() * (key == "dweight")
+        assert abs(diff - slope) <= curvature + forward + rounding
+        # a wrong sign, scale or missing derivative shows: the slope is large
+        assert abs(slope) > 0 and abs(diff - slope) < 0.05 * (abs(slope) + abs(diff)) + 1.0
+
+
+def test_equal_calls_give_equal_bits(cuda_lib):
+    x, w, d = rand(40, 333, 512), rand(41, 400, 512, scale=0.05), rand(42, 333, 200)
+    pre = cuda_lib.gated_ffn(x, w, save_preact=True)["preact"]
+    first = cuda_lib.gated_ffn_backward(d, x, w, pre, want_dbias=True)
+    for _ in range(3):
+        again = cuda_lib.gated_ffn_backward(d, x, w, pre, want_dbias=True)
+        for key in first:
+            assert torch.equal(first[key], again[key]), key
+    for T in (1, 9, 70):
+        a = cuda_lib.linear(x[:T].contiguous(), w)["out"]
+        assert torch.equal(a, cuda_lib.linear(x[:T].contiguous(), w)["out"])
+
+
+# ---------------------------------------------------------------- row map
+
+
+def ids_of(seed, T, K, E, kind):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "one":
+        return torch.full((T, K), E - 1, dtype=torch.int32)
+    if kind == "none":
+        return torch.full((T, K), -1, dtype=torch.int32)
+    ids = torch.randint(0, E, (T, K), generator=g, dtype=torch.int32)     # repeats in a token too
+    if kind == "holes":
+        ids[torch.rand(T, K, generator=g) < 0.3] = -1
+        ids[torch.rand(T, K, generator=g) < 0.05] = E
+        ids[torch.rand(T, K, generator=g) < 0.05] = 2 ** 31 - 1
+    return ids
+
+
+@pytest.mark.parametrize("kind", ["all", "holes", "one", "none"])
+@pytest.mark.parametrize("T,K,E,tile", [(1, 1, 1, 1), (1, 8, 256, 128), (7, 3, 5, 4),
+                                        (256, 8, 256, 128), (300, 6, 60, 16), (1000, 2, 8, 64),
+                                        (5000, 8, 384, 1), (2049, 4, 1024, 7), (341, 6, 33, 3),
+                                        (40000, 8, 128, 32)])
+def test_permute(cuda_lib, kind, T, K, E, tile):
+    ids = ids_of(T + K, T, K, E, kind)
+    got = cuda_lib.permute_tokens(ids.cuda(), E, tile)
+    P = got["row_token"].numel()
+    assert P == cuda_lib.permute_rows(T, K, E, tile)
+    ref = R.layout(ids.tolist(), E, tile, P)
+    for key, r in zip(("idx_map", "row_token", "offsets", "counts"), ref):
+        assert torch.equal(got[key].cpu(), torch.tensor(r, dtype=torch.int32)), key
+
+
+def test_permute_larger_row_buffer_and_no_tokens(cuda_lib):
+    ids = ids_of(3, 50, 4, 16, "all")
+    row_token = torch.full((5000,), 77, dtype=torch.int32, device="cuda")
+    got = cuda_lib.permute_tokens(ids.cuda(), 16, 8, row_token=row_token)
+    ref = R.layout(ids.tolist(), 16, 8, 5000)
+    assert torch.equal(got["row_token"].cpu(), torch.tensor(ref[1], dtype=torch.int32))
+    empty = cuda_lib.permute_tokens(torch.empty(0, 4, dtype=torch.int32, device="cuda"), 16, 8,
+                                    row_token=row_token)
+    assert not empty["offsets"].any() and not empty["counts"].any()
+    assert (row_token == -1).all()
+
+
+# --------------------------------------------------------- expert products
+
+
+def experts_case(mf, T, K, E, tile, kind="holes", seed=50):
+    ids = ids_of(seed, T, K, E, kind)
+    return mf.permute_tokens(ids.cuda(), E, tile)
+
+
+def check_experts(mf, T, K, E, tile, H, I, name, bias, kind):
+    m = experts_case(mf, T, K, E, tile, kind)
+    P = m["row_token"].numel()
+    x = rand(51, T, H)
+    w13, w2 = rand(52, E, 2 * I, H, scale=H ** -0.5), rand(53, E, H, I, scale=I ** -0.5)
+    b13, b2 = (rand(54, E, 2 * I), rand(55, E, H)) if bias else (None, None)
+    h = torch.full((P, I), 7.0, dtype=BF16, device="cuda")
+    y = torch.full((P, H), 7.0, dtype=BF16, device="cuda")
+    assert mf.expert_gated_ffn(x, m["row_token"], m["offsets"], m["counts"], w13, bias=b13,
+                               activation=name, out=h) is h
+    mf.expert_linear(h, m["offsets"], m["counts"], w2, bias=b2, out=y)
+    direct = mf.expert_linear(x, m["offsets"], m["counts"], w13, row_token=m["row_token"],
+                              bias=b13, activation=name)
+    valid = torch.zeros(P, dtype=torch.bool, device="cuda")
+    for e, (first, count) in enumerate(zip(m["offsets"].tolist(), m["counts"].tolist())):
+        if not count:
+            continue
+        rows = slice(first, first + count)
+        valid[rows] = True
+        xe = x[m["row_token"][rows].long()]
+        R.check({"out": h[rows]}, R.gated(xe, w13[e], None if b13 is None else b13[e], name),
+                f"expert {e} up")
+        R.check({"out": y[rows]}, R.linear(h[rows], w2[e], None if b2 is None else b2[e]),
+                f"expert {e} down")
+        R.check({"out": direct[rows]}, R.linear(xe, w13[e], None if b13 is None else b13[e],
+                                                name=name), f"expert {e} gathered linear")
+    assert (h[~valid] == 7).all() and (y[~valid] == 7).all()
+
+
+@pytest.mark.parametrize("T,K,E,tile,H,I", [(1, 8, 16, 128, 256, 64), (1, 1, 1, 1, 64, 8),
+                                            (16, 4, 8, 16, 264, 136), (100, 2, 4, 1, 128, 72),
+                                            (333, 3, 3, 64, 200, 264), (900, 2, 5, 7, 72, 40),
+                                            (40, 4, 60, 8, 512, 128), (12, 2, 6, 4, 35, 21)])
+def test_experts(cuda_lib, T, K, E, tile, H, I):
+    check_experts(cuda_lib, T, K, E, tile, H, I, "silu", False, "holes")
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+def test_experts_epilogues(cuda_lib, name):
+    check_experts(cuda_lib, 60, 3, 5, 8, 136, 72, name, True, "all")
+
+
+@pytest.mark.parametrize("kind", ["one", "none"])
+def test_experts_all_rows_in_one_expert_and_none_at_all(cuda_lib, kind):
+    check_experts(cuda_lib, 300, 2, 6, 16, 128, 64, "silu", False, kind)
+
+
+def test_experts_rows_beyond_the_buffer_and_tokens_beyond_x(cuda_lib):
+    """Rows at or past P are not computed; a row_token outside [0, T) is a row
+    of zeros."""
+    H, I, E = 128, 64, 2
+    x, w = rand(60, 10, H), rand(61, E, 2 * I, H, scale=0.1)
+    row_token = torch.tensor([0, 1, 12, -1, 4, 5, 6, 7], dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, 4, 40], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([4, 30], dtype=torch.int32, device="cuda")
+    guard = torch.full((12, I), 3.0, dtype=BF16, device="cuda")
+    got = cuda_lib.expert_gated_ffn(x, row_token, offsets, counts, w, out=guard[:8])
+    xs = torch.cat([x[:2], torch.zeros(2, H, dtype=BF16, device="cuda"), x[4:8]])
+    for e, rows in ((0, slice(0, 4)), (1, slice(4, 8))):
+        R.check({"out": got[rows]}, R.gated(xs[rows], w[e]), f"expert {e}")
+    assert (guard[8:] == 3).all()
+
+
+# ------------------------------------------------------ streams and graphs
+
+
+def test_calls_follow_the_given_and_the_current_stream(cuda_lib):
+    s = torch.cuda.Stream()
+    x, w = rand(70, 200, 2048), rand(71, 512, 2048, scale=0.02)
+    want = cuda_lib.linear(x, w)["out"]
+    big = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    late = torch.zeros_like(x)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            big.add_(1)                 # keeps s busy while the call is enqueued
+        late.copy_(x)
+        a = cuda_lib.linear(late, w)["out"]
+    b = cuda_lib.linear(late, w, stream=s)["out"]
+    s.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want)
+
+
+def test_two_captured_layers_replay_on_new_inputs(cuda_lib):
+    """Two graphs of forward and backward over their own buffers, replayed in
+    turn and at once on two streams, give what eager calls give."""
+    T, H, I = 96, 256, 136
+    states = []
+    for k in range(2):
+        x, w, d = rand(80 + k, T, H), rand(82 + k, 2 * I, H, scale=0.06), rand(84 + k, T, I)
+        ws = torch.empty(cuda_lib.gated_ffn_backward_workspace_bytes(T, I), dtype=torch.uint8,
+                         device="cuda")
+        pre = torch.empty(T, 2 * I, dtype=BF16, device="cuda")
+
+        def step(x=x, w=w, d=d, ws=ws, pre=pre):
+            f = cuda_lib.gated_ffn(x, w, preact=pre)
+            g = cuda_lib.gated_ffn_backward(d, x, w, pre, want_dbias=True, workspace=ws)
+            return dict(out=f["out"], **g)
+
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = step()
+        states.append((graph, outs, x, w, d, pre, ws))      # the graph's buffers stay alive
+    streams = [torch.cuda.Stream() for _ in states]
+    for rnd in range(3):
+        want = []
+        for k, (_, _, x, w, d, *_) in enumerate(states):
+            x.copy_(rand(90 + rnd * 2 + k, T, H))
+            f = cuda_lib.gated_ffn(x, w, save_preact=True)
+            g = cuda_lib.gated_ffn_backward(d, x, w, f["preact"], want_dbias=True)
+            want.append(dict(out=f["out"], **g))
+        torch.cuda.synchronize()
+        for (graph, *_), s in zip(states, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, outs, *_), ref in zip(states, want):
+            for key in ref:
+                assert torch.equal(outs[key], ref[key]), (rnd, key)
+
+
+def test_experts_graph_replays_on_new_routing(cuda_lib):
+    """One graph of the row map and both expert products, replayed on other
+    ids: counts and offsets change, nothing is read on the host."""
+    T, K, E, H, I, tile = 50, 3, 12, 128, 64, 8
+    x, w13, w2 = rand(1, T, H), rand(2, E, 2 * I, H, scale=0.1), rand(3, E, H, I, scale=0.1)
+    ids = ids_of(1, T, K, E, "all").cuda()
+    P = cuda_lib.permute_rows(T, K, E, tile)
+    y = torch.zeros(P, H, dtype=BF16, device="cuda")
+
+    def step():
+        m = cuda_lib.permute_tokens(ids, E, tile)
+        h = cuda_lib.expert_gated_ffn(x, m["row_token"], m["offsets"], m["counts"], w13)
+        cuda_lib.expert_linear(h, m["offsets"], m["counts"], w2, out=y)
+        return m
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m = step()
+    for seed, kind in ((4, "holes"), (5, "one"), (6, "none"), (7, "all")):
+        ids.copy_(ids_of(seed, T, K, E, kind))
+        y.zero_()
+        graph.replay()
+        got, got_map = y.clone(), {k: v.clone() for k, v in m.items()}
+        y.zero_()
+        ref_map = step()
+        for key in ref_map:
+            assert torch.equal(got_map[key], ref_map[key]), (kind, key)
+        assert torch.equal(got, y), kind
+
+
+# ------------------------------------------------------- the layer together
+
+
+@pytest.mark.parametrize("T,H,I,E,K,tile", [(1, 256, 64, 16, 4, 16), (50, 264, 72, 12, 3, 8),
+                                            (400, 512, 136, 32, 8, 128)])
+def test_moe_layer(cuda_lib, T, H, I, E, K, tile):
+    """Router, gate, row map, expert products, shared expert and finalize as
+    one layer, against the layer in 64 bits on the same routing.  Bound: the
+    finalize's own tolerance, widened by what the bf16 intermediates h, the
+    expert rows and the shared output carry (three roundings of 2^-8 relative
+    to the magnitudes that are summed)."""
+    mf = cuda_lib
+    x = rand(100, T, H)
+    wr, w13, w2 = rand(101, E, H, scale=H ** -0.5), rand(102, E, 2 * I, H, scale=H ** -0.5), \
+        rand(103, E, H, I, scale=I ** -0.5)
+    s13, s2 = rand(104, 2 * I, H, scale=H ** -0.5), rand(105, H, I, scale=I ** -0.5)
+    logits = mf.linear(x, wr, out_dtype=torch.float32)["out"]
+    R.check({"out": logits}, R.linear(x, wr, fp32=True), "logits")
+    route = mf.topk_route(logits, K, "sigmoid")
+    m = mf.permute_tokens(route["expert_ids"], E, tile)
+    h = mf.expert_gated_ffn(x, m["row_token"], m["offsets"], m["counts"], w13)
+    rows = mf.expert_linear(h, m["offsets"], m["counts"], w2)
+    shared = mf.linear(mf.gated_ffn(x, s13)["out"], s2)["out"]
+    bad = mf.check_indices(m["idx_map"], rows.shape[0])
+    out = mf.moe_finalize(rows, m["idx_map"], route["weights"], "fp32", shared,
+                          routed_scale=2.5)["out"]
+    assert int(bad.item()) == 0
+
+    def expert(w_up, w_down):
+        z = x.double() @ w_up.double().mT
+        g, u = z.chunk(2, dim=-1)
+        hh = R.act(g, "silu")[0] * u
+        return hh @ w_down.double().mT, hh.abs() @ w_down.double().abs().mT
+
+    ref, mag = expert(s13, s2)
+    for e in range(E):
+        w = torch.where(route["expert_ids"] == e, route["weights"], 0.0).double().sum(1) * 2.5
+        if w.any():
+            y, ymag = expert(w13[e], w2[e])
+            ref, mag = ref + w[:, None] * y, mag + w[:, None] * ymag
+    bound = 2.0 ** -7 * ref.abs() + 2e-3 + 3 * R.BF16 * mag
+    assert ((out.double() - ref).abs() <= bound).all()
+    rel = ((out.double() - ref).norm() / ref.norm()).item()
+    assert rel < 3 * R.BF16       # three roundings in a row, each at most 2^-8
