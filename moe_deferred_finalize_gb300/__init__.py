@@ -19,7 +19,7 @@ from ._abi import (WKIND, BoundFinalize, MoefError, allreduce_plan, bind,  # noq
                    topk_route, unfused_workspace_bytes, unpack_topk_ids)
 from ._ffn import (ACTIVATION, expert_gated_ffn, expert_linear, gated_ffn,  # noqa: F401
                    gated_ffn_backward, gated_ffn_backward_workspace_bytes, linear,
-                   linear_backward, linear_backward_workspace_bytes, permute_rows,
+                   linear_backward, linear_backward_workspace_bytes, lost_waits, permute_rows,
                    permute_tokens)
 
 __all__ = ["moe_finalize", "moe_finalize_host", "bind", "BoundFinalize", "moe_finalize_unfused",
@@ -29,4 +29,4 @@ __all__ = ["moe_finalize", "moe_finalize_host", "bind", "BoundFinalize", "moe_fi
            "moe_finalize_allreduce_reduce", "allreduce_plan", "linear", "linear_backward",
            "linear_backward_workspace_bytes", "gated_ffn", "gated_ffn_backward",
            "gated_ffn_backward_workspace_bytes", "permute_tokens", "permute_rows",
-           "expert_gated_ffn", "expert_linear", "ACTIVATION"]
+           "expert_gated_ffn", "expert_linear", "ACTIVATION", "lost_waits"]

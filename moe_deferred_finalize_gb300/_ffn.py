@@ -42,6 +42,7 @@ def _lib():
             "moe_expert_gated_ffn": (i32, [vp, i64] + [vp] * 5 + [i32, vp, i64, i32, i32, i32,
                                                                   vp]),
             "moe_expert_linear": (i32, [vp, i64] + [vp] * 5 + [i32, vp, i64, i32, i32, i32, vp]),
+            "moe_ffn_lost_waits": (i32, [ctypes.POINTER(ctypes.c_uint)]),
         }
         for name, (restype, argtypes) in signatures.items():
             fn = getattr(lib, name)
@@ -331,3 +332,16 @@ def expert_linear(x: torch.Tensor, offsets: torch.Tensor, counts: torch.Tensor,
     bf16 [E, N].  Otherwise as ``expert_gated_ffn``."""
     return _expert("moe_expert_linear", False, x, row_token, offsets, counts, weight, bias,
                    activation, out, stream)
+
+
+def lost_waits(device=None) -> int:
+    """Barrier waits of the tensor-core kernels that were given up on the
+    current device (or ``device``) since the library was loaded: 0 unless
+    something is broken.  Waits for the device."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None \
+        else torch.device(device)
+    count = ctypes.c_uint()
+    with _on(dev):
+        st = _lib().moe_ffn_lost_waits(ctypes.byref(count))
+    _raise(st, "moe_ffn_lost_waits")
+    return count.value

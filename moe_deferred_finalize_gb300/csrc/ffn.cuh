@@ -39,6 +39,13 @@ struct Gemm {
 // Plain tiled kernel of fp32 multiply-adds: any size, alignment and layout.
 cudaError_t launch_gemm_simple(const Gemm &g, cudaStream_t stream);
 
+// The tensor-core kernels.  False (nothing launched) when an operand's
+// alignment or pitch rules them out; otherwise *err is the launch's result.
+bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err);
+
+// Barrier waits that gave up since the library was loaded on this device.
+cudaError_t read_lost_waits(unsigned *count);
+
 // dz of the backward passes, its bf16 rounding into dz [T, cols] (null:
 // none), and the column sums into dbias (bf16 [cols], null: none).  Linear:
 // cols = n, dz = dout * act'(preact), or dout without preact.  Gated: cols =

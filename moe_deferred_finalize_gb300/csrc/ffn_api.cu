@@ -30,7 +30,12 @@ size_t backward_bytes(int64_t T, int64_t cols) {
 }
 
 moef_status run_gemm(const Gemm &g, cudaStream_t stream) {
-    return cuda_status(moef::launch_gemm_simple(g, stream));
+    int sms = 0;
+    const moef_status st = cuda_status(moef::current_sms(&sms));
+    if (st != MOEF_OK) return st;
+    cudaError_t err = cudaSuccess;
+    if (!moef::launch_gemm_tc(g, sms, stream, &err)) err = moef::launch_gemm_simple(g, stream);
+    return cuda_status(err);
 }
 
 // The backward pass of z = x weight^T + bias with `cols` features z, from
@@ -265,6 +270,11 @@ moef_status moe_expert_linear(const void *x, int64_t T, const int32_t *row_token
                               cudaStream_t stream) {
     return expert_product(x, T, row_token, offsets, counts, weight, bias, act, 0, out, P, E, N,
                           K, stream);
+}
+
+moef_status moe_ffn_lost_waits(unsigned *count) {
+    if (!count) return MOEF_ERR_NULL;
+    return cuda_status(moef::read_lost_waits(count));
 }
 
 }  // extern "C"

@@ -1,0 +1,687 @@
+// The products of moe_ffn.h on the tensor cores (tcgen05, TMA).
+//
+// out[n, m] = epilogue(sum_k A[m, k] B[n, k]): the MMA's M side carries the
+// output features, its N side the tokens.  That way one token or 256 use the
+// same instruction (N is any multiple of 16), ragged expert groups waste at
+// most 31 columns, and every product of a layer reads its operands as they
+// lie, k-contiguous or m-contiguous (the descriptor's transpose bits).
+//
+// A CTA is six warps: one issues the TMA copies of 64-deep k blocks into a
+// ring of shared-memory stages (128-byte swizzle), one lane of a second
+// issues the MMAs into TMEM, four finish tiles.  The accumulator is double
+// buffered (2 x 256 TMEM columns), so a tile's epilogue runs under the next
+// tile's products.
+//
+// Gated form: the A tile interleaves gate and up rows (g0, u0, g1, u1, ...),
+// which one 4-D tensor map [E][I][2][H] of the weights does in the copy.  A
+// gate and its up value then sit in neighbouring TMEM lanes, and two shuffles
+// a pair of columns bring them into one thread.
+//
+// Two launch forms:
+//   CG = 2  pairs of CTAs share tiles of 256 (m) x up to 256 (n): each CTA
+//           loads half of A and half of B, one instruction drives both SMs'
+//           tensor cores.  Persistent, one pair per two SMs.
+//   CG = 1  128 x up to 256 tiles with k split over a cluster of `split` CTAs:
+//           few tokens give few tiles, and the split spreads the weights over
+//           all SMs.  The partial accumulators meet in shared memory, and each
+//           CTA of the cluster adds and finishes its share of the tile, in
+//           rank order (equal calls give equal bits).
+#include <mutex>
+
+#include "ffn.cuh"
+#include "tc.cuh"
+#include "vec.cuh"
+
+namespace moef {
+namespace {
+
+constexpr int kTcThreads = 192;
+constexpr int kBlockK = 64;                     // k values per stage: one 128-byte swizzle row
+constexpr int kATile = 128 * kBlockK * 2;       // bytes of A per CTA and stage
+constexpr int kMaxBn = 256;
+constexpr int kMaxStages = 16;
+constexpr int kHeader = 6144;                   // barriers, tables
+constexpr int kSmemBytes = 227 * 1024;
+constexpr int kStageArea = kSmemBytes - kHeader - 1024;     // after rounding up to 1024
+constexpr uint64_t kWaitLimitNs = 2000000000;   // a wait gives up after two seconds
+
+// How one launch is cut up (see choose_plan).
+struct TcPlan {
+    int split;          // CTAs along k
+    int bn;             // columns per tile; 0: from the expert counts, on the device
+    int m_tiles, n_tiles;
+    int gather;         // B rows are fetched by row_token
+    int box_rows;       // rows of one B copy (k-contiguous B)
+};
+
+struct Header {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int gave_up;
+    int bn;
+    int tiles;
+    int prefix[MOEF_MAX_EXPERTS + 1];   // column tiles before each expert
+};
+static_assert(sizeof(Header) <= kHeader, "header region");
+
+__device__ unsigned int lost_waits;
+
+// Waits for a barrier's phase; false when the wait gave up (here or in
+// another warp of the CTA), upon which every role leaves its loops.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    for (int i = 0; i < 64; ++i)
+        if (bar_try(bar, parity)) return true;
+    const uint64_t end = now_ns() + kWaitLimitNs;
+    for (;;) {
+        for (int i = 0; i < 32; ++i)
+            if (bar_try(bar, parity)) return true;
+        if (*gave_up) return false;
+        if (now_ns() > end) {
+            *gave_up = 1;
+            atomicAdd(&lost_waits, 1u);
+            return false;
+        }
+    }
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle.  k-contiguous: 8-row
+// groups 1024 bytes apart.  m-contiguous: blocks of 64 m, each 64 k rows of
+// 128 bytes; 8-k groups 1024 bytes apart, m blocks 8192.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, int mn) {
+    const uint32_t lo = ((addr & 0x3FFFF) >> 4) | ((mn ? 8192u >> 4 : 1u) << 16);
+    const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+    return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+struct Tile {
+    int64_t row0;       // first output row
+    int count;          // valid columns (output rows)
+    int bn;             // columns computed
+    int m0;             // first feature
+    int e;              // expert
+};
+
+template <int CG, bool GATED>
+__device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const Header *h, int t) {
+    constexpr int kFeatures = (GATED ? 64 : 128) * CG;
+    Tile r;
+    r.e = 0;
+    int m, n;
+    if (g.E) {
+        int lo = 0, hi = g.E;           // prefix[lo] * m_tiles <= t < prefix[hi] * m_tiles
+        const int column = t / p.m_tiles;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (h->prefix[mid] <= column) lo = mid; else hi = mid;
+        }
+        r.e = lo;
+        const int nt = h->prefix[lo + 1] - h->prefix[lo];
+        const int local = t - h->prefix[lo] * p.m_tiles;
+        m = local / nt;
+        n = local % nt;
+        const int64_t first = g.offsets[lo];
+        const int count = static_cast<int>(min(static_cast<int64_t>(g.counts[lo]),
+                                               static_cast<int64_t>(g.N) - first));
+        r.bn = ((count + nt - 1) / nt + 16 * CG - 1) / (16 * CG) * (16 * CG);
+        r.row0 = first + static_cast<int64_t>(n) * r.bn;
+        r.count = min(r.bn, count - n * r.bn);
+    } else {
+        m = t / p.n_tiles;
+        n = t % p.n_tiles;
+        r.bn = p.bn;
+        r.row0 = static_cast<int64_t>(n) * r.bn;
+        r.count = static_cast<int>(min(static_cast<int64_t>(r.bn), g.N - r.row0));
+    }
+    r.m0 = m * kFeatures;
+    return r;
+}
+
+// ------------------------------------------------------------- epilogue
+
+__device__ __forceinline__ float bf16_value(const uint16_t *p, int64_t i) {
+    return __uint_as_float(static_cast<uint32_t>(__ldg(p + i)) << 16);
+}
+
+__device__ __forceinline__ void store_pair(uint16_t *p, int64_t i, float a, float b, bool both,
+                                           bool vec) {
+    const uint32_t v = pack_bf16x2(a, b);
+    if (vec) {
+        *reinterpret_cast<uint32_t *>(p + i) = v;
+    } else {
+        p[i] = static_cast<uint16_t>(v);
+        if (both) p[i + 1] = static_cast<uint16_t>(v >> 16);
+    }
+}
+
+// Finishes the adjacent features m, m + 1 of output rows; per-thread constants
+// of a tile.  vec: pairs are whole and aligned, one access each.
+template <bool GATED>
+struct Finish {
+    const Gemm &g;
+    int m;
+    bool any, both, vec;
+    float bias[GATED ? 4 : 2];
+
+    __device__ __forceinline__ Finish(const Gemm &gemm, int feature, int e) : g(gemm), m(feature) {
+        any = m < g.M;
+        both = m + 1 < g.M;
+        const uintptr_t out = reinterpret_cast<uintptr_t>(g.out);
+        const uintptr_t rest = reinterpret_cast<uintptr_t>(g.residual) |
+                               reinterpret_cast<uintptr_t>(g.preact);
+        vec = (g.M & 1) == 0 && (rest & 3) == 0 && (out & (g.out_f32 ? 7 : 3)) == 0;
+        const uint16_t *b = g.bias + static_cast<int64_t>(e) * (GATED ? 2 : 1) * g.M;
+        const bool have = g.bias != nullptr;
+        bias[0] = have && any ? bf16_value(b, m) : 0.f;
+        bias[1] = have && both ? bf16_value(b, m + 1) : 0.f;
+        if constexpr (GATED) {
+            bias[2] = have && any ? bf16_value(b, g.M + m) : 0.f;
+            bias[3] = have && both ? bf16_value(b, g.M + m + 1) : 0.f;
+        }
+    }
+
+    __device__ __forceinline__ uint32_t residual(int64_t n) const {
+        const uint16_t *p = g.residual + n * g.M + m;
+        if (vec) return *reinterpret_cast<const uint32_t *>(p);
+        return static_cast<uint32_t>(p[0]) | (both ? static_cast<uint32_t>(p[1]) << 16 : 0u);
+    }
+
+    // Linear: z0, z1 of row n, res its residual pair.
+    __device__ __forceinline__ void linear(int64_t n, float z0, float z1, uint32_t res) const {
+        z0 += bias[0];
+        z1 += bias[1];
+        const int64_t i = n * g.M + m;
+        if (g.preact) store_pair(g.preact, i, z0, z1, both, vec);
+        if (g.act != MOEF_ACT_NONE) {
+            z0 = act_value(z0, g.act);
+            z1 = act_value(z1, g.act);
+        }
+        if (g.residual) {
+            z0 += bf16_lo(res);
+            z1 += bf16_hi(res);
+        }
+        if (!g.out_f32) {
+            store_pair(static_cast<uint16_t *>(g.out), i, z0, z1, both, vec);
+        } else {
+            float *o = static_cast<float *>(g.out) + i;
+            if (vec) {
+                *reinterpret_cast<float2 *>(o) = make_float2(z0, z1);
+            } else {
+                o[0] = z0;
+                if (both) o[1] = z1;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void gated(int64_t n, float g0, float g1, float u0,
+                                          float u1) const {
+        g0 += bias[0];
+        g1 += bias[1];
+        u0 += bias[GATED ? 2 : 0];
+        u1 += bias[GATED ? 3 : 1];
+        if (g.preact) {
+            store_pair(g.preact, n * 2 * g.M + m, g0, g1, both, vec);
+            store_pair(g.preact, n * 2 * g.M + g.M + m, u0, u1, both, vec);
+        }
+        store_pair(static_cast<uint16_t *>(g.out), n * g.M + m, act_value(g0, g.act) * u0,
+                   act_value(g1, g.act) * u1, both, vec);
+    }
+};
+
+// One tile out of TMEM: this warp's 32 lanes (rows of A), all its columns.
+// Lanes swap values so that each holds two adjacent features of one column.
+template <bool GATED>
+__device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_cta, uint32_t tmem,
+                                            int quarter, int lane) {
+    const int feature = m_cta + (GATED ? quarter * 16 + (lane >> 2) * 2
+                                       : quarter * 32 + (lane & ~1));
+    const Finish<GATED> f(g, feature, t.e);
+    const bool odd = lane & 1, upper = lane & 2;
+    for (int c0 = 0; c0 < t.bn; c0 += 32) {
+        uint32_t r[32];
+        tmem_load32(tmem + c0, r);
+        if (c0 >= t.count) continue;
+        if constexpr (GATED) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                // neighbours: (gate, up) of columns c + odd and c + 2 + odd
+                float gate[2], up[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float a = __uint_as_float(r[c + 2 * k]);
+                    const float b = __uint_as_float(r[c + 2 * k + 1]);
+                    const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
+                    gate[k] = odd ? v : a;
+                    up[k] = odd ? b : v;
+                }
+                // the next feature's: lanes with `upper` keep the second column
+                const float vg = __shfl_xor_sync(0xFFFFFFFFu, upper ? gate[0] : gate[1], 2);
+                const float vu = __shfl_xor_sync(0xFFFFFFFFu, upper ? up[0] : up[1], 2);
+                const int col = c0 + c + (lane & 3);
+                if (col < t.count && f.any) {
+                    if (upper) f.gated(t.row0 + col, vg, gate[1], vu, up[1]);
+                    else f.gated(t.row0 + col, gate[0], vg, up[0], vu);
+                }
+            }
+        } else {
+            uint32_t res[16];
+            if (g.residual) {       // all loads before the first store
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int col = c0 + 2 * k + (lane & 1);
+                    res[k] = col < t.count && f.any ? f.residual(t.row0 + col) : 0u;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float a = __uint_as_float(r[2 * k]), b = __uint_as_float(r[2 * k + 1]);
+                const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
+                const int col = c0 + 2 * k + (lane & 1);
+                if (col < t.count && f.any)
+                    f.linear(t.row0 + col, odd ? v : a, odd ? b : v, g.residual ? res[k] : 0u);
+            }
+        }
+    }
+}
+
+// The cluster's partial tiles [column][128 rows of A] in shared memory: this
+// CTA adds and finishes every split-th 192 of the pairs.
+template <bool GATED>
+__device__ __forceinline__ void finish_split(const Gemm &g, const Tile &t, uint32_t buf, int split,
+                                             int rank) {
+    constexpr int kPairs = GATED ? 32 : 64;
+    const int items = t.count * kPairs;
+    for (int i = rank * kTcThreads + threadIdx.x; i < items; i += split * kTcThreads) {
+        const int col = i / kPairs, pair = i % kPairs;
+        const uint32_t at = buf + (col * 128 + pair * (GATED ? 4 : 2)) * 4;
+        const Finish<GATED> f(g, t.m0 + 2 * pair, t.e);
+        if (!f.any) continue;
+        const int64_t n = t.row0 + col;
+        if constexpr (GATED) {
+            float4 s = load_remote4(map_rank(at, 0));
+            for (int k = 1; k < split; ++k) {
+                const float4 v = load_remote4(map_rank(at, k));
+                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            }
+            f.gated(n, s.x, s.z, s.y, s.w);
+        } else {
+            const uint32_t res = g.residual ? f.residual(n) : 0u;
+            float2 s = load_remote2(map_rank(at, 0));
+            for (int k = 1; k < split; ++k) {
+                const float2 v = load_remote2(map_rank(at, k));
+                s.x += v.x; s.y += v.y;
+            }
+            f.linear(n, s.x, s.y, res);
+        }
+    }
+}
+
+// --------------------------------------------------------------- kernel
+
+template <int CG, bool GATED>
+__global__ void __launch_bounds__(kTcThreads, 1)
+gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
+               const __grid_constant__ CUtensorMap map_a,
+               const __grid_constant__ CUtensorMap map_b) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
+    Header *h = reinterpret_cast<Header *>(smem + (base - smem_addr(smem)));
+    const uint32_t stage0 = base + kHeader;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int rank = CG == 2 || p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const bool leader = CG == 1 || rank == 0;
+    volatile int *gave_up = &h->gave_up;
+
+    if (threadIdx.x == 0) {
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
+        for (int i = 0; i < kMaxStages; ++i) {
+            bar_init(smem_addr(&h->full[i]), 1);
+            bar_init(smem_addr(&h->empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(smem_addr(&h->acc_full[i]), 1);
+            bar_init(smem_addr(&h->acc_empty[i]), 4 * CG);
+        }
+        h->gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<CG>(smem_addr(&h->tmem), 2 * kMaxBn);
+    if (warp == 0) {
+        if (g.E) {      // column tiles of each expert
+            int most = 0;
+            for (int e = lane; e < g.E; e += 32) {
+                const int first = g.offsets[e];
+                most = max(most, first < 0 ? 0 : min(g.counts[e], g.N - first));
+            }
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            const int bn = min(kMaxBn, max(1, (most + 16 * CG - 1) / (16 * CG)) * 16 * CG);
+            int before = 0;
+            for (int e0 = 0; e0 < g.E; e0 += 32) {
+                const int e = e0 + lane;
+                int v = 0;
+                if (e < g.E) {
+                    const int first = g.offsets[e];
+                    v = first < 0 ? 0 : max(0, min(g.counts[e], g.N - first));
+                    v = (v + bn - 1) / bn;
+                }
+                int sum = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int w = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                    if (lane >= o) sum += w;
+                }
+                if (e < g.E) h->prefix[e] = before + sum - v;
+                before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+            }
+            if (lane == 0) {
+                h->prefix[g.E] = before;
+                h->bn = bn;
+                h->tiles = before * p.m_tiles;
+            }
+        } else if (lane == 0) {
+            h->bn = p.bn;
+            h->tiles = p.n_tiles * p.m_tiles;
+        }
+    }
+    fence_before();
+    if (CG == 2 || p.split > 1) cluster_sync(); else __syncthreads();
+    fence_after();
+
+    const int tiles = h->tiles;
+    const uint32_t tmem = h->tmem;
+    const int bnc_max = h->bn / CG;                 // B rows per CTA
+    const uint32_t b_bytes = bnc_max * kBlockK * 2;     // a multiple of 2048
+    const uint32_t stage_bytes = kATile + b_bytes;
+    const int stages = min(kMaxStages, static_cast<int>(kStageArea / stage_bytes));
+    const int blocks = (g.K + kBlockK - 1) / kBlockK;
+    const int kb0 = CG == 1 ? static_cast<int>(static_cast<int64_t>(blocks) * rank / p.split) : 0;
+    const int kb1 = CG == 1 ? static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / p.split)
+                            : blocks;
+    const int group = CG == 2 ? 2 : p.split;
+    const int first_tile = blockIdx.x / group, step = gridDim.x / group;
+    const int m_cta_rows = GATED ? 64 : 128;        // features per CTA
+
+    if (warp == 0) {
+        // ---- copies
+        int s = 0;
+        uint32_t phase = 1;
+        for (int ti = first_tile; ti < tiles; ti += step) {
+            const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+            const int bnc = t.bn / CG;
+            const int m0 = t.m0 + (CG == 2 ? rank * m_cta_rows : 0);
+            const int64_t row0 = t.row0 + (CG == 2 ? rank * bnc : 0);
+            const int boxes = g.b_mn ? (bnc + 63) / 64 : (bnc + p.box_rows - 1) / p.box_rows;
+            const uint32_t b_tx = p.gather ? bnc * 128u
+                                  : g.b_mn ? boxes * 8192u : boxes * p.box_rows * 128u;
+            int4 rows = make_int4(-1, -1, -1, -1);
+            if (p.gather && 4 * lane < bnc) {
+                const int valid = t.count - (CG == 2 ? rank * bnc : 0) - 4 * lane;
+                const int32_t *at = g.row_token + row0 + 4 * lane;
+                if (valid > 0) rows.x = at[0];
+                if (valid > 1) rows.y = at[1];
+                if (valid > 2) rows.z = at[2];
+                if (valid > 3) rows.w = at[3];
+            }
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const uint32_t full = smem_addr(&h->full[s]);
+                ok = wait(smem_addr(&h->empty[s]), phase, gave_up);
+                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                const uint32_t a = stage0 + s * stage_bytes, b = a + kATile;
+                const uint32_t bar = CG == 2 ? map_rank(full, 0) : full;
+                if (lane == 0) {
+                    if (leader) bar_expect(full, CG * (kATile + b_tx));
+                    if (g.a_mn) {
+                        tma_2d<CG>(a, &map_a, m0, kb * kBlockK, bar);
+                        tma_2d<CG>(a + 8192, &map_a, m0 + 64, kb * kBlockK, bar);
+                    } else {
+                        tma_4d<CG>(a, &map_a, kb * kBlockK, 0, m0, t.e, bar);
+                    }
+                    if (g.b_mn) {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_2d<CG>(b + i * 8192, &map_b, static_cast<int>(row0) + i * 64,
+                                       kb * kBlockK, bar);
+                    } else if (!p.gather) {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_2d<CG>(b + i * p.box_rows * 128, &map_b, kb * kBlockK,
+                                       static_cast<int>(row0) + i * p.box_rows, bar);
+                    }
+                }
+                if (p.gather) {
+                    __syncwarp();
+                    if (4 * lane < bnc)
+                        tma_gather4<CG>(b + lane * 512, &map_b, kb * kBlockK, rows, bar);
+                }
+                if (++s == stages) { s = 0; phase ^= 1; }
+            }
+            if (!ok) break;
+        }
+        // every stage handed back: no copy or arrival is left in flight
+        for (int i = 0; i < stages; ++i) {
+            if (!wait(smem_addr(&h->empty[s]), phase, gave_up)) break;
+            if (++s == stages) { s = 0; phase ^= 1; }
+        }
+        if (*gave_up) {         // copies still in flight land before the CTA leaves
+            const uint64_t end = now_ns() + 1000000;
+            while (now_ns() < end) __nanosleep(1000);
+        }
+    } else if (warp == 1) {
+        // ---- products
+        if (leader && lane == 0) {
+            int s = 0, n = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int ti = first_tile; ti < tiles && ok; ti += step, ++n) {
+                const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+                // D fp32, A and B bf16, transposes, N, M
+                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
+                                       (static_cast<uint32_t>(g.a_mn) << 15) |
+                                       (static_cast<uint32_t>(g.b_mn) << 16) |
+                                       (static_cast<uint32_t>(t.bn >> 3) << 17) |
+                                       (static_cast<uint32_t>(128 * CG >> 4) << 24);
+                const uint32_t d = tmem + (n & 1) * kMaxBn;
+                const uint32_t a_step = g.a_mn ? 2048 >> 4 : 32 >> 4;
+                const uint32_t b_step = g.b_mn ? 2048 >> 4 : 32 >> 4;
+                if (!wait(smem_addr(&h->acc_empty[n & 1]), ((n >> 1) & 1) ^ 1, gave_up)) break;
+                fence_after();
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!wait(smem_addr(&h->full[s]), phase, gave_up)) { ok = false; break; }
+                    fence_after();
+                    const uint32_t a = stage0 + s * stage_bytes;
+                    const uint64_t da = smem_desc(a, g.a_mn);
+                    const uint64_t db = smem_desc(a + kATile, g.b_mn);
+#pragma unroll
+                    for (int k = 0; k < kBlockK / 16; ++k)
+                        mma_bf16<CG>(d, da + k * a_step, db + k * b_step, idesc,
+                                     kb > kb0 || k > 0);
+                    mma_commit<CG>(smem_addr(&h->empty[s]));
+                    if (++s == stages) { s = 0; phase ^= 1; }
+                }
+                if (ok) mma_commit<CG>(smem_addr(&h->acc_full[n & 1]));
+            }
+        }
+    } else {
+        // ---- epilogue
+        const int quarter = warp & 3;               // the TMEM lanes a warp may read
+        int n = 0;
+        for (int ti = first_tile; ti < tiles; ti += step, ++n) {
+            const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+            const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                 (n & 1) * kMaxBn;
+            const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            fence_after();
+            if (CG == 1 && p.split > 1) {
+                // every MMA has finished, so the stages are free
+                float *buf = reinterpret_cast<float *>(smem + (stage0 - smem_addr(smem)));
+                for (int c0 = 0; c0 < t.count; c0 += 16) {
+                    uint32_t r[16];
+                    tmem_load16(acc + c0, r);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        buf[(c0 + c) * 128 + quarter * 32 + lane] = __uint_as_float(r[c]);
+                }
+            } else {
+                finish_tile<GATED>(g, t, t.m0 + (CG == 2 ? rank * m_cta_rows : 0), acc, quarter,
+                                   lane);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bar = smem_addr(&h->acc_empty[n & 1]);
+                    bar_arrive(CG == 2 ? map_rank(bar, 0) : map_rank(bar, cluster_rank()));
+                }
+            }
+        }
+    }
+    __syncwarp();
+    if (CG == 1 && p.split > 1) {
+        cluster_sync();
+        if (!*gave_up) {
+            const Tile t = tile_at<CG, GATED>(g, p, h, first_tile);
+            finish_split<GATED>(g, t, stage0, p.split, rank);
+        }
+    }
+    fence_before();
+    if (CG == 2 || p.split > 1) cluster_sync(); else __syncthreads();
+    fence_after();
+    if (warp == 1) tmem_free<CG>(tmem, 2 * kMaxBn);
+}
+
+// ----------------------------------------------------------------- host
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once (the library does not link
+// the driver).
+EncodeTiled encoder() {
+    static EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap *map, const void *p, int rank, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box) {
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(p), dims,
+                     strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <int CG, bool GATED>
+cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CUtensorMap &b,
+                  int64_t grid, cudaStream_t stream) {
+    auto *kernel = gemm_tc_kernel<CG, GATED>;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kSmemBytes);
+    if (err == cudaSuccess && p.split > 8)
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(CG == 2 ? 2 : p.split), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 || p.split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, g, p, a, b);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err) {
+    if (!aligned16(g.a) || !aligned16(g.b) || (g.a_mn ? g.M : g.K) % 8 ||
+        (g.b_mn ? g.N : g.K) % 8 || !encoder())
+        return false;
+    const int rows_per_feature = g.gated ? 2 : 1;
+    const int64_t a_rows = static_cast<int64_t>(g.M) * rows_per_feature;
+    TcPlan p = {};
+    p.gather = g.row_token != nullptr;
+    p.split = 1;
+
+    // Pairs of CTAs on 256 x 256 tiles when they fill most of the GPU (and for
+    // expert groups, whose sizes only the device knows); else 128-row tiles
+    // with k split so that the tiles cover the SMs.
+    const int64_t pair_tiles = ceil_div(a_rows, 256) * ceil_div(g.N, kMaxBn);
+    const bool pairs = g.E || pair_tiles * 2 >= num_sms * 0.6;
+    const int unit = pairs ? 32 : 16;
+    if (!g.E) {
+        p.n_tiles = static_cast<int>(ceil_div(g.N, kMaxBn));
+        p.bn = static_cast<int>(ceil_div(ceil_div(g.N, p.n_tiles), unit)) * unit;
+        if (g.b_mn) p.bn = kMaxBn;
+        p.n_tiles = static_cast<int>(ceil_div(g.N, p.bn));
+    }
+    p.m_tiles = static_cast<int>(ceil_div(a_rows, pairs ? 256 : 128));
+    const int64_t blocks = ceil_div(g.K, kBlockK);
+    int64_t grid;
+    if (pairs) {
+        p.box_rows = g.E ? 16 : p.bn / 2;
+        const int64_t tiles = g.E ? INT32_MAX : static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+        grid = 2 * (tiles < num_sms / 2 ? tiles : num_sms / 2);
+    } else {
+        p.box_rows = p.bn;
+        const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+        while (p.split < 16 && p.split * 2 <= blocks && tiles * p.split * 2 <= num_sms)
+            p.split *= 2;
+        grid = p.split > 1 ? tiles * p.split : (tiles < num_sms ? tiles : num_sms);
+    }
+
+    CUtensorMap ma, mb;
+    bool ok;
+    if (g.a_mn) {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.M), static_cast<cuuint64_t>(g.K)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.M) * 2};
+        const cuuint32_t box[2] = {64, 64};
+        ok = encode(&ma, g.a, 2, dims, strides, box);
+    } else {
+        // [E][M][gate, up][K]: a copy of (k, both, features) interleaves the rows
+        const cuuint64_t row = static_cast<cuuint64_t>(g.K) * 2;
+        const cuuint64_t dims[4] = {static_cast<cuuint64_t>(g.K),
+                                    static_cast<cuuint64_t>(rows_per_feature),
+                                    static_cast<cuuint64_t>(g.M),
+                                    static_cast<cuuint64_t>(g.E ? g.E : 1)};
+        const cuuint64_t strides[3] = {row * g.M, row, row * a_rows};
+        const cuuint32_t box[4] = {kBlockK, static_cast<cuuint32_t>(rows_per_feature),
+                                   static_cast<cuuint32_t>(128 / rows_per_feature), 1};
+        ok = encode(&ma, g.a, 4, dims, strides, box);
+    }
+    {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.b_mn ? g.N : g.K),
+                                    static_cast<cuuint64_t>(g.b_mn ? g.K : g.b_rows)};
+        const cuuint64_t strides[1] = {dims[0] * 2};
+        const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(g.b_mn ? 64
+                                                               : p.gather ? 1 : p.box_rows)};
+        ok = ok && encode(&mb, g.b, 2, dims, strides, box);
+    }
+    if (!ok) return false;
+    if (pairs)
+        *err = g.gated ? start<2, true>(g, p, ma, mb, grid, stream)
+                       : start<2, false>(g, p, ma, mb, grid, stream);
+    else
+        *err = g.gated ? start<1, true>(g, p, ma, mb, grid, stream)
+                       : start<1, false>(g, p, ma, mb, grid, stream);
+    return true;
+}
+
+cudaError_t read_lost_waits(unsigned *count) {
+    return cudaMemcpyFromSymbol(count, lost_waits, sizeof(*count));
+}
+
+}  // namespace moef

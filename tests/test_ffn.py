@@ -468,3 +468,9 @@ def test_moe_layer(cuda_lib, T, H, I, E, K, tile):
     assert ((out.double() - ref).abs() <= bound).all()
     rel = ((out.double() - ref).norm() / ref.norm()).item()
     assert rel < 3 * R.BF16       # three roundings in a row, each at most 2^-8
+
+
+def test_no_barrier_wait_was_lost(cuda_lib):
+    """Last: none of the launches above gave up a wait."""
+    torch.cuda.synchronize()
+    assert cuda_lib.lost_waits() == 0

@@ -114,6 +114,10 @@ def test_permute_rows_bounds_every_routing(lib):
     assert lib.moe_permute_rows(4, 2, 8, 16) == 128
 
 
+def test_lost_waits_needs_a_counter(lib):
+    assert lib.moe_ffn_lost_waits(None) == E_NULL
+
+
 def test_expert_argument_errors(lib):
     for f in (lib.moe_expert_gated_ffn, lib.moe_expert_linear):
         base = dict(x=A, T=16, rows=A, offsets=A, counts=A, w=A, bias=NULL, act=0, out=A, P=32,
@@ -196,7 +200,7 @@ def test_header_struct_free_interface_matches_the_binding(lib):
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(root, "include", "moe_ffn.h")).read(),
                   flags=re.S)
     found = re.findall(r"^(?:\w+)\s+(moe_\w+)\(([^;]*)\);", text, flags=re.M)
-    assert len(found) == 11
+    assert len(found) == 12
     for name, params in found:
         fn = getattr(lib, name)
         assert len(fn.argtypes) == len(params.split(",")), name
