@@ -6,9 +6,9 @@
 // most 31 columns, and every product of a layer reads its operands as they
 // lie, k-contiguous or m-contiguous (the descriptor's transpose bits).
 //
-// A CTA is six warps: one issues the TMA copies of 64-deep k blocks into a
+// A CTA is ten warps: one issues the TMA copies of 64-deep k blocks into a
 // ring of shared-memory stages (128-byte swizzle), one lane of a second
-// issues the MMAs into TMEM, four finish tiles.  The accumulator is double
+// issues the MMAs into TMEM, eight finish tiles.  The accumulator is double
 // buffered (2 x 256 TMEM columns), so a tile's epilogue runs under the next
 // tile's products.
 //
@@ -35,7 +35,8 @@
 namespace moef {
 namespace {
 
-constexpr int kTcThreads = 192;
+constexpr int kEpilogueWarps = 8;
+constexpr int kTcThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kBlockK = 64;                     // k values per stage: one 128-byte swizzle row
 constexpr int kATile = 128 * kBlockK * 2;       // bytes of A per CTA and stage
 constexpr int kMaxBn = 256;
@@ -185,10 +186,8 @@ struct Finish {
         return static_cast<uint32_t>(p[0]) | (both ? static_cast<uint32_t>(p[1]) << 16 : 0u);
     }
 
-    // Linear: z0, z1 of row n, res its residual pair.
+    // Linear: z0, z1 of row n (bias added), res its residual pair.
     __device__ __forceinline__ void linear(int64_t n, float z0, float z1, uint32_t res) const {
-        z0 += bias[0];
-        z1 += bias[1];
         const int64_t i = n * g.M + m;
         if (g.preact) store_pair(g.preact, i, z0, z1, both, vec);
         if (g.act != MOEF_ACT_NONE) {
@@ -214,10 +213,6 @@ struct Finish {
 
     __device__ __forceinline__ void gated(int64_t n, float g0, float g1, float u0,
                                           float u1) const {
-        g0 += bias[0];
-        g1 += bias[1];
-        u0 += bias[GATED ? 2 : 0];
-        u1 += bias[GATED ? 3 : 1];
         if (g.preact) {
             store_pair(g.preact, n * 2 * g.M + m, g0, g1, both, vec);
             store_pair(g.preact, n * 2 * g.M + g.M + m, u0, u1, both, vec);
@@ -227,64 +222,163 @@ struct Finish {
     }
 };
 
-// One tile out of TMEM: this warp's 32 lanes (rows of A), all its columns.
-// Lanes swap values so that each holds two adjacent features of one column.
+// act over an array, the choice outside the loop so that its elements overlap.
+template <int N>
+__device__ __forceinline__ void act_all(float (&z)[N], int act) {
+#define MOEF_ACT_LOOP(A)                                        \
+    case A:                                                     \
+        _Pragma("unroll") for (int i = 0; i < N; ++i) z[i] = act_value(z[i], A); \
+        break;
+    switch (act) {
+        MOEF_ACT_LOOP(MOEF_ACT_SILU)
+        MOEF_ACT_LOOP(MOEF_ACT_GELU)
+        MOEF_ACT_LOOP(MOEF_ACT_GELU_TANH)
+        MOEF_ACT_LOOP(MOEF_ACT_RELU)
+        default: break;
+    }
+#undef MOEF_ACT_LOOP
+}
+
+// A 32-column chunk of a tile, element-wise: views whose pairs cannot be one
+// access (odd feature counts, 2-byte aligned outputs).
+template <bool GATED>
+__device__ __noinline__ void finish_scalar(const Finish<GATED> &f, int64_t n, float a, float b,
+                                           float c, float d) {
+    if constexpr (GATED) f.gated(n, a, b, c, d);
+    else f.linear(n, a, b, f.g.residual ? f.residual(n) : 0u);
+}
+
+// One tile out of TMEM: this warp's 32 lanes (rows of A), every other 32
+// columns from 32 * half on.  Lanes swap values so that each holds two
+// adjacent features of one column; bias, activation, residual and stores then
+// run as loops over the chunk, with nothing to decide per value, so their
+// latencies overlap (deciding per pair took 22 us per 256 x 256 tile).
 template <bool GATED>
 __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_cta, uint32_t tmem,
-                                            int quarter, int lane) {
+                                            int quarter, int half, int lane) {
     const int feature = m_cta + (GATED ? quarter * 16 + (lane >> 2) * 2
                                        : quarter * 32 + (lane & ~1));
     const Finish<GATED> f(g, feature, t.e);
     const bool odd = lane & 1, upper = lane & 2;
-    for (int c0 = 0; c0 < t.bn; c0 += 32) {
-        uint32_t r[32];
-        tmem_load32(tmem + c0, r);
-        if (c0 >= t.count) continue;
+    const int64_t M = g.M;
+    for (int c0 = 32 * half; c0 < t.bn; c0 += 64) {
+        if (c0 >= t.count) break;
+        const int64_t row = t.row0 + c0 + (GATED ? lane & 3 : lane & 1);
+        const int left = f.any ? t.count - c0 - (GATED ? lane & 3 : lane & 1) : 0;
         if constexpr (GATED) {
+            uint32_t r[32];
+            tmem_load32(tmem + c0, r);
+            float gate[16], up[16];         // [2k], [2k + 1]: features f, f + 1, column 4k
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-                // neighbours: (gate, up) of columns c + odd and c + 2 + odd
-                float gate[2], up[2];
+            for (int k = 0; k < 8; ++k) {
+                // neighbours: (gate, up) of columns 4k + odd and 4k + 2 + odd
+                float a[2], u[2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float a = __uint_as_float(r[c + 2 * k]);
-                    const float b = __uint_as_float(r[c + 2 * k + 1]);
-                    const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
-                    gate[k] = odd ? v : a;
-                    up[k] = odd ? b : v;
+                for (int j = 0; j < 2; ++j) {
+                    const float lo = __uint_as_float(r[4 * k + 2 * j]);
+                    const float hi = __uint_as_float(r[4 * k + 2 * j + 1]);
+                    const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
+                    a[j] = odd ? v : lo;
+                    u[j] = odd ? hi : v;
                 }
                 // the next feature's: lanes with `upper` keep the second column
-                const float vg = __shfl_xor_sync(0xFFFFFFFFu, upper ? gate[0] : gate[1], 2);
-                const float vu = __shfl_xor_sync(0xFFFFFFFFu, upper ? up[0] : up[1], 2);
-                const int col = c0 + c + (lane & 3);
-                if (col < t.count && f.any) {
-                    if (upper) f.gated(t.row0 + col, vg, gate[1], vu, up[1]);
-                    else f.gated(t.row0 + col, gate[0], vg, up[0], vu);
-                }
+                const float va = __shfl_xor_sync(0xFFFFFFFFu, upper ? a[0] : a[1], 2);
+                const float vu = __shfl_xor_sync(0xFFFFFFFFu, upper ? u[0] : u[1], 2);
+                gate[2 * k] = (upper ? va : a[0]) + f.bias[0];
+                gate[2 * k + 1] = (upper ? a[1] : va) + f.bias[1];
+                up[2 * k] = (upper ? vu : u[0]) + f.bias[GATED ? 2 : 0];
+                up[2 * k + 1] = (upper ? u[1] : vu) + f.bias[GATED ? 3 : 1];
             }
+            if (!f.vec) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (4 * k < left)
+                        finish_scalar<true>(f, row + 4 * k, gate[2 * k], gate[2 * k + 1],
+                                            up[2 * k], up[2 * k + 1]);
+                continue;
+            }
+            if (g.preact) {
+                uint16_t *p = g.preact + row * 2 * M + f.m;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (4 * k < left) {
+                        *reinterpret_cast<uint32_t *>(p + 8 * k * M) =
+                            pack_bf16x2(gate[2 * k], gate[2 * k + 1]);
+                        *reinterpret_cast<uint32_t *>(p + (8 * k + 1) * M) =
+                            pack_bf16x2(up[2 * k], up[2 * k + 1]);
+                    }
+            }
+            act_all(gate, g.act);
+            uint16_t *p = static_cast<uint16_t *>(g.out) + row * M + f.m;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (4 * k < left)
+                    *reinterpret_cast<uint32_t *>(p + 4 * k * M) =
+                        pack_bf16x2(gate[2 * k] * up[2 * k], gate[2 * k + 1] * up[2 * k + 1]);
         } else {
+            const int64_t at = row * M + f.m;
             uint32_t res[16];
-            if (g.residual) {       // all loads before the first store
+            if (g.residual && f.vec) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    res[k] = 2 * k < left ? *reinterpret_cast<const uint32_t *>(
+                                                g.residual + at + 2 * k * M) : 0u;
+            }
+            float z[32];                    // [2k], [2k + 1]: features m, m + 1, column 2k
+            {
+                uint32_t r[32];
+                tmem_load32(tmem + c0, r);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const int col = c0 + 2 * k + (lane & 1);
-                    res[k] = col < t.count && f.any ? f.residual(t.row0 + col) : 0u;
+                    const float lo = __uint_as_float(r[2 * k]), hi = __uint_as_float(r[2 * k + 1]);
+                    const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
+                    z[2 * k] = (odd ? v : lo) + f.bias[0];
+                    z[2 * k + 1] = (odd ? hi : v) + f.bias[1];
                 }
             }
+            if (!f.vec) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float a = __uint_as_float(r[2 * k]), b = __uint_as_float(r[2 * k + 1]);
-                const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
-                const int col = c0 + 2 * k + (lane & 1);
-                if (col < t.count && f.any)
-                    f.linear(t.row0 + col, odd ? v : a, odd ? b : v, g.residual ? res[k] : 0u);
+                for (int k = 0; k < 16; ++k)
+                    if (2 * k < left)
+                        finish_scalar<false>(f, row + 2 * k, z[2 * k], z[2 * k + 1], 0.f, 0.f);
+                continue;
+            }
+            if (g.preact) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (2 * k < left)
+                        *reinterpret_cast<uint32_t *>(g.preact + at + 2 * k * M) =
+                            pack_bf16x2(z[2 * k], z[2 * k + 1]);
+            }
+            act_all(z, g.act);
+            if (g.residual) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    z[2 * k] += bf16_lo(res[k]);
+                    z[2 * k + 1] += bf16_hi(res[k]);
+                }
+            }
+            if (g.out_f32) {
+                float *o = static_cast<float *>(g.out) + at;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (2 * k < left)
+                        *reinterpret_cast<float2 *>(o + 2 * k * M) =
+                            make_float2(z[2 * k], z[2 * k + 1]);
+            } else {
+                uint16_t *o = static_cast<uint16_t *>(g.out) + at;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (2 * k < left)
+                        *reinterpret_cast<uint32_t *>(o + 2 * k * M) =
+                            pack_bf16x2(z[2 * k], z[2 * k + 1]);
             }
         }
     }
 }
 
 // The cluster's partial tiles [column][128 rows of A] in shared memory: this
-// CTA adds and finishes every split-th 192 of the pairs.
+// CTA adds and finishes every split-th kTcThreads of the pairs.
 template <bool GATED>
 __device__ __forceinline__ void finish_split(const Gemm &g, const Tile &t, uint32_t buf, int split,
                                              int rank) {
@@ -302,7 +396,8 @@ __device__ __forceinline__ void finish_split(const Gemm &g, const Tile &t, uint3
                 const float4 v = load_remote4(map_rank(at, k));
                 s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
             }
-            f.gated(n, s.x, s.z, s.y, s.w);
+            f.gated(n, s.x + f.bias[0], s.z + f.bias[1], s.y + f.bias[GATED ? 2 : 0],
+                    s.w + f.bias[GATED ? 3 : 1]);
         } else {
             const uint32_t res = g.residual ? f.residual(n) : 0u;
             float2 s = load_remote2(map_rank(at, 0));
@@ -310,7 +405,7 @@ __device__ __forceinline__ void finish_split(const Gemm &g, const Tile &t, uint3
                 const float2 v = load_remote2(map_rank(at, k));
                 s.x += v.x; s.y += v.y;
             }
-            f.linear(n, s.x, s.y, res);
+            f.linear(n, s.x + f.bias[0], s.y + f.bias[1], res);
         }
     }
 }
@@ -340,7 +435,7 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_addr(&h->acc_full[i]), 1);
-            bar_init(smem_addr(&h->acc_empty[i]), 4 * CG);
+            bar_init(smem_addr(&h->acc_empty[i]), kEpilogueWarps * CG);
         }
         h->gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -503,6 +598,7 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
     } else {
         // ---- epilogue
         const int quarter = warp & 3;               // the TMEM lanes a warp may read
+        const int half = (warp - 2) >> 2;
         int n = 0;
         for (int ti = first_tile; ti < tiles; ti += step, ++n) {
             const Tile t = tile_at<CG, GATED>(g, p, h, ti);
@@ -514,7 +610,7 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
             if (CG == 1 && p.split > 1) {
                 // every MMA has finished, so the stages are free
                 float *buf = reinterpret_cast<float *>(smem + (stage0 - smem_addr(smem)));
-                for (int c0 = 0; c0 < t.count; c0 += 16) {
+                for (int c0 = 16 * half; c0 < t.count; c0 += 32) {
                     uint32_t r[16];
                     tmem_load16(acc + c0, r);
 #pragma unroll
@@ -523,7 +619,7 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                 }
             } else {
                 finish_tile<GATED>(g, t, t.m0 + (CG == 2 ? rank * m_cta_rows : 0), acc, quarter,
-                                   lane);
+                                   half, lane);
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -604,6 +700,25 @@ cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CU
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Columns per tile of the paired form: the width whose waves over the pairs
+// take the least time.  A tile costs its columns plus a fixed part (the A half
+// of its copies, about 32 columns' worth); 4096 rows x 4096 features run in
+// four waves of 224 columns instead of four of 256.  Transposed B is copied
+// in 64-column boxes per CTA, so its tiles are a multiple of 128.
+int pair_columns(const Gemm &g, int64_t m_tiles, int64_t pairs) {
+    int best = kMaxBn;
+    int64_t least = INT64_MAX;
+    for (int bn = kMaxBn; bn >= 128; bn -= g.b_mn ? 128 : 32) {
+        const int64_t waves = ceil_div(m_tiles * ceil_div(g.N, bn), pairs);
+        const int64_t cost = waves * (bn + 32);
+        if (cost < least) {
+            least = cost;
+            best = bn;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err) {
@@ -625,7 +740,8 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
     if (!g.E) {
         p.n_tiles = static_cast<int>(ceil_div(g.N, kMaxBn));
         p.bn = static_cast<int>(ceil_div(ceil_div(g.N, p.n_tiles), unit)) * unit;
-        if (g.b_mn) p.bn = kMaxBn;
+        if (pairs) p.bn = pair_columns(g, ceil_div(a_rows, 256), num_sms / 2);
+        else if (g.b_mn) p.bn = kMaxBn;
         p.n_tiles = static_cast<int>(ceil_div(g.N, p.bn));
     }
     p.m_tiles = static_cast<int>(ceil_div(a_rows, pairs ? 256 : 128));
