@@ -239,7 +239,11 @@ __device__ __forceinline__ void act_all(float (&z)[N], int act) {
 #undef MOEF_ACT_LOOP
 }
 
-// A 32-column chunk of a tile, element-wise: views whose pairs cannot be one
+__device__ __forceinline__ void store2(uint16_t *p, float a, float b) {
+    *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(a, b);
+}
+
+// A pair by itself: views whose pairs cannot be one
 // access (odd feature counts, 2-byte aligned outputs).
 template <bool GATED>
 __device__ __noinline__ void finish_scalar(const Finish<GATED> &f, int64_t n, float a, float b,
@@ -248,29 +252,51 @@ __device__ __noinline__ void finish_scalar(const Finish<GATED> &f, int64_t n, fl
     else f.linear(n, a, b, f.g.residual ? f.residual(n) : 0u);
 }
 
-// One tile out of TMEM: this warp's 32 lanes (rows of A), every other 32
-// columns from 32 * half on.  Lanes swap values so that each holds two
+constexpr int kChunk = 16;      // columns a warp finishes at a time
+
+// One tile out of TMEM: this warp's 32 lanes (rows of A), every other chunk
+// of columns; arrives on `done` once it has read them.  Lanes swap values so that each holds two
 // adjacent features of one column; bias, activation, residual and stores then
 // run as loops over the chunk, with nothing to decide per value, so their
 // latencies overlap (deciding per pair took 22 us per 256 x 256 tile).
-template <bool GATED>
+template <int CG, bool GATED>
 __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_cta, uint32_t tmem,
-                                            int quarter, int half, int lane) {
+                                            int quarter, int half, int lane, uint32_t done) {
     const int feature = m_cta + (GATED ? quarter * 16 + (lane >> 2) * 2
                                        : quarter * 32 + (lane & ~1));
     const Finish<GATED> f(g, feature, t.e);
     const bool odd = lane & 1, upper = lane & 2;
     const int64_t M = g.M;
-    for (int c0 = 32 * half; c0 < t.bn; c0 += 64) {
-        if (c0 >= t.count) break;
-        const int64_t row = t.row0 + c0 + (GATED ? lane & 3 : lane & 1);
-        const int left = f.any ? t.count - c0 - (GATED ? lane & 3 : lane & 1) : 0;
-        if constexpr (GATED) {
-            uint32_t r[32];
-            tmem_load32(tmem + c0, r);
-            float gate[16], up[16];         // [2k], [2k + 1]: features f, f + 1, column 4k
+    const int col = GATED ? lane & 3 : lane & 1;
+    const int end = min(t.bn, (t.count + kChunk - 1) / kChunk * kChunk);
+    if (kChunk * half >= end) {             // nothing for this warp
+        if (lane == 0) bar_arrive(done);
+        return;
+    }
+#pragma unroll 1
+    for (int c0 = kChunk * half; c0 < end; c0 += 2 * kChunk) {
+        const int64_t row = t.row0 + c0 + col;
+        const int left = f.any ? t.count - c0 - col : 0;
+        uint32_t res[kChunk / 2];
+        if constexpr (!GATED) {
+            if (g.residual && f.vec) {
+                const uint16_t *p = g.residual + row * M + f.m;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < kChunk / 2; ++k, p += 2 * M)
+                    res[k] = 2 * k < left ? *reinterpret_cast<const uint32_t *>(p) : 0u;
+            }
+        }
+        uint32_t r[kChunk];
+        tmem_load16(tmem + c0, r);
+        if (c0 + 2 * kChunk >= end) {       // the accumulator has been read
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(done);
+        }
+        if constexpr (GATED) {
+            float gate[kChunk / 2], up[kChunk / 2];     // [2k], [2k + 1]: features f, f + 1,
+#pragma unroll                                          // column 4k
+            for (int k = 0; k < kChunk / 4; ++k) {
                 // neighbours: (gate, up) of columns 4k + odd and 4k + 2 + odd
                 float a[2], u[2];
 #pragma unroll
@@ -291,7 +317,7 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
             }
             if (!f.vec) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < kChunk / 4; ++k)
                     if (4 * k < left)
                         finish_scalar<true>(f, row + 4 * k, gate[2 * k], gate[2 * k + 1],
                                             up[2 * k], up[2 * k + 1]);
@@ -300,78 +326,60 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
             if (g.preact) {
                 uint16_t *p = g.preact + row * 2 * M + f.m;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < kChunk / 4; ++k, p += 8 * M)
                     if (4 * k < left) {
-                        *reinterpret_cast<uint32_t *>(p + 8 * k * M) =
-                            pack_bf16x2(gate[2 * k], gate[2 * k + 1]);
-                        *reinterpret_cast<uint32_t *>(p + (8 * k + 1) * M) =
-                            pack_bf16x2(up[2 * k], up[2 * k + 1]);
+                        store2(p, gate[2 * k], gate[2 * k + 1]);
+                        store2(p + M, up[2 * k], up[2 * k + 1]);
                     }
             }
             act_all(gate, g.act);
             uint16_t *p = static_cast<uint16_t *>(g.out) + row * M + f.m;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (4 * k < left)
-                    *reinterpret_cast<uint32_t *>(p + 4 * k * M) =
-                        pack_bf16x2(gate[2 * k] * up[2 * k], gate[2 * k + 1] * up[2 * k + 1]);
+            for (int k = 0; k < kChunk / 4; ++k, p += 4 * M)
+                if (4 * k < left) store2(p, gate[2 * k] * up[2 * k],
+                                         gate[2 * k + 1] * up[2 * k + 1]);
         } else {
-            const int64_t at = row * M + f.m;
-            uint32_t res[16];
-            if (g.residual && f.vec) {
+            float z[kChunk];                // [2k], [2k + 1]: features m, m + 1, column 2k
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    res[k] = 2 * k < left ? *reinterpret_cast<const uint32_t *>(
-                                                g.residual + at + 2 * k * M) : 0u;
-            }
-            float z[32];                    // [2k], [2k + 1]: features m, m + 1, column 2k
-            {
-                uint32_t r[32];
-                tmem_load32(tmem + c0, r);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float lo = __uint_as_float(r[2 * k]), hi = __uint_as_float(r[2 * k + 1]);
-                    const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
-                    z[2 * k] = (odd ? v : lo) + f.bias[0];
-                    z[2 * k + 1] = (odd ? hi : v) + f.bias[1];
-                }
+            for (int k = 0; k < kChunk / 2; ++k) {
+                const float lo = __uint_as_float(r[2 * k]), hi = __uint_as_float(r[2 * k + 1]);
+                const float v = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
+                z[2 * k] = (odd ? v : lo) + f.bias[0];
+                z[2 * k + 1] = (odd ? hi : v) + f.bias[1];
             }
             if (!f.vec) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
+                for (int k = 0; k < kChunk / 2; ++k)
                     if (2 * k < left)
                         finish_scalar<false>(f, row + 2 * k, z[2 * k], z[2 * k + 1], 0.f, 0.f);
                 continue;
             }
+            const int64_t at = row * M + f.m;
             if (g.preact) {
+                uint16_t *p = g.preact + at;
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (2 * k < left)
-                        *reinterpret_cast<uint32_t *>(g.preact + at + 2 * k * M) =
-                            pack_bf16x2(z[2 * k], z[2 * k + 1]);
+                for (int k = 0; k < kChunk / 2; ++k, p += 2 * M)
+                    if (2 * k < left) store2(p, z[2 * k], z[2 * k + 1]);
             }
             act_all(z, g.act);
             if (g.residual) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
+                for (int k = 0; k < kChunk / 2; ++k) {
                     z[2 * k] += bf16_lo(res[k]);
                     z[2 * k + 1] += bf16_hi(res[k]);
                 }
             }
             if (g.out_f32) {
-                float *o = static_cast<float *>(g.out) + at;
+                float *p = static_cast<float *>(g.out) + at;
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
+                for (int k = 0; k < kChunk / 2; ++k, p += 2 * M)
                     if (2 * k < left)
-                        *reinterpret_cast<float2 *>(o + 2 * k * M) =
-                            make_float2(z[2 * k], z[2 * k + 1]);
+                        *reinterpret_cast<float2 *>(p) = make_float2(z[2 * k], z[2 * k + 1]);
             } else {
-                uint16_t *o = static_cast<uint16_t *>(g.out) + at;
+                uint16_t *p = static_cast<uint16_t *>(g.out) + at;
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (2 * k < left)
-                        *reinterpret_cast<uint32_t *>(o + 2 * k * M) =
-                            pack_bf16x2(z[2 * k], z[2 * k + 1]);
+                for (int k = 0; k < kChunk / 2; ++k, p += 2 * M)
+                    if (2 * k < left) store2(p, z[2 * k], z[2 * k + 1]);
             }
         }
     }
@@ -618,14 +626,10 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                         buf[(c0 + c) * 128 + quarter * 32 + lane] = __uint_as_float(r[c]);
                 }
             } else {
-                finish_tile<GATED>(g, t, t.m0 + (CG == 2 ? rank * m_cta_rows : 0), acc, quarter,
-                                   half, lane);
-                fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    const uint32_t bar = smem_addr(&h->acc_empty[n & 1]);
-                    bar_arrive(CG == 2 ? map_rank(bar, 0) : map_rank(bar, cluster_rank()));
-                }
+                const uint32_t bar = smem_addr(&h->acc_empty[n & 1]);
+                finish_tile<CG, GATED>(g, t, t.m0 + (CG == 2 ? rank * m_cta_rows : 0), acc,
+                                       quarter, half, lane,
+                                       map_rank(bar, CG == 2 ? 0 : cluster_rank()));
             }
         }
     }

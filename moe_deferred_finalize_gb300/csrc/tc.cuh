@@ -64,16 +64,18 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
                  : "memory");
 }
 
-// bar: a shared::cluster address (this CTA's own or another's).
+// bar: a shared::cluster address (this CTA's own or another's).  Relaxed: what
+// it announces (TMEM columns read) is complete before it, and a release would
+// wait for the thread's global stores.
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
 
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile("{\n.reg .pred p;\n"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
                  "selp.u32 %0, 1, 0, p;\n}"
                  : "=r"(done) : "r"(bar), "r"(parity) : "memory");
     return done != 0;
