@@ -44,6 +44,7 @@ constexpr int kMaxStages = 16;
 constexpr int kHeader = 6144;                   // barriers, tables
 constexpr int kSmemBytes = 227 * 1024;
 constexpr int kStageArea = kSmemBytes - kHeader - 1024;     // after rounding up to 1024
+constexpr int kBand = 8;                        // feature tiles per band (see tile_at)
 constexpr uint64_t kWaitLimitNs = 2000000000;   // a wait gives up after two seconds
 
 // How one launch is cut up (see choose_plan).
@@ -127,8 +128,12 @@ __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const He
         r.row0 = first + static_cast<int64_t>(n) * r.bn;
         r.count = min(r.bn, count - n * r.bn);
     } else {
-        m = t / p.n_tiles;
-        n = t % p.n_tiles;
+        // bands of kBand feature tiles, columns outside: the tiles in flight form
+        // a block, so both operands are shared through L2
+        const int band = t / (kBand * p.n_tiles), in_band = t - band * kBand * p.n_tiles;
+        const int wide = min(kBand, p.m_tiles - band * kBand);
+        m = band * kBand + in_band % wide;
+        n = in_band / wide;
         r.bn = p.bn;
         r.row0 = static_cast<int64_t>(n) * r.bn;
         r.count = static_cast<int>(min(static_cast<int64_t>(r.bn), g.N - r.row0));
@@ -386,34 +391,69 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
 }
 
 // The cluster's partial tiles [column][128 rows of A] in shared memory: this
-// CTA adds and finishes every split-th kTcThreads of the pairs.
+// CTA adds and finishes its share of the columns.  A thread keeps one pair of
+// features and takes kBatch columns at a time from four CTAs at a time, so
+// that 16 remote reads (about 0.7 us each) are in flight.
 template <bool GATED>
 __device__ __forceinline__ void finish_split(const Gemm &g, const Tile &t, uint32_t buf, int split,
                                              int rank) {
-    constexpr int kPairs = GATED ? 32 : 64;
-    const int items = t.count * kPairs;
-    for (int i = rank * kTcThreads + threadIdx.x; i < items; i += split * kTcThreads) {
-        const int col = i / kPairs, pair = i % kPairs;
-        const uint32_t at = buf + (col * 128 + pair * (GATED ? 4 : 2)) * 4;
-        const Finish<GATED> f(g, t.m0 + 2 * pair, t.e);
-        if (!f.any) continue;
-        const int64_t n = t.row0 + col;
-        if constexpr (GATED) {
-            float4 s = load_remote4(map_rank(at, 0));
-            for (int k = 1; k < split; ++k) {
-                const float4 v = load_remote4(map_rank(at, k));
-                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    constexpr int kPairs = GATED ? 32 : 64, kBatch = 4, kRanks = 4;
+    constexpr int kColumns = kTcThreads / kPairs;       // columns at a time per CTA
+    const int pair = threadIdx.x % kPairs;
+    const Finish<GATED> f(g, t.m0 + 2 * pair, t.e);
+    if (!f.any) return;
+    const uint32_t at = buf + pair * (GATED ? 16 : 8);
+    const int step = split * kColumns;
+    for (int c0 = rank * kColumns + threadIdx.x / kPairs; c0 < t.count; c0 += kBatch * step) {
+        uint32_t res[kBatch];
+        float4 sum[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int col = c0 + i * step;
+            res[i] = !GATED && g.residual && col < t.count ? f.residual(t.row0 + col) : 0u;
+        }
+        for (int k0 = 0; k0 < split; k0 += kRanks) {
+            float4 v[kRanks][kBatch];
+#pragma unroll
+            for (int k = 0; k < kRanks; ++k) {
+                const uint32_t from = map_rank(at, min(k0 + k, split - 1));
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int col = c0 + i * step;
+                    if (col < t.count && k0 + k < split) {
+                        if constexpr (GATED) {
+                            v[k][i] = load_remote4(from + col * 512);
+                        } else {
+                            const float2 w = load_remote2(from + col * 512);
+                            v[k][i].x = w.x;
+                            v[k][i].y = w.y;
+                        }
+                    }
+                }
             }
-            f.gated(n, s.x + f.bias[0], s.z + f.bias[1], s.y + f.bias[GATED ? 2 : 0],
-                    s.w + f.bias[GATED ? 3 : 1]);
-        } else {
-            const uint32_t res = g.residual ? f.residual(n) : 0u;
-            float2 s = load_remote2(map_rank(at, 0));
-            for (int k = 1; k < split; ++k) {
-                const float2 v = load_remote2(map_rank(at, k));
-                s.x += v.x; s.y += v.y;
-            }
-            f.linear(n, s.x + f.bias[0], s.y + f.bias[1], res);
+#pragma unroll
+            for (int k = 0; k < kRanks; ++k)
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    sum[i].x += v[k][i].x;
+                    sum[i].y += v[k][i].y;
+                    if constexpr (GATED) {
+                        sum[i].z += v[k][i].z;
+                        sum[i].w += v[k][i].w;
+                    }
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int col = c0 + i * step;
+            if (col >= t.count) break;
+            if constexpr (GATED)
+                f.gated(t.row0 + col, sum[i].x + f.bias[0], sum[i].z + f.bias[1],
+                        sum[i].y + f.bias[GATED ? 2 : 0], sum[i].w + f.bias[GATED ? 3 : 1]);
+            else
+                f.linear(t.row0 + col, sum[i].x + f.bias[0], sum[i].y + f.bias[1], res[i]);
         }
     }
 }
@@ -449,6 +489,11 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<CG>(smem_addr(&h->tmem), 2 * kMaxBn);
+    // Launched as a dependent of the previous kernel on the stream: up to here
+    // nothing in global memory was touched.  The next kernel may launch at
+    // once; its CTAs get their SMs as ours leave them.
+    allow_next_kernel();
+    wait_previous_kernel();
     if (warp == 0) {
         if (g.E) {      // column tiles of each expert
             int most = 0;
@@ -487,7 +532,7 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
         }
     }
     fence_before();
-    if (CG == 2 || p.split > 1) cluster_sync(); else __syncthreads();
+    if (CG == 2) cluster_sync(); else __syncthreads();
     fence_after();
 
     const int tiles = h->tiles;
@@ -694,11 +739,13 @@ cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CU
     cfg.blockDim = dim3(kTcThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {static_cast<unsigned>(CG == 2 ? 2 : p.split), 1, 1};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(CG == 2 ? 2 : p.split), 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 || p.split > 1 ? 1 : 0;
+    cfg.numAttrs = CG == 2 || p.split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, g, p, a, b);
 }
 

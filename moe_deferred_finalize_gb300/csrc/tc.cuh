@@ -19,6 +19,19 @@ __device__ __forceinline__ uint64_t now_ns() {
     return t;
 }
 
+// ------------------------------------------------- dependent launches
+
+// Waits until the previous kernel on the stream has completed and flushed (at
+// once when this one was not launched as its programmatic dependent).
+__device__ __forceinline__ void wait_previous_kernel() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Lets the next kernel begin launching.
+__device__ __forceinline__ void allow_next_kernel() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------- cluster
 
 __device__ __forceinline__ uint32_t cluster_rank() {
