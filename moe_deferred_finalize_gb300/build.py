@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_finalize.so")
 SOURCES = ["finalize.cu", "allreduce.cu", "unfused.cu", "routing.cu", "api.cu", "noalloc.cu",
-           "ffn_simple.cu", "ffn_gemm.cu", "ffn_backward.cu", "permute.cu", "ffn_api.cu"]
+           "ffn_simple.cu", "ffn_gemm.cu", "ffn_decode.cu", "ffn_backward.cu", "permute.cu", "ffn_api.cu"]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3",
               "-std=c++17", "-Xcompiler", "-fPIC,-O2,-Wall", "-I", INCLUDE, "-I", CSRC]

@@ -34,7 +34,9 @@ moef_status run_gemm(const Gemm &g, cudaStream_t stream) {
     const moef_status st = cuda_status(moef::current_sms(&sms));
     if (st != MOEF_OK) return st;
     cudaError_t err = cudaSuccess;
-    if (!moef::launch_gemm_tc(g, sms, stream, &err)) err = moef::launch_gemm_simple(g, stream);
+    if (!moef::launch_gemm_decode(g, sms, stream, &err) &&
+        !moef::launch_gemm_tc(g, sms, stream, &err))
+        err = moef::launch_gemm_simple(g, stream);
     return cuda_status(err);
 }
 

@@ -145,7 +145,7 @@ __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const He
 // ------------------------------------------------------------- epilogue
 
 __device__ __forceinline__ float bf16_value(const uint16_t *p, int64_t i) {
-    return __uint_as_float(static_cast<uint32_t>(__ldg(p + i)) << 16);
+    return __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
 }
 
 __device__ __forceinline__ void store_pair(uint16_t *p, int64_t i, float a, float b, bool both,
