@@ -6,9 +6,11 @@
 // most 31 columns, and every product of a layer reads its operands as they
 // lie, k-contiguous or m-contiguous (the descriptor's transpose bits).
 //
-// A CTA is ten warps: one issues the TMA copies of 64-deep k blocks into a
-// ring of shared-memory stages (128-byte swizzle), one lane of a second
-// issues the MMAs into TMEM, eight finish tiles.  The accumulator is double
+// A CTA is eleven warps: two issue the TMA copies of 64-deep k blocks of A and
+// of B into a ring of shared-memory stages (128-byte swizzle), one lane of a
+// third issues the MMAs into TMEM, eight finish tiles.  (One warp for both
+// copies needed 430 clocks a block, near the 512 that the MMAs of the widest
+// tile take.)  The accumulator is double
 // buffered (2 x 256 TMEM columns), so a tile's epilogue runs under the next
 // tile's products.
 //
@@ -26,8 +28,11 @@
 //           all SMs.  The partial accumulators meet in shared memory, and each
 //           CTA of the cluster adds and finishes its share of the tile, in
 //           rank order (equal calls give equal bits).
-#include <mutex>
-
+#ifdef TUNE
+#include <algorithm>
+#include <cstdio>
+#include <cstdlib>
+#endif
 #include "ffn.cuh"
 #include "tc.cuh"
 #include "vec.cuh"
@@ -36,7 +41,8 @@ namespace moef {
 namespace {
 
 constexpr int kEpilogueWarps = 8;
-constexpr int kTcThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kCopyWarp = 2 + kEpilogueWarps;    // copies B; warp 0 copies A
+constexpr int kTcThreads = 32 * (kCopyWarp + 1);
 constexpr int kBlockK = 64;                     // k values per stage: one 128-byte swizzle row
 constexpr int kATile = 128 * kBlockK * 2;       // bytes of A per CTA and stage
 constexpr int kMaxBn = 256;
@@ -45,7 +51,7 @@ constexpr int kHeader = 6144;                   // barriers, tables
 constexpr int kSmemBytes = 227 * 1024;
 constexpr int kStageArea = kSmemBytes - kHeader - 1024;     // after rounding up to 1024
 constexpr int kBand = 8;                        // feature tiles per band (see tile_at)
-constexpr uint64_t kWaitLimitNs = 2000000000;   // a wait gives up after two seconds
+constexpr long long kWaitLimit = 4000000000;     // clocks (two seconds) until a wait gives up
 
 // How one launch is cut up (see choose_plan).
 struct TcPlan {
@@ -71,19 +77,18 @@ __device__ unsigned int lost_waits;
 // Waits for a barrier's phase; false when the wait gave up (here or in
 // another warp of the CTA), upon which every role leaves its loops.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
-    for (int i = 0; i < 64; ++i)
-        if (bar_try(bar, parity)) return true;
-    const uint64_t end = now_ns() + kWaitLimitNs;
-    for (;;) {
-        for (int i = 0; i < 32; ++i)
-            if (bar_try(bar, parity)) return true;
+    if (bar_try(bar, parity)) return true;
+    const long long begin = clock64();
+    for (int i = 1; !bar_try(bar, parity); ++i) {
+        if (i % 64) continue;
         if (*gave_up) return false;
-        if (now_ns() > end) {
+        if (clock64() - begin > kWaitLimit) {
             *gave_up = 1;
             atomicAdd(&lost_waits, 1u);
             return false;
         }
     }
+    return true;
 }
 
 // Shared-memory matrix descriptors, 128-byte swizzle.  k-contiguous: 8-row
@@ -394,17 +399,18 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
 // CTA adds and finishes its share of the columns.  A thread keeps one pair of
 // features and takes kBatch columns at a time from four CTAs at a time, so
 // that 16 remote reads (about 0.7 us each) are in flight.
-template <bool GATED>
-__device__ __forceinline__ void finish_split(const Gemm &g, const Tile &t, uint32_t buf, int split,
-                                             int rank) {
+template <int CG, bool GATED>
+__device__ __forceinline__ void finish_split(const Gemm &g, const Tile &t, int m_cta, uint32_t buf,
+                                             int split, int part, int half) {
     constexpr int kPairs = GATED ? 32 : 64, kBatch = 4, kRanks = 4;
     constexpr int kColumns = kTcThreads / kPairs;       // columns at a time per CTA
+    if (static_cast<int>(threadIdx.x) >= kColumns * kPairs) return;
     const int pair = threadIdx.x % kPairs;
-    const Finish<GATED> f(g, t.m0 + 2 * pair, t.e);
+    const Finish<GATED> f(g, m_cta + 2 * pair, t.e);
     if (!f.any) return;
     const uint32_t at = buf + pair * (GATED ? 16 : 8);
     const int step = split * kColumns;
-    for (int c0 = rank * kColumns + threadIdx.x / kPairs; c0 < t.count; c0 += kBatch * step) {
+    for (int c0 = part * kColumns + threadIdx.x / kPairs; c0 < t.count; c0 += kBatch * step) {
         uint32_t res[kBatch];
         float4 sum[kBatch];
 #pragma unroll
@@ -417,7 +423,7 @@ __device__ __forceinline__ void finish_split(const Gemm &g, const Tile &t, uint3
             float4 v[kRanks][kBatch];
 #pragma unroll
             for (int k = 0; k < kRanks; ++k) {
-                const uint32_t from = map_rank(at, min(k0 + k, split - 1));
+                const uint32_t from = map_rank(at, min(k0 + k, split - 1) * CG + half);
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -470,8 +476,11 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
     Header *h = reinterpret_cast<Header *>(smem + (base - smem_addr(smem)));
     const uint32_t stage0 = base + kHeader;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    // the CTA's place in its cluster: which part of k, and which half of a pair
     const int rank = CG == 2 || p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const bool leader = CG == 1 || rank == 0;
+    const int part = rank / CG, half = rank % CG, lead = part * CG;
+    const bool leader = half == 0;
+    const uint16_t pair = static_cast<uint16_t>(3 << lead);
     volatile int *gave_up = &h->gave_up;
 
     if (threadIdx.x == 0) {
@@ -542,80 +551,124 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
     const uint32_t stage_bytes = kATile + b_bytes;
     const int stages = min(kMaxStages, static_cast<int>(kStageArea / stage_bytes));
     const int blocks = (g.K + kBlockK - 1) / kBlockK;
-    const int kb0 = CG == 1 ? static_cast<int>(static_cast<int64_t>(blocks) * rank / p.split) : 0;
-    const int kb1 = CG == 1 ? static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / p.split)
-                            : blocks;
-    const int group = CG == 2 ? 2 : p.split;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(blocks) * part / p.split);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / p.split);
+    const int group = CG * p.split;
     const int first_tile = blockIdx.x / group, step = gridDim.x / group;
     const int m_cta_rows = GATED ? 64 : 128;        // features per CTA
 
     if (warp == 0) {
-        // ---- copies
-        int s = 0;
-        uint32_t phase = 1;
-        for (int ti = first_tile; ti < tiles; ti += step) {
-            const Tile t = tile_at<CG, GATED>(g, p, h, ti);
-            const int bnc = t.bn / CG;
-            const int m0 = t.m0 + (CG == 2 ? rank * m_cta_rows : 0);
-            const int64_t row0 = t.row0 + (CG == 2 ? rank * bnc : 0);
-            const int boxes = g.b_mn ? (bnc + 63) / 64 : (bnc + p.box_rows - 1) / p.box_rows;
-            const uint32_t b_tx = p.gather ? bnc * 128u
-                                  : g.b_mn ? boxes * 8192u : boxes * p.box_rows * 128u;
-            int4 rows = make_int4(-1, -1, -1, -1);
-            if (p.gather && 4 * lane < bnc) {
-                const int valid = t.count - (CG == 2 ? rank * bnc : 0) - 4 * lane;
-                const int32_t *at = g.row_token + row0 + 4 * lane;
-                if (valid > 0) rows.x = at[0];
-                if (valid > 1) rows.y = at[1];
-                if (valid > 2) rows.z = at[2];
-                if (valid > 3) rows.w = at[3];
-            }
+        // ---- copies of A, and the stages' byte counts
+        if (elect_one()) {
+            int s = 0;
+            uint32_t phase = 1;
             bool ok = true;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                const uint32_t full = smem_addr(&h->full[s]);
-                ok = wait(smem_addr(&h->empty[s]), phase, gave_up);
-                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-                const uint32_t a = stage0 + s * stage_bytes, b = a + kATile;
-                const uint32_t bar = CG == 2 ? map_rank(full, 0) : full;
-                if (lane == 0) {
-                    if (leader) bar_expect(full, CG * (kATile + b_tx));
-                    if (g.a_mn) {
-                        tma_2d<CG>(a, &map_a, m0, kb * kBlockK, bar);
-                        tma_2d<CG>(a + 8192, &map_a, m0 + 64, kb * kBlockK, bar);
-                    } else {
-                        tma_4d<CG>(a, &map_a, kb * kBlockK, 0, m0, t.e, bar);
+            for (int ti = first_tile; ti < tiles && ok; ti += step) {
+                const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+                const int bnc = t.bn / CG, m0 = t.m0 + half * m_cta_rows;
+                const uint32_t b_tx = p.gather ? bnc * 128u
+                                      : g.b_mn ? (bnc + 63) / 64 * 8192u
+                                               : (bnc + p.box_rows - 1) / p.box_rows *
+                                                     p.box_rows * 128u;
+                const uint32_t tx = CG * (kATile + b_tx);
+                auto blocks_of = [&](auto copy) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!wait(smem_addr(&h->empty[s]), phase, gave_up)) return false;
+                        const uint32_t full = smem_addr(&h->full[s]);
+                        if (leader) bar_expect(full, tx);
+                        copy(stage0 + s * stage_bytes, kb * kBlockK,
+                             CG == 2 ? map_rank(full, lead) : full);
+                        if (++s == stages) { s = 0; phase ^= 1; }
                     }
-                    if (g.b_mn) {
-                        for (int i = 0; i < boxes; ++i)
-                            tma_2d<CG>(b + i * 8192, &map_b, static_cast<int>(row0) + i * 64,
-                                       kb * kBlockK, bar);
-                    } else if (!p.gather) {
-                        for (int i = 0; i < boxes; ++i)
-                            tma_2d<CG>(b + i * p.box_rows * 128, &map_b, kb * kBlockK,
-                                       static_cast<int>(row0) + i * p.box_rows, bar);
-                    }
-                }
-                if (p.gather) {
-                    __syncwarp();
-                    if (4 * lane < bnc)
-                        tma_gather4<CG>(b + lane * 512, &map_b, kb * kBlockK, rows, bar);
-                }
+                    return true;
+                };
+                if (g.a_mn)
+                    ok = blocks_of([&](uint32_t a, int k, uint32_t bar) {
+                        tma_2d<CG>(a, &map_a, m0, k, bar);
+                        tma_2d<CG>(a + 8192, &map_a, m0 + 64, k, bar);
+                    });
+                else
+                    ok = blocks_of([&](uint32_t a, int k, uint32_t bar) {
+                        tma_4d<CG>(a, &map_a, k, 0, m0, t.e, bar);
+                    });
+            }
+            // every stage handed back: no copy or arrival is left in flight
+            for (int i = 0; i < stages; ++i) {
+                if (!wait(smem_addr(&h->empty[s]), phase, gave_up)) break;
                 if (++s == stages) { s = 0; phase ^= 1; }
             }
-            if (!ok) break;
+            if (*gave_up)       // copies still in flight land before the CTA leaves
+                for (const long long begin = clock64(); clock64() - begin < 2000000;)
+                    __nanosleep(1000);
         }
-        // every stage handed back: no copy or arrival is left in flight
-        for (int i = 0; i < stages; ++i) {
-            if (!wait(smem_addr(&h->empty[s]), phase, gave_up)) break;
-            if (++s == stages) { s = 0; phase ^= 1; }
+    } else if (warp == kCopyWarp) {
+        // ---- copies of B: one lane, or the warp when it gathers rows
+        int s = 0;
+        uint32_t phase = 1;
+        if (p.gather) {
+            for (int ti = first_tile; ti < tiles; ti += step) {
+                const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+                const int bnc = t.bn / CG;
+                int4 rows = make_int4(-1, -1, -1, -1);      // -1: a row of zeros
+                if (4 * lane < bnc) {
+                    const int valid = t.count - half * bnc - 4 * lane;
+                    const int32_t *at = g.row_token + t.row0 + half * bnc + 4 * lane;
+                    if (valid > 0) rows.x = at[0];
+                    if (valid > 1) rows.y = at[1];
+                    if (valid > 2) rows.z = at[2];
+                    if (valid > 3) rows.w = at[3];
+                }
+                bool ok = true;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = wait(smem_addr(&h->empty[s]), phase, gave_up);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const uint32_t full = smem_addr(&h->full[s]);
+                    if (4 * lane < bnc)
+                        tma_gather4<CG>(stage0 + s * stage_bytes + kATile + lane * 512, &map_b,
+                                        kb * kBlockK, rows, CG == 2 ? map_rank(full, lead) : full);
+                    if (++s == stages) { s = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+            }
+        } else if (elect_one()) {
+            bool ok = true;
+            for (int ti = first_tile; ti < tiles && ok; ti += step) {
+                const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+                const int bnc = t.bn / CG;
+                const int row0 = static_cast<int>(t.row0 + half * bnc);
+                const int rows = g.b_mn ? 64 : p.box_rows;      // of one copy
+                const int boxes = (bnc + rows - 1) / rows;
+                auto blocks_of = [&](auto copy) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!wait(smem_addr(&h->empty[s]), phase, gave_up)) return false;
+                        const uint32_t full = smem_addr(&h->full[s]);
+                        copy(stage0 + s * stage_bytes + kATile, kb * kBlockK,
+                             CG == 2 ? map_rank(full, lead) : full);
+                        if (++s == stages) { s = 0; phase ^= 1; }
+                    }
+                    return true;
+                };
+                if (g.b_mn)
+                    ok = blocks_of([&](uint32_t b, int k, uint32_t bar) {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_2d<CG>(b + i * 8192, &map_b, row0 + i * 64, k, bar);
+                    });
+                else if (boxes == 1)
+                    ok = blocks_of([&](uint32_t b, int k, uint32_t bar) {
+                        tma_2d<CG>(b, &map_b, k, row0, bar);
+                    });
+                else
+                    ok = blocks_of([&](uint32_t b, int k, uint32_t bar) {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_2d<CG>(b + i * rows * 128, &map_b, k, row0 + i * rows, bar);
+                    });
+            }
         }
-        if (*gave_up) {         // copies still in flight land before the CTA leaves
-            const uint64_t end = now_ns() + 1000000;
-            while (now_ns() < end) __nanosleep(1000);
-        }
+        __syncwarp();
     } else if (warp == 1) {
         // ---- products
-        if (leader && lane == 0) {
+        if (leader && elect_one()) {
             int s = 0, n = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -642,16 +695,16 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                     for (int k = 0; k < kBlockK / 16; ++k)
                         mma_bf16<CG>(d, da + k * a_step, db + k * b_step, idesc,
                                      kb > kb0 || k > 0);
-                    mma_commit<CG>(smem_addr(&h->empty[s]));
+                    mma_commit<CG>(smem_addr(&h->empty[s]), pair);
                     if (++s == stages) { s = 0; phase ^= 1; }
                 }
-                if (ok) mma_commit<CG>(smem_addr(&h->acc_full[n & 1]));
+                if (ok) mma_commit<CG>(smem_addr(&h->acc_full[n & 1]), pair);
             }
         }
     } else {
         // ---- epilogue
         const int quarter = warp & 3;               // the TMEM lanes a warp may read
-        const int half = (warp - 2) >> 2;
+        const int side = (warp - 2) >> 2;
         int n = 0;
         for (int ti = first_tile; ti < tiles; ti += step, ++n) {
             const Tile t = tile_at<CG, GATED>(g, p, h, ti);
@@ -660,10 +713,10 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
             const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             fence_after();
-            if (CG == 1 && p.split > 1) {
+            if (p.split > 1) {
                 // every MMA has finished, so the stages are free
                 float *buf = reinterpret_cast<float *>(smem + (stage0 - smem_addr(smem)));
-                for (int c0 = 16 * half; c0 < t.count; c0 += 32) {
+                for (int c0 = 16 * side; c0 < t.count; c0 += 32) {
                     uint32_t r[16];
                     tmem_load16(acc + c0, r);
 #pragma unroll
@@ -672,18 +725,17 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                 }
             } else {
                 const uint32_t bar = smem_addr(&h->acc_empty[n & 1]);
-                finish_tile<CG, GATED>(g, t, t.m0 + (CG == 2 ? rank * m_cta_rows : 0), acc,
-                                       quarter, half, lane,
-                                       map_rank(bar, CG == 2 ? 0 : cluster_rank()));
+                finish_tile<CG, GATED>(g, t, t.m0 + half * m_cta_rows, acc, quarter, side, lane,
+                                       map_rank(bar, CG == 2 ? lead : cluster_rank()));
             }
         }
     }
     __syncwarp();
-    if (CG == 1 && p.split > 1) {
+    if (p.split > 1) {
         cluster_sync();
         if (!*gave_up) {
             const Tile t = tile_at<CG, GATED>(g, p, h, first_tile);
-            finish_split<GATED>(g, t, stage0, p.split, rank);
+            finish_split<CG, GATED>(g, t, t.m0 + half * m_cta_rows, stage0, p.split, part, half);
         }
     }
     fence_before();
@@ -731,7 +783,7 @@ cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CU
     auto *kernel = gemm_tc_kernel<CG, GATED>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kSmemBytes);
-    if (err == cudaSuccess && p.split > 8)
+    if (err == cudaSuccess && CG * p.split > 8)
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -743,9 +795,9 @@ cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CU
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {static_cast<unsigned>(CG == 2 ? 2 : p.split), 1, 1};
+    attr[1].val.clusterDim = {static_cast<unsigned>(CG * p.split), 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 || p.split > 1 ? 2 : 1;
+    cfg.numAttrs = CG * p.split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, g, p, a, b);
 }
 
@@ -786,7 +838,7 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
     // expert groups, whose sizes only the device knows); else 128-row tiles
     // with k split so that the tiles cover the SMs.
     const int64_t pair_tiles = ceil_div(a_rows, 256) * ceil_div(g.N, kMaxBn);
-    const bool pairs = g.E || pair_tiles * 2 >= num_sms * 0.6;
+    bool pairs = g.E || pair_tiles * 2 >= num_sms * 0.6;
     const int unit = pairs ? 32 : 16;
     if (!g.E) {
         p.n_tiles = static_cast<int>(ceil_div(g.N, kMaxBn));
@@ -810,6 +862,19 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
         grid = p.split > 1 ? tiles * p.split : (tiles < num_sms ? tiles : num_sms);
     }
 
+#ifdef TUNE
+    if (const char *e = getenv("TUNE_PLAN")) {
+        int cg, bn, sp;
+        if (sscanf(e, "%d,%d,%d", &cg, &bn, &sp) == 3 && !g.E) {
+            p.bn = bn; p.split = sp; p.n_tiles = (int)ceil_div(g.N, bn);
+            p.m_tiles = (int)ceil_div(a_rows, 128 * cg);
+            p.box_rows = bn / cg;
+            const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+            grid = sp > 1 ? tiles * sp * cg : std::min<int64_t>(tiles, num_sms / cg) * cg;
+            pairs = cg == 2;
+        }
+    }
+#endif
     CUtensorMap ma, mb;
     bool ok;
     if (g.a_mn) {

@@ -13,10 +13,14 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
+// One lane of the (full) warp, the same one every time.  A branch on it is
+// known to hold one thread, so the single-thread instructions in it (copies,
+// MMAs) need no loop over lanes.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(one));
+    return one != 0;
 }
 
 // ------------------------------------------------- dependent launches
@@ -185,12 +189,13 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
                      : "memory");
 }
 
-// Arrives on `bar` (in both CTAs of a pair) once the MMAs issued so far are done.
+// Arrives on `bar` once the MMAs issued so far are done; with CG = 2 in both
+// CTAs of the pair (`pair`: a mask of their ranks).
 template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t pair) {
     if constexpr (CG == 2)
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast"
-                     "::cluster.b64 [%0], %1;" ::"r"(bar), "h"(static_cast<uint16_t>(3))
+                     "::cluster.b64 [%0], %1;" ::"r"(bar), "h"(pair)
                      : "memory");
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
