@@ -28,11 +28,6 @@
 //           all SMs.  The partial accumulators meet in shared memory, and each
 //           CTA of the cluster adds and finishes its share of the tile, in
 //           rank order (equal calls give equal bits).
-#ifdef TUNE
-#include <algorithm>
-#include <cstdio>
-#include <cstdlib>
-#endif
 #include "ffn.cuh"
 #include "tc.cuh"
 #include "vec.cuh"
@@ -53,7 +48,7 @@ constexpr int kStageArea = kSmemBytes - kHeader - 1024;     // after rounding up
 constexpr int kBand = 8;                        // feature tiles per band (see tile_at)
 constexpr long long kWaitLimit = 4000000000;     // clocks (two seconds) until a wait gives up
 
-// How one launch is cut up (see choose_plan).
+// How one launch is cut up (see choose_cut).
 struct TcPlan {
     int split;          // CTAs along k
     int bn;             // columns per tile; 0: from the expert counts, on the device
@@ -803,20 +798,53 @@ cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CU
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Columns per tile of the paired form: the width whose waves over the pairs
-// take the least time.  A tile costs its columns plus a fixed part (the A half
-// of its copies, about 32 columns' worth); 4096 rows x 4096 features run in
-// four waves of 224 columns instead of four of 256.  Transposed B is copied
-// in 64-column boxes per CTA, so its tiles are a multiple of 128.
-int pair_columns(const Gemm &g, int64_t m_tiles, int64_t pairs) {
-    int best = kMaxBn;
-    int64_t least = INT64_MAX;
-    for (int bn = kMaxBn; bn >= 128; bn -= g.b_mn ? 128 : 32) {
-        const int64_t waves = ceil_div(m_tiles * ceil_div(g.N, bn), pairs);
-        const int64_t cost = waves * (bn + 32);
-        if (cost < least) {
-            least = cost;
-            best = bn;
+// How a product that is not grouped is cut: one CTA or a pair per tile, columns
+// per tile, parts of k.  Every choice is priced in SM clocks and the cheapest
+// taken.  The figures are fits to sweeps over 17..4096 rows:
+//   - a 64-deep k block takes the MMAs (2.35 clocks a column), the copies (68
+//     bytes a clock into an SM) or the issue of both (290 clocks), whichever
+//     is longest;
+//   - the epilogue of a tile takes 16 clocks a column, under the next tile's
+//     products except for the last one; tiles joined over a cluster 5000
+//     clocks (two barriers, remote reads) and 45 a column;
+//   - HBM delivers 3580 bytes a clock.
+// Examples: 512 x 4096 x 7168 (gated) runs as 64 pairs of 128 columns, 25 us,
+// against 34 us with 256 columns and k in two parts; 300 x 256 x 7168 as 40
+// tiles with k in eight parts, 10.5 us, against 23 us unsplit.
+struct Cut {
+    int cg, bn, split;
+};
+
+Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms) {
+    const int64_t blocks = (g.K + kBlockK - 1) / kBlockK;
+    const double hbm = 2.0 * (static_cast<double>(a_rows) * g.K +
+                              static_cast<double>(g.N) * g.K +
+                              static_cast<double>(g.N) * g.M) / 3580.0;
+    Cut best = {2, kMaxBn, 1};
+    double least = 1e300;
+    for (int cg = 1; cg <= 2; ++cg) {
+        const int64_t m_tiles = ceil_div(a_rows, 128 * cg);
+        const int unit = g.b_mn ? 64 * cg : 32;     // transposed B is copied 64 columns at a time
+        for (int bn = unit; bn <= kMaxBn; bn += unit) {
+            const int64_t tiles = m_tiles * ceil_div(g.N, bn);
+            const double bytes = kATile + bn / cg * 128.0;
+            double block = 2.35 * bn > 290.0 ? 2.35 * bn : 290.0;
+            if (bytes / 68.0 > block) block = bytes / 68.0;
+            for (int split = 1; split * cg <= 16 && split <= blocks; split *= 2) {
+                if (split > 1 && tiles * split * cg > num_sms) break;
+                const double epilogue = split > 1 ? 5000.0 + 45.0 * bn : 16.0 * bn;
+                double unit_time = static_cast<double>(ceil_div(blocks, split)) * block;
+                if (split == 1 && epilogue > unit_time) unit_time = epilogue;
+                double cost = static_cast<double>(ceil_div(tiles * split, num_sms / cg)) *
+                              unit_time;
+                if (cost < hbm) cost = hbm;
+                cost += epilogue;
+                if (cost < least) {
+                    least = cost;
+                    best = {cg, bn, split};
+                }
+            }
+            if (bn >= g.N) break;
         }
     }
     return best;
@@ -834,47 +862,28 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
     p.gather = g.row_token != nullptr;
     p.split = 1;
 
-    // Pairs of CTAs on 256 x 256 tiles when they fill most of the GPU (and for
-    // expert groups, whose sizes only the device knows); else 128-row tiles
-    // with k split so that the tiles cover the SMs.
-    const int64_t pair_tiles = ceil_div(a_rows, 256) * ceil_div(g.N, kMaxBn);
-    bool pairs = g.E || pair_tiles * 2 >= num_sms * 0.6;
-    const int unit = pairs ? 32 : 16;
-    if (!g.E) {
-        p.n_tiles = static_cast<int>(ceil_div(g.N, kMaxBn));
-        p.bn = static_cast<int>(ceil_div(ceil_div(g.N, p.n_tiles), unit)) * unit;
-        if (pairs) p.bn = pair_columns(g, ceil_div(a_rows, 256), num_sms / 2);
-        else if (g.b_mn) p.bn = kMaxBn;
-        p.n_tiles = static_cast<int>(ceil_div(g.N, p.bn));
-    }
-    p.m_tiles = static_cast<int>(ceil_div(a_rows, pairs ? 256 : 128));
-    const int64_t blocks = ceil_div(g.K, kBlockK);
-    int64_t grid;
-    if (pairs) {
-        p.box_rows = g.E ? 16 : p.bn / 2;
-        const int64_t tiles = g.E ? INT32_MAX : static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-        grid = 2 * (tiles < num_sms / 2 ? tiles : num_sms / 2);
+    // Expert groups, whose sizes only the device knows, run on pairs; their
+    // column counts follow from the row counts there.
+    Cut cut = {2, 0, 1};
+    if (!g.E) cut = choose_cut(g, a_rows, num_sms);
+    p.split = cut.split;
+    p.bn = cut.bn;
+    p.m_tiles = static_cast<int>(ceil_div(a_rows, 128 * cut.cg));
+    int64_t units = INT32_MAX;
+    if (g.E) {
+        p.box_rows = 16;
     } else {
-        p.box_rows = p.bn;
-        const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-        while (p.split < 16 && p.split * 2 <= blocks && tiles * p.split * 2 <= num_sms)
-            p.split *= 2;
-        grid = p.split > 1 ? tiles * p.split : (tiles < num_sms ? tiles : num_sms);
-    }
-
-#ifdef TUNE
-    if (const char *e = getenv("TUNE_PLAN")) {
-        int cg, bn, sp;
-        if (sscanf(e, "%d,%d,%d", &cg, &bn, &sp) == 3 && !g.E) {
-            p.bn = bn; p.split = sp; p.n_tiles = (int)ceil_div(g.N, bn);
-            p.m_tiles = (int)ceil_div(a_rows, 128 * cg);
-            p.box_rows = bn / cg;
-            const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-            grid = sp > 1 ? tiles * sp * cg : std::min<int64_t>(tiles, num_sms / cg) * cg;
-            pairs = cg == 2;
+        p.n_tiles = static_cast<int>(ceil_div(g.N, p.bn));
+        if (!g.b_mn) {      // even out the columns
+            const int unit = 16 * cut.cg;
+            p.bn = static_cast<int>(ceil_div(ceil_div(g.N, p.n_tiles), unit)) * unit;
         }
+        p.box_rows = p.bn / cut.cg;
+        units = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.split;
     }
-#endif
+    const int64_t slots = num_sms / cut.cg;
+    const int64_t grid = cut.cg * (p.split > 1 || units < slots ? units : slots);
+
     CUtensorMap ma, mb;
     bool ok;
     if (g.a_mn) {
@@ -903,7 +912,7 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
         ok = ok && encode(&mb, g.b, 2, dims, strides, box);
     }
     if (!ok) return false;
-    if (pairs)
+    if (cut.cg == 2)
         *err = g.gated ? start<2, true>(g, p, ma, mb, grid, stream)
                        : start<2, false>(g, p, ma, mb, grid, stream);
     else
