@@ -170,7 +170,8 @@ moef_status moe_gated_ffn_backward(const void *dout, const void *x, const void *
  *               offsets[E] is the end of the last expert's rows
  *   counts      int32 [E]: each expert's rows without padding
  *   workspace   moe_permute_workspace_bytes(T, K, E) bytes, 16-byte aligned,
- *               contents irrelevant
+ *               contents irrelevant; may be NULL when that is 0 (up to 131072
+ *               slots)
  *
  * Experts stand in ascending order, an expert's rows in (token, slot) order;
  * all outputs are exact.  P may exceed that number; all P rows are written.  A token may name an expert twice; it gets two rows.

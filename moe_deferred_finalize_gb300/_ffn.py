@@ -51,6 +51,31 @@ def _lib():
     return _LIB
 
 
+_ADDRESS = {}
+
+
+def _address(name):
+    """The entry point's address, for the _fastcall extension."""
+    if name not in _ADDRESS:
+        _ADDRESS[name] = ctypes.cast(getattr(_lib(), name), ctypes.c_void_p).value
+    return _ADDRESS[name]
+
+
+def _fast_device(fast, x):
+    """The device index of x when the one-pass check of the _fastcall
+    extension can take the call (x on the current device), else None."""
+    if fast is None or not isinstance(x, torch.Tensor):
+        return None
+    dev = x.get_device()
+    return dev if dev >= 0 and dev == torch.cuda.current_device() else None
+
+
+def _raw_stream(stream, dev):
+    if stream is None and _abi._RAW_STREAM is not None:
+        return _abi._RAW_STREAM(dev)
+    return _stream(stream, torch.device("cuda", dev))
+
+
 def _activation(name):
     if name not in ACTIVATION:
         raise ValueError(f"activation must be one of {sorted(ACTIVATION)}")
@@ -96,6 +121,10 @@ def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor
     ``out`` may be the residual) and, with ``save_preact`` or a given
     ``preact``, "preact" bf16 [T, N] (x weight^T + bias, for
     ``linear_backward``).  Enqueued on the current stream (or ``stream``)."""
+    res = _fast_linear(x, weight, bias, residual, activation, out, out_dtype, save_preact,
+                       preact, stream)
+    if res is not None:
+        return res
     T, K = _matrix(x, "x", "[T, K]")
     N = _matrix(weight, "weight", "[N, K]")[0]
     dev = x.device
@@ -117,6 +146,60 @@ def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor
                                _OUT_TYPE[out_dtype], _ptr(preact), T, N, K, _stream(stream, dev))
     _raise(st, "moe_linear")
     return res
+
+
+def _fast_linear(x, weight, bias, residual, activation, out, out_dtype, save_preact, preact,
+                 stream):
+    """linear in one pass through the _fastcall extension, which checks DLPack
+    descriptions of the tensors; None when it is missing or a check fails
+    (the Python checks then name the problem)."""
+    fast = _abi._fastcall()
+    try:
+        dev = _fast_device(fast, x)
+        if dev is None:
+            return None
+        act = ACTIVATION[activation]
+        if out is None:
+            out = x.new_empty((x.shape[0], weight.shape[0]), dtype=out_dtype)
+        if save_preact and preact is None:
+            preact = x.new_empty((x.shape[0], weight.shape[0]))
+        d = _abi._TO_DLPACK
+        st = fast.checked_linear(_address("moe_linear"), act, _OUT_TYPE[out.dtype], dev,
+                                 _raw_stream(stream, dev), d(x), d(weight),
+                                 None if bias is None else d(bias),
+                                 None if residual is None else d(residual), d(out),
+                                 None if preact is None else d(preact))
+    except (AttributeError, IndexError, KeyError, TypeError, RuntimeError, BufferError):
+        return None
+    if st < 0:
+        return None
+    _raise(st, "moe_linear")
+    return {"out": out} if preact is None else {"out": out, "preact": preact}
+
+
+def _fast_gated(x, weight, bias, activation, out, save_preact, preact, stream):
+    """gated_ffn likewise."""
+    fast = _abi._fastcall()
+    try:
+        dev = _fast_device(fast, x)
+        if dev is None:
+            return None
+        act = ACTIVATION[activation]
+        rows = weight.shape[0]
+        if out is None:
+            out = x.new_empty((x.shape[0], rows // 2))
+        if save_preact and preact is None:
+            preact = x.new_empty((x.shape[0], rows))
+        d = _abi._TO_DLPACK
+        st = fast.checked_gated(_address("moe_gated_ffn"), act, dev, _raw_stream(stream, dev),
+                                d(x), d(weight), None if bias is None else d(bias), d(out),
+                                None if preact is None else d(preact))
+    except (AttributeError, IndexError, KeyError, TypeError, RuntimeError, BufferError):
+        return None
+    if st < 0:
+        return None
+    _raise(st, "moe_gated_ffn")
+    return {"out": out} if preact is None else {"out": out, "preact": preact}
 
 
 def _backward(where, gated, dout, x, weight, preact, activation, want_dx, want_dweight,
@@ -192,6 +275,9 @@ def gated_ffn(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Ten
     rows; bias bf16 [2I].  Returns a dict with "out" bf16 [T, I] and, with
     ``save_preact`` or a given ``preact``, "preact" bf16 [T, 2I] (both
     projections with their bias, for ``gated_ffn_backward``)."""
+    res = _fast_gated(x, weight, bias, activation, out, save_preact, preact, stream)
+    if res is not None:
+        return res
     T, H = _matrix(x, "x", "[T, H]")
     rows = _matrix(weight, "weight", "[2I, H]")[0]
     if rows % 2:
@@ -254,25 +340,29 @@ def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
     E, tile = int(E), int(tile)
     _check(expert_ids, "expert_ids", _I32, (T, K), dev)
     lib = _lib()
-    if row_token is None:
+    if row_token is None and idx_map is None and offsets is None and counts is None:
+        # one allocation, cut up
         P = int(lib.moe_permute_rows(T, K, E, tile))
-        row_token = torch.empty(P, dtype=torch.int32, device=dev)
+        sizes = [T * K, P, max(E, 0) + 1, max(E, 0)]
+        parts = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes)
+        res = {"idx_map": parts[0].view(T, K), "row_token": parts[1], "offsets": parts[2],
+               "counts": parts[3]}
     else:
-        P = row_token.numel()
-    _check(row_token, "row_token", _I32, (P,), dev)
-    res = {"idx_map": _output(idx_map, "idx_map", torch.int32, (T, K), dev),
-           "row_token": row_token,
-           "offsets": _output(offsets, "offsets", torch.int32, (max(E, 0) + 1,), dev),
-           "counts": _output(counts, "counts", torch.int32, (max(E, 0),), dev)}
-    if workspace is None:
-        need = int(lib.moe_permute_workspace_bytes(T, K, E))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the same device")
-    nbytes = workspace.numel() * workspace.element_size()
+        P = int(lib.moe_permute_rows(T, K, E, tile)) if row_token is None else row_token.numel()
+        res = {"idx_map": _output(idx_map, "idx_map", torch.int32, (T, K), dev),
+               "row_token": _output(row_token, "row_token", torch.int32, (P,), dev),
+               "offsets": _output(offsets, "offsets", torch.int32, (max(E, 0) + 1,), dev),
+               "counts": _output(counts, "counts", torch.int32, (max(E, 0),), dev)}
+    nbytes = int(lib.moe_permute_workspace_bytes(T, K, E))
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the same device")
+        nbytes = workspace.numel() * workspace.element_size()
+    elif nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     with _on(dev):
         st = lib.moe_permute(_ptr(expert_ids), T, K, E, tile, _ptr(res["idx_map"]),
-                             _ptr(row_token), P, _ptr(res["offsets"]), _ptr(res["counts"]),
+                             _ptr(res["row_token"]), P, _ptr(res["offsets"]), _ptr(res["counts"]),
                              _ptr(workspace), nbytes, _stream(stream, dev))
     _raise(st, "moe_permute")
     return res

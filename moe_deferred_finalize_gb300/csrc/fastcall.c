@@ -6,8 +6,9 @@
  * converts them directly, and pack/call go further for repeated calls: the
  * arguments are packed once into a C struct (a capsule) and each call passes
  * only the stream.  checked_call does the Python binding's argument checks
- * on DLPack descriptions of the tensors before calling.  Nothing here
- * computes anything of the finalize.
+ * on DLPack descriptions of the tensors before calling; checked_linear and
+ * checked_gated do so for moe_linear and moe_gated_ffn.  Nothing here
+ * computes anything.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -244,6 +245,85 @@ static PyObject *checked_call(PyObject *self, PyObject *const *a, Py_ssize_t nar
                               (int)id[1], (int)xd[1], splits, threads, flags, stream));
 }
 
+/* ---------------------------------------------------------------------------
+ * checked_linear / checked_gated: the same for moe_linear and moe_gated_ffn.
+ *
+ * checked_linear(fn_address, activation, out_fp32, device, stream, x, weight,
+ *                bias, residual, out, preact) -> status
+ * checked_gated(fn_address, activation, device, stream, x, weight, bias, out,
+ *               preact) -> status
+ * The tensors are DLPack capsules or None; -1 when one fails the checks. */
+typedef int (*linear_fn)(const void *x, const void *weight, const void *bias,
+                         const void *residual, int act, void *out, int out_type, void *preact,
+                         int T, int N, int K, void *stream);
+typedef int (*gated_fn)(const void *x, const void *weight, const void *bias, int act, void *out,
+                        void *preact, int T, int I, int H, void *stream);
+
+/* 1 when the optional bf16 operand t is absent, or dense [a, b] (b < 0: [a]) */
+static int optional_bf16(const dl_tensor *t, int dev, int64_t a, int64_t b) {
+    int64_t d[2];
+    if (!t) return 1;
+    if (b < 0) return dense(t, dev, DL_BFLOAT, 16, 1, d) && d[0] == a;
+    return dense(t, dev, DL_BFLOAT, 16, 2, d) && d[0] == a && d[1] == b;
+}
+
+static PyObject *checked_linear(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    if (nargs != 11) {
+        PyErr_SetString(PyExc_TypeError, "checked_linear takes 11 arguments");
+        return NULL;
+    }
+    linear_fn fn = (linear_fn)as_ptr(a[0]);
+    const int act = (int)PyLong_AsLong(a[1]);
+    const int fp32 = (int)PyLong_AsLong(a[2]);
+    const int dev = (int)PyLong_AsLong(a[3]);
+    void *stream = as_ptr(a[4]);
+    if (PyErr_Occurred()) return NULL;
+    const dl_tensor *t[6];
+    for (int i = 0; i < 6; ++i) {
+        t[i] = described(a[5 + i]);
+        if (PyErr_Occurred()) return NULL;
+    }
+    int64_t x[2], w[2], o[2];
+    const int ok = fn && dense(t[0], dev, DL_BFLOAT, 16, 2, x) &&
+                   dense(t[1], dev, DL_BFLOAT, 16, 2, w) && w[1] == x[1] &&
+                   dense(t[4], dev, fp32 ? DL_FLOAT : DL_BFLOAT, fp32 ? 32 : 16, 2, o) &&
+                   o[0] == x[0] && o[1] == w[0] && optional_bf16(t[2], dev, w[0], -1) &&
+                   optional_bf16(t[3], dev, x[0], w[0]) && optional_bf16(t[5], dev, x[0], w[0]) &&
+                   x[0] <= 0x7FFFFFFF && x[1] <= 0x7FFFFFFF && w[0] <= 0x7FFFFFFF;
+    if (!ok) return PyLong_FromLong(-1);
+    return PyLong_FromLong(fn(address(t[0]), address(t[1]), address(t[2]), address(t[3]), act,
+                              address(t[4]), fp32, address(t[5]), (int)x[0], (int)w[0],
+                              (int)x[1], stream));
+}
+
+static PyObject *checked_gated(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    if (nargs != 9) {
+        PyErr_SetString(PyExc_TypeError, "checked_gated takes 9 arguments");
+        return NULL;
+    }
+    gated_fn fn = (gated_fn)as_ptr(a[0]);
+    const int act = (int)PyLong_AsLong(a[1]);
+    const int dev = (int)PyLong_AsLong(a[2]);
+    void *stream = as_ptr(a[3]);
+    if (PyErr_Occurred()) return NULL;
+    const dl_tensor *t[5];
+    for (int i = 0; i < 5; ++i) {
+        t[i] = described(a[4 + i]);
+        if (PyErr_Occurred()) return NULL;
+    }
+    int64_t x[2], w[2], o[2];
+    const int ok = fn && dense(t[0], dev, DL_BFLOAT, 16, 2, x) &&
+                   dense(t[1], dev, DL_BFLOAT, 16, 2, w) && w[1] == x[1] && w[0] % 2 == 0 &&
+                   dense(t[3], dev, DL_BFLOAT, 16, 2, o) && o[0] == x[0] && 2 * o[1] == w[0] &&
+                   optional_bf16(t[2], dev, w[0], -1) && optional_bf16(t[4], dev, x[0], w[0]) &&
+                   x[0] <= 0x7FFFFFFF && x[1] <= 0x7FFFFFFF && w[0] <= 0x7FFFFFFF;
+    if (!ok) return PyLong_FromLong(-1);
+    return PyLong_FromLong(fn(address(t[0]), address(t[1]), address(t[2]), act, address(t[3]),
+                              address(t[4]), (int)x[0], (int)o[1], (int)x[1], stream));
+}
+
 /* call(capsule, stream_handle) -> status of moe_finalize_ex */
 static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
     (void)self;
@@ -267,6 +347,10 @@ static PyMethodDef methods[] = {
      "Enqueue one moe_finalize_ex call from its arguments; returns the status."},
     {"checked_call", (PyCFunction)(void (*)(void))checked_call, METH_FASTCALL,
      "Check DLPack-described tensors and enqueue one moe_finalize_ex call."},
+    {"checked_linear", (PyCFunction)(void (*)(void))checked_linear, METH_FASTCALL,
+     "Check DLPack-described tensors and enqueue one moe_linear call."},
+    {"checked_gated", (PyCFunction)(void (*)(void))checked_gated, METH_FASTCALL,
+     "Check DLPack-described tensors and enqueue one moe_gated_ffn call."},
     {NULL, NULL, 0, NULL},
 };
 

@@ -61,7 +61,8 @@ cudaError_t launch_dz(const uint16_t *dout, const uint16_t *preact, int act, int
                       uint16_t *dz, float *partial, uint16_t *dbias, int T, int n,
                       cudaStream_t stream);
 
-// The grouped layout (moe_permute); chunks = permute_chunks(T * K).
+// The grouped layout (moe_permute).  permute_chunks: rows of E counts that
+// the workspace holds for that many slots (0: none needed).
 int permute_chunks(int64_t slots);
 cudaError_t launch_permute(const int32_t *ids, int T, int K, int E, int tile, int32_t *idx_map,
                            int32_t *row_token, int64_t P, int32_t *offsets, int32_t *counts,

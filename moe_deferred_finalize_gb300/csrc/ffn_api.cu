@@ -244,10 +244,11 @@ moef_status moe_permute(const int32_t *expert_ids, int T, int K, int E, int tile
         return MOEF_ERR_SHAPE;
     const int64_t rows = moe_permute_rows(T, K, E, tile);
     if ((T > 0 && rows == 0) || P < rows || P > INT_MAX) return MOEF_ERR_SHAPE;
-    if (!offsets || !counts || !workspace || (T > 0 && (!expert_ids || !idx_map)) ||
+    const size_t need = moe_permute_workspace_bytes(T, K, E);
+    if (!offsets || !counts || (need > 0 && !workspace) || (T > 0 && (!expert_ids || !idx_map)) ||
         (P > 0 && !row_token))
         return MOEF_ERR_NULL;
-    if (workspace_bytes < moe_permute_workspace_bytes(T, K, E)) return MOEF_ERR_SHAPE;
+    if (workspace_bytes < need) return MOEF_ERR_SHAPE;
     if (!aligned(workspace, 16) || !aligned(expert_ids, 4) || !aligned(idx_map, 4) ||
         !aligned(row_token, 4) || !aligned(offsets, 4) || !aligned(counts, 4))
         return MOEF_ERR_ALIGN;

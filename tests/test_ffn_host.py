@@ -91,13 +91,18 @@ def test_permute_argument_errors(lib):
     f = lib.moe_permute
     base = dict(ids=A, T=4, K=2, E=8, tile=16, idx=A, rows=A, P=128, offsets=A, counts=A, ws=A,
                 ws_bytes=1 << 20, stream=NULL)
-    for k in ("ids", "idx", "rows", "offsets", "counts", "ws"):
+    for k in ("ids", "idx", "rows", "offsets", "counts"):
         assert call(f, base, **{k: NULL}) == E_NULL
+    many = dict(base, T=1 << 20, P=1 << 30)         # enough slots for the workspace to be used
+    assert lib.moe_permute_workspace_bytes(4, 2, 8) == 0
+    need = lib.moe_permute_workspace_bytes(1 << 20, 2, 8)
+    assert need > 0
+    assert call(f, many, ws=NULL) == E_NULL
+    assert call(f, many, ws_bytes=need - 1) == E_SHAPE
     for k in ("ids", "idx", "rows", "offsets", "counts", "ws"):
         assert call(f, base, **{k: HALF}) == E_ALIGN
     for change in (dict(T=-1), dict(K=0), dict(K=33), dict(E=0), dict(E=1025), dict(tile=0),
-                   dict(P=127), dict(P=1 << 31), dict(ws_bytes=lib.moe_permute_workspace_bytes(
-                       4, 2, 8) - 1), dict(T=2 ** 31 - 1, K=32, P=2 ** 31 - 1)):
+                   dict(P=127), dict(P=1 << 31), dict(T=2 ** 31 - 1, K=32, P=2 ** 31 - 1)):
         assert call(f, base, **change) == E_SHAPE, change
 
 
