@@ -170,7 +170,7 @@ moef_status moe_gated_ffn_backward(const void *dout, const void *x, const void *
  *               offsets[E] is the end of the last expert's rows
  *   counts      int32 [E]: each expert's rows without padding
  *   workspace   moe_permute_workspace_bytes(T, K, E) bytes, 16-byte aligned,
- *               contents irrelevant; may be NULL when that is 0 (up to 131072
+ *               contents irrelevant; may be NULL when that is 0 (up to 16384
  *               slots)
  *
  * Experts stand in ascending order, an expert's rows in (token, slot) order;

@@ -151,24 +151,30 @@ def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor
 def _fast_linear(x, weight, bias, residual, activation, out, out_dtype, save_preact, preact,
                  stream):
     """linear in one pass through the _fastcall extension, which checks DLPack
-    descriptions of the tensors; None when it is missing or a check fails
-    (the Python checks then name the problem)."""
+    descriptions of the tensors (outputs allocated here are passed by address:
+    describing a new tensor costs more than all the rest); None when it is
+    missing or a check fails (the Python checks then name the problem)."""
     fast = _abi._fastcall()
     try:
         dev = _fast_device(fast, x)
         if dev is None:
             return None
         act = ACTIVATION[activation]
+        d = _abi._TO_DLPACK
+        out_at = pre_at = None
         if out is None:
             out = x.new_empty((x.shape[0], weight.shape[0]), dtype=out_dtype)
-        if save_preact and preact is None:
+            out_at = out.data_ptr()
+        if preact is not None:
+            pre_at = d(preact)
+        elif save_preact:
             preact = x.new_empty((x.shape[0], weight.shape[0]))
-        d = _abi._TO_DLPACK
+            pre_at = preact.data_ptr()
         st = fast.checked_linear(_address("moe_linear"), act, _OUT_TYPE[out.dtype], dev,
                                  _raw_stream(stream, dev), d(x), d(weight),
                                  None if bias is None else d(bias),
-                                 None if residual is None else d(residual), d(out),
-                                 None if preact is None else d(preact))
+                                 None if residual is None else d(residual),
+                                 d(out) if out_at is None else out_at, pre_at)
     except (AttributeError, IndexError, KeyError, TypeError, RuntimeError, BufferError):
         return None
     if st < 0:
@@ -186,14 +192,19 @@ def _fast_gated(x, weight, bias, activation, out, save_preact, preact, stream):
             return None
         act = ACTIVATION[activation]
         rows = weight.shape[0]
+        d = _abi._TO_DLPACK
+        out_at = pre_at = None
         if out is None:
             out = x.new_empty((x.shape[0], rows // 2))
-        if save_preact and preact is None:
+            out_at = out.data_ptr()
+        if preact is not None:
+            pre_at = d(preact)
+        elif save_preact:
             preact = x.new_empty((x.shape[0], rows))
-        d = _abi._TO_DLPACK
+            pre_at = preact.data_ptr()
         st = fast.checked_gated(_address("moe_gated_ffn"), act, dev, _raw_stream(stream, dev),
-                                d(x), d(weight), None if bias is None else d(bias), d(out),
-                                None if preact is None else d(preact))
+                                d(x), d(weight), None if bias is None else d(bias),
+                                d(out) if out_at is None else out_at, pre_at)
     except (AttributeError, IndexError, KeyError, TypeError, RuntimeError, BufferError):
         return None
     if st < 0:
@@ -340,19 +351,11 @@ def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
     E, tile = int(E), int(tile)
     _check(expert_ids, "expert_ids", _I32, (T, K), dev)
     lib = _lib()
-    if row_token is None and idx_map is None and offsets is None and counts is None:
-        # one allocation, cut up
-        P = int(lib.moe_permute_rows(T, K, E, tile))
-        sizes = [T * K, P, max(E, 0) + 1, max(E, 0)]
-        parts = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes)
-        res = {"idx_map": parts[0].view(T, K), "row_token": parts[1], "offsets": parts[2],
-               "counts": parts[3]}
-    else:
-        P = int(lib.moe_permute_rows(T, K, E, tile)) if row_token is None else row_token.numel()
-        res = {"idx_map": _output(idx_map, "idx_map", torch.int32, (T, K), dev),
-               "row_token": _output(row_token, "row_token", torch.int32, (P,), dev),
-               "offsets": _output(offsets, "offsets", torch.int32, (max(E, 0) + 1,), dev),
-               "counts": _output(counts, "counts", torch.int32, (max(E, 0),), dev)}
+    P = int(lib.moe_permute_rows(T, K, E, tile)) if row_token is None else row_token.numel()
+    res = {"idx_map": _output(idx_map, "idx_map", torch.int32, (T, K), dev),
+           "row_token": _output(row_token, "row_token", torch.int32, (P,), dev),
+           "offsets": _output(offsets, "offsets", torch.int32, (max(E, 0) + 1,), dev),
+           "counts": _output(counts, "counts", torch.int32, (max(E, 0),), dev)}
     nbytes = int(lib.moe_permute_workspace_bytes(T, K, E))
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():

@@ -252,12 +252,24 @@ static PyObject *checked_call(PyObject *self, PyObject *const *a, Py_ssize_t nar
  *                bias, residual, out, preact) -> status
  * checked_gated(fn_address, activation, device, stream, x, weight, bias, out,
  *               preact) -> status
- * The tensors are DLPack capsules or None; -1 when one fails the checks. */
+ * The tensors are DLPack capsules or None; -1 when one fails the checks.  out
+ * and preact may be addresses (ints): the caller made them for this call, of
+ * the right type and shape. */
 typedef int (*linear_fn)(const void *x, const void *weight, const void *bias,
                          const void *residual, int act, void *out, int out_type, void *preact,
                          int T, int N, int K, void *stream);
 typedef int (*gated_fn)(const void *x, const void *weight, const void *bias, int act, void *out,
                         void *preact, int T, int I, int H, void *stream);
+
+/* an output: its description in *t, or its address in *at when it is an int */
+static int output(PyObject *o, const dl_tensor **t, void **at) {
+    *t = NULL;
+    *at = NULL;
+    if (PyLong_Check(o)) *at = PyLong_AsVoidPtr(o);
+    else *t = described(o);
+    if (*t) *at = address(*t);
+    return !PyErr_Occurred();
+}
 
 /* 1 when the optional bf16 operand t is absent, or dense [a, b] (b < 0: [a]) */
 static int optional_bf16(const dl_tensor *t, int dev, int64_t a, int64_t b) {
@@ -280,20 +292,24 @@ static PyObject *checked_linear(PyObject *self, PyObject *const *a, Py_ssize_t n
     void *stream = as_ptr(a[4]);
     if (PyErr_Occurred()) return NULL;
     const dl_tensor *t[6];
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < 4; ++i) {
         t[i] = described(a[5 + i]);
         if (PyErr_Occurred()) return NULL;
     }
+    void *out, *preact;
+    if (!output(a[9], &t[4], &out) || !output(a[10], &t[5], &preact)) return NULL;
     int64_t x[2], w[2], o[2];
     const int ok = fn && dense(t[0], dev, DL_BFLOAT, 16, 2, x) &&
                    dense(t[1], dev, DL_BFLOAT, 16, 2, w) && w[1] == x[1] &&
-                   dense(t[4], dev, fp32 ? DL_FLOAT : DL_BFLOAT, fp32 ? 32 : 16, 2, o) &&
-                   o[0] == x[0] && o[1] == w[0] && optional_bf16(t[2], dev, w[0], -1) &&
+                   (t[4] ? dense(t[4], dev, fp32 ? DL_FLOAT : DL_BFLOAT, fp32 ? 32 : 16, 2, o) &&
+                               o[0] == x[0] && o[1] == w[0]
+                         : out || !x[0]) &&
+                   optional_bf16(t[2], dev, w[0], -1) &&
                    optional_bf16(t[3], dev, x[0], w[0]) && optional_bf16(t[5], dev, x[0], w[0]) &&
                    x[0] <= 0x7FFFFFFF && x[1] <= 0x7FFFFFFF && w[0] <= 0x7FFFFFFF;
     if (!ok) return PyLong_FromLong(-1);
     return PyLong_FromLong(fn(address(t[0]), address(t[1]), address(t[2]), address(t[3]), act,
-                              address(t[4]), fp32, address(t[5]), (int)x[0], (int)w[0],
+                              out, fp32, preact, (int)x[0], (int)w[0],
                               (int)x[1], stream));
 }
 
@@ -309,19 +325,23 @@ static PyObject *checked_gated(PyObject *self, PyObject *const *a, Py_ssize_t na
     void *stream = as_ptr(a[3]);
     if (PyErr_Occurred()) return NULL;
     const dl_tensor *t[5];
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 3; ++i) {
         t[i] = described(a[4 + i]);
         if (PyErr_Occurred()) return NULL;
     }
+    void *out, *preact;
+    if (!output(a[7], &t[3], &out) || !output(a[8], &t[4], &preact)) return NULL;
     int64_t x[2], w[2], o[2];
     const int ok = fn && dense(t[0], dev, DL_BFLOAT, 16, 2, x) &&
                    dense(t[1], dev, DL_BFLOAT, 16, 2, w) && w[1] == x[1] && w[0] % 2 == 0 &&
-                   dense(t[3], dev, DL_BFLOAT, 16, 2, o) && o[0] == x[0] && 2 * o[1] == w[0] &&
+                   (t[3] ? dense(t[3], dev, DL_BFLOAT, 16, 2, o) && o[0] == x[0] &&
+                               2 * o[1] == w[0]
+                         : out || !x[0]) &&
                    optional_bf16(t[2], dev, w[0], -1) && optional_bf16(t[4], dev, x[0], w[0]) &&
                    x[0] <= 0x7FFFFFFF && x[1] <= 0x7FFFFFFF && w[0] <= 0x7FFFFFFF;
     if (!ok) return PyLong_FromLong(-1);
-    return PyLong_FromLong(fn(address(t[0]), address(t[1]), address(t[2]), act, address(t[3]),
-                              address(t[4]), (int)x[0], (int)o[1], (int)x[1], stream));
+    return PyLong_FromLong(fn(address(t[0]), address(t[1]), address(t[2]), act, out,
+                              preact, (int)x[0], (int)(w[0] / 2), (int)x[1], stream));
 }
 
 /* call(capsule, stream_handle) -> status of moe_finalize_ex */
