@@ -163,12 +163,12 @@ def _fast_linear(x, weight, bias, residual, activation, out, out_dtype, save_pre
         d = _abi._TO_DLPACK
         out_at = pre_at = None
         if out is None:
-            out = x.new_empty((x.shape[0], weight.shape[0]), dtype=out_dtype)
+            out = torch.empty((x.shape[0], weight.shape[0]), dtype=out_dtype, device=x.device)
             out_at = out.data_ptr()
         if preact is not None:
             pre_at = d(preact)
         elif save_preact:
-            preact = x.new_empty((x.shape[0], weight.shape[0]))
+            preact = torch.empty((x.shape[0], weight.shape[0]), dtype=x.dtype, device=x.device)
             pre_at = preact.data_ptr()
         st = fast.checked_linear(_address("moe_linear"), act, _OUT_TYPE[out.dtype], dev,
                                  _raw_stream(stream, dev), d(x), d(weight),
@@ -195,12 +195,12 @@ def _fast_gated(x, weight, bias, activation, out, save_preact, preact, stream):
         d = _abi._TO_DLPACK
         out_at = pre_at = None
         if out is None:
-            out = x.new_empty((x.shape[0], rows // 2))
+            out = torch.empty((x.shape[0], rows // 2), dtype=x.dtype, device=x.device)
             out_at = out.data_ptr()
         if preact is not None:
             pre_at = d(preact)
         elif save_preact:
-            preact = x.new_empty((x.shape[0], rows))
+            preact = torch.empty((x.shape[0], rows), dtype=x.dtype, device=x.device)
             pre_at = preact.data_ptr()
         st = fast.checked_gated(_address("moe_gated_ffn"), act, dev, _raw_stream(stream, dev),
                                 d(x), d(weight), None if bias is None else d(bias),

@@ -4,67 +4,101 @@
 //   gated   dz[:, i] = dout * u * act'(g),  dz[:, n + i] = dout * act(g)
 //
 // One pass over dout and preact (read once, dz written once): bound by HBM
-// bandwidth.  A thread owns one vector of columns and walks kBiasRows rows of
-// it, so the column sums build up in its registers, in fp32 and before dz is
-// rounded; each CTA writes its rows' sums as one row of `partial`, and a
-// second kernel adds those rows in a fixed order (no atomics: equal calls
-// give equal bits).
+// bandwidth.  A CTA takes kBiasRows rows of 32 vectors of columns, a warp
+// every eighth row, all of a thread's loads in flight before their first use;
+// the activation is a template argument, so its arithmetic overlaps.  The
+// column sums build up in registers, in fp32 and before dz is rounded; the
+// CTA adds its warps' sums in order and writes one row of `partial`, and a
+// second kernel adds those rows in order (no atomics: equal calls give equal
+// bits).  2040 x 4096 with GELU: see the results table; 40 us with the
+// activation chosen per value and 32 rows a thread.
 #include "ffn.cuh"
+#include "tc.cuh"
 #include "vec.cuh"
 
 namespace moef {
 namespace {
 
-constexpr int kDzThreads = 128;
+constexpr int kDzWarps = 8;
+constexpr int kDzThreads = 32 * kDzWarps;
+constexpr int kDzRows = kBiasRows / kDzWarps;       // rows per thread
 
-template <int VEC, bool GATED>
+template <int VEC, bool GATED, int ACT>
 __global__ void __launch_bounds__(kDzThreads)
-dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t *dz, float *partial,
-          int T, int n) {
+dz_kernel(const uint16_t *dout, const uint16_t *preact, uint16_t *dz, float *partial, int T,
+          int n) {
     using Ops = VecOps<VEC>;
-    const int cols = GATED ? 2 * n : n;
-    const int t0 = blockIdx.x * kBiasRows, t1 = min(T - t0, kBiasRows) + t0;
-    for (int i = (blockIdx.y * kDzThreads + threadIdx.x) * VEC; i < n;
-         i += gridDim.y * kDzThreads * VEC) {
-        float sum[GATED ? 2 : 1][VEC] = {};
-#pragma unroll 4
-        for (int t = t0; t < t1; ++t) {
-            const int64_t row = static_cast<int64_t>(t) * cols + i;
-            float d[VEC], g[VEC], r[VEC];
-            Ops::to_f32(Ops::load(dout + static_cast<int64_t>(t) * n + i), d);
-            if constexpr (GATED) {
-                float u[VEC], r2[VEC];
-                Ops::to_f32(Ops::load(preact + row), g);
-                Ops::to_f32(Ops::load(preact + row + n), u);
+    using V = typename Ops::V;
+    constexpr int kHalves = GATED ? 2 : 1;
+    __shared__ float sums[kDzWarps][kHalves][32 * VEC];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int cols = kHalves * n;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kBiasRows;
+    allow_next_kernel();
+    wait_previous_kernel();
+    for (int i0 = blockIdx.y * 32 * VEC; i0 < n; i0 += gridDim.y * 32 * VEC) {
+        const int i = i0 + lane * VEC;
+        float sum[kHalves][VEC] = {};
+        if (i < n) {
+            V d[kDzRows] = {}, z[kHalves][kDzRows] = {};
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    float a;
-                    const float da = act_grad(g[j], act, &a);
-                    r[j] = d[j] * u[j] * da;
-                    r2[j] = d[j] * a;
-                    sum[0][j] += r[j];
-                    sum[1][j] += r2[j];
+            for (int r = 0; r < kDzRows; ++r) {
+                const int64_t t = t0 + warp + r * kDzWarps;
+                if (t < T) {
+                    d[r] = Ops::load(dout + t * n + i);
+                    if (GATED || ACT != MOEF_ACT_NONE) z[0][r] = Ops::load(preact + t * cols + i);
+                    if constexpr (GATED) z[1][r] = Ops::load(preact + t * cols + n + i);
                 }
-                // read again by both products: kept in L2 where it fits
-                *reinterpret_cast<typename Ops::V *>(dz + row) = Ops::from_f32(r);
-                *reinterpret_cast<typename Ops::V *>(dz + row + n) = Ops::from_f32(r2);
-            } else {
-                if (preact) Ops::to_f32(Ops::load(preact + row), g);
+            }
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    float a;
-                    r[j] = preact ? d[j] * act_grad(g[j], act, &a) : d[j];
-                    sum[0][j] += r[j];
+            for (int r = 0; r < kDzRows; ++r) {
+                const int64_t t = t0 + warp + r * kDzWarps;
+                if (t >= T) break;
+                float dv[VEC], gv[VEC], out[kHalves][VEC];
+                Ops::to_f32(d[r], dv);
+                Ops::to_f32(z[0][r], gv);
+                if constexpr (GATED) {
+                    float uv[VEC];
+                    Ops::to_f32(z[1][r], uv);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        float a;
+                        const float da = act_grad(gv[j], ACT, &a);
+                        out[0][j] = dv[j] * uv[j] * da;
+                        out[1][j] = dv[j] * a;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        float a;
+                        out[0][j] = ACT == MOEF_ACT_NONE ? dv[j]
+                                                         : dv[j] * act_grad(gv[j], ACT, &a);
+                    }
                 }
-                if (dz) *reinterpret_cast<typename Ops::V *>(dz + row) = Ops::from_f32(r);
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) sum[h][j] += out[h][j];
+                    // read again by both products: an ordinary store keeps it in L2
+                    if (dz) *reinterpret_cast<V *>(dz + t * cols + h * n + i) =
+                                Ops::from_f32(out[h]);
+                }
             }
         }
         if (partial) {
 #pragma unroll
-            for (int h = 0; h < (GATED ? 2 : 1); ++h)
+            for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    partial[static_cast<int64_t>(blockIdx.x) * cols + h * n + i + j] = sum[h][j];
+                for (int j = 0; j < VEC; ++j) sums[warp][h][lane * VEC + j] = sum[h][j];
+            __syncthreads();
+            for (int c = threadIdx.x; c < kHalves * 32 * VEC; c += kDzThreads) {
+                const int h = c / (32 * VEC), k = c % (32 * VEC);
+                float v = sums[0][h][k];
+#pragma unroll
+                for (int w = 1; w < kDzWarps; ++w) v += sums[w][h][k];
+                if (i0 + k < n) partial[blockIdx.x * static_cast<int64_t>(cols) + h * n + i0 + k] = v;
+            }
+            __syncthreads();
         }
     }
 }
@@ -74,6 +108,8 @@ dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t *dz, f
 __global__ void __launch_bounds__(256)
 bias_sum_kernel(const float *partial, int rows, int cols, uint16_t *dbias) {
     __shared__ float s[8][32];
+    allow_next_kernel();
+    wait_previous_kernel();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x / 32;
     float sum = 0.f;
     if (c < cols)
@@ -88,16 +124,37 @@ bias_sum_kernel(const float *partial, int rows, int cols, uint16_t *dbias) {
     }
 }
 
-template <int VEC>
-void start_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated, uint16_t *dz,
-              float *partial, int T, int n, cudaStream_t stream) {
-    const int64_t across = (static_cast<int64_t>(n) + kDzThreads * VEC - 1) / (kDzThreads * VEC);
+template <typename... Params, typename... Args>
+cudaError_t start(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream,
+                  Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+template <int VEC, bool GATED>
+cudaError_t start_dz(const uint16_t *dout, const uint16_t *preact, int act, uint16_t *dz,
+                     float *partial, int T, int n, cudaStream_t stream) {
+    const int64_t across = (static_cast<int64_t>(n) + 32 * VEC - 1) / (32 * VEC);
     const dim3 grid(static_cast<unsigned>((T - 1) / kBiasRows + 1),
                     static_cast<unsigned>(across < 65535 ? across : 65535));
-    if (gated)
-        dz_kernel<VEC, true><<<grid, kDzThreads, 0, stream>>>(dout, preact, act, dz, partial, T, n);
-    else
-        dz_kernel<VEC, false><<<grid, kDzThreads, 0, stream>>>(dout, preact, act, dz, partial, T, n);
+    auto go = [&](auto *kernel) {
+        return start(kernel, grid, kDzThreads, stream, dout, preact, dz, partial, T, n);
+    };
+    switch (act) {
+        case MOEF_ACT_SILU: return go(dz_kernel<VEC, GATED, MOEF_ACT_SILU>);
+        case MOEF_ACT_GELU: return go(dz_kernel<VEC, GATED, MOEF_ACT_GELU>);
+        case MOEF_ACT_GELU_TANH: return go(dz_kernel<VEC, GATED, MOEF_ACT_GELU_TANH>);
+        case MOEF_ACT_RELU: return go(dz_kernel<VEC, GATED, MOEF_ACT_RELU>);
+        default: return go(dz_kernel<VEC, GATED, MOEF_ACT_NONE>);
+    }
 }
 
 }  // namespace
@@ -108,16 +165,18 @@ cudaError_t launch_dz(const uint16_t *dout, const uint16_t *preact, int act, int
     const uintptr_t bits = reinterpret_cast<uintptr_t>(dout) | reinterpret_cast<uintptr_t>(preact) |
                            reinterpret_cast<uintptr_t>(dz);
     float *part = dbias ? partial : nullptr;
-    if (n % 8 == 0 && bits % 16 == 0)
-        start_dz<8>(dout, preact, act, gated, dz, part, T, n, stream);
+    const bool vec = n % 8 == 0 && bits % 16 == 0;
+    cudaError_t err;
+    if (gated)
+        err = vec ? start_dz<8, true>(dout, preact, act, dz, part, T, n, stream)
+                  : start_dz<1, true>(dout, preact, act, dz, part, T, n, stream);
     else
-        start_dz<1>(dout, preact, act, gated, dz, part, T, n, stream);
-    cudaError_t err = cudaGetLastError();
+        err = vec ? start_dz<8, false>(dout, preact, act, dz, part, T, n, stream)
+                  : start_dz<1, false>(dout, preact, act, dz, part, T, n, stream);
     if (err != cudaSuccess || !dbias) return err;
     const int cols = gated ? 2 * n : n;
-    bias_sum_kernel<<<(cols + 31) / 32, 256, 0, stream>>>(partial, (T - 1) / kBiasRows + 1,
-                                                          cols, dbias);
-    return cudaGetLastError();
+    return start(bias_sum_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), 256, stream,
+                 partial, (T - 1) / kBiasRows + 1, cols, dbias);
 }
 
 }  // namespace moef
