@@ -23,11 +23,12 @@
 //   CG = 2  pairs of CTAs share tiles of 256 (m) x up to 256 (n): each CTA
 //           loads half of A and half of B, one instruction drives both SMs'
 //           tensor cores.  Persistent, one pair per two SMs.
-//   CG = 1  128 x up to 256 tiles with k split over a cluster of `split` CTAs:
-//           few tokens give few tiles, and the split spreads the weights over
-//           all SMs.  The partial accumulators meet in shared memory, and each
-//           CTA of the cluster adds and finishes its share of the tile, in
-//           rank order (equal calls give equal bits).
+//   CG = 1  128 x up to 256 tiles: few tokens give few tiles, which spread over
+//           all SMs.
+// k can also be split over a cluster of `split` CTAs or pairs: each finishes
+// its share of the tile's columns, the others send it their sums of those
+// into its shared memory, and it adds them in rank order (equal calls give
+// equal bits).
 #include "ffn.cuh"
 #include "tc.cuh"
 #include "vec.cuh"
@@ -260,26 +261,29 @@ __device__ __noinline__ void finish_scalar(const Finish<GATED> &f, int64_t n, fl
 constexpr int kChunk = 16;      // columns a warp finishes at a time
 
 // One tile out of TMEM: this warp's 32 lanes (rows of A), every other chunk
-// of columns; arrives on `done` once it has read them.  Lanes swap values so that each holds two
+// of the columns [begin, end); arrives on `done` (0: nowhere) once it has read
+// them.  parts > 0: so many other parts' sums of these columns are in `sums`.  Lanes swap values so that each holds two
 // adjacent features of one column; bias, activation, residual and stores then
 // run as loops over the chunk, with nothing to decide per value, so their
 // latencies overlap (deciding per pair took 22 us per 256 x 256 tile).
-template <int CG, bool GATED>
+template <bool GATED>
 __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_cta, uint32_t tmem,
-                                            int quarter, int half, int lane, uint32_t done) {
+                                            int quarter, int side, int lane, uint32_t done,
+                                            int begin, int end, const float *sums, int parts) {
     const int feature = m_cta + (GATED ? quarter * 16 + (lane >> 2) * 2
                                        : quarter * 32 + (lane & ~1));
     const Finish<GATED> f(g, feature, t.e);
     const bool odd = lane & 1, upper = lane & 2;
     const int64_t M = g.M;
     const int col = GATED ? lane & 3 : lane & 1;
-    const int end = min(t.bn, (t.count + kChunk - 1) / kChunk * kChunk);
-    if (kChunk * half >= end) {             // nothing for this warp
-        if (lane == 0) bar_arrive(done);
+    const int own = end - begin;
+    end = min(end, (t.count + kChunk - 1) / kChunk * kChunk);
+    if (begin + kChunk * side >= end) {         // nothing for this warp
+        if (done && lane == 0) bar_arrive(done);
         return;
     }
 #pragma unroll 1
-    for (int c0 = kChunk * half; c0 < end; c0 += 2 * kChunk) {
+    for (int c0 = begin + kChunk * side; c0 < end; c0 += 2 * kChunk) {
         const int64_t row = t.row0 + c0 + col;
         const int left = f.any ? t.count - c0 - col : 0;
         uint32_t res[kChunk / 2];
@@ -293,10 +297,16 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
         }
         uint32_t r[kChunk];
         tmem_load16(tmem + c0, r);
-        if (c0 + 2 * kChunk >= end) {       // the accumulator has been read
+        if (done && c0 + 2 * kChunk >= end) {       // the accumulator has been read
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(done);
+        }
+        for (int k = 0; k < parts; ++k) {
+            const float *from = sums + (k * own + c0 - begin) * 128 + quarter * 32 + lane;
+#pragma unroll
+            for (int c = 0; c < kChunk; ++c)
+                r[c] = __float_as_uint(__uint_as_float(r[c]) + from[c * 128]);
         }
         if constexpr (GATED) {
             float gate[kChunk / 2], up[kChunk / 2];     // [2k], [2k + 1]: features f, f + 1,
@@ -390,72 +400,28 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
     }
 }
 
-// The cluster's partial tiles [column][128 rows of A] in shared memory: this
-// CTA adds and finishes its share of the columns.  A thread keeps one pair of
-// features and takes kBatch columns at a time from four CTAs at a time, so
-// that 16 remote reads (about 0.7 us each) are in flight.
-template <int CG, bool GATED>
-__device__ __forceinline__ void finish_split(const Gemm &g, const Tile &t, int m_cta, uint32_t buf,
-                                             int split, int part, int half) {
-    constexpr int kPairs = GATED ? 32 : 64, kBatch = 4, kRanks = 4;
-    constexpr int kColumns = kTcThreads / kPairs;       // columns at a time per CTA
-    if (static_cast<int>(threadIdx.x) >= kColumns * kPairs) return;
-    const int pair = threadIdx.x % kPairs;
-    const Finish<GATED> f(g, m_cta + 2 * pair, t.e);
-    if (!f.any) return;
-    const uint32_t at = buf + pair * (GATED ? 16 : 8);
-    const int step = split * kColumns;
-    for (int c0 = part * kColumns + threadIdx.x / kPairs; c0 < t.count; c0 += kBatch * step) {
-        uint32_t res[kBatch];
-        float4 sum[kBatch];
+// k in parts: the columns of a tile are shared out over the parts, kChunk at a
+// time, and each part sends its sums of the others' columns into their shared
+// memory, [sender][column][128 rows of A].
+__device__ __forceinline__ int own_columns(int bn, int split) {
+    return ((bn + split - 1) / split + kChunk - 1) / kChunk * kChunk;
+}
+
+template <int CG>
+__device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint32_t buf, int split,
+                                             int part, int half, int quarter, int side, int lane) {
+    const int own = own_columns(t.bn, split);
+    for (int c0 = kChunk * side; c0 < t.count; c0 += 2 * kChunk) {
+        const int owner = c0 / own;
+        if (owner == part) continue;
+        uint32_t r[kChunk];
+        tmem_load16(tmem + c0, r);
+        const int slot = part < owner ? part : part - 1;
+        const uint32_t at = map_rank(
+            buf + ((slot * own + c0 - owner * own) * 128 + quarter * 32 + lane) * 4,
+            owner * CG + half);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int col = c0 + i * step;
-            res[i] = !GATED && g.residual && col < t.count ? f.residual(t.row0 + col) : 0u;
-        }
-        for (int k0 = 0; k0 < split; k0 += kRanks) {
-            float4 v[kRanks][kBatch];
-#pragma unroll
-            for (int k = 0; k < kRanks; ++k) {
-                const uint32_t from = map_rank(at, min(k0 + k, split - 1) * CG + half);
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const int col = c0 + i * step;
-                    if (col < t.count && k0 + k < split) {
-                        if constexpr (GATED) {
-                            v[k][i] = load_remote4(from + col * 512);
-                        } else {
-                            const float2 w = load_remote2(from + col * 512);
-                            v[k][i].x = w.x;
-                            v[k][i].y = w.y;
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kRanks; ++k)
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    sum[i].x += v[k][i].x;
-                    sum[i].y += v[k][i].y;
-                    if constexpr (GATED) {
-                        sum[i].z += v[k][i].z;
-                        sum[i].w += v[k][i].w;
-                    }
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int col = c0 + i * step;
-            if (col >= t.count) break;
-            if constexpr (GATED)
-                f.gated(t.row0 + col, sum[i].x + f.bias[0], sum[i].z + f.bias[1],
-                        sum[i].y + f.bias[GATED ? 2 : 0], sum[i].w + f.bias[GATED ? 3 : 1]);
-            else
-                f.linear(t.row0 + col, sum[i].x + f.bias[0], sum[i].y + f.bias[1], res[i]);
-        }
+        for (int c = 0; c < kChunk; ++c) store_remote(at + c * 512, r[c]);
     }
 }
 
@@ -708,33 +674,33 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
             const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             fence_after();
-            if (p.split > 1) {
-                // every MMA has finished, so the stages are free
-                float *buf = reinterpret_cast<float *>(smem + (stage0 - smem_addr(smem)));
-                for (int c0 = 16 * side; c0 < t.count; c0 += 32) {
-                    uint32_t r[16];
-                    tmem_load16(acc + c0, r);
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        buf[(c0 + c) * 128 + quarter * 32 + lane] = __uint_as_float(r[c]);
-                }
-            } else {
-                const uint32_t bar = smem_addr(&h->acc_empty[n & 1]);
-                finish_tile<CG, GATED>(g, t, t.m0 + half * m_cta_rows, acc, quarter, side, lane,
-                                       map_rank(bar, CG == 2 ? lead : cluster_rank()));
-            }
+            if (p.split > 1) break;         // joined below
+            const uint32_t bar = smem_addr(&h->acc_empty[n & 1]);
+            finish_tile<GATED>(g, t, t.m0 + half * m_cta_rows, acc, quarter, side, lane,
+                               map_rank(bar, CG == 2 ? lead : cluster_rank()), 0, t.bn, nullptr,
+                               0);
         }
     }
     __syncwarp();
     if (p.split > 1) {
-        cluster_sync();
-        if (!*gave_up) {
-            const Tile t = tile_at<CG, GATED>(g, p, h, first_tile);
-            finish_split<CG, GATED>(g, t, t.m0 + half * m_cta_rows, stage0, p.split, part, half);
+        const bool works = warp >= 2 && warp < kCopyWarp;
+        const int quarter = warp & 3, side = (warp - 2) >> 2;
+        const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        cluster_sync();         // every part's products are done, their stages free
+        const Tile t = tile_at<CG, GATED>(g, p, h, first_tile);
+        if (works && !*gave_up)
+            send_columns<CG>(t, acc, stage0, p.split, part, half, quarter, side, lane);
+        cluster_sync();         // every part's sums have arrived
+        if (works && !*gave_up) {
+            const int own = own_columns(t.bn, p.split);
+            finish_tile<GATED>(g, t, t.m0 + half * m_cta_rows, acc, quarter, side, lane, 0,
+                               part * own, (part + 1) * own,
+                               reinterpret_cast<const float *>(smem + (stage0 - smem_addr(smem))),
+                               p.split - 1);
         }
     }
     fence_before();
-    if (CG == 2 || p.split > 1) cluster_sync(); else __syncthreads();
+    if (CG == 2) cluster_sync(); else __syncthreads();
     fence_after();
     if (warp == 1) tmem_free<CG>(tmem, 2 * kMaxBn);
 }
