@@ -30,6 +30,7 @@
 // into its shared memory, and it adds them in rank order (equal calls give
 // equal bits).
 #include "ffn.cuh"
+#include "host.cuh"
 #include "tc.cuh"
 #include "vec.cuh"
 
@@ -764,25 +765,57 @@ cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CU
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Clusters of `size` CTAs with this kernel's shared memory that can run at
+// once: SMs come in groups that a cluster does not span, so 152 SMs hold 36
+// clusters of 4, 15 of 8 and 7 of 16.  Asked once per device and size.
+int active_clusters(int size, int num_sms) {
+    static std::atomic<int> cache[kMaxDevices][17];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
+    int n = cache[dev][size].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    auto *kernel = gemm_tc_kernel<1, false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = num_sms / size > 1 ? num_sms / size / 2 : 1;
+    }
+    cache[dev][size].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // How a product that is not grouped is cut: one CTA or a pair per tile, columns
 // per tile, parts of k.  Every choice is priced in SM clocks and the cheapest
 // taken.  The figures are fits to sweeps over 17..4096 rows:
-//   - a 64-deep k block takes the MMAs (2.35 clocks a column), the copies (68
-//     bytes a clock into an SM) or the issue of both (290 clocks), whichever
-//     is longest;
-//   - the epilogue of a tile takes 16 clocks a column, under the next tile's
-//     products except for the last one; tiles joined over a cluster 5000
-//     clocks (two barriers, remote reads) and 45 a column;
+//   - a 64-deep k block takes the MMAs (2.35 clocks a column), the copies (80
+//     bytes a clock into a single SM, 72 into each of a pair) or the issue of
+//     both (290 clocks), whichever is longest;
+//   - the epilogue of a tile takes 1200 clocks and 20 a column, under the next
+//     tile's products except for the last one; joining k's parts 3300 clocks
+//     (two cluster barriers), 430 a part and 18 a column, for pairs 7000, 430
+//     and 12;
 //   - HBM delivers 3580 bytes a clock.
-// Examples: 512 x 4096 x 7168 (gated) runs as 64 pairs of 128 columns, 25 us,
-// against 34 us with 256 columns and k in two parts; 300 x 256 x 7168 as 40
-// tiles with k in eight parts, 10.5 us, against 23 us unsplit.
+// Examples: 512 x 4096 x 7168 (gated) runs as 64 pairs of 128 columns, 24 us,
+// against 30 us with 256 columns and k in two parts; 300 x 256 x 7168 as 80
+// tiles of 64 columns and an eighth of k, 9.8 us, against 23 us unsplit.
 struct Cut {
     int cg, bn, split;
 };
 
 Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms) {
-    const int64_t blocks = (g.K + kBlockK - 1) / kBlockK;
+    const int64_t blocks = ceil_div(g.K, kBlockK);
     const double hbm = 2.0 * (static_cast<double>(a_rows) * g.K +
                               static_cast<double>(g.N) * g.K +
                               static_cast<double>(g.N) * g.M) / 3580.0;
@@ -790,27 +823,37 @@ Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms) {
     double least = 1e300;
     for (int cg = 1; cg <= 2; ++cg) {
         const int64_t m_tiles = ceil_div(a_rows, 128 * cg);
-        const int unit = g.b_mn ? 64 * cg : 32;     // transposed B is copied 64 columns at a time
-        for (int bn = unit; bn <= kMaxBn; bn += unit) {
-            const int64_t tiles = m_tiles * ceil_div(g.N, bn);
-            const double bytes = kATile + bn / cg * 128.0;
+        // transposed B is copied 64 columns at a time
+        const int unit = g.b_mn ? 64 * cg : 16 * cg;
+        int64_t last = 0;
+        for (int most = g.b_mn ? unit : 32; most <= kMaxBn; most += g.b_mn ? unit : 32) {
+            const int64_t n_tiles = ceil_div(g.N, most);
+            if (n_tiles == last) continue;
+            last = n_tiles;
+            // evened out over the tiles
+            const int bn = g.b_mn ? most
+                                  : static_cast<int>(ceil_div(ceil_div(g.N, n_tiles), unit)) * unit;
+            const int64_t tiles = m_tiles * n_tiles;
+            const double copies = (kATile + bn / cg * 128.0) / (cg == 1 ? 80.0 : 72.0);
             double block = 2.35 * bn > 290.0 ? 2.35 * bn : 290.0;
-            if (bytes / 68.0 > block) block = bytes / 68.0;
+            if (copies > block) block = copies;
             for (int split = 1; split * cg <= 16 && split <= blocks; split *= 2) {
-                if (split > 1 && tiles * split * cg > num_sms) break;
-                const double epilogue = split > 1 ? 5000.0 + 45.0 * bn : 16.0 * bn;
-                double unit_time = static_cast<double>(ceil_div(blocks, split)) * block;
-                if (split == 1 && epilogue > unit_time) unit_time = epilogue;
-                double cost = static_cast<double>(ceil_div(tiles * split, num_sms / cg)) *
-                              unit_time;
+                const int slots = split * cg <= 2 ? num_sms / (split * cg)
+                                                  : active_clusters(split * cg, num_sms);
+                if (split > 1 && tiles > slots) break;
+                const double tail = split == 1 ? 1200.0 + 20.0 * bn
+                                    : cg == 1  ? 3300.0 + 430.0 * split + 18.0 * bn
+                                               : 7000.0 + 430.0 * split + 12.0 * bn;
+                double tile = static_cast<double>(ceil_div(blocks, split)) * block;
+                if (split == 1 && tail > tile) tile = tail;
+                double cost = static_cast<double>(ceil_div(tiles, slots)) * tile;
                 if (cost < hbm) cost = hbm;
-                cost += epilogue;
+                cost += tail;
                 if (cost < least) {
                     least = cost;
                     best = {cg, bn, split};
                 }
             }
-            if (bn >= g.N) break;
         }
     }
     return best;
@@ -840,10 +883,6 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
         p.box_rows = 16;
     } else {
         p.n_tiles = static_cast<int>(ceil_div(g.N, p.bn));
-        if (!g.b_mn) {      // even out the columns
-            const int unit = 16 * cut.cg;
-            p.bn = static_cast<int>(ceil_div(ceil_div(g.N, p.n_tiles), unit)) * unit;
-        }
         p.box_rows = p.bn / cut.cg;
         units = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.split;
     }
