@@ -34,6 +34,7 @@ struct Gemm {
     int E;                      // 0: not grouped
     const int32_t *offsets, *counts, *row_token;
     int64_t b_rows;             // rows of B
+    int64_t b_pitch;            // values from one of its rows (of k: b_mn) to the next
 };
 
 // Plain tiled kernel of fp32 multiply-adds: any size, alignment and layout.
@@ -51,14 +52,14 @@ bool launch_gemm_decode(const Gemm &g, int num_sms, cudaStream_t stream, cudaErr
 // Barrier waits that gave up since the library was loaded on this device.
 cudaError_t read_lost_waits(unsigned *count);
 
-// dz of the backward passes, its bf16 rounding into dz [T, cols] (null:
-// none), and the column sums into dbias (bf16 [cols], null: none).  Linear:
+// dz of the backward passes, its bf16 rounding into dz [T, pitch] (null: none;
+// the values past cols are not written), and the column sums into dbias (bf16 [cols], null: none).  Linear:
 // cols = n, dz = dout * act'(preact), or dout without preact.  Gated: cols =
 // 2n, dout [T, n], preact [T, 2n].  partial: fp32 [ceil(T / kBiasRows), cols]
 // scratch, used with dbias.
 constexpr int kBiasRows = 32;
 cudaError_t launch_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
-                      uint16_t *dz, float *partial, uint16_t *dbias, int T, int n,
+                      uint16_t *dz, int64_t pitch, float *partial, uint16_t *dbias, int T, int n,
                       cudaStream_t stream);
 
 // The grouped layout (moe_permute).  permute_chunks: rows of E counts that

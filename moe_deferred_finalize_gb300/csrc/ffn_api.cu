@@ -19,10 +19,11 @@ bool valid_features(int n) { return n >= 1 && n <= MOEF_MAX_FEATURES; }
 
 const uint16_t *u16(const void *p) { return static_cast<const uint16_t *>(p); }
 
-// Bytes of the bf16 dz and the fp32 partial column sums, each 16-byte aligned.
-size_t dz_bytes(int64_t T, int64_t cols) {
-    return static_cast<size_t>((T * cols * 2 + 15) / 16 * 16);
-}
+// dz has rows of a multiple of 8 values, so that the tensor-core kernels can
+// copy it whatever the number of features is.
+int64_t dz_pitch(int64_t cols) { return (cols + 7) / 8 * 8; }
+
+size_t dz_bytes(int64_t T, int64_t cols) { return static_cast<size_t>(T * dz_pitch(cols) * 2); }
 
 size_t backward_bytes(int64_t T, int64_t cols) {
     const int64_t rows = T > 0 ? (T - 1) / moef::kBiasRows + 1 : 0;
@@ -71,17 +72,20 @@ moef_status backward(const void *dout, const void *x, const void *weight, moef_a
             st = cuda_status(cudaMemsetAsync(dbias, 0, static_cast<size_t>(cols) * 2, stream));
         return st;
     }
-    uint16_t *dz = needs_preact ? static_cast<uint16_t *>(workspace) : nullptr;
+    // dout itself when it is dz and can be copied as it lies
+    const bool has_dz = needs_preact || cols % 8 || !aligned(dout, 16);
+    uint16_t *dz = has_dz && (dx || dweight) ? static_cast<uint16_t *>(workspace) : nullptr;
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                                dz_bytes(T, cols));
-    if (needs_preact || dbias) {
+    if (dz || dbias) {
         const moef_status st = cuda_status(moef::launch_dz(
-            u16(dout), u16(preact), static_cast<int>(act), gated, dz, partial,
+            u16(dout), u16(preact), static_cast<int>(act), gated, dz, dz_pitch(cols), partial,
             static_cast<uint16_t *>(dbias), T, n, stream));
         if (st != MOEF_OK) return st;
     }
     Gemm g{};
-    g.b = needs_preact ? dz : u16(dout);
+    g.b = dz ? dz : u16(dout);
+    g.b_pitch = dz ? dz_pitch(cols) : cols;
     if (dx) {
         g.a = u16(weight);
         g.a_mn = 1;
@@ -136,6 +140,7 @@ moef_status expert_product(const void *x, int64_t T, const int32_t *row_token,
     g.counts = counts;
     g.row_token = row_token;
     g.b_rows = T;
+    g.b_pitch = K;
     return run_gemm(g, stream);
 }
 
@@ -168,6 +173,7 @@ moef_status moe_linear(const void *x, const void *weight, const void *bias,
     g.preact = static_cast<uint16_t *>(preact);
     g.act = static_cast<int>(act);
     g.b_rows = T;
+    g.b_pitch = K;
     return run_gemm(g, stream);
 }
 
@@ -206,6 +212,7 @@ moef_status moe_gated_ffn(const void *x, const void *weight, const void *bias,
     g.preact = static_cast<uint16_t *>(preact);
     g.act = static_cast<int>(act);
     g.b_rows = T;
+    g.b_pitch = H;
     return run_gemm(g, stream);
 }
 

@@ -26,8 +26,8 @@ constexpr int kDzRows = kBiasRows / kDzWarps;       // rows per thread
 
 template <int VEC, bool GATED, int ACT>
 __global__ void __launch_bounds__(kDzThreads)
-dz_kernel(const uint16_t *dout, const uint16_t *preact, uint16_t *dz, float *partial, int T,
-          int n) {
+dz_kernel(const uint16_t *dout, const uint16_t *preact, uint16_t *dz, int64_t pitch,
+          float *partial, int T, int n) {
     using Ops = VecOps<VEC>;
     using V = typename Ops::V;
     constexpr int kHalves = GATED ? 2 : 1;
@@ -35,8 +35,8 @@ dz_kernel(const uint16_t *dout, const uint16_t *preact, uint16_t *dz, float *par
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int cols = kHalves * n;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kBiasRows;
-    allow_next_kernel();
     wait_previous_kernel();
+    allow_next_kernel();
     for (int i0 = blockIdx.y * 32 * VEC; i0 < n; i0 += gridDim.y * 32 * VEC) {
         const int i = i0 + lane * VEC;
         float sum[kHalves][VEC] = {};
@@ -81,7 +81,7 @@ dz_kernel(const uint16_t *dout, const uint16_t *preact, uint16_t *dz, float *par
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) sum[h][j] += out[h][j];
                     // read again by both products: an ordinary store keeps it in L2
-                    if (dz) *reinterpret_cast<V *>(dz + t * cols + h * n + i) =
+                    if (dz) *reinterpret_cast<V *>(dz + t * pitch + h * n + i) =
                                 Ops::from_f32(out[h]);
                 }
             }
@@ -109,8 +109,8 @@ dz_kernel(const uint16_t *dout, const uint16_t *preact, uint16_t *dz, float *par
 __global__ void __launch_bounds__(256)
 bias_sum_kernel(const float *partial, int rows, int cols, uint16_t *dbias) {
     __shared__ float s[8][32];
-    allow_next_kernel();
     wait_previous_kernel();
+    allow_next_kernel();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x / 32;
     float sum = 0.f;
     if (c < cols)
@@ -142,12 +142,12 @@ cudaError_t start(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_
 
 template <int VEC, bool GATED>
 cudaError_t start_dz(const uint16_t *dout, const uint16_t *preact, int act, uint16_t *dz,
-                     float *partial, int T, int n, cudaStream_t stream) {
+                     int64_t pitch, float *partial, int T, int n, cudaStream_t stream) {
     const int64_t across = (static_cast<int64_t>(n) + 32 * VEC - 1) / (32 * VEC);
     const dim3 grid(static_cast<unsigned>((T - 1) / kBiasRows + 1),
                     static_cast<unsigned>(across < 65535 ? across : 65535));
     auto go = [&](auto *kernel) {
-        return start(kernel, grid, kDzThreads, stream, dout, preact, dz, partial, T, n);
+        return start(kernel, grid, kDzThreads, stream, dout, preact, dz, pitch, partial, T, n);
     };
     switch (act) {
         case MOEF_ACT_SILU: return go(dz_kernel<VEC, GATED, MOEF_ACT_SILU>);
@@ -161,7 +161,7 @@ cudaError_t start_dz(const uint16_t *dout, const uint16_t *preact, int act, uint
 }  // namespace
 
 cudaError_t launch_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
-                      uint16_t *dz, float *partial, uint16_t *dbias, int T, int n,
+                      uint16_t *dz, int64_t pitch, float *partial, uint16_t *dbias, int T, int n,
                       cudaStream_t stream) {
     const uintptr_t bits = reinterpret_cast<uintptr_t>(dout) | reinterpret_cast<uintptr_t>(preact) |
                            reinterpret_cast<uintptr_t>(dz);
@@ -169,11 +169,11 @@ cudaError_t launch_dz(const uint16_t *dout, const uint16_t *preact, int act, int
     const bool vec = n % 8 == 0 && bits % 16 == 0;
     cudaError_t err;
     if (gated)
-        err = vec ? start_dz<8, true>(dout, preact, act, dz, part, T, n, stream)
-                  : start_dz<1, true>(dout, preact, act, dz, part, T, n, stream);
+        err = vec ? start_dz<8, true>(dout, preact, act, dz, pitch, part, T, n, stream)
+                  : start_dz<1, true>(dout, preact, act, dz, pitch, part, T, n, stream);
     else
-        err = vec ? start_dz<8, false>(dout, preact, act, dz, part, T, n, stream)
-                  : start_dz<1, false>(dout, preact, act, dz, part, T, n, stream);
+        err = vec ? start_dz<8, false>(dout, preact, act, dz, pitch, part, T, n, stream)
+                  : start_dz<1, false>(dout, preact, act, dz, pitch, part, T, n, stream);
     if (err != cudaSuccess || !dbias) return err;
     const int cols = gated ? 2 * n : n;
     return start(bias_sum_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), 256, stream,

@@ -88,8 +88,8 @@ decode_kernel(const Gemm g, const int features) {
     for (int n = 0; n < NT; ++n)
         x[n] = g.b + static_cast<int64_t>(8 * n + row < g.N ? 8 * n + row : 0) * g.K + k8;
 
-    allow_next_kernel();
     wait_previous_kernel();
+    allow_next_kernel();
 
     float acc[NT][4] = {};
     const int full = g.K / kStepK, steps = (g.K + kStepK - 1) / kStepK;
@@ -208,8 +208,8 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }  // namespace
 
 bool launch_gemm_decode(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err) {
-    if (g.E || g.a_mn || g.b_mn || g.N > 8 * kDecodeTiles || g.K % 8 || !aligned16(g.a) ||
-        !aligned16(g.b))
+    if (g.E || g.a_mn || g.b_mn || g.N > 8 * kDecodeTiles || g.K % 8 || g.b_pitch != g.K ||
+        !aligned16(g.a) || !aligned16(g.b))
         return false;
     *err = g.N <= 8 ? choose<1>(g, num_sms, stream) : choose<2>(g, num_sms, stream);
     return true;

@@ -461,10 +461,9 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
     }
     if (warp == 1) tmem_alloc<CG>(smem_addr(&h->tmem), 2 * kMaxBn);
     // Launched as a dependent of the previous kernel on the stream: up to here
-    // nothing in global memory was touched.  The next kernel may launch at
-    // once; its CTAs get their SMs as ours leave them.
-    allow_next_kernel();
+    // nothing in global memory was touched.
     wait_previous_kernel();
+    allow_next_kernel();
     if (warp == 0) {
         if (g.E) {      // column tiles of each expert
             int most = 0;
@@ -862,8 +861,8 @@ Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms) {
 }  // namespace
 
 bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err) {
-    if (!aligned16(g.a) || !aligned16(g.b) || (g.a_mn ? g.M : g.K) % 8 ||
-        (g.b_mn ? g.N : g.K) % 8 || !encoder())
+    if (!aligned16(g.a) || !aligned16(g.b) || (g.a_mn ? g.M : g.K) % 8 || g.b_pitch % 8 ||
+        !encoder())
         return false;
     const int rows_per_feature = g.gated ? 2 : 1;
     const int64_t a_rows = static_cast<int64_t>(g.M) * rows_per_feature;
@@ -911,7 +910,7 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
     {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.b_mn ? g.N : g.K),
                                     static_cast<cuuint64_t>(g.b_mn ? g.K : g.b_rows)};
-        const cuuint64_t strides[1] = {dims[0] * 2};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.b_pitch) * 2};
         const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(g.b_mn ? 64
                                                                : p.gather ? 1 : p.box_rows)};
         ok = ok && encode(&mb, g.b, 2, dims, strides, box);

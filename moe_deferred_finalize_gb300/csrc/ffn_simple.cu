@@ -58,7 +58,7 @@ gemm_simple_kernel(const Gemm g) {
     const uint16_t *a = g.a + static_cast<int64_t>(e) * arows * g.K;
     const uint16_t *bias = g.bias ? g.bias + static_cast<int64_t>(e) * arows : nullptr;
     const int64_t a_pitch = g.a_mn ? arows : g.K;
-    const int64_t b_pitch = g.b_mn ? g.N : g.K;
+    const int64_t b_pitch = g.b_pitch;
     const int tm = threadIdx.x % 16, tn = threadIdx.x / 16;
 
     for (int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTile; n0 < count;

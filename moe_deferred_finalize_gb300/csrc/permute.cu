@@ -131,8 +131,8 @@ cluster_kernel(const int32_t *ids, int n, int steps, int K, int E, int tile, int
 
     for (int i = threadIdx.x; i < kWarps * E / 2; i += kThreads)
         reinterpret_cast<uint32_t *>(hist)[i] = 0u;
-    allow_next_kernel();
     wait_previous_kernel();
+    allow_next_kernel();
 
     const int i0 = (rank * kWarps + w) * steps * 32 + lane;
     int key[kRun], within[kRun];
@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kThreads)
 count_kernel(const int32_t *ids, int64_t n, int64_t chunk, int E, int32_t *chunk_counts) {
     extern __shared__ int32_t smem[];
     for (int e = threadIdx.x; e < E; e += kThreads) smem[e] = 0;
-    allow_next_kernel();
     wait_previous_kernel();
+    allow_next_kernel();
     __syncthreads();
     const int64_t i0 = blockIdx.x * chunk, i1 = i0 + chunk < n ? i0 + chunk : n;
 #pragma unroll 8
@@ -225,8 +225,8 @@ place_kernel(const int32_t *ids, int64_t n, int64_t chunk, int K, int E, int til
     int32_t *hist = smem + 4 * E;                   // [warps][E]
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     for (int i = threadIdx.x; i < kWarps * E; i += kThreads) hist[i] = 0;
-    allow_next_kernel();
     wait_previous_kernel();
+    allow_next_kernel();
     __syncthreads();
 
     // the warps' counts

@@ -31,7 +31,9 @@ __device__ __forceinline__ void wait_previous_kernel() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Lets the next kernel begin launching.
+// Lets the next kernel begin launching.  Only after wait_previous_kernel: then
+// a kernel that has started can rely on every kernel before the previous one
+// being complete (moe_finalize's MOEF_FLAG_ROUTING_READY does).
 __device__ __forceinline__ void allow_next_kernel() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

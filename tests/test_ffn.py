@@ -471,6 +471,147 @@ def test_moe_layer(cuda_lib, T, H, I, E, K, tile):
     assert rel < 3 * R.BF16       # three roundings in a row, each at most 2^-8
 
 
+@pytest.mark.parametrize("name", ["none", "gelu"])
+@pytest.mark.parametrize("T,N,K", [(300, 1001, 264), (17, 9, 64), (129, 63, 136)])
+def test_backward_of_odd_feature_counts(cuda_lib, name, T, N, K):
+    x, w, d = rand(43, T, K), rand(44, N, K, scale=K ** -0.5), rand(45, T, N, scale=0.1)
+    pre = None if name == "none" else cuda_lib.linear(x, w, save_preact=True)["preact"]
+    got = cuda_lib.linear_backward(d, x, w, activation=name, preact=pre, want_dbias=True)
+    R.check(got, R.backward(d, x, w, pre, name, False), name)
+    if N > 60:
+        w = rand(46, 2 * N, K, scale=K ** -0.5)
+        pre = cuda_lib.gated_ffn(x, w, activation=name, save_preact=True)["preact"]
+        got = cuda_lib.gated_ffn_backward(d, x, w, pre, activation=name, want_dbias=True)
+        R.check(got, R.backward(d, x, w, pre, name, True), "gated " + name)
+
+
+def test_backward_of_a_misaligned_dout(cuda_lib):
+    x, w, d = rand(47, 50, 64), rand(48, 72, 64), rand(49, 50, 72)
+    got = cuda_lib.linear_backward(misaligned(d), x, w, want_dbias=True)
+    R.check(got, R.backward(d, x, w, None, "none", False))
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """Outputs of more than 2^31 elements: the first, middle and last rows."""
+    T, N, K = 300_000, 8192, 64
+    x, w = rand(200, T, K), rand(201, N, K, scale=0.1)
+    out = cuda_lib.linear(x, w)["out"]
+    for rows in (slice(0, 40), slice(262_120, 262_160), slice(T - 40, T)):
+        R.check({"out": out[rows]}, R.linear(x[rows], w), f"rows {rows.start}")
+    del out
+    h = cuda_lib.gated_ffn(x, torch.cat([w, w.flip(0), w, w]), save_preact=True)
+    rows = slice(T - 40, T)
+    R.check({k: v[rows] for k, v in h.items()},
+            R.gated(x[rows], torch.cat([w, w.flip(0), w, w])), "gated")
+
+
+def test_expert_weights_past_32_bits(cuda_lib):
+    E, H, I, T = 300, 4096, 1024, 8         # 2.5e9 weights
+    w = torch.empty(E, 2 * I, H, dtype=BF16, device="cuda")
+    for e in range(0, E, 50):
+        w[e:e + 50].normal_(0.0, H ** -0.5)
+    ids = torch.tensor([[0, E - 1], [E - 1, 255], [256, 257], [1, 2], [299, 298], [3, 4], [5, 6],
+                        [7, 0]], dtype=torch.int32, device="cuda")
+    m = cuda_lib.permute_tokens(ids, E, 4)
+    x = rand(202, T, H)
+    h = cuda_lib.expert_gated_ffn(x, m["row_token"], m["offsets"], m["counts"], w)
+    for t, k in ((0, 1), (1, 1), (2, 0), (4, 0), (7, 1)):
+        row = int(m["idx_map"][t, k])
+        R.check({"out": h[row:row + 1]}, R.gated(x[t:t + 1], w[int(ids[t, k])]), f"{t},{k}")
+
+
+def test_finalize_may_read_the_routing_early_behind_these_kernels(cuda_lib):
+    """moe_finalize with routing_ready reads the row map before the expert
+    product in front of it has finished; the row map must be complete when
+    that product starts, however early the launches overlap."""
+    mf = cuda_lib
+    T, K, E, H, I = 64, 4, 16, 256, 64
+    x, w13, w2 = rand(210, T, H), rand(211, E, 2 * I, H, scale=0.1), rand(212, E, H, I, scale=0.1)
+    shared = rand(213, T, H)
+    wts = torch.rand(T, K, device="cuda")
+    sets = [ids_of(220 + i, T, K, E, "all").cuda() for i in range(4)]
+    P = mf.permute_rows(T, K, E, 8)
+    bufs = {"idx_map": torch.zeros(T, K, dtype=torch.int32, device="cuda"),
+            "row_token": torch.empty(P, dtype=torch.int32, device="cuda"),
+            "offsets": torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+            "counts": torch.empty(E, dtype=torch.int32, device="cuda")}
+    h, y = (torch.zeros(P, n, dtype=BF16, device="cuda") for n in (I, H))
+
+    def layer(ids, ready):
+        m = mf.permute_tokens(ids, E, 8, **bufs)
+        mf.expert_gated_ffn(x, m["row_token"], m["offsets"], m["counts"], w13, out=h)
+        mf.expert_linear(h, m["offsets"], m["counts"], w2, out=y)
+        return mf.moe_finalize(y, m["idx_map"], wts, "fp32", shared, routing_ready=ready)["out"]
+
+    want = []
+    for ids in sets:
+        want.append(layer(ids, False))
+        torch.cuda.synchronize()
+    for _ in range(20):
+        got = [layer(ids, True) for ids in sets]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_calls_from_threads(cuda_lib):
+    """Two host threads on their own streams at once."""
+    import threading
+    xs = [rand(230 + i, 40 + 100 * i, 512) for i in range(2)]
+    w = rand(232, 640, 512, scale=0.05)
+    want = [cuda_lib.linear(x, w)["out"] for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        torch.cuda.set_device(0)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                out = cuda_lib.linear(xs[i], w)["out"]
+                torch.cuda.current_stream().synchronize()
+                if not torch.equal(out, want[i]):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_python_and_one_pass_checks_agree(cuda_lib, monkeypatch):
+    """The checked call through the extension and the Python checks with the
+    ctypes call give the same bits and refuse the same calls."""
+    from moe_deferred_finalize_gb300 import _abi
+    x, w, b, r = rand(240, 20, 128), rand(241, 48, 128), rand(242, 48), rand(243, 20, 48)
+    calls = [lambda: cuda_lib.linear(x, w, bias=b, residual=r, activation="silu",
+                                     save_preact=True),
+             lambda: cuda_lib.linear(x, w, out_dtype=torch.float32),
+             lambda: cuda_lib.gated_ffn(x, w, bias=b, save_preact=True)]
+    bad = [lambda: cuda_lib.linear(x.t(), w), lambda: cuda_lib.linear(x, w[:, :64]),
+           lambda: cuda_lib.linear(x, w, bias=b[:40]), lambda: cuda_lib.linear(x.float(), w),
+           lambda: cuda_lib.linear(x, w, residual=r[:10]), lambda: cuda_lib.linear(x, w, out=x),
+           lambda: cuda_lib.linear(x, w, activation="tanh"),
+           lambda: cuda_lib.linear(x, w, out_dtype=torch.float16),
+           lambda: cuda_lib.linear(x.cpu(), w), lambda: cuda_lib.gated_ffn(x, w[:47]),
+           lambda: cuda_lib.gated_ffn(x, w, out=r), lambda: cuda_lib.gated_ffn(x, w, bias=b[1:]),
+           lambda: cuda_lib.gated_ffn(x, w, preact=x)]
+    for f in bad:
+        with pytest.raises((ValueError, TypeError)):
+            f()
+    fast = [f() for f in calls]
+    monkeypatch.setattr(_abi, "_FAST", None)
+    for f, ref in zip(calls, fast):
+        got = f()
+        assert set(got) == set(ref)
+        for key in ref:
+            assert got[key].dtype == ref[key].dtype and torch.equal(got[key], ref[key])
+    for f in bad:
+        with pytest.raises((ValueError, TypeError)):
+            f()
+
+
 def test_no_barrier_wait_was_lost(cuda_lib):
     """Last: none of the launches above gave up a wait."""
     torch.cuda.synchronize()
