@@ -61,6 +61,15 @@ def _address(name):
     return _ADDRESS[name]
 
 
+def _call(kind, name, *args):
+    """An entry point's status: through the _fastcall extension's ``kind``
+    (direct argument conversion) when it was built, else through ctypes."""
+    fast = _abi._fastcall()
+    if fast is not None:
+        return getattr(fast, kind)(_address(name), *args)
+    return getattr(_lib(), name)(*args)
+
+
 def _fast_device(fast, x):
     """The device index of x when the one-pass check of the _fastcall
     extension can take the call (x on the current device), else None."""
@@ -101,6 +110,13 @@ def _output(t, name, dtype, shape, device):
 def _optional(t, name, shape, device):
     if t is not None:
         _check(t, name, _BF16, shape, device)
+
+
+def _workspace_bytes(workspace, device):
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device or \
+            not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same device")
+    return workspace.numel() * workspace.element_size()
 
 
 def _raise(status, where):
@@ -241,17 +257,15 @@ def _backward(where, gated, dout, x, weight, preact, activation, want_dx, want_d
     lib = _lib()
     size = lib.moe_gated_ffn_backward_workspace_bytes if gated \
         else lib.moe_linear_backward_workspace_bytes
-    need = int(size(T, n))
+    nbytes = int(size(T, n))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the same device")
-    nbytes = workspace.numel() * workspace.element_size()
-    fn = lib.moe_gated_ffn_backward if gated else lib.moe_linear_backward
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    else:
+        nbytes = _workspace_bytes(workspace, dev)
     with _on(dev):
-        st = fn(_ptr(dout), _ptr(x), _ptr(weight), act, _ptr(preact), _ptr(res.get("dx")),
-                _ptr(res.get("dweight")), _ptr(res.get("dbias")), T, n, K, _ptr(workspace),
-                nbytes, _stream(stream, dev))
+        st = _call("call_backward", where, _ptr(dout), _ptr(x), _ptr(weight), act, _ptr(preact),
+                   _ptr(res.get("dx")), _ptr(res.get("dweight")), _ptr(res.get("dbias")), T, n, K,
+                   _ptr(workspace), nbytes, _stream(stream, dev))
     _raise(st, where)
     return res
 
@@ -358,15 +372,13 @@ def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
            "counts": _output(counts, "counts", torch.int32, (max(E, 0),), dev)}
     nbytes = int(lib.moe_permute_workspace_bytes(T, K, E))
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the same device")
-        nbytes = workspace.numel() * workspace.element_size()
+        nbytes = _workspace_bytes(workspace, dev)
     elif nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     with _on(dev):
-        st = lib.moe_permute(_ptr(expert_ids), T, K, E, tile, _ptr(res["idx_map"]),
-                             _ptr(res["row_token"]), P, _ptr(res["offsets"]), _ptr(res["counts"]),
-                             _ptr(workspace), nbytes, _stream(stream, dev))
+        st = _call("call_permute", "moe_permute", _ptr(expert_ids), T, K, E, tile,
+                   _ptr(res["idx_map"]), _ptr(res["row_token"]), P, _ptr(res["offsets"]),
+                   _ptr(res["counts"]), _ptr(workspace), nbytes, _stream(stream, dev))
     _raise(st, "moe_permute")
     return res
 
@@ -391,10 +403,9 @@ def _expert(where, gated, x, row_token, offsets, counts, weight, bias, activatio
         P = row_token.numel()
         _check(row_token, "row_token", _I32, (P,), dev)
     out = _output(out, "out", torch.bfloat16, (P, M), dev)
-    fn = _lib().moe_expert_gated_ffn if gated else _lib().moe_expert_linear
     with _on(dev):
-        st = fn(_ptr(x), T, _ptr(row_token), _ptr(offsets), _ptr(counts), _ptr(weight),
-                _ptr(bias), act, _ptr(out), P, E, M, K, _stream(stream, dev))
+        st = _call("call_expert", where, _ptr(x), T, _ptr(row_token), _ptr(offsets), _ptr(counts),
+                   _ptr(weight), _ptr(bias), act, _ptr(out), P, E, M, K, _stream(stream, dev))
     _raise(st, where)
     return out
 

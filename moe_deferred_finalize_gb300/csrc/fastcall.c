@@ -7,7 +7,8 @@
  * arguments are packed once into a C struct (a capsule) and each call passes
  * only the stream.  checked_call does the Python binding's argument checks
  * on DLPack descriptions of the tensors before calling; checked_linear and
- * checked_gated do so for moe_linear and moe_gated_ffn.  Nothing here
+ * checked_gated do so for moe_linear and moe_gated_ffn, and call_backward,
+ * call_expert and call_permute convert those calls' arguments.  Nothing here
  * computes anything.
  */
 #define PY_SSIZE_T_CLEAN
@@ -344,6 +345,74 @@ static PyObject *checked_gated(PyObject *self, PyObject *const *a, Py_ssize_t na
                               preact, (int)x[0], (int)(w[0] / 2), (int)x[1], stream));
 }
 
+/* ---------------------------------------------------------------------------
+ * call_backward, call_expert, call_permute: the entry points of moe_ffn.h with
+ * many arguments, converted directly.  The first argument is the function's
+ * address, the others are its own in order, pointers as ints or None; the
+ * tensors were checked by the binding. */
+typedef int (*backward_fn)(const void *dout, const void *x, const void *weight, int act,
+                           const void *preact, void *dx, void *dweight, void *dbias, int T,
+                           int n, int K, void *workspace, size_t workspace_bytes, void *stream);
+typedef int (*expert_fn)(const void *x, int64_t T, const int32_t *row_token,
+                         const int32_t *offsets, const int32_t *counts, const void *weight,
+                         const void *bias, int act, void *out, int64_t P, int E, int M, int K,
+                         void *stream);
+typedef int (*permute_fn)(const int32_t *ids, int T, int K, int E, int tile, int32_t *idx_map,
+                          int32_t *row_token, int64_t P, int32_t *offsets, int32_t *counts,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+enum { MOST_ARGS = 15 };
+
+/* n ints (or None, as 0) into v; 0, or -1 with a Python error */
+static int parse_ints(PyObject *const *a, Py_ssize_t nargs, int n, const char *name,
+                      long long *v) {
+    if (nargs != n) {
+        PyErr_Format(PyExc_TypeError, "%s takes %d arguments", name, n);
+        return -1;
+    }
+    for (int i = 0; i < n; ++i) v[i] = a[i] == Py_None ? 0 : PyLong_AsLongLong(a[i]);
+    if (PyErr_Occurred()) return -1;
+    if (!v[0]) {
+        PyErr_SetString(PyExc_ValueError, "null function pointer");
+        return -1;
+    }
+    return 0;
+}
+
+/* PTR(i): argument i as a pointer; INT(i): as an int, out of range as -1 */
+#define PTR(i) ((void *)(intptr_t)v[i])
+#define INT(i) (v[i] < -1 || v[i] > 0x7FFFFFFF ? -1 : (int)v[i])
+
+static PyObject *call_backward(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    long long v[MOST_ARGS];
+    if (parse_ints(a, nargs, 15, "call_backward", v) != 0) return NULL;
+    return PyLong_FromLong(((backward_fn)PTR(0))(PTR(1), PTR(2), PTR(3), INT(4), PTR(5), PTR(6),
+                                                 PTR(7), PTR(8), INT(9), INT(10), INT(11),
+                                                 PTR(12), (size_t)v[13], PTR(14)));
+}
+
+static PyObject *call_expert(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    long long v[MOST_ARGS];
+    if (parse_ints(a, nargs, 15, "call_expert", v) != 0) return NULL;
+    return PyLong_FromLong(((expert_fn)PTR(0))(PTR(1), v[2], PTR(3), PTR(4), PTR(5), PTR(6),
+                                               PTR(7), INT(8), PTR(9), v[10], INT(11), INT(12),
+                                               INT(13), PTR(14)));
+}
+
+static PyObject *call_permute(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    long long v[MOST_ARGS];
+    if (parse_ints(a, nargs, 14, "call_permute", v) != 0) return NULL;
+    return PyLong_FromLong(((permute_fn)PTR(0))(PTR(1), INT(2), INT(3), INT(4), INT(5), PTR(6),
+                                                PTR(7), v[8], PTR(9), PTR(10), PTR(11),
+                                                (size_t)v[12], PTR(13)));
+}
+
+#undef PTR
+#undef INT
+
 /* call(capsule, stream_handle) -> status of moe_finalize_ex */
 static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
     (void)self;
@@ -371,6 +440,12 @@ static PyMethodDef methods[] = {
      "Check DLPack-described tensors and enqueue one moe_linear call."},
     {"checked_gated", (PyCFunction)(void (*)(void))checked_gated, METH_FASTCALL,
      "Check DLPack-described tensors and enqueue one moe_gated_ffn call."},
+    {"call_backward", (PyCFunction)(void (*)(void))call_backward, METH_FASTCALL,
+     "Call moe_linear_backward or moe_gated_ffn_backward."},
+    {"call_expert", (PyCFunction)(void (*)(void))call_expert, METH_FASTCALL,
+     "Call moe_expert_gated_ffn or moe_expert_linear."},
+    {"call_permute", (PyCFunction)(void (*)(void))call_permute, METH_FASTCALL,
+     "Call moe_permute."},
     {NULL, NULL, 0, NULL},
 };
 
