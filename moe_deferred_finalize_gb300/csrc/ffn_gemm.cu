@@ -6,13 +6,13 @@
 // most 31 columns, and every product of a layer reads its operands as they
 // lie, k-contiguous or m-contiguous (the descriptor's transpose bits).
 //
-// A CTA is eleven warps: two issue the TMA copies of 64-deep k blocks of A and
-// of B into a ring of shared-memory stages (128-byte swizzle), one lane of a
-// third issues the MMAs into TMEM, eight finish tiles.  (One warp for both
-// copies needed 430 clocks a block, near the 512 that the MMAs of the widest
-// tile take.)  The accumulator is double
-// buffered (2 x 256 TMEM columns), so a tile's epilogue runs under the next
-// tile's products.
+// A CTA is fourteen warps.  One issues the TMA copies of 64-deep k blocks of A
+// into a ring of shared-memory stages (128-byte swizzle), another those of B;
+// one warp for both needed 430 clocks a block, near the 512 that the MMAs of
+// the widest tile take.  Gathered rows are copied four to an instruction, so B
+// then has four warps.  One lane of a further warp issues the MMAs into TMEM,
+// and eight finish tiles.  The accumulator is double buffered (2 x 256 TMEM
+// columns), so a tile's epilogue runs under the next tile's products.
 //
 // Gated form: the A tile interleaves gate and up rows (g0, u0, g1, u1, ...),
 // which one 4-D tensor map [E][I][2][H] of the weights does in the copy.  A
@@ -39,7 +39,8 @@ namespace {
 
 constexpr int kEpilogueWarps = 8;
 constexpr int kCopyWarp = 2 + kEpilogueWarps;    // copies B; warp 0 copies A
-constexpr int kTcThreads = 32 * (kCopyWarp + 1);
+constexpr int kGatherWarps = 4;                 // copy B from kCopyWarp on when rows are gathered
+constexpr int kTcThreads = 32 * (kCopyWarp + kGatherWarps);
 constexpr int kBlockK = 64;                     // k values per stage: one 128-byte swizzle row
 constexpr int kATile = 128 * kBlockK * 2;       // bytes of A per CTA and stage
 constexpr int kMaxBn = 256;
@@ -562,18 +563,20 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                 for (const long long begin = clock64(); clock64() - begin < 2000000;)
                     __nanosleep(1000);
         }
-    } else if (warp == kCopyWarp) {
-        // ---- copies of B: one lane, or the warp when it gathers rows
+    } else if (warp >= kCopyWarp) {
+        // ---- copies of B: one lane, or eight of each warp when rows are gathered
         int s = 0;
         uint32_t phase = 1;
         if (p.gather) {
+            const int quad = (warp - kCopyWarp) * 8 + (lane & 7);       // of rows
             for (int ti = first_tile; ti < tiles; ti += step) {
                 const Tile t = tile_at<CG, GATED>(g, p, h, ti);
                 const int bnc = t.bn / CG;
                 int4 rows = make_int4(-1, -1, -1, -1);      // -1: a row of zeros
-                if (4 * lane < bnc) {
-                    const int valid = t.count - half * bnc - 4 * lane;
-                    const int32_t *at = g.row_token + t.row0 + half * bnc + 4 * lane;
+                const bool mine = lane < 8 && 4 * quad < bnc;
+                if (mine) {
+                    const int valid = t.count - half * bnc - 4 * quad;
+                    const int32_t *at = g.row_token + t.row0 + half * bnc + 4 * quad;
                     if (valid > 0) rows.x = at[0];
                     if (valid > 1) rows.y = at[1];
                     if (valid > 2) rows.z = at[2];
@@ -585,14 +588,14 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     const uint32_t full = smem_addr(&h->full[s]);
-                    if (4 * lane < bnc)
-                        tma_gather4<CG>(stage0 + s * stage_bytes + kATile + lane * 512, &map_b,
+                    if (mine)
+                        tma_gather4<CG>(stage0 + s * stage_bytes + kATile + quad * 512, &map_b,
                                         kb * kBlockK, rows, CG == 2 ? map_rank(full, lead) : full);
                     if (++s == stages) { s = 0; phase ^= 1; }
                 }
                 if (!ok) break;
             }
-        } else if (elect_one()) {
+        } else if (warp == kCopyWarp && elect_one()) {
             bool ok = true;
             for (int ti = first_tile; ti < tiles && ok; ti += step) {
                 const Tile t = tile_at<CG, GATED>(g, p, h, ti);
