@@ -191,14 +191,33 @@ cudaError_t start(const Gemm &g, int features, cudaStream_t stream) {
                    : cudaLaunchKernelEx(&cfg, decode_kernel<NT, false, W>, g, features);
 }
 
-template <int NT>
-cudaError_t choose(const Gemm &g, int num_sms, cudaStream_t stream) {
-    // Whole MMA rows when they give every SM a CTA, else down to a quarter of
-    // them: 256 router rows run on 64 CTAs instead of 16.  Up to one CTA per
-    // SM has 16 warps, more have 8 each, two to an SM.
+// Features per CTA: whole MMA rows when they give every SM a CTA, else down to
+// a quarter of them: 256 router rows run on 64 CTAs instead of 16.
+int features_per_cta(const Gemm &g, int num_sms) {
     int features = g.gated ? 8 : 16;
     const int least = features / 4;
     while (features > least && (g.M + features - 1) / features < num_sms) features /= 2;
+    return features;
+}
+
+// Whether this kernel or the tensor-core one is faster, from sweeps (us): this
+// one starts in 1.5 and reads 6.9 MB/us with up to 8 rows (3.5 and 6.0 with
+// 16), but a wave of its CTAs takes at least 1.8 (2.2), more than a short k
+// needs; the other one starts in 5.5 and reads 6.7 MB/us.  1 x 65536 x 512:
+// 25.0 here, 15.6 there; 16 x 16384 x 4096: 27.6 and 24.5; 16 x 4096 x 7168:
+// 13.6 and 15.5; 8 x 65536 x 7168: 137 and 140.
+bool pays(const Gemm &g, int features, int num_sms) {
+    const bool two = g.N > 8;
+    const int64_t ctas = (g.M + features - 1) / features;
+    const double mb = 2e-6 * g.M * (g.gated ? 2.0 : 1.0) * g.K;
+    const double waves = static_cast<double>((ctas + 2 * num_sms - 1) / (2 * num_sms));
+    const double read = mb / (two ? 6.0 : 6.9), latency = waves * (two ? 2.2 : 1.8);
+    return (two ? 3.5 : 1.5) + (read > latency ? read : latency) < 5.5 + mb / 6.7;
+}
+
+template <int NT>
+cudaError_t run(const Gemm &g, int features, int num_sms, cudaStream_t stream) {
+    // up to one CTA per SM has 16 warps, more have 8 each, two to an SM
     return (g.M + features - 1) / features <= num_sms ? start<NT, 16>(g, features, stream)
                                                       : start<NT, 8>(g, features, stream);
 }
@@ -211,7 +230,9 @@ bool launch_gemm_decode(const Gemm &g, int num_sms, cudaStream_t stream, cudaErr
     if (g.E || g.a_mn || g.b_mn || g.N > 8 * kDecodeTiles || g.K % 8 || g.b_pitch != g.K ||
         !aligned16(g.a) || !aligned16(g.b))
         return false;
-    *err = g.N <= 8 ? choose<1>(g, num_sms, stream) : choose<2>(g, num_sms, stream);
+    const int features = features_per_cta(g, num_sms);
+    if (!pays(g, features, num_sms)) return false;
+    *err = g.N <= 8 ? run<1>(g, features, num_sms, stream) : run<2>(g, features, num_sms, stream);
     return true;
 }
 

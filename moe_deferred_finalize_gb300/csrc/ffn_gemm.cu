@@ -60,6 +60,7 @@ struct TcPlan {
     int m_tiles, n_tiles;
     int gather;         // B rows are fetched by row_token
     int box_rows;       // rows of one B copy (k-contiguous B)
+    int wide_rows;      // of one copy through map_w, while that many are left (0: no map_w)
 };
 
 struct Header {
@@ -435,7 +436,8 @@ template <int CG, bool GATED>
 __global__ void __launch_bounds__(kTcThreads, 1)
 gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                const __grid_constant__ CUtensorMap map_a,
-               const __grid_constant__ CUtensorMap map_b) {
+               const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
     Header *h = reinterpret_cast<Header *>(smem + (base - smem_addr(smem)));
@@ -626,8 +628,12 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                     });
                 else
                     ok = blocks_of([&](uint32_t b, int k, uint32_t bar) {
-                        for (int i = 0; i < boxes; ++i)
-                            tma_2d<CG>(b + i * rows * 128, &map_b, k, row0 + i * rows, bar);
+                        int at = 0;
+                        if (p.wide_rows)
+                            for (; at + p.wide_rows <= bnc; at += p.wide_rows)
+                                tma_2d<CG>(b + at * 128, &map_w, k, row0 + at, bar);
+                        for (; at < bnc; at += rows)
+                            tma_2d<CG>(b + at * 128, &map_b, k, row0 + at, bar);
                     });
             }
         }
@@ -745,7 +751,7 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 template <int CG, bool GATED>
 cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CUtensorMap &b,
-                  int64_t grid, cudaStream_t stream) {
+                  const CUtensorMap &w, int64_t grid, cudaStream_t stream) {
     auto *kernel = gemm_tc_kernel<CG, GATED>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kSmemBytes);
@@ -764,7 +770,7 @@ cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CU
     attr[1].val.clusterDim = {static_cast<unsigned>(CG * p.split), 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = CG * p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, g, p, a, b);
+    return cudaLaunchKernelEx(&cfg, kernel, g, p, a, b, w);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -893,7 +899,7 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
     const int64_t slots = num_sms / cut.cg;
     const int64_t grid = cut.cg * (p.split > 1 || units < slots ? units : slots);
 
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, mw;
     bool ok;
     if (g.a_mn) {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.M), static_cast<cuuint64_t>(g.K)};
@@ -919,14 +925,20 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
         const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(g.b_mn ? 64
                                                                : p.gather ? 1 : p.box_rows)};
         ok = ok && encode(&mb, g.b, 2, dims, strides, box);
+        mw = mb;
+        if (g.E && !p.gather) {     // ragged groups: wide copies first, narrow ones for the rest
+            p.wide_rows = 64;
+            const cuuint32_t wide[2] = {64, 64};
+            ok = ok && encode(&mw, g.b, 2, dims, strides, wide);
+        }
     }
     if (!ok) return false;
     if (cut.cg == 2)
-        *err = g.gated ? start<2, true>(g, p, ma, mb, grid, stream)
-                       : start<2, false>(g, p, ma, mb, grid, stream);
+        *err = g.gated ? start<2, true>(g, p, ma, mb, mw, grid, stream)
+                       : start<2, false>(g, p, ma, mb, mw, grid, stream);
     else
-        *err = g.gated ? start<1, true>(g, p, ma, mb, grid, stream)
-                       : start<1, false>(g, p, ma, mb, grid, stream);
+        *err = g.gated ? start<1, true>(g, p, ma, mb, mw, grid, stream)
+                       : start<1, false>(g, p, ma, mb, mw, grid, stream);
     return true;
 }
 
