@@ -23,6 +23,10 @@
  * allocated or synchronised, work is enqueued on `stream` of the current
  * device, argument errors are returned before anything is enqueued, and a
  * call may be captured in a CUDA graph.  No call keeps state between calls.
+ * The first call on a device looks up launch limits and sets kernel
+ * attributes; make one of each kind before a capture.  Kernels are launched as
+ * programmatic dependents of the previous kernel on the stream, as in
+ * moe_finalize.h, and touch no global memory before it has completed.
  *
  * Arithmetic: products of bf16 values are summed in fp32; bias, activation,
  * gate product and residual are applied to the unrounded sum, and each output
@@ -163,7 +167,10 @@ moef_status moe_gated_ffn_backward(const void *dout, const void *x, const void *
  *   expert_ids  int32 [T, K]; an id outside [0, E) marks a slot without a row
  *               (a padding token of the batch, an expert of another rank)
  *   tile        each expert's rows are padded up to a multiple of tile (>= 1)
- *   idx_map     int32 [T, K]: the slot's row, or -1 for a slot without one
+ *   idx_map     int32 [T, K]: the slot's row, or -1 for a slot without one.
+ *               moe_finalize needs every entry in [0, P): pass it the tokens
+ *               whose slots all have rows (padding at the end of a batch: a
+ *               smaller T); moe_finalize_check_indices counts the others
  *   row_token   int32 [P]: the token of each row, -1 on padding rows
  *   P           rows of row_token, at least moe_permute_rows(T, K, E, tile)
  *   offsets     int32 [E + 1]: each expert's first row (a multiple of tile);

