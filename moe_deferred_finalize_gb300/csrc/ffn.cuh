@@ -44,6 +44,10 @@ cudaError_t launch_gemm_simple(const Gemm &g, cudaStream_t stream);
 // alignment or pitch rules them out; otherwise *err is the launch's result.
 bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err);
 
+// Two products (not grouped, not gated) in one launch; false (nothing launched)
+// also when two launches are priced lower.
+bool launch_two_gemms_tc(const Gemm *g, int num_sms, cudaStream_t stream, cudaError_t *err);
+
 // The kernel for a handful of rows (at most 8 * kDecodeTiles); false (nothing
 // launched) when the sizes or alignment are not its own.
 constexpr int kDecodeTiles = 2;

@@ -83,30 +83,43 @@ moef_status backward(const void *dout, const void *x, const void *weight, moef_a
             static_cast<uint16_t *>(dbias), T, n, stream));
         if (st != MOEF_OK) return st;
     }
-    Gemm g{};
-    g.b = dz ? dz : u16(dout);
-    g.b_pitch = dz ? dz_pitch(cols) : cols;
+    Gemm g[2] = {};
+    int n_products = 0;
     if (dx) {
-        g.a = u16(weight);
-        g.a_mn = 1;
-        g.M = K;
-        g.N = T;
-        g.K = cols;
-        g.out = dx;
-        g.b_rows = T;
-        const moef_status st = run_gemm(g, stream);
-        if (st != MOEF_OK) return st;
+        Gemm &x_grad = g[n_products++];
+        x_grad.a = u16(weight);
+        x_grad.a_mn = 1;
+        x_grad.M = K;
+        x_grad.N = T;
+        x_grad.K = cols;
+        x_grad.out = dx;
+        x_grad.b_rows = T;
     }
     if (dweight) {
-        g.a = u16(x);
-        g.a_mn = 1;
-        g.b_mn = 1;
-        g.M = K;
-        g.N = cols;
-        g.K = T;
-        g.out = dweight;
-        g.b_rows = cols;
-        return run_gemm(g, stream);
+        Gemm &w_grad = g[n_products++];
+        w_grad.a = u16(x);
+        w_grad.a_mn = 1;
+        w_grad.b_mn = 1;
+        w_grad.M = K;
+        w_grad.N = cols;
+        w_grad.K = T;
+        w_grad.out = dweight;
+        w_grad.b_rows = cols;
+    }
+    for (int i = 0; i < n_products; ++i) {
+        g[i].b = dz ? dz : u16(dout);
+        g[i].b_pitch = dz ? dz_pitch(cols) : cols;
+    }
+    if (n_products == 2) {
+        int sms = 0;
+        const moef_status st = cuda_status(moef::current_sms(&sms));
+        if (st != MOEF_OK) return st;
+        cudaError_t err = cudaSuccess;
+        if (moef::launch_two_gemms_tc(g, sms, stream, &err)) return cuda_status(err);
+    }
+    for (int i = 0; i < n_products; ++i) {
+        const moef_status st = run_gemm(g[i], stream);
+        if (st != MOEF_OK) return st;
     }
     return MOEF_OK;
 }

@@ -20,6 +20,10 @@
 // gate and its up value then sit in neighbouring TMEM lanes, and two shuffles
 // a pair of columns bring them into one thread.
 //
+// The two gradients of a layer are independent and often fill the last round of
+// tiles badly; they run as one launch over both products' tiles when that is
+// priced lower (2040 x 4096 x 4096: see the results table).
+//
 // Two launch forms:
 //   CG = 2  pairs of CTAs share tiles of 256 (m) x up to 256 (n): each CTA
 //           loads half of A and half of B, one instruction drives both SMs'
@@ -61,6 +65,16 @@ struct TcPlan {
     int gather;         // B rows are fetched by row_token
     int box_rows;       // rows of one B copy (k-contiguous B)
     int wide_rows;      // of one copy through map_w, while that many are left (0: no map_w)
+};
+
+// One launch: a product, or two that share the SMs (the gradients of a layer):
+// tiles below tiles0 are the first one's.
+template <int N>
+struct Work {
+    CUtensorMap map[N][3];      // A, B, B in wide copies
+    Gemm g[N];
+    TcPlan p[N];
+    int tiles0;
 };
 
 struct Header {
@@ -433,27 +447,28 @@ __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint3
 
 // --------------------------------------------------------------- kernel
 
-template <int CG, bool GATED>
+template <int CG, bool GATED, int N>
 __global__ void __launch_bounds__(kTcThreads, 1)
-gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
-               const __grid_constant__ CUtensorMap map_a,
-               const __grid_constant__ CUtensorMap map_b,
-               const __grid_constant__ CUtensorMap map_w) {
+gemm_tc_kernel(const __grid_constant__ Work<N> work) {
+    static_assert(N == 1 || (CG == 2 && !GATED), "two products run on pairs, without k in parts");
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
     Header *h = reinterpret_cast<Header *>(smem + (base - smem_addr(smem)));
     const uint32_t stage0 = base + kHeader;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     // the CTA's place in its cluster: which part of k, and which half of a pair
-    const int rank = CG == 2 || p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int split = N == 1 ? work.p[0].split : 1;
+    const int rank = CG == 2 || split > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int part = rank / CG, half = rank % CG, lead = part * CG;
     const bool leader = half == 0;
     const uint16_t pair = static_cast<uint16_t>(3 << lead);
     volatile int *gave_up = &h->gave_up;
 
     if (threadIdx.x == 0) {
-        prefetch_map(&map_a);
-        prefetch_map(&map_b);
+        for (int i = 0; i < N; ++i) {
+            prefetch_map(&work.map[i][0]);
+            prefetch_map(&work.map[i][1]);
+        }
         for (int i = 0; i < kMaxStages; ++i) {
             bar_init(smem_addr(&h->full[i]), 1);
             bar_init(smem_addr(&h->empty[i]), 1);
@@ -471,7 +486,9 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
     wait_previous_kernel();
     allow_next_kernel();
     if (warp == 0) {
-        if (g.E) {      // column tiles of each expert
+        const Gemm &g = work.g[0];
+        const TcPlan &p = work.p[0];
+        if (N == 1 && g.E) {        // column tiles of each expert
             int most = 0;
             for (int e = lane; e < g.E; e += 32) {
                 const int first = g.offsets[e];
@@ -505,6 +522,10 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
         } else if (lane == 0) {
             h->bn = p.bn;
             h->tiles = p.n_tiles * p.m_tiles;
+            if constexpr (N == 2) {
+                h->bn = max(p.bn, work.p[1].bn);
+                h->tiles += work.p[1].n_tiles * work.p[1].m_tiles;
+            }
         }
     }
     fence_before();
@@ -514,15 +535,24 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
     const int tiles = h->tiles;
     const uint32_t tmem = h->tmem;
     const int bnc_max = h->bn / CG;                 // B rows per CTA
-    const uint32_t b_bytes = bnc_max * kBlockK * 2;     // a multiple of 2048
+    // transposed B comes in blocks of 64 columns; a multiple of 2048 bytes
+    const bool any_mn = work.g[0].b_mn || work.g[N - 1].b_mn;
+    const uint32_t b_bytes = (any_mn ? (bnc_max + 63) / 64 * 64 : bnc_max) * kBlockK * 2;
     const uint32_t stage_bytes = kATile + b_bytes;
     const int stages = min(kMaxStages, static_cast<int>(kStageArea / stage_bytes));
-    const int blocks = (g.K + kBlockK - 1) / kBlockK;
-    const int kb0 = static_cast<int>(static_cast<int64_t>(blocks) * part / p.split);
-    const int kb1 = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / p.split);
-    const int group = CG * p.split;
+    const int group = CG * split;
     const int first_tile = blockIdx.x / group, step = gridDim.x / group;
     const int m_cta_rows = GATED ? 64 : 128;        // features per CTA
+    // the product that a tile belongs to, and this part's k blocks of it
+    auto product_of = [&](int ti) { return N == 2 && ti >= work.tiles0 ? 1 : 0; };
+    auto tile_of = [&](int ti, int q) {
+        return tile_at<CG, GATED>(work.g[q], work.p[q], h, q ? ti - work.tiles0 : ti);
+    };
+    auto k_range = [&](int q, int *kb0, int *kb1) {
+        const int blocks = (work.g[q].K + kBlockK - 1) / kBlockK;
+        *kb0 = static_cast<int>(static_cast<int64_t>(blocks) * part / split);
+        *kb1 = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / split);
+    };
 
     if (warp == 0) {
         // ---- copies of A, and the stages' byte counts
@@ -531,7 +561,13 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
             uint32_t phase = 1;
             bool ok = true;
             for (int ti = first_tile; ti < tiles && ok; ti += step) {
-                const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+                const int q = product_of(ti);
+                const Gemm &g = work.g[q];
+                const TcPlan &p = work.p[q];
+                const CUtensorMap *map = &work.map[q][0];
+                const Tile t = tile_of(ti, q);
+                int kb0, kb1;
+                k_range(q, &kb0, &kb1);
                 const int bnc = t.bn / CG, m0 = t.m0 + half * m_cta_rows;
                 const uint32_t b_tx = p.gather ? bnc * 128u
                                       : g.b_mn ? (bnc + 63) / 64 * 8192u
@@ -551,12 +587,12 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                 };
                 if (g.a_mn)
                     ok = blocks_of([&](uint32_t a, int k, uint32_t bar) {
-                        tma_2d<CG>(a, &map_a, m0, k, bar);
-                        tma_2d<CG>(a + 8192, &map_a, m0 + 64, k, bar);
+                        tma_2d<CG>(a, map, m0, k, bar);
+                        tma_2d<CG>(a + 8192, map, m0 + 64, k, bar);
                     });
                 else
                     ok = blocks_of([&](uint32_t a, int k, uint32_t bar) {
-                        tma_4d<CG>(a, &map_a, k, 0, m0, t.e, bar);
+                        tma_4d<CG>(a, map, k, 0, m0, t.e, bar);
                     });
             }
             // every stage handed back: no copy or arrival is left in flight
@@ -572,10 +608,13 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
         // ---- copies of B: one lane, or some of each warp when rows are gathered
         int s = 0;
         uint32_t phase = 1;
-        if (p.gather) {
+        if (N == 1 && work.p[0].gather) {
+            const Gemm &g = work.g[0];
+            int kb0, kb1;
+            k_range(0, &kb0, &kb1);
             const int quad = (warp - kCopyWarp) * kGatherLanes + lane;      // of rows
             for (int ti = first_tile; ti < tiles; ti += step) {
-                const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+                const Tile t = tile_of(ti, 0);
                 const int bnc = t.bn / CG;
                 int4 rows = make_int4(-1, -1, -1, -1);      // -1: a row of zeros
                 const bool mine = lane < kGatherLanes && 4 * quad < bnc;
@@ -594,7 +633,8 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                     if (!ok) break;
                     const uint32_t full = smem_addr(&h->full[s]);
                     if (mine)
-                        tma_gather4<CG>(stage0 + s * stage_bytes + kATile + quad * 512, &map_b,
+                        tma_gather4<CG>(stage0 + s * stage_bytes + kATile + quad * 512,
+                                        &work.map[0][1],
                                         kb * kBlockK, rows, CG == 2 ? map_rank(full, lead) : full);
                     if (++s == stages) { s = 0; phase ^= 1; }
                 }
@@ -603,7 +643,13 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
         } else if (warp == kCopyWarp && elect_one()) {
             bool ok = true;
             for (int ti = first_tile; ti < tiles && ok; ti += step) {
-                const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+                const int q = product_of(ti);
+                const Gemm &g = work.g[q];
+                const TcPlan &p = work.p[q];
+                const CUtensorMap *map = &work.map[q][1], *wide = &work.map[q][2];
+                const Tile t = tile_of(ti, q);
+                int kb0, kb1;
+                k_range(q, &kb0, &kb1);
                 const int bnc = t.bn / CG;
                 const int row0 = static_cast<int>(t.row0 + half * bnc);
                 const int rows = g.b_mn ? 64 : p.box_rows;      // of one copy
@@ -621,20 +667,20 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
                 if (g.b_mn)
                     ok = blocks_of([&](uint32_t b, int k, uint32_t bar) {
                         for (int i = 0; i < boxes; ++i)
-                            tma_2d<CG>(b + i * 8192, &map_b, row0 + i * 64, k, bar);
+                            tma_2d<CG>(b + i * 8192, map, row0 + i * 64, k, bar);
                     });
                 else if (boxes == 1)
                     ok = blocks_of([&](uint32_t b, int k, uint32_t bar) {
-                        tma_2d<CG>(b, &map_b, k, row0, bar);
+                        tma_2d<CG>(b, map, k, row0, bar);
                     });
                 else
                     ok = blocks_of([&](uint32_t b, int k, uint32_t bar) {
                         int at = 0;
                         if (p.wide_rows)
                             for (; at + p.wide_rows <= bnc; at += p.wide_rows)
-                                tma_2d<CG>(b + at * 128, &map_w, k, row0 + at, bar);
+                                tma_2d<CG>(b + at * 128, wide, k, row0 + at, bar);
                         for (; at < bnc; at += rows)
-                            tma_2d<CG>(b + at * 128, &map_b, k, row0 + at, bar);
+                            tma_2d<CG>(b + at * 128, map, k, row0 + at, bar);
                     });
             }
         }
@@ -646,7 +692,11 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
             uint32_t phase = 0;
             bool ok = true;
             for (int ti = first_tile; ti < tiles && ok; ti += step, ++n) {
-                const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+                const int q = product_of(ti);
+                const Gemm &g = work.g[q];
+                const Tile t = tile_of(ti, q);
+                int kb0, kb1;
+                k_range(q, &kb0, &kb1);
                 // D fp32, A and B bf16, transposes, N, M
                 const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
                                        (static_cast<uint32_t>(g.a_mn) << 15) |
@@ -680,35 +730,36 @@ gemm_tc_kernel(const __grid_constant__ Gemm g, const __grid_constant__ TcPlan p,
         const int side = (warp - 2) >> 2;
         int n = 0;
         for (int ti = first_tile; ti < tiles; ti += step, ++n) {
-            const Tile t = tile_at<CG, GATED>(g, p, h, ti);
+            const int q = product_of(ti);
+            const Tile t = tile_of(ti, q);
             const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                  (n & 1) * kMaxBn;
             const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             fence_after();
-            if (p.split > 1) break;         // joined below
+            if (split > 1) break;           // joined below
             const uint32_t bar = smem_addr(&h->acc_empty[n & 1]);
-            finish_tile<GATED>(g, t, t.m0 + half * m_cta_rows, acc, quarter, side, lane,
+            finish_tile<GATED>(work.g[q], t, t.m0 + half * m_cta_rows, acc, quarter, side, lane,
                                map_rank(bar, CG == 2 ? lead : cluster_rank()), 0, t.bn, nullptr,
                                0);
         }
     }
     __syncwarp();
-    if (p.split > 1) {
+    if (N == 1 && split > 1) {
         const bool works = warp >= 2 && warp < kCopyWarp;
         const int quarter = warp & 3, side = (warp - 2) >> 2;
         const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         cluster_sync();         // every part's products are done, their stages free
-        const Tile t = tile_at<CG, GATED>(g, p, h, first_tile);
+        const Tile t = tile_of(first_tile, 0);
         if (works && !*gave_up)
-            send_columns<CG>(t, acc, stage0, p.split, part, half, quarter, side, lane);
+            send_columns<CG>(t, acc, stage0, split, part, half, quarter, side, lane);
         cluster_sync();         // every part's sums have arrived
         if (works && !*gave_up) {
-            const int own = own_columns(t.bn, p.split);
-            finish_tile<GATED>(g, t, t.m0 + half * m_cta_rows, acc, quarter, side, lane, 0,
+            const int own = own_columns(t.bn, split);
+            finish_tile<GATED>(work.g[0], t, t.m0 + half * m_cta_rows, acc, quarter, side, lane, 0,
                                part * own, (part + 1) * own,
                                reinterpret_cast<const float *>(smem + (stage0 - smem_addr(smem))),
-                               p.split - 1);
+                               split - 1);
         }
     }
     fence_before();
@@ -750,13 +801,15 @@ bool encode(CUtensorMap *map, const void *p, int rank, const cuuint64_t *dims,
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-template <int CG, bool GATED>
-cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CUtensorMap &b,
-                  const CUtensorMap &w, int64_t grid, cudaStream_t stream) {
-    auto *kernel = gemm_tc_kernel<CG, GATED>;
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int CG, bool GATED, int N>
+cudaError_t start(const Work<N> &work, int64_t grid, cudaStream_t stream) {
+    auto *kernel = gemm_tc_kernel<CG, GATED, N>;
+    const int cluster = CG * (N == 1 ? work.p[0].split : 1);
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kSmemBytes);
-    if (err == cudaSuccess && CG * p.split > 8)
+    if (err == cudaSuccess && cluster > 8)
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -768,13 +821,11 @@ cudaError_t start(const Gemm &g, const TcPlan &p, const CUtensorMap &a, const CU
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {static_cast<unsigned>(CG * p.split), 1, 1};
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = CG * p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, g, p, a, b, w);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, work);
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Clusters of `size` CTAs with this kernel's shared memory that can run at
 // once: SMs come in groups that a cluster does not span, so 152 SMs hold 36
@@ -785,7 +836,7 @@ int active_clusters(int size, int num_sms) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
     int n = cache[dev][size].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    auto *kernel = gemm_tc_kernel<1, false>;
+    auto *kernel = gemm_tc_kernel<1, false, 1>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(size));
     cfg.blockDim = dim3(kTcThreads);
@@ -825,34 +876,45 @@ struct Cut {
     int cg, bn, split;
 };
 
-Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms) {
+// Clocks of one k block of a tile.
+double block_clocks(const Gemm &g, int cg, int bn) {
+    const int columns = bn / cg;
+    const double copies =
+        (kATile + (g.b_mn ? (columns + 63) / 64 * 64 : columns) * 128.0) / (cg == 1 ? 80.0 : 72.0);
+    const double mma = 2.35 * bn > 290.0 ? 2.35 * bn : 290.0;
+    return copies > mma ? copies : mma;
+}
+
+double epilogue_clocks(int bn) { return 1200.0 + 20.0 * bn; }
+
+// Tiles of at most `most` columns, evened out.
+int even_columns(const Gemm &g, int cg, int most) {
+    const int unit = 16 * cg;
+    return static_cast<int>(ceil_div(ceil_div(g.N, ceil_div(g.N, most)), unit)) * unit;
+}
+
+Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms, double *price) {
     const int64_t blocks = ceil_div(g.K, kBlockK);
     const double hbm = 2.0 * (static_cast<double>(a_rows) * g.K +
                               static_cast<double>(g.N) * g.K +
                               static_cast<double>(g.N) * g.M) / 3580.0;
     Cut best = {2, kMaxBn, 1};
-    double least = 1e300;
+    *price = 1e300;
     for (int cg = 1; cg <= 2; ++cg) {
         const int64_t m_tiles = ceil_div(a_rows, 128 * cg);
-        // transposed B is copied 64 columns at a time
-        const int unit = g.b_mn ? 64 * cg : 16 * cg;
         int64_t last = 0;
-        for (int most = g.b_mn ? unit : 32; most <= kMaxBn; most += g.b_mn ? unit : 32) {
+        for (int most = 32; most <= kMaxBn; most += 32) {
             const int64_t n_tiles = ceil_div(g.N, most);
             if (n_tiles == last) continue;
             last = n_tiles;
-            // evened out over the tiles
-            const int bn = g.b_mn ? most
-                                  : static_cast<int>(ceil_div(ceil_div(g.N, n_tiles), unit)) * unit;
+            const int bn = even_columns(g, cg, most);
             const int64_t tiles = m_tiles * n_tiles;
-            const double copies = (kATile + bn / cg * 128.0) / (cg == 1 ? 80.0 : 72.0);
-            double block = 2.35 * bn > 290.0 ? 2.35 * bn : 290.0;
-            if (copies > block) block = copies;
+            const double block = block_clocks(g, cg, bn);
             for (int split = 1; split * cg <= 16 && split <= blocks; split *= 2) {
                 const int slots = split * cg <= 2 ? num_sms / (split * cg)
                                                   : active_clusters(split * cg, num_sms);
                 if (split > 1 && tiles > slots) break;
-                const double tail = split == 1 ? 1200.0 + 20.0 * bn
+                const double tail = split == 1 ? epilogue_clocks(bn)
                                     : cg == 1  ? 3300.0 + 430.0 * split + 18.0 * bn
                                                : 7000.0 + 430.0 * split + 12.0 * bn;
                 double tile = static_cast<double>(ceil_div(blocks, split)) * block;
@@ -860,8 +922,8 @@ Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms) {
                 double cost = static_cast<double>(ceil_div(tiles, slots)) * tile;
                 if (cost < hbm) cost = hbm;
                 cost += tail;
-                if (cost < least) {
-                    least = cost;
+                if (cost < *price) {
+                    *price = cost;
                     best = {cg, bn, split};
                 }
             }
@@ -870,43 +932,68 @@ Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms) {
     return best;
 }
 
-}  // namespace
+// The same for two products in one launch, on pairs without k in parts: the
+// tiles go round the pairs one by one, the first product's before the second's.
+double choose_two(const Gemm *g, int num_sms, int *bn) {
+    const int pairs = num_sms / 2;
+    double least = 1e300;
+    for (int a = 64; a <= kMaxBn; a += 32) {
+        const int bn0 = even_columns(g[0], 2, a);
+        const double time0 = ceil_div(g[0].K, kBlockK) * block_clocks(g[0], 2, bn0);
+        const double tail0 = epilogue_clocks(bn0), unit0 = time0 > tail0 ? time0 : tail0;
+        const int64_t n0 = ceil_div(g[0].M, 256) * ceil_div(g[0].N, bn0);
+        for (int b = 64; b <= kMaxBn; b += 32) {
+            const int bn1 = even_columns(g[1], 2, b);
+            const double time1 = ceil_div(g[1].K, kBlockK) * block_clocks(g[1], 2, bn1);
+            const double tail1 = epilogue_clocks(bn1), unit1 = time1 > tail1 ? time1 : tail1;
+            const int64_t n1 = ceil_div(g[1].M, 256) * ceil_div(g[1].N, bn1);
+            // the pairs at the ends of the last rounds have the most to do
+            const int64_t ends[4] = {0, n0 % pairs, (n0 + n1 + pairs - 1) % pairs, pairs - 1};
+            double most = 0.0;
+            for (int64_t j : ends) {
+                const int64_t c0 = j < n0 ? (n0 - 1 - j) / pairs + 1 : 0;
+                const int64_t c = j < n0 + n1 ? (n0 + n1 - 1 - j) / pairs + 1 : 0;
+                const double load = c0 * unit0 + (c - c0) * unit1;
+                if (load > most) most = load;
+            }
+            most += tail0 > tail1 ? tail0 : tail1;
+            if (most < least) {
+                least = most;
+                bn[0] = bn0;
+                bn[1] = bn1;
+            }
+        }
+    }
+    return least;
+}
 
-bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err) {
-    if (!aligned16(g.a) || !aligned16(g.b) || (g.a_mn ? g.M : g.K) % 8 || g.b_pitch % 8 ||
-        !encoder())
-        return false;
+bool can_copy(const Gemm &g) {
+    return aligned16(g.a) && aligned16(g.b) && (g.a_mn ? g.M : g.K) % 8 == 0 &&
+           g.b_pitch % 8 == 0 && encoder();
+}
+
+// Plan and tensor maps of one product; false when the driver refuses a map.
+bool describe(const Gemm &g, const Cut &cut, TcPlan *plan, CUtensorMap *map) {
+    TcPlan &p = *plan;
+    p = {};
     const int rows_per_feature = g.gated ? 2 : 1;
     const int64_t a_rows = static_cast<int64_t>(g.M) * rows_per_feature;
-    TcPlan p = {};
     p.gather = g.row_token != nullptr;
-    p.split = 1;
-
-    // Expert groups, whose sizes only the device knows, run on pairs; their
-    // column counts follow from the row counts there.
-    Cut cut = {2, 0, 1};
-    if (!g.E) cut = choose_cut(g, a_rows, num_sms);
     p.split = cut.split;
     p.bn = cut.bn;
     p.m_tiles = static_cast<int>(ceil_div(a_rows, 128 * cut.cg));
-    int64_t units = INT32_MAX;
     if (g.E) {
         p.box_rows = 16;
     } else {
         p.n_tiles = static_cast<int>(ceil_div(g.N, p.bn));
         p.box_rows = p.bn / cut.cg;
-        units = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.split;
     }
-    const int64_t slots = num_sms / cut.cg;
-    const int64_t grid = cut.cg * (p.split > 1 || units < slots ? units : slots);
-
-    CUtensorMap ma, mb, mw;
     bool ok;
     if (g.a_mn) {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.M), static_cast<cuuint64_t>(g.K)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.M) * 2};
         const cuuint32_t box[2] = {64, 64};
-        ok = encode(&ma, g.a, 2, dims, strides, box);
+        ok = encode(&map[0], g.a, 2, dims, strides, box);
     } else {
         // [E][M][gate, up][K]: a copy of (k, both, features) interleaves the rows
         const cuuint64_t row = static_cast<cuuint64_t>(g.K) * 2;
@@ -917,29 +1004,73 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
         const cuuint64_t strides[3] = {row * g.M, row, row * a_rows};
         const cuuint32_t box[4] = {kBlockK, static_cast<cuuint32_t>(rows_per_feature),
                                    static_cast<cuuint32_t>(128 / rows_per_feature), 1};
-        ok = encode(&ma, g.a, 4, dims, strides, box);
+        ok = encode(&map[0], g.a, 4, dims, strides, box);
     }
-    {
-        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.b_mn ? g.N : g.K),
-                                    static_cast<cuuint64_t>(g.b_mn ? g.K : g.b_rows)};
-        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.b_pitch) * 2};
-        const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(g.b_mn ? 64
-                                                               : p.gather ? 1 : p.box_rows)};
-        ok = ok && encode(&mb, g.b, 2, dims, strides, box);
-        mw = mb;
-        if (g.E && !p.gather) {     // ragged groups: wide copies first, narrow ones for the rest
-            p.wide_rows = 64;
-            const cuuint32_t wide[2] = {64, 64};
-            ok = ok && encode(&mw, g.b, 2, dims, strides, wide);
-        }
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.b_mn ? g.N : g.K),
+                                static_cast<cuuint64_t>(g.b_mn ? g.K : g.b_rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.b_pitch) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(g.b_mn      ? 64
+                                                           : p.gather ? 1
+                                                                      : p.box_rows)};
+    ok = ok && encode(&map[1], g.b, 2, dims, strides, box);
+    map[2] = map[1];
+    if (g.E && !p.gather) {     // ragged groups: wide copies first, narrow ones for the rest
+        p.wide_rows = 64;
+        const cuuint32_t wide[2] = {64, 64};
+        ok = ok && encode(&map[2], g.b, 2, dims, strides, wide);
     }
-    if (!ok) return false;
+    return ok;
+}
+
+}  // namespace
+
+bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err) {
+    if (!can_copy(g)) return false;
+    // Expert groups, whose sizes only the device knows, run on pairs; their
+    // column counts follow from the row counts there.
+    Cut cut = {2, 0, 1};
+    double price;
+    if (!g.E) cut = choose_cut(g, static_cast<int64_t>(g.M) * (g.gated ? 2 : 1), num_sms, &price);
+    Work<1> work;
+    work.g[0] = g;
+    work.tiles0 = 0;
+    if (!describe(g, cut, &work.p[0], work.map[0])) return false;
+    const TcPlan &p = work.p[0];
+    const int64_t units = g.E ? INT32_MAX
+                              : static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.split;
+    const int64_t slots = num_sms / cut.cg;
+    const int64_t grid = cut.cg * (p.split > 1 || units < slots ? units : slots);
     if (cut.cg == 2)
-        *err = g.gated ? start<2, true>(g, p, ma, mb, mw, grid, stream)
-                       : start<2, false>(g, p, ma, mb, mw, grid, stream);
+        *err = g.gated ? start<2, true>(work, grid, stream) : start<2, false>(work, grid, stream);
     else
-        *err = g.gated ? start<1, true>(g, p, ma, mb, mw, grid, stream)
-                       : start<1, false>(g, p, ma, mb, mw, grid, stream);
+        *err = g.gated ? start<1, true>(work, grid, stream) : start<1, false>(work, grid, stream);
+    return true;
+}
+
+bool launch_two_gemms_tc(const Gemm *g, int num_sms, cudaStream_t stream, cudaError_t *err) {
+    if (!can_copy(g[0]) || !can_copy(g[1])) return false;
+    // longer tiles first; two launches cost the second one's start, about 5000
+    // clocks, but each may be cut as suits it
+    const Gemm *order[2] = {&g[0], &g[1]};
+    if (g[1].K > g[0].K) {
+        order[0] = &g[1];
+        order[1] = &g[0];
+    }
+    Work<2> work;
+    work.g[0] = *order[0];
+    work.g[1] = *order[1];
+    int bn[2];
+    double apart[2];
+    const double together = choose_two(work.g, num_sms, bn);
+    for (int i = 0; i < 2; ++i) (void)choose_cut(work.g[i], work.g[i].M, num_sms, &apart[i]);
+    if (together > apart[0] + apart[1] + 5000.0) return false;
+    for (int i = 0; i < 2; ++i)
+        if (!describe(work.g[i], {2, bn[i], 1}, &work.p[i], work.map[i])) return false;
+    work.tiles0 = work.p[0].m_tiles * work.p[0].n_tiles;
+    const int64_t units = static_cast<int64_t>(work.tiles0) +
+                          static_cast<int64_t>(work.p[1].m_tiles) * work.p[1].n_tiles;
+    const int64_t slots = num_sms / 2;
+    *err = start<2, false>(work, 2 * (units < slots ? units : slots), stream);
     return true;
 }
 

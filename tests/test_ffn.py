@@ -485,6 +485,19 @@ def test_backward_of_odd_feature_counts(cuda_lib, name, T, N, K):
         R.check(got, R.backward(d, x, w, pre, name, True), "gated " + name)
 
 
+@pytest.mark.parametrize("T,N,K", [(2040, 1000, 1544), (3000, 2048, 2048), (64, 4096, 1024),
+                                   (4096, 64, 1024), (1500, 3000, 264), (5000, 520, 72)])
+def test_large_backward(cuda_lib, T, N, K):
+    """Many tiles: both gradients in one launch, or each in its own."""
+    x, w, d = rand(250, T, K), rand(251, N, K, scale=K ** -0.5), rand(252, T, N, scale=0.1)
+    both = cuda_lib.linear_backward(d, x, w, want_dbias=True)
+    ref = R.backward(d, x, w, None, "none", False)
+    R.check(both, ref)
+    alone = {**cuda_lib.linear_backward(d, x, w, want_dweight=False),
+             **cuda_lib.linear_backward(d, x, w, want_dx=False)}
+    R.check(alone, ref, "alone")
+
+
 def test_backward_of_a_misaligned_dout(cuda_lib):
     x, w, d = rand(47, 50, 64), rand(48, 72, 64), rand(49, 50, 72)
     got = cuda_lib.linear_backward(misaligned(d), x, w, want_dbias=True)
