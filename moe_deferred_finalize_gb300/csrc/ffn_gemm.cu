@@ -59,12 +59,13 @@ constexpr long long kWaitLimit = 4000000000;     // clocks (two seconds) until a
 
 // How one launch is cut up (see choose_cut).
 struct TcPlan {
-    int split;          // CTAs along k
+    int log_split;      // 2^log_split parts of k
+    int received;       // bytes of the other parts' sums
     int bn;             // columns per tile; 0: from the expert counts, on the device
     int m_tiles, n_tiles;
     int gather;         // B rows are fetched by row_token
     int box_rows;       // rows of one B copy (k-contiguous B)
-    int wide_rows;      // of one copy through map_w, while that many are left (0: no map_w)
+    int wide_rows;      // of one copy through the third map, while that many are left (0: none)
 };
 
 // One launch: a product, or two that share the SMs (the gradients of a layer):
@@ -150,10 +151,11 @@ __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const He
     } else {
         // bands of kBand feature tiles, columns outside: the tiles in flight form
         // a block, so both operands are shared through L2
-        const int band = t / (kBand * p.n_tiles), in_band = t - band * kBand * p.n_tiles;
-        const int wide = min(kBand, p.m_tiles - band * kBand);
-        m = band * kBand + in_band % wide;
-        n = in_band / wide;
+        const unsigned per_band = kBand * p.n_tiles, band = static_cast<unsigned>(t) / per_band;
+        const unsigned in_band = t - band * per_band;
+        const unsigned wide = min(kBand, p.m_tiles - static_cast<int>(band) * kBand);
+        n = wide == kBand ? in_band / kBand : in_band / wide;
+        m = band * kBand + in_band - n * wide;
         r.bn = p.bn;
         r.row0 = static_cast<int64_t>(n) * r.bn;
         r.count = static_cast<int>(min(static_cast<int64_t>(r.bn), g.N - r.row0));
@@ -423,7 +425,7 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
 // k in parts: the columns of a tile are shared out over the parts, kChunk at a
 // time, and each part sends its sums of the others' columns into their shared
 // memory, [sender][column][128 rows of A].
-__device__ __forceinline__ int own_columns(int bn, int split) {
+__host__ __device__ __forceinline__ int own_columns(int bn, int split) {
     return ((bn + split - 1) / split + kChunk - 1) / kChunk * kChunk;
 }
 
@@ -447,6 +449,42 @@ __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint3
 
 // --------------------------------------------------------------- kernel
 
+// Expert groups (one warp): the width of the column tiles, from the largest
+// group, and the number of tiles before each expert.
+template <int CG>
+__device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Header *h, int lane) {
+    int most = 0;
+    for (int e = lane; e < g.E; e += 32) {
+        const int first = g.offsets[e];
+        most = max(most, first < 0 ? 0 : min(g.counts[e], g.N - first));
+    }
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    const int bn = min(kMaxBn, max(1, (most + 16 * CG - 1) / (16 * CG)) * 16 * CG);
+    int before = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 32) {
+        const int e = e0 + lane;
+        int v = 0;
+        if (e < g.E) {
+            const int first = g.offsets[e];
+            v = first < 0 ? 0 : max(0, min(g.counts[e], g.N - first));
+            v = (v + bn - 1) / bn;
+        }
+        int sum = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += w;
+        }
+        if (e < g.E) h->prefix[e] = before + sum - v;
+        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (lane == 0) {
+        h->prefix[g.E] = before;
+        h->bn = bn;
+        h->tiles = before * p.m_tiles;
+    }
+}
+
 template <int CG, bool GATED, int N>
 __global__ void __launch_bounds__(kTcThreads, 1)
 gemm_tc_kernel(const __grid_constant__ Work<N> work) {
@@ -454,15 +492,16 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
     Header *h = reinterpret_cast<Header *>(smem + (base - smem_addr(smem)));
-    const uint32_t stage0 = base + kHeader;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     // the CTA's place in its cluster: which part of k, and which half of a pair
-    const int split = N == 1 ? work.p[0].split : 1;
+    const int log_split = N == 1 ? work.p[0].log_split : 0, split = 1 << log_split;
     const int rank = CG == 2 || split > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int part = rank / CG, half = rank % CG, lead = part * CG;
     const bool leader = half == 0;
     const uint16_t pair = static_cast<uint16_t>(3 << lead);
     volatile int *gave_up = &h->gave_up;
+    // expert groups: the tiles follow from what the previous kernels wrote
+    const bool grouped = N == 1 && work.g[0].E;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < N; ++i) {
@@ -481,67 +520,44 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<CG>(smem_addr(&h->tmem), 2 * kMaxBn);
-    // Launched as a dependent of the previous kernel on the stream: up to here
-    // nothing in global memory was touched.
-    wait_previous_kernel();
-    allow_next_kernel();
-    if (warp == 0) {
-        const Gemm &g = work.g[0];
-        const TcPlan &p = work.p[0];
-        if (N == 1 && g.E) {        // column tiles of each expert
-            int most = 0;
-            for (int e = lane; e < g.E; e += 32) {
-                const int first = g.offsets[e];
-                most = max(most, first < 0 ? 0 : min(g.counts[e], g.N - first));
-            }
-            most = __reduce_max_sync(0xFFFFFFFFu, most);
-            const int bn = min(kMaxBn, max(1, (most + 16 * CG - 1) / (16 * CG)) * 16 * CG);
-            int before = 0;
-            for (int e0 = 0; e0 < g.E; e0 += 32) {
-                const int e = e0 + lane;
-                int v = 0;
-                if (e < g.E) {
-                    const int first = g.offsets[e];
-                    v = first < 0 ? 0 : max(0, min(g.counts[e], g.N - first));
-                    v = (v + bn - 1) / bn;
-                }
-                int sum = v;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int w = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                    if (lane >= o) sum += w;
-                }
-                if (e < g.E) h->prefix[e] = before + sum - v;
-                before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-            }
-            if (lane == 0) {
-                h->prefix[g.E] = before;
-                h->bn = bn;
-                h->tiles = before * p.m_tiles;
-            }
-        } else if (lane == 0) {
-            h->bn = p.bn;
-            h->tiles = p.n_tiles * p.m_tiles;
-            if constexpr (N == 2) {
-                h->bn = max(p.bn, work.p[1].bn);
-                h->tiles += work.p[1].n_tiles * work.p[1].m_tiles;
-            }
-        }
+    if (grouped) {
+        wait_previous_kernel();
+        allow_next_kernel();
+        if (warp == 0) count_tiles<CG>(work.g[0], work.p[0], h, lane);
     }
     fence_before();
-    if (CG == 2) cluster_sync(); else __syncthreads();
+    if (CG == 2) {
+        cluster_sync();
+    } else {
+        if (split > 1) cluster_arrive();        // awaited before the first remote store
+        __syncthreads();
+    }
     fence_after();
 
-    const int tiles = h->tiles;
     const uint32_t tmem = h->tmem;
-    const int bnc_max = h->bn / CG;                 // B rows per CTA
+    int tiles, bn_max;
+    if (grouped) {
+        tiles = h->tiles;
+        bn_max = h->bn;
+    } else {
+        tiles = work.p[0].n_tiles * work.p[0].m_tiles;
+        bn_max = work.p[0].bn;
+        if constexpr (N == 2) {
+            tiles += work.p[1].n_tiles * work.p[1].m_tiles;
+            bn_max = max(bn_max, work.p[1].bn);
+        }
+    }
+    const uint32_t received = base + kHeader;       // the other parts' sums
+    const uint32_t stage0 = received + (N == 1 ? work.p[0].received : 0);
+    const int bnc_max = bn_max / CG;                // B rows per CTA
     // transposed B comes in blocks of 64 columns; a multiple of 2048 bytes
     const bool any_mn = work.g[0].b_mn || work.g[N - 1].b_mn;
     const uint32_t b_bytes = (any_mn ? (bnc_max + 63) / 64 * 64 : bnc_max) * kBlockK * 2;
     const uint32_t stage_bytes = kATile + b_bytes;
-    const int stages = min(kMaxStages, static_cast<int>(kStageArea / stage_bytes));
-    const int group = CG * split;
-    const int first_tile = blockIdx.x / group, step = gridDim.x / group;
+    const int stages = min(static_cast<unsigned>(kMaxStages),
+                           (kStageArea - (stage0 - received)) / stage_bytes);
+    const int first_tile = (blockIdx.x / CG) >> log_split;
+    const int step = (gridDim.x / CG) >> log_split;
     const int m_cta_rows = GATED ? 64 : 128;        // features per CTA
     // the product that a tile belongs to, and this part's k blocks of it
     auto product_of = [&](int ti) { return N == 2 && ti >= work.tiles0 ? 1 : 0; };
@@ -550,8 +566,14 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     };
     auto k_range = [&](int q, int *kb0, int *kb1) {
         const int blocks = (work.g[q].K + kBlockK - 1) / kBlockK;
-        *kb0 = static_cast<int>(static_cast<int64_t>(blocks) * part / split);
-        *kb1 = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / split);
+        *kb0 = (blocks * part) >> log_split;        // blocks < 2^25, part < 16
+        *kb1 = (blocks * (part + 1)) >> log_split;
+    };
+    // Launched as a dependent of the previous kernel on the stream: everything
+    // up to a role's first tile comes from the parameters, and global memory is
+    // touched behind this.
+    auto begin = [&](int ti) {
+        if (ti == first_tile && !grouped) wait_previous_kernel();
     };
 
     if (warp == 0) {
@@ -574,6 +596,8 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                                                : (bnc + p.box_rows - 1) / p.box_rows *
                                                      p.box_rows * 128u;
                 const uint32_t tx = CG * (kATile + b_tx);
+                begin(ti);
+                if (ti == first_tile) allow_next_kernel();
                 auto blocks_of = [&](auto copy) {
                     for (int kb = kb0; kb < kb1; ++kb) {
                         if (!wait(smem_addr(&h->empty[s]), phase, gave_up)) return false;
@@ -654,6 +678,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 const int row0 = static_cast<int>(t.row0 + half * bnc);
                 const int rows = g.b_mn ? 64 : p.box_rows;      // of one copy
                 const int boxes = (bnc + rows - 1) / rows;
+                begin(ti);
                 auto blocks_of = [&](auto copy) {
                     for (int kb = kb0; kb < kb1; ++kb) {
                         if (!wait(smem_addr(&h->empty[s]), phase, gave_up)) return false;
@@ -734,6 +759,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
             const Tile t = tile_of(ti, q);
             const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                  (n & 1) * kMaxBn;
+            begin(ti);
             const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             fence_after();
@@ -749,16 +775,17 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         const bool works = warp >= 2 && warp < kCopyWarp;
         const int quarter = warp & 3, side = (warp - 2) >> 2;
         const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        cluster_sync();         // every part's products are done, their stages free
+        if (CG == 1) cluster_wait();        // every part has started
         const Tile t = tile_of(first_tile, 0);
         if (works && !*gave_up)
-            send_columns<CG>(t, acc, stage0, split, part, half, quarter, side, lane);
+            send_columns<CG>(t, acc, received, split, part, half, quarter, side, lane);
         cluster_sync();         // every part's sums have arrived
         if (works && !*gave_up) {
             const int own = own_columns(t.bn, split);
             finish_tile<GATED>(work.g[0], t, t.m0 + half * m_cta_rows, acc, quarter, side, lane, 0,
                                part * own, (part + 1) * own,
-                               reinterpret_cast<const float *>(smem + (stage0 - smem_addr(smem))),
+                               reinterpret_cast<const float *>(smem + (received -
+                                                                       smem_addr(smem))),
                                split - 1);
         }
     }
@@ -806,7 +833,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 template <int CG, bool GATED, int N>
 cudaError_t start(const Work<N> &work, int64_t grid, cudaStream_t stream) {
     auto *kernel = gemm_tc_kernel<CG, GATED, N>;
-    const int cluster = CG * (N == 1 ? work.p[0].split : 1);
+    const int cluster = CG << (N == 1 ? work.p[0].log_split : 0);
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kSmemBytes);
     if (err == cudaSuccess && cluster > 8)
@@ -876,6 +903,11 @@ struct Cut {
     int cg, bn, split;
 };
 
+// Shared memory for the other parts' sums.
+constexpr int kMaxReceived = 64 * 1024;
+
+int received_bytes(int bn, int split) { return (split - 1) * own_columns(bn, split) * 512; }
+
 // Clocks of one k block of a tile.
 double block_clocks(const Gemm &g, int cg, int bn) {
     const int columns = bn / cg;
@@ -913,7 +945,8 @@ Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms, double *price) {
             for (int split = 1; split * cg <= 16 && split <= blocks; split *= 2) {
                 const int slots = split * cg <= 2 ? num_sms / (split * cg)
                                                   : active_clusters(split * cg, num_sms);
-                if (split > 1 && tiles > slots) break;
+                if (split > 1 && (tiles > slots || received_bytes(bn, split) > kMaxReceived))
+                    break;
                 const double tail = split == 1 ? epilogue_clocks(bn)
                                     : cg == 1  ? 3300.0 + 430.0 * split + 18.0 * bn
                                                : 7000.0 + 430.0 * split + 12.0 * bn;
@@ -979,7 +1012,8 @@ bool describe(const Gemm &g, const Cut &cut, TcPlan *plan, CUtensorMap *map) {
     const int rows_per_feature = g.gated ? 2 : 1;
     const int64_t a_rows = static_cast<int64_t>(g.M) * rows_per_feature;
     p.gather = g.row_token != nullptr;
-    p.split = cut.split;
+    while (1 << p.log_split < cut.split) ++p.log_split;
+    p.received = received_bytes(cut.bn, cut.split);
     p.bn = cut.bn;
     p.m_tiles = static_cast<int>(ceil_div(a_rows, 128 * cut.cg));
     if (g.E) {
@@ -1037,9 +1071,9 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
     if (!describe(g, cut, &work.p[0], work.map[0])) return false;
     const TcPlan &p = work.p[0];
     const int64_t units = g.E ? INT32_MAX
-                              : static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.split;
+                              : static_cast<int64_t>(p.m_tiles) * p.n_tiles << p.log_split;
     const int64_t slots = num_sms / cut.cg;
-    const int64_t grid = cut.cg * (p.split > 1 || units < slots ? units : slots);
+    const int64_t grid = cut.cg * (p.log_split > 0 || units < slots ? units : slots);
     if (cut.cg == 2)
         *err = g.gated ? start<2, true>(work, grid, stream) : start<2, false>(work, grid, stream);
     else
