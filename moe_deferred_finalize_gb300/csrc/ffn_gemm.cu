@@ -854,15 +854,14 @@ cudaError_t start(const Work<N> &work, int64_t grid, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kernel, work);
 }
 
-// Clusters of `size` CTAs with this kernel's shared memory that can run at
-// once: SMs come in groups that a cluster does not span, so 152 SMs hold 36
-// clusters of 4, 15 of 8 and 7 of 16.  Asked once per device and size.
-int active_clusters(int size, int num_sms) {
-    static std::atomic<int> cache[kMaxDevices][17];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
-    int n = cache[dev][size].load(std::memory_order_relaxed);
-    if (n > 0) return n;
+// Clusters of 1, 2, 4, 8 and 16 CTAs with this kernel's shared memory that can
+// run at once: SMs come in groups that a cluster does not span, so 152 SMs
+// hold 36 clusters of 4, 15 of 8 and 7 of 16.  Asked once per device.
+struct Slots {
+    int n[5];
+};
+
+int ask_active_clusters(int size, int num_sms) {
     auto *kernel = gemm_tc_kernel<1, false, 1>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(size));
@@ -873,6 +872,7 @@ int active_clusters(int size, int num_sms) {
     attr[0].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    int n = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
             cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
@@ -881,24 +881,39 @@ int active_clusters(int size, int num_sms) {
         (void)cudaGetLastError();
         n = num_sms / size > 1 ? num_sms / size / 2 : 1;
     }
-    cache[dev][size].store(n, std::memory_order_relaxed);
     return n;
+}
+
+Slots cluster_slots(int num_sms) {
+    static std::atomic<int> cache[kMaxDevices][5];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
+    Slots s = {{num_sms, num_sms / 2, 0, 0, 0}};
+    for (int i = 2; i < 5; ++i) {
+        s.n[i] = cache[dev][i].load(std::memory_order_relaxed);
+        if (s.n[i] > 0) continue;
+        s.n[i] = ask_active_clusters(1 << i, num_sms);
+        cache[dev][i].store(s.n[i], std::memory_order_relaxed);
+    }
+    return s;
 }
 
 // How a product that is not grouped is cut: one CTA or a pair per tile, columns
 // per tile, parts of k.  Every choice is priced in SM clocks and the cheapest
 // taken.  The figures are fits to sweeps over 17..4096 rows:
-//   - a 64-deep k block takes the MMAs (2.35 clocks a column), the copies (80
-//     bytes a clock into a single SM, 72 into each of a pair) or the issue of
-//     both (290 clocks), whichever is longest;
-//   - the epilogue of a tile takes 1200 clocks and 20 a column, under the next
-//     tile's products except for the last one; joining k's parts 3300 clocks
-//     (two cluster barriers), 430 a part and 18 a column, for pairs 7000, 430
-//     and 12;
-//   - HBM delivers 3580 bytes a clock.
+//   - a 64-deep k block takes the MMAs (2.7 clocks a column, 2.35 on a pair,
+//     which reads half of B), the copies (80
+//     bytes a clock into a single SM, 72 into each of a pair), the issue of
+//     both (290 clocks) or the latency of a copy (2000) shared by the stages
+//     in flight, whichever is longest;
+//   - a tile costs 300 clocks more, and its epilogue 1200 and 20 a column, under
+//     the next tile's products except for the last one; joining k's parts 2500
+//     (pairs 4500), 300 a part and 30 a column; pairs 1800 for their barriers;
+//   - HBM delivers 3580 bytes a clock; the shorter of its time and the SMs'
+//     counts 15 %.
 // Examples: 512 x 4096 x 7168 (gated) runs as 64 pairs of 128 columns, 24 us,
-// against 30 us with 256 columns and k in two parts; 300 x 256 x 7168 as 80
-// tiles of 64 columns and an eighth of k, 9.8 us, against 23 us unsplit.
+// against 29 us with 256 columns and k in two parts; 300 x 256 x 7168 as 80
+// tiles of 64 columns and an eighth of k, 8.2 us, against 20 us unsplit.
 struct Cut {
     int cg, bn, split;
 };
@@ -909,12 +924,15 @@ constexpr int kMaxReceived = 64 * 1024;
 int received_bytes(int bn, int split) { return (split - 1) * own_columns(bn, split) * 512; }
 
 // Clocks of one k block of a tile.
-double block_clocks(const Gemm &g, int cg, int bn) {
+double block_clocks(const Gemm &g, int cg, int bn, int received) {
     const int columns = bn / cg;
-    const double copies =
-        (kATile + (g.b_mn ? (columns + 63) / 64 * 64 : columns) * 128.0) / (cg == 1 ? 80.0 : 72.0);
-    const double mma = 2.35 * bn > 290.0 ? 2.35 * bn : 290.0;
-    return copies > mma ? copies : mma;
+    const int bytes = kATile + (g.b_mn ? (columns + 63) / 64 * 64 : columns) * 128;
+    const double copies = bytes / (cg == 1 ? 80.0 : 72.0);
+    const double latency = 2000.0 / ((kStageArea - received) / bytes);
+    const double mma = (cg == 1 ? 2.7 : 2.35) * bn;
+    double clocks = mma > 290.0 ? mma : 290.0;
+    if (copies > clocks) clocks = copies;
+    return latency > clocks ? latency : clocks;
 }
 
 double epilogue_clocks(int bn) { return 1200.0 + 20.0 * bn; }
@@ -925,7 +943,7 @@ int even_columns(const Gemm &g, int cg, int most) {
     return static_cast<int>(ceil_div(ceil_div(g.N, ceil_div(g.N, most)), unit)) * unit;
 }
 
-Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms, double *price) {
+Cut choose_cut(const Gemm &g, int64_t a_rows, const Slots &slots_of, double *price) {
     const int64_t blocks = ceil_div(g.K, kBlockK);
     const double hbm = 2.0 * (static_cast<double>(a_rows) * g.K +
                               static_cast<double>(g.N) * g.K +
@@ -941,20 +959,19 @@ Cut choose_cut(const Gemm &g, int64_t a_rows, int num_sms, double *price) {
             last = n_tiles;
             const int bn = even_columns(g, cg, most);
             const int64_t tiles = m_tiles * n_tiles;
-            const double block = block_clocks(g, cg, bn);
-            for (int split = 1; split * cg <= 16 && split <= blocks; split *= 2) {
-                const int slots = split * cg <= 2 ? num_sms / (split * cg)
-                                                  : active_clusters(split * cg, num_sms);
-                if (split > 1 && (tiles > slots || received_bytes(bn, split) > kMaxReceived))
-                    break;
+            for (int log = 0; cg << log <= 16 && 1 << log <= blocks; ++log) {
+                const int split = 1 << log, slots = slots_of.n[log + cg - 1];
+                const int received = received_bytes(bn, split);
+                if (split > 1 && (tiles > slots || received > kMaxReceived)) break;
                 const double tail = split == 1 ? epilogue_clocks(bn)
-                                    : cg == 1  ? 3300.0 + 430.0 * split + 18.0 * bn
-                                               : 7000.0 + 430.0 * split + 12.0 * bn;
-                double tile = static_cast<double>(ceil_div(blocks, split)) * block;
+                                    : cg == 1  ? 2500.0 + 300.0 * split + 30.0 * bn
+                                               : 4500.0 + 300.0 * split + 30.0 * bn;
+                double tile = static_cast<double>(ceil_div(blocks, split)) *
+                              block_clocks(g, cg, bn, received);
                 if (split == 1 && tail > tile) tile = tail;
-                double cost = static_cast<double>(ceil_div(tiles, slots)) * tile;
-                if (cost < hbm) cost = hbm;
-                cost += tail;
+                double cost = static_cast<double>(ceil_div(tiles, slots)) * (tile + 300.0);
+                cost = cost < hbm ? hbm + 0.15 * cost : cost + 0.15 * hbm;
+                cost += tail + (cg == 2 ? 1800.0 : 0.0);
                 if (cost < *price) {
                     *price = cost;
                     best = {cg, bn, split};
@@ -972,13 +989,15 @@ double choose_two(const Gemm *g, int num_sms, int *bn) {
     double least = 1e300;
     for (int a = 64; a <= kMaxBn; a += 32) {
         const int bn0 = even_columns(g[0], 2, a);
-        const double time0 = ceil_div(g[0].K, kBlockK) * block_clocks(g[0], 2, bn0);
-        const double tail0 = epilogue_clocks(bn0), unit0 = time0 > tail0 ? time0 : tail0;
+        const double time0 = ceil_div(g[0].K, kBlockK) * block_clocks(g[0], 2, bn0, 0);
+        const double tail0 = epilogue_clocks(bn0);
+        const double unit0 = 300.0 + (time0 > tail0 ? time0 : tail0);
         const int64_t n0 = ceil_div(g[0].M, 256) * ceil_div(g[0].N, bn0);
         for (int b = 64; b <= kMaxBn; b += 32) {
             const int bn1 = even_columns(g[1], 2, b);
-            const double time1 = ceil_div(g[1].K, kBlockK) * block_clocks(g[1], 2, bn1);
-            const double tail1 = epilogue_clocks(bn1), unit1 = time1 > tail1 ? time1 : tail1;
+            const double time1 = ceil_div(g[1].K, kBlockK) * block_clocks(g[1], 2, bn1, 0);
+            const double tail1 = epilogue_clocks(bn1);
+            const double unit1 = 300.0 + (time1 > tail1 ? time1 : tail1);
             const int64_t n1 = ceil_div(g[1].M, 256) * ceil_div(g[1].N, bn1);
             // the pairs at the ends of the last rounds have the most to do
             const int64_t ends[4] = {0, n0 % pairs, (n0 + n1 + pairs - 1) % pairs, pairs - 1};
@@ -989,7 +1008,7 @@ double choose_two(const Gemm *g, int num_sms, int *bn) {
                 const double load = c0 * unit0 + (c - c0) * unit1;
                 if (load > most) most = load;
             }
-            most += tail0 > tail1 ? tail0 : tail1;
+            most += 1800.0 + (tail0 > tail1 ? tail0 : tail1);
             if (most < least) {
                 least = most;
                 bn[0] = bn0;
@@ -1064,7 +1083,9 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
     // column counts follow from the row counts there.
     Cut cut = {2, 0, 1};
     double price;
-    if (!g.E) cut = choose_cut(g, static_cast<int64_t>(g.M) * (g.gated ? 2 : 1), num_sms, &price);
+    if (!g.E)
+        cut = choose_cut(g, static_cast<int64_t>(g.M) * (g.gated ? 2 : 1), cluster_slots(num_sms),
+                         &price);
     Work<1> work;
     work.g[0] = g;
     work.tiles0 = 0;
@@ -1096,7 +1117,8 @@ bool launch_two_gemms_tc(const Gemm *g, int num_sms, cudaStream_t stream, cudaEr
     int bn[2];
     double apart[2];
     const double together = choose_two(work.g, num_sms, bn);
-    for (int i = 0; i < 2; ++i) (void)choose_cut(work.g[i], work.g[i].M, num_sms, &apart[i]);
+    const Slots slots_of = cluster_slots(num_sms);
+    for (int i = 0; i < 2; ++i) (void)choose_cut(work.g[i], work.g[i].M, slots_of, &apart[i]);
     if (together > apart[0] + apart[1] + 5000.0) return false;
     for (int i = 0; i < 2; ++i)
         if (!describe(work.g[i], {2, bn[i], 1}, &work.p[i], work.map[i])) return false;
