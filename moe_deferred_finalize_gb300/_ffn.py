@@ -344,6 +344,16 @@ def gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
                      want_dx, want_dweight, want_dbias, dx, dweight, dbias, workspace, stream)
 
 
+def _permute_sizes(T, K, E, tile):
+    """(rows of the layout at most, bytes of workspace)."""
+    fast = _abi._fastcall()
+    if fast is not None:
+        return fast.permute_sizes(_address("moe_permute_rows"),
+                                  _address("moe_permute_workspace_bytes"), T, K, E, tile)
+    lib = _lib()
+    return lib.moe_permute_rows(T, K, E, tile), lib.moe_permute_workspace_bytes(T, K, E)
+
+
 def permute_rows(T: int, K: int, E: int, tile: int) -> int:
     """The most rows the grouped layout of T x K slots over E experts can need."""
     return int(_lib().moe_permute_rows(int(T), int(K), int(E), int(tile)))
@@ -365,13 +375,13 @@ def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
     dev = expert_ids.device
     E, tile = int(E), int(tile)
     _check(expert_ids, "expert_ids", _I32, (T, K), dev)
-    lib = _lib()
-    P = int(lib.moe_permute_rows(T, K, E, tile)) if row_token is None else row_token.numel()
+    P, nbytes = _permute_sizes(T, K, E, tile)
+    if row_token is not None:
+        P = row_token.numel()
     res = {"idx_map": _output(idx_map, "idx_map", torch.int32, (T, K), dev),
            "row_token": _output(row_token, "row_token", torch.int32, (P,), dev),
            "offsets": _output(offsets, "offsets", torch.int32, (max(E, 0) + 1,), dev),
            "counts": _output(counts, "counts", torch.int32, (max(E, 0),), dev)}
-    nbytes = int(lib.moe_permute_workspace_bytes(T, K, E))
     if workspace is not None:
         nbytes = _workspace_bytes(workspace, dev)
     elif nbytes:

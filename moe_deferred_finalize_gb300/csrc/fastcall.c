@@ -410,6 +410,21 @@ static PyObject *call_permute(PyObject *self, PyObject *const *a, Py_ssize_t nar
                                                 (size_t)v[12], PTR(13)));
 }
 
+/* permute_sizes(moe_permute_rows, moe_permute_workspace_bytes, T, K, E, tile)
+ * -> (rows, workspace bytes); the first two are the functions' addresses */
+static PyObject *permute_sizes(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    long long v[MOST_ARGS];
+    if (parse_ints(a, nargs, 6, "permute_sizes", v) != 0) return NULL;
+    if (!v[1]) {
+        PyErr_SetString(PyExc_ValueError, "null function pointer");
+        return NULL;
+    }
+    const int64_t rows = ((int64_t(*)(int, int, int, int))PTR(0))(INT(2), INT(3), INT(4), INT(5));
+    const size_t bytes = ((size_t(*)(int, int, int))PTR(1))(INT(2), INT(3), INT(4));
+    return Py_BuildValue("Ln", (long long)rows, (Py_ssize_t)bytes);
+}
+
 #undef PTR
 #undef INT
 
@@ -446,6 +461,8 @@ static PyMethodDef methods[] = {
      "Call moe_expert_gated_ffn or moe_expert_linear."},
     {"call_permute", (PyCFunction)(void (*)(void))call_permute, METH_FASTCALL,
      "Call moe_permute."},
+    {"permute_sizes", (PyCFunction)(void (*)(void))permute_sizes, METH_FASTCALL,
+     "Call moe_permute_rows and moe_permute_workspace_bytes."},
     {NULL, NULL, 0, NULL},
 };
 
