@@ -51,7 +51,7 @@ constexpr int kBlockK = 64;                     // k values per stage: one 128-b
 constexpr int kATile = 128 * kBlockK * 2;       // bytes of A per CTA and stage
 constexpr int kMaxBn = 256;
 constexpr int kMaxStages = 16;
-constexpr int kHeader = 6144;                   // barriers, tables
+constexpr int kHeader = 13 * 1024;              // barriers, tables
 constexpr int kSmemBytes = 227 * 1024;
 constexpr int kStageArea = kSmemBytes - kHeader - 1024;     // after rounding up to 1024
 constexpr int kBand = 8;                        // feature tiles per band (see tile_at)
@@ -84,7 +84,8 @@ struct Header {
     int gave_up;
     int bn;
     int tiles;
-    int prefix[MOEF_MAX_EXPERTS + 1];   // column tiles before each expert
+    // expert groups: column tiles before each, first row, rows
+    int prefix[MOEF_MAX_EXPERTS + 1], first[MOEF_MAX_EXPERTS], count[MOEF_MAX_EXPERTS];
 };
 static_assert(sizeof(Header) <= kHeader, "header region");
 
@@ -142,11 +143,9 @@ __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const He
         const int local = t - h->prefix[lo] * p.m_tiles;
         m = local / nt;
         n = local % nt;
-        const int64_t first = g.offsets[lo];
-        const int count = static_cast<int>(min(static_cast<int64_t>(g.counts[lo]),
-                                               static_cast<int64_t>(g.N) - first));
+        const int count = h->count[lo];
         r.bn = ((count + nt - 1) / nt + 16 * CG - 1) / (16 * CG) * (16 * CG);
-        r.row0 = first + static_cast<int64_t>(n) * r.bn;
+        r.row0 = static_cast<int64_t>(h->first[lo]) + n * r.bn;
         r.count = min(r.bn, count - n * r.bn);
     } else {
         // bands of kBand feature tiles, columns outside: the tiles in flight form
@@ -449,32 +448,36 @@ __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint3
 
 // --------------------------------------------------------------- kernel
 
-// Expert groups (one warp): the width of the column tiles, from the largest
-// group, and the number of tiles before each expert.
+// Expert groups (all threads): their rows, clipped to the buffer, the width of
+// the column tiles, from the largest group, and the tiles before each expert.
 template <int CG>
-__device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Header *h, int lane) {
+__device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Header *h) {
+    const int lane = threadIdx.x & 31;
     int most = 0;
-    for (int e = lane; e < g.E; e += 32) {
-        const int first = g.offsets[e];
-        most = max(most, first < 0 ? 0 : min(g.counts[e], g.N - first));
+    for (int e = threadIdx.x; e < g.E; e += kTcThreads) {
+        const int first = g.offsets[e], rows = g.counts[e];
+        const int count = first < 0 ? 0 : max(0, min(rows, g.N - first));
+        h->first[e] = first;
+        h->count[e] = count;
+        most = max(most, count);
     }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if (lane == 0) h->prefix[threadIdx.x / 32] = most;      // until the scan below
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    most = __reduce_max_sync(0xFFFFFFFFu, lane < kTcThreads / 32 ? h->prefix[lane] : 0);
     const int bn = min(kMaxBn, max(1, (most + 16 * CG - 1) / (16 * CG)) * 16 * CG);
     int before = 0;
     for (int e0 = 0; e0 < g.E; e0 += 32) {
         const int e = e0 + lane;
-        int v = 0;
-        if (e < g.E) {
-            const int first = g.offsets[e];
-            v = first < 0 ? 0 : max(0, min(g.counts[e], g.N - first));
-            v = (v + bn - 1) / bn;
-        }
+        const int v = e < g.E ? (h->count[e] + bn - 1) / bn : 0;
         int sum = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int w = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if (lane >= o) sum += w;
         }
+        __syncwarp();
         if (e < g.E) h->prefix[e] = before + sum - v;
         before += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
@@ -523,7 +526,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     if (grouped) {
         wait_previous_kernel();
         allow_next_kernel();
-        if (warp == 0) count_tiles<CG>(work.g[0], work.p[0], h, lane);
+        count_tiles<CG>(work.g[0], work.p[0], h);
     }
     fence_before();
     if (CG == 2) {
