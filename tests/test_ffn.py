@@ -238,6 +238,7 @@ def ids_of(seed, T, K, E, kind):
                                         (256, 8, 256, 128), (300, 6, 60, 16), (1000, 2, 8, 64),
                                         (5000, 8, 384, 1), (2049, 4, 1024, 7), (341, 6, 33, 3),
                                         (16384, 8, 256, 128), (16385, 8, 60, 2),
+                                        (2200, 8, 1024, 3), (2048, 8, 1024, 1),
                                         (40000, 8, 128, 32)])
 def test_permute(cuda_lib, kind, T, K, E, tile):
     ids = ids_of(T + K, T, K, E, kind)
