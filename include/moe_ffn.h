@@ -35,8 +35,9 @@
  * Alignment: bf16 pointers must be 2-byte aligned, fp32 and int32 pointers
  * 4-byte aligned (else MOEF_ERR_ALIGN).  The tensor-core path is used when
  * every matrix operand is 16-byte aligned with rows of a multiple of 8
- * values; any other case takes a path of plain fused multiply-adds with the
- * same results up to the order of the sums.
+ * values; any other case takes a slower path of single-value loads with the
+ * same results up to the order of the sums.  (The number of output features
+ * may be odd on either path; moe_linear_backward's inputs K decide for it.)
  *
  * Outputs must not overlap inputs, except where an entry point says so.
  */

@@ -37,7 +37,7 @@ struct Gemm {
     int64_t b_pitch;            // values from one of its rows (of k: b_mn) to the next
 };
 
-// Plain tiled kernel of fp32 multiply-adds: any size, alignment and layout.
+// Tiled kernel of single-value loads: any size, alignment and layout.
 cudaError_t launch_gemm_simple(const Gemm &g, cudaStream_t stream);
 
 // The tensor-core kernels.  False (nothing launched) when an operand's
