@@ -229,8 +229,58 @@ def _fast_gated(x, weight, bias, activation, out, save_preact, preact, stream):
     return {"out": out} if preact is None else {"out": out, "preact": preact}
 
 
+_GRADS = ("dx", "dweight", "dbias")
+
+
+def _fast_backward(where, gated, dout, x, weight, preact, activation, want, given, workspace,
+                   stream):
+    """A backward call likewise."""
+    fast = _abi._fastcall()
+    try:
+        dev = _fast_device(fast, dout)
+        if dev is None:
+            return None
+        act = ACTIVATION[activation]
+        T, n = dout.shape
+        d, device = _abi._TO_DLPACK, dout.device
+        res, at = {}, []
+        for name, wanted, t, like in zip(_GRADS, want, given, (x, weight, weight)):
+            if t is not None:
+                res[name] = t
+                at.append(d(t))
+            elif wanted:
+                res[name] = t = torch.empty(like.shape if name != "dbias" else like.shape[:1],
+                                            dtype=torch.bfloat16, device=device)
+                at.append(t.data_ptr())
+            else:
+                at.append(None)
+        if workspace is not None:
+            nbytes = _workspace_bytes(workspace, device)
+        else:
+            nbytes = fast.call_size(_address(where + "_workspace_bytes"), T, n)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        if not res:
+            return None
+        st = fast.checked_backward(_address(where), gated, act, dev, _raw_stream(stream, dev),
+                                   d(dout), d(x), d(weight), None if preact is None else d(preact),
+                                   *at, None if workspace is None else workspace.data_ptr(),
+                                   nbytes)
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError, RuntimeError,
+            BufferError):
+        return None
+    if st < 0:
+        return None
+    _raise(st, where)
+    return res
+
+
 def _backward(where, gated, dout, x, weight, preact, activation, want_dx, want_dweight,
               want_dbias, dx, dweight, dbias, workspace, stream):
+    res = _fast_backward(where, gated, dout, x, weight, preact, activation,
+                         (want_dx, want_dweight, want_dbias), (dx, dweight, dbias), workspace,
+                         stream)
+    if res is not None:
+        return res
     T, n = _matrix(dout, "dout", "[T, features]")
     dev = dout.device
     K = _matrix(x, "x", "[T, inputs]")[1]
@@ -394,7 +444,39 @@ def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
     return res
 
 
+def _fast_expert(where, gated, x, row_token, offsets, counts, weight, bias, activation, out,
+                 stream):
+    """An expert product likewise."""
+    fast = _abi._fastcall()
+    try:
+        dev = _fast_device(fast, x)
+        if dev is None:
+            return None
+        act = ACTIVATION[activation]
+        d = _abi._TO_DLPACK
+        if out is None:
+            M = weight.shape[1]
+            out = torch.empty(((x if row_token is None else row_token).shape[0],
+                               M // 2 if gated else M), dtype=x.dtype, device=x.device)
+            at = out.data_ptr()
+        else:
+            at = d(out)
+        st = fast.checked_expert(_address(where), gated, act, dev, _raw_stream(stream, dev), d(x),
+                                 None if row_token is None else d(row_token), d(offsets),
+                                 d(counts), d(weight), None if bias is None else d(bias), at)
+    except (AttributeError, IndexError, KeyError, TypeError, RuntimeError, BufferError):
+        return None
+    if st < 0:
+        return None
+    _raise(st, where)
+    return out
+
+
 def _expert(where, gated, x, row_token, offsets, counts, weight, bias, activation, out, stream):
+    res = _fast_expert(where, gated, x, row_token, offsets, counts, weight, bias, activation, out,
+                       stream)
+    if res is not None:
+        return res
     T, K = _matrix(x, "x", "[T, inputs]")
     dev = x.device
     if not isinstance(weight, torch.Tensor) or weight.dim() != 3:

@@ -7,9 +7,9 @@
  * arguments are packed once into a C struct (a capsule) and each call passes
  * only the stream.  checked_call does the Python binding's argument checks
  * on DLPack descriptions of the tensors before calling; checked_linear and
- * checked_gated do so for moe_linear and moe_gated_ffn, and call_backward,
- * call_expert and call_permute convert those calls' arguments.  Nothing here
- * computes anything.
+ * checked_gated, checked_backward and checked_expert do so for the products
+ * of moe_ffn.h, and call_backward, call_expert and call_permute convert those
+ * calls' arguments.  Nothing here computes anything.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -410,6 +410,101 @@ static PyObject *call_permute(PyObject *self, PyObject *const *a, Py_ssize_t nar
                                                 (size_t)v[12], PTR(13)));
 }
 
+/* checked_backward(fn_address, gated, activation, device, stream, dout, x,
+ *                  weight, preact, dx, dweight, dbias, workspace,
+ *                  workspace_bytes) -> status
+ * The checks of the binding's backward calls, then the call.  dout to preact
+ * are DLPack capsules (preact or None), the gradients capsules, addresses of
+ * outputs made for this call, or None; workspace is an address or None.  -1
+ * when a tensor fails the checks. */
+static PyObject *checked_backward(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    if (nargs != 14) {
+        PyErr_SetString(PyExc_TypeError, "checked_backward takes 14 arguments");
+        return NULL;
+    }
+    backward_fn fn = (backward_fn)as_ptr(a[0]);
+    const int gated = (int)PyLong_AsLong(a[1]);
+    const int act = (int)PyLong_AsLong(a[2]);
+    const int dev = (int)PyLong_AsLong(a[3]);
+    void *stream = as_ptr(a[4]);
+    void *workspace = as_ptr(a[12]);
+    const size_t bytes = (size_t)PyLong_AsUnsignedLongLong(a[13]);
+    if (PyErr_Occurred()) return NULL;
+    const dl_tensor *t[4], *o[3];
+    void *grad[3];
+    for (int i = 0; i < 4; ++i) {
+        t[i] = described(a[5 + i]);
+        if (PyErr_Occurred()) return NULL;
+    }
+    for (int i = 0; i < 3; ++i) {
+        o[i] = NULL;
+        grad[i] = NULL;
+        if (a[9 + i] != Py_None && !output(a[9 + i], &o[i], &grad[i])) return NULL;
+    }
+    int64_t d[3], x[3], w[3];
+    int ok = fn && dense(t[0], dev, DL_BFLOAT, 16, 2, d) && dense(t[1], dev, DL_BFLOAT, 16, 2, x) &&
+             dense(t[2], dev, DL_BFLOAT, 16, 2, w) && x[0] == d[0] && w[1] == x[1] &&
+             w[0] == (gated ? 2 * d[1] : d[1]);
+    ok = ok && (gated || act ? t[3] != NULL : 1) && optional_bf16(t[3], dev, d[0], w[0]);
+    ok = ok && optional_bf16(o[0], dev, x[0], x[1]) && optional_bf16(o[1], dev, w[0], w[1]) &&
+         optional_bf16(o[2], dev, w[0], -1) && d[0] <= 0x7FFFFFFF && d[1] <= 0x7FFFFFFF &&
+         x[1] <= 0x7FFFFFFF;
+    if (!ok) return PyLong_FromLong(-1);
+    /* the preactivations of the identity are not read */
+    return PyLong_FromLong(fn(address(t[0]), address(t[1]), address(t[2]), act,
+                              gated || act ? address(t[3]) : NULL, grad[0], grad[1], grad[2],
+                              (int)d[0], (int)d[1], (int)x[1], workspace, bytes, stream));
+}
+
+/* checked_expert(fn_address, gated, activation, device, stream, x, row_token,
+ *                offsets, counts, weight, bias, out) -> status
+ * Likewise for the expert products: capsules; row_token and bias may be None,
+ * out an address. */
+static PyObject *checked_expert(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    if (nargs != 12) {
+        PyErr_SetString(PyExc_TypeError, "checked_expert takes 12 arguments");
+        return NULL;
+    }
+    expert_fn fn = (expert_fn)as_ptr(a[0]);
+    const int gated = (int)PyLong_AsLong(a[1]);
+    const int act = (int)PyLong_AsLong(a[2]);
+    const int dev = (int)PyLong_AsLong(a[3]);
+    void *stream = as_ptr(a[4]);
+    if (PyErr_Occurred()) return NULL;
+    const dl_tensor *t[6], *o;
+    void *out;
+    for (int i = 0; i < 6; ++i) {
+        t[i] = described(a[5 + i]);
+        if (PyErr_Occurred()) return NULL;
+    }
+    if (!output(a[11], &o, &out)) return NULL;
+    int64_t x[3], r[3], f[3], c[3], w[3], b[3];
+    int ok = fn && dense(t[0], dev, DL_BFLOAT, 16, 2, x) && dense(t[4], dev, DL_BFLOAT, 16, 3, w) &&
+             w[2] == x[1] && dense(t[2], dev, DL_INT, 32, 1, f) && f[0] == w[0] + 1 &&
+             dense(t[3], dev, DL_INT, 32, 1, c) && c[0] == w[0] && (!gated || w[1] % 2 == 0);
+    ok = ok && (!t[1] || dense(t[1], dev, DL_INT, 32, 1, r)) &&
+         (!t[5] || (dense(t[5], dev, DL_BFLOAT, 16, 2, b) && b[0] == w[0] && b[1] == w[1]));
+    if (!ok) return PyLong_FromLong(-1);
+    const int64_t P = t[1] ? r[0] : x[0], M = gated ? w[1] / 2 : w[1];
+    ok = (o ? optional_bf16(o, dev, P, M) : out || !P) && w[0] <= 0x7FFFFFFF && M <= 0x7FFFFFFF &&
+         x[1] <= 0x7FFFFFFF;
+    if (!ok) return PyLong_FromLong(-1);
+    return PyLong_FromLong(fn(address(t[0]), x[0], (const int32_t *)address(t[1]),
+                              (const int32_t *)address(t[2]), (const int32_t *)address(t[3]),
+                              address(t[4]), address(t[5]), act, out, P, (int)w[0], (int)M,
+                              (int)x[1], stream));
+}
+
+/* call_size(fn_address, a, b) -> a size_t function of two ints */
+static PyObject *call_size(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    long long v[MOST_ARGS];
+    if (parse_ints(a, nargs, 3, "call_size", v) != 0) return NULL;
+    return PyLong_FromSize_t(((size_t(*)(int, int))PTR(0))(INT(1), INT(2)));
+}
+
 /* permute_sizes(moe_permute_rows, moe_permute_workspace_bytes, T, K, E, tile)
  * -> (rows, workspace bytes); the first two are the functions' addresses */
 static PyObject *permute_sizes(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
@@ -461,6 +556,12 @@ static PyMethodDef methods[] = {
      "Call moe_expert_gated_ffn or moe_expert_linear."},
     {"call_permute", (PyCFunction)(void (*)(void))call_permute, METH_FASTCALL,
      "Call moe_permute."},
+    {"checked_backward", (PyCFunction)(void (*)(void))checked_backward, METH_FASTCALL,
+     "Check DLPack-described tensors and enqueue one backward call."},
+    {"checked_expert", (PyCFunction)(void (*)(void))checked_expert, METH_FASTCALL,
+     "Check DLPack-described tensors and enqueue one expert product."},
+    {"call_size", (PyCFunction)(void (*)(void))call_size, METH_FASTCALL,
+     "Call a size function of two ints."},
     {"permute_sizes", (PyCFunction)(void (*)(void))permute_sizes, METH_FASTCALL,
      "Call moe_permute_rows and moe_permute_workspace_bytes."},
     {NULL, NULL, 0, NULL},

@@ -599,10 +599,25 @@ def test_python_and_one_pass_checks_agree(cuda_lib, monkeypatch):
     ctypes call give the same bits and refuse the same calls."""
     from moe_deferred_finalize_gb300 import _abi
     x, w, b, r = rand(240, 20, 128), rand(241, 48, 128), rand(242, 48), rand(243, 20, 48)
+    wx, bx = rand(244, 2, 48, 128), rand(245, 2, 48)
+    token = torch.arange(12, dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, 8, 12], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([5, 4], dtype=torch.int32, device="cuda")
+    filled = torch.zeros(12, 24, dtype=BF16, device="cuda")
+    wide = torch.zeros(12, 48, dtype=BF16, device="cuda")
     calls = [lambda: cuda_lib.linear(x, w, bias=b, residual=r, activation="silu",
                                      save_preact=True),
              lambda: cuda_lib.linear(x, w, out_dtype=torch.float32),
-             lambda: cuda_lib.gated_ffn(x, w, bias=b, save_preact=True)]
+             lambda: cuda_lib.gated_ffn(x, w, bias=b, save_preact=True),
+             lambda: cuda_lib.linear_backward(r, x, w, activation="silu", preact=r,
+                                              want_dbias=True),
+             lambda: cuda_lib.linear_backward(r, x, w, preact=r, want_dx=False),
+             lambda: cuda_lib.gated_ffn_backward(r[:, :24].contiguous(), x, w, r,
+                                                 want_dbias=True),
+             lambda: {"out": cuda_lib.expert_gated_ffn(x, token, offsets, counts, wx,
+                                                       out=filled.clone())},
+             lambda: {"out": cuda_lib.expert_linear(x[:12].contiguous(), offsets, counts, wx,
+                                                    bias=bx, out=wide.clone())}]
     bad = [lambda: cuda_lib.linear(x.t(), w), lambda: cuda_lib.linear(x, w[:, :64]),
            lambda: cuda_lib.linear(x, w, bias=b[:40]), lambda: cuda_lib.linear(x.float(), w),
            lambda: cuda_lib.linear(x, w, residual=r[:10]), lambda: cuda_lib.linear(x, w, out=x),
@@ -610,7 +625,20 @@ def test_python_and_one_pass_checks_agree(cuda_lib, monkeypatch):
            lambda: cuda_lib.linear(x, w, out_dtype=torch.float16),
            lambda: cuda_lib.linear(x.cpu(), w), lambda: cuda_lib.gated_ffn(x, w[:47]),
            lambda: cuda_lib.gated_ffn(x, w, out=r), lambda: cuda_lib.gated_ffn(x, w, bias=b[1:]),
-           lambda: cuda_lib.gated_ffn(x, w, preact=x)]
+           lambda: cuda_lib.gated_ffn(x, w, preact=x),
+           lambda: cuda_lib.linear_backward(r, x, w, activation="silu"),
+           lambda: cuda_lib.linear_backward(r, x, w, activation="silu", preact=x),
+           lambda: cuda_lib.linear_backward(r[:10], x, w), lambda: cuda_lib.linear_backward(x, x, w),
+           lambda: cuda_lib.linear_backward(r, x, w, dx=r),
+           lambda: cuda_lib.linear_backward(r, x, w, dbias=b[:40]),
+           lambda: cuda_lib.linear_backward(r, x, w, want_dx=False, want_dweight=False),
+           lambda: cuda_lib.gated_ffn_backward(r, x, w, r),
+           lambda: cuda_lib.expert_gated_ffn(x, token, offsets[:2], counts, wx),
+           lambda: cuda_lib.expert_gated_ffn(x, token.long(), offsets, counts, wx),
+           lambda: cuda_lib.expert_gated_ffn(x, token, offsets, counts, wx[0]),
+           lambda: cuda_lib.expert_linear(x, offsets, counts, wx, out=filled),
+           lambda: cuda_lib.expert_linear(x, offsets, counts, wx, bias=b),
+           lambda: cuda_lib.expert_linear(x, offsets, counts, wx[:, :, :64])]
     for f in bad:
         with pytest.raises((ValueError, TypeError)):
             f()
