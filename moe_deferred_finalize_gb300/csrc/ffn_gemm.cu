@@ -22,7 +22,7 @@
 //
 // The two gradients of a layer are independent and often fill the last round of
 // tiles badly; they run as one launch over both products' tiles when that is
-// priced lower (2040 x 4096 x 4096: see the results table).
+// priced lower (2040 x 4096 x 4096 with its dz pass: 108 us apart, 97 together).
 //
 // Two launch forms:
 //   CG = 2  pairs of CTAs share tiles of 256 (m) x up to 256 (n): each CTA
