@@ -92,14 +92,20 @@ static_assert(sizeof(Header) <= kHeader, "header region");
 __device__ unsigned int lost_waits;
 
 // Waits for a barrier's phase; false when the wait gave up (here or in
-// another warp of the CTA), upon which every role leaves its loops.
+// another warp of the CTA), upon which every role leaves its loops.  Only time
+// in which the warp ran counts: a gap between two looks at the clock (the
+// process lost its time slice) counts as kGap at most.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
     if (bar_try(bar, parity)) return true;
-    const long long begin = clock64();
+    constexpr long long kGap = 1 << 20;
+    long long last = clock64(), spent = 0;
     for (int i = 1; !bar_try(bar, parity); ++i) {
         if (i % 64) continue;
         if (*gave_up) return false;
-        if (clock64() - begin > kWaitLimit) {
+        const long long now = clock64();
+        spent += min(now - last, kGap);
+        last = now;
+        if (spent > kWaitLimit) {
             *gave_up = 1;
             atomicAdd(&lost_waits, 1u);
             return false;

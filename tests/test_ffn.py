@@ -66,6 +66,18 @@ def test_linear_in_place_residual_and_given_outputs(cuda_lib):
     R.check(got, ref)
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 264, 512), (5, 264, 512), (12, 640, 4096), (64, 264, 8192),
+                                   (300, 264, 4096), (2000, 1000, 264)])
+def test_in_place_residual_in_every_form(cuda_lib, T, N, K):
+    """Decode kernel, single tiles, k in parts, pairs: out is the residual."""
+    x, w, r = rand(18, T, K), rand(19, N, K, scale=K ** -0.5), rand(20, T, N)
+    ref = R.linear(x, w, None, r, "gelu_tanh")
+    want = cuda_lib.linear(x, w, residual=r, activation="gelu_tanh")["out"]
+    got = cuda_lib.linear(x, w, residual=r, activation="gelu_tanh", out=r)
+    R.check(got, ref)
+    assert torch.equal(got["out"], want)
+
+
 def test_linear_misaligned_operands(cuda_lib):
     x, w, b, r = rand(12, 33, 128), rand(13, 72, 128, scale=0.1), rand(14, 72), rand(15, 33, 72)
     ref = R.linear(x, w, b, r, "gelu")
@@ -315,6 +327,10 @@ def test_experts_epilogues(cuda_lib, name):
 @pytest.mark.parametrize("kind", ["one", "none"])
 def test_experts_all_rows_in_one_expert_and_none_at_all(cuda_lib, kind):
     check_experts(cuda_lib, 300, 2, 6, 16, 128, 64, "silu", False, kind)
+
+
+def test_experts_at_the_most_experts(cuda_lib):
+    check_experts(cuda_lib, 700, 2, 1024, 2, 64, 24, "silu", True, "holes")
 
 
 def test_experts_rows_beyond_the_buffer_and_tokens_beyond_x(cuda_lib):
