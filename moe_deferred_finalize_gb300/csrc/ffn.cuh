@@ -3,6 +3,7 @@
 // and the launchers.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -40,13 +41,25 @@ struct Gemm {
 // Tiled kernel of single-value loads: any size, alignment and layout.
 cudaError_t launch_gemm_simple(const Gemm &g, cudaStream_t stream);
 
+// The column sums that launch_dz left per kBiasRows rows: dbias[c] = sum of
+// partial[:, c], rows added in order.
+struct BiasSum {
+    const float *partial;       // fp32 [rows, cols]
+    uint16_t *dbias;            // bf16 [cols], null: nothing to do
+    int rows, cols;
+};
+cudaError_t launch_bias_sum(const BiasSum &b, cudaStream_t stream);
+
 // The tensor-core kernels.  False (nothing launched) when an operand's
 // alignment or pitch rules them out; otherwise *err is the launch's result.
-bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err);
+// The launch also does `bias` on warps that have nothing to copy.
+bool launch_gemm_tc(const Gemm &g, const BiasSum &bias, int num_sms, cudaStream_t stream,
+                    cudaError_t *err);
 
 // Two products (not grouped, not gated) in one launch; false (nothing launched)
 // also when two launches are priced lower.
-bool launch_two_gemms_tc(const Gemm *g, int num_sms, cudaStream_t stream, cudaError_t *err);
+bool launch_two_gemms_tc(const Gemm *g, const BiasSum &bias, int num_sms, cudaStream_t stream,
+                         cudaError_t *err);
 
 // The kernel for a handful of rows (at most 8 * kDecodeTiles); false (nothing
 // launched) when the sizes or alignment are not its own.
@@ -57,13 +70,13 @@ bool launch_gemm_decode(const Gemm &g, int num_sms, cudaStream_t stream, cudaErr
 cudaError_t read_lost_waits(unsigned *count);
 
 // dz of the backward passes, its bf16 rounding into dz [T, pitch] (null: none;
-// the values past cols are not written), and the column sums into dbias (bf16 [cols], null: none).  Linear:
-// cols = n, dz = dout * act'(preact), or dout without preact.  Gated: cols =
-// 2n, dout [T, n], preact [T, 2n].  partial: fp32 [ceil(T / kBiasRows), cols]
-// scratch, used with dbias.
+// the values past cols are not written), and its column sums over kBiasRows
+// rows at a time into partial (fp32 [ceil(T / kBiasRows), cols], null: none).
+// Linear: cols = n, dz = dout * act'(preact), or dout without preact.  Gated:
+// cols = 2n, dout [T, n], preact [T, 2n].
 constexpr int kBiasRows = 32;
 cudaError_t launch_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
-                      uint16_t *dz, int64_t pitch, float *partial, uint16_t *dbias, int T, int n,
+                      uint16_t *dz, int64_t pitch, float *partial, int T, int n,
                       cudaStream_t stream);
 
 // The grouped layout (moe_permute).  permute_chunks: rows of E counts that
@@ -89,6 +102,15 @@ __device__ __forceinline__ float act_value(float z, int act) {
         case MOEF_ACT_RELU: return z > 0.f || z != z ? z : 0.f;
         default: return z;
     }
+}
+
+// One column of a BiasSum.
+__device__ __forceinline__ void sum_columns(const BiasSum &b, int c) {
+    if (c >= b.cols) return;
+    float sum = 0.f;
+#pragma unroll 16
+    for (int r = 0; r < b.rows; ++r) sum += b.partial[static_cast<int64_t>(r) * b.cols + c];
+    b.dbias[c] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
 }
 
 // act'(z), and act(z) in *value.

@@ -30,15 +30,18 @@ size_t backward_bytes(int64_t T, int64_t cols) {
     return dz_bytes(T, cols) + static_cast<size_t>(rows * cols * 4);
 }
 
-moef_status run_gemm(const Gemm &g, cudaStream_t stream) {
+// One product, and the bias gradient that goes with it (taken out of *bias).
+moef_status run_gemm(const Gemm &g, moef::BiasSum *bias, cudaStream_t stream) {
     int sms = 0;
     const moef_status st = cuda_status(moef::current_sms(&sms));
     if (st != MOEF_OK) return st;
     cudaError_t err = cudaSuccess;
-    if (!moef::launch_gemm_decode(g, sms, stream, &err) &&
-        !moef::launch_gemm_tc(g, sms, stream, &err))
-        err = moef::launch_gemm_simple(g, stream);
-    return cuda_status(err);
+    if (moef::launch_gemm_decode(g, sms, stream, &err)) return cuda_status(err);
+    if (moef::launch_gemm_tc(g, *bias, sms, stream, &err)) {
+        bias->dbias = nullptr;
+        return cuda_status(err);
+    }
+    return cuda_status(moef::launch_gemm_simple(g, stream));
 }
 
 // The backward pass of z = x weight^T + bias with `cols` features z, from
@@ -79,10 +82,12 @@ moef_status backward(const void *dout, const void *x, const void *weight, moef_a
                                                dz_bytes(T, cols));
     if (dz || dbias) {
         const moef_status st = cuda_status(moef::launch_dz(
-            u16(dout), u16(preact), static_cast<int>(act), gated, dz, dz_pitch(cols), partial,
-            static_cast<uint16_t *>(dbias), T, n, stream));
+            u16(dout), u16(preact), static_cast<int>(act), gated, dz, dz_pitch(cols),
+            dbias ? partial : nullptr, T, n, stream));
         if (st != MOEF_OK) return st;
     }
+    moef::BiasSum bias = {partial, static_cast<uint16_t *>(dbias),
+                          (T - 1) / moef::kBiasRows + 1, cols};
     Gemm g[2] = {};
     int n_products = 0;
     if (dx) {
@@ -115,13 +120,13 @@ moef_status backward(const void *dout, const void *x, const void *weight, moef_a
         const moef_status st = cuda_status(moef::current_sms(&sms));
         if (st != MOEF_OK) return st;
         cudaError_t err = cudaSuccess;
-        if (moef::launch_two_gemms_tc(g, sms, stream, &err)) return cuda_status(err);
+        if (moef::launch_two_gemms_tc(g, bias, sms, stream, &err)) return cuda_status(err);
     }
     for (int i = 0; i < n_products; ++i) {
-        const moef_status st = run_gemm(g[i], stream);
+        const moef_status st = run_gemm(g[i], &bias, stream);
         if (st != MOEF_OK) return st;
     }
-    return MOEF_OK;
+    return cuda_status(moef::launch_bias_sum(bias, stream));
 }
 
 moef_status expert_product(const void *x, int64_t T, const int32_t *row_token,
@@ -154,7 +159,8 @@ moef_status expert_product(const void *x, int64_t T, const int32_t *row_token,
     g.row_token = row_token;
     g.b_rows = T;
     g.b_pitch = K;
-    return run_gemm(g, stream);
+    moef::BiasSum none = {};
+    return run_gemm(g, &none, stream);
 }
 
 }  // namespace
@@ -187,7 +193,8 @@ moef_status moe_linear(const void *x, const void *weight, const void *bias,
     g.act = static_cast<int>(act);
     g.b_rows = T;
     g.b_pitch = K;
-    return run_gemm(g, stream);
+    moef::BiasSum none = {};
+    return run_gemm(g, &none, stream);
 }
 
 size_t moe_linear_backward_workspace_bytes(int T, int N) {
@@ -226,7 +233,8 @@ moef_status moe_gated_ffn(const void *x, const void *weight, const void *bias,
     g.act = static_cast<int>(act);
     g.b_rows = T;
     g.b_pitch = H;
-    return run_gemm(g, stream);
+    moef::BiasSum none = {};
+    return run_gemm(g, &none, stream);
 }
 
 size_t moe_gated_ffn_backward_workspace_bytes(int T, int I) {

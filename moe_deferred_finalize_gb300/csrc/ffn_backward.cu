@@ -8,9 +8,9 @@
 // every eighth row, all of a thread's loads in flight before their first use;
 // the activation is a template argument, so its arithmetic overlaps.  The
 // column sums build up in registers, in fp32 and before dz is rounded; the
-// CTA adds its warps' sums in order and writes one row of `partial`, and a
-// second kernel adds those rows in order (no atomics: equal calls give equal
-// bits).  2040 x 4096 with GELU takes 12.6 us (4.0 TB/s; with the activation
+// CTA adds its warps' sums in order and writes one row of `partial`, whose rows
+// are then added in order (no atomics: equal calls give equal bits) by idle
+// warps of the product that follows, or by a kernel of its own.  2040 x 4096 with GELU takes 12.6 us (4.0 TB/s; with the activation
 // chosen per value and 32 rows a thread it took 40 us), 4096 x 2048 gated with
 // SiLU 15.5 us (5.4 TB/s).
 #include "ffn.cuh"
@@ -104,25 +104,11 @@ dz_kernel(const uint16_t *dout, const uint16_t *preact, uint16_t *dz, int64_t pi
     }
 }
 
-// dbias[c] = sum of partial[:, c]: 32 columns a CTA, 8 warps taking every
-// eighth row, their sums added in warp order.
-__global__ void __launch_bounds__(256)
-bias_sum_kernel(const float *partial, int rows, int cols, uint16_t *dbias) {
-    __shared__ float s[8][32];
+__global__ void __launch_bounds__(32)
+bias_sum_kernel(const BiasSum b) {
     wait_previous_kernel();
     allow_next_kernel();
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x / 32;
-    float sum = 0.f;
-    if (c < cols)
-        for (int r = w; r < rows; r += 8) sum += partial[static_cast<int64_t>(r) * cols + c];
-    s[w][threadIdx.x & 31] = sum;
-    __syncthreads();
-    if (w == 0 && c < cols) {
-        sum = s[0][threadIdx.x];
-#pragma unroll
-        for (int k = 1; k < 8; ++k) sum += s[k][threadIdx.x];
-        dbias[c] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
-    }
+    sum_columns(b, blockIdx.x * 32 + threadIdx.x);
 }
 
 template <typename... Params, typename... Args>
@@ -161,23 +147,21 @@ cudaError_t start_dz(const uint16_t *dout, const uint16_t *preact, int act, uint
 }  // namespace
 
 cudaError_t launch_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
-                      uint16_t *dz, int64_t pitch, float *partial, uint16_t *dbias, int T, int n,
+                      uint16_t *dz, int64_t pitch, float *partial, int T, int n,
                       cudaStream_t stream) {
     const uintptr_t bits = reinterpret_cast<uintptr_t>(dout) | reinterpret_cast<uintptr_t>(preact) |
                            reinterpret_cast<uintptr_t>(dz);
-    float *part = dbias ? partial : nullptr;
     const bool vec = n % 8 == 0 && bits % 16 == 0;
-    cudaError_t err;
     if (gated)
-        err = vec ? start_dz<8, true>(dout, preact, act, dz, pitch, part, T, n, stream)
-                  : start_dz<1, true>(dout, preact, act, dz, pitch, part, T, n, stream);
-    else
-        err = vec ? start_dz<8, false>(dout, preact, act, dz, pitch, part, T, n, stream)
-                  : start_dz<1, false>(dout, preact, act, dz, pitch, part, T, n, stream);
-    if (err != cudaSuccess || !dbias) return err;
-    const int cols = gated ? 2 * n : n;
-    return start(bias_sum_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), 256, stream,
-                 partial, (T - 1) / kBiasRows + 1, cols, dbias);
+        return vec ? start_dz<8, true>(dout, preact, act, dz, pitch, partial, T, n, stream)
+                   : start_dz<1, true>(dout, preact, act, dz, pitch, partial, T, n, stream);
+    return vec ? start_dz<8, false>(dout, preact, act, dz, pitch, partial, T, n, stream)
+               : start_dz<1, false>(dout, preact, act, dz, pitch, partial, T, n, stream);
+}
+
+cudaError_t launch_bias_sum(const BiasSum &b, cudaStream_t stream) {
+    if (!b.dbias) return cudaSuccess;
+    return start(bias_sum_kernel, dim3(static_cast<unsigned>((b.cols + 31) / 32)), 32, stream, b);
 }
 
 }  // namespace moef

@@ -76,6 +76,7 @@ struct Work {
     Gemm g[N];
     TcPlan p[N];
     int tiles0;
+    BiasSum bias;
 };
 
 struct Header {
@@ -673,7 +674,16 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 }
                 if (!ok) break;
             }
-        } else if (warp == kCopyWarp && elect_one()) {
+        } else if (warp > kCopyWarp) {
+            // the bias gradient, 32 columns a warp
+            if (work.bias.dbias) {
+                wait_previous_kernel();
+                constexpr int kWarps = kGatherWarps - 1;
+                for (int c = (blockIdx.x * kWarps + warp - kCopyWarp - 1) * 32;
+                     c < work.bias.cols; c += gridDim.x * kWarps * 32)
+                    sum_columns(work.bias, c + lane);
+            }
+        } else if (elect_one()) {
             bool ok = true;
             for (int ti = first_tile; ti < tiles && ok; ti += step) {
                 const int q = product_of(ti);
@@ -1086,7 +1096,8 @@ bool describe(const Gemm &g, const Cut &cut, TcPlan *plan, CUtensorMap *map) {
 
 }  // namespace
 
-bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err) {
+bool launch_gemm_tc(const Gemm &g, const BiasSum &bias, int num_sms, cudaStream_t stream,
+                    cudaError_t *err) {
     if (!can_copy(g)) return false;
     // Expert groups, whose sizes only the device knows, run on pairs; their
     // column counts follow from the row counts there.
@@ -1098,6 +1109,7 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
     Work<1> work;
     work.g[0] = g;
     work.tiles0 = 0;
+    work.bias = bias;
     if (!describe(g, cut, &work.p[0], work.map[0])) return false;
     const TcPlan &p = work.p[0];
     const int64_t units = g.E ? INT32_MAX
@@ -1111,7 +1123,8 @@ bool launch_gemm_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t
     return true;
 }
 
-bool launch_two_gemms_tc(const Gemm *g, int num_sms, cudaStream_t stream, cudaError_t *err) {
+bool launch_two_gemms_tc(const Gemm *g, const BiasSum &bias, int num_sms, cudaStream_t stream,
+                         cudaError_t *err) {
     if (!can_copy(g[0]) || !can_copy(g[1])) return false;
     // longer tiles first; two launches cost the second one's start, about 5000
     // clocks, but each may be cut as suits it
@@ -1123,6 +1136,7 @@ bool launch_two_gemms_tc(const Gemm *g, int num_sms, cudaStream_t stream, cudaEr
     Work<2> work;
     work.g[0] = *order[0];
     work.g[1] = *order[1];
+    work.bias = bias;
     int bn[2];
     double apart[2];
     const double together = choose_two(work.g, num_sms, bn);
