@@ -196,6 +196,7 @@ struct Finish {
     bool any, both, vec;
     float bias[GATED ? 4 : 2];
 
+    // e: the expert whose bias is loaded; negative: none
     __device__ __forceinline__ Finish(const Gemm &gemm, int feature, int e) : g(gemm), m(feature) {
         any = m < g.M;
         both = m + 1 < g.M;
@@ -204,7 +205,7 @@ struct Finish {
                                reinterpret_cast<uintptr_t>(g.preact);
         vec = (g.M & 1) == 0 && (rest & 3) == 0 && (out & (g.out_f32 ? 7 : 3)) == 0;
         const uint16_t *b = g.bias + static_cast<int64_t>(e) * (GATED ? 2 : 1) * g.M;
-        const bool have = g.bias != nullptr;
+        const bool have = e >= 0 && g.bias != nullptr;
         bias[0] = have && any ? bf16_value(b, m) : 0.f;
         bias[1] = have && both ? bf16_value(b, m + 1) : 0.f;
         if constexpr (GATED) {
@@ -279,50 +280,77 @@ __device__ __forceinline__ void store2(uint16_t *p, float a, float b) {
 // A pair by itself: for views whose pairs cannot be one access (odd feature
 // counts, 2-byte aligned outputs).
 template <bool GATED>
-__device__ __noinline__ void finish_scalar(const Finish<GATED> &f, int64_t n, float a, float b,
+__device__ __noinline__ void finish_scalar(const Gemm &g, int m, int64_t n, float a, float b,
                                            float c, float d) {
+    const Finish<GATED> f(g, m, -1);
     if constexpr (GATED) f.gated(n, a, b, c, d);
-    else f.linear(n, a, b, f.g.residual ? f.residual(n) : 0u);
+    else f.linear(n, a, b, g.residual ? f.residual(n) : 0u);
 }
 
 constexpr int kChunk = 16;      // columns a warp finishes at a time
 
-// One tile out of TMEM: this warp's 32 lanes (rows of A), every other chunk
-// of the columns [begin, end); arrives on `done` (0: nowhere) once it has read
-// them.  parts > 0: so many other parts' sums of these columns are in `sums`.
-// Lanes swap values so that each holds two adjacent features of one column;
-// bias, activation, residual and stores then run as loops over the chunk, with
-// nothing to decide per value, so their latencies overlap (deciding per pair
-// took 22 us per 256 x 256 tile, now about 3).
+// A warp's part of one tile: its 32 lanes (rows of A), every other chunk of the
+// columns [begin, end).  Made before the accumulator is waited for, so that the
+// bias and the first chunk's residual are there by then.
 template <bool GATED>
-__device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_cta, uint32_t tmem,
-                                            int quarter, int side, int lane, uint32_t done,
-                                            int begin, int end, const float *sums, int parts) {
-    const int feature = m_cta + (GATED ? quarter * 16 + (lane >> 2) * 2
-                                       : quarter * 32 + (lane & ~1));
-    const Finish<GATED> f(g, feature, t.e);
+struct TilePart {
+    const Finish<GATED> f;
+    const Tile t;
+    int lane, quarter, first, own, begin, end;
+    uint32_t next[GATED ? 1 : kChunk / 2];      // residual pairs of the next chunk
+
+    __device__ __forceinline__ TilePart(const Gemm &g, const Tile &tile, int m_cta, int warp_quarter,
+                                        int side, int warp_lane, int from, int to)
+        : f(g, m_cta + (GATED ? warp_quarter * 16 + (warp_lane >> 2) * 2
+                              : warp_quarter * 32 + (warp_lane & ~1)), tile.e),
+          t(tile), lane(warp_lane), quarter(warp_quarter), first(from + kChunk * side),
+          own(to - from), begin(from),
+          end(min(to, (tile.count + kChunk - 1) / kChunk * kChunk)) {
+        if (first < end) load_residual(first);
+    }
+    // row of the output and columns left, for this lane's first column of a chunk
+    __device__ __forceinline__ int column() const { return GATED ? lane & 3 : lane & 1; }
+    __device__ __forceinline__ int left(int c0) const {
+        return f.any ? t.count - c0 - column() : 0;
+    }
+    __device__ __forceinline__ void load_residual(int c0) {
+        if constexpr (!GATED) {
+            if (f.g.residual && f.vec) {
+                const int64_t M = f.g.M;
+                const uint16_t *p = f.g.residual + (t.row0 + c0 + column()) * M + f.m;
+                const int n = left(c0);
+#pragma unroll
+                for (int k = 0; k < kChunk / 2; ++k, p += 2 * M)
+                    next[k] = 2 * k < n ? *reinterpret_cast<const uint32_t *>(p) : 0u;
+            }
+        }
+    }
+};
+
+// The part out of TMEM; arrives on `done` (0: nowhere) once it has read its
+// columns.  parts > 0: so many other parts' sums of these columns are in
+// `sums`.  Lanes swap values so that each holds two adjacent features of one
+// column; bias, activation, residual and stores then run as loops over the
+// chunk, with nothing to decide per value, so their latencies overlap
+// (deciding per pair took 22 us per 256 x 256 tile, now about 3).
+template <bool GATED>
+__device__ __forceinline__ void finish_tile(TilePart<GATED> &part, uint32_t tmem, uint32_t done,
+                                            const float *sums, int parts) {
+    const Finish<GATED> &f = part.f;
+    const Gemm &g = f.g;
+    const Tile &t = part.t;
+    const int lane = part.lane, own = part.own, begin = part.begin, end = part.end;
+    const int quarter = part.quarter;
     const bool odd = lane & 1, upper = lane & 2;
     const int64_t M = g.M;
-    const int col = GATED ? lane & 3 : lane & 1;
-    const int own = end - begin;
-    end = min(end, (t.count + kChunk - 1) / kChunk * kChunk);
-    if (begin + kChunk * side >= end) {         // nothing for this warp
+    if (part.first >= end) {            // nothing for this warp
         if (done && lane == 0) bar_arrive(done);
         return;
     }
 #pragma unroll 1
-    for (int c0 = begin + kChunk * side; c0 < end; c0 += 2 * kChunk) {
-        const int64_t row = t.row0 + c0 + col;
-        const int left = f.any ? t.count - c0 - col : 0;
-        uint32_t res[kChunk / 2];
-        if constexpr (!GATED) {
-            if (g.residual && f.vec) {
-                const uint16_t *p = g.residual + row * M + f.m;
-#pragma unroll
-                for (int k = 0; k < kChunk / 2; ++k, p += 2 * M)
-                    res[k] = 2 * k < left ? *reinterpret_cast<const uint32_t *>(p) : 0u;
-            }
-        }
+    for (int c0 = part.first; c0 < end; c0 += 2 * kChunk) {
+        const int64_t row = t.row0 + c0 + part.column();
+        const int left = part.left(c0);
         uint32_t r[kChunk];
         tmem_load16(tmem + c0, r);
         if (done && c0 + 2 * kChunk >= end) {       // the accumulator has been read
@@ -330,6 +358,12 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
             __syncwarp();
             if (lane == 0) bar_arrive(done);
         }
+        uint32_t res[GATED ? 1 : kChunk / 2];
+        if constexpr (!GATED) {
+#pragma unroll
+            for (int k = 0; k < kChunk / 2; ++k) res[k] = part.next[k];
+        }
+        if (c0 + 2 * kChunk < end) part.load_residual(c0 + 2 * kChunk);
         for (int k = 0; k < parts; ++k) {
             const float *from = sums + (k * own + c0 - begin) * 128 + quarter * 32 + lane;
 #pragma unroll
@@ -362,7 +396,7 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
 #pragma unroll
                 for (int k = 0; k < kChunk / 4; ++k)
                     if (4 * k < left)
-                        finish_scalar<true>(f, row + 4 * k, gate[2 * k], gate[2 * k + 1],
+                        finish_scalar<true>(g, f.m, row + 4 * k, gate[2 * k], gate[2 * k + 1],
                                             up[2 * k], up[2 * k + 1]);
                 continue;
             }
@@ -394,7 +428,7 @@ __device__ __forceinline__ void finish_tile(const Gemm &g, const Tile &t, int m_
 #pragma unroll
                 for (int k = 0; k < kChunk / 2; ++k)
                     if (2 * k < left)
-                        finish_scalar<false>(f, row + 2 * k, z[2 * k], z[2 * k + 1], 0.f, 0.f);
+                        finish_scalar<false>(g, f.m, row + 2 * k, z[2 * k], z[2 * k + 1], 0.f, 0.f);
                 continue;
             }
             const int64_t at = row * M + f.m;
@@ -779,14 +813,20 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
             const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                  (n & 1) * kMaxBn;
             begin(ti);
+            if (split > 1) {        // joined below
+                const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
+                (void)__all_sync(0xFFFFFFFFu, ok);
+                fence_after();
+                break;
+            }
+            TilePart<GATED> part_of(work.g[q], t, t.m0 + half * m_cta_rows, quarter, side, lane, 0,
+                                    t.bn);
             const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             fence_after();
-            if (split > 1) break;           // joined below
             const uint32_t bar = smem_addr(&h->acc_empty[n & 1]);
-            finish_tile<GATED>(work.g[q], t, t.m0 + half * m_cta_rows, acc, quarter, side, lane,
-                               map_rank(bar, CG == 2 ? lead : cluster_rank()), 0, t.bn, nullptr,
-                               0);
+            finish_tile<GATED>(part_of, acc, map_rank(bar, CG == 2 ? lead : cluster_rank()),
+                               nullptr, 0);
         }
     }
     __syncwarp();
@@ -798,14 +838,18 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         const Tile t = tile_of(first_tile, 0);
         if (works && !*gave_up)
             send_columns<CG>(t, acc, received, split, part, half, quarter, side, lane);
-        cluster_sync();         // every part's sums have arrived
-        if (works && !*gave_up) {
-            const int own = own_columns(t.bn, split);
-            finish_tile<GATED>(work.g[0], t, t.m0 + half * m_cta_rows, acc, quarter, side, lane, 0,
-                               part * own, (part + 1) * own,
-                               reinterpret_cast<const float *>(smem + (received -
-                                                                       smem_addr(smem))),
-                               split - 1);
+        const int own = own_columns(t.bn, split);
+        if (works) {
+            TilePart<GATED> part_of(work.g[0], t, t.m0 + half * m_cta_rows, quarter, side, lane,
+                                    part * own, (part + 1) * own);
+            cluster_sync();         // every part's sums have arrived
+            if (!*gave_up)
+                finish_tile<GATED>(part_of, acc, 0,
+                                   reinterpret_cast<const float *>(smem + (received -
+                                                                           smem_addr(smem))),
+                                   split - 1);
+        } else {
+            cluster_sync();
         }
     }
     fence_before();
