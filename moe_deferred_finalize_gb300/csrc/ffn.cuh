@@ -61,9 +61,9 @@ bool launch_gemm_tc(const Gemm &g, const BiasSum &bias, int num_sms, cudaStream_
 bool launch_two_gemms_tc(const Gemm *g, const BiasSum &bias, int num_sms, cudaStream_t stream,
                          cudaError_t *err);
 
-// The kernel for a handful of rows (at most 8 * kDecodeTiles); false (nothing
-// launched) when the sizes or alignment are not its own.
-constexpr int kDecodeTiles = 2;
+// The kernel for a handful of rows; false (nothing launched) when the sizes or
+// alignment are not its own, or the tensor-core one is faster.
+constexpr int kDecodeRows = 8;
 bool launch_gemm_decode(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err);
 
 // Barrier waits that gave up since the library was loaded on this device.

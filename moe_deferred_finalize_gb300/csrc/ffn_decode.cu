@@ -7,8 +7,8 @@
 // fragment slot holds, as long as A and B agree, so a lane's 16-byte load of
 // row g (8 consecutive k) is taken as the k slots of two MMAs, and the same
 // 16 bytes of token g feed the B side.  No shared memory, no transposition
-// before the warps' partial sums meet at the end.  Each warp has up to four
-// steps (8 KB of weights) in flight.
+// before the warps' partial sums meet at the end.  Each warp has four steps (8
+// KB of weights) in flight, 16 warps an SM.
 //
 // Against the tensor-core kernel with k split over a cluster it saves the
 // pipeline set-up, two cluster barriers and the remote reads.
@@ -65,13 +65,13 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// NT: tiles of 8 tokens.  features: output features of this CTA, at most 16 (8
-// gated); fewer leave MMA rows empty and spread a small matrix over more SMs.
-template <int NT, bool GATED, int W>
+// features: output features of this CTA, at most 16 (8 gated); fewer leave MMA
+// rows empty and spread a small matrix over more SMs.
+template <bool GATED, int W>
 __global__ void __launch_bounds__(32 * W, 16 / W)
 decode_kernel(const Gemm g, const int features) {
-    __shared__ float part[W][16][8 * NT + 1];
-    constexpr int kDepth = NT == 1 ? 4 : 2;     // steps in flight per warp
+    __shared__ float part[W][16][kDecodeRows + 1];
+    constexpr int kDepth = 4;                   // steps in flight per warp
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int m0 = blockIdx.x * features;
     const int row = lane >> 2, k8 = (lane & 3) * 8;
@@ -83,19 +83,16 @@ decode_kernel(const Gemm g, const int features) {
                        : row + 8 < features && m0 + row + 8 < g.M ? m0 + row + 8 : m0;
     const uint16_t *a_lo = g.a + static_cast<int64_t>(lo_row) * g.K + k8;
     const uint16_t *a_hi = g.a + static_cast<int64_t>(hi_row) * g.K + k8;
-    const uint16_t *x[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        x[n] = g.b + static_cast<int64_t>(8 * n + row < g.N ? 8 * n + row : 0) * g.K + k8;
+    const uint16_t *x = g.b + static_cast<int64_t>(row < g.N ? row : 0) * g.K + k8;
 
     wait_previous_kernel();
     allow_next_kernel();
 
-    float acc[NT][4] = {};
+    float acc[4] = {};
     const int full = g.K / kStepK, steps = (g.K + kStepK - 1) / kStepK;
     int s0 = warp;
     for (; s0 + W * (kDepth - 1) < full; s0 += W * kDepth) {
-        uint4 lo[kDepth][2], hi[kDepth][2], xv[kDepth][2][NT];
+        uint4 lo[kDepth][2], hi[kDepth][2], xv[kDepth][2];
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
 #pragma unroll
@@ -103,19 +100,15 @@ decode_kernel(const Gemm g, const int features) {
                 const int k = (s0 + d * W) * kStepK + 32 * j;
                 lo[d][j] = load_once(a_lo + k);
                 hi[d][j] = load_once(a_hi + k);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) xv[d][j][n] = load_once(x[n] + k);
+                xv[d][j] = load_once(x + k);
             }
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    mma_16bytes(acc[n], lo[d][j], hi[d][j], xv[d][j][n]);
+            for (int j = 0; j < 2; ++j) mma_16bytes(acc, lo[d][j], hi[d][j], xv[d][j]);
     }
     if (s0 < steps) {       // fewer than kDepth steps, the last one maybe partial
-        uint4 lo[kDepth][2], hi[kDepth][2], xv[kDepth][2][NT];
+        uint4 lo[kDepth][2], hi[kDepth][2], xv[kDepth][2];
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
 #pragma unroll
@@ -124,25 +117,18 @@ decode_kernel(const Gemm g, const int features) {
                 const bool in = k + k8 < g.K;
                 lo[d][j] = load_if(a_lo + k, in);
                 hi[d][j] = load_if(a_hi + k, in);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) xv[d][j][n] = load_if(x[n] + k, in);
+                xv[d][j] = load_if(x + k, in);
             }
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    mma_16bytes(acc[n], lo[d][j], hi[d][j], xv[d][j][n]);
+            for (int j = 0; j < 2; ++j) mma_16bytes(acc, lo[d][j], hi[d][j], xv[d][j]);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int c = 8 * n + (lane & 3) * 2;
-        part[warp][row][c] = acc[n][0];
-        part[warp][row][c + 1] = acc[n][1];
-        part[warp][row + 8][c] = acc[n][2];
-        part[warp][row + 8][c + 1] = acc[n][3];
-    }
+    const int c = (lane & 3) * 2;
+    part[warp][row][c] = acc[0];
+    part[warp][row][c + 1] = acc[1];
+    part[warp][row + 8][c] = acc[2];
+    part[warp][row + 8][c + 1] = acc[3];
     __syncthreads();
 
     // the warps' sums in warp order, features along the threads
@@ -176,10 +162,10 @@ decode_kernel(const Gemm g, const int features) {
     }
 }
 
-template <int NT, int W>
-cudaError_t start(const Gemm &g, int features, cudaStream_t stream) {
+template <int W>
+cudaError_t start(const Gemm &g, int ctas, int features, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((g.M + features - 1) / features);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(32 * W);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -187,8 +173,8 @@ cudaError_t start(const Gemm &g, int features, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return g.gated ? cudaLaunchKernelEx(&cfg, decode_kernel<NT, true, W>, g, features)
-                   : cudaLaunchKernelEx(&cfg, decode_kernel<NT, false, W>, g, features);
+    return g.gated ? cudaLaunchKernelEx(&cfg, decode_kernel<true, W>, g, features)
+                   : cudaLaunchKernelEx(&cfg, decode_kernel<false, W>, g, features);
 }
 
 // Features per CTA: whole MMA rows when they give every SM a CTA, else down to
@@ -201,25 +187,18 @@ int features_per_cta(const Gemm &g, int num_sms) {
 }
 
 // Whether this kernel or the tensor-core one is faster, from sweeps (us): this
-// one starts in 1.5 and reads 6.9 MB/us with up to 8 rows (3.5 and 6.0 with
-// 16), but a wave of its CTAs takes at least 1.8 (2.2), more than a short k
-// needs; the other one starts in 5.5 and reads 6.7 MB/us.  1 x 65536 x 512:
-// 25.0 here, 15.6 there; 16 x 16384 x 4096: 27.6 and 24.5; 16 x 4096 x 7168:
-// 13.6 and 15.5; 8 x 65536 x 7168: 137 and 140.
-bool pays(const Gemm &g, int features, int num_sms) {
-    const bool two = g.N > 8;
-    const int64_t ctas = (g.M + features - 1) / features;
+// one starts in 1.5 and reads 6.9 MB/us, but a round of its CTAs takes at least
+// 1.8, more than a short k needs; the other one starts in 3.8 and reads 6.7
+// MB/us.  1 x 65536 x 512: 25 here, 13.7 there; 1 x 4096 x 7168: 11.3 and 12.7;
+// 1 x 65536 x 7168: 131-134 and 138, 8 rows of it 135-139 and 138.  From 9 rows
+// on, a second fragment of tokens made this one slower than the other everywhere
+// but at a router's size (16 x 4096 x 7168: 13.9 and 12.8; 16 x 256 x 7168: 6.1
+// and 6.4).
+bool pays(const Gemm &g, int ctas, int num_sms) {
     const double mb = 2e-6 * g.M * (g.gated ? 2.0 : 1.0) * g.K;
-    const double waves = static_cast<double>((ctas + 2 * num_sms - 1) / (2 * num_sms));
-    const double read = mb / (two ? 6.0 : 6.9), latency = waves * (two ? 2.2 : 1.8);
-    return (two ? 3.5 : 1.5) + (read > latency ? read : latency) < 5.5 + mb / 6.7;
-}
-
-template <int NT>
-cudaError_t run(const Gemm &g, int features, int num_sms, cudaStream_t stream) {
-    // up to one CTA per SM has 16 warps, more have 8 each, two to an SM
-    return (g.M + features - 1) / features <= num_sms ? start<NT, 16>(g, features, stream)
-                                                      : start<NT, 8>(g, features, stream);
+    const int at_once = (ctas <= num_sms ? 1 : ctas <= 2 * num_sms ? 2 : 4) * num_sms;
+    const double latency = 1.8 * ((ctas + at_once - 1) / at_once), read = mb / 6.9;
+    return 1.5 + (read > latency ? read : latency) < 3.8 + mb / 6.7;
 }
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -227,12 +206,18 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }  // namespace
 
 bool launch_gemm_decode(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err) {
-    if (g.E || g.a_mn || g.b_mn || g.N > 8 * kDecodeTiles || g.K % 8 || g.b_pitch != g.K ||
+    if (g.E || g.a_mn || g.b_mn || g.N > kDecodeRows || g.K % 8 || g.b_pitch != g.K ||
         !aligned16(g.a) || !aligned16(g.b))
         return false;
     const int features = features_per_cta(g, num_sms);
-    if (!pays(g, features, num_sms)) return false;
-    *err = g.N <= 8 ? run<1>(g, features, num_sms, stream) : run<2>(g, features, num_sms, stream);
+    const int ctas = (g.M + features - 1) / features;
+    if (!pays(g, ctas, num_sms)) return false;
+    // The SMs hold 16 warps of this kernel (128 registers): one CTA of 16, two
+    // of 8 or four of 4, whichever gets most CTAs running at once (65536 rows
+    // of 7168: 136 us in CTAs of 8 warps, 131 of 4; 8192 of 1024: 5.5 and 4.8).
+    *err = ctas <= num_sms       ? start<16>(g, ctas, features, stream)
+           : ctas <= 2 * num_sms ? start<8>(g, ctas, features, stream)
+                                 : start<4>(g, ctas, features, stream);
     return true;
 }
 

@@ -51,7 +51,7 @@ def test_linear_epilogue(cuda_lib, name, T, N, K):
                         f"{name} bias={bias is not None} res={res is not None} {dt}")
 
 
-@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 31, 33, 63, 65, 127, 128, 129, 192, 257, 1025])
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 15, 16, 17, 31, 33, 63, 65, 127, 128, 129, 192, 257, 1025])
 def test_linear_every_row_count_class(cuda_lib, T):
     x, w = rand(7, T, 320), rand(8, 392, 320, scale=0.05)
     R.check(cuda_lib.linear(x, w), R.linear(x, w), f"T={T}")
