@@ -182,7 +182,8 @@ moef_status moe_gated_ffn_backward(const void *dout, const void *x, const void *
  *               slots)
  *
  * Experts stand in ascending order, an expert's rows in (token, slot) order;
- * all outputs are exact.  P may exceed that number; all P rows are written.  A token may name an expert twice; it gets two rows.
+ * all outputs are exact.  P may exceed that number; all P rows are written.  A
+ * token may name an expert twice; it gets two rows.
  * 1 <= K <= MOEF_MAX_K, 1 <= E <= MOEF_MAX_EXPERTS, T >= 0 (T = 0 writes zero
  * offsets and counts and -1 to row_token).
  *
@@ -211,7 +212,8 @@ moef_status moe_permute(const int32_t *expert_ids, int T, int K, int E, int tile
  *   weight     bf16 [E, 2I, H] ([E, N, K])
  *   bias       bf16 [E, 2I] ([E, N]), or NULL
  *   out        bf16 [P, I] ([P, N]); rows of no expert are left as they were
- *   T >= 0, P >= 0, 1 <= E <= MOEF_MAX_EXPERTS
+ *   T, P       0 .. INT_MAX; with either 0 nothing is enqueued
+ *   E          1 .. MOEF_MAX_EXPERTS
  *
  * The layout is read on the device.  Rows at or past P are not computed, and
  * a row_token outside [0, T) reads as a row of zeros.

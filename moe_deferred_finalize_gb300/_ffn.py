@@ -51,6 +51,12 @@ def _lib():
     return _LIB
 
 
+def _int(n):
+    """n as a C int; what does not fit becomes -1, which every entry point
+    refuses (ctypes would drop the high bits)."""
+    return n if -1 <= n <= 0x7FFFFFFF else -1
+
+
 _ADDRESS = {}
 
 
@@ -159,7 +165,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor
         res["preact"] = preact = _output(preact, "preact", torch.bfloat16, (T, N), dev)
     with _on(dev):
         st = _lib().moe_linear(_ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), act, _ptr(out),
-                               _OUT_TYPE[out_dtype], _ptr(preact), T, N, K, _stream(stream, dev))
+                               _OUT_TYPE[out_dtype], _ptr(preact), _int(T), _int(N), _int(K),
+                               _stream(stream, dev))
     _raise(st, "moe_linear")
     return res
 
@@ -307,22 +314,22 @@ def _backward(where, gated, dout, x, weight, preact, activation, want_dx, want_d
     lib = _lib()
     size = lib.moe_gated_ffn_backward_workspace_bytes if gated \
         else lib.moe_linear_backward_workspace_bytes
-    nbytes = int(size(T, n))
+    nbytes = int(size(_int(T), _int(n)))
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     else:
         nbytes = _workspace_bytes(workspace, dev)
     with _on(dev):
         st = _call("call_backward", where, _ptr(dout), _ptr(x), _ptr(weight), act, _ptr(preact),
-                   _ptr(res.get("dx")), _ptr(res.get("dweight")), _ptr(res.get("dbias")), T, n, K,
-                   _ptr(workspace), nbytes, _stream(stream, dev))
+                   _ptr(res.get("dx")), _ptr(res.get("dweight")), _ptr(res.get("dbias")), _int(T),
+                   _int(n), _int(K), _ptr(workspace), nbytes, _stream(stream, dev))
     _raise(st, where)
     return res
 
 
 def linear_backward_workspace_bytes(T: int, N: int) -> int:
     """Bytes of workspace linear_backward needs for T rows of N features."""
-    return int(_lib().moe_linear_backward_workspace_bytes(int(T), int(N)))
+    return int(_lib().moe_linear_backward_workspace_bytes(_int(int(T)), _int(int(N))))
 
 
 def linear_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *,
@@ -369,14 +376,15 @@ def gated_ffn(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Ten
         res["preact"] = preact = _output(preact, "preact", torch.bfloat16, (T, rows), dev)
     with _on(dev):
         st = _lib().moe_gated_ffn(_ptr(x), _ptr(weight), _ptr(bias), act, _ptr(out),
-                                  _ptr(preact), T, I, H, _stream(stream, dev))
+                                  _ptr(preact), _int(T), _int(I), _int(H),
+                                  _stream(stream, dev))
     _raise(st, "moe_gated_ffn")
     return res
 
 
 def gated_ffn_backward_workspace_bytes(T: int, I: int) -> int:
     """Bytes of workspace gated_ffn_backward needs for T rows of I features."""
-    return int(_lib().moe_gated_ffn_backward_workspace_bytes(int(T), int(I)))
+    return int(_lib().moe_gated_ffn_backward_workspace_bytes(_int(int(T)), _int(int(I))))
 
 
 def gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
@@ -401,12 +409,13 @@ def _permute_sizes(T, K, E, tile):
         return fast.permute_sizes(_address("moe_permute_rows"),
                                   _address("moe_permute_workspace_bytes"), T, K, E, tile)
     lib = _lib()
+    T, K, E, tile = _int(T), _int(K), _int(E), _int(tile)
     return lib.moe_permute_rows(T, K, E, tile), lib.moe_permute_workspace_bytes(T, K, E)
 
 
 def permute_rows(T: int, K: int, E: int, tile: int) -> int:
     """The most rows the grouped layout of T x K slots over E experts can need."""
-    return int(_lib().moe_permute_rows(int(T), int(K), int(E), int(tile)))
+    return int(_permute_sizes(int(T), int(K), int(E), int(tile))[0])
 
 
 def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
@@ -437,8 +446,8 @@ def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
     elif nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     with _on(dev):
-        st = _call("call_permute", "moe_permute", _ptr(expert_ids), T, K, E, tile,
-                   _ptr(res["idx_map"]), _ptr(res["row_token"]), P, _ptr(res["offsets"]),
+        st = _call("call_permute", "moe_permute", _ptr(expert_ids), _int(T), _int(K), _int(E),
+                   _int(tile), _ptr(res["idx_map"]), _ptr(res["row_token"]), P, _ptr(res["offsets"]),
                    _ptr(res["counts"]), _ptr(workspace), nbytes, _stream(stream, dev))
     _raise(st, "moe_permute")
     return res
@@ -498,7 +507,8 @@ def _expert(where, gated, x, row_token, offsets, counts, weight, bias, activatio
     out = _output(out, "out", torch.bfloat16, (P, M), dev)
     with _on(dev):
         st = _call("call_expert", where, _ptr(x), T, _ptr(row_token), _ptr(offsets), _ptr(counts),
-                   _ptr(weight), _ptr(bias), act, _ptr(out), P, E, M, K, _stream(stream, dev))
+                   _ptr(weight), _ptr(bias), act, _ptr(out), P, _int(E), _int(M), _int(K),
+                   _stream(stream, dev))
     _raise(st, where)
     return out
 

@@ -119,6 +119,18 @@ def test_permute_rows_bounds_every_routing(lib):
     assert lib.moe_permute_rows(4, 2, 8, 16) == 128
 
 
+def test_sizes_past_a_c_int_are_refused_not_cut_off(lib):
+    """2^32 + 1 cut to 32 bits would be 1: a valid size of another problem."""
+    import moe_deferred_finalize_gb300 as M
+    big = 2 ** 32 + 1
+    assert M.linear_backward_workspace_bytes(big, 8) == 0
+    assert M.linear_backward_workspace_bytes(8, big) == 0
+    assert M.gated_ffn_backward_workspace_bytes(big, 8) == 0
+    for sizes in ((big, 1, 1, 1), (1, big, 1, 1), (1, 1, big, 1), (1, 1, 1, big)):
+        assert M.permute_rows(*sizes) == 0, sizes
+    assert M.permute_rows(1, 1, 1, 1) == 1
+
+
 def test_lost_waits_needs_a_counter(lib):
     assert lib.moe_ffn_lost_waits(None) == E_NULL
 
