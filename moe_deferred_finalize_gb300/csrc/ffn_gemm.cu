@@ -11,9 +11,9 @@
 // one warp for both needed 430 clocks a block, near the 512 that the MMAs of
 // the widest tile take.  Gathered rows are copied four to an instruction, so B
 // then has six warps (64 experts of 4096 x 1536, 32768 rows: 1681 us with one
-// warp, 659 with four, 589 with six).  One lane of a further warp issues the MMAs into TMEM,
-// and eight finish tiles.  The accumulator is double buffered (2 x 256 TMEM
-// columns), so a tile's epilogue runs under the next tile's products.
+// warp, 659 with four, 589 with six).  One lane of a further warp issues the MMAs
+// into TMEM, and eight warps finish tiles.  The accumulator is double buffered (2
+// x 256 TMEM columns), so a tile's epilogue runs under the next tile's products.
 //
 // Gated form: the A tile interleaves gate and up rows (g0, u0, g1, u1, ...),
 // which one 4-D tensor map [E][I][2][H] of the weights does in the copy.  A
@@ -151,7 +151,7 @@ __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const He
         m = local / nt;
         n = local % nt;
         const int count = h->count[lo];
-        r.bn = ((count + nt - 1) / nt + 16 * CG - 1) / (16 * CG) * (16 * CG);
+        r.bn = ((count - 1) / nt + 16 * CG) / (16 * CG) * (16 * CG);
         r.row0 = static_cast<int64_t>(h->first[lo]) + n * r.bn;
         r.count = min(r.bn, count - n * r.bn);
     } else {
@@ -507,11 +507,11 @@ __device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Head
     __syncthreads();
     if (threadIdx.x >= 32) return;
     most = __reduce_max_sync(0xFFFFFFFFu, lane < kTcThreads / 32 ? h->prefix[lane] : 0);
-    const int bn = min(kMaxBn, max(1, (most + 16 * CG - 1) / (16 * CG)) * 16 * CG);
+    const int bn = max(1, (min(most, kMaxBn) + 16 * CG - 1) / (16 * CG)) * 16 * CG;
     int before = 0;
     for (int e0 = 0; e0 < g.E; e0 += 32) {
         const int e = e0 + lane;
-        const int v = e < g.E ? (h->count[e] + bn - 1) / bn : 0;
+        const int v = e < g.E && h->count[e] > 0 ? (h->count[e] - 1) / bn + 1 : 0;
         int sum = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -1198,7 +1198,8 @@ bool launch_two_gemms_tc(const Gemm *g, const BiasSum &bias, int num_sms, cudaSt
 }
 
 cudaError_t read_lost_waits(unsigned *count) {
-    return cudaMemcpyFromSymbol(count, lost_waits, sizeof(*count));
+    const cudaError_t err = cudaDeviceSynchronize();    // the copy waits for its own stream only
+    return err != cudaSuccess ? err : cudaMemcpyFromSymbol(count, lost_waits, sizeof(*count));
 }
 
 }  // namespace moef

@@ -670,6 +670,42 @@ def test_python_and_one_pass_checks_agree(cuda_lib, monkeypatch):
             f()
 
 
+def test_sizes_past_a_c_int_are_refused(cuda_lib):
+    """2^32 + 5 rows must not become 5."""
+    x = torch.empty(2 ** 32 + 5, 1, dtype=BF16, device="cuda")
+    w = torch.ones(1, 1, dtype=BF16, device="cuda")
+    with pytest.raises(cuda_lib.MoefError):
+        cuda_lib.linear(x, w, out=x.view(2 ** 32 + 5, 1))
+    with pytest.raises(cuda_lib.MoefError):
+        cuda_lib.gated_ffn(x, torch.ones(2, 1, dtype=BF16, device="cuda"), out=x)
+    with pytest.raises(cuda_lib.MoefError):
+        cuda_lib.linear_backward(x, x, w, want_dx=False, want_dweight=True)
+
+
+def test_expert_with_the_most_rows(cuda_lib):
+    """One expert with 2^31 - 1 rows: nothing in the cut of the tiles may pass 31 bits."""
+    P, K, N = 2 ** 31 - 1, 8, 8
+    x = torch.zeros(P, K, dtype=BF16, device="cuda")
+    some = [0, 1, 255, 256, P // 2, P - 257, P - 2, P - 1]
+    x[some] = rand(3, len(some), K)
+    w = rand(4, 1, N, K)
+    offsets = torch.tensor([0, P], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([P], dtype=torch.int32, device="cuda")
+    out = torch.full((P, N), 7.0, dtype=BF16, device="cuda")
+    cuda_lib.expert_linear(x, offsets, counts, w, out=out)
+    R.check({"out": out[some]}, {"out": R.linear(x[some], w[0])["out"]}, "rows")
+    assert int((out[: 2 ** 20] == 7.0).sum()) == 0 and int((out[-2 ** 20:] == 7.0).sum()) == 0
+
+
+def test_lost_waits_waits_for_every_stream(cuda_lib):
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        done.record()
+    assert cuda_lib.lost_waits() == 0
+    assert done.query()
+
+
 def test_no_barrier_wait_was_lost(cuda_lib):
     """Last: none of the launches above gave up a wait."""
     torch.cuda.synchronize()
