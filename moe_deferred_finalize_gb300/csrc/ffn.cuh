@@ -41,7 +41,7 @@ struct Gemm {
 // Tiled kernel of single-value loads: any size, alignment and layout.
 cudaError_t launch_gemm_simple(const Gemm &g, cudaStream_t stream);
 
-// The column sums that launch_dz left per kBiasRows rows: dbias[c] = sum of
+// The column sums that launch_dz left per sum_rows(T) rows: dbias[c] = sum of
 // partial[:, c], rows added in order.
 struct BiasSum {
     const float *partial;       // fp32 [rows, cols]
@@ -70,11 +70,11 @@ bool launch_gemm_decode(const Gemm &g, int num_sms, cudaStream_t stream, cudaErr
 cudaError_t read_lost_waits(unsigned *count);
 
 // dz of the backward passes, its bf16 rounding into dz [T, pitch] (null: none;
-// the values past cols are not written), and its column sums over kBiasRows
-// rows at a time into partial (fp32 [ceil(T / kBiasRows), cols], null: none).
+// the values past cols are not written), and its column sums over sum_rows(T)
+// rows at a time into partial (fp32 [ceil(T / sum_rows(T)), cols], null: none).
 // Linear: cols = n, dz = dout * act'(preact), or dout without preact.  Gated:
 // cols = 2n, dout [T, n], preact [T, 2n].
-constexpr int kBiasRows = 32;
+int sum_rows(int T);        // T >= 1
 cudaError_t launch_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
                       uint16_t *dz, int64_t pitch, float *partial, int T, int n,
                       cudaStream_t stream);

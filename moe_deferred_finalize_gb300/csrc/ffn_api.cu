@@ -26,7 +26,7 @@ int64_t dz_pitch(int64_t cols) { return (cols + 7) / 8 * 8; }
 size_t dz_bytes(int64_t T, int64_t cols) { return static_cast<size_t>(T * dz_pitch(cols) * 2); }
 
 size_t backward_bytes(int64_t T, int64_t cols) {
-    const int64_t rows = T > 0 ? (T - 1) / moef::kBiasRows + 1 : 0;
+    const int64_t rows = T > 0 ? (T - 1) / moef::sum_rows(static_cast<int>(T)) + 1 : 0;
     return dz_bytes(T, cols) + static_cast<size_t>(rows * cols * 4);
 }
 
@@ -87,7 +87,7 @@ moef_status backward(const void *dout, const void *x, const void *weight, moef_a
         if (st != MOEF_OK) return st;
     }
     moef::BiasSum bias = {partial, static_cast<uint16_t *>(dbias),
-                          (T - 1) / moef::kBiasRows + 1, cols};
+                          (T - 1) / moef::sum_rows(T) + 1, cols};
     Gemm g[2] = {};
     int n_products = 0;
     if (dx) {

@@ -140,6 +140,24 @@ def test_gated_ffn_backward(cuda_lib, name, T, I, H):
     R.check(got, R.backward(d, x, w, pre, name, True), name)
 
 
+@pytest.mark.parametrize("T", [16384, 16385, 40001])
+@pytest.mark.parametrize("n", [1, 5, 8, 24, 64, 100, 264, 520])
+def test_backward_of_many_rows(cuda_lib, T, n):
+    """The column sums of many rows, over few and many columns."""
+    x, w, d = rand(60, T, 64), rand(61, n, 64, scale=0.1), rand(62, T, n, scale=0.1)
+    pre = cuda_lib.linear(x, w, save_preact=True)["preact"]
+    got = cuda_lib.linear_backward(d, x, w, activation="silu", preact=pre, want_dbias=True)
+    ref = R.backward(d, x, w, pre, "silu", False)
+    R.check(got, ref, "linear")
+    got = cuda_lib.linear_backward(d, x, w, activation="silu", preact=pre, want_dx=False,
+                                   want_dweight=False, want_dbias=True)
+    R.check(got, {"dbias": ref["dbias"]}, "dbias alone")
+    w = rand(63, 2 * n, 64, scale=0.1)
+    pre = cuda_lib.gated_ffn(x, w, save_preact=True)["preact"]
+    got = cuda_lib.gated_ffn_backward(d, x, w, pre, want_dbias=True)
+    R.check(got, R.backward(d, x, w, pre, "silu", True), "gated")
+
+
 def test_backward_gives_what_is_wanted(cuda_lib):
     x, w, d = rand(36, 40, 64), rand(37, 48, 64), rand(38, 40, 48)
     full = cuda_lib.linear_backward(d, x, w, want_dbias=True)
