@@ -413,6 +413,42 @@ def _permute_sizes(T, K, E, tile):
     return lib.moe_permute_rows(T, K, E, tile), lib.moe_permute_workspace_bytes(T, K, E)
 
 
+def _fast_permute(expert_ids, E, tile, row_token, idx_map, offsets, counts, workspace, stream):
+    """permute_tokens likewise."""
+    fast = _abi._fastcall()
+    try:
+        dev = _fast_device(fast, expert_ids)
+        if dev is None:
+            return None
+        E, tile = int(E), int(tile)
+        T, K = expert_ids.shape
+        P, nbytes = _permute_sizes(T, K, E, tile)
+        d, device, i32 = _abi._TO_DLPACK, expert_ids.device, torch.int32
+        res, at = {}, []
+        for name, t, shape in (("idx_map", idx_map, (T, K)), ("row_token", row_token, (P,)),
+                               ("offsets", offsets, (E + 1,)), ("counts", counts, (E,))):
+            if t is None:
+                res[name] = t = torch.empty(shape, dtype=i32, device=device)
+                at.append(t.data_ptr())
+            else:
+                res[name] = t
+                at.append(d(t))
+        if workspace is not None:
+            nbytes = _workspace_bytes(workspace, device)
+        elif nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        st = fast.checked_permute(_address("moe_permute"), dev, _raw_stream(stream, dev), E, tile,
+                                  P, d(expert_ids), *at,
+                                  None if workspace is None else workspace.data_ptr(), nbytes)
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError, RuntimeError,
+            BufferError):
+        return None
+    if st < 0:
+        return None
+    _raise(st, "moe_permute")
+    return res
+
+
 def permute_rows(T: int, K: int, E: int, tile: int) -> int:
     """The most rows the grouped layout of T x K slots over E experts can need."""
     return int(_permute_sizes(int(T), int(K), int(E), int(tile))[0])
@@ -430,6 +466,10 @@ def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
     "offsets" int32 [E + 1] and "counts" int32 [E].  Ids outside [0, E) get
     no row: idx_map is -1 there, which ``moe_finalize`` must not be given
     (leave such tokens out of its T; ``check_indices`` counts them)."""
+    res = _fast_permute(expert_ids, E, tile, row_token, idx_map, offsets, counts, workspace,
+                        stream)
+    if res is not None:
+        return res
     T, K = _matrix(expert_ids, "expert_ids", "[T, K]")
     dev = expert_ids.device
     E, tile = int(E), int(tile)

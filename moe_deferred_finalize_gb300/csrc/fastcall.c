@@ -7,9 +7,9 @@
  * arguments are packed once into a C struct (a capsule) and each call passes
  * only the stream.  checked_call does the Python binding's argument checks
  * on DLPack descriptions of the tensors before calling; checked_linear and
- * checked_gated, checked_backward and checked_expert do so for the products
- * of moe_ffn.h, and call_backward, call_expert and call_permute convert those
- * calls' arguments.  Nothing here computes anything.
+ * checked_gated, checked_backward, checked_expert and checked_permute do so for
+ * the calls of moe_ffn.h, and call_backward, call_expert and call_permute
+ * convert those calls' arguments.  Nothing here computes anything.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -497,6 +497,54 @@ static PyObject *checked_expert(PyObject *self, PyObject *const *a, Py_ssize_t n
                               (int)x[1], stream));
 }
 
+/* 1 when the output t is dense int32 [a, b] (b < 0: [a]), or was given by its
+ * address (null only when it is empty) */
+static int int32_output(const dl_tensor *t, const void *at, int dev, int64_t a, int64_t b) {
+    int64_t d[2];
+    if (!t) return at || a * b == 0;
+    if (b < 0) return dense(t, dev, DL_INT, 32, 1, d) && d[0] == a;
+    return dense(t, dev, DL_INT, 32, 2, d) && d[0] == a && d[1] == b;
+}
+
+/* checked_permute(fn_address, device, stream, E, tile, P, expert_ids, idx_map,
+ *                 row_token, offsets, counts, workspace, workspace_bytes) ->
+ * status.  Likewise for moe_permute: expert_ids is a capsule, the outputs
+ * capsules or addresses, workspace an address or None; P is the size of a
+ * row_token given by its address. */
+static PyObject *checked_permute(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    if (nargs != 13) {
+        PyErr_SetString(PyExc_TypeError, "checked_permute takes 13 arguments");
+        return NULL;
+    }
+    permute_fn fn = (permute_fn)as_ptr(a[0]);
+    const int dev = (int)PyLong_AsLong(a[1]);
+    void *stream = as_ptr(a[2]);
+    const int64_t E = PyLong_AsLongLong(a[3]), tile = PyLong_AsLongLong(a[4]);
+    int64_t P = PyLong_AsLongLong(a[5]);
+    void *workspace = as_ptr(a[11]);
+    const size_t bytes = (size_t)PyLong_AsUnsignedLongLong(a[12]);
+    if (PyErr_Occurred()) return NULL;
+    const dl_tensor *ids = described(a[6]), *o[4];
+    void *at[4];
+    if (PyErr_Occurred()) return NULL;
+    for (int i = 0; i < 4; ++i)
+        if (!output(a[7 + i], &o[i], &at[i])) return NULL;
+    int64_t d[2], r[1];
+    int ok = fn && dense(ids, dev, DL_INT, 32, 2, d) && d[0] <= 0x7FFFFFFF && d[1] <= 0x7FFFFFFF &&
+             E >= 0 && E < 0x7FFFFFFF && tile >= 0 && tile <= 0x7FFFFFFF;
+    if (ok && o[1]) {
+        ok = dense(o[1], dev, DL_INT, 32, 1, r);
+        P = r[0];
+    }
+    ok = ok && int32_output(o[0], at[0], dev, d[0], d[1]) && int32_output(o[1], at[1], dev, P, -1) &&
+         int32_output(o[2], at[2], dev, E + 1, -1) && int32_output(o[3], at[3], dev, E, -1);
+    if (!ok) return PyLong_FromLong(-1);
+    return PyLong_FromLong(fn((const int32_t *)address(ids), (int)d[0], (int)d[1], (int)E,
+                              (int)tile, (int32_t *)at[0], (int32_t *)at[1], P, (int32_t *)at[2],
+                              (int32_t *)at[3], workspace, bytes, stream));
+}
+
 /* call_size(fn_address, a, b) -> a size_t function of two ints */
 static PyObject *call_size(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
     (void)self;
@@ -560,6 +608,8 @@ static PyMethodDef methods[] = {
      "Check DLPack-described tensors and enqueue one backward call."},
     {"checked_expert", (PyCFunction)(void (*)(void))checked_expert, METH_FASTCALL,
      "Check DLPack-described tensors and enqueue one expert product."},
+    {"checked_permute", (PyCFunction)(void (*)(void))checked_permute, METH_FASTCALL,
+     "Check DLPack-described tensors and enqueue one moe_permute call."},
     {"call_size", (PyCFunction)(void (*)(void))call_size, METH_FASTCALL,
      "Call a size function of two ints."},
     {"permute_sizes", (PyCFunction)(void (*)(void))permute_sizes, METH_FASTCALL,

@@ -688,6 +688,54 @@ def test_python_and_one_pass_checks_agree(cuda_lib, monkeypatch):
             f()
 
 
+def test_row_map_python_and_one_pass_checks_agree(cuda_lib, monkeypatch):
+    from moe_deferred_finalize_gb300 import _abi
+    ids = torch.randint(-1, 16, (50, 4), dtype=torch.int32, device="cuda")
+    P = cuda_lib.permute_rows(50, 4, 16, 8)
+
+    def i32(*shape):
+        return torch.full(shape, -7, dtype=torch.int32, device="cuda")
+
+    calls = [lambda: cuda_lib.permute_tokens(ids, 16, 8),
+             lambda: cuda_lib.permute_tokens(ids[:0], 16, 8),
+             lambda: cuda_lib.permute_tokens(ids, 16),
+             lambda: cuda_lib.permute_tokens(ids.repeat(100, 1), 16, 8),
+             lambda: cuda_lib.permute_tokens(ids, 16, 8, row_token=i32(P + 9), idx_map=i32(50, 4)),
+             lambda: cuda_lib.permute_tokens(ids, 16, 8, offsets=i32(17), counts=i32(16))]
+    bad = [lambda: cuda_lib.permute_tokens(ids.long(), 16, 8),
+           lambda: cuda_lib.permute_tokens(ids.t(), 16, 8),
+           lambda: cuda_lib.permute_tokens(ids[0], 16, 8),
+           lambda: cuda_lib.permute_tokens(ids.cpu(), 16, 8),
+           lambda: cuda_lib.permute_tokens(ids, 0, 8),
+           lambda: cuda_lib.permute_tokens(ids, -3, 8),
+           lambda: cuda_lib.permute_tokens(ids, 1025, 8),
+           lambda: cuda_lib.permute_tokens(ids, 16, 0),
+           lambda: cuda_lib.permute_tokens(ids, 16, 2 ** 32 + 8),
+           lambda: cuda_lib.permute_tokens(ids, 16, 8, row_token=i32(P - 1)),
+           lambda: cuda_lib.permute_tokens(ids, 16, 8, row_token=i32(P, 1)),
+           lambda: cuda_lib.permute_tokens(ids, 16, 8, idx_map=i32(4, 50)),
+           lambda: cuda_lib.permute_tokens(ids, 16, 8, offsets=i32(16)),
+           lambda: cuda_lib.permute_tokens(ids, 16, 8, counts=i32(17)),
+           lambda: cuda_lib.permute_tokens(ids.repeat(100, 1), 16, 8, workspace=i32(1))]
+
+    def errors():
+        kinds = []
+        for f in bad:
+            with pytest.raises((ValueError, TypeError, cuda_lib.MoefError)) as e:
+                f()
+            kinds.append(e.type)
+        return kinds
+
+    fast, kinds = [f() for f in calls], errors()
+    monkeypatch.setattr(_abi, "_FAST", None)
+    for f, ref in zip(calls, fast):
+        got = f()
+        assert list(got) == list(ref)
+        for key in ref:
+            assert got[key].dtype == torch.int32 and torch.equal(got[key], ref[key])
+    assert errors() == kinds
+
+
 def test_sizes_past_a_c_int_are_refused(cuda_lib):
     """2^32 + 5 rows must not become 5."""
     x = torch.empty(2 ** 32 + 5, 1, dtype=BF16, device="cuda")
