@@ -33,7 +33,8 @@
 // k can also be split over a cluster of `split` CTAs or pairs: each finishes
 // its share of the tile's columns, the others send it their sums of those
 // into its shared memory, and it adds them in rank order (equal calls give
-// equal bits).
+// equal bits).  Expert groups choose the split on the device, where the number
+// of tiles is known: a cluster's units share one tile's k, or take tiles alone.
 #include "ffn.cuh"
 #include "host.cuh"
 #include "tc.cuh"
@@ -59,9 +60,9 @@ constexpr long long kWaitLimit = 4000000000;     // clocks (two seconds) until a
 
 // How one launch is cut up (see choose_cut).
 struct TcPlan {
-    int log_split;      // 2^log_split parts of k
-    int received;       // bytes of the other parts' sums
-    int bn;             // columns per tile; 0: from the expert counts, on the device
+    int log_split;      // 2^log_split parts of k; groups: at most, chosen on the device
+    int received;       // bytes of the other parts' sums (not groups)
+    int bn;             // columns per tile; groups: at most, they follow from the counts
     int m_tiles, n_tiles;
     int gather;         // B rows are fetched by row_token
     int box_rows;       // rows of one B copy (k-contiguous B)
@@ -85,6 +86,7 @@ struct Header {
     int gave_up;
     int bn;
     int tiles;
+    int log_split;
     // expert groups: column tiles before each, first row, rows
     int prefix[MOEF_MAX_EXPERTS + 1], first[MOEF_MAX_EXPERTS], count[MOEF_MAX_EXPERTS];
 };
@@ -469,9 +471,16 @@ __host__ __device__ __forceinline__ int own_columns(int bn, int split) {
     return ((bn + split - 1) / split + kChunk - 1) / kChunk * kChunk;
 }
 
+// Shared memory for the other parts' sums.
+constexpr int kMaxReceived = 64 * 1024;
+
+__host__ __device__ __forceinline__ int received_bytes(int bn, int split) {
+    return (split - 1) * own_columns(bn, split) * 512;
+}
+
 template <int CG>
 __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint32_t buf, int split,
-                                             int part, int half, int quarter, int side, int lane) {
+                                             int part, int rank0, int quarter, int side, int lane) {
     const int own = own_columns(t.bn, split);
     for (int c0 = kChunk * side; c0 < t.count; c0 += 2 * kChunk) {
         const int owner = c0 / own;
@@ -481,7 +490,7 @@ __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint3
         const int slot = part < owner ? part : part - 1;
         const uint32_t at = map_rank(
             buf + ((slot * own + c0 - owner * own) * 128 + quarter * 32 + lane) * 4,
-            owner * CG + half);
+            rank0 + owner * CG);
 #pragma unroll
         for (int c = 0; c < kChunk; ++c) store_remote(at + c * 512, r[c]);
     }
@@ -490,7 +499,9 @@ __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint3
 // --------------------------------------------------------------- kernel
 
 // Expert groups (all threads): their rows, clipped to the buffer, the width of
-// the column tiles, from the largest group, and the tiles before each expert.
+// the column tiles, from the largest group, the tiles before each expert, and
+// the parts of k: as many as the launch's clusters have room for while each
+// halving saves more k blocks (400 clocks) than it costs to join.
 template <int CG>
 __device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Header *h) {
     const int lane = threadIdx.x & 31;
@@ -507,7 +518,7 @@ __device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Head
     __syncthreads();
     if (threadIdx.x >= 32) return;
     most = __reduce_max_sync(0xFFFFFFFFu, lane < kTcThreads / 32 ? h->prefix[lane] : 0);
-    const int bn = max(1, (min(most, kMaxBn) + 16 * CG - 1) / (16 * CG)) * 16 * CG;
+    const int bn = max(1, (min(most, p.bn) + 16 * CG - 1) / (16 * CG)) * 16 * CG;
     int before = 0;
     for (int e0 = 0; e0 < g.E; e0 += 32) {
         const int e = e0 + lane;
@@ -523,9 +534,16 @@ __device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Head
         before += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
     if (lane == 0) {
+        const int tiles = before * p.m_tiles, units = gridDim.x / CG;
+        int blocks = (g.K + kBlockK - 1) / kBlockK, log = 0;
+        while (log < p.log_split && tiles <= units >> (log + 1) &&
+               received_bytes(bn, 2 << log) <= kMaxReceived &&
+               (blocks /= 2) * 400 > (log ? 300 << log : 1500 + 10 * bn))
+            ++log;
         h->prefix[g.E] = before;
         h->bn = bn;
-        h->tiles = before * p.m_tiles;
+        h->tiles = tiles;
+        h->log_split = log;
     }
 }
 
@@ -537,10 +555,10 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
     Header *h = reinterpret_cast<Header *>(smem + (base - smem_addr(smem)));
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    // the CTA's place in its cluster: which part of k, and which half of a pair
-    const int log_split = N == 1 ? work.p[0].log_split : 0, split = 1 << log_split;
-    const int rank = CG == 2 || split > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int part = rank / CG, half = rank % CG, lead = part * CG;
+    // the CTA's place in its cluster: which unit, and which half of a pair
+    const bool clustered = N == 1 && work.p[0].log_split > 0;
+    const int rank = CG == 2 || clustered ? static_cast<int>(cluster_rank()) : 0;
+    const int unit = rank / CG, half = rank % CG, lead = unit * CG;
     const bool leader = half == 0;
     const uint16_t pair = static_cast<uint16_t>(3 << lead);
     volatile int *gave_up = &h->gave_up;
@@ -573,17 +591,23 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     if (CG == 2) {
         cluster_sync();
     } else {
-        if (split > 1) cluster_arrive();        // awaited before the first remote store
+        if (clustered) cluster_arrive();        // awaited before the first remote store
         __syncthreads();
     }
     fence_after();
 
     const uint32_t tmem = h->tmem;
-    int tiles, bn_max;
+    int tiles, bn_max, log_split = 0, bytes_received = 0;
     if (grouped) {
         tiles = h->tiles;
         bn_max = h->bn;
+        log_split = h->log_split;
+        bytes_received = received_bytes(bn_max, 1 << log_split);
     } else {
+        if (N == 1) {
+            log_split = work.p[0].log_split;
+            bytes_received = work.p[0].received;
+        }
         tiles = work.p[0].n_tiles * work.p[0].m_tiles;
         bn_max = work.p[0].bn;
         if constexpr (N == 2) {
@@ -592,7 +616,8 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         }
     }
     const uint32_t received = base + kHeader;       // the other parts' sums
-    const uint32_t stage0 = received + (N == 1 ? work.p[0].received : 0);
+    const uint32_t stage0 = received + bytes_received;
+    const int split = 1 << log_split, part = unit & (split - 1);
     const int bnc_max = bn_max / CG;                // B rows per CTA
     // transposed B comes in blocks of 64 columns; a multiple of 2048 bytes
     const bool any_mn = work.g[0].b_mn || work.g[N - 1].b_mn;
@@ -601,7 +626,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     const int stages = min(static_cast<unsigned>(kMaxStages),
                            (kStageArea - (stage0 - received)) / stage_bytes);
     const int first_tile = (blockIdx.x / CG) >> log_split;
-    const int step = (gridDim.x / CG) >> log_split;
+    const int step = (gridDim.x / CG) >> log_split;     // k in parts: at least as many as tiles
     const int m_cta_rows = GATED ? 64 : 128;        // features per CTA
     // the product that a tile belongs to, and this part's k blocks of it
     auto product_of = [&](int ti) { return N == 2 && ti >= work.tiles0 ? 1 : 0; };
@@ -835,11 +860,12 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         const int quarter = warp & 3, side = (warp - 2) >> 2;
         const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         if (CG == 1) cluster_wait();        // every part has started
-        const Tile t = tile_of(first_tile, 0);
-        if (works && !*gave_up)
-            send_columns<CG>(t, acc, received, split, part, half, quarter, side, lane);
-        const int own = own_columns(t.bn, split);
-        if (works) {
+        if (works && first_tile < tiles) {
+            const Tile t = tile_of(first_tile, 0);
+            if (!*gave_up)
+                send_columns<CG>(t, acc, received, split, part, (unit - part) * CG + half, quarter,
+                                 side, lane);
+            const int own = own_columns(t.bn, split);
             TilePart<GATED> part_of(work.g[0], t, t.m0 + half * m_cta_rows, quarter, side, lane,
                                     part * own, (part + 1) * own);
             cluster_sync();         // every part's sums have arrived
@@ -852,6 +878,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
             cluster_sync();
         }
     }
+    if (CG == 1 && clustered && split == 1) cluster_wait();
     fence_before();
     if (CG == 2) cluster_sync(); else __syncthreads();
     fence_after();
@@ -961,6 +988,11 @@ Slots cluster_slots(int num_sms) {
     return s;
 }
 
+// One CTA or a pair per tile, columns per tile, parts of k.
+struct Cut {
+    int cg, bn, split;
+};
+
 // How a product that is not grouped is cut: one CTA or a pair per tile, columns
 // per tile, parts of k.  Every choice is priced in SM clocks and the cheapest
 // taken.  The figures are fits to sweeps over 17..4096 rows:
@@ -977,15 +1009,6 @@ Slots cluster_slots(int num_sms) {
 // Examples: 512 x 4096 x 7168 (gated) runs as 64 pairs of 128 columns, 24 us,
 // against 29 us with 256 columns and k in two parts; 300 x 256 x 7168 as 80
 // tiles of 64 columns and an eighth of k, 8.2 us, against 20 us unsplit.
-struct Cut {
-    int cg, bn, split;
-};
-
-// Shared memory for the other parts' sums.
-constexpr int kMaxReceived = 64 * 1024;
-
-int received_bytes(int bn, int split) { return (split - 1) * own_columns(bn, split) * 512; }
-
 // Clocks of one k block of a tile.
 double block_clocks(const Gemm &g, int cg, int bn, int received) {
     const int columns = bn / cg;
@@ -1082,6 +1105,23 @@ double choose_two(const Gemm *g, int num_sms, int *bn) {
     return least;
 }
 
+// Expert groups, whose sizes only the device knows.  If there can be at most two
+// tiles an SM (a tile per group, and one for each 128 rows), single CTAs in
+// clusters of 4, or 8 if the most tiles leave room for that many parts of k: the
+// device then cuts k as far as the tiles that there are leave units idle.
+// One token, 2 of 8 experts of 1536 x 4096 (gated): 15.2 us, 20.9 by pairs
+// without parts; 13 tokens, 8 of 8 experts of 320 x 5400: 18.6 and 28.8; 300
+// tokens, 1 of 8 experts of 512 x 1024: 9.6 and 10.7.  Otherwise pairs, which
+// read half of B each and have no SM left over (36 clusters of 4 fill 144 of
+// 152): 1000 tokens, 8 of 64 experts of 512 x 2048: 57 us, 70 by clusters.
+Cut choose_groups(const Gemm &g, const Slots &slots_of) {
+    const int64_t groups = g.E < g.N ? g.E : g.N;
+    const int64_t most = ceil_div(static_cast<int64_t>(g.M) * (g.gated ? 2 : 1), 128) *
+                         (groups + g.N / 128);
+    if (most > 2 * slots_of.n[0]) return {2, kMaxBn, 1};
+    return {1, 128, most <= slots_of.n[3] ? 8 : 4};
+}
+
 bool can_copy(const Gemm &g) {
     return aligned16(g.a) && aligned16(g.b) && (g.a_mn ? g.M : g.K) % 8 == 0 &&
            g.b_pitch % 8 == 0 && encoder();
@@ -1143,23 +1183,24 @@ bool describe(const Gemm &g, const Cut &cut, TcPlan *plan, CUtensorMap *map) {
 bool launch_gemm_tc(const Gemm &g, const BiasSum &bias, int num_sms, cudaStream_t stream,
                     cudaError_t *err) {
     if (!can_copy(g)) return false;
-    // Expert groups, whose sizes only the device knows, run on pairs; their
-    // column counts follow from the row counts there.
-    Cut cut = {2, 0, 1};
     double price;
-    if (!g.E)
-        cut = choose_cut(g, static_cast<int64_t>(g.M) * (g.gated ? 2 : 1), cluster_slots(num_sms),
-                         &price);
+    const Slots slots_of = cluster_slots(num_sms);
+    const Cut cut = g.E ? choose_groups(g, slots_of)
+                        : choose_cut(g, static_cast<int64_t>(g.M) * (g.gated ? 2 : 1), slots_of,
+                                     &price);
     Work<1> work;
     work.g[0] = g;
     work.tiles0 = 0;
     work.bias = bias;
     if (!describe(g, cut, &work.p[0], work.map[0])) return false;
     const TcPlan &p = work.p[0];
-    const int64_t units = g.E ? INT32_MAX
-                              : static_cast<int64_t>(p.m_tiles) * p.n_tiles << p.log_split;
+    int64_t units = static_cast<int64_t>(p.m_tiles) * p.n_tiles << p.log_split;
     const int64_t slots = num_sms / cut.cg;
-    const int64_t grid = cut.cg * (p.log_split > 0 || units < slots ? units : slots);
+    if (g.E)        // as many clusters as can run at once: the device shares the tiles out
+        units = static_cast<int64_t>(slots_of.n[p.log_split + cut.cg - 1]) << p.log_split;
+    else if (p.log_split == 0 && units > slots)
+        units = slots;
+    const int64_t grid = cut.cg * units;
     if (cut.cg == 2)
         *err = g.gated ? start<2, true>(work, grid, stream) : start<2, false>(work, grid, stream);
     else

@@ -347,6 +347,51 @@ def test_experts_all_rows_in_one_expert_and_none_at_all(cuda_lib, kind):
     check_experts(cuda_lib, 300, 2, 6, 16, 128, 64, "silu", False, kind)
 
 
+@pytest.mark.parametrize("T,K,E,tile,H,I", [(1, 2, 128, 1, 3016, 256), (13, 8, 8, 128, 5400, 320),
+                                            (5, 1, 3, 4, 4096, 72), (1, 1, 1, 1, 7168, 64),
+                                            (2, 4, 8, 1, 2048, 1000), (90, 4, 16, 64, 3000, 184),
+                                            (200, 1, 2, 1, 4104, 136), (3, 3, 7, 16, 2056, 2000)])
+@pytest.mark.parametrize("kind", ["all", "holes", "one"])
+def test_experts_with_few_tiles_and_long_sums(cuda_lib, T, K, E, tile, H, I, kind):
+    check_experts(cuda_lib, T, K, E, tile, H, I, "gelu", True, kind)
+
+
+def test_experts_graph_replays_where_the_split_differs(cuda_lib):
+    """One captured call on routings from one group to many: equal to the eager
+    call's bits, and the same again."""
+    T, E, H, I = 24, 16, 4096, 264
+    x, w = rand(5, T, H), rand(6, E, 2 * I, H, scale=0.02)
+    wd = rand(7, E, 1000, I, scale=0.05)
+    ids = ids_of(1, T, 1, E, "all").cuda()
+    h = torch.zeros(cuda_lib.permute_rows(T, 1, E, 1), I, dtype=BF16, device="cuda")
+    y = torch.zeros(h.shape[0], 1000, dtype=BF16, device="cuda")
+
+    def step():
+        m = cuda_lib.permute_tokens(ids, E, 1)
+        cuda_lib.expert_gated_ffn(x, m["row_token"], m["offsets"], m["counts"], w, out=h)
+        cuda_lib.expert_linear(h, m["offsets"], m["counts"], wd, out=y)
+        return m
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m = step()
+    for groups in (1, 2, 3, 5, 11, 16, 4, 1):
+        ids.copy_((torch.arange(T, device="cuda") % groups).int()[:, None])
+        h.zero_()
+        step()
+        want = h.clone(), y.clone()
+        for _ in range(3):
+            h.zero_()
+            y.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(h, want[0]) and torch.equal(y, want[1]), groups
+        rows = slice(int(m["offsets"][0]), int(m["offsets"][0]) + int(m["counts"][0]))
+        R.check({"out": h[rows]}, R.gated(x[m["row_token"][rows].long()], w[0]), f"{groups}")
+
+
 def test_experts_at_the_most_experts(cuda_lib):
     check_experts(cuda_lib, 700, 2, 1024, 2, 64, 24, "silu", True, "holes")
 
