@@ -89,6 +89,27 @@ cudaError_t launch_permute(const int32_t *ids, int T, int K, int E, int tile, in
 #ifdef __CUDACC__
 namespace {
 
+// Phi(z), the standard normal distribution function, within 5e-6 of its size
+// wherever that is above 1e-30, and exp(-z^2 / 2) in *bell.  Phi(-u) exp(u^2 / 2)
+// is smooth and bounded on u >= 0; a polynomial of degree 7 in t = 1 / (1 + 0.35
+// u), fitted for the least relative error up to u = 14 (3.1e-7), takes its place.
+// The upper half is 1 - Phi(-u).  One quotient and one exponential: 20 million
+// GELUs in a product's epilogue took 31 us more than none with erfcf.
+__device__ __forceinline__ float normal_cdf(float z, float *bell) {
+    const float t = __fdividef(1.f, 1.f + 0.35f * fabsf(z));
+    float q = 0.04894243553f;
+    q = q * t - 0.2021192462f;
+    q = q * t + 0.2406407595f;
+    q = q * t - 0.01702339575f;
+    q = q * t + 0.1559614688f;
+    q = q * t + 0.1333550960f;
+    q = q * t + 0.1402703375f;
+    q = q * t - 2.731550558e-5f;
+    *bell = __expf(-0.5f * z * z);
+    q *= *bell;
+    return z < 0.f ? q : 1.f - q;
+}
+
 // The activations in the forms that lose nothing to cancellation: z / (1 +
 // exp(-q)) stays accurate relative to its size where 1 + tanh or 1 + erf
 // would cancel.  __fdividef gives 0 for denominators above 2^126, where the
@@ -96,7 +117,10 @@ namespace {
 __device__ __forceinline__ float act_value(float z, int act) {
     switch (act) {
         case MOEF_ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
-        case MOEF_ACT_GELU: return 0.5f * z * erfcf(-0.70710678f * z);
+        case MOEF_ACT_GELU: {
+            float bell;
+            return z * normal_cdf(z, &bell);
+        }
         case MOEF_ACT_GELU_TANH:
             return __fdividef(z, 1.f + __expf(-1.59576912f * (z + 0.044715f * z * z * z)));
         case MOEF_ACT_RELU: return z > 0.f || z != z ? z : 0.f;
@@ -122,9 +146,10 @@ __device__ __forceinline__ float act_grad(float z, int act, float *value) {
             return s * (1.f + z * (1.f - s));
         }
         case MOEF_ACT_GELU: {
-            const float phi = 0.5f * erfcf(-0.70710678f * z);
+            float bell;
+            const float phi = normal_cdf(z, &bell);
             *value = z * phi;
-            return phi + 0.39894228f * z * __expf(-0.5f * z * z);
+            return phi + 0.39894228f * z * bell;
         }
         case MOEF_ACT_GELU_TANH: {
             const float s = __fdividef(1.f, 1.f + __expf(-1.59576912f *

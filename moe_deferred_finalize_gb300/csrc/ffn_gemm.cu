@@ -12,8 +12,10 @@
 // the widest tile take.  Gathered rows are copied four to an instruction, so B
 // then has six warps (64 experts of 4096 x 1536, 32768 rows: 1681 us with one
 // warp, 659 with four, 589 with six).  One lane of a further warp issues the MMAs
-// into TMEM, and eight warps finish tiles.  The accumulator is double buffered (2
-// x 256 TMEM columns), so a tile's epilogue runs under the next tile's products.
+// into TMEM, and eight warps finish tiles, twelve when the gathering ones are free
+// (4096 x 4864 x 64, bound by its epilogue: 16.5 us with eight, 14.5 with twelve;
+// with a residual 29.8 and 25.1).  The accumulator is double buffered (2 x 256
+// TMEM columns), so a tile's epilogue runs under the next tile's products.
 //
 // Gated form: the A tile interleaves gate and up rows (g0, u0, g1, u1, ...),
 // which one 4-D tensor map [E][I][2][H] of the weights does in the copy.  A
@@ -43,8 +45,8 @@
 namespace moef {
 namespace {
 
-constexpr int kEpilogueWarps = 8;
-constexpr int kCopyWarp = 2 + kEpilogueWarps;    // copies B; warp 0 copies A
+constexpr int kCopyWarp = 10;                   // copies B; warp 0 copies A
+constexpr int kBiasWarp = kCopyWarp + 1;        // sums bias gradients
 constexpr int kGatherWarps = 6;                 // copy B from kCopyWarp on when rows are gathered
 constexpr int kGatherLanes = (32 + kGatherWarps - 1) / kGatherWarps;   // of each; 4 rows a lane
 constexpr int kTcThreads = 32 * (kCopyWarp + kGatherWarps);
@@ -291,22 +293,22 @@ __device__ __noinline__ void finish_scalar(const Gemm &g, int m, int64_t n, floa
 
 constexpr int kChunk = 16;      // columns a warp finishes at a time
 
-// A warp's part of one tile: its 32 lanes (rows of A), every other chunk of the
-// columns [begin, end).  Made before the accumulator is waited for, so that the
+// A warp's part of one tile: its 32 lanes (rows of A), every second or third chunk
+// (one for each of the `sides` warps of these lanes) of the columns [begin, end).  Made before the accumulator is waited for, so that the
 // bias and the first chunk's residual are there by then.
 template <bool GATED>
 struct TilePart {
     const Finish<GATED> f;
     const Tile t;
-    int lane, quarter, first, own, begin, end;
+    int lane, quarter, first, stride, own, begin, end;
     uint32_t next[GATED ? 1 : kChunk / 2];      // residual pairs of the next chunk
 
     __device__ __forceinline__ TilePart(const Gemm &g, const Tile &tile, int m_cta, int warp_quarter,
-                                        int side, int warp_lane, int from, int to)
+                                        int side, int sides, int warp_lane, int from, int to)
         : f(g, m_cta + (GATED ? warp_quarter * 16 + (warp_lane >> 2) * 2
                               : warp_quarter * 32 + (warp_lane & ~1)), tile.e),
           t(tile), lane(warp_lane), quarter(warp_quarter), first(from + kChunk * side),
-          own(to - from), begin(from),
+          stride(kChunk * sides), own(to - from), begin(from),
           end(min(to, (tile.count + kChunk - 1) / kChunk * kChunk)) {
         if (first < end) load_residual(first);
     }
@@ -342,7 +344,7 @@ __device__ __forceinline__ void finish_tile(TilePart<GATED> &part, uint32_t tmem
     const Gemm &g = f.g;
     const Tile &t = part.t;
     const int lane = part.lane, own = part.own, begin = part.begin, end = part.end;
-    const int quarter = part.quarter;
+    const int quarter = part.quarter, stride = part.stride;
     const bool odd = lane & 1, upper = lane & 2;
     const int64_t M = g.M;
     if (part.first >= end) {            // nothing for this warp
@@ -350,12 +352,12 @@ __device__ __forceinline__ void finish_tile(TilePart<GATED> &part, uint32_t tmem
         return;
     }
 #pragma unroll 1
-    for (int c0 = part.first; c0 < end; c0 += 2 * kChunk) {
+    for (int c0 = part.first; c0 < end; c0 += stride) {
         const int64_t row = t.row0 + c0 + part.column();
         const int left = part.left(c0);
         uint32_t r[kChunk];
         tmem_load16(tmem + c0, r);
-        if (done && c0 + 2 * kChunk >= end) {       // the accumulator has been read
+        if (done && c0 + stride >= end) {       // the accumulator has been read
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(done);
@@ -365,7 +367,7 @@ __device__ __forceinline__ void finish_tile(TilePart<GATED> &part, uint32_t tmem
 #pragma unroll
             for (int k = 0; k < kChunk / 2; ++k) res[k] = part.next[k];
         }
-        if (c0 + 2 * kChunk < end) part.load_residual(c0 + 2 * kChunk);
+        if (c0 + stride < end) part.load_residual(c0 + stride);
         for (int k = 0; k < parts; ++k) {
             const float *from = sums + (k * own + c0 - begin) * 128 + quarter * 32 + lane;
 #pragma unroll
@@ -480,9 +482,10 @@ __host__ __device__ __forceinline__ int received_bytes(int bn, int split) {
 
 template <int CG>
 __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint32_t buf, int split,
-                                             int part, int rank0, int quarter, int side, int lane) {
+                                             int part, int rank0, int quarter, int side, int sides,
+                                             int lane) {
     const int own = own_columns(t.bn, split);
-    for (int c0 = kChunk * side; c0 < t.count; c0 += 2 * kChunk) {
+    for (int c0 = kChunk * side; c0 < t.count; c0 += kChunk * sides) {
         const int owner = c0 / own;
         if (owner == part) continue;
         uint32_t r[kChunk];
@@ -562,6 +565,13 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     const bool leader = half == 0;
     const uint16_t pair = static_cast<uint16_t>(3 << lead);
     volatile int *gave_up = &h->gave_up;
+    // the warps that finish tiles, two for each quarter of the lanes, or three with
+    // those that have no rows to gather: a warp may read the TMEM lanes of its
+    // number modulo 4
+    const bool gathers = N == 1 && work.p[0].gather;
+    const int sides = gathers ? 2 : 3, quarter = warp & 3;
+    const int side = warp >= 2 && warp < kCopyWarp ? (warp - 2) >> 2
+                     : !gathers && warp > kBiasWarp ? 2 : -1;
     // expert groups: the tiles follow from what the previous kernels wrote
     const bool grouped = N == 1 && work.g[0].E;
 
@@ -576,7 +586,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_addr(&h->acc_full[i]), 1);
-            bar_init(smem_addr(&h->acc_empty[i]), kEpilogueWarps * CG);
+            bar_init(smem_addr(&h->acc_empty[i]), 4 * sides * CG);
         }
         h->gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -697,11 +707,11 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 for (const long long begin = clock64(); clock64() - begin < 2000000;)
                     __nanosleep(1000);
         }
-    } else if (warp >= kCopyWarp) {
+    } else if (warp >= kCopyWarp && side < 0) {
         // ---- copies of B: one lane, or some of each warp when rows are gathered
         int s = 0;
         uint32_t phase = 1;
-        if (N == 1 && work.p[0].gather) {
+        if (gathers) {
             const Gemm &g = work.g[0];
             int kb0, kb1;
             k_range(0, &kb0, &kb1);
@@ -734,12 +744,10 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 if (!ok) break;
             }
         } else if (warp > kCopyWarp) {
-            // the bias gradient, 32 columns a warp
+            // the bias gradient, 32 columns a CTA
             if (work.bias.dbias) {
                 wait_previous_kernel();
-                constexpr int kWarps = kGatherWarps - 1;
-                for (int c = (blockIdx.x * kWarps + warp - kCopyWarp - 1) * 32;
-                     c < work.bias.cols; c += gridDim.x * kWarps * 32)
+                for (int c = blockIdx.x * 32; c < work.bias.cols; c += gridDim.x * 32)
                     sum_columns(work.bias, c + lane);
             }
         } else if (elect_one()) {
@@ -829,8 +837,6 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         }
     } else {
         // ---- epilogue
-        const int quarter = warp & 3;               // the TMEM lanes a warp may read
-        const int side = (warp - 2) >> 2;
         int n = 0;
         for (int ti = first_tile; ti < tiles; ti += step, ++n) {
             const int q = product_of(ti);
@@ -844,8 +850,8 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 fence_after();
                 break;
             }
-            TilePart<GATED> part_of(work.g[q], t, t.m0 + half * m_cta_rows, quarter, side, lane, 0,
-                                    t.bn);
+            TilePart<GATED> part_of(work.g[q], t, t.m0 + half * m_cta_rows, quarter, side, sides,
+                                    lane, 0, t.bn);
             const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             fence_after();
@@ -856,18 +862,16 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     }
     __syncwarp();
     if (N == 1 && split > 1) {
-        const bool works = warp >= 2 && warp < kCopyWarp;
-        const int quarter = warp & 3, side = (warp - 2) >> 2;
         const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         if (CG == 1) cluster_wait();        // every part has started
-        if (works && first_tile < tiles) {
+        if (side >= 0 && first_tile < tiles) {
             const Tile t = tile_of(first_tile, 0);
             if (!*gave_up)
                 send_columns<CG>(t, acc, received, split, part, (unit - part) * CG + half, quarter,
-                                 side, lane);
+                                 side, sides, lane);
             const int own = own_columns(t.bn, split);
-            TilePart<GATED> part_of(work.g[0], t, t.m0 + half * m_cta_rows, quarter, side, lane,
-                                    part * own, (part + 1) * own);
+            TilePart<GATED> part_of(work.g[0], t, t.m0 + half * m_cta_rows, quarter, side, sides,
+                                    lane, part * own, (part + 1) * own);
             cluster_sync();         // every part's sums have arrived
             if (!*gave_up)
                 finish_tile<GATED>(part_of, acc, 0,
