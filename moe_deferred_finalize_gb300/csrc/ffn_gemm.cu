@@ -1013,10 +1013,15 @@ struct Cut {
 // Examples: 512 x 4096 x 7168 (gated) runs as 64 pairs of 128 columns, 24 us,
 // against 29 us with 256 columns and k in two parts; 300 x 256 x 7168 as 80
 // tiles of 64 columns and an eighth of k, 8.2 us, against 20 us unsplit.
+// Bytes of a CTA's k block of both operands.
+int block_bytes(const Gemm &g, int cg, int bn) {
+    const int columns = bn / cg;
+    return kATile + (g.b_mn ? (columns + 63) / 64 * 64 : columns) * 128;
+}
+
 // Clocks of one k block of a tile.
 double block_clocks(const Gemm &g, int cg, int bn, int received) {
-    const int columns = bn / cg;
-    const int bytes = kATile + (g.b_mn ? (columns + 63) / 64 * 64 : columns) * 128;
+    const int bytes = block_bytes(g, cg, bn);
     const double copies = bytes / (cg == 1 ? 80.0 : 72.0);
     const double latency = 2000.0 / ((kStageArea - received) / bytes);
     const double mma = (cg == 1 ? 2.7 : 2.35) * bn;
@@ -1074,19 +1079,30 @@ Cut choose_cut(const Gemm &g, int64_t a_rows, const Slots &slots_of, double *pri
 
 // The same for two products in one launch, on pairs without k in parts: the
 // tiles go round the pairs one by one, the first product's before the second's.
+// The stages are as large as the larger product's; a product with one tile of
+// columns shares no operand between its tiles and waits for HBM, 4000 clocks, in
+// the fewer stages (12 x 4736 x 5192: both gradients 42 us in one launch, 33 in
+// two).
 double choose_two(const Gemm *g, int num_sms, int *bn) {
     const int pairs = num_sms / 2;
+    auto product_clocks = [](const Gemm &p, int columns, int bytes) {
+        const double latency = (p.N <= columns ? 4000.0 : 2000.0) / (kStageArea / bytes);
+        const double clocks = block_clocks(p, 2, columns, 0);
+        return ceil_div(p.K, kBlockK) * (latency > clocks ? latency : clocks);
+    };
     double least = 1e300;
     for (int a = 64; a <= kMaxBn; a += 32) {
         const int bn0 = even_columns(g[0], 2, a);
-        const double time0 = ceil_div(g[0].K, kBlockK) * block_clocks(g[0], 2, bn0, 0);
+        const int bytes0 = block_bytes(g[0], 2, bn0);
         const double tail0 = epilogue_clocks(bn0);
-        const double unit0 = 300.0 + (time0 > tail0 ? time0 : tail0);
         const int64_t n0 = ceil_div(g[0].M, 256) * ceil_div(g[0].N, bn0);
         for (int b = 64; b <= kMaxBn; b += 32) {
             const int bn1 = even_columns(g[1], 2, b);
-            const double time1 = ceil_div(g[1].K, kBlockK) * block_clocks(g[1], 2, bn1, 0);
+            const int bytes1 = block_bytes(g[1], 2, bn1), bytes = bytes0 > bytes1 ? bytes0 : bytes1;
+            const double time0 = product_clocks(g[0], bn0, bytes);
+            const double time1 = product_clocks(g[1], bn1, bytes);
             const double tail1 = epilogue_clocks(bn1);
+            const double unit0 = 300.0 + (time0 > tail0 ? time0 : tail0);
             const double unit1 = 300.0 + (time1 > tail1 ? time1 : tail1);
             const int64_t n1 = ceil_div(g[1].M, 256) * ceil_div(g[1].N, bn1);
             // the pairs at the ends of the last rounds have the most to do
