@@ -17,10 +17,12 @@
 // with a residual 29.8 and 25.1).  The accumulator is double buffered (2 x 256
 // TMEM columns), so a tile's epilogue runs under the next tile's products.
 //
-// Gated form: the A tile interleaves gate and up rows (g0, u0, g1, u1, ...),
-// which one 4-D tensor map [E][I][2][H] of the weights does in the copy.  A
-// gate and its up value then sit in neighbouring TMEM lanes, and two shuffles
-// a pair of columns bring them into one thread.
+// Gated form: the A tile interleaves gate and up rows, which one tensor map of
+// the weights does in the copy: eight of each in turn ([E][I / 8][2][8][H]), so
+// that a gate and its up value come into one thread's fragments.  Where the
+// number of features is not a multiple of 8, or an output is not 16-byte
+// aligned, the rows alternate one by one ([E][I][2][H]), and two shuffles a pair
+// of columns bring the values together.
 //
 // The two gradients of a layer are independent and often fill the last round of
 // tiles badly; they run as one launch over both products' tiles when that is
@@ -37,6 +39,8 @@
 // into its shared memory, and it adds them in rank order (equal calls give
 // equal bits).  Expert groups choose the split on the device, where the number
 // of tiles is known: a cluster's units share one tile's k, or take tiles alone.
+#include <stddef.h>
+
 #include "ffn.cuh"
 #include "host.cuh"
 #include "tc.cuh"
@@ -55,6 +59,8 @@ constexpr int kATile = 128 * kBlockK * 2;       // bytes of A per CTA and stage
 constexpr int kMaxBn = 256;
 constexpr int kMaxStages = 16;
 constexpr int kHeader = 13 * 1024;              // barriers, tables
+constexpr int kStash = 1024;                    // bytes of each epilogue warp
+constexpr int kStashes = 12 * kStash;           // over the tables when there are no groups
 constexpr int kSmemBytes = 227 * 1024;
 constexpr int kStageArea = kSmemBytes - kHeader - 1024;     // after rounding up to 1024
 constexpr int kBand = 8;                        // feature tiles per band (see tile_at)
@@ -69,6 +75,7 @@ struct TcPlan {
     int gather;         // B rows are fetched by row_token
     int box_rows;       // rows of one B copy (k-contiguous B)
     int wide_rows;      // of one copy through the third map, while that many are left (0: none)
+    int vectors;        // rows of the output are whole, aligned 16-byte pieces
 };
 
 // One launch: a product, or two that share the SMs (the gradients of a layer):
@@ -92,7 +99,8 @@ struct Header {
     // expert groups: column tiles before each, first row, rows
     int prefix[MOEF_MAX_EXPERTS + 1], first[MOEF_MAX_EXPERTS], count[MOEF_MAX_EXPERTS];
 };
-static_assert(sizeof(Header) <= kHeader, "header region");
+static_assert(sizeof(Header) <= kHeader && offsetof(Header, prefix) <= kHeader - kStashes,
+              "header region");
 
 __device__ unsigned int lost_waits;
 
@@ -331,6 +339,10 @@ struct TilePart {
     }
 };
 
+// Where the sums of k's other parts have TMEM lane `lane` of column c: neither
+// lanes by columns (the sender, and finish_tile) nor fragments meet in a bank.
+__device__ __forceinline__ int sum_lane(int lane, int c) { return lane ^ ((c >> 1 & 3) << 3); }
+
 // The part out of TMEM; arrives on `done` (0: nowhere) once it has read its
 // columns.  parts > 0: so many other parts' sums of these columns are in
 // `sums`.  Lanes swap values so that each holds two adjacent features of one
@@ -369,10 +381,10 @@ __device__ __forceinline__ void finish_tile(TilePart<GATED> &part, uint32_t tmem
         }
         if (c0 + stride < end) part.load_residual(c0 + stride);
         for (int k = 0; k < parts; ++k) {
-            const float *from = sums + (k * own + c0 - begin) * 128 + quarter * 32 + lane;
+            const float *from = sums + (k * own + c0 - begin) * 128 + quarter * 32;
 #pragma unroll
             for (int c = 0; c < kChunk; ++c)
-                r[c] = __float_as_uint(__uint_as_float(r[c]) + from[c * 128]);
+                r[c] = __float_as_uint(__uint_as_float(r[c]) + from[c * 128 + sum_lane(lane, c)]);
         }
         if constexpr (GATED) {
             float gate[kChunk / 2], up[kChunk / 2];     // [2k], [2k + 1]: features f, f + 1,
@@ -466,6 +478,205 @@ __device__ __forceinline__ void finish_tile(TilePart<GATED> &part, uint32_t tmem
     }
 }
 
+// The same where rows are whole 16-byte pieces, which is nearly always.  The
+// chunk comes as fragments of 8 x 8 matrices, is finished as it is, packed in
+// pairs of columns, and transposed through the warp's stash into 16-byte pieces of
+// rows: a third of the instructions, which is what the other form is bound by
+// (4096 x 4864 x 64: 14.5 us there, 11.2 here; gated 13.7 and 10.6).
+template <bool GATED, bool RESIDUAL>
+struct WidePart {
+    const Gemm &g;
+    const Tile t;
+    int lane, quarter, first, stride, own, begin, end, m;
+    float bias[4];                      // of the features this thread has (gated: gate, up, ...)
+    uint4 next[RESIDUAL ? 2 : 1];       // residual pieces of the next chunk
+    static constexpr int kPieces = GATED ? 2 : 4;       // of a row
+
+    __device__ __forceinline__ WidePart(const Gemm &gemm, const Tile &tile, int m_cta,
+                                        int warp_quarter, int side, int sides, int warp_lane,
+                                        int from, int to)
+        : g(gemm), t(tile), lane(warp_lane), quarter(warp_quarter), first(from + kChunk * side),
+          stride(kChunk * sides), own(to - from), begin(from),
+          end(min(to, (tile.count + kChunk - 1) / kChunk * kChunk)),
+          m(m_cta + warp_quarter * 8 * kPieces) {
+        const uint16_t *b = g.bias + static_cast<int64_t>(t.e) * (GATED ? 2 : 1) * g.M;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int feature = m + 8 * (GATED ? i >> 1 : i) + (lane >> 2);
+            bias[i] = g.bias && feature < g.M
+                          ? bf16_value(b, GATED && (i & 1) ? g.M + feature : feature) : 0.f;
+        }
+        if (first < end) load_residual(first);
+    }
+    // this thread's piece p of a chunk: its token, or -1 where there is none
+    __device__ __forceinline__ int token(int p, int c0) const {
+        const int n = 8 * p + lane / kPieces;
+        return c0 + n < t.count && m + 8 * (lane % kPieces) < g.M ? n : -1;
+    }
+    __device__ __forceinline__ int64_t at(int c0, int n, int64_t pitch) const {
+        return (t.row0 + c0 + n) * pitch + m + 8 * (lane % kPieces);
+    }
+    __device__ __forceinline__ void load_residual(int c0) {
+        if constexpr (RESIDUAL) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int n = token(p, c0);
+                next[p] = make_uint4(0, 0, 0, 0);
+                if (n >= 0)
+                    next[p] = *reinterpret_cast<const uint4 *>(g.residual + at(c0, n, g.M));
+            }
+        }
+    }
+    // stash offsets: row (token) and piece of matrix lane / 8, row lane % 8, and of
+    // this thread's piece; swizzled so that eight rows, or pieces, meet no bank
+    __device__ __forceinline__ uint32_t matrix_at(int u) const {
+        if constexpr (GATED) {
+            const int i = lane >> 3, row = 8 * (i >> 1) + (lane & 7);
+            return row * 32 + (((i & 1) ^ (row >> 2 & 1)) << 4);
+        } else {
+            const int row = lane & 7;
+            return u * 512 + row * 64 + (((lane >> 3) ^ (row >> 1)) << 4);
+        }
+    }
+    __device__ __forceinline__ uint32_t piece_at(int p) const {
+        if constexpr (GATED) return (lane >> 1) * 32 + (((lane & 1) ^ (lane >> 3 & 1)) << 4);
+        else return p * 512 + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3)) << 4);
+    }
+};
+
+// A chunk of bf16 pairs (w[j][i]: columns 8 j .., features 8 i ..) to rows of p.
+template <bool GATED, bool RESIDUAL>
+__device__ __forceinline__ void store_chunk(const WidePart<GATED, RESIDUAL> &part, uint32_t stash,
+                                            const uint32_t (&w)[2][GATED ? 2 : 4], int c0,
+                                            uint16_t *p, int64_t pitch) {
+    __syncwarp();               // the stash has been read
+    if constexpr (GATED) {
+        store_transposed(stash + part.matrix_at(0), w[0][0], w[0][1], w[1][0], w[1][1]);
+    } else {
+        store_transposed(stash + part.matrix_at(0), w[0][0], w[0][1], w[0][2], w[0][3]);
+        store_transposed(stash + part.matrix_at(1), w[1][0], w[1][1], w[1][2], w[1][3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < (GATED ? 1 : 2); ++k) {
+        const uint4 v = shared_load16(stash + part.piece_at(k));
+        const int n = part.token(k, c0);
+        if (n >= 0) *reinterpret_cast<uint4 *>(p + part.at(c0, n, pitch)) = v;
+    }
+}
+
+template <bool GATED, bool RESIDUAL>
+__device__ __forceinline__ void finish_wide(WidePart<GATED, RESIDUAL> &part, uint32_t stash, uint32_t tmem,
+                                            uint32_t done, const float *sums, int parts) {
+    const Gemm &g = part.g;
+    const int lane = part.lane, end = part.end, stride = part.stride;
+    if (part.first >= end) {            // nothing for this warp
+        if (done && lane == 0) bar_arrive(done);
+        return;
+    }
+#pragma unroll 1
+    for (int c0 = part.first; c0 < end; c0 += stride) {
+        uint32_t r[kChunk];
+        tmem_load_fragments(tmem + c0, r);
+        if (done && c0 + stride >= end) {       // the accumulator has been read
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(done);
+        }
+        uint32_t res[2][4];             // the residual, as fragments
+        if constexpr (RESIDUAL) {
+            __syncwarp();
+#pragma unroll
+            for (int p = 0; p < 2; ++p) shared_store16(stash + part.piece_at(p), part.next[p]);
+            if (c0 + stride < end) part.load_residual(c0 + stride);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) load_transposed(stash + part.matrix_at(j), res[j]);
+        }
+        float z[2][4][2];               // [columns 8 j ..][features 8 i .., gated: gate, up][pair]
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    z[j][i][e] = __uint_as_float(r[8 * (i >> 1) + 4 * j + 2 * (i & 1) + e]);
+        for (int k = 0; k < parts; ++k) {
+            const float *from = sums + (k * part.own + c0 - part.begin) * 128 + part.quarter * 32;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int c = 8 * j + 2 * (lane & 3) + e;
+                        z[j][i][e] += from[c * 128 + sum_lane(8 * i + (lane >> 2), c)];
+                    }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) z[j][i][e] += part.bias[i];
+        if constexpr (GATED) {
+            uint32_t w[2][2];
+            if (g.preact) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            w[j][i] = pack_bf16x2(z[j][2 * i + h][0], z[j][2 * i + h][1]);
+                    store_chunk(part, stash, w, c0,
+                                      g.preact + static_cast<int64_t>(h) * g.M,
+                                      2 * static_cast<int64_t>(g.M));
+                }
+            }
+            float a[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a[k] = z[k >> 2][k & 2][k & 1];
+            act_all(a, g.act);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    w[j][i] = pack_bf16x2(a[4 * j + 2 * i] * z[j][2 * i + 1][0],
+                                          a[4 * j + 2 * i + 1] * z[j][2 * i + 1][1]);
+            store_chunk(part, stash, w, c0, static_cast<uint16_t *>(g.out), g.M);
+        } else {
+            uint32_t w[2][4];
+            if (g.preact) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[j][i] = pack_bf16x2(z[j][i][0], z[j][i][1]);
+                store_chunk(part, stash, w, c0, g.preact, g.M);
+            }
+            float a[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) a[k] = z[k >> 3][k >> 1 & 3][k & 1];
+            act_all(a, g.act);
+            if constexpr (RESIDUAL) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        a[8 * j + 2 * i] += bf16_lo(res[j][i]);
+                        a[8 * j + 2 * i + 1] += bf16_hi(res[j][i]);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[j][i] = pack_bf16x2(a[8 * j + 2 * i], a[8 * j + 2 * i + 1]);
+            store_chunk(part, stash, w, c0, static_cast<uint16_t *>(g.out), g.M);
+        }
+    }
+}
+
 // k in parts: the columns of a tile are shared out over the parts, kChunk at a
 // time, and each part sends its sums of the others' columns into their shared
 // memory, [sender][column][128 rows of A].
@@ -492,10 +703,10 @@ __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint3
         tmem_load16(tmem + c0, r);
         const int slot = part < owner ? part : part - 1;
         const uint32_t at = map_rank(
-            buf + ((slot * own + c0 - owner * own) * 128 + quarter * 32 + lane) * 4,
-            rank0 + owner * CG);
+            buf + ((slot * own + c0 - owner * own) * 128 + quarter * 32) * 4, rank0 + owner * CG);
 #pragma unroll
-        for (int c = 0; c < kChunk; ++c) store_remote(at + c * 512, r[c]);
+        for (int c = 0; c < kChunk; ++c)
+            store_remote(at + (c * 128 + sum_lane(lane, c)) * 4, r[c]);
     }
 }
 
@@ -625,7 +836,9 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
             bn_max = max(bn_max, work.p[1].bn);
         }
     }
-    const uint32_t received = base + kHeader;       // the other parts' sums
+    // the epilogue warps' stashes, the other parts' sums, the stages
+    const uint32_t stash = base + kHeader - (grouped ? 0 : kStashes) + (4 * side + quarter) * kStash;
+    const uint32_t received = base + kHeader + (grouped ? kStashes : 0);
     const uint32_t stage0 = received + bytes_received;
     const int split = 1 << log_split, part = unit & (split - 1);
     const int bnc_max = bn_max / CG;                // B rows per CTA
@@ -634,7 +847,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     const uint32_t b_bytes = (any_mn ? (bnc_max + 63) / 64 * 64 : bnc_max) * kBlockK * 2;
     const uint32_t stage_bytes = kATile + b_bytes;
     const int stages = min(static_cast<unsigned>(kMaxStages),
-                           (kStageArea - (stage0 - received)) / stage_bytes);
+                           (base + kHeader + kStageArea - stage0) / stage_bytes);
     const int first_tile = (blockIdx.x / CG) >> log_split;
     const int step = (gridDim.x / CG) >> log_split;     // k in parts: at least as many as tiles
     const int m_cta_rows = GATED ? 64 : 128;        // features per CTA
@@ -692,6 +905,10 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                     ok = blocks_of([&](uint32_t a, int k, uint32_t bar) {
                         tma_2d<CG>(a, map, m0, k, bar);
                         tma_2d<CG>(a + 8192, map, m0 + 64, k, bar);
+                    });
+                else if (GATED && p.vectors)
+                    ok = blocks_of([&](uint32_t a, int k, uint32_t bar) {
+                        tma_5d<CG>(a, map, k, 0, 0, m0 >> 3, t.e, bar);
                     });
                 else
                     ok = blocks_of([&](uint32_t a, int k, uint32_t bar) {
@@ -850,14 +1067,33 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 fence_after();
                 break;
             }
-            TilePart<GATED> part_of(work.g[q], t, t.m0 + half * m_cta_rows, quarter, side, sides,
-                                    lane, 0, t.bn);
-            const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            fence_after();
-            const uint32_t bar = smem_addr(&h->acc_empty[n & 1]);
-            finish_tile<GATED>(part_of, acc, map_rank(bar, CG == 2 ? lead : cluster_rank()),
-                               nullptr, 0);
+            const uint32_t done = map_rank(smem_addr(&h->acc_empty[n & 1]),
+                                           CG == 2 ? lead : cluster_rank());
+            auto finish = [&](auto &part_of, auto out_of_tmem) {
+                const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
+                if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+                fence_after();
+                out_of_tmem(part_of);
+                return true;
+            };
+            const int m0 = t.m0 + half * m_cta_rows;
+            bool ok;
+            auto wide = [&](auto &w) { finish_wide(w, stash, acc, done, nullptr, 0); };
+            if (work.p[q].vectors && !GATED && work.g[q].residual) {
+                WidePart<GATED, !GATED> part_of(work.g[q], t, m0, quarter, side, sides, lane, 0,
+                                                t.bn);
+                ok = finish(part_of, wide);
+            } else if (work.p[q].vectors) {
+                WidePart<GATED, false> part_of(work.g[q], t, m0, quarter, side, sides, lane, 0,
+                                               t.bn);
+                ok = finish(part_of, wide);
+            } else {
+                TilePart<GATED> part_of(work.g[q], t, m0, quarter, side, sides, lane, 0, t.bn);
+                ok = finish(part_of, [&](auto &w) {
+                    finish_tile<GATED>(w, acc, done, nullptr, 0);
+                });
+            }
+            if (!ok) break;
         }
     }
     __syncwarp();
@@ -870,14 +1106,25 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 send_columns<CG>(t, acc, received, split, part, (unit - part) * CG + half, quarter,
                                  side, sides, lane);
             const int own = own_columns(t.bn, split);
-            TilePart<GATED> part_of(work.g[0], t, t.m0 + half * m_cta_rows, quarter, side, sides,
-                                    lane, part * own, (part + 1) * own);
-            cluster_sync();         // every part's sums have arrived
-            if (!*gave_up)
-                finish_tile<GATED>(part_of, acc, 0,
-                                   reinterpret_cast<const float *>(smem + (received -
-                                                                           smem_addr(smem))),
-                                   split - 1);
+            const float *sums = reinterpret_cast<const float *>(smem + (received -
+                                                                        smem_addr(smem)));
+            const int m0 = t.m0 + half * m_cta_rows, from = part * own;
+            if (work.p[0].vectors && !GATED && work.g[0].residual) {
+                WidePart<GATED, !GATED> part_of(work.g[0], t, m0, quarter, side, sides, lane, from,
+                                                from + own);
+                cluster_sync();         // every part's sums have arrived
+                if (!*gave_up) finish_wide(part_of, stash, acc, 0, sums, split - 1);
+            } else if (work.p[0].vectors) {
+                WidePart<GATED, false> part_of(work.g[0], t, m0, quarter, side, sides, lane, from,
+                                               from + own);
+                cluster_sync();
+                if (!*gave_up) finish_wide(part_of, stash, acc, 0, sums, split - 1);
+            } else {
+                TilePart<GATED> part_of(work.g[0], t, m0, quarter, side, sides, lane, from,
+                                        from + own);
+                cluster_sync();
+                if (!*gave_up) finish_tile<GATED>(part_of, acc, 0, sums, split - 1);
+            }
         } else {
             cluster_sync();
         }
@@ -1030,7 +1277,7 @@ double block_clocks(const Gemm &g, int cg, int bn, int received) {
     return latency > clocks ? latency : clocks;
 }
 
-double epilogue_clocks(int bn) { return 1200.0 + 20.0 * bn; }
+double epilogue_clocks(int bn) { return 800.0 + 13.0 * bn; }
 
 // Tiles of at most `most` columns, evened out.
 int even_columns(const Gemm &g, int cg, int most) {
@@ -1154,6 +1401,8 @@ bool describe(const Gemm &g, const Cut &cut, TcPlan *plan, CUtensorMap *map) {
     const int rows_per_feature = g.gated ? 2 : 1;
     const int64_t a_rows = static_cast<int64_t>(g.M) * rows_per_feature;
     p.gather = g.row_token != nullptr;
+    p.vectors = g.M % 8 == 0 && !g.out_f32 && aligned16(g.out) && aligned16(g.residual) &&
+                aligned16(g.preact);
     while (1 << p.log_split < cut.split) ++p.log_split;
     p.received = received_bytes(cut.bn, cut.split);
     p.bn = cut.bn;
@@ -1170,6 +1419,15 @@ bool describe(const Gemm &g, const Cut &cut, TcPlan *plan, CUtensorMap *map) {
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.M) * 2};
         const cuuint32_t box[2] = {64, 64};
         ok = encode(&map[0], g.a, 2, dims, strides, box);
+    } else if (g.gated && p.vectors) {
+        // [E][M / 8][gate, up][8][K]
+        const cuuint64_t row = static_cast<cuuint64_t>(g.K) * 2;
+        const cuuint64_t dims[5] = {static_cast<cuuint64_t>(g.K), 8, 2,
+                                    static_cast<cuuint64_t>(g.M / 8),
+                                    static_cast<cuuint64_t>(g.E ? g.E : 1)};
+        const cuuint64_t strides[4] = {row, row * g.M, row * 8, row * a_rows};
+        const cuuint32_t box[5] = {kBlockK, 8, 2, 8, 1};
+        ok = encode(&map[0], g.a, 5, dims, strides, box);
     } else {
         // [E][M][gate, up][K]: a copy of (k, both, features) interleaves the rows
         const cuuint64_t row = static_cast<cuuint64_t>(g.K) * 2;
