@@ -51,7 +51,8 @@ def test_linear_epilogue(cuda_lib, name, T, N, K):
                         f"{name} bias={bias is not None} res={res is not None} {dt}")
 
 
-@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 15, 16, 17, 31, 33, 63, 65, 127, 128, 129, 192, 257, 1025])
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 15, 16, 17, 31, 33, 63, 65, 127, 128, 129, 192, 257,
+                               1025])
 def test_linear_every_row_count_class(cuda_lib, T):
     x, w = rand(7, T, 320), rand(8, 392, 320, scale=0.05)
     R.check(cuda_lib.linear(x, w), R.linear(x, w), f"T={T}")
@@ -390,6 +391,40 @@ def test_experts_graph_replays_where_the_split_differs(cuda_lib):
             assert torch.equal(h, want[0]) and torch.equal(y, want[1]), groups
         rows = slice(int(m["offsets"][0]), int(m["offsets"][0]) + int(m["counts"][0]))
         R.check({"out": h[rows]}, R.gated(x[m["row_token"][rows].long()], w[0]), f"{groups}")
+
+
+@pytest.mark.parametrize("offset", [0, 1, 4])
+@pytest.mark.parametrize("T,K,N", [(3, 4096, 264), (40, 2048, 264), (70, 512, 136),
+                                   (300, 128, 1032)])
+def test_outputs_at_any_offset(cuda_lib, T, K, N, offset):
+    """Aligned operands, outputs (and residual) of an allocation at 0, 2 and 8
+    bytes: the same values, nothing written around them."""
+    def view(rows, cols, fill):
+        flat = torch.full((rows * cols + offset + 8,), fill, dtype=BF16, device="cuda")
+        return flat, flat[offset:offset + rows * cols].view(rows, cols)
+
+    def untouched(flat, rows, cols):
+        return (flat[:offset] == 9).all() and (flat[offset + rows * cols:] == 9).all()
+
+    x, w, b, r = rand(8, T, K), rand(9, 2 * N, K, scale=0.03), rand(10, 2 * N), rand(11, T, N)
+    res = view(T, N, 9.0)[1].copy_(r)
+    (of, out), (pf, pre) = view(T, N, 9.0), view(T, N, 9.0)
+    cuda_lib.linear(x, w[:N], bias=b[:N], residual=res, activation="silu", out=out, preact=pre)
+    R.check({"out": out, "preact": pre}, R.linear(x, w[:N], b[:N], r, "silu"), "linear")
+    assert untouched(of, T, N) and untouched(pf, T, N)
+    (of, out), (pf, pre) = view(T, N, 9.0), view(T, 2 * N, 9.0)
+    cuda_lib.gated_ffn(x, w, bias=b, out=out, preact=pre)
+    R.check({"out": out, "preact": pre}, R.gated(x, w, b), "gated")
+    assert untouched(of, T, N) and untouched(pf, T, 2 * N)
+    m = cuda_lib.permute_tokens(torch.arange(T, dtype=torch.int32, device="cuda")[:, None] % 2, 2)
+    of, out = view(T, N, 9.0)
+    cuda_lib.expert_gated_ffn(x, m["row_token"], m["offsets"], m["counts"],
+                              torch.stack([w, w.flip(0)]), out=out)
+    rows = m["row_token"].long()
+    split = int(m["offsets"][1])
+    R.check({"out": out[:split]}, R.gated(x[rows[:split]], w), "expert 0")
+    R.check({"out": out[split:]}, R.gated(x[rows[split:]], w.flip(0)), "expert 1")
+    assert untouched(of, T, N)
 
 
 def test_experts_at_the_most_experts(cuda_lib):
