@@ -26,7 +26,7 @@
 //
 // The two gradients of a layer are independent and often fill the last round of
 // tiles badly; they run as one launch over both products' tiles when that is
-// priced lower (2040 x 4096 x 4096 with its dz pass: 108 us apart, 97 together).
+// priced lower (746 x 2512 x 4968: 43 us apart, 36.5 together).
 //
 // Two launch forms:
 //   CG = 2  pairs of CTAs share tiles of 256 (m) x up to 256 (n): each CTA
@@ -1248,11 +1248,10 @@ struct Cut {
 // per tile, parts of k.  Every choice is priced in SM clocks and the cheapest
 // taken.  The figures are fits to sweeps over 17..4096 rows:
 //   - a 64-deep k block takes the MMAs (2.7 clocks a column, 2.35 on a pair,
-//     which reads half of B), the copies (80
-//     bytes a clock into a single SM, 72 into each of a pair), the issue of
-//     both (290 clocks) or the latency of a copy (2000) shared by the stages
-//     in flight, whichever is longest;
-//   - a tile costs 300 clocks more, and its epilogue 1200 and 20 a column, under
+//     which reads half of B), the copies (80 bytes a clock into a single SM, 72
+//     into each of a pair), the issue of both (290 clocks) or the latency of a
+//     copy (2000) shared by the stages in flight, whichever is longest;
+//   - a tile costs 300 clocks more, and its epilogue 800 and 13 a column, under
 //     the next tile's products except for the last one; joining k's parts 2500
 //     (pairs 4500), 300 a part and 30 a column; pairs 1800 for their barriers;
 //   - HBM delivers 3580 bytes a clock; the shorter of its time and the SMs'
@@ -1260,6 +1259,7 @@ struct Cut {
 // Examples: 512 x 4096 x 7168 (gated) runs as 64 pairs of 128 columns, 24 us,
 // against 29 us with 256 columns and k in two parts; 300 x 256 x 7168 as 80
 // tiles of 64 columns and an eighth of k, 8.2 us, against 20 us unsplit.
+
 // Bytes of a CTA's k block of both operands.
 int block_bytes(const Gemm &g, int cg, int bn) {
     const int columns = bn / cg;
