@@ -89,14 +89,42 @@ cudaError_t launch_permute(const int32_t *ids, int T, int K, int E, int tile, in
 #ifdef __CUDACC__
 namespace {
 
+// 2^x and 1 / x as one instruction each, results below the normal range as 0,
+// which the activations multiply into an error below 1e-35.  (__expf and
+// __fdividef spend three or four instructions more on that range; the issue of
+// instructions is what activations cost: 20 million SiLUs 6 us, now 5.)
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.44269504f;
+
+// 1 / (1 + exp(-z)).
+__device__ __forceinline__ float sigmoid(float z) {
+    return reciprocal_ftz(1.f + exp2_ftz(-kLog2e * z));
+}
+
+// sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)): (1 + tanh) / 2 of GELU's tanh form.
+__device__ __forceinline__ float sigmoid_cubic(float z) {
+    const float c = -1.59576912f * kLog2e;
+    return reciprocal_ftz(1.f + exp2_ftz(z * (c + 0.044715f * c * (z * z))));
+}
+
 // Phi(z), the standard normal distribution function, within 5e-6 of its size
 // wherever that is above 1e-30, and exp(-z^2 / 2) in *bell.  Phi(-u) exp(u^2 / 2)
 // is smooth and bounded on u >= 0; a polynomial of degree 7 in t = 1 / (1 + 0.35
 // u), fitted for the least relative error up to u = 14 (3.1e-7), takes its place.
-// The upper half is 1 - Phi(-u).  One quotient and one exponential: 20 million
-// GELUs in a product's epilogue took 31 us more than none with erfcf.
+// The upper half is 1 - Phi(-u).  20 million GELUs in a product's epilogue took
+// 31 us with erfcf, 10 so.
 __device__ __forceinline__ float normal_cdf(float z, float *bell) {
-    const float t = __fdividef(1.f, 1.f + 0.35f * fabsf(z));
+    const float t = reciprocal_ftz(1.f + 0.35f * fabsf(z));
     float q = 0.04894243553f;
     q = q * t - 0.2021192462f;
     q = q * t + 0.2406407595f;
@@ -105,24 +133,21 @@ __device__ __forceinline__ float normal_cdf(float z, float *bell) {
     q = q * t + 0.1333550960f;
     q = q * t + 0.1402703375f;
     q = q * t - 2.731550558e-5f;
-    *bell = __expf(-0.5f * z * z);
+    *bell = exp2_ftz(-0.5f * kLog2e * (z * z));
     q *= *bell;
     return z < 0.f ? q : 1.f - q;
 }
 
-// The activations in the forms that lose nothing to cancellation: z / (1 +
-// exp(-q)) stays accurate relative to its size where 1 + tanh or 1 + erf
-// would cancel.  __fdividef gives 0 for denominators above 2^126, where the
-// quotient has left the normal range of bf16 and fp32 or is about to.
+// The activations in the forms that lose nothing to cancellation: z sigmoid(q)
+// stays accurate relative to its size where 1 + tanh or 1 + erf would cancel.
 __device__ __forceinline__ float act_value(float z, int act) {
     switch (act) {
-        case MOEF_ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
+        case MOEF_ACT_SILU: return z * sigmoid(z);
         case MOEF_ACT_GELU: {
             float bell;
             return z * normal_cdf(z, &bell);
         }
-        case MOEF_ACT_GELU_TANH:
-            return __fdividef(z, 1.f + __expf(-1.59576912f * (z + 0.044715f * z * z * z)));
+        case MOEF_ACT_GELU_TANH: return z * sigmoid_cubic(z);
         case MOEF_ACT_RELU: return z > 0.f || z != z ? z : 0.f;
         default: return z;
     }
@@ -141,7 +166,7 @@ __device__ __forceinline__ void sum_columns(const BiasSum &b, int c) {
 __device__ __forceinline__ float act_grad(float z, int act, float *value) {
     switch (act) {
         case MOEF_ACT_SILU: {
-            const float s = __fdividef(1.f, 1.f + __expf(-z));
+            const float s = sigmoid(z);
             *value = z * s;
             return s * (1.f + z * (1.f - s));
         }
@@ -152,8 +177,7 @@ __device__ __forceinline__ float act_grad(float z, int act, float *value) {
             return phi + 0.39894228f * z * bell;
         }
         case MOEF_ACT_GELU_TANH: {
-            const float s = __fdividef(1.f, 1.f + __expf(-1.59576912f *
-                                                         (z + 0.044715f * z * z * z)));
+            const float s = sigmoid_cubic(z);
             *value = z * s;
             const float d = s * (1.f - s);      // 0 far out, where z * z may overflow
             return d == 0.f ? s : s + d * z * 1.59576912f * (1.f + 0.134145f * z * z);
