@@ -507,6 +507,14 @@ struct WidePart {
                           ? bf16_value(b, GATED && (i & 1) ? g.M + feature : feature) : 0.f;
         }
         if (first < end) load_residual(first);
+        // the other chunks into L2, a row a lane (4096 x 4864 x 64: 24.7 -> 22.8 us)
+        if constexpr (RESIDUAL) {
+            const int row = lane & 15;
+            if (m < g.M)
+                for (int c0 = first + (lane < 16 ? 1 : 2) * stride; c0 < end; c0 += 2 * stride)
+                    if (c0 + row < t.count)
+                        prefetch_l2(g.residual + (t.row0 + c0 + row) * g.M + m);
+        }
     }
     // this thread's piece p of a chunk: its token, or -1 where there is none
     __device__ __forceinline__ int token(int p, int c0) const {
