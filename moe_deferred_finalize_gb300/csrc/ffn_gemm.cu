@@ -308,8 +308,9 @@ __device__ __noinline__ void finish_scalar(const Gemm &g, int m, int64_t n, floa
 constexpr int kChunk = 16;      // columns a warp finishes at a time
 
 // A warp's part of one tile: its 32 lanes (rows of A), every second or third chunk
-// (one for each of the `sides` warps of these lanes) of the columns [begin, end).  Made before the accumulator is waited for, so that the
-// bias and the first chunk's residual are there by then.
+// (one for each of the `sides` warps of these lanes) of the columns [begin, end).
+// Made before the accumulator is waited for, so that the bias and the first
+// chunk's residual are there by then.
 template <bool GATED>
 struct TilePart {
     const Finish<GATED> f;
@@ -580,8 +581,9 @@ __device__ __forceinline__ void store_chunk(const WidePart<GATED, RESIDUAL> &par
 }
 
 template <bool GATED, bool RESIDUAL>
-__device__ __forceinline__ void finish_wide(WidePart<GATED, RESIDUAL> &part, uint32_t stash, uint32_t tmem,
-                                            uint32_t done, const float *sums, int parts) {
+__device__ __forceinline__ void finish_wide(WidePart<GATED, RESIDUAL> &part, uint32_t stash,
+                                            uint32_t tmem, uint32_t done, const float *sums,
+                                            int parts) {
     const Gemm &g = part.g;
     const int lane = part.lane, end = part.end, stride = part.stride;
     if (part.first >= end) {            // nothing for this warp
@@ -851,7 +853,8 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         }
     }
     // the epilogue warps' stashes, the other parts' sums, the stages
-    const uint32_t stash = base + kHeader - (grouped ? 0 : kStashes) + (4 * side + quarter) * kStash;
+    const uint32_t stash = base + kHeader - (grouped ? 0 : kStashes) +
+                           (4 * side + quarter) * kStash;
     const uint32_t received = base + kHeader + (grouped ? kStashes : 0);
     const uint32_t stage0 = received + bytes_received;
     const int split = 1 << log_split, part = unit & (split - 1);
