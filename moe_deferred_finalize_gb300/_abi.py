@@ -166,6 +166,39 @@ def _stream(stream, device) -> int:
     return int(stream)
 
 
+def _elsewhere(stream, device) -> bool:
+    """Whether ``stream`` is another one than ``device``'s current stream."""
+    return device is not None and device.type == "cuda" and \
+        _stream(stream, None) != _stream(None, device)
+
+
+def _device(t):
+    return t.device if isinstance(t, torch.Tensor) else None
+
+
+def _under(fn, device, args):
+    """fn(**args) on args["stream"], a stream of ``device`` that is not its
+    current one, for a call that allocates.  The allocator hands a block out
+    again in the order of the stream it was allocated on, so what the call
+    allocates is allocated on the stream its kernels run on: a workspace, freed
+    on return, is not given to the current stream while they use it, and no
+    block is taken that work on the current stream still uses.  Returned tensors
+    are marked as used on the current stream too, so that a caller there may drop
+    them at any time."""
+    stream = args.pop("stream")
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream, None), device=device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected one on {device}")
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        res = fn(**args)
+    for t in res.values() if isinstance(res, dict) else res if isinstance(res, tuple) else (res,):
+        if t is not None:
+            t.record_stream(current)
+    return res
+
+
 _EX_ADDRESS = None
 
 

@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from . import _abi
-from ._abi import MoefError, _check, _on, _ptr, _stream
+from ._abi import MoefError, _check, _device, _elsewhere, _on, _ptr, _stream, _under
 
 ACTIVATION = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
 
@@ -142,7 +142,11 @@ def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor
     dict with "out" [T, N] (``out_dtype`` bfloat16 or float32; a given bf16
     ``out`` may be the residual) and, with ``save_preact`` or a given
     ``preact``, "preact" bf16 [T, N] (x weight^T + bias, for
-    ``linear_backward``).  Enqueued on the current stream (or ``stream``)."""
+    ``linear_backward``).  Enqueued on the current stream (or ``stream``, on
+    which what the call allocates is then allocated too)."""
+    if stream is not None and (out is None or save_preact and preact is None) and \
+            _elsewhere(stream, _device(x)):
+        return _under(linear, x.device, dict(locals()))
     res = _fast_linear(x, weight, bias, residual, activation, out, out_dtype, save_preact,
                        preact, stream)
     if res is not None:
@@ -343,6 +347,11 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *
     what the forward call saved, needed unless the activation is "none".
     The gradient of the residual is ``dout`` itself.  ``workspace``: at least
     ``linear_backward_workspace_bytes`` bytes, allocated when not given."""
+    if stream is not None and (workspace is None or want_dx and dx is None or
+                               want_dweight and dweight is None or
+                               want_dbias and dbias is None) and \
+            _elsewhere(stream, _device(dout)):
+        return _under(linear_backward, dout.device, dict(locals()))
     return _backward("moe_linear_backward", False, dout, x, weight, preact, activation, want_dx,
                      want_dweight, want_dbias, dx, dweight, dbias, workspace, stream)
 
@@ -357,6 +366,9 @@ def gated_ffn(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Ten
     rows; bias bf16 [2I].  Returns a dict with "out" bf16 [T, I] and, with
     ``save_preact`` or a given ``preact``, "preact" bf16 [T, 2I] (both
     projections with their bias, for ``gated_ffn_backward``)."""
+    if stream is not None and (out is None or save_preact and preact is None) and \
+            _elsewhere(stream, _device(x)):
+        return _under(gated_ffn, x.device, dict(locals()))
     res = _fast_gated(x, weight, bias, activation, out, save_preact, preact, stream)
     if res is not None:
         return res
@@ -398,6 +410,11 @@ def gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
     bf16 [T, 2I]: the requested of "dx" bf16 [T, H], "dweight" bf16 [2I, H]
     and "dbias" bf16 [2I].  ``workspace``: at least
     ``gated_ffn_backward_workspace_bytes`` bytes, allocated when not given."""
+    if stream is not None and (workspace is None or want_dx and dx is None or
+                               want_dweight and dweight is None or
+                               want_dbias and dbias is None) and \
+            _elsewhere(stream, _device(dout)):
+        return _under(gated_ffn_backward, dout.device, dict(locals()))
     return _backward("moe_gated_ffn_backward", True, dout, x, weight, preact, activation,
                      want_dx, want_dweight, want_dbias, dx, dweight, dbias, workspace, stream)
 
@@ -466,6 +483,10 @@ def permute_tokens(expert_ids: torch.Tensor, E: int, tile: int = 1, *,
     "offsets" int32 [E + 1] and "counts" int32 [E].  Ids outside [0, E) get
     no row: idx_map is -1 there, which ``moe_finalize`` must not be given
     (leave such tokens out of its T; ``check_indices`` counts them)."""
+    if stream is not None and \
+            (row_token is None or idx_map is None or offsets is None or counts is None or
+             workspace is None) and _elsewhere(stream, _device(expert_ids)):
+        return _under(permute_tokens, expert_ids.device, dict(locals()))
     res = _fast_permute(expert_ids, E, tile, row_token, idx_map, offsets, counts, workspace,
                         stream)
     if res is not None:
@@ -565,6 +586,8 @@ def expert_gated_ffn(x: torch.Tensor, row_token: Optional[torch.Tensor], offsets
     [E] as from ``permute_tokens``; weight bf16 [E, 2I, H]; bias bf16 [E, 2I].
     Rows of no expert are left as they were (unset when ``out`` is allocated
     here)."""
+    if stream is not None and out is None and _elsewhere(stream, _device(x)):
+        return _under(expert_gated_ffn, x.device, dict(locals()))
     return _expert("moe_expert_gated_ffn", True, x, row_token, offsets, counts, weight, bias,
                    activation, out, stream)
 
@@ -577,6 +600,8 @@ def expert_linear(x: torch.Tensor, offsets: torch.Tensor, counts: torch.Tensor,
     [P, N], the ``permuted_out`` of ``moe_finalize``.  x bf16 [P, K] in the
     layout itself, or [T, K] with ``row_token``; weight bf16 [E, N, K]; bias
     bf16 [E, N].  Otherwise as ``expert_gated_ffn``."""
+    if stream is not None and out is None and _elsewhere(stream, _device(x)):
+        return _under(expert_linear, x.device, dict(locals()))
     return _expert("moe_expert_linear", False, x, row_token, offsets, counts, weight, bias,
                    activation, out, stream)
 

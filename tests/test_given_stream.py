@@ -1,0 +1,208 @@
+"""Calls on a given stream (``stream=``) that allocate: what they allocate
+belongs to that stream, so that neither a workspace freed on return nor a
+recycled block is shared with work on the current stream."""
+import pytest
+import torch
+
+import ffn_ref as R
+
+BF16 = torch.bfloat16
+CURRENT, OTHER = 0x70, 0x90     # stream handles
+
+
+class Entered(Exception):
+    """The given stream was made the current one."""
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on cuda:0."""
+    device = property(lambda self: torch.device("cuda", 0))
+
+
+def fake(*shape, dtype=BF16):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnDevice)
+
+
+@pytest.fixture
+def entry_points(monkeypatch):
+    """The package with streams that only tell whether they were entered."""
+    import moe_deferred_finalize_gb300 as mf
+    from moe_deferred_finalize_gb300 import _abi, build
+    build.build_library()
+
+    def enter(stream):
+        raise Entered(stream)
+
+    monkeypatch.setattr(_abi, "_RAW_STREAM", lambda index: CURRENT)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    monkeypatch.setattr(torch.cuda, "stream", enter)
+    return mf
+
+
+def i32(*shape):
+    return fake(*shape, dtype=torch.int32)
+
+
+# name, required arguments, all that the call would allocate
+PRODUCTS = [
+    ("linear", lambda: (fake(4, 8), fake(8, 8)),
+     dict(out=(4, 8), preact=(4, 8)), dict(save_preact=True)),
+    ("linear_backward", lambda: (fake(4, 8), fake(4, 8), fake(8, 8)),
+     dict(dx=(4, 8), dweight=(8, 8), dbias=(8,), workspace=(4096,)), dict(want_dbias=True)),
+    ("gated_ffn", lambda: (fake(4, 8), fake(16, 8)),
+     dict(out=(4, 8), preact=(4, 16)), dict(save_preact=True)),
+    ("gated_ffn_backward", lambda: (fake(4, 8), fake(4, 8), fake(16, 8), fake(4, 16)),
+     dict(dx=(4, 8), dweight=(16, 8), dbias=(16,), workspace=(4096,)), dict(want_dbias=True)),
+    ("permute_tokens", lambda: (i32(4, 2), 8),
+     dict(row_token=(8,), idx_map=(4, 2), offsets=(9,), counts=(8,), workspace=(4096,)), {}),
+    ("expert_gated_ffn", lambda: (fake(4, 8), i32(4), i32(3), i32(2), fake(2, 16, 8)),
+     dict(out=(4, 8)), {}),
+    ("expert_linear", lambda: (fake(4, 8), i32(3), i32(2), fake(2, 8, 8)), dict(out=(4, 8)), {}),
+]
+
+
+@pytest.mark.parametrize("name,args,outputs,options", PRODUCTS, ids=[p[0] for p in PRODUCTS])
+def test_allocations_belong_to_the_given_stream(entry_points, name, args, outputs, options):
+    fn, a = getattr(entry_points, name), args()
+    integers = name == "permute_tokens"
+    given = {k: fake(*s, dtype=torch.int32 if integers else BF16) for k, s in outputs.items()}
+    with pytest.raises(Entered) as e:
+        fn(*a, **options, stream=OTHER)
+    assert e.value.args == ((OTHER, torch.device("cuda", 0)),)
+    for missing in given:
+        some = {k: v for k, v in given.items() if k != missing}
+        with pytest.raises(Entered):
+            fn(*a, **options, **some, stream=OTHER)
+    # nothing to allocate, or the current stream: straight on to the checks,
+    # which find that these tensors are not on a GPU
+    for kw in (dict(given, stream=OTHER), dict(stream=CURRENT), {}):
+        with pytest.raises(Exception) as e:
+            fn(*a, **options, **kw)
+        assert e.type is not Entered
+
+
+def test_a_stream_of_another_device_is_refused(entry_points, monkeypatch):
+    class Stream:
+        cuda_stream, device = OTHER, torch.device("cuda", 1)
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    with pytest.raises(ValueError, match="cuda:1"):
+        entry_points.linear(fake(4, 8), fake(8, 8), stream=Stream())
+
+
+# ----------------------------------------------------------------- on a GPU
+
+
+def rand(seed, *shape, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.empty(shape, dtype=BF16, device="cuda").normal_(0.0, scale, generator=g)
+
+
+def busy(stream):
+    """Some 25 ms of work on the stream."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(50_000_000)
+
+
+def handles(stream):
+    return [stream, stream.cuda_stream]
+
+
+def fill_like(nbytes, value):
+    """The current stream takes and fills whatever block of that size is free."""
+    return [torch.full((nbytes,), value, dtype=torch.uint8, device="cuda") for _ in range(6)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("is_gated", [False, True])
+def test_backward_workspace_is_not_shared(cuda_lib, is_gated):
+    T, n, K = 600, 256, 128
+    cols = 2 * n if is_gated else n
+    x, w, d, pre = rand(1, T, K), rand(2, cols, K, scale=0.1), rand(3, T, n), rand(4, T, cols)
+    ref = R.backward(d, x, w, pre, "gelu", is_gated)
+    if is_gated:
+        nbytes = cuda_lib.gated_ffn_backward_workspace_bytes(T, n)
+    else:
+        nbytes = cuda_lib.linear_backward_workspace_bytes(T, n)
+    side = torch.cuda.Stream()
+    for stream in handles(side):
+        torch.cuda.synchronize()
+        busy(side)
+        if is_gated:
+            got = cuda_lib.gated_ffn_backward(d, x, w, pre, activation="gelu", want_dbias=True,
+                                              stream=stream)
+        else:
+            got = cuda_lib.linear_backward(d, x, w, activation="gelu", preact=pre,
+                                           want_dbias=True, stream=stream)
+        kept = fill_like(nbytes, 0x41)          # bf16 12.06, were it read as dz
+        torch.cuda.synchronize()
+        R.check(got, ref)
+        del kept
+
+
+@pytest.mark.gpu
+def test_row_map_workspace_is_not_shared(cuda_lib):
+    T, K, E, tile = 5000, 4, 32, 8              # 20000 slots: two kernels, counts between them
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    ids = torch.randint(-1, E, (T, K), dtype=torch.int32, device="cuda", generator=g)
+    want = cuda_lib.permute_tokens(ids, E, tile)
+    side = torch.cuda.Stream()
+    for stream in handles(side):
+        torch.cuda.synchronize()
+        busy(side)
+        got = cuda_lib.permute_tokens(ids, E, tile, stream=stream)
+        kept = fill_like(4096, 0) + fill_like(65536, 0)
+        torch.cuda.synchronize()
+        for key in want:
+            assert torch.equal(got[key], want[key]), key
+        del kept
+
+
+@pytest.mark.gpu
+def test_outputs_do_not_take_blocks_still_in_use(cuda_lib):
+    """A block freed by the host while the current stream has yet to read it
+    does not become an output of a call on another stream."""
+    T, n, K = 200, 512, 256
+    x, w, w2 = rand(6, T, K), rand(7, n, K, scale=0.06), rand(8, 2 * n, K, scale=0.06)
+    we, offsets = w.view(1, n, K), torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([T], dtype=torch.int32, device="cuda")
+    side, current = torch.cuda.Stream(), torch.cuda.current_stream()
+    calls = [lambda s: cuda_lib.linear(x, w, save_preact=True, stream=s),
+             lambda s: cuda_lib.gated_ffn(x, w2, stream=s),
+             lambda s: {"out": cuda_lib.expert_linear(x, offsets, counts, we, stream=s)}]
+    for call in calls:
+        want = call(None)
+        for stream in handles(side):
+            old = [torch.full((T, n), 3.0, dtype=BF16, device="cuda") for _ in range(8)]
+            read = torch.empty(8, T, n, dtype=BF16, device="cuda")
+            torch.cuda.synchronize()
+            busy(current)
+            torch.stack(old, out=read)
+            del old
+            got = call(stream)
+            torch.cuda.synchronize()
+            assert (read == 3).all()
+            for key in want:
+                assert torch.equal(got[key], want[key])
+
+
+@pytest.mark.gpu
+def test_results_may_be_dropped_while_the_current_stream_reads_them(cuda_lib):
+    x, w = rand(9, 200, 256), rand(10, 512, 256, scale=0.06)
+    side, current = torch.cuda.Stream(), torch.cuda.current_stream()
+    want = cuda_lib.linear(x, w)["out"]
+    for stream in handles(side):
+        torch.cuda.synchronize()
+        got = cuda_lib.linear(x, w, stream=stream)["out"]
+        current.wait_stream(side)
+        busy(current)
+        copy = got * 1.0
+        del got
+        with torch.cuda.stream(side):
+            kept = fill_like(want.numel() * 2, 0x41)
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want)
+        del kept
