@@ -176,6 +176,13 @@ def _device(t):
     return t.device if isinstance(t, torch.Tensor) else None
 
 
+def _missing(residual, out, residual_out, norm_out, write_out):
+    """Whether a finalize with these arguments allocates an output."""
+    if residual is None:
+        return out is None
+    return residual_out is None or norm_out is None or write_out and out is None
+
+
 def _under(fn, device, args):
     """fn(**args) on args["stream"], a stream of ``device`` that is not its
     current one, for a call that allocates.  The allocator hands a block out
@@ -186,6 +193,8 @@ def _under(fn, device, args):
     are marked as used on the current stream too, so that a caller there may drop
     them at any time."""
     stream = args.pop("stream")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream(stream, None), device=device)
     elif stream.device != device:
@@ -193,7 +202,9 @@ def _under(fn, device, args):
     current = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
         res = fn(**args)
-    for t in res.values() if isinstance(res, dict) else res if isinstance(res, tuple) else (res,):
+    made = res.outputs if isinstance(res, BoundFinalize) else res
+    for t in made.values() if isinstance(made, dict) else \
+            made if isinstance(made, tuple) else (made,):
         if t is not None:
             t.record_stream(current)
     return res
@@ -321,11 +332,15 @@ def moe_finalize(permuted_out: torch.Tensor, idx_map: torch.Tensor, weights: tor
     residual bf16 [T, H] with gamma bf16 [H].  Outputs are allocated when not
     given; with a residual, ``write_out=False`` skips ``out``.  Returns a dict
     with "out" and, with a residual, "residual_out" and "norm_out".
-    Enqueued on the current stream (or ``stream``); nothing is synchronised.
+    Enqueued on the current stream (or ``stream``, on which what the call
+    allocates is then allocated too); nothing is synchronised.
     ``routing_ready``: idx_map and weights were complete before the previous
     kernel on the stream started (MOEF_FLAG_ROUTING_READY).  ``pdl=False``:
     launch as a plain stream-ordered kernel (MOEF_FLAG_NO_PDL).
     """
+    if stream is not None and _missing(residual, out, residual_out, norm_out, write_out) and \
+            _elsewhere(stream, _device(permuted_out)):
+        return _under(moe_finalize, permuted_out.device, dict(locals()))
     res = _checked_fast(permuted_out, idx_map, weights, wkind, shared_out, routed_scale,
                         residual, gamma, eps, out, residual_out, norm_out, write_out, splits,
                         threads, (FLAG_ROUTING_READY if routing_ready else 0) |
@@ -418,6 +433,10 @@ def moe_finalize_unfused(permuted_out: torch.Tensor, idx_map: torch.Tensor,
     RMSNorm) with a bf16 intermediate in ``workspace`` (allocated when not
     given): the A/B baseline of the fused ``moe_finalize``.  Same arguments;
     ``out`` is always produced."""
+    if stream is not None and \
+            (workspace is None or _missing(residual, out, residual_out, norm_out, True)) and \
+            _elsewhere(stream, _device(permuted_out)):
+        return _under(moe_finalize_unfused, permuted_out.device, dict(locals()))
     args, res = _marshal(permuted_out, idx_map, weights, wkind, shared_out, routed_scale,
                          residual, gamma, eps, out, residual_out, norm_out, True, 0, 0)
     T, H = idx_map.shape[0], permuted_out.shape[1]
@@ -540,6 +559,9 @@ def bind(permuted_out: torch.Tensor, idx_map: torch.Tensor, weights: torch.Tenso
     """Check and marshal a finalize once (arguments as for ``moe_finalize``);
     the returned object enqueues it on ``stream`` (default: the current
     stream at bind time) each time it is called."""
+    if stream is not None and _missing(residual, out, residual_out, norm_out, write_out) and \
+            _elsewhere(stream, _device(permuted_out)):
+        return _under(bind, permuted_out.device, dict(locals()))
     args, res = _marshal(permuted_out, idx_map, weights, wkind, shared_out, routed_scale,
                          residual, gamma, eps, out, residual_out, norm_out, write_out, splits,
                          threads, routing_ready=routing_ready, pdl=pdl)
@@ -634,6 +656,12 @@ def moe_finalize_allreduce(ranks, wkind: str, *, routed_scale: float = 1.0,
     if not 1 <= R <= MAX_RANKS:
         raise ValueError(f"1 <= R <= {MAX_RANKS} ranks")
     dev = _call_device(device, residual, out, residual_out)
+    if stream is not None and _missing(residual, out, residual_out, norm_out, write_out) and \
+            _elsewhere(stream, dev):
+        return _under(moe_finalize_allreduce, dev, dict(
+            ranks=ranks, wkind=wkind, routed_scale=routed_scale, residual=residual, gamma=gamma,
+            eps=eps, out=out, residual_out=residual_out, norm_out=norm_out, write_out=write_out,
+            device=dev, stream=stream))
     x0, i0 = ranks[0]["permuted_out"], ranks[0]["idx_map"]
     if x0.dim() != 2 or i0.dim() != 2:
         raise ValueError("permuted_out is [P, H] and idx_map is [T, K]")
@@ -668,6 +696,8 @@ def moe_finalize_partial(permuted_out: torch.Tensor, idx_map: torch.Tensor,
     """Phase 1 of the two-phase all-reduce-fused finalize: this rank's
     unrounded partial (weighted rows + shared output) as fp32 [T, H]
     (allocated when not given).  Arguments as for ``moe_finalize``."""
+    if stream is not None and partial is None and _elsewhere(stream, _device(permuted_out)):
+        return _under(moe_finalize_partial, permuted_out.device, dict(locals()))
     if wkind not in WKIND:
         raise ValueError(f"wkind must be one of {sorted(WKIND)}")
     device = permuted_out.device
@@ -710,6 +740,12 @@ def moe_finalize_allreduce_reduce(partials, *, residual: Optional[torch.Tensor] 
     for r, t in enumerate(partials):
         _check_peer(t, f"partials[{r}]", (torch.float32,), (T, H))
     dev = _call_device(device, residual, out, residual_out)
+    if stream is not None and _missing(residual, out, residual_out, norm_out, write_out) and \
+            _elsewhere(stream, dev):
+        return _under(moe_finalize_allreduce_reduce, dev, dict(
+            partials=partials, residual=residual, gamma=gamma, eps=eps, out=out,
+            residual_out=residual_out, norm_out=norm_out, write_out=write_out, device=dev,
+            stream=stream))
     res = _epilogue(T, H, dev, residual, gamma, out, residual_out, norm_out, write_out, None)
     arr = (ctypes.c_void_p * R)(*[t.data_ptr() for t in partials])
     with _on(dev):
@@ -742,6 +778,8 @@ def topk_route(logits: torch.Tensor, K: int, kind: str = "sigmoid", *,
     """Top-K gate over fp32 logits [T, E] (see include/moe_finalize.h):
     returns the requested of "expert_ids" int32 [T, K], "weights" fp32
     [T, K] and "packed" int32 [T, K] words."""
+    if stream is not None and _elsewhere(stream, _device(logits)):
+        return _under(topk_route, logits.device, dict(locals()))
     if kind not in GATE:
         raise ValueError(f"kind must be one of {sorted(GATE)}")
     if logits.device.type != "cuda" or logits.dtype != torch.float32 or logits.dim() != 2 \
@@ -768,6 +806,8 @@ def topk_route(logits: torch.Tensor, K: int, kind: str = "sigmoid", *,
 def pack_topk_ids(expert_ids: torch.Tensor, weights: torch.Tensor,
                   packed: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """(expert_id << 16) | bf16_rne(weight) words, same shape as the inputs."""
+    if stream is not None and packed is None and _elsewhere(stream, _device(expert_ids)):
+        return _under(pack_topk_ids, expert_ids.device, dict(locals()))
     if not isinstance(expert_ids, torch.Tensor) or not expert_ids.is_cuda:
         raise ValueError("expert_ids must be a CUDA tensor")
     dev = expert_ids.device
@@ -787,6 +827,9 @@ def pack_topk_ids(expert_ids: torch.Tensor, weights: torch.Tensor,
 def unpack_topk_ids(packed: torch.Tensor, expert_ids: Optional[torch.Tensor] = None,
                     weights: Optional[torch.Tensor] = None, stream=None):
     """Packed int32 words -> (expert ids int32, weights float32), same shape."""
+    if stream is not None and (expert_ids is None or weights is None) and \
+            _elsewhere(stream, _device(packed)):
+        return _under(unpack_topk_ids, packed.device, dict(locals()))
     if packed.device.type != "cuda" or packed.dtype != torch.int32 or not packed.is_contiguous():
         raise ValueError("packed must be a contiguous int32 CUDA tensor")
     device = packed.device
@@ -808,6 +851,8 @@ def check_indices(idx_map: torch.Tensor, P: int, counter: Optional[torch.Tensor]
                   stream=None) -> torch.Tensor:
     """Enqueue a count of idx_map entries outside [0, P); returns the device
     int32 [1] counter (read it after the stream has run)."""
+    if stream is not None and counter is None and _elsewhere(stream, _device(idx_map)):
+        return _under(check_indices, idx_map.device, dict(locals()))
     if idx_map.dim() != 2 or idx_map.dtype != torch.int32 or not idx_map.is_contiguous():
         raise ValueError("idx_map must be a contiguous int32 [T, K] tensor")
     device = idx_map.device

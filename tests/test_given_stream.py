@@ -27,12 +27,17 @@ def fake(*shape, dtype=BF16):
 def entry_points(monkeypatch):
     """The package with streams that only tell whether they were entered."""
     import moe_deferred_finalize_gb300 as mf
-    from moe_deferred_finalize_gb300 import _abi, build
-    build.build_library()
+    from moe_deferred_finalize_gb300 import _abi, _ffn
 
     def enter(stream):
         raise Entered(stream)
 
+    def library():
+        raise RuntimeError("these tensors must not reach the library")
+
+    monkeypatch.setattr(_abi, "_lib", library)
+    monkeypatch.setattr(_ffn, "_lib", library)
+    monkeypatch.setattr(_abi, "_FAST", None)
     monkeypatch.setattr(_abi, "_RAW_STREAM", lambda index: CURRENT)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
@@ -62,9 +67,53 @@ PRODUCTS = [
 ]
 
 
-@pytest.mark.parametrize("name,args,outputs,options", PRODUCTS, ids=[p[0] for p in PRODUCTS])
-def test_allocations_belong_to_the_given_stream(entry_points, name, args, outputs, options):
+def f32(*shape):
+    return fake(*shape, dtype=torch.float32)
+
+
+def finalize_args():
+    return fake(8, 8), i32(4, 2), f32(4, 2), "fp32", fake(4, 8)
+
+
+def norm():
+    return dict(residual=fake(4, 8), gamma=fake(8))
+
+
+def one_rank():
+    x, idx, w, _, shared = finalize_args()
+    return [dict(permuted_out=x, idx_map=idx, weights=w, shared_out=shared)], "fp32"
+
+
+NORM_OUTPUTS = dict(out=(4, 8), residual_out=(4, 8), norm_out=(4, 8))
+FINALIZE = [
+    ("moe_finalize", finalize_args, dict(out=(4, 8)), {}),
+    ("moe_finalize", finalize_args, NORM_OUTPUTS, norm),
+    ("moe_finalize_unfused", finalize_args, dict(out=(4, 8), workspace=(4096,)), {}),
+    ("bind", finalize_args, NORM_OUTPUTS, norm),
+    ("moe_finalize_partial", finalize_args, dict(partial=(4, 8)), {}),
+    ("moe_finalize_allreduce", one_rank, NORM_OUTPUTS, norm),
+    ("moe_finalize_allreduce_reduce", lambda: ([f32(4, 8)],), NORM_OUTPUTS, norm),
+    ("pack_topk_ids", lambda: (i32(4, 2), f32(4, 2)), dict(packed=(4, 2)), {}),
+    ("unpack_topk_ids", lambda: (i32(4, 2),), dict(expert_ids=(4, 2), weights=(4, 2)), {}),
+    ("check_indices", lambda: (i32(4, 2), 8), dict(counter=(1,)), {}),
+]
+
+
+def test_gate_outputs_belong_to_the_given_stream(entry_points):
+    with pytest.raises(Entered):
+        entry_points.topk_route(f32(4, 8), 2, stream=OTHER)
+
+
+@pytest.mark.parametrize("name,args,outputs,options", PRODUCTS + FINALIZE,
+                         ids=[p[0] for p in PRODUCTS + FINALIZE])
+def test_allocations_belong_to_the_given_stream(entry_points, monkeypatch, name, args, outputs,
+                                                options):
+    # some take their device from the outputs too, or the current one
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(OnDevice, "is_cuda", True, raising=False)
+    monkeypatch.setattr(OnDevice, "get_device", lambda self: 0, raising=False)
     fn, a = getattr(entry_points, name), args()
+    options = options() if callable(options) else options
     integers = name == "permute_tokens"
     given = {k: fake(*s, dtype=torch.int32 if integers else BF16) for k, s in outputs.items()}
     with pytest.raises(Entered) as e:
@@ -74,8 +123,8 @@ def test_allocations_belong_to_the_given_stream(entry_points, name, args, output
         some = {k: v for k, v in given.items() if k != missing}
         with pytest.raises(Entered):
             fn(*a, **options, **some, stream=OTHER)
-    # nothing to allocate, or the current stream: straight on to the checks,
-    # which find that these tensors are not on a GPU
+    # nothing to allocate, or the current stream: straight on to the checks
+    monkeypatch.setattr(OnDevice, "is_cuda", False)
     for kw in (dict(given, stream=OTHER), dict(stream=CURRENT), {}):
         with pytest.raises(Exception) as e:
             fn(*a, **options, **kw)
@@ -161,6 +210,71 @@ def test_row_map_workspace_is_not_shared(cuda_lib):
         del kept
 
 
+def finalize_case(T=128, K=2, H=4096, E=8):
+    """Arguments of moe_finalize: token t's slots are rows t K .. of x."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    idx = torch.randperm(T * K, device="cuda", generator=g).int().view(T, K)
+    return rand(12, T * K, H), idx, torch.rand(T, K, device="cuda", generator=g), "fp32", \
+        rand(13, T, H)
+
+
+@pytest.mark.gpu
+def test_unfused_workspace_is_not_shared(cuda_lib):
+    args = finalize_case()
+    T, H = args[4].shape
+    want = cuda_lib.moe_finalize_unfused(*args)["out"]
+    side = torch.cuda.Stream()
+    for stream in handles(side):
+        torch.cuda.synchronize()
+        busy(side)
+        got = cuda_lib.moe_finalize_unfused(*args, stream=stream)["out"]
+        kept = fill_like(cuda_lib.unfused_workspace_bytes(T, H), 0x41)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del kept
+
+
+@pytest.mark.gpu
+def test_every_call_on_another_stream_gives_the_same_bits(cuda_lib):
+    args = finalize_case()
+    x, idx, w, _, shared = args
+    res = dict(residual=rand(14, *shared.shape), gamma=rand(15, shared.shape[1]))
+    logits = torch.rand(40, 16, device="cuda")
+    ids = torch.randint(0, 16, (40, 2), dtype=torch.int32, device="cuda")
+    words = cuda_lib.pack_topk_ids(ids, w[:40].contiguous())
+    ranks = [dict(permuted_out=x, idx_map=idx, weights=w, shared_out=shared)] * 2
+    partial = cuda_lib.moe_finalize_partial(*args)
+    calls = [lambda **s: cuda_lib.moe_finalize(*args, **s),
+             lambda **s: cuda_lib.moe_finalize(*args, **res, write_out=False, **s),
+             lambda **s: cuda_lib.moe_finalize_unfused(*args, **res, **s),
+             lambda **s: cuda_lib.bind(*args, **res, **s)(),
+             lambda **s: cuda_lib.moe_finalize_partial(*args, **s),
+             lambda **s: cuda_lib.moe_finalize_allreduce(ranks, "fp32", **res, **s),
+             lambda **s: cuda_lib.moe_finalize_allreduce_reduce([partial, partial], **res, **s),
+             lambda **s: cuda_lib.topk_route(logits, 4, want_packed=True, **s),
+             lambda **s: cuda_lib.pack_topk_ids(ids, w[:40].contiguous(), **s),
+             lambda **s: cuda_lib.unpack_topk_ids(words, **s),
+             lambda **s: cuda_lib.check_indices(idx, idx.numel() - 3, **s)]
+
+    def tensors(r):
+        r = list(r.values()) if isinstance(r, dict) else r
+        r = r if isinstance(r, (list, tuple)) else [r]
+        return [t.clone() for t in r if t is not None]
+
+    for i, call in enumerate(calls):
+        want = tensors(call())
+        side = torch.cuda.Stream()
+        for stream in handles(side):
+            side.wait_stream(torch.cuda.current_stream())
+            r = call(stream=stream)
+            torch.cuda.current_stream().wait_stream(side)
+            got = tensors(r)
+            assert len(got) == len(want)
+            for a, b in zip(got, want):
+                assert torch.equal(a, b), i
+
+
 @pytest.mark.gpu
 def test_outputs_do_not_take_blocks_still_in_use(cuda_lib):
     """A block freed by the host while the current stream has yet to read it
@@ -169,10 +283,13 @@ def test_outputs_do_not_take_blocks_still_in_use(cuda_lib):
     x, w, w2 = rand(6, T, K), rand(7, n, K, scale=0.06), rand(8, 2 * n, K, scale=0.06)
     we, offsets = w.view(1, n, K), torch.tensor([0, T], dtype=torch.int32, device="cuda")
     counts = torch.tensor([T], dtype=torch.int32, device="cuda")
+    idx = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1)
+    one = torch.ones(T, 1, device="cuda")
     side, current = torch.cuda.Stream(), torch.cuda.current_stream()
     calls = [lambda s: cuda_lib.linear(x, w, save_preact=True, stream=s),
              lambda s: cuda_lib.gated_ffn(x, w2, stream=s),
-             lambda s: {"out": cuda_lib.expert_linear(x, offsets, counts, we, stream=s)}]
+             lambda s: {"out": cuda_lib.expert_linear(x, offsets, counts, we, stream=s)},
+             lambda s: cuda_lib.moe_finalize(x, idx, one, "fp32", x, stream=s)]
     for call in calls:
         want = call(None)
         for stream in handles(side):
