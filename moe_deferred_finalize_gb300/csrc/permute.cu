@@ -101,12 +101,19 @@ __device__ __forceinline__ void place_experts(const Tables &t, int E, int tile, 
     __syncthreads();
 }
 
+// A lane's first padding row: the layout may end at row 2^31 - 1, which the sum passes.
+__device__ __forceinline__ constexpr int64_t padding_row(int32_t pad, int lane) {
+    return static_cast<int64_t>(pad) + lane;
+}
+static_assert(padding_row(INT32_MAX, 31) == int64_t{INT32_MAX} + 31, "64-bit rows");
+
 // -1 on the padding rows and behind the last expert, shared by `ctas` CTAs.
 __device__ __forceinline__ void fill_padding(const Tables &t, int E, int32_t *row_token,
                                              int64_t P, int cta, int ctas) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     for (int e = cta * kWarps + w; e < E; e += ctas * kWarps)
-        for (int64_t r = t.pad[e] + lane; r < t.next[e]; r += 32) row_token[r] = -1;
+        for (int64_t r = padding_row(t.pad[e], lane); r < t.next[e]; r += 32)
+            row_token[r] = -1;
     for (int64_t r = t.next[E - 1] + static_cast<int64_t>(cta) * kThreads + threadIdx.x; r < P;
          r += static_cast<int64_t>(ctas) * kThreads)
         row_token[r] = -1;
