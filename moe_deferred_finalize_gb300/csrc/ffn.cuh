@@ -38,6 +38,12 @@ struct Gemm {
     int64_t b_pitch;            // values from one of its rows (of k: b_mn) to the next
 };
 
+// Steps of `step` values that cover k >= 1 of them.  k is a token count in
+// dweight, up to 2^31 - 1, which rounding up in 32 bits would pass.
+__host__ __device__ constexpr int steps_of(int k, int step) { return (k - 1) / step + 1; }
+static_assert(steps_of(INT32_MAX, 64) == 1 << 25 && steps_of(64, 64) == 1 && steps_of(65, 64) == 2,
+              "steps of the longest sums");
+
 // Tiled kernel of single-value loads: any size, alignment and layout.
 cudaError_t launch_gemm_simple(const Gemm &g, cudaStream_t stream);
 

@@ -765,7 +765,7 @@ __device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Head
     }
     if (lane == 0) {
         const int tiles = before * p.m_tiles, units = gridDim.x / CG;
-        int blocks = (g.K + kBlockK - 1) / kBlockK, log = 0;
+        int blocks = steps_of(g.K, kBlockK), log = 0;
         while (log < p.log_split && tiles <= units >> (log + 1) &&
                received_bytes(bn, 2 << log) <= kMaxReceived &&
                (blocks /= 2) * 400 > (log ? 300 << log : 1500 + 10 * bn))
@@ -874,8 +874,8 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         return tile_at<CG, GATED>(work.g[q], work.p[q], h, q ? ti - work.tiles0 : ti);
     };
     auto k_range = [&](int q, int *kb0, int *kb1) {
-        const int blocks = (work.g[q].K + kBlockK - 1) / kBlockK;
-        *kb0 = (blocks * part) >> log_split;        // blocks < 2^25, part < 16
+        const int blocks = steps_of(work.g[q].K, kBlockK);
+        *kb0 = (blocks * part) >> log_split;        // blocks <= 2^25, part < 16
         *kb1 = (blocks * (part + 1)) >> log_split;
     };
     // Launched as a dependent of the previous kernel on the stream: everything

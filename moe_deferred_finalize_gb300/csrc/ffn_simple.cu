@@ -95,6 +95,7 @@ gemm_simple_kernel(const Gemm g) {
     const uint16_t *a = g.a + static_cast<int64_t>(e) * arows * g.K;
     const uint16_t *bias = g.bias ? g.bias + static_cast<int64_t>(e) * arows : nullptr;
     const int64_t a_pitch = g.a_mn ? arows : g.K;
+    const int steps = steps_of(g.K, kStep);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int wm = warp & 3, wn = warp >> 2;
     // the warp's two blocks of 16 rows of A: gate and up, or adjacent ones
@@ -117,13 +118,14 @@ gemm_simple_kernel(const Gemm g) {
         Staged<kRowsB> next_b;
         next_a.load(a, g.a_mn, a_pitch, 0, g.K, a_row);
         next_b.load(g.b, g.b_mn, g.b_pitch, 0, g.K, b_row);
-        for (int k0 = 0; k0 < g.K; k0 += kStep) {
+        for (int step = 0; step < steps; ++step) {
             next_a.store(sa, g.a_mn);
             next_b.store(sb, g.b_mn);
             __syncthreads();
-            if (k0 + kStep < g.K) {
-                next_a.load(a, g.a_mn, a_pitch, k0 + kStep, g.K, a_row);
-                next_b.load(g.b, g.b_mn, g.b_pitch, k0 + kStep, g.K, b_row);
+            if (step + 1 < steps) {
+                const int k0 = (step + 1) * kStep;
+                next_a.load(a, g.a_mn, a_pitch, k0, g.K, a_row);
+                next_b.load(g.b, g.b_mn, g.b_pitch, k0, g.K, b_row);
             }
 #pragma unroll
             for (int k = 0; k < kStep; k += 16) {

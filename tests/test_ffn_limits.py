@@ -3,6 +3,8 @@ steps of k come near 2^31."""
 import pytest
 import torch
 
+import ffn_ref as R
+
 BF16 = torch.bfloat16
 MOST = 2 ** 31 - 1
 
@@ -22,3 +24,21 @@ def test_row_map_that_ends_at_the_last_row(cuda_lib):
         for at in range(1, MOST, 2 ** 28):      # in pieces: comparisons are 64-bit indexed
             assert bool((token[at:at + 2 ** 28] == -1).all())
         del m, token
+
+
+@pytest.mark.gpu
+def test_weight_gradient_over_the_most_rows(cuda_lib):
+    """2^31 - 1 rows, which dweight sums over: a few carry values, the first and
+    last blocks of 64 among them, the others are zeros and add nothing."""
+    N, K = 8, 8
+    x = torch.zeros(MOST, K, dtype=BF16, device="cuda")
+    dout = torch.zeros(MOST, N, dtype=BF16, device="cuda")
+    some = [0, 1, 63, 64, 2 ** 30, MOST - 64, MOST - 63, MOST - 33, MOST - 32, MOST - 2, MOST - 1]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    for t in (x, dout):
+        t[some] = torch.randn(len(some), 8, device="cuda", generator=g).to(BF16)
+    w = torch.ones(N, K, dtype=BF16, device="cuda")
+    got = cuda_lib.linear_backward(dout, x, w, want_dx=False, want_dbias=True)
+    R.check(got, R.backward(dout[some], x[some], w, None, "none", False))
+    assert cuda_lib.lost_waits() == 0
