@@ -1051,6 +1051,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 const uint32_t d = tmem + (n & 1) * kMaxBn;
                 const uint32_t a_step = g.a_mn ? 2048 >> 4 : 32 >> 4;
                 const uint32_t b_step = g.b_mn ? 2048 >> 4 : 32 >> 4;
+                begin(ti);      // or the previous kernel's time counts as a copy's
                 if (!wait(smem_addr(&h->acc_empty[n & 1]), ((n >> 1) & 1) ^ 1, gave_up)) break;
                 fence_after();
                 for (int kb = kb0; kb < kb1; ++kb) {
