@@ -65,6 +65,7 @@ constexpr int kSmemBytes = 227 * 1024;
 constexpr int kStageArea = kSmemBytes - kHeader - 1024;     // after rounding up to 1024
 constexpr int kBand = 8;                        // feature tiles per band (see tile_at)
 constexpr long long kWaitLimit = 4000000000;     // clocks (two seconds) until a wait gives up
+constexpr long long kBlockLimit = 4096;          // more for each k block that it waits for
 
 // How one launch is cut up (see choose_cut).
 struct TcPlan {
@@ -107,8 +108,10 @@ __device__ unsigned int lost_waits;
 // Waits for a barrier's phase; false when the wait gave up (here or in
 // another warp of the CTA), upon which every role leaves its loops.  Only time
 // in which the warp ran counts: a gap between two looks at the clock (the
-// process lost its time slice) counts as kGap at most.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+// process lost its time slice) counts as kGap at most.  A whole tile's wait has
+// its k blocks added: dweight of 2^31 - 1 rows takes 2 million of 460 ns a CTA.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *gave_up,
+                                     int blocks = 0) {
     if (bar_try(bar, parity)) return true;
     constexpr long long kGap = 1 << 20;
     long long last = clock64(), spent = 0;
@@ -118,7 +121,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
         const long long now = clock64();
         spent += min(now - last, kGap);
         last = now;
-        if (spent > kWaitLimit) {
+        if (spent > kWaitLimit + blocks * kBlockLimit) {
             *gave_up = 1;
             atomicAdd(&lost_waits, 1u);
             return false;
@@ -878,6 +881,12 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         *kb0 = (blocks * part) >> log_split;        // blocks <= 2^25, part < 16
         *kb1 = (blocks * (part + 1)) >> log_split;
     };
+    auto wait_for_tile = [&](int n, int q) {
+        int kb0, kb1;
+        k_range(q, &kb0, &kb1);
+        const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up, kb1 - kb0);
+        return __all_sync(0xFFFFFFFFu, ok);
+    };
     // Launched as a dependent of the previous kernel on the stream: everything
     // up to a role's first tile comes from the parameters, and global memory is
     // touched behind this.
@@ -1080,16 +1089,14 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                                  (n & 1) * kMaxBn;
             begin(ti);
             if (split > 1) {        // joined below
-                const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
-                (void)__all_sync(0xFFFFFFFFu, ok);
+                (void)wait_for_tile(n, q);
                 fence_after();
                 break;
             }
             const uint32_t done = map_rank(smem_addr(&h->acc_empty[n & 1]),
                                            CG == 2 ? lead : cluster_rank());
             auto finish = [&](auto &part_of, auto out_of_tmem) {
-                const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up);
-                if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+                if (!wait_for_tile(n, q)) return false;
                 fence_after();
                 out_of_tmem(part_of);
                 return true;
