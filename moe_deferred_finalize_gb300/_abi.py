@@ -200,8 +200,12 @@ def _under(fn, device, args):
     elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, expected one on {device}")
     current = torch.cuda.current_stream(device)
-    with torch.cuda.stream(stream):
-        res = fn(**args)
+    with _on(device):
+        torch.cuda.set_stream(stream)       # a sixth of the time of torch.cuda.stream()
+        try:
+            res = fn(**args)
+        finally:
+            torch.cuda.set_stream(current)
     made = res.outputs if isinstance(res, BoundFinalize) else res
     for t in made.values() if isinstance(made, dict) else \
             made if isinstance(made, tuple) else (made,):

@@ -30,7 +30,8 @@ def entry_points(monkeypatch):
     from moe_deferred_finalize_gb300 import _abi, _ffn
 
     def enter(stream):
-        raise Entered(stream)
+        if stream is not None:          # None: the current one, set again on the way out
+            raise Entered(stream)
 
     def library():
         raise RuntimeError("these tensors must not reach the library")
@@ -41,7 +42,8 @@ def entry_points(monkeypatch):
     monkeypatch.setattr(_abi, "_RAW_STREAM", lambda index: CURRENT)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
-    monkeypatch.setattr(torch.cuda, "stream", enter)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "set_stream", enter)
     return mf
 
 
@@ -109,7 +111,6 @@ def test_gate_outputs_belong_to_the_given_stream(entry_points):
 def test_allocations_belong_to_the_given_stream(entry_points, monkeypatch, name, args, outputs,
                                                 options):
     # some take their device from the outputs too, or the current one
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(OnDevice, "is_cuda", True, raising=False)
     monkeypatch.setattr(OnDevice, "get_device", lambda self: 0, raising=False)
     fn, a = getattr(entry_points, name), args()
@@ -304,6 +305,22 @@ def test_outputs_do_not_take_blocks_still_in_use(cuda_lib):
             assert (read == 3).all()
             for key in want:
                 assert torch.equal(got[key], want[key])
+
+
+@pytest.mark.gpu
+def test_the_current_stream_stays_current(cuda_lib):
+    """Also when the call is refused, and from a stream that is not the default."""
+    x, w = rand(9, 20, 64), rand(10, 32, 64)
+    side, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(mine):
+        for stream in handles(side):
+            cuda_lib.linear(x, w, stream=stream)
+            assert torch.cuda.current_stream() == mine
+            with pytest.raises(ValueError):
+                cuda_lib.linear(x, w[:, :32], stream=stream)
+            assert torch.cuda.current_stream() == mine
+    torch.cuda.synchronize()
 
 
 @pytest.mark.gpu
