@@ -142,8 +142,9 @@ def linear(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Tensor
     dict with "out" [T, N] (``out_dtype`` bfloat16 or float32; a given bf16
     ``out`` may be the residual) and, with ``save_preact`` or a given
     ``preact``, "preact" bf16 [T, N] (x weight^T + bias, for
-    ``linear_backward``).  Enqueued on the current stream (or ``stream``, on
-    which what the call allocates is then allocated too)."""
+    ``linear_backward``, which gives the gradients: no call here is recorded
+    by autograd).  Enqueued on the current stream (or ``stream``, on which
+    what the call allocates is then allocated too)."""
     if stream is not None and (out is None or save_preact and preact is None) and \
             _elsewhere(stream, _device(x)):
         return _under(linear, x.device, dict(locals()))
@@ -365,7 +366,8 @@ def gated_ffn(x: torch.Tensor, weight: torch.Tensor, *, bias: Optional[torch.Ten
     x bf16 [T, H]; weight bf16 [2I, H], the I gate rows and then the I up
     rows; bias bf16 [2I].  Returns a dict with "out" bf16 [T, I] and, with
     ``save_preact`` or a given ``preact``, "preact" bf16 [T, 2I] (both
-    projections with their bias, for ``gated_ffn_backward``)."""
+    projections with their bias, for ``gated_ffn_backward``; not recorded by
+    autograd)."""
     if stream is not None and (out is None or save_preact and preact is None) and \
             _elsewhere(stream, _device(x)):
         return _under(gated_ffn, x.device, dict(locals()))
