@@ -1,6 +1,8 @@
 """Calls on a given stream (``stream=``) that allocate: what they allocate
 belongs to that stream, so that neither a workspace freed on return nor a
 recycled block is shared with work on the current stream."""
+import ctypes
+
 import pytest
 import torch
 
@@ -321,6 +323,36 @@ def test_the_current_stream_stays_current(cuda_lib):
                 cuda_lib.linear(x, w[:, :32], stream=stream)
             assert torch.cuda.current_stream() == mine
     torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_handles_of_every_kind(cuda_lib):
+    """The legacy default stream by its handles, from another current stream; a
+    ctypes pointer; a graph whose capture the given stream has joined."""
+    x, w = rand(9, 20, 64), rand(10, 32, 64)
+    want = cuda_lib.linear(x, w)["out"]
+    side, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(mine):
+        for stream in (0, torch.cuda.default_stream(), ctypes.c_void_p(0),
+                       ctypes.c_void_p(side.cuda_stream)):
+            got = cuda_lib.linear(x, w, stream=stream)["out"]
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+    ws = {}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        ws["out"] = cuda_lib.linear(x, w, stream=side)["out"]
+        ws["grads"] = cuda_lib.linear_backward(ws["out"], x, w, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    x.copy_(rand(11, 20, 64))
+    graph.replay()
+    torch.cuda.synchronize()
+    want = cuda_lib.linear(x, w)["out"]
+    assert torch.equal(ws["out"], want)
+    for key, t in cuda_lib.linear_backward(want, x, w).items():
+        assert torch.equal(ws["grads"][key], t)
 
 
 @pytest.mark.gpu
