@@ -42,3 +42,31 @@ def test_weight_gradient_over_the_most_rows(cuda_lib):
     got = cuda_lib.linear_backward(dout, x, w, want_dx=False, want_dbias=True)
     R.check(got, R.backward(dout[some], x[some], w, None, "none", False))
     assert cuda_lib.lost_waits() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [8, 24])
+def test_products_over_the_most_rows(cuda_lib, N):
+    """2^31 - 1 rows forward and through dx: nothing in the tiles' places may pass 31
+    bits.  A few rows carry values, the first and last tiles' among them."""
+    K = 8
+    x = torch.zeros(MOST, K, dtype=BF16, device="cuda")
+    some = [0, 1, 255, 256, 2 ** 30, MOST - 257, MOST - 256, MOST - 33, MOST - 2, MOST - 1]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    x[some] = torch.randn(len(some), K, device="cuda", generator=g).to(BF16)
+    w = torch.randn(N, K, device="cuda", generator=g).to(BF16)
+
+    def zeros_elsewhere(out):
+        assert int(out[:2 ** 20].count_nonzero(dim=1).bool().sum()) == 4
+        assert int(out[-2 ** 20:].count_nonzero(dim=1).bool().sum()) == 5
+        assert int(out[2 ** 30 - 1000:2 ** 30 + 1000].count_nonzero(dim=1).bool().sum()) == 1
+
+    out = cuda_lib.linear(x, w)["out"]
+    R.check({"out": out[some]}, {"out": R.linear(x[some], w)["out"]})
+    zeros_elsewhere(out)
+    if N == K:
+        dx = cuda_lib.linear_backward(x, x, w, want_dweight=False, dx=out)["dx"]
+        R.check({"dx": dx[some]}, {"dx": R.backward(x[some], x[some], w, None, "none", False)["dx"]})
+        zeros_elsewhere(dx)
+    assert cuda_lib.lost_waits() == 0
