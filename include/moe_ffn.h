@@ -235,8 +235,9 @@ moef_status moe_expert_linear(const void *x, int64_t T, const int32_t *row_token
  * hand work to each other through barriers; a wait that has not ended after
  * two seconds, and 2 us more for each 64 values of k summed meanwhile (which no
  * correct run comes near: 0.5 us at most), is given up, the launch ends with
- * undefined outputs, and the count kept here for the current device goes up.  Writes the count since the library was loaded; waits for the device
- * (call it outside the hot path, not during a capture).
+ * undefined outputs, and the count kept here for the current device goes up.
+ * Writes the count since the library was loaded; waits for the device (call it
+ * outside the hot path, not during a capture).
  */
 moef_status moe_ffn_lost_waits(unsigned *count);
 

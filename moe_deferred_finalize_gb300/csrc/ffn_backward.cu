@@ -13,9 +13,9 @@
 // 1.66e-3.  The column sums build up in registers, in fp32 and before dz is
 // rounded; the CTA adds its lanes' sums in order and writes one row of `partial`,
 // whose rows are then added in order (no atomics: equal calls give equal bits) by
-// idle warps of the product that follows, or by a kernel of its own.  2040 x 4096 with GELU takes 12.2 us (4.1
-// TB/s; with the activation chosen per value and 32 rows a thread it took 40 us),
-// 4096 x 2048 gated with SiLU 15.8 us (5.3 TB/s).
+// idle warps of the product that follows, or by a kernel of its own.  2040 x 4096
+// with GELU takes 12.2 us (4.1 TB/s; with the activation chosen per value and 32
+// rows a thread it took 40 us), 4096 x 2048 gated with SiLU 15.8 us (5.3 TB/s).
 #include "ffn.cuh"
 #include "tc.cuh"
 #include "vec.cuh"
