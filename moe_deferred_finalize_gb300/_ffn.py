@@ -42,6 +42,10 @@ def _lib():
             "moe_expert_gated_ffn": (i32, [vp, i64] + [vp] * 5 + [i32, vp, i64, i32, i32, i32,
                                                                   vp]),
             "moe_expert_linear": (i32, [vp, i64] + [vp] * 5 + [i32, vp, i64, i32, i32, i32, vp]),
+            "moe_expert_gated_ffn_save": (i32, [vp, i64] + [vp] * 5 + [i32, vp, vp, i64, i32, i32,
+                                                                       i32, vp]),
+            "moe_expert_linear_save": (i32, [vp, i64] + [vp] * 5 + [i32, vp, vp, i64, i32, i32,
+                                                                    i32, vp]),
             "moe_ffn_lost_waits": (i32, [ctypes.POINTER(ctypes.c_uint)]),
         }
         for name, (restype, argtypes) in signatures.items():
@@ -544,11 +548,13 @@ def _fast_expert(where, gated, x, row_token, offsets, counts, weight, bias, acti
     return out
 
 
-def _expert(where, gated, x, row_token, offsets, counts, weight, bias, activation, out, stream):
-    res = _fast_expert(where, gated, x, row_token, offsets, counts, weight, bias, activation, out,
-                       stream)
-    if res is not None:
-        return res
+def _expert(where, gated, x, row_token, offsets, counts, weight, bias, activation, out, preact,
+            stream):
+    if preact is None:
+        res = _fast_expert(where, gated, x, row_token, offsets, counts, weight, bias, activation,
+                           out, stream)
+        if res is not None:
+            return res
     T, K = _matrix(x, "x", "[T, inputs]")
     dev = x.device
     if not isinstance(weight, torch.Tensor) or weight.dim() != 3:
@@ -568,6 +574,15 @@ def _expert(where, gated, x, row_token, offsets, counts, weight, bias, activatio
         P = row_token.numel()
         _check(row_token, "row_token", _I32, (P,), dev)
     out = _output(out, "out", torch.bfloat16, (P, M), dev)
+    if preact is not None:
+        _check(preact, "preact", _BF16, (P, rows), dev)
+        with _on(dev):
+            st = getattr(_lib(), where + "_save")(
+                _ptr(x), T, _ptr(row_token), _ptr(offsets), _ptr(counts), _ptr(weight),
+                _ptr(bias), act, _ptr(out), _ptr(preact), P, _int(E), _int(M), _int(K),
+                _stream(stream, dev))
+        _raise(st, where + "_save")
+        return out
     with _on(dev):
         st = _call("call_expert", where, _ptr(x), T, _ptr(row_token), _ptr(offsets), _ptr(counts),
                    _ptr(weight), _ptr(bias), act, _ptr(out), P, _int(E), _int(M), _int(K),
@@ -579,7 +594,8 @@ def _expert(where, gated, x, row_token, offsets, counts, weight, bias, activatio
 def expert_gated_ffn(x: torch.Tensor, row_token: Optional[torch.Tensor], offsets: torch.Tensor,
                      counts: torch.Tensor, weight: torch.Tensor, *,
                      bias: Optional[torch.Tensor] = None, activation: str = "silu",
-                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                     out: Optional[torch.Tensor] = None,
+                     preact: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``gated_ffn`` over rows grouped by expert (include/moe_ffn.h): out
     bf16 [P, I], row r of expert e from x row ``row_token[r]`` (row r itself
     with ``row_token=None``) and weight[e].
@@ -587,25 +603,27 @@ def expert_gated_ffn(x: torch.Tensor, row_token: Optional[torch.Tensor], offsets
     x bf16 [T, H]; row_token int32 [P], offsets int32 [E + 1] and counts int32
     [E] as from ``permute_tokens``; weight bf16 [E, 2I, H]; bias bf16 [E, 2I].
     Rows of no expert are left as they were (unset when ``out`` is allocated
-    here)."""
+    here).  ``preact``: a bf16 [P, 2I] tensor that receives both projections
+    with their bias, for ``expert_gated_ffn_backward``."""
     if stream is not None and out is None and _elsewhere(stream, _device(x)):
         return _under(expert_gated_ffn, x.device, dict(locals()))
     return _expert("moe_expert_gated_ffn", True, x, row_token, offsets, counts, weight, bias,
-                   activation, out, stream)
+                   activation, out, preact, stream)
 
 
 def expert_linear(x: torch.Tensor, offsets: torch.Tensor, counts: torch.Tensor,
                   weight: torch.Tensor, *, row_token: Optional[torch.Tensor] = None,
                   bias: Optional[torch.Tensor] = None, activation: str = "none",
-                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                  out: Optional[torch.Tensor] = None, preact: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
     """act(x weight[e]^T + bias[e]) over rows grouped by expert: out bf16
     [P, N], the ``permuted_out`` of ``moe_finalize``.  x bf16 [P, K] in the
     layout itself, or [T, K] with ``row_token``; weight bf16 [E, N, K]; bias
-    bf16 [E, N].  Otherwise as ``expert_gated_ffn``."""
+    bf16 [E, N]; ``preact`` bf16 [P, N].  Otherwise as ``expert_gated_ffn``."""
     if stream is not None and out is None and _elsewhere(stream, _device(x)):
         return _under(expert_linear, x.device, dict(locals()))
     return _expert("moe_expert_linear", False, x, row_token, offsets, counts, weight, bias,
-                   activation, out, stream)
+                   activation, out, preact, stream)
 
 
 def lost_waits(device=None) -> int:

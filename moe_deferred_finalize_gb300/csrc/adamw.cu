@@ -1,0 +1,288 @@
+// AdamW over many tensors (moe_adamw_step).
+//
+// Bound by HBM: a value with fp32 states and master moves 28 bytes for some forty
+// operations.  A warp takes 256 values of a tensor at a time, eight a lane, all its
+// loads in flight before the first use; the table of tensors comes with the launch's
+// parameters, so that nothing is copied or kept between calls, and a warp walks it
+// forward as its pieces go up.  256 values are also what an 8-bit state's scale is
+// for, so a warp has a scale's values to itself and finds the largest by shuffles.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "tc.cuh"
+#include "train.cuh"
+#include "vec.cuh"
+
+namespace moef {
+namespace {
+
+constexpr int kPiece = 256;             // values a warp takes at a time
+constexpr int kAdamThreads = 256;
+constexpr int kPerCta = kAdamThreads / 32;
+constexpr int kCtasPerSm = 4;
+constexpr float kE4m3Max = 448.f, kE4m3Least = 0.001953125f;    // 2^-9
+constexpr int kFewTensors = 48, kManyTensors = 256;             // of a launch
+
+template <int N>
+struct Table {
+    moef_adamw_tensor t[N];
+    uint32_t end[N];                    // pieces up to each tensor's last
+    int n;
+};
+static_assert(sizeof(Table<kManyTensors>) + sizeof(AdamWFactors) <= 32000, "launch parameters");
+
+// Eight values of an array of `left` more (at least one), 16-byte accesses where
+// `whole`.
+__device__ __forceinline__ void load8(const float *p, float (&f)[8], int64_t left, bool whole) {
+    if (whole) {
+        const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
+        const float4 b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = i < left ? p[i] : 0.f;
+    }
+}
+__device__ __forceinline__ void load8(const uint16_t *p, float (&f)[8], int64_t left, bool whole) {
+    if (whole) {
+        VecOps<8>::to_f32(VecOps<8>::load(p), f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = i < left ? __uint_as_float(static_cast<uint32_t>(p[i]) << 16) : 0.f;
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float (&f)[8], int64_t left, bool whole) {
+    if (whole) {
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
+        __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = f[i];
+    }
+}
+__device__ __forceinline__ void store8(uint16_t *p, const float (&f)[8], int64_t left,
+                                       bool whole) {
+    if (whole) {
+        *reinterpret_cast<uint4 *>(p) = VecOps<8>::from_f32(f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+    }
+}
+
+// Eight e4m3 codes as they lie in memory.
+__device__ __forceinline__ uint2 load_codes(const uint8_t *p, int64_t left, bool whole) {
+    uint2 c = make_uint2(0, 0);
+    if (whole) return __ldcs(reinterpret_cast<const uint2 *>(p));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) (i < 4 ? c.x : c.y) |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+    return c;
+}
+__device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t pair = (i < 2 ? c.x : c.y) >> (16 * (i & 1));
+        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>(pair & 0xFFFFu), __NV_E4M3));
+        const float2 v = __half22float2(h);
+        f[2 * i] = v.x * scale;
+        f[2 * i + 1] = v.y * scale;
+    }
+}
+
+// The piece's scale, and its values as codes of it.  ROOT: values above 0 keep a
+// code above 0.
+template <bool ROOT>
+__device__ __forceinline__ void encode8(const float (&f)[8], uint8_t *p, float *scale_at, int lane,
+                                        int64_t left, bool whole) {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(f[i]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    // A code is the rounding of the rounded quotient: a product with the scale's
+    // reciprocal, off by a unit in the last place, would put one value in a million
+    // on the other side of a code's border, an eighth of the value away.
+    const float scale = most * (1.f / kE4m3Max), unit = scale > 0.f ? scale : 1.f;
+    if (lane == 0) *scale_at = scale;
+    uint32_t word[2] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 v = make_float2(__fdiv_rn(f[2 * i], unit), __fdiv_rn(f[2 * i + 1], unit));
+        if constexpr (ROOT) {
+            if (v.x > 0.f) v.x = fmaxf(v.x, kE4m3Least);
+            if (v.y > 0.f) v.y = fmaxf(v.y, kE4m3Least);
+        }
+        word[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE,
+                                                                       __NV_E4M3))
+                        << (16 * (i & 1));
+    }
+    if (whole) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(word[0], word[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = static_cast<uint8_t>(word[i >> 2] >> (8 * (i & 3)));
+    }
+}
+
+// Within 2^-22 of the root, as its use below allows.
+__device__ __forceinline__ float fast_sqrt(float x) {
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <typename P, typename G, bool MASTER, bool EIGHT, int N>
+__global__ void __launch_bounds__(kAdamThreads, kCtasPerSm)
+adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ AdamWFactors f) {
+    __shared__ float s_bias[2];
+    const int lane = threadIdx.x & 31;
+    wait_previous_kernel();
+    allow_next_kernel();
+    float bias1 = f.bias1, root_bias2 = f.root_bias2;
+    if (f.device_step) {
+        if (threadIdx.x < 2) {      // 1 - beta^step without cancellation
+            const int step = max(1, *f.device_step);
+            const double b = -expm1(step * (threadIdx.x ? f.log_beta2 : f.log_beta1));
+            s_bias[threadIdx.x] = static_cast<float>(threadIdx.x ? sqrt(b) : b);
+        }
+        __syncthreads();
+        bias1 = s_bias[0];
+        root_bias2 = s_bias[1];
+    }
+    const float lr = f.device_lr ? *f.device_lr : f.lr;
+    const float keep = 1.f - lr * f.weight_decay, step_size = lr / bias1;
+    const float root = 1.f / root_bias2;
+    const float grad_scale = f.grad_scale ? *f.grad_scale : 1.f;
+
+    const uint32_t pieces = table.end[table.n - 1], stride = gridDim.x * kPerCta;
+    int at = 0;
+    for (uint32_t piece = blockIdx.x * kPerCta + threadIdx.x / 32; piece < pieces;
+         piece += stride) {
+        while (piece >= table.end[at]) ++at;
+        const moef_adamw_tensor &t = table.t[at];
+        const int64_t block = piece - (at ? table.end[at - 1] : 0);
+        const int64_t i = block * kPiece + lane * 8, left = t.n - i;
+        const uintptr_t bits = reinterpret_cast<uintptr_t>(t.param) |
+                               reinterpret_cast<uintptr_t>(t.master) |
+                               reinterpret_cast<uintptr_t>(t.grad);
+        const uintptr_t states = reinterpret_cast<uintptr_t>(t.exp_avg) |
+                                 reinterpret_cast<uintptr_t>(t.exp_avg_sq);
+        const bool whole = left >= 8 && bits % 16 == 0 && states % (EIGHT ? 8 : 16) == 0;
+        float g[8] = {}, p[8] = {}, m[8] = {}, v[8] = {};
+        if (left > 0) {
+            load8(static_cast<const G *>(t.grad) + i, g, left, whole);
+            if constexpr (MASTER) load8(t.master + i, p, left, whole);
+            else load8(static_cast<const P *>(t.param) + i, p, left, whole);
+        }
+        if constexpr (EIGHT) {
+            uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
+            const float scale_m = t.exp_avg_scale[block], scale_v = t.exp_avg_sq_scale[block];
+            if (left > 0) {
+                cm = load_codes(static_cast<const uint8_t *>(t.exp_avg) + i, left, whole);
+                cv = load_codes(static_cast<const uint8_t *>(t.exp_avg_sq) + i, left, whole);
+            }
+            decode8(cm, scale_m, m);
+            decode8(cv, scale_v, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= v[k];
+        } else if (left > 0) {
+            load8(static_cast<const float *>(t.exp_avg) + i, m, left, whole);
+            load8(static_cast<const float *>(t.exp_avg_sq) + i, v, left, whole);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            g[k] *= grad_scale;
+            m[k] = fmaf(f.rest1, g[k], __fmul_rn(f.beta1, m[k]));
+            v[k] = fmaf(f.rest2, __fmul_rn(g[k], g[k]), __fmul_rn(f.beta2, v[k]));
+            const float s = EIGHT ? __fsqrt_rn(v[k]) : fast_sqrt(v[k]);
+            p[k] = keep * p[k] - __fdividef(step_size * m[k], fmaf(s, root, f.eps));
+            if constexpr (EIGHT) v[k] = s;
+        }
+        if (left > 0) {
+            if constexpr (MASTER) store8(t.master + i, p, left, whole);
+            store8(static_cast<P *>(t.param) + i, p, left, whole);
+        }
+        if constexpr (EIGHT) {
+            encode8<false>(m, static_cast<uint8_t *>(t.exp_avg) + i, t.exp_avg_scale + block, lane,
+                           left, whole);
+            encode8<true>(v, static_cast<uint8_t *>(t.exp_avg_sq) + i, t.exp_avg_sq_scale + block,
+                          lane, left, whole);
+        } else if (left > 0) {
+            store8(static_cast<float *>(t.exp_avg) + i, m, left, whole);
+            store8(static_cast<float *>(t.exp_avg_sq) + i, v, left, whole);
+        }
+    }
+}
+
+template <typename P, typename G, bool MASTER, bool EIGHT, int N>
+cudaError_t start_adamw(const moef_adamw_tensor *tensors, int n, const AdamWFactors &f,
+                        int num_sms, cudaStream_t stream) {
+    Table<N> table;
+    int64_t pieces = 0;
+    for (int i = 0; i < n; ++i) {
+        table.t[i] = tensors[i];
+        pieces += (tensors[i].n + kPiece - 1) / kPiece;
+        if (pieces > UINT32_MAX - (1 << 20)) return cudaErrorInvalidValue;
+        table.end[i] = static_cast<uint32_t>(pieces);
+    }
+    table.n = n;
+    if (pieces == 0) return cudaSuccess;
+    const int64_t need = (pieces + kPerCta - 1) / kPerCta;
+    const int64_t most = static_cast<int64_t>(num_sms) * kCtasPerSm;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(need < most ? need : most));
+    cfg.blockDim = dim3(kAdamThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, adamw_kernel<P, G, MASTER, EIGHT, N>, table, f);
+}
+
+template <typename P, typename G, bool MASTER, bool EIGHT>
+cudaError_t start_all(const moef_adamw_tensor *tensors, int n, const AdamWFactors &f, int num_sms,
+                      cudaStream_t stream) {
+    if (n <= kFewTensors)
+        return start_adamw<P, G, MASTER, EIGHT, kFewTensors>(tensors, n, f, num_sms, stream);
+    for (int i = 0; i < n; i += kManyTensors) {
+        const cudaError_t err = start_adamw<P, G, MASTER, EIGHT, kManyTensors>(
+            tensors + i, n - i < kManyTensors ? n - i : kManyTensors, f, num_sms, stream);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const moef_adamw_tensor *tensors, int n, const AdamWFactors &f,
+                         int state_bits, int masters, int param_f32, int grad_f32,
+                         int num_sms, cudaStream_t stream) {
+    auto go = [&](auto *start32, auto *start8) {
+        return (state_bits == 8 ? start8 : start32)(tensors, n, f, num_sms, stream);
+    };
+    if (param_f32)
+        return grad_f32 ? go(start_all<float, float, false, false>,
+                             start_all<float, float, false, true>)
+                        : go(start_all<float, uint16_t, false, false>,
+                             start_all<float, uint16_t, false, true>);
+    if (masters)
+        return grad_f32 ? go(start_all<uint16_t, float, true, false>,
+                             start_all<uint16_t, float, true, true>)
+                        : go(start_all<uint16_t, uint16_t, true, false>,
+                             start_all<uint16_t, uint16_t, true, true>);
+    return grad_f32 ? go(start_all<uint16_t, float, false, false>,
+                         start_all<uint16_t, float, false, true>)
+                    : go(start_all<uint16_t, uint16_t, false, false>,
+                         start_all<uint16_t, uint16_t, false, true>);
+}
+
+}  // namespace moef

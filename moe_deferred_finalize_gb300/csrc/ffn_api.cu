@@ -6,6 +6,7 @@
 #include "ffn.cuh"
 #include "host.cuh"
 #include "internal.cuh"
+#include "moe_train.h"
 
 namespace {
 
@@ -132,7 +133,7 @@ moef_status backward(const void *dout, const void *x, const void *weight, moef_a
 moef_status expert_product(const void *x, int64_t T, const int32_t *row_token,
                            const int32_t *offsets, const int32_t *counts, const void *weight,
                            const void *bias, moef_activation act, int gated, void *out,
-                           int64_t P, int E, int M, int K, cudaStream_t stream) {
+                           void *preact, int64_t P, int E, int M, int K, cudaStream_t stream) {
     if (T < 0 || T > INT_MAX || P < 0 || P > INT_MAX || E < 1 || E > MOEF_MAX_EXPERTS ||
         !valid_features(M) || !valid_features(K))
         return MOEF_ERR_SHAPE;
@@ -141,7 +142,7 @@ moef_status expert_product(const void *x, int64_t T, const int32_t *row_token,
     if (T == 0 || P == 0) return MOEF_OK;
     if (!x || !offsets || !counts || !weight || !out) return MOEF_ERR_NULL;
     if (!aligned(x, 2) || !aligned(weight, 2) || !aligned(bias, 2) || !aligned(out, 2) ||
-        !aligned(row_token, 4) || !aligned(offsets, 4) || !aligned(counts, 4))
+        !aligned(preact, 2) || !aligned(row_token, 4) || !aligned(offsets, 4) || !aligned(counts, 4))
         return MOEF_ERR_ALIGN;
     Gemm g{};
     g.a = u16(weight);
@@ -152,6 +153,7 @@ moef_status expert_product(const void *x, int64_t T, const int32_t *row_token,
     g.gated = gated;
     g.bias = u16(bias);
     g.out = out;
+    g.preact = static_cast<uint16_t *>(preact);
     g.act = static_cast<int>(act);
     g.E = E;
     g.offsets = offsets;
@@ -290,8 +292,8 @@ moef_status moe_expert_gated_ffn(const void *x, int64_t T, const int32_t *row_to
                                  const void *weight, const void *bias, moef_activation act,
                                  void *out, int64_t P, int E, int I, int H,
                                  cudaStream_t stream) {
-    return expert_product(x, T, row_token, offsets, counts, weight, bias, act, 1, out, P, E, I,
-                          H, stream);
+    return expert_product(x, T, row_token, offsets, counts, weight, bias, act, 1, out, nullptr,
+                          P, E, I, H, stream);
 }
 
 moef_status moe_expert_linear(const void *x, int64_t T, const int32_t *row_token,
@@ -299,8 +301,26 @@ moef_status moe_expert_linear(const void *x, int64_t T, const int32_t *row_token
                               const void *weight, const void *bias, moef_activation act,
                               void *out, int64_t P, int E, int N, int K,
                               cudaStream_t stream) {
-    return expert_product(x, T, row_token, offsets, counts, weight, bias, act, 0, out, P, E, N,
-                          K, stream);
+    return expert_product(x, T, row_token, offsets, counts, weight, bias, act, 0, out, nullptr,
+                          P, E, N, K, stream);
+}
+
+moef_status moe_expert_gated_ffn_save(const void *x, int64_t T, const int32_t *row_token,
+                                      const int32_t *offsets, const int32_t *counts,
+                                      const void *weight, const void *bias,
+                                      moef_activation act, void *out, void *preact, int64_t P,
+                                      int E, int I, int H, cudaStream_t stream) {
+    return expert_product(x, T, row_token, offsets, counts, weight, bias, act, 1, out, preact, P,
+                          E, I, H, stream);
+}
+
+moef_status moe_expert_linear_save(const void *x, int64_t T, const int32_t *row_token,
+                                   const int32_t *offsets, const int32_t *counts,
+                                   const void *weight, const void *bias, moef_activation act,
+                                   void *out, void *preact, int64_t P, int E, int N, int K,
+                                   cudaStream_t stream) {
+    return expert_product(x, T, row_token, offsets, counts, weight, bias, act, 0, out, preact, P,
+                          E, N, K, stream);
 }
 
 moef_status moe_ffn_lost_waits(unsigned *count) {

@@ -1,0 +1,258 @@
+// dz of the expert products' backward passes, over the rows of the experts alone,
+// and their bias gradients.
+//
+//   linear  dz = dout * act'(preact)
+//   gated   dz[:, i] = dout * u * act'(g),  dz[:, n + i] = dout * act(g)
+//
+// Both are bound by HBM: dout and preact are read once, dz is written once.  The
+// layout's rows are P at most, but how many the experts have only the device knows,
+// and with few tokens most of P is behind the last of them (16 tokens, top-8 of
+// 256, tiles of 128: 128 rows of 16384).  Each CTA counts the experts' pieces of
+// eight rows itself and takes every gridDim-th of them, a row a warp.
+#include "ffn.cuh"
+#include "tc.cuh"
+#include "train.cuh"
+#include "vec.cuh"
+
+namespace moef {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kLoads = 4;               // vectors of a lane in flight
+constexpr int kCtasPerSm = 4;
+
+// Rows of expert e: first, and how many, clipped to the buffer as the products clip
+// them.
+__device__ __forceinline__ int rows_of(const Groups &g, int e, int *first) {
+    *first = g.offsets[e];
+    if (*first < 0) return 0;
+    const int64_t room = g.P - *first;
+    return static_cast<int>(max(static_cast<int64_t>(0),
+                                min(static_cast<int64_t>(g.counts[e]), room)));
+}
+
+// dz of VEC columns: out[0] (linear, or the gate's) and out[1] (the up projection's).
+template <int VEC, bool GATED>
+__device__ __forceinline__ void dz_of(const float (&d)[VEC], const float (&z)[VEC],
+                                      const float (&u)[VEC], int act,
+                                      float (&out)[GATED ? 2 : 1][VEC]) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        float a;
+        const float da = act_grad(z[j], act, &a);
+        if constexpr (GATED) {
+            out[0][j] = d[j] * u[j] * da;
+            out[1][j] = d[j] * a;
+        } else {
+            out[0][j] = d[j] * da;
+        }
+    }
+}
+
+// ACT: the activation, or -1 to take it from `act`.
+template <int VEC, bool GATED, int ACT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t *dz,
+                 int64_t pitch, const Groups g, int n) {
+    using Ops = VecOps<VEC>;
+    using V = typename Ops::V;
+    __shared__ int s_pieces[MOEF_MAX_EXPERTS + 1], s_first[MOEF_MAX_EXPERTS],
+        s_rows[MOEF_MAX_EXPERTS], s_warp[kWarps];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int cols = GATED ? 2 * n : n;
+    wait_previous_kernel();
+    allow_next_kernel();
+    // the pieces before each expert: a scan over four experts a thread
+    constexpr int kEach = MOEF_MAX_EXPERTS / kThreads;
+    int own[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int e = threadIdx.x * kEach + i;
+        own[i] = 0;
+        if (e < g.E) {
+            s_rows[e] = rows_of(g, e, &s_first[e]);
+            own[i] = (s_rows[e] + kWarps - 1) / kWarps;
+        }
+        sum += own[i];
+    }
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o) before += v;
+    }
+    if (lane == 31) s_warp[warp] = before;
+    __syncthreads();
+    before -= sum;
+    int total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_warp[w];
+        total += s_warp[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        s_pieces[threadIdx.x * kEach + i] = before;
+        before += own[i];
+    }
+    __syncthreads();
+
+    for (int piece = blockIdx.x; piece < total; piece += gridDim.x) {
+        int lo = 0, hi = g.E;           // s_pieces[lo] <= piece < s_pieces[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_pieces[mid] <= piece) lo = mid; else hi = mid;
+        }
+        const int at = (piece - s_pieces[lo]) * kWarps + warp;
+        if (at >= s_rows[lo]) continue;
+        const int64_t row = static_cast<int64_t>(s_first[lo]) + at;
+        for (int i0 = lane * VEC; i0 < n; i0 += 32 * VEC * kLoads) {
+            V d[kLoads], z[kLoads], u[kLoads];
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) {
+                const int i = i0 + 32 * VEC * l;
+                if (i >= n) break;
+                d[l] = Ops::load(dout + row * n + i);
+                if (preact) z[l] = Ops::load(preact + row * cols + i);
+                if constexpr (GATED) u[l] = Ops::load(preact + row * cols + n + i);
+            }
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) {
+                const int i = i0 + 32 * VEC * l;
+                if (i >= n) break;
+                float df[VEC], zf[VEC] = {}, uf[VEC] = {}, out[GATED ? 2 : 1][VEC];
+                Ops::to_f32(d[l], df);
+                if (preact) Ops::to_f32(z[l], zf);
+                if constexpr (GATED) Ops::to_f32(u[l], uf);
+                dz_of<VEC, GATED>(df, zf, uf, ACT < 0 ? act : ACT, out);
+                // read again by both products: an ordinary store keeps it in L2
+#pragma unroll
+                for (int h = 0; h < (GATED ? 2 : 1); ++h)
+                    *reinterpret_cast<V *>(dz + row * pitch + h * n + i) = Ops::from_f32(out[h]);
+            }
+        }
+    }
+}
+
+// dbias of one expert and 32 vectors of columns: a warp takes every eighth row, the
+// warps' sums are added in order.
+template <int VEC, bool GATED>
+__global__ void __launch_bounds__(kThreads)
+expert_dbias_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t *dbias,
+                    const Groups g, int n) {
+    using Ops = VecOps<VEC>;
+    using V = typename Ops::V;
+    constexpr int kHalves = GATED ? 2 : 1, kRows = 4;
+    __shared__ float sums[kWarps][kHalves][32 * VEC];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int cols = kHalves * n, i = (blockIdx.x * 32 + lane) * VEC;
+    wait_previous_kernel();
+    allow_next_kernel();
+    int first;
+    const int rows = rows_of(g, blockIdx.y, &first);
+    float sum[kHalves][VEC] = {};
+    for (int r0 = warp; i < n && r0 < rows; r0 += kWarps * kRows) {
+        V d[kRows], z[kRows], u[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            if (r0 + k * kWarps >= rows) break;
+            const int64_t row = static_cast<int64_t>(first) + r0 + k * kWarps;
+            d[k] = Ops::load(dout + row * n + i);
+            if (preact) z[k] = Ops::load(preact + row * cols + i);
+            if constexpr (GATED) u[k] = Ops::load(preact + row * cols + n + i);
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            if (r0 + k * kWarps >= rows) break;
+            float df[VEC], zf[VEC] = {}, uf[VEC] = {}, out[kHalves][VEC];
+            Ops::to_f32(d[k], df);
+            if (preact) Ops::to_f32(z[k], zf);
+            if constexpr (GATED) Ops::to_f32(u[k], uf);
+            dz_of<VEC, GATED>(df, zf, uf, act, out);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) sum[h][j] += out[h][j];
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sums[warp][h][j * 32 + lane] = sum[h][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < kHalves * 32 * VEC; c += kThreads) {
+        const int h = c / (32 * VEC), k = c % (32 * VEC);
+        const int column = (blockIdx.x * 32 + k / VEC) * VEC + k % VEC;
+        if (column >= n) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += sums[w][h][k % VEC * 32 + k / VEC];
+        dbias[static_cast<int64_t>(blockIdx.y) * cols + h * n + column] =
+            __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    }
+}
+
+template <typename... Params, typename... Args>
+cudaError_t start(void (*kernel)(Params...), dim3 grid, cudaStream_t stream, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+bool vectors(const void *a, const void *b, const void *c, int n) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+                           reinterpret_cast<uintptr_t>(c);
+    return n % 8 == 0 && bits % 16 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_expert_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
+                             uint16_t *dz, int64_t pitch, const Groups &g, int n, int num_sms,
+                             cudaStream_t stream) {
+    const int64_t need = (g.P + kWarps - 1) / kWarps + (g.E < g.P ? g.E : g.P);
+    const int64_t most = static_cast<int64_t>(num_sms) * kCtasPerSm;
+    const dim3 grid(static_cast<unsigned>(need < most ? need : most));
+    auto go = [&](auto *kernel) {
+        return start(kernel, grid, stream, dout, preact, act, dz, pitch, g, n);
+    };
+    if (!vectors(dout, preact, dz, n))
+        return gated ? go(expert_dz_kernel<1, true, -1>) : go(expert_dz_kernel<1, false, -1>);
+    switch (act) {
+        case MOEF_ACT_SILU:
+            return gated ? go(expert_dz_kernel<8, true, MOEF_ACT_SILU>)
+                         : go(expert_dz_kernel<8, false, MOEF_ACT_SILU>);
+        case MOEF_ACT_GELU:
+            return gated ? go(expert_dz_kernel<8, true, MOEF_ACT_GELU>)
+                         : go(expert_dz_kernel<8, false, MOEF_ACT_GELU>);
+        case MOEF_ACT_GELU_TANH:
+            return gated ? go(expert_dz_kernel<8, true, MOEF_ACT_GELU_TANH>)
+                         : go(expert_dz_kernel<8, false, MOEF_ACT_GELU_TANH>);
+        case MOEF_ACT_RELU:
+            return gated ? go(expert_dz_kernel<8, true, MOEF_ACT_RELU>)
+                         : go(expert_dz_kernel<8, false, MOEF_ACT_RELU>);
+        default:
+            return gated ? go(expert_dz_kernel<8, true, MOEF_ACT_NONE>)
+                         : go(expert_dz_kernel<8, false, MOEF_ACT_NONE>);
+    }
+}
+
+cudaError_t launch_expert_dbias(const uint16_t *dout, const uint16_t *preact, int act, int gated,
+                                uint16_t *dbias, const Groups &g, int n, cudaStream_t stream) {
+    const bool vec = vectors(dout, preact, nullptr, n);
+    const int across = vec ? 256 : 32;
+    const dim3 grid(static_cast<unsigned>((n - 1) / across + 1), static_cast<unsigned>(g.E));
+    auto go = [&](auto *kernel) {
+        return start(kernel, grid, stream, dout, preact, act, dbias, g, n);
+    };
+    if (vec) return gated ? go(expert_dbias_kernel<8, true>) : go(expert_dbias_kernel<8, false>);
+    return gated ? go(expert_dbias_kernel<1, true>) : go(expert_dbias_kernel<1, false>);
+}
+
+}  // namespace moef

@@ -81,9 +81,10 @@ struct TcPlan {
 
 // One launch: a product, or two that share the SMs (the gradients of a layer):
 // tiles below tiles0 are the first one's.
-template <int N>
+template <int N, bool DW = false>
 struct Work {
-    CUtensorMap map[N][3];      // A, B, B in wide copies
+    // A, B, B in wide copies; grouped dweight: A, B, single rows of A and of B
+    CUtensorMap map[N][DW ? 4 : 3];
     Gemm g[N];
     TcPlan p[N];
     int tiles0;
@@ -145,15 +146,27 @@ struct Tile {
     int bn;             // columns computed
     int m0;             // first feature
     int e;              // expert
+    // grouped dweight: the first row of B's columns, and the expert's rows: k
+    int b0, first, rows;
 };
 
-template <int CG, bool GATED>
+template <int CG, bool GATED, bool DW>
 __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const Header *h, int t) {
     constexpr int kFeatures = (GATED ? 64 : 128) * CG;
     Tile r;
     r.e = 0;
     int m, n;
-    if (g.E) {
+    if constexpr (DW) {     // an expert's tiles share its rows of both operands
+        const int each = p.m_tiles * p.n_tiles, e = t / each, local = t - e * each;
+        n = local / p.m_tiles;
+        m = local - n * p.m_tiles;
+        r.bn = p.bn;
+        r.b0 = n * r.bn;
+        r.row0 = static_cast<int64_t>(e) * g.N + r.b0;
+        r.count = min(r.bn, g.N - r.b0);
+        r.first = h->first[e];
+        r.rows = h->count[e];
+    } else if (g.E) {
         int lo = 0, hi = g.E;           // prefix[lo] * m_tiles <= t < prefix[hi] * m_tiles
         const int column = t / p.m_tiles;
         while (hi - lo > 1) {
@@ -310,6 +323,13 @@ __device__ __noinline__ void finish_scalar(const Gemm &g, int m, int64_t n, floa
 
 constexpr int kChunk = 16;      // columns a warp finishes at a time
 
+// dweight of an expert without rows is 0; its tiles had no product.
+__device__ __forceinline__ void zero_without_rows(uint32_t (&r)[kChunk], const Tile &t) {
+    if (t.rows > 0) return;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) r[i] = 0;
+}
+
 // A warp's part of one tile: its 32 lanes (rows of A), every second or third chunk
 // (one for each of the `sides` warps of these lanes) of the columns [begin, end).
 // Made before the accumulator is waited for, so that the bias and the first
@@ -359,7 +379,7 @@ __device__ __forceinline__ int sum_lane(int lane, int c) { return lane ^ ((c >> 
 // column; bias, activation, residual and stores then run as loops over the
 // chunk, with nothing to decide per value, so their latencies overlap
 // (deciding per pair took 22 us per 256 x 256 tile, now about 3).
-template <bool GATED>
+template <bool DW, bool GATED>
 __device__ __forceinline__ void finish_tile(TilePart<GATED> &part, uint32_t tmem, uint32_t done,
                                             const float *sums, int parts) {
     const Finish<GATED> &f = part.f;
@@ -379,6 +399,7 @@ __device__ __forceinline__ void finish_tile(TilePart<GATED> &part, uint32_t tmem
         const int left = part.left(c0);
         uint32_t r[kChunk];
         tmem_load16(tmem + c0, r);
+        if constexpr (DW) zero_without_rows(r, t);
         if (done && c0 + stride >= end) {       // the accumulator has been read
             fence_before();
             __syncwarp();
@@ -583,7 +604,7 @@ __device__ __forceinline__ void store_chunk(const WidePart<GATED, RESIDUAL> &par
     }
 }
 
-template <bool GATED, bool RESIDUAL>
+template <bool DW, bool GATED, bool RESIDUAL>
 __device__ __forceinline__ void finish_wide(WidePart<GATED, RESIDUAL> &part, uint32_t stash,
                                             uint32_t tmem, uint32_t done, const float *sums,
                                             int parts) {
@@ -597,6 +618,7 @@ __device__ __forceinline__ void finish_wide(WidePart<GATED, RESIDUAL> &part, uin
     for (int c0 = part.first; c0 < end; c0 += stride) {
         uint32_t r[kChunk];
         tmem_load_fragments(tmem + c0, r);
+        if constexpr (DW) zero_without_rows(r, part.t);
         if (done && c0 + stride >= end) {       // the accumulator has been read
             fence_before();
             __syncwarp();
@@ -735,16 +757,25 @@ __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint3
 // the column tiles, from the largest group, the tiles before each expert, and
 // the parts of k: as many as the launch's clusters have room for while each
 // halving saves more k blocks (400 clocks) than it costs to join.
-template <int CG>
+// Grouped dweight: the rows alone, every expert has the same tiles.
+template <int CG, bool DW>
 __device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Header *h) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, room = DW ? g.K : g.N;
     int most = 0;
     for (int e = threadIdx.x; e < g.E; e += kTcThreads) {
         const int first = g.offsets[e], rows = g.counts[e];
-        const int count = first < 0 ? 0 : max(0, min(rows, g.N - first));
+        const int count = first < 0 ? 0 : max(0, min(rows, room - first));
         h->first[e] = first;
         h->count[e] = count;
         most = max(most, count);
+    }
+    if constexpr (DW) {
+        if (threadIdx.x == 0) {
+            h->bn = p.bn;
+            h->tiles = g.E * p.m_tiles * p.n_tiles;
+            h->log_split = 0;
+        }
+        return;
     }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     if (lane == 0) h->prefix[threadIdx.x / 32] = most;      // until the scan below
@@ -780,9 +811,42 @@ __device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Head
     }
 }
 
-template <int CG, bool GATED, int N>
+// The rows of a k block of grouped dweight (t.rows a token count): how many, and in
+// steps of the MMAs' 16.
+struct BlockRows {
+    int rows, steps;
+    __device__ __forceinline__ BlockRows(const Tile &t, int kb)
+        : rows(min(kBlockK, t.rows - kb * kBlockK)), steps((rows + 15) >> 4) {}
+    // rows 4 quad .. of the block, those past the expert's as zeros
+    __device__ __forceinline__ int4 quad_rows(int first, int quad) const {
+        const int r = 4 * quad;
+        return make_int4(r < rows ? first + r : -1, r + 1 < rows ? first + r + 1 : -1,
+                         r + 2 < rows ? first + r + 2 : -1, r + 3 < rows ? first + r + 3 : -1);
+    }
+};
+
+// A block of grouped dweight, `boxes` times 64 columns from x on.  The last block of
+// an expert ends where the next one's rows, or padding with anything in it, begin:
+// its rows come four to a copy, with zeros behind the last.
+template <int CG>
+__device__ __forceinline__ void copy_block(const BlockRows &b, uint32_t dst, int boxes,
+                                           const CUtensorMap *map, const CUtensorMap *rows_map,
+                                           int x, int row0, uint32_t bar) {
+    if (b.rows == kBlockK) {
+        for (int i = 0; i < boxes; ++i) tma_2d<CG>(dst + i * 8192, map, x + 64 * i, row0, bar);
+    } else {
+        for (int quad = 0; quad < 4 * b.steps; ++quad) {
+            const int4 rows = b.quad_rows(row0, quad);
+            for (int i = 0; i < boxes; ++i)
+                tma_gather4<CG>(dst + i * 8192 + quad * 512, rows_map, x + 64 * i, rows, bar);
+        }
+    }
+}
+
+template <int CG, bool GATED, int N, bool DW>
 __global__ void __launch_bounds__(kTcThreads, 1)
-gemm_tc_kernel(const __grid_constant__ Work<N> work) {
+gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
+    static_assert(!DW || (N == 1 && !GATED), "grouped dweight is one product");
     static_assert(N == 1 || (CG == 2 && !GATED), "two products run on pairs, without k in parts");
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = (smem_addr(smem) + 1023) & ~1023u;
@@ -825,7 +889,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     if (grouped) {
         wait_previous_kernel();
         allow_next_kernel();
-        count_tiles<CG>(work.g[0], work.p[0], h);
+        count_tiles<CG, DW>(work.g[0], work.p[0], h);
     }
     fence_before();
     if (CG == 2) {
@@ -874,16 +938,21 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
     // the product that a tile belongs to, and this part's k blocks of it
     auto product_of = [&](int ti) { return N == 2 && ti >= work.tiles0 ? 1 : 0; };
     auto tile_of = [&](int ti, int q) {
-        return tile_at<CG, GATED>(work.g[q], work.p[q], h, q ? ti - work.tiles0 : ti);
+        return tile_at<CG, GATED, DW>(work.g[q], work.p[q], h, q ? ti - work.tiles0 : ti);
     };
-    auto k_range = [&](int q, int *kb0, int *kb1) {
+    auto k_range = [&](int q, const Tile &t, int *kb0, int *kb1) {
+        if constexpr (DW) {
+            *kb0 = 0;
+            *kb1 = t.rows > 0 ? steps_of(t.rows, kBlockK) : 0;
+            return;
+        }
         const int blocks = steps_of(work.g[q].K, kBlockK);
         *kb0 = (blocks * part) >> log_split;        // blocks <= 2^25, part < 16
         *kb1 = (blocks * (part + 1)) >> log_split;
     };
-    auto wait_for_tile = [&](int n, int q) {
+    auto wait_for_tile = [&](int n, int q, const Tile &t) {
         int kb0, kb1;
-        k_range(q, &kb0, &kb1);
+        k_range(q, t, &kb0, &kb1);
         const bool ok = wait(smem_addr(&h->acc_full[n & 1]), (n >> 1) & 1, gave_up, kb1 - kb0);
         return __all_sync(0xFFFFFFFFu, ok);
     };
@@ -907,7 +976,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 const CUtensorMap *map = &work.map[q][0];
                 const Tile t = tile_of(ti, q);
                 int kb0, kb1;
-                k_range(q, &kb0, &kb1);
+                k_range(q, t, &kb0, &kb1);
                 const int bnc = t.bn / CG, m0 = t.m0 + half * m_cta_rows;
                 const uint32_t b_tx = p.gather ? bnc * 128u
                                       : g.b_mn ? (bnc + 63) / 64 * 8192u
@@ -916,6 +985,22 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 const uint32_t tx = CG * (kATile + b_tx);
                 begin(ti);
                 if (ti == first_tile) allow_next_kernel();
+                if constexpr (DW) {     // of B here: the lanes that gather have A
+                    const int boxes = (bnc + 63) / 64;
+                    for (int kb = 0; kb < kb1; ++kb) {
+                        const BlockRows b(t, kb);
+                        ok = wait(smem_addr(&h->empty[s]), phase, gave_up);
+                        if (!ok) break;
+                        const uint32_t full = smem_addr(&h->full[s]);
+                        if (leader) bar_expect(full, CG * (2 + boxes) * b.steps * 16 * 128);
+                        copy_block<CG>(b, stage0 + s * stage_bytes + kATile, boxes,
+                                       &work.map[0][1], &work.map[0][DW ? 3 : 1],
+                                       t.b0 + half * bnc, t.first + kb * kBlockK,
+                                       CG == 2 ? map_rank(full, lead) : full);
+                        if (++s == stages) { s = 0; phase ^= 1; }
+                    }
+                    continue;
+                }
                 auto blocks_of = [&](auto copy) {
                     for (int kb = kb0; kb < kb1; ++kb) {
                         if (!wait(smem_addr(&h->empty[s]), phase, gave_up)) return false;
@@ -927,7 +1012,12 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                     }
                     return true;
                 };
-                if (g.a_mn)
+                if (g.a_mn && grouped)
+                    ok = blocks_of([&](uint32_t a, int k, uint32_t bar) {
+                        tma_3d<CG>(a, map, m0, k, t.e, bar);
+                        tma_3d<CG>(a + 8192, map, m0 + 64, k, t.e, bar);
+                    });
+                else if (g.a_mn)
                     ok = blocks_of([&](uint32_t a, int k, uint32_t bar) {
                         tma_2d<CG>(a, map, m0, k, bar);
                         tma_2d<CG>(a + 8192, map, m0 + 64, k, bar);
@@ -954,10 +1044,50 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
         // ---- copies of B: one lane, or some of each warp when rows are gathered
         int s = 0;
         uint32_t phase = 1;
-        if (gathers) {
+        if (DW && gathers) {
+            // A: a lane has four rows of a block, and 64 of its 128 columns; the next
+            // block's row numbers come while this one's stage is waited for
+            const Gemm &g = work.g[0];
+            const int own = (warp - kCopyWarp) * kGatherLanes + lane;
+            const int quad = own & 15, column = (own >> 4) * 64;
+            for (int ti = first_tile; ti < tiles; ti += step) {
+                const Tile t = tile_of(ti, 0);
+                const int blocks = t.rows > 0 ? steps_of(t.rows, kBlockK) : 0;
+                const int x = t.m0 + half * m_cta_rows + column;
+                auto rows_at = [&](int kb) {
+                    int4 rows = make_int4(-1, -1, -1, -1);      // -1: a row of zeros
+                    const int left = t.rows - kb * kBlockK - 4 * quad;
+                    if (lane < kGatherLanes && own < 32 && left > 0) {
+                        const int32_t *at = g.row_token + t.first + kb * kBlockK + 4 * quad;
+                        rows.x = at[0];
+                        if (left > 1) rows.y = at[1];
+                        if (left > 2) rows.z = at[2];
+                        if (left > 3) rows.w = at[3];
+                    }
+                    return rows;
+                };
+                bool ok = true;
+                int4 next = rows_at(0);
+                for (int kb = 0; kb < blocks; ++kb) {
+                    const BlockRows b(t, kb);
+                    const int4 rows = next;
+                    if (kb + 1 < blocks) next = rows_at(kb + 1);
+                    ok = wait(smem_addr(&h->empty[s]), phase, gave_up);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const uint32_t full = smem_addr(&h->full[s]);
+                    if (lane < kGatherLanes && own < 32 && quad < 4 * b.steps)
+                        tma_gather4<CG>(stage0 + s * stage_bytes + column * 128 + quad * 512,
+                                        &work.map[0][2], x, rows,
+                                        CG == 2 ? map_rank(full, lead) : full);
+                    if (++s == stages) { s = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+            }
+        } else if (gathers) {
             const Gemm &g = work.g[0];
             int kb0, kb1;
-            k_range(0, &kb0, &kb1);
+            k_range(0, Tile{}, &kb0, &kb1);
             const int quad = (warp - kCopyWarp) * kGatherLanes + lane;      // of rows
             for (int ti = first_tile; ti < tiles; ti += step) {
                 const Tile t = tile_of(ti, 0);
@@ -1002,7 +1132,20 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 const CUtensorMap *map = &work.map[q][1], *wide = &work.map[q][2];
                 const Tile t = tile_of(ti, q);
                 int kb0, kb1;
-                k_range(q, &kb0, &kb1);
+                k_range(q, t, &kb0, &kb1);
+                if constexpr (DW) {     // of A here
+                    for (int kb = 0; kb < kb1; ++kb) {
+                        ok = wait(smem_addr(&h->empty[s]), phase, gave_up);
+                        if (!ok) break;
+                        const uint32_t full = smem_addr(&h->full[s]);
+                        copy_block<CG>(BlockRows(t, kb), stage0 + s * stage_bytes, 2,
+                                       &work.map[0][0], wide, t.m0 + half * m_cta_rows,
+                                       t.first + kb * kBlockK,
+                                       CG == 2 ? map_rank(full, lead) : full);
+                        if (++s == stages) { s = 0; phase ^= 1; }
+                    }
+                    continue;
+                }
                 const int bnc = t.bn / CG;
                 const int row0 = static_cast<int>(t.row0 + half * bnc);
                 const int rows = g.b_mn ? 64 : p.box_rows;      // of one copy
@@ -1050,7 +1193,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 const Gemm &g = work.g[q];
                 const Tile t = tile_of(ti, q);
                 int kb0, kb1;
-                k_range(q, &kb0, &kb1);
+                k_range(q, t, &kb0, &kb1);
                 // D fp32, A and B bf16, transposes, N, M
                 const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
                                        (static_cast<uint32_t>(g.a_mn) << 15) |
@@ -1069,10 +1212,12 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                     const uint32_t a = stage0 + s * stage_bytes;
                     const uint64_t da = smem_desc(a, g.a_mn);
                     const uint64_t db = smem_desc(a + kATile, g.b_mn);
+                    const int steps = DW ? BlockRows(t, kb).steps : kBlockK / 16;
 #pragma unroll
                     for (int k = 0; k < kBlockK / 16; ++k)
-                        mma_bf16<CG>(d, da + k * a_step, db + k * b_step, idesc,
-                                     kb > kb0 || k > 0);
+                        if (!DW || k < steps)
+                            mma_bf16<CG>(d, da + k * a_step, db + k * b_step, idesc,
+                                         kb > kb0 || k > 0);
                     mma_commit<CG>(smem_addr(&h->empty[s]), pair);
                     if (++s == stages) { s = 0; phase ^= 1; }
                 }
@@ -1089,22 +1234,22 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                                  (n & 1) * kMaxBn;
             begin(ti);
             if (split > 1) {        // joined below
-                (void)wait_for_tile(n, q);
+                (void)wait_for_tile(n, q, t);
                 fence_after();
                 break;
             }
             const uint32_t done = map_rank(smem_addr(&h->acc_empty[n & 1]),
                                            CG == 2 ? lead : cluster_rank());
             auto finish = [&](auto &part_of, auto out_of_tmem) {
-                if (!wait_for_tile(n, q)) return false;
+                if (!wait_for_tile(n, q, t)) return false;
                 fence_after();
                 out_of_tmem(part_of);
                 return true;
             };
             const int m0 = t.m0 + half * m_cta_rows;
             bool ok;
-            auto wide = [&](auto &w) { finish_wide(w, stash, acc, done, nullptr, 0); };
-            if (work.p[q].vectors && !GATED && work.g[q].residual) {
+            auto wide = [&](auto &w) { finish_wide<DW>(w, stash, acc, done, nullptr, 0); };
+            if (!DW && work.p[q].vectors && !GATED && work.g[q].residual) {
                 WidePart<GATED, !GATED> part_of(work.g[q], t, m0, quarter, side, sides, lane, 0,
                                                 t.bn);
                 ok = finish(part_of, wide);
@@ -1115,14 +1260,14 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
             } else {
                 TilePart<GATED> part_of(work.g[q], t, m0, quarter, side, sides, lane, 0, t.bn);
                 ok = finish(part_of, [&](auto &w) {
-                    finish_tile<GATED>(w, acc, done, nullptr, 0);
+                    finish_tile<DW>(w, acc, done, nullptr, 0);
                 });
             }
             if (!ok) break;
         }
     }
     __syncwarp();
-    if (N == 1 && split > 1) {
+    if (N == 1 && !DW && split > 1) {
         const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         if (CG == 1) cluster_wait();        // every part has started
         if (side >= 0 && first_tile < tiles) {
@@ -1138,17 +1283,17 @@ gemm_tc_kernel(const __grid_constant__ Work<N> work) {
                 WidePart<GATED, !GATED> part_of(work.g[0], t, m0, quarter, side, sides, lane, from,
                                                 from + own);
                 cluster_sync();         // every part's sums have arrived
-                if (!*gave_up) finish_wide(part_of, stash, acc, 0, sums, split - 1);
+                if (!*gave_up) finish_wide<false>(part_of, stash, acc, 0, sums, split - 1);
             } else if (work.p[0].vectors) {
                 WidePart<GATED, false> part_of(work.g[0], t, m0, quarter, side, sides, lane, from,
                                                from + own);
                 cluster_sync();
-                if (!*gave_up) finish_wide(part_of, stash, acc, 0, sums, split - 1);
+                if (!*gave_up) finish_wide<false>(part_of, stash, acc, 0, sums, split - 1);
             } else {
                 TilePart<GATED> part_of(work.g[0], t, m0, quarter, side, sides, lane, from,
                                         from + own);
                 cluster_sync();
-                if (!*gave_up) finish_tile<GATED>(part_of, acc, 0, sums, split - 1);
+                if (!*gave_up) finish_tile<false>(part_of, acc, 0, sums, split - 1);
             }
         } else {
             cluster_sync();
@@ -1196,9 +1341,9 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int CG, bool GATED, int N>
-cudaError_t start(const Work<N> &work, int64_t grid, cudaStream_t stream) {
-    auto *kernel = gemm_tc_kernel<CG, GATED, N>;
+template <int CG, bool GATED, int N, bool DW = false>
+cudaError_t start(const Work<N, DW> &work, int64_t grid, cudaStream_t stream) {
+    auto *kernel = gemm_tc_kernel<CG, GATED, N, DW>;
     const int cluster = CG << (N == 1 ? work.p[0].log_split : 0);
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kSmemBytes);
@@ -1228,7 +1373,7 @@ struct Slots {
 };
 
 int ask_active_clusters(int size, int num_sms) {
-    auto *kernel = gemm_tc_kernel<1, false, 1>;
+    auto *kernel = gemm_tc_kernel<1, false, 1, false>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(size));
     cfg.blockDim = dim3(kTcThreads);
@@ -1439,7 +1584,14 @@ bool describe(const Gemm &g, const Cut &cut, TcPlan *plan, CUtensorMap *map) {
         p.box_rows = p.bn / cut.cg;
     }
     bool ok;
-    if (g.a_mn) {
+    if (g.a_mn && g.E) {
+        const cuuint64_t row = static_cast<cuuint64_t>(g.M) * 2;
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(g.M), static_cast<cuuint64_t>(g.K),
+                                    static_cast<cuuint64_t>(g.E)};
+        const cuuint64_t strides[2] = {row, row * g.K};
+        const cuuint32_t box[3] = {64, 64, 1};
+        ok = encode(&map[0], g.a, 3, dims, strides, box);
+    } else if (g.a_mn) {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.M), static_cast<cuuint64_t>(g.K)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.M) * 2};
         const cuuint32_t box[2] = {64, 64};
@@ -1538,6 +1690,42 @@ bool launch_two_gemms_tc(const Gemm *g, const BiasSum &bias, int num_sms, cudaSt
                           static_cast<int64_t>(work.p[1].m_tiles) * work.p[1].n_tiles;
     const int64_t slots = num_sms / 2;
     *err = start<2, false>(work, 2 * (units < slots ? units : slots), stream);
+    return true;
+}
+
+// Pairs of CTAs: an expert's tile is 256 inputs by up to 256 features, all its rows
+// in one sum.  Narrower while that leaves pairs without a tile.
+bool launch_group_dweight_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err) {
+    if (!can_copy(g)) return false;
+    Work<1, true> work;
+    work.g[0] = g;
+    work.tiles0 = 0;
+    work.bias = {};
+    TcPlan &p = work.p[0];
+    p = {};
+    p.gather = g.row_token != nullptr;
+    p.vectors = g.M % 8 == 0 && aligned16(g.out);
+    p.m_tiles = static_cast<int>(ceil_div(g.M, 256));
+    const int64_t slots = num_sms / 2;
+    int most = kMaxBn;
+    while (most > 64 && g.E * p.m_tiles * ceil_div(g.N, most) < slots) most /= 2;
+    p.bn = even_columns(g, 2, most);
+    p.n_tiles = static_cast<int>(ceil_div(g.N, p.bn));
+    const int64_t tiles = static_cast<int64_t>(g.E) * p.m_tiles * p.n_tiles;
+    if (tiles > INT32_MAX) return false;
+    const cuuint64_t dims[2][2] = {
+        {static_cast<cuuint64_t>(g.M), static_cast<cuuint64_t>(g.a_rows)},
+        {static_cast<cuuint64_t>(g.N), static_cast<cuuint64_t>(g.b_rows)}};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(g.M) * 2,
+                                   static_cast<cuuint64_t>(g.b_pitch) * 2};
+    const cuuint32_t block[2] = {64, 64}, rows[2] = {64, 1};
+    for (int i = 0; i < 2; ++i) {
+        const void *operand = i ? g.b : g.a;
+        if (!encode(&work.map[0][i], operand, 2, dims[i], &strides[i], block) ||
+            !encode(&work.map[0][2 + i], operand, 2, dims[i], &strides[i], rows))
+            return false;
+    }
+    *err = start<2, false, 1, true>(work, 2 * (tiles < slots ? tiles : slots), stream);
     return true;
 }
 

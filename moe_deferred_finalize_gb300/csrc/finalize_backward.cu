@@ -1,0 +1,496 @@
+// Gradients of the finalize, of the row gather and of the top-K gate.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "tc.cuh"
+#include "train.cuh"
+#include "vec.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace moef {
+namespace {
+
+constexpr int kMaxThreads = 512;
+constexpr int kWarps = kMaxThreads / 32;
+constexpr int kMaxSplits = 8;
+constexpr int kMaxVpt = 8;
+constexpr int kMaxPartials = 1024;      // rows of dgamma's sums
+constexpr int kSlots = 8;               // of a token, in flight at a time
+
+// How one launch is cut: `splits` CTAs (a cluster) take a token's slices of
+// `slice` vectors; clusters go round the tokens.
+struct Cut {
+    int splits, slice, threads, vpt, nvec;
+    int64_t clusters;
+};
+
+// acc[u] summed over the warp; lane 4 u has sum u.  Halving the number of values
+// at each of the first steps takes 9 shuffles, 40 for eight sums by themselves.
+__device__ __forceinline__ float warp_sum8(float (&acc)[8], int lane) {
+#pragma unroll
+    for (int half = 4, bit = 16; half >= 1; half >>= 1, bit >>= 1) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int u = 0; u < half; ++u) {
+            const float give = up ? acc[u] : acc[u + half];
+            const float keep = up ? acc[u + half] : acc[u];
+            acc[u] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, bit);
+        }
+    }
+    float v = acc[0];
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+    return v;
+}
+
+template <int VPT, int VEC, bool NORM, bool CLUSTER>
+__global__ void __launch_bounds__(kMaxThreads)
+finalize_backward_kernel(const __grid_constant__ FinalizeBackward p,
+                         const __grid_constant__ Cut cut) {
+    using Ops = VecOps<VEC>;
+    using V = typename Ops::V;
+    __shared__ int64_t s_row[2][MOEF_MAX_K];            // first value of the slot's row, -1: none
+    __shared__ float s_w[2][MOEF_MAX_K];
+    __shared__ float2 s_sum[2][kWarps];
+    __shared__ float s_dot[2][kWarps][MOEF_MAX_K];
+    __shared__ float2 s_part[2][kMaxSplits];            // the cluster's sums
+    __shared__ float s_parts[2][kMaxSplits][MOEF_MAX_K];
+    extern __shared__ float s_gamma[];                  // dgamma of this CTA's tokens
+
+    const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int warps = nt >> 5, K = p.K;
+    const int split = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+    const int64_t cluster = CLUSTER ? blockIdx.x / cut.splits : blockIdx.x;
+    const int v_begin = split * cut.slice, v_end = min(v_begin + cut.slice, cut.nvec);
+    const bool sums_gamma = NORM && p.dgamma;
+    if (CLUSTER) cluster_arrive();
+    if (sums_gamma)
+        for (int i = tid; i < VPT * VEC * nt; i += nt) s_gamma[i] = 0.f;
+    auto gamma_at = [&](int j, int q) -> float & {      // four values of a thread side by side
+        return VEC == 8 ? s_gamma[((j * 2 + (q >> 2)) * nt + tid) * 4 + (q & 3)]
+                        : s_gamma[j * nt + tid];
+    };
+    wait_previous_kernel();
+    allow_next_kernel();
+    if (CLUSTER) cluster_wait();
+
+    int64_t next_row = -1;
+    float next_w = 0.f;
+    auto fetch = [&](int64_t t) {
+        if (t < p.T && tid < K) {
+            const int64_t slot = t * K + tid;
+            const int row = __ldg(p.idx + slot);
+            next_row = row >= 0 && row < p.P ? static_cast<int64_t>(row) * p.H : -1;
+            next_w = p.drows ? decode_weight(p.weights, p.wkind, slot) * p.routed_scale : 0.f;
+        }
+    };
+    // the CTA's dot products of token t, its warps' added in order
+    auto dots = [&](int par) {
+        float v = 0.f;
+        for (int w = 0; w < warps; ++w) v += s_dot[par][w][tid];
+        return v;
+    };
+    fetch(cluster);
+    int par = 0;
+    int64_t last = -1;
+    for (int64_t t = cluster; t < p.T; t += cut.clusters, par ^= 1) {
+        const int64_t tok = t * p.H;
+        if (tid < K) {
+            s_row[par][tid] = next_row;
+            s_w[par][tid] = next_w;
+        }
+        fetch(t + cut.clusters);
+        float inv = 0.f, mean = 0.f;
+        V dn[VPT] = {}, r[VPT] = {};
+        if constexpr (NORM) {
+            float2 sum = make_float2(0.f, 0.f);         // of r^2 and dnorm gamma r
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = v_begin + tid + j * nt;
+                if (v < v_end) {
+                    const int64_t e = static_cast<int64_t>(v) * VEC;
+                    dn[j] = Ops::load(p.dnorm + tok + e);
+                    r[j] = Ops::load(p.r + tok + e);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = v_begin + tid + j * nt;
+                if (v < v_end) {
+                    float d[VEC], x[VEC], g[VEC];
+                    Ops::to_f32(dn[j], d);
+                    Ops::to_f32(r[j], x);
+                    Ops::to_f32(Ops::load_reused(p.gamma + static_cast<int64_t>(v) * VEC), g);
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) {
+                        sum.x = fmaf(x[q], x[q], sum.x);
+                        sum.y = fmaf(d[q] * g[q], x[q], sum.y);
+                    }
+                }
+            }
+            sum.x = warp_sum(sum.x);
+            sum.y = warp_sum(sum.y);
+            if (lane == 0) s_sum[par][warp] = sum;
+        }
+        __syncthreads();
+        if (!CLUSTER && last >= 0 && tid < K && p.dweights)
+            p.dweights[last * K + tid] = dots(par ^ 1) * p.routed_scale;
+        last = t;
+        if constexpr (NORM) {
+            float2 sum = make_float2(0.f, 0.f);
+            for (int w = 0; w < warps; ++w) {
+                sum.x += s_sum[par][w].x;
+                sum.y += s_sum[par][w].y;
+            }
+            if constexpr (CLUSTER) {
+                cg::cluster_group group = cg::this_cluster();
+                if (tid < cut.splits) *group.map_shared_rank(&s_part[par][split], tid) = sum;
+                group.sync();
+                sum = make_float2(0.f, 0.f);
+                for (int i = 0; i < cut.splits; ++i) {
+                    sum.x += s_part[par][i].x;
+                    sum.y += s_part[par][i].y;
+                }
+            }
+            inv = rsqrtf(sum.x / static_cast<float>(p.H) + p.eps);
+            mean = inv * inv * (sum.y / static_cast<float>(p.H));
+        }
+        for (int base = v_begin; base < v_end; base += nt * VPT) {
+            float dm[VPT][VEC];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = base + tid + j * nt;
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) dm[j][q] = 0.f;
+                if (v >= v_end) continue;
+                const int64_t e = static_cast<int64_t>(v) * VEC;
+                V d_out = {}, d_res = {};
+                if (p.dres) d_res = Ops::load(p.dres + tok + e);
+                if (p.dout) d_out = Ops::load(p.dout + tok + e);
+                Ops::to_f32(d_res, dm[j]);
+                float f[VEC];
+                if constexpr (NORM) {
+                    float d[VEC], x[VEC], g[VEC];
+                    Ops::to_f32(dn[j], d);
+                    Ops::to_f32(r[j], x);
+                    Ops::to_f32(Ops::load_reused(p.gamma + e), g);
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) {
+                        dm[j][q] = fmaf(inv, d[q] * g[q] - x[q] * mean, dm[j][q]);
+                        if (sums_gamma) gamma_at(j, q) += d[q] * x[q] * inv;
+                    }
+                }
+                if (p.dresidual) Ops::store(p.dresidual + tok + e, Ops::from_f32(dm[j]));
+                Ops::to_f32(d_out, f);
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) dm[j][q] += f[q];
+                if (p.dshared) Ops::store(p.dshared + tok + e, Ops::from_f32(dm[j]));
+            }
+            if (!p.drows && !p.dweights) continue;
+            for (int k0 = 0; k0 < K; k0 += kSlots) {
+                float acc[kSlots] = {};
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    const int v = base + tid + j * nt;
+                    if (v >= v_end) continue;
+                    const int64_t e = static_cast<int64_t>(v) * VEC;
+                    V x[kSlots] = {};
+                    if (p.dweights) {
+#pragma unroll
+                        for (int u = 0; u < kSlots; ++u)
+                            if (k0 + u < K && s_row[par][k0 + u] >= 0)
+                                x[u] = Ops::load_row(p.rows + s_row[par][k0 + u] + e);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kSlots; ++u) {
+                        if (k0 + u >= K || s_row[par][k0 + u] < 0) continue;
+                        float f[VEC];
+                        Ops::to_f32(x[u], f);
+#pragma unroll
+                        for (int q = 0; q < VEC; ++q) acc[u] = fmaf(f[q], dm[j][q], acc[u]);
+                        if (p.drows) {
+                            const float w = s_w[par][k0 + u];
+#pragma unroll
+                            for (int q = 0; q < VEC; ++q) f[q] = w * dm[j][q];
+                            Ops::store(p.drows + s_row[par][k0 + u] + e, Ops::from_f32(f));
+                        }
+                    }
+                }
+                const float v = warp_sum8(acc, lane);
+                const int k = k0 + (lane >> 2);
+                if ((lane & 3) == 0 && k < K) {
+                    float *at = &s_dot[par][warp][k];
+                    *at = base == v_begin ? v : *at + v;
+                }
+            }
+        }
+        if constexpr (CLUSTER) {
+            __syncthreads();
+            cg::cluster_group group = cg::this_cluster();
+            if (tid < K) *group.map_shared_rank(&s_parts[par][split][tid], 0) = dots(par);
+            group.sync();
+            if (split == 0 && tid < K && p.dweights) {
+                float v = 0.f;
+                for (int i = 0; i < cut.splits; ++i) v += s_parts[par][i][tid];
+                p.dweights[t * K + tid] = v * p.routed_scale;
+            }
+        }
+    }
+    if (!CLUSTER && last >= 0) {
+        __syncthreads();
+        if (tid < K && p.dweights) p.dweights[last * K + tid] = dots(par ^ 1) * p.routed_scale;
+    }
+    if (sums_gamma) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = v_begin + tid + j * nt;
+            if (v < v_end)
+#pragma unroll
+                for (int q = 0; q < VEC; ++q)
+                    p.partial[cluster * p.H + static_cast<int64_t>(v) * VEC + q] = gamma_at(j, q);
+        }
+    }
+}
+
+// dgamma = the column sums of partial [rows, H]: 32 columns a CTA, its eight
+// warps every eighth row each, added in order.
+__global__ void __launch_bounds__(256)
+gamma_sum_kernel(const float *partial, uint16_t *dgamma, int rows, int H) {
+    __shared__ float sums[8][32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+    wait_previous_kernel();
+    allow_next_kernel();
+    float sum = 0.f;
+    if (c < H) {
+#pragma unroll 8
+        for (int i = warp; i < rows; i += 8) sum += partial[static_cast<int64_t>(i) * H + c];
+    }
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && c < H) {
+#pragma unroll
+        for (int w = 1; w < 8; ++w) sum += sums[w][lane];
+        dgamma[c] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
+    }
+}
+
+template <typename... Params, typename... Args>
+cudaError_t start(void (*kernel)(Params...), int64_t grid, int threads, size_t smem, int cluster,
+                  cudaStream_t stream, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+template <int VPT, int VEC, bool NORM, bool CLUSTER>
+cudaError_t start_backward(const FinalizeBackward &p, const Cut &cut, cudaStream_t stream) {
+    auto *kernel = finalize_backward_kernel<VPT, VEC, NORM, CLUSTER>;
+    const size_t smem = NORM && p.dgamma ? sizeof(float) * VPT * VEC * cut.threads : 0;
+    if (smem > 32 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (err != cudaSuccess) return err;
+    }
+    return start(kernel, cut.clusters * cut.splits, cut.threads, smem, cut.splits, stream, p, cut);
+}
+
+template <int VPT, int VEC>
+cudaError_t start_backward(const FinalizeBackward &p, const Cut &cut, cudaStream_t stream) {
+    if (p.dnorm)
+        return cut.splits > 1 ? start_backward<VPT, VEC, true, true>(p, cut, stream)
+                              : start_backward<VPT, VEC, true, false>(p, cut, stream);
+    return cut.splits > 1 ? start_backward<VPT, VEC, false, true>(p, cut, stream)
+                          : start_backward<VPT, VEC, false, false>(p, cut, stream);
+}
+
+template <int VEC>
+cudaError_t start_backward(const FinalizeBackward &p, const Cut &cut, cudaStream_t stream) {
+    switch (cut.vpt) {
+        case 1: return start_backward<1, VEC>(p, cut, stream);
+        case 2: return start_backward<2, VEC>(p, cut, stream);
+        case 4: return start_backward<4, VEC>(p, cut, stream);
+        default: return start_backward<8, VEC>(p, cut, stream);
+    }
+}
+
+bool vector_rows(int H, std::initializer_list<const void *> pointers) {
+    uintptr_t bits = 0;
+    for (const void *q : pointers) bits |= reinterpret_cast<uintptr_t>(q);
+    return H % 8 == 0 && bits % 16 == 0;
+}
+
+// ------------------------------------------------------------- row gather
+
+constexpr int kUnpermuteThreads = 128;
+
+// A thread sums one vector of a token: its slots' rows, eight loads in flight, and
+// what is added.
+template <int VEC>
+__global__ void __launch_bounds__(kUnpermuteThreads)
+unpermute_kernel(const __grid_constant__ Unpermute p, int nvec, int slices) {
+    using Ops = VecOps<VEC>;
+    using V = typename Ops::V;
+    __shared__ int64_t s_row[MOEF_MAX_K];
+    const int64_t t = blockIdx.x / slices;
+    const int v = (blockIdx.x - t * slices) * kUnpermuteThreads + threadIdx.x;
+    wait_previous_kernel();
+    allow_next_kernel();
+    if (threadIdx.x < p.K) {
+        const int row = __ldg(p.idx + t * p.K + threadIdx.x);
+        s_row[threadIdx.x] = row >= 0 && row < p.P ? static_cast<int64_t>(row) * p.H : -1;
+    }
+    const int64_t e = static_cast<int64_t>(v) * VEC, at = t * p.H + e;
+    V add[2] = {};
+    if (v < nvec) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (p.add[i]) add[i] = Ops::load(p.add[i] + at);
+    }
+    __syncthreads();
+    if (v >= nvec) return;
+    float acc[VEC] = {}, f[VEC];
+    for (int k0 = 0; k0 < p.K; k0 += kSlots) {
+        V x[kSlots] = {};
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u)
+            if (k0 + u < p.K && s_row[k0 + u] >= 0) x[u] = Ops::load_row(p.rows + s_row[k0 + u] + e);
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u) {
+            Ops::to_f32(x[u], f);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) acc[q] += f[q];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        Ops::to_f32(add[i], f);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) acc[q] += f[q];
+    }
+    Ops::store(p.out + at, Ops::from_f32(acc));
+}
+
+// ------------------------------------------------------------------- gate
+
+constexpr int kGateThreads = 128;
+
+// A warp takes a token: lane k has slot k, and every lane writes its pieces of the
+// row, zeros but for the chosen experts.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kGateThreads)
+gate_backward_kernel(const __grid_constant__ GateBackward p) {
+    const int lane = threadIdx.x & 31, K = p.K;
+    wait_previous_kernel();
+    allow_next_kernel();
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kGateThreads / 32);
+    for (int64_t t = blockIdx.x * static_cast<int64_t>(kGateThreads / 32) + threadIdx.x / 32;
+         t < p.T; t += warps) {
+        int id = -1;
+        float w = 0.f, dw = 0.f;
+        if (lane < K) {
+            id = p.ids[t * K + lane];
+            if (id < 0 || id >= p.E) id = -1;
+            if (id >= 0) {
+                w = p.weights[t * K + lane];
+                dw = p.dweights[t * K + lane];
+            }
+        }
+        float d = w * (dw - warp_sum(w * dw));
+        if (p.kind == MOEF_GATE_SIGMOID && id >= 0)
+            d *= 1.f / (1.f + expf(p.logits[t * p.E + id]));
+        T *row = static_cast<T *>(p.dlogits) + t * p.E;
+        for (int c0 = 0; c0 < p.E; c0 += 32 * VEC) {
+            const int c = c0 + lane * VEC;
+            float f[VEC] = {};
+            for (int k = 0; k < K; ++k) {
+                const int at = __shfl_sync(0xFFFFFFFFu, id, k) - c;
+                const float dk = __shfl_sync(0xFFFFFFFFu, d, k);
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) f[q] += at == q ? dk : 0.f;
+            }
+            if (c >= p.E) continue;
+            if constexpr (VEC == 1) {
+                if constexpr (sizeof(T) == 4) row[c] = f[0];
+                else row[c] = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+            } else if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<float4 *>(row + c) = make_float4(f[0], f[1], f[2], f[3]);
+            } else {
+                *reinterpret_cast<uint4 *>(row + c) = VecOps<8>::from_f32(f);
+            }
+        }
+    }
+}
+
+}  // namespace
+
+int finalize_backward_partials(int T) { return T < kMaxPartials ? T : kMaxPartials; }
+
+bool finalize_backward_fits(int64_t nvec) {
+    return nvec <= static_cast<int64_t>(kMaxThreads) * kMaxVpt * kMaxSplits;
+}
+
+cudaError_t launch_finalize_backward(const FinalizeBackward &p, int num_sms,
+                                     cudaStream_t stream) {
+    const bool vec = vector_rows(p.H, {p.rows, p.r, p.gamma, p.dout, p.dres, p.dnorm, p.drows,
+                                       p.dshared, p.dresidual});
+    Cut cut;
+    cut.nvec = vec ? p.H / 8 : p.H;
+    cut.splits = 1;
+    while (cut.splits < kMaxSplits &&
+           (2 * static_cast<int64_t>(p.T) * cut.splits <= 4 * num_sms && cut.nvec >= 64 * cut.splits ||
+            p.dnorm && cut.nvec > static_cast<int64_t>(kMaxThreads) * kMaxVpt * cut.splits))
+        cut.splits *= 2;
+    cut.slice = (cut.nvec - 1) / cut.splits + 1;
+    cut.splits = (cut.nvec - 1) / cut.slice + 1;        // none is empty
+    cut.vpt = 1;
+    while (cut.vpt < kMaxVpt && cut.slice > kMaxThreads * cut.vpt) cut.vpt *= 2;
+    const int need = (cut.slice - 1) / cut.vpt + 1;
+    cut.threads = need < kMaxThreads ? (need + 31) / 32 * 32 : kMaxThreads;
+    int64_t clusters = static_cast<int64_t>(num_sms) * (2048 / cut.threads) / 2 / cut.splits;
+    if (clusters < 1) clusters = 1;
+    if (clusters > kMaxPartials) clusters = kMaxPartials;
+    cut.clusters = clusters < p.T ? clusters : p.T;
+    cudaError_t err = vec ? start_backward<8>(p, cut, stream) : start_backward<1>(p, cut, stream);
+    if (err == cudaSuccess && p.dgamma)
+        err = start(gamma_sum_kernel, (p.H - 1) / 32 + 1, 256, 0, 1, stream, p.partial, p.dgamma,
+                    static_cast<int>(cut.clusters), p.H);
+    return err;
+}
+
+int64_t unpermute_ctas(int T, int H) {
+    return static_cast<int64_t>(T) * ((H - 1) / kUnpermuteThreads + 1);
+}
+
+cudaError_t launch_unpermute(const Unpermute &p, cudaStream_t stream) {
+    const bool vec = vector_rows(p.H, {p.rows, p.add[0], p.add[1], p.out});
+    const int nvec = vec ? p.H / 8 : p.H;
+    const int slices = (nvec - 1) / kUnpermuteThreads + 1;
+    const int64_t grid = static_cast<int64_t>(p.T) * slices;
+    return vec ? start(unpermute_kernel<8>, grid, kUnpermuteThreads, 0, 1, stream, p, nvec, slices)
+               : start(unpermute_kernel<1>, grid, kUnpermuteThreads, 0, 1, stream, p, nvec, slices);
+}
+
+cudaError_t launch_gate_backward(const GateBackward &p, int num_sms, cudaStream_t stream) {
+    const int64_t need = (static_cast<int64_t>(p.T) + kGateThreads / 32 - 1) / (kGateThreads / 32);
+    const int64_t most = static_cast<int64_t>(num_sms) * 16;
+    const int64_t grid = need < most ? need : most;
+    const bool vec = reinterpret_cast<uintptr_t>(p.dlogits) % 16 == 0 && p.E % (p.f32 ? 4 : 8) == 0;
+    if (p.f32)
+        return start(vec ? gate_backward_kernel<float, 4> : gate_backward_kernel<float, 1>, grid,
+                     kGateThreads, 0, 1, stream, p);
+    return start(vec ? gate_backward_kernel<uint16_t, 8> : gate_backward_kernel<uint16_t, 1>, grid,
+                 kGateThreads, 0, 1, stream, p);
+}
+
+}  // namespace moef
