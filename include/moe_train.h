@@ -158,15 +158,18 @@ moef_status moe_expert_linear_save(const void *x, int64_t T, const int32_t *row_
  *   dweight        bf16 [E, 2I, H] ([E, N, K]) or NULL; zeros for an expert
  *                  without rows
  *   dbias          bf16 [E, 2I] ([E, N]) or NULL          (at least one non-NULL)
- *   workspace      moe_expert_backward_workspace_bytes(P, cols) bytes, cols the
- *                  width of dz (2I, or N), 16-byte aligned
+ *   workspace      moe_expert_backward_workspace_bytes(P, cols, inputs) bytes,
+ *                  16-byte aligned: cols the width of dz (2I, or N); inputs the
+ *                  width of x (H, or K) when dweight is wanted and x cannot be
+ *                  copied as it lies (with row_token, when the width is not a
+ *                  multiple of 8, or x not 16-byte aligned), else 0
  *
  * Rows of no expert are read by nothing that counts: they may hold anything.
  * Rows at or past P, and experts whose offset is negative, take no part.  dz
  * is rounded to bf16 for the two products; dbias sums it before that.  A
  * row_token outside [0, T) counts as a row of zeros in dweight.
  */
-size_t moe_expert_backward_workspace_bytes(int64_t P, int cols);
+size_t moe_expert_backward_workspace_bytes(int64_t P, int cols, int inputs);
 
 moef_status moe_expert_gated_ffn_backward(const void *dout, const void *x, int64_t T,
                                           const int32_t *row_token, const int32_t *offsets,

@@ -10,10 +10,10 @@ from typing import Optional, Sequence
 import torch
 
 from . import _abi
-from ._abi import (_WDTYPE, GATE, WKIND, _check, _device, _elsewhere, _on, _ptr, _stream,
-                   _under)
-from ._ffn import (_BF16, _I32, _OUT_TYPE, _activation, _int, _matrix, _optional, _output,
-                   _raise, _workspace_bytes)
+from ._abi import (_WCODE, _WDTYPE, GATE, WKIND, _check, _device, _elsewhere, _on, _ptr,
+                   _stream, _under)
+from ._ffn import (_BF16, _I32, _OUT_TYPE, ACTIVATION, _activation, _fast_device, _int, _matrix,
+                   _optional, _output, _raise, _raw_stream, _workspace_bytes)
 
 _F32 = (torch.float32,)
 BLOCK = 256         # values of an 8-bit AdamW state that share a scale
@@ -53,7 +53,7 @@ def _lib():
                                       [i32] * 3 + [vp, sz, vp]),
             "moe_unpermute": (i32, [vp, i64] + [vp] * 4 + [i32] * 3 + [vp]),
             "moe_topk_route_backward": (i32, [vp] * 4 + [i32] * 4 + [vp, i32, vp]),
-            "moe_expert_backward_workspace_bytes": (sz, [i64, i32]),
+            "moe_expert_backward_workspace_bytes": (sz, [i64, i32, i32]),
             "moe_expert_gated_ffn_backward": (i32, expert),
             "moe_expert_linear_backward": (i32, expert),
             "moe_adamw_step": (i32, [ctypes.POINTER(AdamWTensor), i32,
@@ -64,6 +64,44 @@ def _lib():
             fn.restype, fn.argtypes = restype, argtypes
         _LIB = lib
     return _LIB
+
+
+_ADDRESS = {}
+
+
+def _address(name):
+    """The entry point's address, for the _fastcall extension."""
+    if name not in _ADDRESS:
+        _ADDRESS[name] = ctypes.cast(getattr(_lib(), name), ctypes.c_void_p).value
+    return _ADDRESS[name]
+
+
+# what the one-pass calls below leave to the checks that name the problem
+_REFUSED = (AttributeError, IndexError, KeyError, TypeError, ValueError, RuntimeError,
+            BufferError)
+
+
+def _describe(t):
+    return None if t is None else _abi._TO_DLPACK(t)
+
+
+class _Outputs:
+    """Outputs of a one-pass call: a dict of them, and what the extension is
+    given: descriptions of those that the caller gave, the addresses of those
+    made here."""
+
+    def __init__(self):
+        self.res, self.at = {}, []
+
+    def add(self, name, wanted, given, shape, dtype, device):
+        if given is not None:
+            self.res[name] = given
+            self.at.append(_abi._TO_DLPACK(given))
+        elif wanted:
+            self.res[name] = t = torch.empty(shape, dtype=dtype, device=device)
+            self.at.append(t.data_ptr())
+        else:
+            self.at.append(None)
 
 
 def finalize_backward_workspace_bytes(T: int, H: int) -> int:
@@ -110,6 +148,12 @@ def moe_finalize_backward(permuted_out: torch.Tensor, idx_map: torch.Tensor,
         for name in ("norm", "residual", "separate"):
             del args[name]
         return _under(moe_finalize_backward, permuted_out.device, args)
+    res = _fast_finalize_backward(permuted_out, idx_map, weights, wkind, dout, routed_scale,
+                                  dresidual_out, dnorm_out, residual_out, gamma, eps, want_drows,
+                                  want_dweights, want_dgamma, drows, dweights, dshared,
+                                  dresidual, dgamma, workspace, stream)
+    if res is not None:
+        return res
     if wkind not in WKIND:
         raise ValueError(f"wkind must be one of {sorted(WKIND)}")
     P, H = _matrix(permuted_out, "permuted_out", "[P, H]")
@@ -167,6 +211,86 @@ def moe_finalize_backward(permuted_out: torch.Tensor, idx_map: torch.Tensor,
     return res
 
 
+def _fast_finalize_backward(permuted_out, idx_map, weights, wkind, dout, routed_scale,
+                            dresidual_out, dnorm_out, residual_out, gamma, eps, want_drows,
+                            want_dweights, want_dgamma, drows, dweights, dshared, dresidual,
+                            dgamma, workspace, stream):
+    """moe_finalize_backward in one pass through the _fastcall extension, which
+    checks DLPack descriptions of the tensors; None when it is missing or a check
+    fails."""
+    fast = _abi._fastcall()
+    norm = dnorm_out is not None
+    residual = norm or dresidual_out is not None
+    if not residual and (dout is None or dshared is not None or dresidual is not None) or \
+            dgamma is not None and not norm:
+        return None
+    try:
+        dev = _fast_device(fast, permuted_out)
+        if dev is None:
+            return None
+        device, shape = permuted_out.device, (idx_map.shape[0], permuted_out.shape[1])
+        separate = residual and dout is not None
+        if residual and not separate and dshared is not None:
+            return None
+        o = _Outputs()
+        o.add("drows", want_drows, drows, permuted_out.shape, torch.bfloat16, device)
+        o.add("dweights", want_dweights, dweights, idx_map.shape, torch.float32, device)
+        o.add("dshared", separate, dshared, shape, torch.bfloat16, device)
+        o.add("dresidual", residual, dresidual, shape, torch.bfloat16, device)
+        o.add("dgamma", norm and want_dgamma, dgamma, shape[1:], torch.bfloat16, device)
+        res = o.res
+        if not res:
+            return None
+        if residual and not separate:
+            res["dshared"] = res["dresidual"]
+        nbytes, at = 0, None
+        if "dgamma" in res:
+            if workspace is not None:
+                nbytes = _workspace_bytes(workspace, device)
+            else:
+                nbytes = fast.call_size(_address("moe_finalize_backward_workspace_bytes"), *shape)
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes \
+                    else None
+            at = _ptr(workspace)
+        code, bits = _WCODE[wkind]
+        st = fast.checked_finalize_backward(
+            _address("moe_finalize_backward"), WKIND[wkind], code, bits, routed_scale, eps, dev,
+            _raw_stream(stream, dev), at, nbytes, _abi._TO_DLPACK(permuted_out),
+            _abi._TO_DLPACK(idx_map), _abi._TO_DLPACK(weights), _describe(residual_out),
+            _describe(gamma), _describe(dout), _describe(dresidual_out), _describe(dnorm_out),
+            *o.at)
+    except _REFUSED:
+        return None
+    if st < 0:
+        return None
+    _raise(st, "moe_finalize_backward")
+    return res
+
+
+def _fast_unpermute(rows, idx_map, adds, out, stream):
+    """unpermute_tokens likewise."""
+    fast = _abi._fastcall()
+    try:
+        dev = _fast_device(fast, rows)
+        if dev is None:
+            return None
+        if out is None:
+            out = torch.empty((idx_map.shape[0], rows.shape[1]), dtype=torch.bfloat16,
+                              device=rows.device)
+            at = out.data_ptr()
+        else:
+            at = _abi._TO_DLPACK(out)
+        st = fast.checked_unpermute(_address("moe_unpermute"), dev, _raw_stream(stream, dev),
+                                    _abi._TO_DLPACK(rows), _abi._TO_DLPACK(idx_map),
+                                    _describe(adds[0]), _describe(adds[1]), at)
+    except _REFUSED:
+        return None
+    if st < 0:
+        return None
+    _raise(st, "moe_unpermute")
+    return out
+
+
 def unpermute_tokens(rows: torch.Tensor, idx_map: torch.Tensor, *, add=None,
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rows grouped by expert back to their tokens (include/moe_train.h): out
@@ -178,23 +302,51 @@ def unpermute_tokens(rows: torch.Tensor, idx_map: torch.Tensor, *, add=None,
     sequence of at most two; ``out`` may be one of them."""
     if stream is not None and out is None and _elsewhere(stream, _device(rows)):
         return _under(unpermute_tokens, rows.device, dict(locals()))
+    adds = [] if add is None else [add] if isinstance(add, torch.Tensor) else list(add)
+    if len(adds) > 2:
+        raise ValueError("add is at most two tensors")
+    adds += [None] * (2 - len(adds))
+    res = _fast_unpermute(rows, idx_map, adds, out, stream)
+    if res is not None:
+        return res
     P, H = _matrix(rows, "rows", "[P, H]")
     T, K = _matrix(idx_map, "idx_map", "[T, K]")
     dev = rows.device
     _check(rows, "rows", _BF16, (P, H), dev)
     _check(idx_map, "idx_map", _I32, (T, K), dev)
-    adds = [] if add is None else [add] if isinstance(add, torch.Tensor) else list(add)
-    if len(adds) > 2:
-        raise ValueError("add is at most two tensors")
     for t in adds:
-        _check(t, "add", _BF16, (T, H), dev)
+        _optional(t, "add", (T, H), dev)
     out = _output(out, "out", torch.bfloat16, (T, H), dev)
-    adds += [None] * (2 - len(adds))
     with _on(dev):
         st = _lib().moe_unpermute(_ptr(rows), P, _ptr(idx_map), _ptr(adds[0]), _ptr(adds[1]),
                                   _ptr(out), _int(T), _int(K), _int(H), _stream(stream, dev))
     _raise(st, "moe_unpermute")
     return out
+
+
+def _fast_gate_backward(dweights, weights, expert_ids, E, kind, logits, out_dtype, dlogits,
+                        stream):
+    """topk_route_backward likewise."""
+    fast = _abi._fastcall()
+    try:
+        dev = _fast_device(fast, dweights)
+        if dev is None:
+            return None
+        if dlogits is None:
+            dlogits = torch.empty((dweights.shape[0], E), dtype=out_dtype, device=dweights.device)
+            at = dlogits.data_ptr()
+        else:
+            at = _abi._TO_DLPACK(dlogits)
+        st = fast.checked_gate_backward(
+            _address("moe_topk_route_backward"), dev, _raw_stream(stream, dev), E, GATE[kind],
+            _OUT_TYPE[dlogits.dtype], _abi._TO_DLPACK(dweights), _abi._TO_DLPACK(weights),
+            _abi._TO_DLPACK(expert_ids), _describe(logits), at)
+    except _REFUSED:
+        return None
+    if st < 0:
+        return None
+    _raise(st, "moe_topk_route_backward")
+    return dlogits
 
 
 def topk_route_backward(dweights: torch.Tensor, weights: torch.Tensor, expert_ids: torch.Tensor,
@@ -209,6 +361,10 @@ def topk_route_backward(dweights: torch.Tensor, weights: torch.Tensor, expert_id
     whose id is outside [0, E) (padding) count for nothing."""
     if stream is not None and dlogits is None and _elsewhere(stream, _device(dweights)):
         return _under(topk_route_backward, dweights.device, dict(locals()))
+    res = _fast_gate_backward(dweights, weights, expert_ids, E, kind, logits, out_dtype, dlogits,
+                              stream)
+    if res is not None:
+        return res
     if kind not in GATE:
         raise ValueError(f"kind must be one of {sorted(GATE)}")
     T, K = _matrix(dweights, "dweights", "[T, K]")
@@ -233,15 +389,60 @@ def topk_route_backward(dweights: torch.Tensor, weights: torch.Tensor, expert_id
     return dlogits
 
 
-def expert_backward_workspace_bytes(P: int, cols: int) -> int:
+def expert_backward_workspace_bytes(P: int, cols: int, inputs: int = 0) -> int:
     """Bytes of workspace the expert products' backward calls need for P rows of
-    ``cols`` features before the activation (2I gated, N linear)."""
-    return int(_lib().moe_expert_backward_workspace_bytes(int(P), _int(int(cols))))
+    ``cols`` features before the activation (2I gated, N linear).  ``inputs``:
+    the width of x, when dweight is wanted and x has a row map, a width that is
+    not a multiple of 8, or is not 16-byte aligned."""
+    return int(_lib().moe_expert_backward_workspace_bytes(int(P), _int(int(cols)),
+                                                          _int(int(inputs))))
+
+
+def _fast_expert_backward(where, gated, dout, x, row_token, offsets, counts, weight, preact,
+                          activation, want, given, workspace, stream):
+    """An expert product's backward call likewise."""
+    fast = _abi._fastcall()
+    try:
+        dev = _fast_device(fast, dout)
+        if dev is None:
+            return None
+        act, device = ACTIVATION[activation], dout.device
+        P, (E, cols, K) = dout.shape[0], weight.shape
+        o = _Outputs()
+        for name, wanted, t, shape in zip(("dx", "dweight", "dbias"), want, given,
+                                          ((P, K), (E, cols, K), (E, cols))):
+            o.add(name, wanted, t, shape, torch.bfloat16, device)
+        if not o.res:
+            return None
+        if workspace is not None:
+            nbytes = _workspace_bytes(workspace, device)
+        else:
+            copies = "dweight" in o.res and (row_token is not None or K % 8 or
+                                             x.data_ptr() % 16)
+            nbytes = fast.call_size3(_address("moe_expert_backward_workspace_bytes"), P, cols,
+                                     K if copies else 0)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        d = _abi._TO_DLPACK
+        st = fast.checked_expert_backward(
+            _address(where), gated, act, dev, _raw_stream(stream, dev), _ptr(workspace), nbytes,
+            d(dout), d(x), _describe(row_token), d(offsets), d(counts), d(weight),
+            _describe(preact), *o.at)
+    except _REFUSED:
+        return None
+    if st < 0:
+        return None
+    _raise(st, where)
+    return o.res
 
 
 def _expert_backward(where, gated, dout, x, row_token, offsets, counts, weight, preact,
                      activation, want_dx, want_dweight, want_dbias, dx, dweight, dbias,
                      workspace, stream):
+    res = _fast_expert_backward(where, gated, dout, x, row_token, offsets, counts, weight, preact,
+                                activation, (want_dx, want_dweight, want_dbias),
+                                (dx, dweight, dbias), workspace, stream)
+    if res is not None:
+        return res
     P, n = _matrix(dout, "dout", "[P, features]")
     dev = dout.device
     T, K = _matrix(x, "x", "[T, inputs]")
@@ -274,7 +475,8 @@ def _expert_backward(where, gated, dout, x, row_token, offsets, counts, weight, 
     if not res:
         raise ValueError("no gradient is wanted")
     if workspace is None:
-        nbytes = expert_backward_workspace_bytes(P, cols) if P and cols else 0
+        copies = "dweight" in res and (row_token is not None or K % 8 or x.data_ptr() % 16)
+        nbytes = expert_backward_workspace_bytes(P, cols, K if copies else 0) if P and cols else 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     else:
         nbytes = _workspace_bytes(workspace, dev)
@@ -303,7 +505,7 @@ def expert_gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor,
     expert are left as they were), "dweight" bf16 [E, 2I, H] (zeros for an
     expert without rows) and "dbias" bf16 [E, 2I].  x, row_token, offsets,
     counts and weight as in the forward call.  ``workspace``: at least
-    ``expert_backward_workspace_bytes(P, 2I)`` bytes, allocated when not given."""
+    ``expert_backward_workspace_bytes(P, 2I, H)`` bytes, allocated when not given."""
     if stream is not None and (workspace is None or want_dx and dx is None or
                                want_dweight and dweight is None or
                                want_dbias and dbias is None) and \

@@ -1,11 +1,11 @@
 // AdamW over many tensors (moe_adamw_step).
 //
 // Bound by HBM: a value with fp32 states and master moves 28 bytes for some forty
-// operations.  A warp takes 256 values of a tensor at a time, eight a lane, all its
-// loads in flight before the first use; the table of tensors comes with the launch's
-// parameters, so that nothing is copied or kept between calls, and a warp walks it
-// forward as its pieces go up.  256 values are also what an 8-bit state's scale is
-// for, so a warp has a scale's values to itself and finds the largest by shuffles.
+// operations.  A warp takes 256 values of a tensor, eight a lane, all its loads in
+// flight before the first use; the table of tensors comes with the launch's
+// parameters, so that nothing is copied or kept between calls.  256 values are also
+// what an 8-bit state's scale is for, so a warp has a scale's values to itself and
+// finds the largest by shuffles.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -19,7 +19,6 @@ namespace {
 constexpr int kPiece = 256;             // values a warp takes at a time
 constexpr int kAdamThreads = 256;
 constexpr int kPerCta = kAdamThreads / 32;
-constexpr int kCtasPerSm = 4;
 constexpr float kE4m3Max = 448.f, kE4m3Least = 0.001953125f;    // 2^-9
 constexpr int kFewTensors = 48, kManyTensors = 256;             // of a launch
 
@@ -31,12 +30,24 @@ struct Table {
 };
 static_assert(sizeof(Table<kManyTensors>) + sizeof(AdamWFactors) <= 32000, "launch parameters");
 
+// Within 2^-22 of the root and the reciprocal, which the step allows.
+__device__ __forceinline__ float fast_sqrt(float x) {
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Eight values of an array of `left` more (at least one), 16-byte accesses where
 // `whole`.
 __device__ __forceinline__ void load8(const float *p, float (&f)[8], int64_t left, bool whole) {
     if (whole) {
-        const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
-        const float4 b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+        const float4 a = reinterpret_cast<const float4 *>(p)[0];
+        const float4 b = reinterpret_cast<const float4 *>(p)[1];
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     } else {
@@ -46,7 +57,7 @@ __device__ __forceinline__ void load8(const float *p, float (&f)[8], int64_t lef
 }
 __device__ __forceinline__ void load8(const uint16_t *p, float (&f)[8], int64_t left, bool whole) {
     if (whole) {
-        VecOps<8>::to_f32(VecOps<8>::load(p), f);
+        VecOps<8>::to_f32(*reinterpret_cast<const uint4 *>(p), f);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -55,8 +66,8 @@ __device__ __forceinline__ void load8(const uint16_t *p, float (&f)[8], int64_t 
 }
 __device__ __forceinline__ void store8(float *p, const float (&f)[8], int64_t left, bool whole) {
     if (whole) {
-        __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
-        __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -77,7 +88,7 @@ __device__ __forceinline__ void store8(uint16_t *p, const float (&f)[8], int64_t
 // Eight e4m3 codes as they lie in memory.
 __device__ __forceinline__ uint2 load_codes(const uint8_t *p, int64_t left, bool whole) {
     uint2 c = make_uint2(0, 0);
-    if (whole) return __ldcs(reinterpret_cast<const uint2 *>(p));
+    if (whole) return *reinterpret_cast<const uint2 *>(p);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < left) (i < 4 ? c.x : c.y) |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
@@ -95,6 +106,20 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[8]) {
     }
 }
 
+// x / y and sqrt(x), rounded to nearest: an approximation and one step of Newton's
+// method on its residual, which an fma gives exactly (P. Markstein, IBM J. Res. Dev.
+// 34, 1990; the quotient needs y's reciprocal rounded to nearest).  Three and five
+// instructions where the library's functions take about ten each, which 8-bit states
+// are bound by otherwise.  Finite x in the ranges below.
+__device__ __forceinline__ float rounded_quotient(float x, float y, float reciprocal) {
+    const float q = x * reciprocal;
+    return fmaf(fmaf(-q, y, x), reciprocal, q);
+}
+__device__ __forceinline__ float rounded_sqrt(float x) {
+    const float r = rsqrtf(x), s = x * r;
+    return x > 1e-30f ? fmaf(fmaf(-s, s, x), 0.5f * r, s) : fast_sqrt(x);
+}
+
 // The piece's scale, and its values as codes of it.  ROOT: values above 0 keep a
 // code above 0.
 template <bool ROOT>
@@ -107,13 +132,16 @@ __device__ __forceinline__ void encode8(const float (&f)[8], uint8_t *p, float *
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     // A code is the rounding of the rounded quotient: a product with the scale's
     // reciprocal, off by a unit in the last place, would put one value in a million
-    // on the other side of a code's border, an eighth of the value away.
-    const float scale = most * (1.f / kE4m3Max), unit = scale > 0.f ? scale : 1.f;
+    // on the other side of a code's border, an eighth of the value away.  Scales
+    // whose reciprocal is not a normal number count as 0.
+    const float top = most * (1.f / kE4m3Max), scale = top > 1e-37f ? top : 0.f;
+    const float reciprocal = scale > 0.f ? __frcp_rn(scale) : 0.f;
     if (lane == 0) *scale_at = scale;
     uint32_t word[2] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 v = make_float2(__fdiv_rn(f[2 * i], unit), __fdiv_rn(f[2 * i + 1], unit));
+        float2 v = make_float2(rounded_quotient(f[2 * i], scale, reciprocal),
+                               rounded_quotient(f[2 * i + 1], scale, reciprocal));
         if constexpr (ROOT) {
             if (v.x > 0.f) v.x = fmaxf(v.x, kE4m3Least);
             if (v.y > 0.f) v.y = fmaxf(v.y, kE4m3Least);
@@ -131,15 +159,8 @@ __device__ __forceinline__ void encode8(const float (&f)[8], uint8_t *p, float *
     }
 }
 
-// Within 2^-22 of the root, as its use below allows.
-__device__ __forceinline__ float fast_sqrt(float x) {
-    float y;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 template <typename P, typename G, bool MASTER, bool EIGHT, int N>
-__global__ void __launch_bounds__(kAdamThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kAdamThreads)
 adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ AdamWFactors f) {
     __shared__ float s_bias[2];
     const int lane = threadIdx.x & 31;
@@ -149,8 +170,8 @@ adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ Ada
     if (f.device_step) {
         if (threadIdx.x < 2) {      // 1 - beta^step without cancellation
             const int step = max(1, *f.device_step);
-            const double b = -expm1(step * (threadIdx.x ? f.log_beta2 : f.log_beta1));
-            s_bias[threadIdx.x] = static_cast<float>(threadIdx.x ? sqrt(b) : b);
+            const float b = -expm1f(step * (threadIdx.x ? f.log_beta2 : f.log_beta1));
+            s_bias[threadIdx.x] = threadIdx.x ? sqrtf(b) : b;
         }
         __syncthreads();
         bias1 = s_bias[0];
@@ -161,11 +182,13 @@ adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ Ada
     const float root = 1.f / root_bias2;
     const float grad_scale = f.grad_scale ? *f.grad_scale : 1.f;
 
-    const uint32_t pieces = table.end[table.n - 1], stride = gridDim.x * kPerCta;
-    int at = 0;
-    for (uint32_t piece = blockIdx.x * kPerCta + threadIdx.x / 32; piece < pieces;
-         piece += stride) {
-        while (piece >= table.end[at]) ++at;
+    const uint32_t piece = blockIdx.x * kPerCta + threadIdx.x / 32;
+    if (piece < table.end[table.n - 1]) {
+        int at = 0;                     // the first tensor that ends behind the piece
+        for (int hi = table.n - 1; at < hi;) {
+            const int mid = (at + hi) >> 1;
+            if (table.end[mid] > piece) hi = mid; else at = mid + 1;
+        }
         const moef_adamw_tensor &t = table.t[at];
         const int64_t block = piece - (at ? table.end[at - 1] : 0);
         const int64_t i = block * kPiece + lane * 8, left = t.n - i;
@@ -201,8 +224,8 @@ adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ Ada
             g[k] *= grad_scale;
             m[k] = fmaf(f.rest1, g[k], __fmul_rn(f.beta1, m[k]));
             v[k] = fmaf(f.rest2, __fmul_rn(g[k], g[k]), __fmul_rn(f.beta2, v[k]));
-            const float s = EIGHT ? __fsqrt_rn(v[k]) : fast_sqrt(v[k]);
-            p[k] = keep * p[k] - __fdividef(step_size * m[k], fmaf(s, root, f.eps));
+            const float s = EIGHT ? rounded_sqrt(v[k]) : fast_sqrt(v[k]);
+            p[k] = keep * p[k] - step_size * m[k] * fast_reciprocal(fmaf(s, root, f.eps));
             if constexpr (EIGHT) v[k] = s;
         }
         if (left > 0) {
@@ -223,21 +246,20 @@ adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ Ada
 
 template <typename P, typename G, bool MASTER, bool EIGHT, int N>
 cudaError_t start_adamw(const moef_adamw_tensor *tensors, int n, const AdamWFactors &f,
-                        int num_sms, cudaStream_t stream) {
+                        cudaStream_t stream) {
     Table<N> table;
     int64_t pieces = 0;
     for (int i = 0; i < n; ++i) {
         table.t[i] = tensors[i];
         pieces += (tensors[i].n + kPiece - 1) / kPiece;
-        if (pieces > UINT32_MAX - (1 << 20)) return cudaErrorInvalidValue;
         table.end[i] = static_cast<uint32_t>(pieces);
     }
     table.n = n;
     if (pieces == 0) return cudaSuccess;
-    const int64_t need = (pieces + kPerCta - 1) / kPerCta;
-    const int64_t most = static_cast<int64_t>(num_sms) * kCtasPerSm;
+    // One piece a warp: 396M values with fp32 states and master take 1561 us (7.1
+    // TB/s), 1918 with four CTAs an SM that go round, 1590 with streaming hints.
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(need < most ? need : most));
+    cfg.gridDim = dim3(static_cast<unsigned>((pieces + kPerCta - 1) / kPerCta));
     cfg.blockDim = dim3(kAdamThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -249,13 +271,13 @@ cudaError_t start_adamw(const moef_adamw_tensor *tensors, int n, const AdamWFact
 }
 
 template <typename P, typename G, bool MASTER, bool EIGHT>
-cudaError_t start_all(const moef_adamw_tensor *tensors, int n, const AdamWFactors &f, int num_sms,
+cudaError_t start_all(const moef_adamw_tensor *tensors, int n, const AdamWFactors &f,
                       cudaStream_t stream) {
     if (n <= kFewTensors)
-        return start_adamw<P, G, MASTER, EIGHT, kFewTensors>(tensors, n, f, num_sms, stream);
+        return start_adamw<P, G, MASTER, EIGHT, kFewTensors>(tensors, n, f, stream);
     for (int i = 0; i < n; i += kManyTensors) {
         const cudaError_t err = start_adamw<P, G, MASTER, EIGHT, kManyTensors>(
-            tensors + i, n - i < kManyTensors ? n - i : kManyTensors, f, num_sms, stream);
+            tensors + i, n - i < kManyTensors ? n - i : kManyTensors, f, stream);
         if (err != cudaSuccess) return err;
     }
     return cudaSuccess;
@@ -265,9 +287,9 @@ cudaError_t start_all(const moef_adamw_tensor *tensors, int n, const AdamWFactor
 
 cudaError_t launch_adamw(const moef_adamw_tensor *tensors, int n, const AdamWFactors &f,
                          int state_bits, int masters, int param_f32, int grad_f32,
-                         int num_sms, cudaStream_t stream) {
+                         cudaStream_t stream) {
     auto go = [&](auto *start32, auto *start8) {
-        return (state_bits == 8 ? start8 : start32)(tensors, n, f, num_sms, stream);
+        return (state_bits == 8 ? start8 : start32)(tensors, n, f, stream);
     };
     if (param_f32)
         return grad_f32 ? go(start_all<float, float, false, false>,

@@ -9,7 +9,9 @@
  * on DLPack descriptions of the tensors before calling; checked_linear and
  * checked_gated, checked_backward, checked_expert and checked_permute do so for
  * the calls of moe_ffn.h, and call_backward, call_expert and call_permute
- * convert those calls' arguments.  Nothing here computes anything.
+ * convert those calls' arguments; checked_finalize_backward,
+ * checked_unpermute, checked_gate_backward and checked_expert_backward are the
+ * same for moe_train.h.  Nothing here computes anything.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -545,12 +547,208 @@ static PyObject *checked_permute(PyObject *self, PyObject *const *a, Py_ssize_t 
                               (int32_t *)at[3], workspace, bytes, stream));
 }
 
+/* ---------------------------------------------------------------------------
+ * The checked calls of moe_train.h.  Inputs are capsules or None, outputs
+ * capsules, addresses of outputs made for this call, or None; -1 when a tensor
+ * fails the binding's checks. */
+typedef int (*finalize_backward_fn)(const void *rows, int64_t P, const int32_t *idx,
+                                    const void *weights, int wkind, float scale, const void *r,
+                                    const void *gamma, float eps, const void *dout,
+                                    const void *dres, const void *dnorm, void *drows,
+                                    float *dweights, void *dshared, void *dresidual,
+                                    void *dgamma, int T, int K, int H, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+typedef int (*unpermute_fn)(const void *rows, int64_t P, const int32_t *idx, const void *add0,
+                            const void *add1, void *out, int T, int K, int H, void *stream);
+typedef int (*gate_backward_fn)(const float *dweights, const float *weights, const int32_t *ids,
+                                const float *logits, int T, int E, int K, int kind,
+                                void *dlogits, int out_type, void *stream);
+typedef int (*expert_backward_fn)(const void *dout, const void *x, int64_t T,
+                                  const int32_t *row_token, const int32_t *offsets,
+                                  const int32_t *counts, const void *weight, int act,
+                                  const void *preact, void *dx, void *dweight, void *dbias,
+                                  int64_t P, int E, int n, int K, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* n descriptions (or NULL) from a; 0 with a Python error */
+static int describe_all(PyObject *const *a, int n, const dl_tensor **t) {
+    for (int i = 0; i < n; ++i) {
+        t[i] = described(a[i]);
+        if (PyErr_Occurred()) return 0;
+    }
+    return 1;
+}
+
+/* n outputs (or None) from a likewise */
+static int output_all(PyObject *const *a, int n, const dl_tensor **t, void **at) {
+    for (int i = 0; i < n; ++i) {
+        t[i] = NULL;
+        at[i] = NULL;
+        if (a[i] != Py_None && !output(a[i], &t[i], &at[i])) return 0;
+    }
+    return 1;
+}
+
+/* checked_finalize_backward(fn_address, wkind, weight_code, weight_bits,
+ *     routed_scale, eps, device, stream, workspace, workspace_bytes,
+ *     permuted_out, idx_map, weights, residual_out, gamma, dout,
+ *     dresidual_out, dnorm_out, drows, dweights, dshared, dresidual, dgamma) */
+static PyObject *checked_finalize_backward(PyObject *self, PyObject *const *a,
+                                           Py_ssize_t nargs) {
+    (void)self;
+    if (nargs != 23) {
+        PyErr_SetString(PyExc_TypeError, "checked_finalize_backward takes 23 arguments");
+        return NULL;
+    }
+    finalize_backward_fn fn = (finalize_backward_fn)as_ptr(a[0]);
+    const int wkind = (int)PyLong_AsLong(a[1]);
+    const uint8_t wcode = (uint8_t)PyLong_AsLong(a[2]);
+    const uint8_t wbits = (uint8_t)PyLong_AsLong(a[3]);
+    const float scale = (float)PyFloat_AsDouble(a[4]);
+    const float eps = (float)PyFloat_AsDouble(a[5]);
+    const int dev = (int)PyLong_AsLong(a[6]);
+    void *stream = as_ptr(a[7]);
+    void *workspace = as_ptr(a[8]);
+    const size_t bytes = (size_t)PyLong_AsUnsignedLongLong(a[9]);
+    if (PyErr_Occurred()) return NULL;
+    const dl_tensor *t[8], *o[5];
+    void *at[5];
+    if (!describe_all(a + 10, 8, t) || !output_all(a + 18, 5, o, at)) return NULL;
+    int64_t x[2], id[2], w[2], d[2];
+    int ok = fn && dense(t[0], dev, DL_BFLOAT, 16, 2, x) && dense(t[1], dev, DL_INT, 32, 2, id) &&
+             dense(t[2], dev, wcode, wbits, 2, w) && w[0] == id[0] && w[1] == id[1] &&
+             x[1] <= 0x7FFFFFFF && id[0] <= 0x7FFFFFFF && id[1] <= 0x7FFFFFFF;
+    if (!ok) return PyLong_FromLong(-1);
+    ok = optional_bf16(t[3], dev, id[0], x[1]) && optional_bf16(t[4], dev, x[1], -1) &&
+         (t[7] != NULL) == (t[3] != NULL) && (t[7] != NULL) == (t[4] != NULL) &&
+         optional_bf16(t[5], dev, id[0], x[1]) && optional_bf16(t[6], dev, id[0], x[1]) &&
+         optional_bf16(t[7], dev, id[0], x[1]) && optional_bf16(o[0], dev, x[0], x[1]) &&
+         (!o[1] || (dense(o[1], dev, DL_FLOAT, 32, 2, d) && d[0] == id[0] && d[1] == id[1])) &&
+         optional_bf16(o[2], dev, id[0], x[1]) && optional_bf16(o[3], dev, id[0], x[1]) &&
+         optional_bf16(o[4], dev, x[1], -1);
+    if (!ok) return PyLong_FromLong(-1);
+    return PyLong_FromLong(fn(address(t[0]), x[0], (const int32_t *)address(t[1]), address(t[2]),
+                              wkind, scale, address(t[3]), address(t[4]), eps, address(t[5]),
+                              address(t[6]), address(t[7]), at[0], (float *)at[1], at[2], at[3],
+                              at[4], (int)id[0], (int)id[1], (int)x[1], workspace, bytes,
+                              stream));
+}
+
+/* checked_unpermute(fn_address, device, stream, rows, idx_map, add0, add1, out) */
+static PyObject *checked_unpermute(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    if (nargs != 8) {
+        PyErr_SetString(PyExc_TypeError, "checked_unpermute takes 8 arguments");
+        return NULL;
+    }
+    unpermute_fn fn = (unpermute_fn)as_ptr(a[0]);
+    const int dev = (int)PyLong_AsLong(a[1]);
+    void *stream = as_ptr(a[2]);
+    if (PyErr_Occurred()) return NULL;
+    const dl_tensor *t[4], *o;
+    void *out;
+    if (!describe_all(a + 3, 4, t) || !output_all(a + 7, 1, &o, &out)) return NULL;
+    int64_t x[2], id[2];
+    const int ok = fn && dense(t[0], dev, DL_BFLOAT, 16, 2, x) &&
+                   dense(t[1], dev, DL_INT, 32, 2, id) && x[1] <= 0x7FFFFFFF &&
+                   id[0] <= 0x7FFFFFFF && id[1] <= 0x7FFFFFFF &&
+                   optional_bf16(t[2], dev, id[0], x[1]) &&
+                   optional_bf16(t[3], dev, id[0], x[1]) && optional_bf16(o, dev, id[0], x[1]) &&
+                   (out || id[0] * x[1] == 0);
+    if (!ok) return PyLong_FromLong(-1);
+    return PyLong_FromLong(fn(address(t[0]), x[0], (const int32_t *)address(t[1]), address(t[2]),
+                              address(t[3]), out, (int)id[0], (int)id[1], (int)x[1], stream));
+}
+
+/* checked_gate_backward(fn_address, device, stream, E, kind, out_fp32, dweights,
+ *                       weights, expert_ids, logits, dlogits) */
+static PyObject *checked_gate_backward(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    if (nargs != 11) {
+        PyErr_SetString(PyExc_TypeError, "checked_gate_backward takes 11 arguments");
+        return NULL;
+    }
+    gate_backward_fn fn = (gate_backward_fn)as_ptr(a[0]);
+    const int dev = (int)PyLong_AsLong(a[1]);
+    void *stream = as_ptr(a[2]);
+    const int64_t E = PyLong_AsLongLong(a[3]);
+    const int kind = (int)PyLong_AsLong(a[4]);
+    const int fp32 = (int)PyLong_AsLong(a[5]);
+    if (PyErr_Occurred()) return NULL;
+    const dl_tensor *t[4], *o;
+    void *out;
+    if (!describe_all(a + 6, 4, t) || !output_all(a + 10, 1, &o, &out)) return NULL;
+    int64_t dw[2], d[2];
+    int ok = fn && E >= 0 && E <= 0x7FFFFFFF && dense(t[0], dev, DL_FLOAT, 32, 2, dw) &&
+             dense(t[1], dev, DL_FLOAT, 32, 2, d) && d[0] == dw[0] && d[1] == dw[1] &&
+             dense(t[2], dev, DL_INT, 32, 2, d) && d[0] == dw[0] && d[1] == dw[1] &&
+             dw[0] <= 0x7FFFFFFF && dw[1] <= 0x7FFFFFFF;
+    ok = ok && (t[3] ? dense(t[3], dev, DL_FLOAT, 32, 2, d) && d[0] == dw[0] && d[1] == E
+                     : kind == 0) &&
+         (o ? dense(o, dev, fp32 ? DL_FLOAT : DL_BFLOAT, fp32 ? 32 : 16, 2, d) &&
+                  d[0] == dw[0] && d[1] == E
+            : out || dw[0] * E == 0);
+    if (!ok) return PyLong_FromLong(-1);
+    return PyLong_FromLong(fn((const float *)address(t[0]), (const float *)address(t[1]),
+                              (const int32_t *)address(t[2]), (const float *)address(t[3]),
+                              (int)dw[0], (int)E, (int)dw[1], kind, out, fp32, stream));
+}
+
+/* checked_expert_backward(fn_address, gated, activation, device, stream,
+ *     workspace, workspace_bytes, dout, x, row_token, offsets, counts, weight,
+ *     preact, dx, dweight, dbias) */
+static PyObject *checked_expert_backward(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    if (nargs != 17) {
+        PyErr_SetString(PyExc_TypeError, "checked_expert_backward takes 17 arguments");
+        return NULL;
+    }
+    expert_backward_fn fn = (expert_backward_fn)as_ptr(a[0]);
+    const int gated = (int)PyLong_AsLong(a[1]);
+    const int act = (int)PyLong_AsLong(a[2]);
+    const int dev = (int)PyLong_AsLong(a[3]);
+    void *stream = as_ptr(a[4]);
+    void *workspace = as_ptr(a[5]);
+    const size_t bytes = (size_t)PyLong_AsUnsignedLongLong(a[6]);
+    if (PyErr_Occurred()) return NULL;
+    const dl_tensor *t[7], *o[3];
+    void *grad[3];
+    if (!describe_all(a + 7, 7, t) || !output_all(a + 14, 3, o, grad)) return NULL;
+    int64_t d[2], x[2], r[1], f[1], c[1], w[3], g[3];
+    int ok = fn && dense(t[0], dev, DL_BFLOAT, 16, 2, d) && dense(t[1], dev, DL_BFLOAT, 16, 2, x) &&
+             dense(t[5], dev, DL_BFLOAT, 16, 3, w) && w[1] == (gated ? 2 * d[1] : d[1]) &&
+             w[2] == x[1] && dense(t[3], dev, DL_INT, 32, 1, f) && f[0] == w[0] + 1 &&
+             dense(t[4], dev, DL_INT, 32, 1, c) && c[0] == w[0] &&
+             (t[2] ? dense(t[2], dev, DL_INT, 32, 1, r) && r[0] == d[0] : x[0] == d[0]) &&
+             (gated || act ? t[6] != NULL : 1) && optional_bf16(t[6], dev, d[0], w[1]) &&
+             w[0] <= 0x7FFFFFFF && d[1] <= 0x3FFFFFFF && x[1] <= 0x7FFFFFFF;
+    ok = ok && optional_bf16(o[0], dev, d[0], x[1]) &&
+         (!o[1] || (dense(o[1], dev, DL_BFLOAT, 16, 3, g) && g[0] == w[0] && g[1] == w[1] &&
+                    g[2] == w[2])) &&
+         optional_bf16(o[2], dev, w[0], w[1]);
+    if (!ok) return PyLong_FromLong(-1);
+    /* the preactivations of the identity are not read */
+    return PyLong_FromLong(fn(address(t[0]), address(t[1]), x[0], (const int32_t *)address(t[2]),
+                              (const int32_t *)address(t[3]), (const int32_t *)address(t[4]),
+                              address(t[5]), act, gated || act ? address(t[6]) : NULL, grad[0],
+                              grad[1], grad[2], d[0], (int)w[0], (int)d[1], (int)x[1], workspace,
+                              bytes, stream));
+}
+
 /* call_size(fn_address, a, b) -> a size_t function of two ints */
 static PyObject *call_size(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
     (void)self;
     long long v[MOST_ARGS];
     if (parse_ints(a, nargs, 3, "call_size", v) != 0) return NULL;
     return PyLong_FromSize_t(((size_t(*)(int, int))PTR(0))(INT(1), INT(2)));
+}
+
+/* call_size3(fn_address, a, b, c) -> a size_t function of an int64 and two ints */
+static PyObject *call_size3(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    (void)self;
+    long long v[MOST_ARGS];
+    if (parse_ints(a, nargs, 4, "call_size3", v) != 0) return NULL;
+    return PyLong_FromSize_t(((size_t(*)(int64_t, int, int))PTR(0))(v[1], INT(2), INT(3)));
 }
 
 /* permute_sizes(moe_permute_rows, moe_permute_workspace_bytes, T, K, E, tile)
@@ -610,8 +808,18 @@ static PyMethodDef methods[] = {
      "Check DLPack-described tensors and enqueue one expert product."},
     {"checked_permute", (PyCFunction)(void (*)(void))checked_permute, METH_FASTCALL,
      "Check DLPack-described tensors and enqueue one moe_permute call."},
+    {"checked_finalize_backward", (PyCFunction)(void (*)(void))checked_finalize_backward,
+     METH_FASTCALL, "Check DLPack-described tensors and enqueue one moe_finalize_backward call."},
+    {"checked_unpermute", (PyCFunction)(void (*)(void))checked_unpermute, METH_FASTCALL,
+     "Check DLPack-described tensors and enqueue one moe_unpermute call."},
+    {"checked_gate_backward", (PyCFunction)(void (*)(void))checked_gate_backward, METH_FASTCALL,
+     "Check DLPack-described tensors and enqueue one moe_topk_route_backward call."},
+    {"checked_expert_backward", (PyCFunction)(void (*)(void))checked_expert_backward,
+     METH_FASTCALL, "Check DLPack-described tensors and enqueue one expert backward call."},
     {"call_size", (PyCFunction)(void (*)(void))call_size, METH_FASTCALL,
      "Call a size function of two ints."},
+    {"call_size3", (PyCFunction)(void (*)(void))call_size3, METH_FASTCALL,
+     "Call a size function of an int64 and two ints."},
     {"permute_sizes", (PyCFunction)(void (*)(void))permute_sizes, METH_FASTCALL,
      "Call moe_permute_rows and moe_permute_workspace_bytes."},
     {NULL, NULL, 0, NULL},

@@ -21,8 +21,8 @@ namespace moef {
 // out = act(gate) * up.  Grouped (E > 0): A is [E, M or 2M, K] ([E, K, M] when m is
 // contiguous), the rows n of expert e are offsets[e] .. offsets[e] + counts[e], row n
 // read from row row_token[n] of B.
-// Grouped dweight (group_k): k runs over each expert's rows, A = x [a_rows, M], row
-// k read from row row_token[k], B = dz [b_rows, N], out [E, N, M].
+// Grouped dweight: k runs over each expert's rows of A = x [K, M] and B = dz [K, N],
+// both in the layout, out [E, N, M].
 struct Gemm {
     const uint16_t *a, *b;
     int a_mn, b_mn;             // 1: the operand is contiguous along m (n), not k
@@ -38,8 +38,7 @@ struct Gemm {
     const int32_t *offsets, *counts, *row_token;
     int64_t b_rows;             // rows of B
     int64_t b_pitch;            // values from one of its rows (of k: b_mn) to the next
-    int group_k;
-    int64_t a_rows;
+    int64_t a_pitch;            // the same of A, for grouped dweight
 };
 
 // Steps of `step` values that cover k >= 1 of them.  k is a token count in
@@ -71,10 +70,9 @@ bool launch_gemm_tc(const Gemm &g, const BiasSum &bias, int num_sms, cudaStream_
 bool launch_two_gemms_tc(const Gemm *g, const BiasSum &bias, int num_sms, cudaStream_t stream,
                          cudaError_t *err);
 
-// The grouped dweight (group_k) on the tensor cores, false likewise, and by the
-// kernel of single-value loads.
-bool launch_group_dweight_tc(const Gemm &g, int num_sms, cudaStream_t stream, cudaError_t *err);
-cudaError_t launch_group_dweight_simple(const Gemm &g, cudaStream_t stream);
+// The grouped dweight, on the tensor cores: both operands 16-byte aligned, pitches
+// multiples of 8.
+cudaError_t launch_group_dweight(const Gemm &g, int num_sms, cudaStream_t stream);
 
 // The kernel for a handful of rows; false (nothing launched) when the sizes or
 // alignment are not its own, or the tensor-core one is faster.

@@ -1,5 +1,5 @@
-// dz of the expert products' backward passes, over the rows of the experts alone,
-// and their bias gradients.
+// dz of the expert products' backward passes, over the rows of the experts alone, the
+// rows of x beside it, and their bias gradients.
 //
 //   linear  dz = dout * act'(preact)
 //   gated   dz[:, i] = dout * u * act'(g),  dz[:, n + i] = dout * act(g)
@@ -9,6 +9,12 @@
 // and with few tokens most of P is behind the last of them (16 tokens, top-8 of
 // 256, tiles of 128: 128 rows of 16384).  Each CTA counts the experts' pieces of
 // eight rows itself and takes every gridDim-th of them, a row a warp.
+//
+// dweight sums over rows, which its product copies in blocks of 64: rows of x that
+// lie scattered (a row map) or cannot be copied as they are (odd sizes, misaligned
+// views) are laid out once here.  Gathered by the product itself, four rows of 128
+// bytes to a copy, they came at 17 bytes a clock: 32768 rows, 64 experts of 4096 x
+// 7168 took 1742 us, 1259 from rows in order, which take 130 us to write.
 #include "ffn.cuh"
 #include "tc.cuh"
 #include "train.cuh"
@@ -49,11 +55,37 @@ __device__ __forceinline__ void dz_of(const float (&d)[VEC], const float (&z)[VE
     }
 }
 
+// A row of x by a warp; one outside x as zeros.
+__device__ __forceinline__ void copy_row(const RowCopy &c, int64_t row, int lane) {
+    const int64_t token = c.row_token ? c.row_token[row] : row;
+    const bool have = token >= 0 && token < c.T;
+    const uint16_t *from = c.x + (have ? token : 0) * c.K;
+    uint16_t *to = c.to + row * c.pitch;
+    if (c.K % 8 == 0 && reinterpret_cast<uintptr_t>(c.x) % 16 == 0) {
+        constexpr int kStride = 32 * 8;
+        for (int i0 = lane * 8; i0 < c.K; i0 += kStride * kLoads) {
+            uint4 v[kLoads];
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) {
+                v[l] = make_uint4(0, 0, 0, 0);
+                if (have && i0 + kStride * l < c.K)
+                    v[l] = __ldg(reinterpret_cast<const uint4 *>(from + i0 + kStride * l));
+            }
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l)
+                if (i0 + kStride * l < c.K)
+                    *reinterpret_cast<uint4 *>(to + i0 + kStride * l) = v[l];
+        }
+    } else {
+        for (int i = lane; i < c.K; i += 32) to[i] = have ? from[i] : 0;
+    }
+}
+
 // ACT: the activation, or -1 to take it from `act`.
 template <int VEC, bool GATED, int ACT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t *dz,
-                 int64_t pitch, const Groups g, int n) {
+                 int64_t pitch, const Groups g, int n, const RowCopy copy) {
     using Ops = VecOps<VEC>;
     using V = typename Ops::V;
     __shared__ int s_pieces[MOEF_MAX_EXPERTS + 1], s_first[MOEF_MAX_EXPERTS],
@@ -105,7 +137,8 @@ expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t
         const int at = (piece - s_pieces[lo]) * kWarps + warp;
         if (at >= s_rows[lo]) continue;
         const int64_t row = static_cast<int64_t>(s_first[lo]) + at;
-        for (int i0 = lane * VEC; i0 < n; i0 += 32 * VEC * kLoads) {
+        if (copy.to) copy_row(copy, row, lane);
+        for (int i0 = lane * VEC; dz && i0 < n; i0 += 32 * VEC * kLoads) {
             V d[kLoads], z[kLoads], u[kLoads];
 #pragma unroll
             for (int l = 0; l < kLoads; ++l) {
@@ -214,13 +247,13 @@ bool vectors(const void *a, const void *b, const void *c, int n) {
 }  // namespace
 
 cudaError_t launch_expert_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
-                             uint16_t *dz, int64_t pitch, const Groups &g, int n, int num_sms,
-                             cudaStream_t stream) {
+                             uint16_t *dz, int64_t pitch, const Groups &g, int n,
+                             const RowCopy &copy, int num_sms, cudaStream_t stream) {
     const int64_t need = (g.P + kWarps - 1) / kWarps + (g.E < g.P ? g.E : g.P);
     const int64_t most = static_cast<int64_t>(num_sms) * kCtasPerSm;
     const dim3 grid(static_cast<unsigned>(need < most ? need : most));
     auto go = [&](auto *kernel) {
-        return start(kernel, grid, stream, dout, preact, act, dz, pitch, g, n);
+        return start(kernel, grid, stream, dout, preact, act, dz, pitch, g, n, copy);
     };
     if (!vectors(dout, preact, dz, n))
         return gated ? go(expert_dz_kernel<1, true, -1>) : go(expert_dz_kernel<1, false, -1>);

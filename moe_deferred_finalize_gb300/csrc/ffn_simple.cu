@@ -52,21 +52,6 @@ struct Staged {
                           : p[row * pitch + k0 + k];
         }
     }
-    // Rows r0 .. of a k x rows matrix whose row for k is k_at(k) (negative: zeros).
-    template <typename At>
-    __device__ __forceinline__ void load_k(const uint16_t *p, int64_t pitch, int r0, int rows,
-                                           int k0, int K, At k_at) {
-#pragma unroll
-        for (int i = 0; i < ROWS * kStep / kSimpleThreads; ++i) {
-            int r, k;
-            place(i, 1, &r, &k);
-            v[i] = 0;
-            if (r0 + r < rows && k0 + k < K) {
-                const int64_t at = k_at(k0 + k);
-                if (at >= 0) v[i] = p[at * pitch + r0 + r];
-            }
-        }
-    }
     __device__ __forceinline__ void store(uint16_t (*s)[kPad], int mn) const {
 #pragma unroll
         for (int i = 0; i < ROWS * kStep / kSimpleThreads; ++i) {
@@ -90,28 +75,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// A step's products: the warp's two blocks of 16 rows of A by its 32 rows of B.
-__device__ __forceinline__ void multiply(float (&acc)[2][4][4], const uint16_t (*sa)[kPad],
-                                         const uint16_t (*sb)[kPad], int block0, int block1,
-                                         int wn, int lane) {
-#pragma unroll
-    for (int k = 0; k < kStep; k += 16) {
-        uint32_t fa[2][4], fb[2][4];
-        const int row = lane & 15, half = lane >> 4;
-        ldmatrix4(fa[0], &sa[block0 + row][k + 8 * half]);
-        ldmatrix4(fa[1], &sa[block1 + row][k + 8 * half]);
-        // b: n rows 0..7, 8..15, each k 0..7 and 8..15
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            ldmatrix4(fb[j], &sb[wn * 32 + j * 16 + (lane & 7) + 8 * half][k + (lane & 8)]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                mma(acc[i][j], fa[i], fb[j >> 1][(j & 1) * 2], fb[j >> 1][(j & 1) * 2 + 1]);
-    }
 }
 
 template <bool GATED>
@@ -164,7 +127,23 @@ gemm_simple_kernel(const Gemm g) {
                 next_a.load(a, g.a_mn, a_pitch, k0, g.K, a_row);
                 next_b.load(g.b, g.b_mn, g.b_pitch, k0, g.K, b_row);
             }
-            multiply(acc, sa, sb, block0, block1, wn, lane);
+#pragma unroll
+            for (int k = 0; k < kStep; k += 16) {
+                uint32_t fa[2][4], fb[2][4];
+                const int row = lane & 15, half = lane >> 4;
+                ldmatrix4(fa[0], &sa[block0 + row][k + 8 * half]);
+                ldmatrix4(fa[1], &sa[block1 + row][k + 8 * half]);
+                // b: n rows 0..7, 8..15, each k 0..7 and 8..15
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    ldmatrix4(fb[j], &sb[wn * 32 + j * 16 + (lane & 7) + 8 * half]
+                                        [k + (lane & 8)]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma(acc[i][j], fa[i], fb[j >> 1][(j & 1) * 2], fb[j >> 1][(j & 1) * 2 + 1]);
+            }
             __syncthreads();
         }
         auto finish = [&](int m, int c, float z, float u) {
@@ -203,62 +182,7 @@ gemm_simple_kernel(const Gemm g) {
     }
 }
 
-// The grouped dweight: blockIdx.z is the expert, k its rows.
-__global__ void __launch_bounds__(kSimpleThreads, 2)
-group_dweight_simple_kernel(const Gemm g) {
-    __shared__ __align__(16) uint16_t sa[kRowsA][kPad], sb[kRowsB][kPad];
-    const int e = blockIdx.z, m0 = blockIdx.x * kRowsA;
-    const int64_t first = g.offsets[e];
-    const int64_t room = g.K - first;
-    const int rows = first < 0 || room <= 0
-                         ? 0 : static_cast<int>(min(static_cast<int64_t>(max(g.counts[e], 0)), room));
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int wm = warp & 3, wn = warp >> 2;
-    auto a_at = [&](int k) -> int64_t {
-        const int64_t row = first + k;
-        if (!g.row_token) return row;
-        const int token = g.row_token[row];
-        return token < g.a_rows ? token : -1;
-    };
-    auto b_at = [&](int k) { return first + k; };
-    uint16_t *out = static_cast<uint16_t *>(g.out) + static_cast<int64_t>(e) * g.N * g.M;
-    for (int64_t n0 = static_cast<int64_t>(blockIdx.y) * kRowsB; n0 < g.N;
-         n0 += static_cast<int64_t>(gridDim.y) * kRowsB) {
-        float acc[2][4][4] = {};
-        for (int k0 = 0; k0 < rows; k0 += kStep) {
-            Staged<kRowsA> a;
-            Staged<kRowsB> b;
-            a.load_k(g.a, g.M, m0, g.M, k0, rows, a_at);
-            b.load_k(g.b, g.b_pitch, static_cast<int>(n0), g.N, k0, rows, b_at);
-            a.store(sa, 1);
-            b.store(sb, 1);
-            __syncthreads();
-            multiply(acc, sa, sb, wm * 32, wm * 32 + 16, wn, lane);
-            __syncthreads();
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int m = m0 + wm * 32 + 16 * i + (lane >> 2) + (q & 2) * 4;
-                    const int64_t n = n0 + wn * 32 + j * 8 + (lane & 3) * 2 + (q & 1);
-                    if (m < g.M && n < g.N) out[n * g.M + m] = to_bf16(acc[i][j][q]);
-                }
-    }
-}
-
 }  // namespace
-
-cudaError_t launch_group_dweight_simple(const Gemm &g, cudaStream_t stream) {
-    const int64_t n_tiles = (static_cast<int64_t>(g.N) + kRowsB - 1) / kRowsB;
-    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(g.M) + kRowsA - 1) / kRowsA),
-                    static_cast<unsigned>(n_tiles < 65535 ? n_tiles : 65535),
-                    static_cast<unsigned>(g.E));
-    group_dweight_simple_kernel<<<grid, kSimpleThreads, 0, stream>>>(g);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_gemm_simple(const Gemm &g, cudaStream_t stream) {
     const int features = g.gated ? 64 : 128;

@@ -45,7 +45,7 @@ __device__ __forceinline__ float warp_sum8(float (&acc)[8], int lane) {
 }
 
 template <int VPT, int VEC, bool NORM, bool CLUSTER>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, VPT <= 2 ? 2 : 1)
 finalize_backward_kernel(const __grid_constant__ FinalizeBackward p,
                          const __grid_constant__ Cut cut) {
     using Ops = VecOps<VEC>;
@@ -449,12 +449,12 @@ cudaError_t launch_finalize_backward(const FinalizeBackward &p, int num_sms,
     cut.splits = 1;
     while (cut.splits < kMaxSplits &&
            (2 * static_cast<int64_t>(p.T) * cut.splits <= 4 * num_sms && cut.nvec >= 64 * cut.splits ||
-            p.dnorm && cut.nvec > static_cast<int64_t>(kMaxThreads) * kMaxVpt * cut.splits))
+            p.dnorm && cut.nvec > static_cast<int64_t>(kMaxThreads) * 2 * cut.splits))
         cut.splits *= 2;
     cut.slice = (cut.nvec - 1) / cut.splits + 1;
     cut.splits = (cut.nvec - 1) / cut.slice + 1;        // none is empty
     cut.vpt = 1;
-    while (cut.vpt < kMaxVpt && cut.slice > kMaxThreads * cut.vpt) cut.vpt *= 2;
+    while (cut.vpt < (p.dnorm ? kMaxVpt : 2) && cut.slice > kMaxThreads * cut.vpt) cut.vpt *= 2;
     const int need = (cut.slice - 1) / cut.vpt + 1;
     cut.threads = need < kMaxThreads ? (need + 31) / 32 * 32 : kMaxThreads;
     int64_t clusters = static_cast<int64_t>(num_sms) * (2048 / cut.threads) / 2 / cut.splits;

@@ -57,23 +57,31 @@ struct AdamWFactors {
     float beta1, beta2, rest1, rest2;   // rest: 1 - beta
     float eps, lr, weight_decay;
     float bias1, root_bias2;            // 1 - beta1^step, sqrt(1 - beta2^step)
-    double log_beta1, log_beta2;        // for device_step
+    float log_beta1, log_beta2;         // for device_step
     const int32_t *device_step;
     const float *device_lr, *grad_scale;
 };
 cudaError_t launch_adamw(const moef_adamw_tensor *tensors, int n, const AdamWFactors &f,
                          int state_bits, int masters, int param_f32, int grad_f32,
-                         int num_sms, cudaStream_t stream);
+                         cudaStream_t stream);
 
-// dz of the expert products over the rows of the experts alone, and dbias.
+// dz of the expert products over the rows of the experts alone, the rows of x that
+// they were made from laid out beside it, and dbias.
 struct Groups {
     const int32_t *offsets, *counts;
     int E;
     int64_t P;
 };
+struct RowCopy {
+    const uint16_t *x;          // [T, K]
+    const int32_t *row_token;   // [P], or null: row r of x
+    uint16_t *to;               // [P, pitch], null: nothing to do
+    int64_t T, pitch;
+    int K;
+};
 cudaError_t launch_expert_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
                              uint16_t *dz, int64_t pitch, const Groups &groups, int n,
-                             int num_sms, cudaStream_t stream);
+                             const RowCopy &copy, int num_sms, cudaStream_t stream);
 cudaError_t launch_expert_dbias(const uint16_t *dout, const uint16_t *preact, int act, int gated,
                                 uint16_t *dbias, const Groups &groups, int n,
                                 cudaStream_t stream);

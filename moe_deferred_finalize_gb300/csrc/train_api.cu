@@ -21,10 +21,15 @@ bool valid_features(int n) { return n >= 1 && n <= MOEF_MAX_FEATURES; }
 
 moef_status sms_of_device(int *sms) { return cuda_status(moef::current_sms(sms)); }
 
-// dz has rows of a multiple of 8 values, as in the dense backward passes.
+// dz and laid out rows of x have a multiple of 8 values, as the dense dz.
 int64_t dz_pitch(int64_t cols) { return (cols + 7) / 8 * 8; }
 
 size_t dz_bytes(int64_t P, int64_t cols) { return static_cast<size_t>(P * dz_pitch(cols) * 2); }
+
+// Whether dweight's product can copy x as it lies.
+bool lies_in_blocks(const void *x, const int32_t *row_token, int K) {
+    return !row_token && K % 8 == 0 && aligned(x, 16);
+}
 
 // A product over rows grouped by expert.
 moef_status run_group(const Gemm &g, int sms, cudaStream_t stream) {
@@ -48,13 +53,15 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
     const bool needs_preact = gated || act != MOEF_ACT_NONE;
     if (!needs_preact && preact) return MOEF_ERR_ARG;
     const int cols = gated ? 2 * n : n;
+    const bool copies_x = dweight && !lies_in_blocks(x, row_token, K);
     // without a token or a row there is nothing to read: zeros
     const bool empty = T == 0 || P == 0;
     if (!empty) {
         if (!dout || !offsets || !counts || (needs_preact && !preact) || (dx && !weight) ||
             (dweight && !x) || !workspace)
             return MOEF_ERR_NULL;
-        if (workspace_bytes < dz_bytes(P, cols)) return MOEF_ERR_SHAPE;
+        if (workspace_bytes < moe_expert_backward_workspace_bytes(P, cols, copies_x ? K : 0))
+            return MOEF_ERR_SHAPE;
         if (!aligned(workspace, 16)) return MOEF_ERR_ALIGN;
     }
     for (const void *p : {dout, x, weight, preact, static_cast<const void *>(dx),
@@ -76,9 +83,12 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
     // dout itself when it is dz and can be copied as it lies
     const bool has_dz = needs_preact || cols % 8 || !aligned(dout, 16);
     uint16_t *dz = has_dz && (dx || dweight) ? u16(workspace) : nullptr;
-    if (dz)
+    moef::RowCopy copy = {};
+    if (copies_x)
+        copy = {u16(x), row_token, u16(workspace) + P * dz_pitch(cols), T, dz_pitch(K), K};
+    if (dz || copies_x)
         st = cuda_status(moef::launch_expert_dz(u16(dout), u16(preact), static_cast<int>(act),
-                                                gated, dz, dz_pitch(cols), groups, n, sms,
+                                                gated, dz, dz_pitch(cols), groups, n, copy, sms,
                                                 stream));
     if (st == MOEF_OK && dbias)
         st = cuda_status(moef::launch_expert_dbias(u16(dout), u16(preact), static_cast<int>(act),
@@ -102,18 +112,13 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
     }
     if (st == MOEF_OK && dweight) {
         Gemm d = g;
-        d.group_k = 1;
-        d.a = u16(x);
-        d.a_rows = T;
-        d.row_token = row_token;
+        d.a = copies_x ? copy.to : u16(x);
+        d.a_pitch = copies_x ? copy.pitch : K;
         d.b_mn = 1;
         d.N = cols;
         d.K = static_cast<int>(P);
         d.out = dweight;
-        cudaError_t err = cudaSuccess;
-        if (!moef::launch_group_dweight_tc(d, sms, stream, &err))
-            err = moef::launch_group_dweight_simple(d, stream);
-        st = cuda_status(err);
+        st = cuda_status(moef::launch_group_dweight(d, sms, stream));
     }
     return st;
 }
@@ -245,9 +250,11 @@ moef_status moe_topk_route_backward(const float *dweights, const float *weights,
     return cuda_status(moef::launch_gate_backward(p, sms, stream));
 }
 
-size_t moe_expert_backward_workspace_bytes(int64_t P, int cols) {
-    if (P < 0 || P > INT_MAX || cols < 1 || cols > 2 * MOEF_MAX_FEATURES) return 0;
-    return dz_bytes(P, cols);
+size_t moe_expert_backward_workspace_bytes(int64_t P, int cols, int inputs) {
+    if (P < 0 || P > INT_MAX || cols < 1 || cols > 2 * MOEF_MAX_FEATURES || inputs < 0 ||
+        inputs > MOEF_MAX_FEATURES)
+        return 0;
+    return dz_bytes(P, cols) + dz_bytes(P, inputs);
 }
 
 moef_status moe_expert_gated_ffn_backward(const void *dout, const void *x, int64_t T,
@@ -310,9 +317,6 @@ moef_status moe_adamw_step(const moef_adamw_tensor *tensors, int n,
             return MOEF_ERR_ALIGN;
     }
     if (pieces == 0) return MOEF_OK;
-    int sms = 0;
-    const moef_status st = sms_of_device(&sms);
-    if (st != MOEF_OK) return st;
     moef::AdamWFactors f{};
     f.beta1 = static_cast<float>(c.beta1);
     f.beta2 = static_cast<float>(c.beta2);
@@ -322,17 +326,18 @@ moef_status moe_adamw_step(const moef_adamw_tensor *tensors, int n,
     f.lr = static_cast<float>(c.lr);
     f.weight_decay = static_cast<float>(c.weight_decay);
     // log(0) = -inf gives 1 - beta^step = 1
-    f.log_beta1 = log(c.beta1);
-    f.log_beta2 = log(c.beta2);
+    const double log1 = log(c.beta1), log2 = log(c.beta2);
     const int step = c.device_step ? 1 : c.step;
-    f.bias1 = static_cast<float>(-expm1(step * f.log_beta1));
-    f.root_bias2 = static_cast<float>(sqrt(-expm1(step * f.log_beta2)));
+    f.log_beta1 = static_cast<float>(log1);
+    f.log_beta2 = static_cast<float>(log2);
+    f.bias1 = static_cast<float>(-expm1(step * log1));
+    f.root_bias2 = static_cast<float>(sqrt(-expm1(step * log2)));
     f.device_step = c.device_step;
     f.device_lr = c.device_lr;
     f.grad_scale = c.grad_scale;
     return cuda_status(moef::launch_adamw(tensors, n, f, c.state_bits, masters,
                                           c.param_type == MOEF_OUT_FP32,
-                                          c.grad_type == MOEF_OUT_FP32, sms, stream));
+                                          c.grad_type == MOEF_OUT_FP32, stream));
 }
 
 }  // extern "C"

@@ -125,9 +125,17 @@ def test_expert_backward_argument_errors(lib, gated):
     for k in ("row_token", "offsets", "counts"):
         assert call(f, EXPERT, **{k: HALF}) == E_ALIGN, k
     assert call(f, EXPERT, ws=A + 8) == E_ALIGN
-    need = lib.moe_expert_backward_workspace_bytes(40, cols)
-    assert need == 40 * cols * 2
-    assert call(f, EXPERT, ws_bytes=need - 1) == E_SHAPE
+    size = lib.moe_expert_backward_workspace_bytes
+    assert size(40, cols, 0) == 40 * cols * 2 and size(40, cols, 8) == 40 * (cols + 8) * 2
+    assert size(40, 9, 17) == 40 * (16 + 24) * 2
+    assert size(-1, 8, 0) == size(40, 0, 0) == size(40, 8, -1) == 0
+    # rows of x are laid out with a row map, an odd width, a misaligned x
+    assert call(f, EXPERT, ws_bytes=size(40, cols, 8) - 1) == E_SHAPE
+    in_layout = dict(row_token=NULL, T=40, ws_bytes=size(40, cols, 0) - 1)
+    assert call(f, EXPERT, **in_layout) == E_SHAPE
+    in_layout["ws_bytes"] += 1
+    assert call(f, EXPERT, **in_layout, x=HALF) == E_SHAPE
+    assert call(f, EXPERT, **in_layout, K=9) == E_SHAPE
     for k, vs in (("T", (-1, 1 << 31)), ("P", (-1, 1 << 31)), ("E", (0, 1025)),
                   ("n", (0, (1 << 24) + 1)), ("K", (0, (1 << 24) + 1))):
         for v in vs:
