@@ -98,8 +98,7 @@ struct Header {
     int bn;
     int tiles;
     int log_split;
-    // expert groups: column tiles before each (grouped dweight: the experts, those
-    // with most rows first), first row, rows
+    // expert groups: column tiles before each, first row, rows
     int prefix[MOEF_MAX_EXPERTS + 1], first[MOEF_MAX_EXPERTS], count[MOEF_MAX_EXPERTS];
 };
 static_assert(sizeof(Header) <= kHeader && offsetof(Header, prefix) <= kHeader - kStashes,
@@ -157,16 +156,8 @@ __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const He
     Tile r;
     r.e = 0;
     int m, n;
-    if constexpr (DW) {
-        // Tiles in the order of their experts' rows, most first; the rounds of the grid
-        // take them from its front and its back in turn, so that each pair of CTAs has
-        // a product that is long and one that is mostly written by turns: the output of
-        // the one goes out under the products of the other (64 experts of 4096 x 7168
-        // with 50 to 1925 rows: 1600 us in the experts' order).
-        const int round = gridDim.x / CG, i = t / round;
-        const int at = (i >> 1) * round + t - i * round;
-        const int each = p.m_tiles * p.n_tiles, from = i & 1 ? h->tiles - 1 - at : at;
-        const int place = from / each, local = from - place * each, e = h->prefix[place];
+    if constexpr (DW) {     // an expert's tiles share its rows of both operands
+        const int each = p.m_tiles * p.n_tiles, e = t / each, local = t - e * each;
         n = local / p.m_tiles;
         m = local - n * p.m_tiles;
         r.bn = p.bn;
@@ -779,14 +770,6 @@ __device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Head
         most = max(most, count);
     }
     if constexpr (DW) {
-        __syncthreads();        // prefix: the experts by their rows, most first
-        for (int e = threadIdx.x; e < g.E; e += kTcThreads) {
-            const int own = h->count[e];
-            int place = 0;
-            for (int j = 0; j < g.E; ++j)
-                place += h->count[j] > own || (h->count[j] == own && j < e);
-            h->prefix[place] = e;
-        }
         if (threadIdx.x == 0) {
             h->bn = p.bn;
             h->tiles = g.E * p.m_tiles * p.n_tiles;

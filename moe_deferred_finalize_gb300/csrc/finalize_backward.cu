@@ -385,8 +385,10 @@ unpermute_kernel(const __grid_constant__ Unpermute p, int nvec, int slices) {
 
 constexpr int kGateThreads = 128;
 
-// A warp takes a token: lane k has slot k, and every lane writes its pieces of the
-// row, zeros but for the chosen experts.
+// A warp takes a token: the row is written as zeros, and then lane k puts slot k's
+// value into it (the warp's barrier orders the two).  Bound by the writes at large T
+// (comparing every column with every id took 9.4 us at T = 16384 and 256 experts, as
+// many instructions as the bytes have time for eight times over).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kGateThreads)
 gate_backward_kernel(const __grid_constant__ GateBackward p) {
@@ -410,24 +412,25 @@ gate_backward_kernel(const __grid_constant__ GateBackward p) {
         if (p.kind == MOEF_GATE_SIGMOID && id >= 0)
             d *= 1.f / (1.f + expf(p.logits[t * p.E + id]));
         T *row = static_cast<T *>(p.dlogits) + t * p.E;
-        for (int c0 = 0; c0 < p.E; c0 += 32 * VEC) {
-            const int c = c0 + lane * VEC;
-            float f[VEC] = {};
+        for (int c = lane * VEC; c < p.E; c += 32 * VEC) {
+            if constexpr (VEC == 1) row[c] = 0;
+            else *reinterpret_cast<uint4 *>(row + c) = make_uint4(0, 0, 0, 0);
+        }
+        // a token that names an expert twice: its first slot has the sum, in slot order
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+        const bool first = id >= 0 && (same & ((1u << lane) - 1)) == 0;
+        if (__any_sync(0xFFFFFFFFu, id >= 0 && !first)) {
+            float sum = 0.f;
             for (int k = 0; k < K; ++k) {
-                const int at = __shfl_sync(0xFFFFFFFFu, id, k) - c;
                 const float dk = __shfl_sync(0xFFFFFFFFu, d, k);
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) f[q] += at == q ? dk : 0.f;
+                if (same >> k & 1) sum += dk;
             }
-            if (c >= p.E) continue;
-            if constexpr (VEC == 1) {
-                if constexpr (sizeof(T) == 4) row[c] = f[0];
-                else row[c] = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
-            } else if constexpr (sizeof(T) == 4) {
-                *reinterpret_cast<float4 *>(row + c) = make_float4(f[0], f[1], f[2], f[3]);
-            } else {
-                *reinterpret_cast<uint4 *>(row + c) = VecOps<8>::from_f32(f);
-            }
+            d = sum;
+        }
+        __syncwarp();
+        if (first) {
+            if constexpr (sizeof(T) == 4) row[id] = d;
+            else row[id] = __bfloat16_as_ushort(__float2bfloat16_rn(d));
         }
     }
 }
