@@ -39,6 +39,7 @@ struct Gemm {
     int64_t b_rows;             // rows of B
     int64_t b_pitch;            // values from one of its rows (of k: b_mn) to the next
     int64_t a_pitch;            // the same of A, for grouped dweight
+    int a_zeros, b_zeros;       // the operand has zeros behind spaced rows
 };
 
 // Steps of `step` values that cover k >= 1 of them.  k is a token count in
@@ -101,6 +102,15 @@ cudaError_t launch_permute(const int32_t *ids, int T, int K, int E, int tile, in
 
 #ifdef __CUDACC__
 namespace {
+
+// Whether an expert's rows, rounded up to a multiple of 16, end before the next
+// expert's first row (or the end of the layout) and the buffer's end.  When all do,
+// no two experts share the rows in between: the backward pass fills those of its
+// workspace with zeros, and its product may read them.  Both ask this.
+__device__ __forceinline__ int spaced_rows(int first, int rows, int next, int64_t P) {
+    const int64_t end = static_cast<int64_t>(first) + ((static_cast<int64_t>(rows) + 15) & ~15LL);
+    return first >= 0 && first <= next && end <= next && end <= P;
+}
 
 // 2^x and 1 / x as one instruction each, results below the normal range as 0,
 // which the activations multiply into an error below 1e-35.  (__expf and

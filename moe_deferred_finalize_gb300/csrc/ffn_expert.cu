@@ -8,13 +8,19 @@
 // layout's rows are P at most, but how many the experts have only the device knows,
 // and with few tokens most of P is behind the last of them (16 tokens, top-8 of
 // 256, tiles of 128: 128 rows of 16384).  Each CTA counts the experts' pieces of
-// eight rows itself and takes every gridDim-th of them, a row a warp.
+// eight rows itself and takes every gridDim-th of them, a row a warp.  Where there
+// are fewer pieces than CTAs, a piece's columns are shared out over several (100
+// tokens, two of 8 experts of 1040 x 1536: 10.2 us by 25 CTAs).
 //
 // dweight sums over rows, which its product copies in blocks of 64: rows of x that
 // lie scattered (a row map) or cannot be copied as they are (odd sizes, misaligned
 // views) are laid out once here.  Gathered by the product itself, four rows of 128
 // bytes to a copy, they came at 17 bytes a clock: 32768 rows, 64 experts of 4096 x
 // 7168 took 1742 us, 1259 from rows in order, which take 130 us to write.
+//
+// Where the layout leaves room, the rows behind an expert's last are zeros up to a
+// multiple of 16 here: the product then copies its last block like the others (see
+// spaced_rows).
 #include "ffn.cuh"
 #include "tc.cuh"
 #include "train.cuh"
@@ -26,6 +32,9 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kLoads = 4;               // vectors of a lane in flight
 constexpr int kCtasPerSm = 4;
+
+// An expert's rows rounded up to the 16 that one step of dweight's product sums.
+__device__ __forceinline__ int rounded_rows(int rows) { return (rows + 15) & ~15; }
 
 // Rows of expert e: first, and how many, clipped to the buffer as the products clip
 // them.
@@ -55,29 +64,30 @@ __device__ __forceinline__ void dz_of(const float (&d)[VEC], const float (&z)[VE
     }
 }
 
-// A row of x by a warp; one outside x as zeros.
-__device__ __forceinline__ void copy_row(const RowCopy &c, int64_t row, int lane) {
-    const int64_t token = c.row_token ? c.row_token[row] : row;
-    const bool have = token >= 0 && token < c.T;
+// A row of x by a warp; without one, or outside x, zeros.
+__device__ __forceinline__ void copy_row(const RowCopy &c, int64_t row, bool have, int part,
+                                         int parts, int lane) {
+    const int64_t token = have && c.row_token ? c.row_token[row] : row;
+    have = have && token >= 0 && token < c.T;
     const uint16_t *from = c.x + (have ? token : 0) * c.K;
     uint16_t *to = c.to + row * c.pitch;
     if (c.K % 8 == 0 && reinterpret_cast<uintptr_t>(c.x) % 16 == 0) {
-        constexpr int kStride = 32 * 8;
-        for (int i0 = lane * 8; i0 < c.K; i0 += kStride * kLoads) {
+        const int stride = parts * 32 * 8;
+        for (int i0 = (part * 32 + lane) * 8; i0 < c.K; i0 += stride * kLoads) {
             uint4 v[kLoads];
 #pragma unroll
             for (int l = 0; l < kLoads; ++l) {
                 v[l] = make_uint4(0, 0, 0, 0);
-                if (have && i0 + kStride * l < c.K)
-                    v[l] = __ldg(reinterpret_cast<const uint4 *>(from + i0 + kStride * l));
+                if (have && i0 + stride * l < c.K)
+                    v[l] = __ldg(reinterpret_cast<const uint4 *>(from + i0 + stride * l));
             }
 #pragma unroll
             for (int l = 0; l < kLoads; ++l)
-                if (i0 + kStride * l < c.K)
-                    *reinterpret_cast<uint4 *>(to + i0 + kStride * l) = v[l];
+                if (i0 + stride * l < c.K)
+                    *reinterpret_cast<uint4 *>(to + i0 + stride * l) = v[l];
         }
     } else {
-        for (int i = lane; i < c.K; i += 32) to[i] = have ? from[i] : 0;
+        for (int i = part * 32 + lane; i < c.K; i += parts * 32) to[i] = have ? from[i] : 0;
     }
 }
 
@@ -89,22 +99,28 @@ expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t
     using Ops = VecOps<VEC>;
     using V = typename Ops::V;
     __shared__ int s_pieces[MOEF_MAX_EXPERTS + 1], s_first[MOEF_MAX_EXPERTS],
-        s_rows[MOEF_MAX_EXPERTS], s_warp[kWarps];
+        s_rows[MOEF_MAX_EXPERTS], s_warp[kWarps];       // s_rows: of x, not those of zeros
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int cols = GATED ? 2 * n : n;
     wait_previous_kernel();
     allow_next_kernel();
     // the pieces before each expert: a scan over four experts a thread
     constexpr int kEach = MOEF_MAX_EXPERTS / kThreads;
-    int own[kEach], sum = 0;
+    int own[kEach], sum = 0, spaced = 1;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int e = threadIdx.x * kEach + i;
         own[i] = 0;
         if (e < g.E) {
-            s_rows[e] = rows_of(g, e, &s_first[e]);
-            own[i] = (s_rows[e] + kWarps - 1) / kWarps;
+            own[i] = s_rows[e] = rows_of(g, e, &s_first[e]);
+            spaced &= spaced_rows(s_first[e], own[i], g.offsets[e + 1], g.P);
         }
+    }
+    spaced = __syncthreads_and(spaced);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (spaced) own[i] = rounded_rows(own[i]);
+        own[i] = (own[i] + kWarps - 1) / kWarps;
         sum += own[i];
     }
     int before = sum;
@@ -128,21 +144,37 @@ expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t
     }
     __syncthreads();
 
-    for (int piece = blockIdx.x; piece < total; piece += gridDim.x) {
+    const int widest = max(n / VEC, copy.to ? copy.K / 8 : 0);      // vectors of a row
+    const int parts = total > 0 ? max(1, min(static_cast<int>(gridDim.x) / total, widest / 32)) : 1;
+    // total * parts is at most the larger of total and the grid
+    for (unsigned unit = blockIdx.x; unit < static_cast<unsigned>(total * parts);
+         unit += gridDim.x) {
+        const int piece = unit / parts, part = unit - piece * parts;
         int lo = 0, hi = g.E;           // s_pieces[lo] <= piece < s_pieces[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (s_pieces[mid] <= piece) lo = mid; else hi = mid;
         }
         const int at = (piece - s_pieces[lo]) * kWarps + warp;
-        if (at >= s_rows[lo]) continue;
+        const int rows = s_rows[lo];
+        if (at >= (spaced ? rounded_rows(rows) : rows)) continue;
         const int64_t row = static_cast<int64_t>(s_first[lo]) + at;
-        if (copy.to) copy_row(copy, row, lane);
-        for (int i0 = lane * VEC; dz && i0 < n; i0 += 32 * VEC * kLoads) {
+        const bool have = at < rows;
+        const int stride = parts * 32 * VEC;
+        if (copy.to) copy_row(copy, row, have, part, parts, lane);
+        if (!have && dz) {
+            const float zeros[VEC] = {};
+            for (int i = (part * 32 + lane) * VEC; i < n; i += stride)
+#pragma unroll
+                for (int h = 0; h < (GATED ? 2 : 1); ++h)
+                    *reinterpret_cast<V *>(dz + row * pitch + h * n + i) = Ops::from_f32(zeros);
+            continue;
+        }
+        for (int i0 = (part * 32 + lane) * VEC; dz && i0 < n; i0 += stride * kLoads) {
             V d[kLoads], z[kLoads], u[kLoads];
 #pragma unroll
             for (int l = 0; l < kLoads; ++l) {
-                const int i = i0 + 32 * VEC * l;
+                const int i = i0 + stride * l;
                 if (i >= n) break;
                 d[l] = Ops::load(dout + row * n + i);
                 if (preact) z[l] = Ops::load(preact + row * cols + i);
@@ -150,7 +182,7 @@ expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t
             }
 #pragma unroll
             for (int l = 0; l < kLoads; ++l) {
-                const int i = i0 + 32 * VEC * l;
+                const int i = i0 + stride * l;
                 if (i >= n) break;
                 float df[VEC], zf[VEC] = {}, uf[VEC] = {}, out[GATED ? 2 : 1][VEC];
                 Ops::to_f32(d[l], df);
@@ -249,9 +281,7 @@ bool vectors(const void *a, const void *b, const void *c, int n) {
 cudaError_t launch_expert_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
                              uint16_t *dz, int64_t pitch, const Groups &g, int n,
                              const RowCopy &copy, int num_sms, cudaStream_t stream) {
-    const int64_t need = (g.P + kWarps - 1) / kWarps + (g.E < g.P ? g.E : g.P);
-    const int64_t most = static_cast<int64_t>(num_sms) * kCtasPerSm;
-    const dim3 grid(static_cast<unsigned>(need < most ? need : most));
+    const dim3 grid(static_cast<unsigned>(num_sms * kCtasPerSm));
     auto go = [&](auto *kernel) {
         return start(kernel, grid, stream, dout, preact, act, dz, pitch, g, n, copy);
     };

@@ -98,6 +98,7 @@ struct Header {
     int bn;
     int tiles;
     int log_split;
+    int spaced;
     // expert groups: column tiles before each, first row, rows
     int prefix[MOEF_MAX_EXPERTS + 1], first[MOEF_MAX_EXPERTS], count[MOEF_MAX_EXPERTS];
 };
@@ -761,19 +762,22 @@ __device__ __forceinline__ void send_columns(const Tile &t, uint32_t tmem, uint3
 template <int CG, bool DW>
 __device__ __forceinline__ void count_tiles(const Gemm &g, const TcPlan &p, Header *h) {
     const int lane = threadIdx.x & 31, room = DW ? g.K : g.N;
-    int most = 0;
+    int most = 0, spaced = 1;
     for (int e = threadIdx.x; e < g.E; e += kTcThreads) {
         const int first = g.offsets[e], rows = g.counts[e];
         const int count = first < 0 ? 0 : max(0, min(rows, room - first));
         h->first[e] = first;
         h->count[e] = count;
         most = max(most, count);
+        if constexpr (DW) spaced &= spaced_rows(first, count, g.offsets[e + 1], room);
     }
     if constexpr (DW) {
+        spaced = __syncthreads_and(spaced);
         if (threadIdx.x == 0) {
             h->bn = p.bn;
             h->tiles = g.E * p.m_tiles * p.n_tiles;
             h->log_split = 0;
+            h->spaced = spaced;
         }
         return;
     }
@@ -827,12 +831,19 @@ struct BlockRows {
 
 // A block of grouped dweight, `boxes` times 64 columns from x on.  The last block of
 // an expert ends where the next one's rows, or padding with anything in it, begin:
-// its rows come four to a copy, with zeros behind the last.
+// its rows come four to a copy, with zeros behind the last, at 17 bytes a clock (a
+// ninth block of 8 rows cost 0.26 us a tile, a whole one takes 0.33).  With zeros
+// behind them already (`zeros`), they come as whole blocks, of which the products
+// take the steps that have rows.
+__device__ __forceinline__ uint32_t block_bytes(const BlockRows &b, bool zeros, int boxes) {
+    return boxes * (zeros ? 8192 : b.steps * 16 * 128);
+}
+
 template <int CG>
-__device__ __forceinline__ void copy_block(const BlockRows &b, uint32_t dst, int boxes,
+__device__ __forceinline__ void copy_block(const BlockRows &b, bool zeros, uint32_t dst, int boxes,
                                            const CUtensorMap *map, const CUtensorMap *rows_map,
                                            int x, int row0, uint32_t bar) {
-    if (b.rows == kBlockK) {
+    if (zeros || b.rows == kBlockK) {
         for (int i = 0; i < boxes; ++i) tma_2d<CG>(dst + i * 8192, map, x + 64 * i, row0, bar);
     } else {
         for (int quad = 0; quad < 4 * b.steps; ++quad) {
@@ -992,8 +1003,11 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
                         ok = wait(smem_addr(&h->empty[s]), phase, gave_up);
                         if (!ok) break;
                         const uint32_t full = smem_addr(&h->full[s]);
-                        if (leader) bar_expect(full, CG * (2 + boxes) * b.steps * 16 * 128);
-                        copy_block<CG>(b, stage0 + s * stage_bytes + kATile, boxes,
+                        const bool zeros = h->spaced && g.b_zeros;
+                        if (leader)
+                            bar_expect(full, CG * (block_bytes(b, h->spaced && g.a_zeros, 2) +
+                                                   block_bytes(b, zeros, boxes)));
+                        copy_block<CG>(b, zeros, stage0 + s * stage_bytes + kATile, boxes,
                                        &work.map[0][1], &work.map[0][DW ? 3 : 1],
                                        t.b0 + half * bnc, t.first + kb * kBlockK,
                                        CG == 2 ? map_rank(full, lead) : full);
@@ -1098,7 +1112,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
                         ok = wait(smem_addr(&h->empty[s]), phase, gave_up);
                         if (!ok) break;
                         const uint32_t full = smem_addr(&h->full[s]);
-                        copy_block<CG>(BlockRows(t, kb), stage0 + s * stage_bytes, 2,
+                        copy_block<CG>(BlockRows(t, kb), h->spaced && g.a_zeros, stage0 + s * stage_bytes, 2,
                                        &work.map[0][0], wide, t.m0 + half * m_cta_rows,
                                        t.first + kb * kBlockK,
                                        CG == 2 ? map_rank(full, lead) : full);
@@ -1654,7 +1668,8 @@ bool launch_two_gemms_tc(const Gemm *g, const BiasSum &bias, int num_sms, cudaSt
 }
 
 // Pairs of CTAs: an expert's tile is 256 inputs by up to 256 features, all its rows
-// in one sum.  Narrower while that leaves pairs without a tile.
+// in one sum.  The width is priced as choose_cut prices its cuts, with as many rows
+// for each expert as the buffer has.
 cudaError_t launch_group_dweight(const Gemm &g, int num_sms, cudaStream_t stream) {
     if (!encoder()) return cudaErrorNotSupported;
     Work<1, true> work;
@@ -1666,9 +1681,18 @@ cudaError_t launch_group_dweight(const Gemm &g, int num_sms, cudaStream_t stream
     p.vectors = g.M % 8 == 0 && aligned16(g.out);
     p.m_tiles = static_cast<int>(ceil_div(g.M, 256));
     const int64_t slots = num_sms / 2;
-    int most = kMaxBn;
-    while (most > 64 && g.E * p.m_tiles * ceil_div(g.N, most) < slots) most /= 2;
-    p.bn = even_columns(g, 2, most);
+    const int64_t blocks = ceil_div(ceil_div(g.K, g.E), kBlockK);
+    double least = 1e300;
+    for (int most = 32; most <= kMaxBn; most += 32) {
+        const int bn = even_columns(g, 2, most);
+        const double sum = blocks * block_clocks(g, 2, bn, 0), tail = epilogue_clocks(bn);
+        const int64_t rounds = ceil_div(g.E * p.m_tiles * ceil_div(g.N, bn), slots);
+        const double price = rounds * ((sum > tail ? sum : tail) + 300.0) + tail;
+        if (price <= least) {
+            least = price;
+            p.bn = bn;
+        }
+    }
     p.n_tiles = static_cast<int>(ceil_div(g.N, p.bn));
     const int64_t tiles = static_cast<int64_t>(g.E) * p.m_tiles * p.n_tiles;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;

@@ -114,7 +114,9 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
         Gemm d = g;
         d.a = copies_x ? copy.to : u16(x);
         d.a_pitch = copies_x ? copy.pitch : K;
+        d.a_zeros = copies_x;
         d.b_mn = 1;
+        d.b_zeros = dz != nullptr;
         d.N = cols;
         d.K = static_cast<int>(P);
         d.out = dweight;
