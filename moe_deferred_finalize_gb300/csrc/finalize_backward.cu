@@ -509,24 +509,26 @@ finalize_backward_ring_kernel(const __grid_constant__ FinalizeBackward p,
     }
 }
 
-// dgamma = the column sums of partial [rows, H]: 32 columns a CTA, its eight
-// warps every eighth row each, added in order.
-__global__ void __launch_bounds__(256)
+// dgamma = the column sums of partial [rows, H]: 32 columns a CTA, its warps every
+// sixteenth row each, added in order.
+constexpr int kSumWarps = 16;
+
+__global__ void __launch_bounds__(32 * kSumWarps)
 gamma_sum_kernel(const float *partial, uint16_t *dgamma, int rows, int H) {
-    __shared__ float sums[8][32];
+    __shared__ float sums[kSumWarps][32];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
     wait_previous_kernel();
     allow_next_kernel();
     float sum = 0.f;
     if (c < H) {
 #pragma unroll 8
-        for (int i = warp; i < rows; i += 8) sum += partial[static_cast<int64_t>(i) * H + c];
+        for (int i = warp; i < rows; i += kSumWarps) sum += partial[static_cast<int64_t>(i) * H + c];
     }
     sums[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && c < H) {
 #pragma unroll
-        for (int w = 1; w < 8; ++w) sum += sums[w][lane];
+        for (int w = 1; w < kSumWarps; ++w) sum += sums[w][lane];
         dgamma[c] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
     }
 }
@@ -750,7 +752,7 @@ cudaError_t launch_finalize_backward(const FinalizeBackward &p, int num_sms,
     if (!vec || cut.splits > 1 || !start_ring(p, cut, stream, &err))
         err = vec ? start_backward<8>(p, cut, stream) : start_backward<1>(p, cut, stream);
     if (err == cudaSuccess && p.dgamma)
-        err = start(gamma_sum_kernel, (p.H - 1) / 32 + 1, 256, 0, 1, stream, p.partial, p.dgamma,
+        err = start(gamma_sum_kernel, (p.H - 1) / 32 + 1, 32 * kSumWarps, 0, 1, stream, p.partial, p.dgamma,
                     static_cast<int>(cut.clusters), p.H);
     return err;
 }
