@@ -164,7 +164,8 @@ moef_status moe_expert_linear_save(const void *x, int64_t T, const int32_t *row_
  *                  copied as it lies (with row_token, when the width is not a
  *                  multiple of 8, or x not 16-byte aligned), else 0
  *
- * Rows of no expert are read by nothing that counts: they may hold anything.
+ * With T or P 0 dweight and dbias are zeros and nothing else is done.  Rows of
+ * no expert are read by nothing that counts: they may hold anything.
  * Rows at or past P, and experts whose offset is negative, take no part.  dz
  * is rounded to bf16 for the two products; dbias sums it before that.  A
  * row_token outside [0, T) counts as a row of zeros in dweight.

@@ -85,25 +85,6 @@ def _describe(t):
     return None if t is None else _abi._TO_DLPACK(t)
 
 
-class _Outputs:
-    """Outputs of a one-pass call: a dict of them, and what the extension is
-    given: descriptions of those that the caller gave, the addresses of those
-    made here."""
-
-    def __init__(self):
-        self.res, self.at = {}, []
-
-    def add(self, name, wanted, given, shape, dtype, device):
-        if given is not None:
-            self.res[name] = given
-            self.at.append(_abi._TO_DLPACK(given))
-        elif wanted:
-            self.res[name] = t = torch.empty(shape, dtype=dtype, device=device)
-            self.at.append(t.data_ptr())
-        else:
-            self.at.append(None)
-
-
 def finalize_backward_workspace_bytes(T: int, H: int) -> int:
     """Bytes of workspace moe_finalize_backward needs for dgamma."""
     return int(_lib().moe_finalize_backward_workspace_bytes(_int(int(T)), _int(int(H))))
@@ -228,37 +209,65 @@ def _fast_finalize_backward(permuted_out, idx_map, weights, wkind, dout, routed_
         dev = _fast_device(fast, permuted_out)
         if dev is None:
             return None
-        device, shape = permuted_out.device, (idx_map.shape[0], permuted_out.shape[1])
+        device, d, empty_like = permuted_out.device, _abi._TO_DLPACK, torch.empty_like
+        like = dnorm_out if norm else dresidual_out
         separate = residual and dout is not None
         if residual and not separate and dshared is not None:
             return None
-        o = _Outputs()
-        o.add("drows", want_drows, drows, permuted_out.shape, torch.bfloat16, device)
-        o.add("dweights", want_dweights, dweights, idx_map.shape, torch.float32, device)
-        o.add("dshared", separate, dshared, shape, torch.bfloat16, device)
-        o.add("dresidual", residual, dresidual, shape, torch.bfloat16, device)
-        o.add("dgamma", norm and want_dgamma, dgamma, shape[1:], torch.bfloat16, device)
-        res = o.res
-        if not res:
-            return None
-        if residual and not separate:
-            res["dshared"] = res["dresidual"]
-        nbytes, at = 0, None
-        if "dgamma" in res:
+        # what the extension is given for an output: the description of one that the
+        # caller gave, the address of one made here
+        res, at = {}, [None] * 5
+        if drows is not None:
+            res["drows"], at[0] = drows, d(drows)
+        elif want_drows:
+            res["drows"] = drows = empty_like(permuted_out)
+            at[0] = drows.data_ptr()
+        if dweights is not None:
+            res["dweights"], at[1] = dweights, d(dweights)
+        elif want_dweights:
+            res["dweights"] = dweights = torch.empty(idx_map.shape, dtype=torch.float32,
+                                                     device=device)
+            at[1] = dweights.data_ptr()
+        if residual:
+            if dresidual is None:
+                dresidual = empty_like(like)
+                at[3] = dresidual.data_ptr()
+            else:
+                at[3] = d(dresidual)
+            res["dresidual"] = dresidual
+            if not separate:
+                res["dshared"] = dresidual
+            elif dshared is None:
+                res["dshared"] = dshared = empty_like(like)
+                at[2] = dshared.data_ptr()
+            else:
+                res["dshared"], at[2] = dshared, d(dshared)
+        nbytes, ws = 0, None
+        if norm and (want_dgamma or dgamma is not None):
+            if dgamma is None:
+                dgamma = empty_like(gamma)
+                at[4] = dgamma.data_ptr()
+            else:
+                at[4] = d(dgamma)
+            res["dgamma"] = dgamma
             if workspace is not None:
                 nbytes = _workspace_bytes(workspace, device)
             else:
-                nbytes = fast.call_size(_address("moe_finalize_backward_workspace_bytes"), *shape)
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes \
-                    else None
-            at = _ptr(workspace)
+                nbytes = fast.call_size(_address("moe_finalize_backward_workspace_bytes"),
+                                        idx_map.shape[0], permuted_out.shape[1])
+                if nbytes:
+                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            ws = None if workspace is None else workspace.data_ptr()
+        if not res:
+            return None
         code, bits = _WCODE[wkind]
         st = fast.checked_finalize_backward(
             _address("moe_finalize_backward"), WKIND[wkind], code, bits, routed_scale, eps, dev,
-            _raw_stream(stream, dev), at, nbytes, _abi._TO_DLPACK(permuted_out),
-            _abi._TO_DLPACK(idx_map), _abi._TO_DLPACK(weights), _describe(residual_out),
-            _describe(gamma), _describe(dout), _describe(dresidual_out), _describe(dnorm_out),
-            *o.at)
+            _raw_stream(stream, dev), ws, nbytes, d(permuted_out), d(idx_map), d(weights),
+            None if residual_out is None else d(residual_out), None if gamma is None else d(gamma),
+            None if dout is None else d(dout),
+            None if dresidual_out is None else d(dresidual_out),
+            None if dnorm_out is None else d(dnorm_out), *at)
     except _REFUSED:
         return None
     if st < 0:
@@ -408,31 +417,37 @@ def _fast_expert_backward(where, gated, dout, x, row_token, offsets, counts, wei
             return None
         act, device = ACTIVATION[activation], dout.device
         P, (E, cols, K) = dout.shape[0], weight.shape
-        o = _Outputs()
+        d, res, at = _abi._TO_DLPACK, {}, []
         for name, wanted, t, shape in zip(("dx", "dweight", "dbias"), want, given,
                                           ((P, K), (E, cols, K), (E, cols))):
-            o.add(name, wanted, t, shape, torch.bfloat16, device)
-        if not o.res:
+            if t is not None:
+                res[name] = t
+                at.append(d(t))
+            elif wanted:
+                res[name] = t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+                at.append(t.data_ptr())
+            else:
+                at.append(None)
+        if not res:
             return None
         if workspace is not None:
             nbytes = _workspace_bytes(workspace, device)
         else:
-            copies = "dweight" in o.res and (row_token is not None or K % 8 or
-                                             x.data_ptr() % 16)
+            copies = "dweight" in res and (row_token is not None or K % 8 or
+                                           x.data_ptr() % 16)
             nbytes = fast.call_size3(_address("moe_expert_backward_workspace_bytes"), P, cols,
                                      K if copies else 0)
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-        d = _abi._TO_DLPACK
         st = fast.checked_expert_backward(
             _address(where), gated, act, dev, _raw_stream(stream, dev), _ptr(workspace), nbytes,
             d(dout), d(x), _describe(row_token), d(offsets), d(counts), d(weight),
-            _describe(preact), *o.at)
+            _describe(preact), *at)
     except _REFUSED:
         return None
     if st < 0:
         return None
     _raise(st, where)
-    return o.res
+    return res
 
 
 def _expert_backward(where, gated, dout, x, row_token, offsets, counts, weight, preact,
@@ -556,11 +571,10 @@ class BoundAdamW:
     """An AdamW step whose tensors were checked and marshalled once (``bind_adamw``).
 
     Calling it enqueues one step over them.  The tensors must stay alive and
-    keep their storage while the object is used, and their device must be the
-    current CUDA device when it is called."""
+    keep their storage while the object is used."""
 
-    def __init__(self, table, kept, config, device):
-        self._table, self._kept, self._config, self._device = table, kept, config, device
+    def __init__(self, table, kept, types, device):
+        self._table, self._kept, self._types, self._device = table, kept, types, device
         self._fn = _lib().moe_adamw_step
 
     def __call__(self, *, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -569,18 +583,18 @@ class BoundAdamW:
         """One step.  ``step``: the number of this step, from 1, or an int32
         device number; ``lr``: a number, or a float32 device number;
         ``grad_scale``: a float32 device number that multiplies the gradients."""
-        c, dev = self._config, self._device
-        on_device = isinstance(step, torch.Tensor)
-        c.device_step = _ptr(_number(step, "step", torch.int32, dev)) if on_device else None
-        c.step = 1 if on_device else _int(int(step))
+        dev = self._device
+        device_step = device_lr = None
+        if isinstance(step, torch.Tensor):
+            device_step, step = _ptr(_number(step, "step", torch.int32, dev)), 1
         if isinstance(lr, torch.Tensor):
-            c.device_lr, c.lr = _ptr(_number(lr, "lr", torch.float32, dev)), 0.0
-        else:
-            c.device_lr, c.lr = None, float(lr)
-        c.beta1, c.beta2 = float(betas[0]), float(betas[1])
-        c.eps, c.weight_decay = float(eps), float(weight_decay)
-        c.grad_scale = _ptr(_number(grad_scale, "grad_scale", torch.float32, dev))
-        st = self._fn(self._table, len(self._table), ctypes.byref(c), _stream(stream, dev))
+            device_lr, lr = _ptr(_number(lr, "lr", torch.float32, dev)), 0.0
+        config = AdamWConfig(lr, betas[0], betas[1], eps, weight_decay, device_step, device_lr,
+                             _ptr(_number(grad_scale, "grad_scale", torch.float32, dev)),
+                             _int(int(step)), *self._types)
+        with _on(dev):
+            st = self._fn(self._table, len(self._table), ctypes.byref(config),
+                          _stream(stream, dev))
         _raise(st, "moe_adamw_step")
 
 
@@ -645,9 +659,8 @@ def bind_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                 t = lists[name][i]
                 _check(t, f"{name}[{i}]", (t_dtype,), shape, dev)
                 setattr(row, field, t.data_ptr())
-    config = AdamWConfig(state_bits=8 if eight else 32, param_type=_OUT_TYPE[dtype],
-                         grad_type=_OUT_TYPE[grad_dtype])
-    return BoundAdamW(table, kept, config, dev)
+    return BoundAdamW(table, kept, (8 if eight else 32, _OUT_TYPE[dtype], _OUT_TYPE[grad_dtype]),
+                      dev)
 
 
 def adamw_state(params: Sequence[torch.Tensor], bits: int = 32, master: bool = False) -> dict:
@@ -682,6 +695,5 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     of what it returns."""
     bound = bind_adamw(params, grads, exp_avg, exp_avg_sq, masters=masters,
                        exp_avg_scale=exp_avg_scale, exp_avg_sq_scale=exp_avg_sq_scale)
-    with _on(bound._device):
-        bound(step=step, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
-              grad_scale=grad_scale, stream=stream)
+    bound(step=step, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
+          grad_scale=grad_scale, stream=stream)

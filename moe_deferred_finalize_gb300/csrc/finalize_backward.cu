@@ -405,14 +405,16 @@ finalize_backward_ring_kernel(const __grid_constant__ FinalizeBackward p,
             inv = rsqrtf(sum.x / static_cast<float>(p.H) + p.eps);
             mean = inv * inv * (sum.y / static_cast<float>(p.H));
         }
+        // both gradients are here before either output is written, which may be them
         float dm[VPT][8] = {};
+        uint4 d_out[VPT] = {};
         int i = NORM ? 2 : 0;
         if (p.dres) {
-            uint4 x[VPT];
-            take(i++, x);
+            take(i++, d_out);
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) Ops::to_f32(x[j], dm[j]);
+            for (int j = 0; j < VPT; ++j) Ops::to_f32(d_out[j], dm[j]);
         }
+        if (p.dout) take(i++, d_out);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + j * nt;
@@ -441,12 +443,10 @@ finalize_backward_ring_kernel(const __grid_constant__ FinalizeBackward p,
             if (p.dresidual) Ops::store(p.dresidual + tok + v * 8, Ops::from_f32(dm[j]));
         }
         if (p.dout) {
-            uint4 x[VPT];
-            take(i++, x);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 float f[8];
-                Ops::to_f32(x[j], f);
+                Ops::to_f32(d_out[j], f);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) dm[j][q] += f[q];
             }

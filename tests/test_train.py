@@ -767,3 +767,217 @@ def test_two_streams_at_once(cuda_lib):
             assert torch.equal(res["dx"][have], want["dx"][have])
         for k in ("dweights", "dgamma", "dshared", "dresidual"):
             assert torch.equal(f[k], fwant[k])
+
+
+# ------------------------------------------- other sizes, paths and callers
+
+
+@pytest.mark.parametrize("T", [20, 900])       # one CTA a slice; rows through the ring
+@pytest.mark.parametrize("K", [1, 8])
+def test_finalize_backward_outputs_on_either_input(cuda_lib, T, K):
+    """dshared and dresidual in place of dout and dresidual_out, either way round."""
+    mf = cuda_lib
+    case = (T, K, 16, 2048, 8, "fp32", True, True, True, 0.1)
+    rows, m, w, dout, kw = finalize_inputs(mf, case)
+    want = mf.moe_finalize_backward(rows, m["idx_map"], w, "fp32", dout, **kw)
+    for swap in (False, True):
+        a, b = dout.clone(), kw["dresidual_out"].clone()
+        out = dict(dshared=b, dresidual=a) if swap else dict(dshared=a, dresidual=b)
+        got = mf.moe_finalize_backward(rows, m["idx_map"], w, "fp32", a,
+                                       **{**kw, "dresidual_out": b}, **out)
+        for k in ("dshared", "dresidual", "dweights", "dgamma"):
+            assert torch.equal(got[k], want[k]), (swap, k)
+
+
+RING = [
+    # T, K, E, H, tile, wkind, norm, dout, dres, absent: both sides of the ring's rules
+    (400, 8, 16, 7168, 8, "fp32", True, True, True, 0.1),
+    (400, 8, 16, 7168, 8, "packed", True, False, False, 0.0),
+    (400, 5, 16, 8192, 1, "fp32", True, True, True, 0.5),
+    (500, 4, 8, 7168, 1, "bf16", False, True, False, 0.2),
+    (500, 3, 8, 7168, 1, "bf16", False, True, False, 0.2),
+    (2500, 32, 40, 128, 1, "fp32", True, True, False, 0.1),
+    (3000, 2, 8, 8, 1, "fp32", True, True, True, 0.0),
+    (700, 6, 8, 4096, 1, "fp32", False, True, True, 1.0),
+    (610, 8, 16, 8200, 1, "fp32", True, True, True, 0.0),
+]
+
+
+@pytest.mark.parametrize("case", RING, ids=str)
+def test_finalize_backward_many_tokens(cuda_lib, case):
+    mf = cuda_lib
+    rows, m, w, dout, kw = finalize_inputs(mf, case, seed=2)
+    drows0 = torch.full_like(rows, 7.0)
+    res = mf.moe_finalize_backward(rows, m["idx_map"], w, case[5], dout, routed_scale=0.5,
+                                   drows=drows0.clone(), **kw)
+    check_finalize(case, rows, m, w, dout, kw, res, drows0, 0.5, 1e-6)
+    one = mf.moe_finalize_backward(rows, m["idx_map"], w, case[5], dout, routed_scale=0.5,
+                                   want_drows=False, **kw)
+    two = mf.moe_finalize_backward(rows, m["idx_map"], w, case[5], dout, routed_scale=0.5,
+                                   want_dweights=False, drows=drows0.clone(), **kw)
+    for k in res:
+        for other in (one, two):
+            if k in other:
+                assert torch.equal(other[k], res[k]), k
+
+
+def test_one_pass_calls_equal_checked_calls(cuda_lib, monkeypatch):
+    """The same results with and without the call extension."""
+    mf = cuda_lib
+    from moe_deferred_finalize_gb300 import _abi
+    if _abi._fastcall() is None:
+        pytest.skip("_fastcall not built (no Python headers)")
+    fcase = (30, 4, 8, 256, 8, "bf16", True, True, True, 0.1)
+    rows, m, w, dout, kw = finalize_inputs(mf, fcase)
+    ecase = (60, 2, 4, 128, 72, 8, "silu", True, True, 2)
+    em, x, ew, edout, preact = expert_inputs(mf, ecase)
+    lcase = (60, 2, 4, 128, 72, 8, "none", True, False, 2)
+    lm, lx, lw, ldout, _ = expert_inputs(mf, lcase)
+    logits = torch.randn(20, 16, device="cuda")
+    route = mf.topk_route(logits, 4)
+    dw = torch.randn(20, 4, device="cuda")
+    add = normal(gen(0), 30, 256)
+
+    def everything():
+        zero = torch.zeros_like
+        r = {("f", k): v for k, v in mf.moe_finalize_backward(
+            rows, m["idx_map"], w, "bf16", dout, drows=zero(rows), **kw).items()}
+        r.update({("e", k): v for k, v in expert_call(
+            mf, ecase, em, x, ew, edout, preact,
+            dx=zero(normal(gen(0), edout.shape[0], 128))).items()})
+        r.update({("l", k): v for k, v in expert_call(
+            mf, lcase, lm, lx, lw, ldout, None,
+            dx=zero(normal(gen(0), ldout.shape[0], 128))).items()})
+        r["u"] = mf.unpermute_tokens(rows, m["idx_map"], add=add)
+        r["g"] = mf.topk_route_backward(dw, route["weights"], route["expert_ids"], 16,
+                                        logits=logits)
+        return r
+
+    fast = everything()
+    monkeypatch.setattr(_abi, "_FAST", None)
+    slow = everything()
+    assert fast.keys() == slow.keys()
+    for k in fast:
+        assert torch.equal(fast[k], slow[k]), k
+
+
+def test_refusals_name_the_tensor(cuda_lib):
+    """What the one-pass checks refuse, the binding names."""
+    mf = cuda_lib
+    fcase = (6, 2, 4, 64, 1, "fp32", True, True, True, 0.0)
+    rows, m, w, dout, kw = finalize_inputs(mf, fcase)
+    idx = m["idx_map"]
+    bad = [(dict(dout=dout.float()), "dout"), (dict(dout=dout[:5]), "dout"),
+           (dict(weights=w.to(BF16)), "weights"), (dict(residual_out=None), "residual_out"),
+           (dict(gamma=kw["gamma"][:8]), "gamma"), (dict(dgamma=dout), "dgamma"),
+           (dict(drows=rows[:1]), "drows"), (dict(dresidual=dout.T.contiguous().T), "dresidual"),
+           (dict(idx_map=idx.long()), "idx_map")]
+    for change, name in bad:
+        args = dict(permuted_out=rows, idx_map=idx, weights=w, wkind="fp32", dout=dout, **kw)
+        with pytest.raises((ValueError, TypeError), match=name):
+            mf.moe_finalize_backward(**{**args, **change})
+    with pytest.raises(ValueError, match="go with dnorm_out"):
+        mf.moe_finalize_backward(rows, idx, w, "fp32", dout, gamma=kw["gamma"])
+    with pytest.raises(ValueError, match="no gradient"):
+        mf.moe_finalize_backward(rows, idx, w, "fp32")
+    with pytest.raises(ValueError, match="at most two"):
+        mf.unpermute_tokens(rows, idx, add=[dout] * 3)
+    with pytest.raises(ValueError, match="add"):
+        mf.unpermute_tokens(rows, idx, add=dout[:, :8].contiguous())
+    ecase = (20, 2, 4, 64, 24, 1, "silu", False, True, 0)
+    em, x, ew, edout, preact = expert_inputs(mf, ecase)
+    args = dict(dout=edout, x=x, row_token=em["row_token"], offsets=em["offsets"],
+                counts=em["counts"], weight=ew, preact=preact)
+    for change, name in [(dict(preact=preact[:, :8].contiguous()), "preact"),
+                         (dict(weight=ew[:, :8].contiguous()), "weight"),
+                         (dict(row_token=em["row_token"][:3]), "row_token"),
+                         (dict(row_token=None), "row_token"), (dict(dweight=ew[0]), "dweight"),
+                         (dict(offsets=em["offsets"][:2]), "offsets")]:
+        with pytest.raises((ValueError, TypeError), match=name):
+            mf.expert_gated_ffn_backward(**{**args, **change})
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(mf.MoefError, match="SHAPE"):
+        mf.expert_gated_ffn_backward(**args, workspace=small)
+    p = [torch.zeros(8, dtype=BF16, device="cuda")]
+    state = mf.adamw_state(p)
+    for change in (dict(grads=[p[0][:4]]), dict(grads=p * 2), dict(masters=[p[0]]),
+                   dict(exp_avg=[p[0]]), dict(exp_avg_scale=[torch.zeros(1, device="cuda")])):
+        with pytest.raises(ValueError):
+            mf.bind_adamw(**{**dict(params=p, grads=p, **state), **change})
+    with pytest.raises(ValueError, match="lr"):
+        mf.adamw_step(p, p, step=1, lr=torch.zeros(2, device="cuda"), **state)
+    with pytest.raises(mf.MoefError, match="ARG"):
+        mf.adamw_step(p, p, step=0, **state)
+
+
+@pytest.mark.slow
+def test_rows_past_31_bits(cuda_lib):
+    """Row offsets past 2^31 values, in every operand that has rows."""
+    mf, g = cuda_lib, gen(11)
+    P, H, T, K = 300_000, 7168, 40, 4
+    rows = torch.zeros((P, H), dtype=BF16, device="cuda")
+    idx = torch.randint(P - 1000, P, (T, K), generator=g, device="cuda").int()
+    idx = (torch.arange(P - T * K, P, device="cuda").int()).view(T, K).contiguous()
+    rows[P - 1000:] = normal(g, 1000, H)
+    w = torch.rand(T, K, generator=g, device="cuda")
+    dout = normal(g, T, H)
+    res = mf.moe_finalize_backward(rows, idx, w, "fp32", dout)
+    ref = T_.finalize_backward(rows[P - 1000:], idx - (P - 1000), w.double(), 1.0, dout)
+    T_.check(res["dweights"], ref["dweights"], "dweights")
+    T_.check(res["drows"][idx.long()], ref["drows"], "drows")
+    T_.check(mf.unpermute_tokens(rows, idx), T_.unpermute(rows[P - 1000:], idx - (P - 1000), []),
+             "unpermute")
+    del rows, res
+    torch.cuda.empty_cache()
+    # many tokens: dense rows past 2^31 values
+    T, K, H = 310_000, 1, 7168
+    rows = normal(g, 8, H)
+    idx = torch.full((T, K), -1, dtype=torch.int32, device="cuda")
+    idx[-4:, 0] = torch.arange(4, device="cuda").int()
+    dout = torch.zeros((T, H), dtype=BF16, device="cuda")
+    dout[-4:] = normal(g, 4, H)
+    w = torch.ones((T, K), device="cuda")
+    res = mf.moe_finalize_backward(rows, idx, w, "fp32", dout)
+    T_.check(res["drows"][:4], T_.rounded(dout[-4:].double(), torch.zeros_like(dout[-4:]).double()),
+             "drows")
+    out = mf.unpermute_tokens(rows, idx, add=dout)
+    T_.check(out[-4:], T_.unpermute(rows, idx[-4:], [dout[-4:]]), "unpermute")
+
+
+@pytest.mark.slow
+def test_expert_rows_past_31_bits(cuda_lib):
+    mf, g = cuda_lib, gen(12)
+    P, E, H, I = 540_000, 2, 64, 2048           # dz: 540000 x 4096
+    offsets = torch.tensor([0, P - 70, P], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([30, 70], dtype=torch.int32, device="cuda")
+    token = torch.zeros(P, dtype=torch.int32, device="cuda")
+    token[-70:] = torch.arange(70, device="cuda").int()
+    x, w = normal(g, 70, H), normal(g, E, 2 * I, H, scale=0.1)
+    dout = torch.zeros((P, I), dtype=BF16, device="cuda")
+    preact = torch.zeros((P, 2 * I), dtype=BF16, device="cuda")
+    for rows in (slice(0, 30), slice(P - 70, P)):
+        n = rows.stop - rows.start
+        dout[rows], preact[rows] = normal(g, n, I), normal(g, n, 2 * I)
+    res = mf.expert_gated_ffn_backward(dout, x, token, offsets, counts, w, preact,
+                                       want_dbias=True)
+    ref = T_.expert_backward(dout[-70:], x, token[-70:], offsets[1:] - (P - 70), counts[1:],
+                             w[1:], preact[-70:], "silu", True)
+    T_.check(res["dx"][-70:], ref["dx"], "dx")
+    T_.check(res["dweight"][1:], ref["dweight"], "dweight")
+    T_.check(res["dbias"][1:], ref["dbias"], "dbias")
+
+
+@pytest.mark.slow
+def test_adamw_past_31_bits(cuda_lib):
+    mf = cuda_lib
+    n = 2 ** 31 + 1000
+    p = [torch.ones(n, dtype=BF16, device="cuda")]
+    grad = [torch.zeros(n, dtype=BF16, device="cuda")]
+    grad[0][-700:] = 0.5
+    state = mf.adamw_state(p, bits=8)
+    mf.adamw_step(p, grad, step=1, lr=0.125, weight_decay=0.0, eps=0.0, **state)
+    # m = 0.05, sqrt(v) = 0.0158: a step of lr; zero gradients with eps = 0 are 0 / 0
+    assert (p[0][-700:].float() == 0.875).all()
+    assert (state["exp_avg"][0][-700:].float() == 448).all()
+    assert not state["exp_avg"][0][:1000].float().any()
+    assert abs(float(state["exp_avg_scale"][0][-1]) * 448 - 0.05) < 1e-8
