@@ -605,7 +605,7 @@ __device__ __forceinline__ void store_chunk(const WidePart<GATED, RESIDUAL> &par
     }
 }
 
-template <bool DW, bool GATED, bool RESIDUAL>
+template <bool GATED, bool RESIDUAL>
 __device__ __forceinline__ void finish_wide(WidePart<GATED, RESIDUAL> &part, uint32_t stash,
                                             uint32_t tmem, uint32_t done, const float *sums,
                                             int parts) {
@@ -619,7 +619,6 @@ __device__ __forceinline__ void finish_wide(WidePart<GATED, RESIDUAL> &part, uin
     for (int c0 = part.first; c0 < end; c0 += stride) {
         uint32_t r[kChunk];
         tmem_load_fragments(tmem + c0, r);
-        if constexpr (DW) zero_without_rows(r, part.t);
         if (done && c0 + stride >= end) {       // the accumulator has been read
             fence_before();
             __syncwarp();
@@ -716,6 +715,52 @@ __device__ __forceinline__ void finish_wide(WidePart<GATED, RESIDUAL> &part, uin
                     w[j][i] = pack_bf16x2(a[8 * j + 2 * i], a[8 * j + 2 * i + 1]);
             store_chunk(part, stash, w, c0, static_cast<uint16_t *>(g.out), g.M);
         }
+    }
+}
+
+// The same for grouped dweight, which is mostly written: the sums alone, the next
+// chunk's on their way out of TMEM while one is stored.
+__device__ __forceinline__ void finish_dweight(WidePart<false, false> &part, uint32_t stash,
+                                               uint32_t tmem, uint32_t done) {
+    const int lane = part.lane, end = part.end, stride = part.stride;
+    uint16_t *out = static_cast<uint16_t *>(part.g.out);
+    if (part.first >= end) {            // nothing for this warp
+        if (lane == 0) bar_arrive(done);
+        return;
+    }
+    uint32_t r[2][kChunk];
+    auto store = [&](uint32_t (&v)[kChunk], int c0) {
+        zero_without_rows(v, part.t);
+        uint32_t w[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = 8 * (i >> 1) + 4 * j + 2 * (i & 1);
+                w[j][i] = pack_bf16x2(__uint_as_float(v[at]), __uint_as_float(v[at + 1]));
+            }
+        store_chunk(part, stash, w, c0, out, part.g.M);
+    };
+    // next: the chunk behind c0, whose sums go to v
+    auto ahead = [&](uint32_t (&v)[kChunk], int next) {
+        if (next < end) {
+            tmem_load_fragments_ahead(tmem + next, v);
+        } else {                        // the accumulator has been read
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(done);
+        }
+    };
+    tmem_load_fragments_ahead(tmem + part.first, r[0]);
+#pragma unroll 1
+    for (int c0 = part.first; c0 < end; c0 += 2 * stride) {
+        tmem_wait(r[0]);
+        ahead(r[1], c0 + stride);
+        store(r[0], c0);
+        if (c0 + stride >= end) break;
+        tmem_wait(r[1]);
+        ahead(r[0], c0 + 2 * stride);
+        store(r[1], c0 + stride);
     }
 }
 
@@ -1222,8 +1267,22 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
             };
             const int m0 = t.m0 + half * m_cta_rows;
             bool ok;
-            auto wide = [&](auto &w) { finish_wide<DW>(w, stash, acc, done, nullptr, 0); };
-            if (!DW && work.p[q].vectors && !GATED && work.g[q].residual) {
+            auto wide = [&](auto &w) {
+                if constexpr (DW) finish_dweight(w, stash, acc, done);
+                else finish_wide(w, stash, acc, done, nullptr, 0);
+            };
+            if constexpr (DW) {
+                if (work.p[q].vectors) {
+                    WidePart<false, false> part_of(work.g[q], t, m0, quarter, side, sides, lane, 0,
+                                                   t.bn);
+                    ok = finish(part_of, wide);
+                } else {
+                    TilePart<false> part_of(work.g[q], t, m0, quarter, side, sides, lane, 0, t.bn);
+                    ok = finish(part_of, [&](auto &w) {
+                        finish_tile<DW>(w, acc, done, nullptr, 0);
+                    });
+                }
+            } else if (work.p[q].vectors && !GATED && work.g[q].residual) {
                 WidePart<GATED, !GATED> part_of(work.g[q], t, m0, quarter, side, sides, lane, 0,
                                                 t.bn);
                 ok = finish(part_of, wide);
@@ -1257,12 +1316,12 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
                 WidePart<GATED, !GATED> part_of(work.g[0], t, m0, quarter, side, sides, lane, from,
                                                 from + own);
                 cluster_sync();         // every part's sums have arrived
-                if (!*gave_up) finish_wide<false>(part_of, stash, acc, 0, sums, split - 1);
+                if (!*gave_up) finish_wide(part_of, stash, acc, 0, sums, split - 1);
             } else if (work.p[0].vectors) {
                 WidePart<GATED, false> part_of(work.g[0], t, m0, quarter, side, sides, lane, from,
                                                from + own);
                 cluster_sync();
-                if (!*gave_up) finish_wide<false>(part_of, stash, acc, 0, sums, split - 1);
+                if (!*gave_up) finish_wide(part_of, stash, acc, 0, sums, split - 1);
             } else {
                 TilePart<GATED> part_of(work.g[0], t, m0, quarter, side, sides, lane, from,
                                         from + own);

@@ -9,6 +9,7 @@ For profilers: one process, a handful of launches, a known input size.
   python -m moe_deferred_finalize_gb300.run_case --tp 8 16 --form one_shot --iters 3
   python -m moe_deferred_finalize_gb300.run_case --tp-procs 16 --iters 300
   python -m moe_deferred_finalize_gb300.run_case --layer 256 --iters 20
+  python -m moe_deferred_finalize_gb300.run_case --train 4096 --iters 3
 
 --tp-procs times the orchestration of the all-reduce-fused finalize across
 processes (moe_deferred_finalize_gb300.tp, two-phase form): two processes on
@@ -19,6 +20,11 @@ wall time per step and of the barrier alone.
 map, expert products, shared expert, finalize with RMSNorm; 256 experts, top-8,
 H = 7168, I = 2048, random weights made on the device, 23 GB) as one captured
 graph, and prints its time and that of each step.
+
+--train runs a training step of such a layer with 64 experts on that many tokens:
+forward with what the backward pass needs kept, the gradients of all inputs and
+weights, and an AdamW step with fp32 master weights and states of --state-bits
+(28 GB with 8); also as one captured graph, with the time of each part.
 """
 import argparse
 import time
@@ -125,6 +131,11 @@ def _layer(T, iters):
             rows, m["idx_map"], route["weights"], "fp32", shared, routed_scale=2.5,
             residual=residual, gamma=gamma, write_out=False))
 
+    _report("layer", T, layer, t, iters)
+
+
+def _report(what, T, whole, parts, iters):
+    """The time of `whole` and of each of the parts that it filled in."""
     def timed(fn, n):
         fn()
         torch.cuda.synchronize()
@@ -140,11 +151,79 @@ def _layer(T, iters):
         del kept
         return a.elapsed_time(b) * 1e3 / n
 
-    total = timed(layer, iters)
+    total = timed(whole, iters)
     # each step by itself, on the layer's own operands (small ones run from L2)
-    parts = {name: timed(fn, iters) for name, fn in list(t.items())}
-    print(f"layer: T={T} {total:.1f} us; " +
-          ", ".join(f"{name} {us:.1f}" for name, us in parts.items()))
+    each = {name: timed(fn, iters) for name, fn in list(parts.items())}
+    print(f"{what}: T={T} {total:.1f} us; " +
+          ", ".join(f"{name} {us:.1f}" for name, us in each.items()))
+
+
+def _train(T, iters, bits):
+    E, K, H, I, tile = 64, 8, 7168, 2048, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def rand(*shape, scale=1.0):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(
+            0.0, scale, generator=g)
+
+    x, residual = rand(T, H), rand(T, H, scale=2.0)
+    dnorm, dres = rand(T, H, scale=0.01), rand(T, H, scale=0.01)
+    w = {"router": rand(E, H, scale=H ** -0.5), "w13": rand(E, 2 * I, H, scale=H ** -0.5),
+         "w2": rand(E, H, I, scale=I ** -0.5), "s13": rand(2 * I, H, scale=H ** -0.5),
+         "s2": rand(H, I, scale=I ** -0.5), "gamma": rand(H)}
+    d = {k: torch.zeros_like(v) for k, v in w.items()}
+    update = mf.bind_adamw(list(w.values()), list(d.values()),
+                           **mf.adamw_state(list(w.values()), bits, master=True))
+    count = torch.zeros(1, dtype=torch.int32, device="cuda")
+    P = mf.permute_rows(T, K, E, tile)
+    preact = torch.empty((P, 2 * I), dtype=torch.bfloat16, device="cuda")
+    drows, dh, dxr = (torch.empty((P, n), dtype=torch.bfloat16, device="cuda") for n in (H, I, H))
+    t = {}
+
+    def part(name, fn):
+        t[name] = fn
+        return fn()
+
+    def step():
+        logits = part("router", lambda: mf.linear(x, w["router"], out_dtype=torch.float32)["out"])
+        route = part("gate", lambda: mf.topk_route(logits, K, "sigmoid"))
+        m = part("row map", lambda: mf.permute_tokens(route["expert_ids"], E, tile))
+        offsets, counts = m["offsets"], m["counts"]
+        h = part("experts up", lambda: mf.expert_gated_ffn(
+            x, m["row_token"], offsets, counts, w["w13"], preact=preact))
+        rows = part("experts down", lambda: mf.expert_linear(h, offsets, counts, w["w2"]))
+        up = part("shared up", lambda: mf.gated_ffn(x, w["s13"], save_preact=True))
+        shared = part("shared down", lambda: mf.linear(up["out"], w["s2"])["out"])
+        out = part("finalize", lambda: mf.moe_finalize(
+            rows, m["idx_map"], route["weights"], "fp32", shared, routed_scale=2.5,
+            residual=residual, gamma=w["gamma"], write_out=False))
+        f = part("finalize backward", lambda: mf.moe_finalize_backward(
+            rows, m["idx_map"], route["weights"], "fp32", routed_scale=2.5, dresidual_out=dres,
+            dnorm_out=dnorm, residual_out=out["residual_out"], gamma=w["gamma"], drows=drows,
+            dgamma=d["gamma"]))
+        part("experts down backward", lambda: mf.expert_linear_backward(
+            drows, h, offsets, counts, w["w2"], dx=dh, dweight=d["w2"]))
+        part("experts up backward", lambda: mf.expert_gated_ffn_backward(
+            dh, x, m["row_token"], offsets, counts, w["w13"], preact, dx=dxr, dweight=d["w13"]))
+        s2 = part("shared down backward", lambda: mf.linear_backward(
+            f["dshared"], up["out"], w["s2"], dweight=d["s2"]))
+        s13 = part("shared up backward", lambda: mf.gated_ffn_backward(
+            s2["dx"], x, w["s13"], up["preact"], dweight=d["s13"]))
+        dlogits = part("gate backward", lambda: mf.topk_route_backward(
+            f["dweights"], route["weights"], route["expert_ids"], E, "sigmoid", logits=logits))
+        r = part("router backward", lambda: mf.linear_backward(dlogits, x, w["router"],
+                                                               dweight=d["router"]))
+        dx = part("unpermute", lambda: mf.unpermute_tokens(dxr, m["idx_map"],
+                                                           add=(s13["dx"], r["dx"])))
+
+        def adamw():
+            count.add_(1)
+            update(step=count, lr=1e-4)
+            return dx
+
+        return part("adamw", adamw)
+
+    _report(f"train, {bits}-bit states", T, step, t, iters)
 
 
 def main(argv=None):
@@ -161,6 +240,10 @@ def main(argv=None):
                    help="time the two-process orchestration (two-phase form, R=2) at batch T "
                         "(1, 16 or 256) on GPU 0 for --iters steps")
     g.add_argument("--layer", type=int, metavar="T", help="run a whole MoE layer on T tokens")
+    g.add_argument("--train", type=int, metavar="T",
+                   help="run a training step of an MoE layer on T tokens")
+    ap.add_argument("--state-bits", type=int, choices=[8, 32], default=8,
+                    help="with --train: bits of the AdamW states")
     ap.add_argument("--form", choices=["one_shot", "two_phase", "plain"], default="one_shot",
                     help="with --tp: one-shot, two-phase (phase 1 per rank, then phase 2), "
                          "or the plain finalize of rank 0's operands")
@@ -173,6 +256,9 @@ def main(argv=None):
     args = ap.parse_args(argv)
     if args.layer:
         _layer(args.layer, args.iters)
+        return
+    if args.train:
+        _train(args.train, args.iters, args.state_bits)
         return
     if args.tp_procs:
         _tp_procs(args.tp_procs, args.iters)
