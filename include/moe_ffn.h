@@ -16,7 +16,8 @@
  *   shared_out    = moe_linear(hs, w_down)             bf16 [T, H]
  *   out           = moe_finalize(permuted_out, row map, weights, shared_out)
  *
- * moe_linear and moe_gated_ffn also have their backward passes.
+ * moe_linear and moe_gated_ffn also have their backward passes; those of the
+ * expert products, the gate and the finalize are in moe_train.h.
  *
  * Conventions are those of moe_finalize.h: device pointers, bf16 as raw bit
  * patterns, dense row-major arrays, the caller owns every buffer, nothing is

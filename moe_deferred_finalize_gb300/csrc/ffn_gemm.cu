@@ -28,6 +28,11 @@
 // tiles badly; they run as one launch over both products' tiles when that is
 // priced lower (746 x 2512 x 4968: 43 us apart, 36.5 together).
 //
+// Grouped dweight sums over each expert's own rows: every expert has the same tiles,
+// with as many k blocks as it has rows (none: zeros are written), both operands m- and
+// n-contiguous.  64 experts of 4096 x 7168: 1250 us at 512 rows each (1540 TFLOP/s),
+// 704 at 128 (bound by writing 3.8 GB, 5.3 TB/s), 1025 for 8 experts of 4096 rows (1875).
+//
 // Two launch forms:
 //   CG = 2  pairs of CTAs share tiles of 256 (m) x up to 256 (n): each CTA
 //           loads half of A and half of B, one instruction drives both SMs'
