@@ -246,6 +246,89 @@ def test_adamw_state_on_the_host():
     assert set(s) == {"exp_avg", "exp_avg_sq"} and not s["exp_avg"][0].any()
 
 
+# ---------------------------------------------------------- given streams
+
+CURRENT, OTHER = 0x70, 0x90     # stream handles
+
+
+class Entered(Exception):
+    """The given stream was made the current one."""
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on cuda:0."""
+    device = property(lambda self: torch.device("cuda", 0))
+
+
+def fake(*shape, dtype=BF16):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnDevice)
+
+
+def i32(*shape):
+    return fake(*shape, dtype=torch.int32)
+
+
+def f32(*shape):
+    return fake(*shape, dtype=F32)
+
+
+FINALIZE_ARGS = lambda: (fake(8, 8), i32(4, 2), f32(4, 2), "fp32", fake(4, 8))   # noqa: E731
+NORM = lambda: dict(dnorm_out=fake(4, 8), residual_out=fake(4, 8), gamma=fake(8))   # noqa: E731
+# name, required arguments, all that the call would allocate, options
+ALLOCATING = [
+    ("moe_finalize_backward", FINALIZE_ARGS, dict(drows=(8, 8), dweights=(4, 2)), dict),
+    ("moe_finalize_backward", FINALIZE_ARGS,
+     dict(drows=(8, 8), dweights=(4, 2), dshared=(4, 8), dresidual=(4, 8), dgamma=(8,),
+          workspace=(4096,)), NORM),
+    ("unpermute_tokens", lambda: (fake(8, 8), i32(4, 2)), dict(out=(4, 8)), dict),
+    ("topk_route_backward", lambda: (f32(4, 2), f32(4, 2), i32(4, 2), 8, "softmax"),
+     dict(dlogits=(4, 8)), dict),
+    ("expert_linear_backward", lambda: (fake(8, 8), fake(8, 8), i32(3), i32(2), fake(2, 8, 8)),
+     dict(dx=(8, 8), dweight=(2, 8, 8), dbias=(2, 8), workspace=(4096,)),
+     lambda: dict(want_dbias=True)),
+    ("expert_gated_ffn_backward",
+     lambda: (fake(8, 8), fake(4, 8), i32(8), i32(3), i32(2), fake(2, 16, 8), fake(8, 16)),
+     dict(dx=(8, 8), dweight=(2, 16, 8), dbias=(2, 16), workspace=(4096,)),
+     lambda: dict(want_dbias=True)),
+]
+
+
+@pytest.mark.parametrize("name,args,outputs,options", ALLOCATING)
+def test_allocations_belong_to_the_given_stream(monkeypatch, name, args, outputs, options):
+    import moe_deferred_finalize_gb300 as mf
+    from moe_deferred_finalize_gb300 import _abi, _train
+
+    def enter(stream):
+        if stream is not None:          # None: the current one, set again on the way out
+            raise Entered(stream)
+
+    def library():
+        raise RuntimeError("these tensors must not reach the library")
+
+    monkeypatch.setattr(_abi, "_lib", library)
+    monkeypatch.setattr(_train, "_lib", library)
+    monkeypatch.setattr(_abi, "_FAST", None)
+    monkeypatch.setattr(_abi, "_RAW_STREAM", lambda index: CURRENT)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "set_stream", enter)
+    fn, a, options = getattr(mf, name), args(), options()
+    given = {k: fake(*s) for k, s in outputs.items()}
+    with pytest.raises(Entered) as e:
+        fn(*a, **options, stream=OTHER)
+    assert e.value.args == ((OTHER, torch.device("cuda", 0)),)
+    for missing in given:
+        some = {k: v for k, v in given.items() if k != missing}
+        with pytest.raises(Entered):
+            fn(*a, **options, **some, stream=OTHER)
+    # nothing to allocate, or the current stream: straight on to the checks
+    for kw in (dict(given, stream=OTHER), dict(stream=CURRENT), {}):
+        with pytest.raises(Exception) as e:
+            fn(*a, **options, **kw)
+        assert e.type is not Entered
+
+
 # ------------------------------------------------------------- references
 
 
