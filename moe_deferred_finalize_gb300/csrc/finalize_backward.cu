@@ -540,7 +540,7 @@ gamma_sum_kernel(const float *partial, uint16_t *dgamma, int rows, int H) {
     allow_next_kernel();
     float sum = 0.f;
     if (c < H) {
-#pragma unroll 8
+#pragma unroll 16
         for (int i = warp; i < rows; i += kSumWarps) sum += partial[static_cast<int64_t>(i) * H + c];
     }
     sums[warp][lane] = sum;
@@ -574,9 +574,10 @@ template <int VPT, int VEC, bool NORM, bool CLUSTER>
 cudaError_t start_backward(const FinalizeBackward &p, const Cut &cut, cudaStream_t stream) {
     auto *kernel = finalize_backward_kernel<VPT, VEC, NORM, CLUSTER>;
     const size_t smem = NORM && p.dgamma ? sizeof(float) * VPT * VEC * cut.threads : 0;
-    if (smem > 32 * 1024) {
+    constexpr int kMost = sizeof(float) * VPT * VEC * kMaxThreads;
+    if (NORM && kMost > 32 * 1024) {    // the same for every call: threads may race to set it
         const cudaError_t err = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (err != cudaSuccess) return err;
     }
     return start(kernel, cut.clusters * cut.splits, cut.threads, smem, cut.splits, stream, p, cut);
@@ -584,11 +585,15 @@ cudaError_t start_backward(const FinalizeBackward &p, const Cut &cut, cudaStream
 
 template <int VPT, int VEC>
 cudaError_t start_backward(const FinalizeBackward &p, const Cut &cut, cudaStream_t stream) {
-    if (p.dnorm)
+    // more than two vectors a thread: rows with RMSNorm over the largest cluster alone
+    if constexpr (VPT > 2)
+        return start_backward<VPT, VEC, true, true>(p, cut, stream);
+    else if (p.dnorm)
         return cut.splits > 1 ? start_backward<VPT, VEC, true, true>(p, cut, stream)
                               : start_backward<VPT, VEC, true, false>(p, cut, stream);
-    return cut.splits > 1 ? start_backward<VPT, VEC, false, true>(p, cut, stream)
-                          : start_backward<VPT, VEC, false, false>(p, cut, stream);
+    else
+        return cut.splits > 1 ? start_backward<VPT, VEC, false, true>(p, cut, stream)
+                              : start_backward<VPT, VEC, false, false>(p, cut, stream);
 }
 
 template <int VEC>

@@ -80,10 +80,8 @@ struct RowCopy {
     int K;
 };
 cudaError_t launch_expert_dz(const uint16_t *dout, const uint16_t *preact, int act, int gated,
-                             uint16_t *dz, int64_t pitch, const Groups &groups, int n,
-                             const RowCopy &copy, int num_sms, cudaStream_t stream);
-cudaError_t launch_expert_dbias(const uint16_t *dout, const uint16_t *preact, int act, int gated,
-                                uint16_t *dbias, const Groups &groups, int n,
-                                cudaStream_t stream);
+                             uint16_t *dz, int64_t pitch, uint16_t *dbias,
+                             const Groups &groups, int n, const RowCopy &copy, int num_sms,
+                             cudaStream_t stream);
 
 }  // namespace moef

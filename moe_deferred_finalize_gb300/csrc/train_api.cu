@@ -86,13 +86,9 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
     moef::RowCopy copy = {};
     if (copies_x)
         copy = {u16(x), row_token, u16(workspace) + P * dz_pitch(cols), T, dz_pitch(K), K};
-    if (dz || copies_x)
-        st = cuda_status(moef::launch_expert_dz(u16(dout), u16(preact), static_cast<int>(act),
-                                                gated, dz, dz_pitch(cols), groups, n, copy, sms,
-                                                stream));
-    if (st == MOEF_OK && dbias)
-        st = cuda_status(moef::launch_expert_dbias(u16(dout), u16(preact), static_cast<int>(act),
-                                                   gated, u16(dbias), groups, n, stream));
+    st = cuda_status(moef::launch_expert_dz(u16(dout), u16(preact), static_cast<int>(act), gated,
+                                            dz, dz_pitch(cols), u16(dbias), groups, n, copy, sms,
+                                            stream));
     Gemm g{};
     g.b = dz ? dz : u16(dout);
     g.b_pitch = dz ? dz_pitch(cols) : cols;
