@@ -159,9 +159,12 @@ moef_status moe_expert_linear_save(const void *x, int64_t T, const int32_t *row_
  *                  without rows
  *   dbias          bf16 [E, 2I] ([E, N]) or NULL          (at least one non-NULL)
  *   workspace      moe_expert_backward_workspace_bytes(P, cols, inputs) bytes,
- *                  16-byte aligned: cols the width of dz (2I, or N); inputs the
- *                  width of x (H, or K) when dweight is wanted and x cannot be
- *                  copied as it lies (with row_token, when the width is not a
+ *                  16-byte aligned (NULL when that is 0): cols the width of dz
+ *                  (2I, or N), 0 when dout is dz and lies so that it can be
+ *                  copied (linear without an activation, N a multiple of 8, dout
+ *                  16-byte aligned) or neither dx nor dweight is wanted; inputs
+ *                  the width of x (H, or K) when dweight is wanted and x cannot
+ *                  be copied as it lies (with row_token, when the width is not a
  *                  multiple of 8, or x not 16-byte aligned), else 0
  *
  * With T or P 0 dweight and dbias are zeros and nothing else is done.  Rows of

@@ -400,11 +400,21 @@ def topk_route_backward(dweights: torch.Tensor, weights: torch.Tensor, expert_id
 
 def expert_backward_workspace_bytes(P: int, cols: int, inputs: int = 0) -> int:
     """Bytes of workspace the expert products' backward calls need for P rows of
-    ``cols`` features before the activation (2I gated, N linear).  ``inputs``:
-    the width of x, when dweight is wanted and x has a row map, a width that is
-    not a multiple of 8, or is not 16-byte aligned."""
+    ``cols`` features before the activation (2I gated, N linear; 0 for a linear
+    product without one whose dout is 16-byte aligned, N a multiple of 8).
+    ``inputs``: the width of x, when dweight is wanted and x has a row map, a
+    width that is not a multiple of 8, or is not 16-byte aligned."""
     return int(_lib().moe_expert_backward_workspace_bytes(int(P), _int(int(cols)),
                                                           _int(int(inputs))))
+
+
+def _expert_workspace(res, dout, x, row_token, P, cols, K, act, gated):
+    """The arguments of expert_backward_workspace_bytes for a call with these
+    outputs."""
+    products = "dx" in res or "dweight" in res
+    makes_dz = products and (gated or act or cols % 8 or dout.data_ptr() % 16)
+    copies_x = "dweight" in res and (row_token is not None or K % 8 or x.data_ptr() % 16)
+    return P, cols if makes_dz else 0, K if copies_x else 0
 
 
 def _fast_expert_backward(where, gated, dout, x, row_token, offsets, counts, weight, preact,
@@ -433,10 +443,9 @@ def _fast_expert_backward(where, gated, dout, x, row_token, offsets, counts, wei
         if workspace is not None:
             nbytes = _workspace_bytes(workspace, device)
         else:
-            copies = "dweight" in res and (row_token is not None or K % 8 or
-                                           x.data_ptr() % 16)
-            nbytes = fast.call_size3(_address("moe_expert_backward_workspace_bytes"), P, cols,
-                                     K if copies else 0)
+            nbytes = fast.call_size3(
+                _address("moe_expert_backward_workspace_bytes"),
+                *_expert_workspace(res, dout, x, row_token, P, cols, K, act, gated))
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
         st = fast.checked_expert_backward(
             _address(where), gated, act, dev, _raw_stream(stream, dev), _ptr(workspace), nbytes,
@@ -490,8 +499,8 @@ def _expert_backward(where, gated, dout, x, row_token, offsets, counts, weight, 
     if not res:
         raise ValueError("no gradient is wanted")
     if workspace is None:
-        copies = "dweight" in res and (row_token is not None or K % 8 or x.data_ptr() % 16)
-        nbytes = expert_backward_workspace_bytes(P, cols, K if copies else 0) if P and cols else 0
+        nbytes = expert_backward_workspace_bytes(
+            *_expert_workspace(res, dout, x, row_token, P, cols, K, act, gated))
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     else:
         nbytes = _workspace_bytes(workspace, dev)

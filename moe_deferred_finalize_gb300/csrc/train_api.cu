@@ -54,13 +54,16 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
     if (!needs_preact && preact) return MOEF_ERR_ARG;
     const int cols = gated ? 2 * n : n;
     const bool copies_x = dweight && !lies_in_blocks(x, row_token, K);
+    // dout itself when it is dz and can be copied as it lies
+    const bool makes_dz = (dx || dweight) && (needs_preact || cols % 8 || !aligned(dout, 16));
     // without a token or a row there is nothing to read: zeros
     const bool empty = T == 0 || P == 0;
     if (!empty) {
         if (!dout || !offsets || !counts || (needs_preact && !preact) || (dx && !weight) ||
-            (dweight && !x) || !workspace)
+            (dweight && !x) || (!workspace && (makes_dz || copies_x)))
             return MOEF_ERR_NULL;
-        if (workspace_bytes < moe_expert_backward_workspace_bytes(P, cols, copies_x ? K : 0))
+        if (workspace_bytes <
+            moe_expert_backward_workspace_bytes(P, makes_dz ? cols : 0, copies_x ? K : 0))
             return MOEF_ERR_SHAPE;
         if (!aligned(workspace, 16)) return MOEF_ERR_ALIGN;
     }
@@ -80,12 +83,11 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
     st = sms_of_device(&sms);
     if (st != MOEF_OK) return st;
     const moef::Groups groups = {offsets, counts, E, P};
-    // dout itself when it is dz and can be copied as it lies
-    const bool has_dz = needs_preact || cols % 8 || !aligned(dout, 16);
-    uint16_t *dz = has_dz && (dx || dweight) ? u16(workspace) : nullptr;
+    uint16_t *dz = makes_dz ? u16(workspace) : nullptr;
     moef::RowCopy copy = {};
     if (copies_x)
-        copy = {u16(x), row_token, u16(workspace) + P * dz_pitch(cols), T, dz_pitch(K), K};
+        copy = {u16(x), row_token, u16(workspace) + (dz ? P * dz_pitch(cols) : 0), T, dz_pitch(K),
+                K};
     st = cuda_status(moef::launch_expert_dz(u16(dout), u16(preact), static_cast<int>(act), gated,
                                             dz, dz_pitch(cols), u16(dbias), groups, n, copy, sms,
                                             stream));
@@ -249,7 +251,7 @@ moef_status moe_topk_route_backward(const float *dweights, const float *weights,
 }
 
 size_t moe_expert_backward_workspace_bytes(int64_t P, int cols, int inputs) {
-    if (P < 0 || P > INT_MAX || cols < 1 || cols > 2 * MOEF_MAX_FEATURES || inputs < 0 ||
+    if (P < 0 || P > INT_MAX || cols < 0 || cols > 2 * MOEF_MAX_FEATURES || inputs < 0 ||
         inputs > MOEF_MAX_FEATURES)
         return 0;
     return dz_bytes(P, cols) + dz_bytes(P, inputs);

@@ -430,6 +430,24 @@ def test_expert_backward_linear_gathered(cuda_lib):
         T_.check(res[k], ref[k], k)
 
 
+def test_expert_backward_without_a_workspace(cuda_lib):
+    """dout as dz: none is needed; dbias alone needs none either."""
+    mf = cuda_lib
+    case = (40, 2, 4, 64, 48, 16, "none", True, False, 0)
+    m, x, w, dout, _ = expert_inputs(mf, case)
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    res = expert_call(mf, case, m, x, w, dout, None, workspace=none)
+    check_experts(case, m, x, w, dout, None, res)
+    case = (40, 2, 4, 64, 48, 16, "silu", True, True, 0)
+    m, x, w, dout, preact = expert_inputs(mf, case)
+    res = expert_call(mf, case, m, x, w, dout, preact, workspace=none, want_dx=False,
+                      want_dweight=False)
+    assert set(res) == {"dbias"}
+    check_experts(case, m, x, w, dout, preact, res)
+    with pytest.raises(mf.MoefError):
+        expert_call(mf, case, m, x, w, dout, preact, workspace=none)
+
+
 def test_expert_backward_odd_layouts(cuda_lib):
     """Experts out of order, with gaps, without rows, past the buffer, in front of it."""
     mf, g = cuda_lib, gen(6)

@@ -128,7 +128,7 @@ def test_expert_backward_argument_errors(lib, gated):
     size = lib.moe_expert_backward_workspace_bytes
     assert size(40, cols, 0) == 40 * cols * 2 and size(40, cols, 8) == 40 * (cols + 8) * 2
     assert size(40, 9, 17) == 40 * (16 + 24) * 2
-    assert size(-1, 8, 0) == size(40, 0, 0) == size(40, 8, -1) == 0
+    assert size(-1, 8, 0) == size(40, 0, 0) == size(40, 8, -1) == size(40, -1, 8) == 0
     # rows of x are laid out with a row map, an odd width, a misaligned x
     assert call(f, EXPERT, ws_bytes=size(40, cols, 8) - 1) == E_SHAPE
     in_layout = dict(row_token=NULL, T=40, ws_bytes=size(40, cols, 0) - 1)
