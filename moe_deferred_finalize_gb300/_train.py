@@ -651,23 +651,28 @@ def bind_adamw(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     grad_dtype = getattr(lists["grads"][0], "dtype", None)
     if grad_dtype not in _OUT_TYPE:
         raise ValueError("grads must be bfloat16 or float32")
-    table = (AdamWTensor * len(params))()
     kept = [params] + [ts for ts in lists.values() if ts is not None]
+    # the table's columns in its order: name, tensors, type, one value a block
+    columns = [("params", params, dtype, False), ("masters", lists["masters"], torch.float32, False),
+               ("grads", lists["grads"], grad_dtype, False),
+               ("exp_avg", lists["exp_avg"], state, False),
+               ("exp_avg_sq", lists["exp_avg_sq"], state, False),
+               ("exp_avg_scale", lists["exp_avg_scale"], torch.float32, True),
+               ("exp_avg_sq_scale", lists["exp_avg_sq_scale"], torch.float32, True)]
+    table, index = (AdamWTensor * len(params))(), dev.index
     for i, p in enumerate(params):
-        _check(p, f"params[{i}]", (dtype,), p.shape, dev)
-        blocks = (-(-p.numel() // BLOCK),)
-        row = table[i]
-        row.param, row.n = p.data_ptr(), p.numel()
-        for name, field, t_dtype, shape in (
-                ("grads", "grad", grad_dtype, p.shape), ("exp_avg", "exp_avg", state, p.shape),
-                ("exp_avg_sq", "exp_avg_sq", state, p.shape),
-                ("masters", "master", torch.float32, p.shape),
-                ("exp_avg_scale", "exp_avg_scale", torch.float32, blocks),
-                ("exp_avg_sq_scale", "exp_avg_sq_scale", torch.float32, blocks)):
-            if lists[name] is not None:
-                t = lists[name][i]
-                _check(t, f"{name}[{i}]", (t_dtype,), shape, dev)
-                setattr(row, field, t.data_ptr())
+        shape, n = p.shape, p.numel()
+        blocks, row = (-(-n // BLOCK),), []
+        for name, ts, t_dtype, per_block in columns:
+            if ts is None:
+                row.append(None)
+                continue
+            t, want = ts[i], blocks if per_block else shape
+            if not isinstance(t, torch.Tensor) or t.get_device() != index or \
+                    t.dtype is not t_dtype or t.shape != want or not t.is_contiguous():
+                _check(t, f"{name}[{i}]", (t_dtype,), want, dev)    # names the problem
+            row.append(t.data_ptr())
+        table[i] = tuple(row) + (n,)
     return BoundAdamW(table, kept, (8 if eight else 32, _OUT_TYPE[dtype], _OUT_TYPE[grad_dtype]),
                       dev)
 
