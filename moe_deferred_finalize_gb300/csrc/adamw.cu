@@ -1,12 +1,14 @@
 // AdamW over many tensors (moe_adamw_step).
 //
 // Bound by HBM: a value with fp32 states and master moves 28 bytes for some forty
-// operations.  A warp takes 256 values of a tensor, eight a lane, all its loads in
-// flight before the first use; the table of tensors comes with the launch's
+// operations.  A warp takes 256 values of a tensor, eight a lane (four and four, so
+// that each of its accesses is one piece of memory), all its loads in flight before
+// the first use; the table of tensors comes with the launch's
 // parameters, so that nothing is copied or kept between calls.  256 values are also
 // what an 8-bit state's scale is for, so a warp has a scale's values to itself and
 // finds the largest by shuffles.  396M values: 1.56 ms with fp32 states and master
-// weights (7.1 TB/s), 1.06 ms with 8-bit states (6.0 TB/s, the SMs' issue 65 % busy).
+// weights (7.1 TB/s), 1.02 ms with 8-bit states (6.3 TB/s; their 75 instructions a
+// value keep the SMs' issue two thirds busy).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -18,7 +20,8 @@ namespace moef {
 namespace {
 
 constexpr int kPiece = 256;             // values a warp takes at a time
-constexpr int kAdamThreads = 256;
+constexpr int kAdamThreads = 128;       // 256: 8-bit states 1.06 ms, 512: 1.20
+constexpr int kEightCtas = 12;          // of an SM, with 8-bit states: 10 1.05 ms, 14 1.07
 constexpr int kPerCta = kAdamThreads / 32;
 constexpr float kE4m3Max = 448.f, kE4m3Least = 0.001953125f;    // 2^-9
 constexpr int kFewTensors = 48, kManyTensors = 256;             // of a launch
@@ -43,56 +46,67 @@ __device__ __forceinline__ float fast_reciprocal(float x) {
     return y;
 }
 
-// Eight values of an array of `left` more (at least one), 16-byte accesses where
-// `whole`.
+// Where a lane's value i is, from its first.
+__device__ constexpr int place(int i) { return (i & 3) + kPiece / 2 * (i >> 2); }
+
+// A lane's eight values of an array of `left` more (at least one), four to an access
+// where `whole`.
 __device__ __forceinline__ void load8(const float *p, float (&f)[8], int64_t left, bool whole) {
     if (whole) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0];
-        const float4 b = reinterpret_cast<const float4 *>(p)[1];
+        const float4 a = *reinterpret_cast<const float4 *>(p);
+        const float4 b = *reinterpret_cast<const float4 *>(p + kPiece / 2);
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < left ? p[i] : 0.f;
+        for (int i = 0; i < 8; ++i) f[i] = place(i) < left ? p[place(i)] : 0.f;
     }
 }
 __device__ __forceinline__ void load8(const uint16_t *p, float (&f)[8], int64_t left, bool whole) {
     if (whole) {
-        VecOps<8>::to_f32(*reinterpret_cast<const uint4 *>(p), f);
+        const uint2 a = *reinterpret_cast<const uint2 *>(p);
+        const uint2 b = *reinterpret_cast<const uint2 *>(p + kPiece / 2);
+        VecOps<8>::to_f32(make_uint4(a.x, a.y, b.x, b.y), f);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            f[i] = i < left ? __uint_as_float(static_cast<uint32_t>(p[i]) << 16) : 0.f;
+            f[i] = place(i) < left
+                       ? __uint_as_float(static_cast<uint32_t>(p[place(i)]) << 16) : 0.f;
     }
 }
 __device__ __forceinline__ void store8(float *p, const float (&f)[8], int64_t left, bool whole) {
     if (whole) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4 *>(p + kPiece / 2) = make_float4(f[4], f[5], f[6], f[7]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = f[i];
+            if (place(i) < left) p[place(i)] = f[i];
     }
 }
 __device__ __forceinline__ void store8(uint16_t *p, const float (&f)[8], int64_t left,
                                        bool whole) {
     if (whole) {
-        *reinterpret_cast<uint4 *>(p) = VecOps<8>::from_f32(f);
+        const uint4 w = VecOps<8>::from_f32(f);
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w.x, w.y);
+        *reinterpret_cast<uint2 *>(p + kPiece / 2) = make_uint2(w.z, w.w);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+            if (place(i) < left) p[place(i)] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
     }
 }
 
 // Eight e4m3 codes as they lie in memory.
 __device__ __forceinline__ uint2 load_codes(const uint8_t *p, int64_t left, bool whole) {
     uint2 c = make_uint2(0, 0);
-    if (whole) return *reinterpret_cast<const uint2 *>(p);
+    if (whole)
+        return make_uint2(*reinterpret_cast<const uint32_t *>(p),
+                          *reinterpret_cast<const uint32_t *>(p + kPiece / 2));
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (i < left) (i < 4 ? c.x : c.y) |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+        if (place(i) < left)
+            (i < 4 ? c.x : c.y) |= static_cast<uint32_t>(p[place(i)]) << (8 * (i & 3));
     return c;
 }
 __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[8]) {
@@ -154,16 +168,17 @@ __device__ __forceinline__ void encode8(const float (&f)[8], uint8_t *p, float *
                         << (16 * (i & 1));
     }
     if (whole) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(word[0], word[1]);
+        *reinterpret_cast<uint32_t *>(p) = word[0];
+        *reinterpret_cast<uint32_t *>(p + kPiece / 2) = word[1];
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = static_cast<uint8_t>(word[i >> 2] >> (8 * (i & 3)));
+            if (place(i) < left) p[place(i)] = static_cast<uint8_t>(word[i >> 2] >> (8 * (i & 3)));
     }
 }
 
 template <typename P, typename G, bool MASTER, bool EIGHT, int N>
-__global__ void __launch_bounds__(kAdamThreads)
+__global__ void __launch_bounds__(kAdamThreads, EIGHT ? kEightCtas : 1)
 adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ AdamWFactors f) {
     __shared__ float s_bias[2];
     const int lane = threadIdx.x & 31;
@@ -194,13 +209,14 @@ adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ Ada
         }
         const moef_adamw_tensor &t = table.t[at];
         const int64_t block = piece - (at ? table.end[at - 1] : 0);
-        const int64_t i = block * kPiece + lane * 8, left = t.n - i;
+        const int64_t i = block * kPiece + lane * 4, left = t.n - i;
         const uintptr_t bits = reinterpret_cast<uintptr_t>(t.param) |
                                reinterpret_cast<uintptr_t>(t.master) |
                                reinterpret_cast<uintptr_t>(t.grad);
         const uintptr_t states = reinterpret_cast<uintptr_t>(t.exp_avg) |
                                  reinterpret_cast<uintptr_t>(t.exp_avg_sq);
-        const bool whole = left >= 8 && bits % 16 == 0 && states % (EIGHT ? 8 : 16) == 0;
+        const bool whole = left >= kPiece / 2 + 4 && bits % 16 == 0 &&
+                           states % (EIGHT ? 8 : 16) == 0;
         float g[8] = {}, p[8] = {}, m[8] = {}, v[8] = {};
         if (left > 0) {
             load8(static_cast<const G *>(t.grad) + i, g, left, whole);
@@ -260,10 +276,9 @@ cudaError_t start_adamw(const moef_adamw_tensor *tensors, int n, const AdamWFact
     }
     table.n = n;
     if (pieces == 0) return cudaSuccess;
-    // One piece a warp: 396M values with fp32 states and master take 1565 us (7.1
-    // TB/s), 1918 with four CTAs an SM that go round, 1625 with four pieces a warp,
-    // 1590 with streaming hints; 8-bit states 1076 us (5.9 TB/s), 1153 with four
-    // pieces: about 75 instructions a value keep the SMs' issue 70 % busy there.
+    // One piece a warp: 396M values with fp32 states and master take 1565 us, 1918
+    // with four CTAs an SM that go round, 1625 with four pieces a warp, 1590 with
+    // streaming hints.
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((pieces + kPerCta - 1) / kPerCta));
     cfg.blockDim = dim3(kAdamThreads);

@@ -1162,9 +1162,9 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
                         ok = wait(smem_addr(&h->empty[s]), phase, gave_up);
                         if (!ok) break;
                         const uint32_t full = smem_addr(&h->full[s]);
-                        copy_block<CG>(BlockRows(t, kb), h->spaced && g.a_zeros, stage0 + s * stage_bytes, 2,
-                                       &work.map[0][0], wide, t.m0 + half * m_cta_rows,
-                                       t.first + kb * kBlockK,
+                        copy_block<CG>(BlockRows(t, kb), h->spaced && g.a_zeros,
+                                       stage0 + s * stage_bytes, 2, &work.map[0][0], wide,
+                                       t.m0 + half * m_cta_rows, t.first + kb * kBlockK,
                                        CG == 2 ? map_rank(full, lead) : full);
                         if (++s == stages) { s = 0; phase ^= 1; }
                     }
