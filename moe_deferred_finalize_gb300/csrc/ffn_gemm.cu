@@ -156,23 +156,13 @@ struct Tile {
     int b0, first, rows;
 };
 
-template <int CG, bool GATED, bool DW>
+template <int CG, bool GATED>
 __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const Header *h, int t) {
     constexpr int kFeatures = (GATED ? 64 : 128) * CG;
     Tile r;
     r.e = 0;
     int m, n;
-    if constexpr (DW) {     // an expert's tiles share its rows of both operands
-        const int each = p.m_tiles * p.n_tiles, e = t / each, local = t - e * each;
-        n = local / p.m_tiles;
-        m = local - n * p.m_tiles;
-        r.bn = p.bn;
-        r.b0 = n * r.bn;
-        r.row0 = static_cast<int64_t>(e) * g.N + r.b0;
-        r.count = min(r.bn, g.N - r.b0);
-        r.first = h->first[e];
-        r.rows = h->count[e];
-    } else if (g.E) {
+    if (g.E) {
         int lo = 0, hi = g.E;           // prefix[lo] * m_tiles <= t < prefix[hi] * m_tiles
         const int column = t / p.m_tiles;
         while (hi - lo > 1) {
@@ -209,6 +199,55 @@ __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const He
     r.m0 = m * kFeatures;
     return r;
 }
+
+// The tiles of one role, in turn.  Grouped dweight has few k blocks a tile (512 rows:
+// eight, 4100 clocks), which the quotients of a tile's place would hold up: one thread
+// of dependent instructions, 800 clocks in which no product is issued (64 experts of
+// 4096 x 7168: 1250 us so).  All experts have the same tiles, an expert's one after
+// the other, so the place steps forward by sums.
+template <int CG, bool GATED, int N, bool DW>
+struct Walk {
+    const Work<N, DW> &work;
+    const Header *h;
+    int e, n, m, de, dn, dm;            // grouped dweight: the next tile, and a step
+
+    __device__ __forceinline__ Walk(const Work<N, DW> &w, const Header *header, int first, int step)
+        : work(w), h(header) {
+        if constexpr (DW) {
+            const int m_tiles = w.p[0].m_tiles, each = m_tiles * w.p[0].n_tiles;
+            e = first / each;
+            n = (first - e * each) / m_tiles;
+            m = first - e * each - n * m_tiles;
+            de = step / each;
+            dn = (step - de * each) / m_tiles;
+            dm = step - de * each - dn * m_tiles;
+        }
+    }
+    // tile ti, a tile of product q
+    __device__ __forceinline__ Tile next(int ti, int q) {
+        if constexpr (!DW) {
+            return tile_at<CG, GATED>(work.g[q], work.p[q], h, q ? ti - work.tiles0 : ti);
+        } else {
+            const TcPlan &p = work.p[0];
+            const int features = work.g[0].N;
+            Tile r;
+            r.e = 0;
+            r.bn = p.bn;
+            r.b0 = n * p.bn;
+            r.row0 = static_cast<int64_t>(e) * features + r.b0;
+            r.count = min(p.bn, features - r.b0);
+            r.m0 = m * 128 * CG;
+            r.first = h->first[e];
+            r.rows = h->count[e];
+            m += dm;
+            if (m >= p.m_tiles) { m -= p.m_tiles; ++n; }
+            n += dn;
+            if (n >= p.n_tiles) { n -= p.n_tiles; ++e; }
+            e += de;
+            return r;
+        }
+    }
+};
 
 // ------------------------------------------------------------- epilogue
 
@@ -999,7 +1038,7 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
     // the product that a tile belongs to, and this part's k blocks of it
     auto product_of = [&](int ti) { return N == 2 && ti >= work.tiles0 ? 1 : 0; };
     auto tile_of = [&](int ti, int q) {
-        return tile_at<CG, GATED, DW>(work.g[q], work.p[q], h, q ? ti - work.tiles0 : ti);
+        return tile_at<CG, GATED>(work.g[q], work.p[q], h, q ? ti - work.tiles0 : ti);
     };
     auto k_range = [&](int q, const Tile &t, int *kb0, int *kb1) {
         if constexpr (DW) {
@@ -1030,12 +1069,13 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
             int s = 0;
             uint32_t phase = 1;
             bool ok = true;
+            Walk<CG, GATED, N, DW> walk(work, h, first_tile, step);
             for (int ti = first_tile; ti < tiles && ok; ti += step) {
                 const int q = product_of(ti);
                 const Gemm &g = work.g[q];
                 const TcPlan &p = work.p[q];
                 const CUtensorMap *map = &work.map[q][0];
-                const Tile t = tile_of(ti, q);
+                const Tile t = walk.next(ti, q);
                 int kb0, kb1;
                 k_range(q, t, &kb0, &kb1);
                 const int bnc = t.bn / CG, m0 = t.m0 + half * m_cta_rows;
@@ -1149,12 +1189,13 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
             }
         } else if (elect_one()) {
             bool ok = true;
+            Walk<CG, GATED, N, DW> walk(work, h, first_tile, step);
             for (int ti = first_tile; ti < tiles && ok; ti += step) {
                 const int q = product_of(ti);
                 const Gemm &g = work.g[q];
                 const TcPlan &p = work.p[q];
                 const CUtensorMap *map = &work.map[q][1], *wide = &work.map[q][2];
-                const Tile t = tile_of(ti, q);
+                const Tile t = walk.next(ti, q);
                 int kb0, kb1;
                 k_range(q, t, &kb0, &kb1);
                 if constexpr (DW) {     // of A here
@@ -1212,10 +1253,11 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
             int s = 0, n = 0;
             uint32_t phase = 0;
             bool ok = true;
+            Walk<CG, GATED, N, DW> walk(work, h, first_tile, step);
             for (int ti = first_tile; ti < tiles && ok; ti += step, ++n) {
                 const int q = product_of(ti);
                 const Gemm &g = work.g[q];
-                const Tile t = tile_of(ti, q);
+                const Tile t = walk.next(ti, q);
                 int kb0, kb1;
                 k_range(q, t, &kb0, &kb1);
                 // D fp32, A and B bf16, transposes, N, M
@@ -1251,9 +1293,10 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
     } else {
         // ---- epilogue
         int n = 0;
+        Walk<CG, GATED, N, DW> walk(work, h, first_tile, step);
         for (int ti = first_tile; ti < tiles; ti += step, ++n) {
             const int q = product_of(ti);
-            const Tile t = tile_of(ti, q);
+            const Tile t = walk.next(ti, q);
             const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                  (n & 1) * kMaxBn;
             begin(ti);
