@@ -30,8 +30,12 @@
 //
 // Grouped dweight sums over each expert's own rows: every expert has the same tiles,
 // with as many k blocks as it has rows (none: zeros are written), both operands m- and
-// n-contiguous.  64 experts of 4096 x 7168: 1250 us at 512 rows each (1540 TFLOP/s),
-// 704 at 128 (bound by writing 3.8 GB, 5.3 TB/s), 1025 for 8 experts of 4096 rows (1875).
+// n-contiguous.  64 experts of 4096 x 7168: 1190-1240 us by box at 512 rows each (1590
+// TFLOP/s), 684 at 128 (writing 3.8 GB at 5.5 TB/s); 8 experts of 4096 rows 1000-1035
+// (1900).  Without its stores the first takes 1077 us: writing is what few k blocks a
+// tile are held by, whatever the stores are (lanes' 32-byte pieces 1347, boxes of
+// shared memory by TMA 1239), as long as the tiles in flight make up whole rows of the
+// output (by TMA, columns last: 1405).
 //
 // Two launch forms:
 //   CG = 2  pairs of CTAs share tiles of 256 (m) x up to 256 (n): each CTA
@@ -203,7 +207,7 @@ __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const He
 // The tiles of one role, in turn.  Grouped dweight has few k blocks a tile (512 rows:
 // eight, 4100 clocks), which the quotients of a tile's place would hold up: one thread
 // of dependent instructions, 800 clocks in which no product is issued (64 experts of
-// 4096 x 7168: 1250 us so).  All experts have the same tiles, an expert's one after
+// 4096 x 7168 with 61 to 2188 rows: 1504 us so, 1462 without).  All experts have the same tiles, an expert's one after
 // the other, so the place steps forward by sums.
 template <int CG, bool GATED, int N, bool DW>
 struct Walk {
@@ -763,7 +767,8 @@ __device__ __forceinline__ void finish_wide(WidePart<GATED, RESIDUAL> &part, uin
 }
 
 // The same for grouped dweight, which is mostly written: the sums alone, the next
-// chunk's on their way out of TMEM while one is stored.
+// chunk's on their way out of TMEM while one is stored (64 experts of 128 rows, 4096 x
+// 7168: 851 us with finish_wide, 704 so).
 __device__ __forceinline__ void finish_dweight(WidePart<false, false> &part, uint32_t stash,
                                                uint32_t tmem, uint32_t done) {
     const int lane = part.lane, end = part.end, stride = part.stride;
