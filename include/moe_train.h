@@ -68,8 +68,8 @@ extern "C" {
  * A slot whose idx_map is outside [0, P) has no row: its dweights is 0.  No two
  * slots may name the same row.  dm stays in fp32 up to each output's rounding.
  * In place: dshared or dresidual may equal dout or dresidual_out.
- * T = 0 writes zeros to dgamma.  MOEF_ERR_SHAPE when a row is too long for one
- * cluster: with dnorm_out, more than 32768 pieces of 8 values (of single
+ * T = 0 writes zeros to dgamma.  1 <= H <= 2^30.  MOEF_ERR_SHAPE when a row is
+ * too long for one cluster: with dnorm_out, more than 32768 pieces of 8 values (of single
  * values, where H % 8 != 0 or a pointer is not 16-byte aligned).
  */
 size_t moe_finalize_backward_workspace_bytes(int T, int H);
@@ -96,7 +96,7 @@ moef_status moe_finalize_backward(const void *permuted_out, int64_t P, const int
  *   add0, add1   bf16 [T, H], each or NULL;  out bf16 [T, H], may equal either
  *            (MOEF_ERR_SHAPE when T ceil(H / 128) passes INT_MAX)
  *   P >= 0 (rows may be NULL with P = 0), T >= 0 (0 enqueues nothing),
- *   1 <= K <= MOEF_MAX_K, H >= 1
+ *   1 <= K <= MOEF_MAX_K, 1 <= H <= 2^30
  */
 moef_status moe_unpermute(const void *rows, int64_t P, const int32_t *idx_map, const void *add0,
                           const void *add1, void *out, int T, int K, int H,

@@ -94,33 +94,42 @@ __device__ __forceinline__ void copy_row(const RowCopy &c, int64_t row, bool hav
     }
 }
 
-// dbias of one expert and 32 vectors of columns: a warp takes every eighth row, the
-// warps' sums are added in order.
+// dbias of one expert and a block of columns: some of a warp's lanes along the columns,
+// the others along the rows (8 and 4 with 16-byte vectors: a CTA takes 64 rows at a
+// time, for an expert's rows are all one CTA's); a warp's sums are joined by shuffles,
+// the warps' in order.
+template <int VEC>
+constexpr int kColumnLanes = VEC == 8 ? 8 : 32;
+template <int VEC>
+constexpr int kBiasColumns = kColumnLanes<VEC> * VEC;
+
 template <int VEC, bool GATED>
 __device__ __forceinline__ void sum_bias(const uint16_t *dout, const uint16_t *preact, int act,
                                          uint16_t *dbias, const Groups &g, int n, int e, int block,
-                                         float (&sums)[kWarps][GATED ? 2 : 1][32 * VEC]) {
+                                         float (&sums)[kWarps][GATED ? 2 : 1][kBiasColumns<VEC>]) {
     using Ops = VecOps<VEC>;
     using V = typename Ops::V;
-    constexpr int kHalves = GATED ? 2 : 1, kRows = kLoads;
+    constexpr int kHalves = GATED ? 2 : 1, kRows = kLoads, kAcross = kColumnLanes<VEC>;
+    constexpr int kStep = kWarps * (32 / kAcross);          // rows of one load of all warps
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int cols = kHalves * n, i = (block * 32 + lane) * VEC;
+    const int cols = kHalves * n, at = (lane % kAcross) * VEC, i = block * kBiasColumns<VEC> + at;
     int first;
     const int rows = rows_of(g, e, &first);
     float sum[kHalves][VEC] = {};
-    for (int r0 = warp; i < n && r0 < rows; r0 += kWarps * kRows) {
+    for (int64_t r0 = warp * (32 / kAcross) + lane / kAcross; i < n && r0 < rows;
+         r0 += kStep * kRows) {
         V d[kRows], z[kRows], u[kRows];
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-            if (r0 + k * kWarps >= rows) break;
-            const int64_t row = static_cast<int64_t>(first) + r0 + k * kWarps;
+            if (r0 + k * kStep >= rows) break;
+            const int64_t row = first + r0 + k * kStep;
             d[k] = Ops::load(dout + row * n + i);
             if (preact) z[k] = Ops::load(preact + row * cols + i);
             if constexpr (GATED) u[k] = Ops::load(preact + row * cols + n + i);
         }
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-            if (r0 + k * kWarps >= rows) break;
+            if (r0 + k * kStep >= rows) break;
             float df[VEC], zf[VEC] = {}, uf[VEC] = {}, out[kHalves][VEC];
             Ops::to_f32(d[k], df);
             if (preact) Ops::to_f32(z[k], zf);
@@ -132,26 +141,32 @@ __device__ __forceinline__ void sum_bias(const uint16_t *dout, const uint16_t *p
                 for (int j = 0; j < VEC; ++j) sum[h][j] += out[h][j];
         }
     }
+    __syncwarp();
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sums[warp][h][j * 32 + lane] = sum[h][j];
+        for (int j = 0; j < VEC; ++j) {
+#pragma unroll
+            for (int o = kAcross; o < 32; o <<= 1)
+                sum[h][j] += __shfl_xor_sync(0xFFFFFFFFu, sum[h][j], o);
+            if (lane < kAcross) sums[warp][h][at + j] = sum[h][j];
+        }
     __syncthreads();
-    for (int c = threadIdx.x; c < kHalves * 32 * VEC; c += kThreads) {
-        const int h = c / (32 * VEC), k = c % (32 * VEC);
-        const int column = (block * 32 + k / VEC) * VEC + k % VEC;
+    for (int c = threadIdx.x; c < kHalves * kBiasColumns<VEC>; c += kThreads) {
+        const int h = c / kBiasColumns<VEC>, k = c % kBiasColumns<VEC>;
+        const int column = block * kBiasColumns<VEC> + k;
         if (column >= n) continue;
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += sums[w][h][k % VEC * 32 + k / VEC];
+        for (int w = 0; w < kWarps; ++w) v += sums[w][h][k];
         dbias[static_cast<int64_t>(e) * cols + h * n + column] =
             __bfloat16_as_ushort(__float2bfloat16_rn(v));
     }
 }
 
 // One launch: the first dz_ctas CTAs make dz and lay out x, the others dbias, which
-// reads the same rows at the same time (100 tokens, two of 8 experts of 1040 x 1536:
-// 7 us and 6 in two launches).  ACT: the activation, or -1 to take it from `act`.
+// reads the same rows at the same time (100 tokens, two of 8 experts of 1040 x 1536,
+// the whole backward pass: 35 us with two launches, 30.5 so).  ACT: the activation, or -1 to take it from `act`.
 template <int VEC, bool GATED, int ACT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t *dz,
@@ -166,7 +181,7 @@ expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t
     };
     __shared__ union {
         Pieces pieces;
-        float sums[kWarps][GATED ? 2 : 1][32 * VEC];
+        float sums[kWarps][GATED ? 2 : 1][kBiasColumns<VEC>];
     } shared;
     int *const s_pieces = shared.pieces.before, *const s_first = shared.pieces.first;
     int *const s_rows = shared.pieces.rows, *const s_warp = shared.pieces.warp;
@@ -175,7 +190,7 @@ expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t
     wait_previous_kernel();
     allow_next_kernel();
     if (static_cast<int>(blockIdx.x) >= dz_ctas) {
-        const unsigned across = (n - 1) / (32 * VEC) + 1, at = blockIdx.x - dz_ctas;
+        const unsigned across = (n - 1) / kBiasColumns<VEC> + 1, at = blockIdx.x - dz_ctas;
         sum_bias<VEC, GATED>(dout, preact, ACT < 0 ? act : ACT, dbias, g, n, at / across,
                              at % across, shared.sums);
         return;
@@ -196,7 +211,7 @@ expert_dz_kernel(const uint16_t *dout, const uint16_t *preact, int act, uint16_t
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         if (spaced) own[i] = rounded_rows(own[i]);
-        own[i] = (own[i] + kWarps - 1) / kWarps;
+        own[i] = own[i] > 0 ? steps_of(own[i], kWarps) : 0;
         sum += own[i];
     }
     int before = sum;
@@ -301,7 +316,8 @@ cudaError_t launch_expert_dz(const uint16_t *dout, const uint16_t *preact, int a
                              const RowCopy &copy, int num_sms, cudaStream_t stream) {
     const bool vec = vectors(dout, preact, dz, n);
     const int dz_ctas = dz || copy.to ? num_sms * kCtasPerSm : 0;
-    const int64_t sums = dbias ? static_cast<int64_t>(g.E) * ((n - 1) / (vec ? 256 : 32) + 1) : 0;
+    const int across = vec ? kBiasColumns<8> : kBiasColumns<1>;
+    const int64_t sums = dbias ? static_cast<int64_t>(g.E) * ((n - 1) / across + 1) : 0;
     const dim3 grid(static_cast<unsigned>(dz_ctas + sums));
     if (grid.x == 0) return cudaSuccess;
     auto go = [&](auto *kernel) {

@@ -207,8 +207,8 @@ __device__ __forceinline__ Tile tile_at(const Gemm &g, const TcPlan &p, const He
 // The tiles of one role, in turn.  Grouped dweight has few k blocks a tile (512 rows:
 // eight, 4100 clocks), which the quotients of a tile's place would hold up: one thread
 // of dependent instructions, 800 clocks in which no product is issued (64 experts of
-// 4096 x 7168 with 61 to 2188 rows: 1504 us so, 1462 without).  All experts have the same tiles, an expert's one after
-// the other, so the place steps forward by sums.
+// 4096 x 7168 with 61 to 2188 rows: 1504 us so, 1462 without).  All experts have the
+// same tiles, an expert's one after the other, so the place steps forward by sums.
 template <int CG, bool GATED, int N, bool DW>
 struct Walk {
     const Work<N, DW> &work;

@@ -19,6 +19,10 @@ uint16_t *u16(void *p) { return static_cast<uint16_t *>(p); }
 
 bool valid_features(int n) { return n >= 1 && n <= MOEF_MAX_FEATURES; }
 
+// Hidden sizes whose columns the kernels can count past without leaving an int.
+constexpr int kMaxHidden = 1 << 30;
+bool valid_hidden(int H) { return H >= 1 && H <= kMaxHidden; }
+
 moef_status sms_of_device(int *sms) { return cuda_status(moef::current_sms(sms)); }
 
 // dz and laid out rows of x have a multiple of 8 values, as the dense dz.
@@ -130,7 +134,7 @@ bool not_negative(double v) { return isfinite(v) && v >= 0.0; }
 extern "C" {
 
 size_t moe_finalize_backward_workspace_bytes(int T, int H) {
-    if (T <= 0 || H <= 0) return 0;
+    if (T <= 0 || !valid_hidden(H)) return 0;
     return static_cast<size_t>(moef::finalize_backward_partials(T)) * H * sizeof(float);
 }
 
@@ -142,7 +146,7 @@ moef_status moe_finalize_backward(const void *permuted_out, int64_t P, const int
                                   void *drows, float *dweights, void *dshared, void *dresidual,
                                   void *dgamma, int T, int K, int H, void *workspace,
                                   size_t workspace_bytes, cudaStream_t stream) {
-    if (T < 0 || K < 1 || K > MOEF_MAX_K || H < 1) return MOEF_ERR_SHAPE;
+    if (T < 0 || K < 1 || K > MOEF_MAX_K || !valid_hidden(H)) return MOEF_ERR_SHAPE;
     if (wkind != MOEF_W_FP32 && wkind != MOEF_W_BF16 && wkind != MOEF_W_PACKED_TOPK)
         return MOEF_ERR_ARG;
     if (!drows && !dweights && !dshared && !dresidual && !dgamma) return MOEF_ERR_NULL;
@@ -206,7 +210,7 @@ moef_status moe_finalize_backward(const void *permuted_out, int64_t P, const int
 moef_status moe_unpermute(const void *rows, int64_t P, const int32_t *idx_map, const void *add0,
                           const void *add1, void *out, int T, int K, int H,
                           cudaStream_t stream) {
-    if (T < 0 || P < 0 || K < 1 || K > MOEF_MAX_K || H < 1) return MOEF_ERR_SHAPE;
+    if (T < 0 || P < 0 || K < 1 || K > MOEF_MAX_K || !valid_hidden(H)) return MOEF_ERR_SHAPE;
     if (moef::unpermute_ctas(T, H) > INT_MAX) return MOEF_ERR_SHAPE;
     if (T == 0) return MOEF_OK;
     if ((P > 0 && !rows) || !idx_map || !out) return MOEF_ERR_NULL;

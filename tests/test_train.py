@@ -870,8 +870,13 @@ def test_finalize_backward_many_tokens(cuda_lib, case):
                                    want_drows=False, **kw)
     two = mf.moe_finalize_backward(rows, m["idx_map"], w, case[5], dout, routed_scale=0.5,
                                    want_dweights=False, drows=drows0.clone(), **kw)
+    others = [one, two]
+    if case[6] or case[8]:
+        others.append(mf.moe_finalize_backward(rows, m["idx_map"], w, case[5], dout,
+                                               routed_scale=0.5, want_drows=False,
+                                               want_dweights=False, **kw))
     for k in res:
-        for other in (one, two):
+        for other in others:
             if k in other:
                 assert torch.equal(other[k], res[k]), k
 
@@ -1020,6 +1025,27 @@ def test_expert_rows_past_31_bits(cuda_lib):
     T_.check(res["dx"][-70:], ref["dx"], "dx")
     T_.check(res["dweight"][1:], ref["dweight"], "dweight")
     T_.check(res["dbias"][1:], ref["dbias"], "dbias")
+
+
+@pytest.mark.slow
+def test_expert_rows_up_to_the_last(cuda_lib):
+    """2^31 - 1 rows of one feature: their dz and dx, the last one's too."""
+    mf, P, K = cuda_lib, 2 ** 31 - 1, 8
+    offsets = torch.tensor([0, P], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([P], dtype=torch.int32, device="cuda")
+    w = torch.arange(1, K + 1, device="cuda").to(BF16).view(1, 1, K)
+    dout = torch.full((P, 1), 2.0, dtype=BF16, device="cuda")
+    dout[-1] = 3.0
+    x = torch.empty((1, K), dtype=BF16, device="cuda").expand(P, K)
+    with pytest.raises(ValueError, match="contiguous"):
+        mf.expert_linear_backward(dout, x, offsets, counts, w)
+    token = torch.zeros(P, dtype=torch.int32, device="cuda")
+    res = mf.expert_linear_backward(dout, x[:1].contiguous(), offsets, counts, w,
+                                    row_token=token, want_dweight=False)
+    row = w.view(K).float()
+    for r, scale in ((0, 2), (2 ** 30 + 5, 2), (P - 2, 2), (P - 1, 3)):
+        assert torch.equal(res["dx"][r].float(), scale * row), r
+    assert mf.lost_waits() == 0
 
 
 @pytest.mark.slow

@@ -52,7 +52,7 @@ def test_finalize_backward_argument_errors(lib):
     assert call(f, FINALIZE, ws=A + 8) == E_ALIGN
     need = lib.moe_finalize_backward_workspace_bytes(4, 8)
     assert call(f, FINALIZE, ws_bytes=need - 1) == E_SHAPE
-    for k, vs in (("T", (-1,)), ("K", (0, 33)), ("H", (0, -1)), ("P", (0, -1))):
+    for k, vs in (("T", (-1,)), ("K", (0, 33)), ("H", (0, -1, (1 << 30) + 1)), ("P", (0, -1))):
         for v in vs:
             assert call(f, FINALIZE, **{k: v}) == E_SHAPE, (k, v)
     for v in (-1, 3):
@@ -83,7 +83,7 @@ def test_unpermute_argument_errors(lib):
     for k in ("rows", "add0", "add1", "out"):
         assert call(f, UNPERMUTE, **{k: ODD}) == E_ALIGN
     assert call(f, UNPERMUTE, idx=HALF) == E_ALIGN
-    for k, vs in (("T", (-1,)), ("P", (-1,)), ("K", (0, 33)), ("H", (0,))):
+    for k, vs in (("T", (-1,)), ("P", (-1,)), ("K", (0, 33)), ("H", (0, (1 << 30) + 1))):
         for v in vs:
             assert call(f, UNPERMUTE, **{k: v}) == E_SHAPE
     assert call(f, UNPERMUTE, T=INT_MAX, H=129) == E_SHAPE
