@@ -123,7 +123,8 @@ def moe_finalize_backward(permuted_out: torch.Tensor, idx_map: torch.Tensor,
     if stream is not None and \
             (want_drows and drows is None or want_dweights and dweights is None or
              residual and dresidual is None or separate and dshared is None or
-             norm and want_dgamma and (dgamma is None or workspace is None)) and \
+             norm and (want_dgamma or dgamma is not None) and
+             (dgamma is None or workspace is None)) and \
             _elsewhere(stream, _device(permuted_out)):
         args = dict(locals())
         for name in ("norm", "residual", "separate"):

@@ -424,10 +424,13 @@ def test_expert_backward_linear_gathered(cuda_lib):
     token[int(m["offsets"][1])] = T
     token[int(m["offsets"][2])] = -5
     x, w, dout = normal(g, T, H), normal(g, E, N, H), normal(g, P, N)
-    res = mf.expert_linear_backward(dout, x, m["offsets"], m["counts"], w, row_token=token)
-    ref = T_.expert_backward(dout, x, token, m["offsets"], m["counts"], w, None, "none", False)
-    for k in res:
-        T_.check(res[k], ref[k], k)
+    preact = normal(g, P, N)
+    for act, pre in (("none", None), ("gelu", preact)):
+        res = mf.expert_linear_backward(dout, x, m["offsets"], m["counts"], w, row_token=token,
+                                        activation=act, preact=pre, want_dbias=True)
+        ref = T_.expert_backward(dout, x, token, m["offsets"], m["counts"], w, pre, act, False)
+        for k in res:
+            T_.check(res[k], ref[k], k)
 
 
 def test_expert_backward_without_a_workspace(cuda_lib):
@@ -793,6 +796,56 @@ def test_layer_training_step_in_a_graph(cuda_lib, bits):
     for k, ts in runs[0][1].items():
         for a, b in zip(ts, runs[1][1][k]):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), k
+
+
+def test_threads_with_streams_of_their_own(cuda_lib):
+    """Four threads at once, each with other sizes, on its own stream."""
+    import threading
+    mf = cuda_lib
+    jobs, wants, errors = [], [], []
+    for i, (H, T) in enumerate(((256, 40), (4104, 20), (20008, 8), (7168, 350))):
+        fcase = (T, 4, 8, H, 8, "fp32", True, True, True, 0.1)
+        rows, m, w, dout, kw = finalize_inputs(mf, fcase, seed=i)
+        ecase = (40 + 30 * i, 2, 4, 128, 40 + 8 * i, 8, "silu", True, True, 1)
+        jobs.append(((rows, m, w, dout, kw), ecase, expert_inputs(mf, ecase, seed=i),
+                     adamw_inputs(mf, (300 + i, 1000), 8, True, BF16, BF16, False, seed=i)))
+
+    def work(job, adam):
+        (rows, m, w, dout, kw), ecase, e, _ = job
+        f = mf.moe_finalize_backward(rows, m["idx_map"], w, "fp32", dout, **kw)
+        r = expert_call(mf, ecase, *e)
+        u = mf.unpermute_tokens(f["drows"], m["idx_map"], add=f["dshared"])
+        mf.adamw_step(adam[0], adam[1], step=1, **adam[2])
+        return [f["dweights"], f["dgamma"], f["dresidual"], u, r["dweight"], r["dbias"]] + adam[0]
+
+    for job in jobs:
+        adam = job[3]
+        copy = ([t.clone() for t in adam[0]], adam[1],
+                {k: [t.clone() for t in ts] for k, ts in adam[2].items()})
+        wants.append(work(job, copy))
+    torch.cuda.synchronize()
+
+    def thread(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    adam = jobs[i][3]
+                    copy = ([t.clone() for t in adam[0]], adam[1],
+                            {k: [t.clone() for t in ts] for k, ts in adam[2].items()})
+                    got = work(jobs[i], copy)
+                    torch.cuda.current_stream().synchronize()
+                    for a, b in zip(got, wants[i]):
+                        assert torch.equal(a, b)
+        except BaseException as e:      # noqa: B902
+            errors.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[0]
+    assert mf.lost_waits() == 0
 
 
 def test_two_streams_at_once(cuda_lib):

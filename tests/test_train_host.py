@@ -280,6 +280,9 @@ ALLOCATING = [
     ("moe_finalize_backward", FINALIZE_ARGS,
      dict(drows=(8, 8), dweights=(4, 2), dshared=(4, 8), dresidual=(4, 8), dgamma=(8,),
           workspace=(4096,)), NORM),
+    ("moe_finalize_backward", FINALIZE_ARGS,
+     dict(drows=(8, 8), dweights=(4, 2), dshared=(4, 8), dresidual=(4, 8), workspace=(4096,)),
+     lambda: dict(NORM(), dgamma=fake(8), want_dgamma=False)),
     ("unpermute_tokens", lambda: (fake(8, 8), i32(4, 2)), dict(out=(4, 8)), dict),
     ("topk_route_backward", lambda: (f32(4, 2), f32(4, 2), i32(4, 2), 8, "softmax"),
      dict(dlogits=(4, 8)), dict),
