@@ -12,10 +12,10 @@
 // products are summed by shuffles, eight at a time, and then over the warps in order.
 // A token is one CTA's, or, when there are few tokens, one cluster's, whose CTAs
 // share its columns and join their two sums and their dot products through
-// distributed shared memory (T = 16: 128 CTAs, 10.2 us with the sum of dgamma; 9 us of
-// it are two launches' latencies).  CTAs go round the tokens and add up dgamma in
-// shared memory, each thread its own columns, so that at most 1024 rows of sums are
-// left for a kernel that adds them in order (8 us at 304 rows of 7168).  With many
+// distributed shared memory (T = 16: 128 CTAs, and 8 for dgamma, 8.2 us).  CTAs go round
+// the tokens and add up dgamma in shared memory, each thread its own columns, so that at
+// most 1024 rows of sums are left for a kernel that adds them in order (8 us at 304 rows
+// of 7168); up to 32 tokens one more cluster takes dgamma instead.  With many
 // tokens the rows come through a ring (see below): 225 us at T = 4096, 0.85 of the
 // copy rate.
 #include <cooperative_groups.h>
@@ -35,6 +35,10 @@ constexpr int kWarps = kMaxThreads / 32;
 constexpr int kMaxSplits = 8;
 constexpr int kMaxVpt = 8;
 constexpr int kMaxPartials = 1024;      // rows of dgamma's sums
+// whose dgamma needs none: one launch against two, in us, at H = 7168: 7.1 : 8.7 for 8
+// tokens, 9.4 : 10.8 for 32, 13.3 : 11.9 for 48; at H = 32768 19.0 : 20.6 for 32 and
+// 34.4 : 32.5 for 48; at H = 262144 206 : 213 for 32
+constexpr int kDirectTokens = 32;
 constexpr int kSlots = 8;               // of a token, in flight at a time
 
 // How one launch is cut: `splits` CTAs (a cluster) take a token's slices of
@@ -63,6 +67,58 @@ __device__ __forceinline__ float warp_sum8(float (&acc)[8], int lane) {
     return v;
 }
 
+// dgamma of a few tokens by one cluster (or CTA) beside those that take the tokens: its
+// CTAs share the tokens for their inverse RMS, which all of them get, and then the
+// columns.  dnorm and r are read once more, out of L2; the launch of a kernel that sums
+// rows, and the rows' workspace, are spared (T = 16, top-8, 7168: 10.2 us in two kernels).
+template <int VEC, bool CLUSTER>
+__device__ __forceinline__ void direct_gamma(const FinalizeBackward &p, const Cut &cut, int split) {
+    using Ops = VecOps<VEC>;
+    __shared__ float s_inv[kDirectTokens], s_warp[kWarps];
+    const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int t = split; t < p.T; t += cut.splits) {
+        float sum = 0.f;
+#pragma unroll 4
+        for (int v = tid; v < cut.nvec; v += nt) {
+            float x[VEC];
+            Ops::to_f32(Ops::load_reused(p.r + static_cast<int64_t>(t) * p.H +
+                                         static_cast<int64_t>(v) * VEC), x);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) sum = fmaf(x[q], x[q], sum);
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) s_warp[warp] = sum;
+        __syncthreads();
+        sum = 0.f;
+        for (int w = 0; w < nt >> 5; ++w) sum += s_warp[w];
+        const float inv = rsqrtf(sum / static_cast<float>(p.H) + p.eps);
+        if constexpr (CLUSTER) {
+            if (tid < cut.splits) *cg::this_cluster().map_shared_rank(&s_inv[t], tid) = inv;
+        } else {
+            if (tid == 0) s_inv[t] = inv;
+        }
+        __syncthreads();
+    }
+    if constexpr (CLUSTER) cg::this_cluster().sync();
+    const int v_end = min((split + 1) * cut.slice, cut.nvec);
+    for (int v = split * cut.slice + tid; v < v_end; v += nt) {
+        const int64_t e = static_cast<int64_t>(v) * VEC;
+        float acc[VEC] = {};
+#pragma unroll 4
+        for (int t = 0; t < p.T; ++t) {
+            const int64_t at = static_cast<int64_t>(t) * p.H + e;
+            float d[VEC], x[VEC];
+            Ops::to_f32(Ops::load_reused(p.dnorm + at), d);
+            Ops::to_f32(Ops::load_reused(p.r + at), x);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) acc[q] = fmaf(d[q] * x[q], s_inv[t], acc[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < VEC; ++q)
+            p.dgamma[e + q] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[q]));
+    }
+}
+
 template <int VPT, int VEC, bool NORM, bool CLUSTER>
 __global__ void __launch_bounds__(kMaxThreads, VPT <= 2 ? 2 : 1)
 finalize_backward_kernel(const __grid_constant__ FinalizeBackward p,
@@ -82,7 +138,7 @@ finalize_backward_kernel(const __grid_constant__ FinalizeBackward p,
     const int split = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int64_t cluster = CLUSTER ? blockIdx.x / cut.splits : blockIdx.x;
     const int v_begin = split * cut.slice, v_end = min(v_begin + cut.slice, cut.nvec);
-    const bool sums_gamma = NORM && p.dgamma;
+    const bool sums_gamma = NORM && p.dgamma && p.T > kDirectTokens;
     if (CLUSTER) cluster_arrive();
     if (sums_gamma)
         for (int i = tid; i < VPT * VEC * nt; i += nt) s_gamma[i] = 0.f;
@@ -93,6 +149,10 @@ finalize_backward_kernel(const __grid_constant__ FinalizeBackward p,
     wait_previous_kernel();
     allow_next_kernel();
     if (CLUSTER) cluster_wait();
+    if (NORM && cluster == cut.clusters) {      // one more than the tokens need
+        direct_gamma<VEC, CLUSTER>(p, cut, split);
+        return;
+    }
 
     int64_t next_row = -1;
     float next_w = 0.f;
@@ -575,14 +635,16 @@ cudaError_t start(void (*kernel)(Params...), int64_t grid, int threads, size_t s
 template <int VPT, int VEC, bool NORM, bool CLUSTER>
 cudaError_t start_backward(const FinalizeBackward &p, const Cut &cut, cudaStream_t stream) {
     auto *kernel = finalize_backward_kernel<VPT, VEC, NORM, CLUSTER>;
-    const size_t smem = NORM && p.dgamma ? sizeof(float) * VPT * VEC * cut.threads : 0;
+    const bool direct = p.dgamma && p.T <= kDirectTokens;
+    const size_t smem = NORM && p.dgamma && !direct ? sizeof(float) * VPT * VEC * cut.threads : 0;
     constexpr int kMost = sizeof(float) * VPT * VEC * kMaxThreads;
     if (NORM && kMost > 32 * 1024) {    // the same for every call: threads may race to set it
         const cudaError_t err = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (err != cudaSuccess) return err;
     }
-    return start(kernel, cut.clusters * cut.splits, cut.threads, smem, cut.splits, stream, p, cut);
+    return start(kernel, (cut.clusters + direct) * cut.splits, cut.threads, smem, cut.splits,
+                 stream, p, cut);
 }
 
 template <int VPT, int VEC>
@@ -748,7 +810,9 @@ gate_backward_kernel(const __grid_constant__ GateBackward p) {
 
 }  // namespace
 
-int finalize_backward_partials(int T) { return T < kMaxPartials ? T : kMaxPartials; }
+int finalize_backward_partials(int T) {
+    return T <= kDirectTokens ? 0 : T < kMaxPartials ? T : kMaxPartials;
+}
 
 bool finalize_backward_fits(int64_t nvec) {
     return nvec <= static_cast<int64_t>(kMaxThreads) * kMaxVpt * kMaxSplits;
@@ -776,9 +840,9 @@ cudaError_t launch_finalize_backward(const FinalizeBackward &p, int num_sms,
     if (clusters > kMaxPartials) clusters = kMaxPartials;
     cut.clusters = clusters < p.T ? clusters : p.T;
     cudaError_t err = cudaSuccess;
-    if (!vec || cut.splits > 1 || !start_ring(p, cut, stream, &err))
+    if (!vec || cut.splits > 1 || p.T <= kDirectTokens || !start_ring(p, cut, stream, &err))
         err = vec ? start_backward<8>(p, cut, stream) : start_backward<1>(p, cut, stream);
-    if (err == cudaSuccess && p.dgamma)
+    if (err == cudaSuccess && p.dgamma && p.T > kDirectTokens)
         err = start(gamma_sum_kernel, (p.H - 1) / 32 + 1, 32 * kSumWarps, 0, 1, stream, p.partial, p.dgamma,
                     static_cast<int>(cut.clusters), p.H);
     return err;

@@ -158,10 +158,10 @@ moef_status moe_finalize_backward(const void *permuted_out, int64_t P, const int
             (dnorm_out != nullptr) != (gamma != nullptr) || (dgamma && !dnorm_out))
             return MOEF_ERR_ARG;
         if (dnorm_out && (!(eps >= 0.f) || isinf(eps))) return MOEF_ERR_ARG;
-        if (dgamma) {
+        const size_t need = moe_finalize_backward_workspace_bytes(T, H);
+        if (dgamma && need) {
             if (!workspace) return MOEF_ERR_NULL;
-            if (workspace_bytes < moe_finalize_backward_workspace_bytes(T, H))
-                return MOEF_ERR_SHAPE;
+            if (workspace_bytes < need) return MOEF_ERR_SHAPE;
             if (!aligned(workspace, 16)) return MOEF_ERR_ALIGN;
         }
     }

@@ -71,6 +71,11 @@ FINALIZE = [
     (3, 2, 4, 240000, 1, "fp32", True, True, True, 0.0),
     (90, 2, 4, 70000, 1, "fp32", True, True, True, 0.1),
     (60, 3, 4, 12008, 1, "bf16", True, False, True, 0.1),
+    # both sides of the number of tokens whose dgamma is taken directly
+    (32, 2, 4, 7168, 1, "fp32", True, True, True, 0.1),
+    (33, 2, 4, 7168, 1, "fp32", True, True, True, 0.1),
+    (32, 2, 4, 24, 1, "fp32", True, True, True, 0.1),
+    (1, 2, 4, 7168, 1, "fp32", True, True, True, 0.5),
 ]
 
 

@@ -28,7 +28,7 @@ def call(fn, base, **change):
 
 
 FINALIZE = dict(rows=A, P=16, idx=A, w=A, wkind=0, scale=1.0, r=A, gamma=A, eps=1e-6, dout=A,
-                dres=A, dnorm=A, drows=A, dweights=A, dshared=A, dresidual=A, dgamma=A, T=4, K=2,
+                dres=A, dnorm=A, drows=A, dweights=A, dshared=A, dresidual=A, dgamma=A, T=40, K=2,
                 H=8, ws=A, ws_bytes=1 << 20, stream=NULL)
 
 
@@ -50,7 +50,7 @@ def test_finalize_backward_argument_errors(lib):
     for k in ("idx", "w", "dweights"):
         assert call(f, FINALIZE, **{k: HALF}) == E_ALIGN, k
     assert call(f, FINALIZE, ws=A + 8) == E_ALIGN
-    need = lib.moe_finalize_backward_workspace_bytes(4, 8)
+    need = lib.moe_finalize_backward_workspace_bytes(40, 8)
     assert call(f, FINALIZE, ws_bytes=need - 1) == E_SHAPE
     for k, vs in (("T", (-1,)), ("K", (0, 33)), ("H", (0, -1, (1 << 30) + 1)), ("P", (0, -1))):
         for v in vs:
@@ -68,7 +68,7 @@ def test_finalize_backward_argument_errors(lib):
 def test_finalize_backward_workspace(lib):
     size = lib.moe_finalize_backward_workspace_bytes
     assert size(0, 8) == size(4, 0) == size(-1, 8) == 0
-    assert size(1, 8) == 32
+    assert size(1, 8) == size(32, 8) == 0 and size(33, 8) == 33 * 32
     assert size(INT_MAX, 7168) == size(5000, 7168) == 1024 * 7168 * 4
 
 
