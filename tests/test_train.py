@@ -456,6 +456,49 @@ def test_expert_backward_without_a_workspace(cuda_lib):
         expert_call(mf, case, m, x, w, dout, preact, workspace=none)
 
 
+@pytest.mark.parametrize("sizes", [(40000, 200, 64), (300, 40, 1000), (5000, 2000, 2000)], ids=str)
+def test_expert_backward_products_side_by_side(cuda_lib, sizes):
+    """dweight begins while dx runs: both are complete for what comes next on the stream, a
+    dx of many rounds beside a dweight of few tiles and the other way round, in plain calls
+    and in a replayed graph."""
+    mf, g = cuda_lib, gen(31)
+    T, n, H = sizes
+    _, m = routing(mf, g, T, 1, 4, 16)
+    P = m["row_token"].numel()
+    x, w = normal(g, T, H), normal(g, 4, 2 * n, H, scale=H ** -0.5)
+    dout, preact = poisoned(g, m, P, n, scale=0.1), poisoned(g, m, P, 2 * n)
+
+    def call(**kw):
+        return mf.expert_gated_ffn_backward(dout, x, m["row_token"], m["offsets"], m["counts"], w,
+                                            preact, **kw)
+
+    dx0 = torch.zeros(P, H, dtype=BF16, device="cuda")
+    dx = call(dx=dx0.clone(), want_dweight=False)["dx"]
+    dweight = call(want_dx=False)["dweight"]
+    out, dw = dx0.clone(), torch.empty_like(w)
+
+    def step():
+        out.zero_()
+        dw.zero_()
+        call(dx=out, dweight=dw)
+        return out.clone(), dw.clone()
+
+    for _ in range(10):
+        a, b = step()
+        sums = mf.unpermute_tokens(out, m["idx_map"])
+        assert torch.equal(a, dx) and torch.equal(b, dweight)
+        assert torch.equal(sums, mf.unpermute_tokens(dx, m["idx_map"]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a, b = step()
+    for _ in range(10):
+        a.zero_()
+        b.zero_()
+        graph.replay()
+        assert torch.equal(a, dx) and torch.equal(b, dweight)
+    assert mf.lost_waits() == 0
+
+
 def test_expert_backward_odd_layouts(cuda_lib):
     """Experts out of order, with gaps, without rows, past the buffer, in front of it."""
     mf, g = cuda_lib, gen(6)
