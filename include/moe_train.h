@@ -63,7 +63,8 @@ extern "C" {
  *                  (at least one output non-NULL)
  *   workspace      moe_finalize_backward_workspace_bytes(T, H) bytes with
  *                  dgamma, 16-byte aligned, contents irrelevant; may be NULL
- *                  without dgamma or when that is 0 (up to 32 tokens)
+ *                  without dgamma or when that is 0 (up to 32 tokens, 16
+ *                  if H % 8 != 0)
  *
  * A slot whose idx_map is outside [0, P) has no row: its dweights is 0.  No two
  * slots may name the same row.  dm stays in fp32 up to each output's rounding.

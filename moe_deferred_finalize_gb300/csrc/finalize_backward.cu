@@ -35,10 +35,7 @@ constexpr int kWarps = kMaxThreads / 32;
 constexpr int kMaxSplits = 8;
 constexpr int kMaxVpt = 8;
 constexpr int kMaxPartials = 1024;      // rows of dgamma's sums
-// whose dgamma needs none: one launch against two, in us, at H = 7168: 7.1 : 8.7 for 8
-// tokens, 9.4 : 10.8 for 32, 13.3 : 11.9 for 48; at H = 32768 19.0 : 20.6 for 32 and
-// 34.4 : 32.5 for 48; at H = 262144 206 : 213 for 32
-constexpr int kDirectTokens = 32;
+constexpr int kDirectTokens = 32;       // the most whose dgamma needs none
 constexpr int kSlots = 8;               // of a token, in flight at a time
 
 // How one launch is cut: `splits` CTAs (a cluster) take a token's slices of
@@ -66,6 +63,13 @@ __device__ __forceinline__ float warp_sum8(float (&acc)[8], int lane) {
     v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
     return v;
 }
+
+// Whether dgamma is taken directly (below), without rows of sums.  One launch against
+// two, in us, at H = 7168: 7.1 : 8.7 for 8 tokens, 9.4 : 10.8 for 32, 13.3 : 11.9 for 48;
+// at H = 32768 19.0 : 20.6 for 32 and 34.4 : 32.5 for 48; at H = 262144 206 : 213 for 32.
+// Single values, H = 32767: 39 : 41 for 16 and 81 : 48 for 24.  The sizes alone decide, as
+// they do on the workspace.
+bool direct_dgamma(int T, int H) { return T <= (H % 8 ? kDirectTokens / 2 : kDirectTokens); }
 
 // dgamma of a few tokens by one cluster (or CTA) beside those that take the tokens: its
 // CTAs share the tokens for their inverse RMS, which all of them get, and then the
@@ -138,7 +142,7 @@ finalize_backward_kernel(const __grid_constant__ FinalizeBackward p,
     const int split = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int64_t cluster = CLUSTER ? blockIdx.x / cut.splits : blockIdx.x;
     const int v_begin = split * cut.slice, v_end = min(v_begin + cut.slice, cut.nvec);
-    const bool sums_gamma = NORM && p.dgamma && p.T > kDirectTokens;
+    const bool sums_gamma = NORM && p.partial;
     if (CLUSTER) cluster_arrive();
     if (sums_gamma)
         for (int i = tid; i < VPT * VEC * nt; i += nt) s_gamma[i] = 0.f;
@@ -635,16 +639,15 @@ cudaError_t start(void (*kernel)(Params...), int64_t grid, int threads, size_t s
 template <int VPT, int VEC, bool NORM, bool CLUSTER>
 cudaError_t start_backward(const FinalizeBackward &p, const Cut &cut, cudaStream_t stream) {
     auto *kernel = finalize_backward_kernel<VPT, VEC, NORM, CLUSTER>;
-    const bool direct = p.dgamma && p.T <= kDirectTokens;
-    const size_t smem = NORM && p.dgamma && !direct ? sizeof(float) * VPT * VEC * cut.threads : 0;
+    const size_t smem = NORM && p.partial ? sizeof(float) * VPT * VEC * cut.threads : 0;
     constexpr int kMost = sizeof(float) * VPT * VEC * kMaxThreads;
     if (NORM && kMost > 32 * 1024) {    // the same for every call: threads may race to set it
         const cudaError_t err = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (err != cudaSuccess) return err;
     }
-    return start(kernel, (cut.clusters + direct) * cut.splits, cut.threads, smem, cut.splits,
-                 stream, p, cut);
+    const int64_t clusters = cut.clusters + (p.dgamma && !p.partial);
+    return start(kernel, clusters * cut.splits, cut.threads, smem, cut.splits, stream, p, cut);
 }
 
 template <int VPT, int VEC>
@@ -810,8 +813,8 @@ gate_backward_kernel(const __grid_constant__ GateBackward p) {
 
 }  // namespace
 
-int finalize_backward_partials(int T) {
-    return T <= kDirectTokens ? 0 : T < kMaxPartials ? T : kMaxPartials;
+int finalize_backward_partials(int T, int H) {
+    return direct_dgamma(T, H) ? 0 : T < kMaxPartials ? T : kMaxPartials;
 }
 
 bool finalize_backward_fits(int64_t nvec) {
@@ -840,9 +843,9 @@ cudaError_t launch_finalize_backward(const FinalizeBackward &p, int num_sms,
     if (clusters > kMaxPartials) clusters = kMaxPartials;
     cut.clusters = clusters < p.T ? clusters : p.T;
     cudaError_t err = cudaSuccess;
-    if (!vec || cut.splits > 1 || p.T <= kDirectTokens || !start_ring(p, cut, stream, &err))
+    if (!vec || cut.splits > 1 || (p.dgamma && !p.partial) || !start_ring(p, cut, stream, &err))
         err = vec ? start_backward<8>(p, cut, stream) : start_backward<1>(p, cut, stream);
-    if (err == cudaSuccess && p.dgamma && p.T > kDirectTokens)
+    if (err == cudaSuccess && p.partial)
         err = start(gamma_sum_kernel, (p.H - 1) / 32 + 1, 32 * kSumWarps, 0, 1, stream, p.partial, p.dgamma,
                     static_cast<int>(cut.clusters), p.H);
     return err;

@@ -23,12 +23,12 @@ struct FinalizeBackward {
     uint16_t *drows;
     float *dweights;
     uint16_t *dshared, *dresidual, *dgamma;
-    float *partial;                     // fp32 [clusters, H] with dgamma
+    float *partial;                     // fp32 [clusters, H] when dgamma needs it
     int T, K, H;
 };
 
 // Rows of partial that a launch can need; and whether a row fits.
-int finalize_backward_partials(int T);
+int finalize_backward_partials(int T, int H);
 bool finalize_backward_fits(int64_t nvec);
 cudaError_t launch_finalize_backward(const FinalizeBackward &p, int num_sms, cudaStream_t stream);
 

@@ -136,7 +136,7 @@ extern "C" {
 
 size_t moe_finalize_backward_workspace_bytes(int T, int H) {
     if (T <= 0 || !valid_hidden(H)) return 0;
-    return static_cast<size_t>(moef::finalize_backward_partials(T)) * H * sizeof(float);
+    return static_cast<size_t>(moef::finalize_backward_partials(T, H)) * H * sizeof(float);
 }
 
 moef_status moe_finalize_backward(const void *permuted_out, int64_t P, const int32_t *idx_map,
@@ -201,7 +201,8 @@ moef_status moe_finalize_backward(const void *permuted_out, int64_t P, const int
     p.dshared = u16(dshared);
     p.dresidual = u16(dresidual);
     p.dgamma = u16(dgamma);
-    p.partial = static_cast<float *>(workspace);
+    if (dgamma && moef::finalize_backward_partials(T, H))
+        p.partial = static_cast<float *>(workspace);
     p.T = T;
     p.K = K;
     p.H = H;

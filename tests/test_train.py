@@ -75,6 +75,8 @@ FINALIZE = [
     (32, 2, 4, 7168, 1, "fp32", True, True, True, 0.1),
     (33, 2, 4, 7168, 1, "fp32", True, True, True, 0.1),
     (32, 2, 4, 24, 1, "fp32", True, True, True, 0.1),
+    (16, 2, 4, 2049, 1, "fp32", True, True, True, 0.1),
+    (17, 2, 4, 2049, 1, "fp32", True, True, True, 0.1),
     (1, 2, 4, 7168, 1, "fp32", True, True, True, 0.5),
 ]
 

@@ -68,7 +68,8 @@ def test_finalize_backward_argument_errors(lib):
 def test_finalize_backward_workspace(lib):
     size = lib.moe_finalize_backward_workspace_bytes
     assert size(0, 8) == size(4, 0) == size(-1, 8) == 0
-    assert size(1, 8) == size(32, 8) == 0 and size(33, 8) == 33 * 32
+    assert size(1, 8) == size(32, 8) == size(16, 9) == 0
+    assert size(33, 8) == 33 * 32 and size(17, 9) == 17 * 36
     assert size(INT_MAX, 7168) == size(5000, 7168) == 1024 * 7168 * 4
 
 
