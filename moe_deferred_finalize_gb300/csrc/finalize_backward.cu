@@ -673,8 +673,10 @@ cudaError_t start_backward(const FinalizeBackward &p, const Cut &cut, cudaStream
     }
 }
 
-// The ring's form, when a token has enough items for it and a row few enough pieces
-// for two CTAs an SM; false (nothing launched) otherwise.
+// The ring's form, when a token has enough items for it, the CTA's threads have a whole
+// row between them (without RMSNorm rows may be longer: the plain form goes over them in
+// steps) and its pieces are few enough for two CTAs an SM; false (nothing launched)
+// otherwise.
 constexpr int kRingBytes = 102 * 1024;
 
 template <int VPT, int NS>
@@ -682,7 +684,7 @@ bool start_ring(const FinalizeBackward &p, Cut cut, cudaStream_t stream, cudaErr
     const int items = (p.dnorm ? 2 : 0) + (p.dres ? 1 : 0) + (p.dout ? 1 : 0) + p.K;
     const int pieces = VPT * cut.threads;
     const size_t smem = static_cast<size_t>(pieces) * 16 * (NS + (p.dnorm && p.dgamma ? 2 : 0));
-    if (items < NS + 1 || smem > kRingBytes) return false;
+    if (items < NS + 1 || pieces < cut.nvec || smem > kRingBytes) return false;
     auto *kernel = p.dnorm ? finalize_backward_ring_kernel<VPT, NS, true>
                            : finalize_backward_ring_kernel<VPT, NS, false>;
     *err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);

@@ -984,6 +984,36 @@ def test_finalize_backward_many_tokens(cuda_lib, case):
                 assert torch.equal(other[k], res[k]), k
 
 
+LONG_ROWS = [
+    # as RING, without the norm: rows of up to 8192 values fit a CTA's threads, longer ones
+    # (one piece, one value more among them) are gone over in steps
+    (400, 8, 8, 8192, 1, "fp32", False, True, False, 0.1),
+    (400, 4, 8, 8200, 1, "fp32", False, True, False, 0.1),
+    (400, 4, 8, 8193, 1, "bf16", False, True, True, 0.1),
+    (700, 8, 8, 16384, 8, "fp32", False, True, False, 0.0),
+    (320, 5, 8, 16392, 1, "packed", False, False, True, 0.2),
+    (400, 8, 16, 20000, 1, "fp32", False, True, True, 0.1),
+    (310, 32, 40, 9000, 1, "fp32", False, True, True, 0.5),
+]
+
+
+@pytest.mark.parametrize("case", LONG_ROWS, ids=str)
+def test_finalize_backward_long_rows_without_norm(cuda_lib, case):
+    """All columns of all outputs, which are made in place of values that no gradient has."""
+    mf = cuda_lib
+    T, H, dres = case[0], case[3], case[8]
+    rows, m, w, dout, kw = finalize_inputs(mf, case, seed=5)
+    drows0 = torch.full_like(rows, 7.0)
+    outs = dict(drows=drows0.clone(), dweights=torch.full((T, case[1]), NAN, device="cuda"))
+    if dres:
+        outs["dresidual"] = torch.full((T, H), NAN, dtype=BF16, device="cuda")
+        if dout is not None:
+            outs["dshared"] = torch.full((T, H), NAN, dtype=BF16, device="cuda")
+    res = mf.moe_finalize_backward(rows, m["idx_map"], w, case[5], dout, routed_scale=2.5, **outs,
+                                   **kw)
+    check_finalize(case, rows, m, w, dout, kw, res, drows0, 2.5, 1e-6)
+
+
 def test_one_pass_calls_equal_checked_calls(cuda_lib, monkeypatch):
     """The same results with and without the call extension."""
     mf = cuda_lib
