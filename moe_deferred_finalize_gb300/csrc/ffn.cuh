@@ -40,7 +40,6 @@ struct Gemm {
     int64_t b_pitch;            // values from one of its rows (of k: b_mn) to the next
     int64_t a_pitch;            // the same of A, for grouped dweight
     int a_zeros, b_zeros;       // the operand has zeros behind spaced rows
-    int beside;                 // grouped dweight: needs nothing of the previous kernel, dx
 };
 
 // Steps of `step` values that cover k >= 1 of them.  k is a token count in

@@ -991,16 +991,9 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<CG>(smem_addr(&h->tmem), 2 * kMaxBn);
-    // dweight beside dx, the previous kernel: dx's CTAs let this one begin once the
-    // kernels in front of it were complete, and nothing of dx is read here.  CTAs then
-    // fill SMs that dx leaves, 100 tokens of 8 experts 1.6 us, 4096 of 64 8 us sooner.
-    // The next kernel may begin, and this grid end, only when dx is complete too.
-    const bool beside = DW && work.g[0].beside;
     if (grouped) {
-        if (!beside) {
-            wait_previous_kernel();
-            allow_next_kernel();
-        }
+        wait_previous_kernel();
+        allow_next_kernel();
         count_tiles<CG, DW>(work.g[0], work.p[0], h);
     }
     fence_before();
@@ -1393,10 +1386,6 @@ gemm_tc_kernel(const __grid_constant__ Work<N, DW> work) {
         }
     }
     if (CG == 1 && clustered && split == 1) cluster_wait();
-    if (beside) {
-        wait_previous_kernel();
-        allow_next_kernel();
-    }
     fence_before();
     if (CG == 2) cluster_sync(); else __syncthreads();
     fence_after();

@@ -122,7 +122,6 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
         d.N = cols;
         d.K = static_cast<int>(P);
         d.out = dweight;
-        d.beside = dx != nullptr;
         st = cuda_status(moef::launch_group_dweight(d, sms, stream));
     }
     return st;

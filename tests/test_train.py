@@ -501,6 +501,42 @@ def test_expert_backward_products_side_by_side(cuda_lib, sizes):
     assert mf.lost_waits() == 0
 
 
+@pytest.mark.parametrize("sizes", [(40000, 200, 64), (300, 40, 1000), (5000, 1000, 2000)], ids=str)
+def test_finalize_may_read_dx_early_behind_dweight(cuda_lib, sizes):
+    """moe_finalize with routing_ready reads its weights before the kernel in front of it,
+    dweight's, has finished: every kernel before that one must be complete by then.  dx,
+    as bf16 weights, is the last of them."""
+    mf, g = cuda_lib, gen(32)
+    T, n, H = sizes
+    _, m = routing(mf, g, T, 1, 4, 16)
+    P = m["row_token"].numel()
+    x, w = normal(g, T, H), normal(g, 4, 2 * n, H, scale=H ** -0.5)
+    dout, preact = poisoned(g, m, P, n, scale=0.1), poisoned(g, m, P, 2 * n)
+    zeros = torch.zeros(P, H, dtype=BF16, device="cuda")
+    dx, dw = zeros.clone(), torch.empty_like(w)
+    workspace = torch.empty(mf.expert_backward_workspace_bytes(P, 2 * n, H), dtype=torch.uint8,
+                            device="cuda")
+    F = P * H // 8 // 64 * 64       # the last rows of dx too, as 8 weights a token
+    rows = normal(g, 64, 64)
+    idx = torch.arange(F * 8, device="cuda").remainder(64).view(F, 8).int()
+    weights = dx.view(-1)[-F * 8:].view(F, 8)
+    out = torch.empty(F, 64, dtype=BF16, device="cuda")
+
+    def call(ready):
+        dx.copy_(zeros)
+        mf.expert_gated_ffn_backward(dout, x, m["row_token"], m["offsets"], m["counts"], w, preact,
+                                     dx=dx, dweight=dw, workspace=workspace)
+        return mf.moe_finalize(rows, idx, weights, "bf16", shared, routing_ready=ready,
+                               out=out)["out"].clone()
+
+    shared = torch.zeros(F, 64, dtype=BF16, device="cuda")
+    want = call(False)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        assert torch.equal(call(True), want)
+    assert mf.lost_waits() == 0
+
+
 def test_expert_backward_odd_layouts(cuda_lib):
     """Experts out of order, with gaps, without rows, past the buffer, in front of it."""
     mf, g = cuda_lib, gen(6)
