@@ -227,7 +227,10 @@ moef_status moe_expert_linear_backward(const void *dout, const void *x, int64_t 
  * or of a scaled loss).
  *
  * Alignment: 16 bytes (8 bits: 8 for the states) of all of a tensor's arrays
- * allow 16-byte accesses; others take single values.  A gradient that is not
+ * allow 16-byte accesses; others take single values.  A v that passes the largest
+ * fp32 number (a scaled gradient above 1.8e19 can) is infinite, and the value moves by
+ * its decay alone: for good with fp32 states, while 8 bits store a sqrt(v) of 2^64
+ * (1 - 2^-20) at most, which decays again.  A gradient that is not
  * finite leaves its value's states not finite (8 bits: those of its 256).
  * MOEF_ERR_ARG for lr, eps or weight_decay negative or not finite, a beta
  * outside [0, 1), step < 1 without device_step, or state_bits other than 8

@@ -125,7 +125,7 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[8]) {
 // method on its residual, which an fma gives exactly (P. Markstein, IBM J. Res. Dev.
 // 34, 1990; the quotient needs y's reciprocal rounded to nearest).  Three and five
 // instructions where the library's functions take about ten each, which 8-bit states
-// are bound by otherwise.  Finite x in the ranges below.
+// are bound by otherwise.  The root is of 0 <= x < 2^127.
 __device__ __forceinline__ float rounded_quotient(float x, float y, float reciprocal) {
     const float q = x * reciprocal;
     return fmaf(fmaf(-q, y, x), reciprocal, q);
@@ -136,6 +136,12 @@ __device__ __forceinline__ float rounded_sqrt(float x) {
     const float s = x * r;
     return fmaf(fmaf(-s, s, x), 0.5f * r, s);
 }
+__device__ __forceinline__ bool has_rounded_sqrt(float x) {
+    return __float_as_uint(x) < 0x7F000000u;
+}
+// The largest root that is stored, 2^64 (1 - 2^-20): its code and scale give a value
+// whose square is finite, so a v that passed the largest number decays again.
+constexpr float kMostRoot = 0x1.ffffep63f;
 
 // The piece's scale, and its values as codes of it.  ROOT: values above 0 keep a
 // code above 0.
@@ -238,15 +244,34 @@ adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ Ada
             load8(static_cast<const float *>(t.exp_avg) + i, m, left, whole);
             load8(static_cast<const float *>(t.exp_avg_sq) + i, v, left, whole);
         }
+        bool usual = true;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             g[k] *= grad_scale;
             m[k] = fmaf(f.rest1, g[k], __fmul_rn(f.beta1, m[k]));
             v[k] = fmaf(f.rest2, __fmul_rn(g[k], g[k]), __fmul_rn(f.beta2, v[k]));
-            const float s = EIGHT ? rounded_sqrt(v[k]) : fast_sqrt(v[k]);
+            usual = usual && has_rounded_sqrt(v[k]);
+        }
+        if constexpr (EIGHT) {          // v becomes its root
+            if (usual) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = rounded_sqrt(v[k]);
+            } else {                    // a square past the largest number, NaN
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = sqrtf(v[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float s = EIGHT ? v[k] : fast_sqrt(v[k]);
             p[k] = fmaf(keep, p[k],
                         -(step_size * m[k]) * fast_reciprocal(fmaf(s, root, f.eps)));
-            if constexpr (EIGHT) v[k] = s;
+        }
+        if constexpr (EIGHT) {
+            if (!usual) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = v[k] > kMostRoot ? kMostRoot : v[k];
+            }
         }
         if (left > 0) {
             if constexpr (MASTER) store8(t.master + i, p, left, whole);

@@ -756,6 +756,48 @@ def test_adamw_not_finite(cuda_lib):
         assert torch.isfinite(m[:256]).all() and torch.isfinite(m[768:]).all()
 
 
+@pytest.mark.parametrize("grad", [BF16, F32], ids=str)
+def test_adamw_square_past_the_largest_number(cuda_lib, grad):
+    """A finite gradient whose square is infinite in fp32: its value moves by its decay
+    alone, the same in both widths of states; all other values as without it; nothing is
+    NaN, then or later.  In 8 bits sqrt(v) is stored as 2^64 (1 - 2^-20)."""
+    mf, at = cuda_lib, [300, 2000, 2047]
+    ends = {}
+    for bits in (32, 8):
+        clean = adamw_inputs(mf, (4100,), bits, False, F32, grad, False)
+        spike = adamw_inputs(mf, (4100,), bits, False, F32, grad, False)
+        p0 = spike[0][0].clone()
+        spike[1][0][at] = torch.tensor([1e20, -3e19, 1e38], device="cuda").to(grad)
+        for inputs in (clean, spike):
+            mf.adamw_step(*inputs[:2], step=1, **HYPER, **inputs[2])
+        p = spike[0][0]
+        keep = torch.tensor(1.0) - torch.tensor(HYPER["lr"]) * torch.tensor(HYPER["weight_decay"])
+        assert torch.equal(p[at], p0[at] * keep.cuda())
+        others = torch.ones(4100, dtype=torch.bool, device="cuda")
+        others[at] = False
+        assert torch.equal(p[others], clean[0][0][others])
+        m, v = adamw_states(spike[2], 0)
+        assert torch.isfinite(m).all()
+        if bits == 8:
+            root = v[at].sqrt()         # the largest of its 256: code 448, scale within 2^-22
+            assert ((root / (2.0 ** 64 * (1 - 2.0 ** -20)) - 1).abs() <= 2.0 ** -21).all()
+            for a, b in zip(clean[2].values(), spike[2].values()):      # blocks without it
+                n = 1 if a[0].dtype == F32 else 256
+                for i in (0, 2, 6, 8, 16):
+                    block = slice(n * i, min(n * i + n, a[0].numel()))
+                    assert torch.equal(a[0][block].view(torch.uint8),
+                                       b[0][block].view(torch.uint8))
+        ends[bits] = p[at].clone()
+        for step in (2, 3, 4):          # back to ordinary gradients
+            mf.adamw_step(spike[0], clean[1], step=step, **HYPER, **spike[2])
+            assert torch.isfinite(spike[0][0]).all() and torch.isfinite(spike[2]["exp_avg"][0]
+                                                                        .float()).all()
+        if bits == 8:
+            later = adamw_states(spike[2], 0)[1]
+            assert (later[at] < v[at]).all()
+    assert torch.equal(ends[8], ends[32])
+
+
 # ---------------------------------------------------------- all together
 
 
