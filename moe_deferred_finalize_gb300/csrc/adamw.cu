@@ -125,19 +125,20 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[8]) {
 // method on its residual, which an fma gives exactly (P. Markstein, IBM J. Res. Dev.
 // 34, 1990; the quotient needs y's reciprocal rounded to nearest).  Three and five
 // instructions where the library's functions take about ten each, which 8-bit states
-// are bound by otherwise.  The root is of 0 <= x < 2^127.
+// are bound by otherwise.  The root is of 2^-126 <= x < 2^127: below that range neither
+// the approximation nor the residual is one.
 __device__ __forceinline__ float rounded_quotient(float x, float y, float reciprocal) {
     const float q = x * reciprocal;
     return fmaf(fmaf(-q, y, x), reciprocal, q);
 }
 __device__ __forceinline__ float rounded_sqrt(float x) {
-    float r;        // below the normal range the root is off by 1e-19 at most
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(x, 1.17549435e-38f)));
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     const float s = x * r;
     return fmaf(fmaf(-s, s, x), 0.5f * r, s);
 }
 __device__ __forceinline__ bool has_rounded_sqrt(float x) {
-    return __float_as_uint(x) < 0x7F000000u;
+    return __float_as_uint(x) - 0x00800000u < 0x7F000000u - 0x00800000u;
 }
 // The largest root that is stored, 2^64 (1 - 2^-20): its code and scale give a value
 // whose square is finite, so a v that passed the largest number decays again.
@@ -256,7 +257,7 @@ adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ Ada
             if (usual) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = rounded_sqrt(v[k]);
-            } else {                    // a square past the largest number, NaN
+            } else {                    // 0, below the normal range, past the largest number, NaN
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = sqrtf(v[k]);
             }

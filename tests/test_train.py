@@ -798,6 +798,39 @@ def test_adamw_square_past_the_largest_number(cuda_lib, grad):
     assert torch.equal(ends[8], ends[32])
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_squares_below_the_normal_range(cuda_lib, bits):
+    """Gradients of 3e-22 to 3e-19, whose squares fp32 holds below its normal range, and
+    zeros among them, with eps = 0: the step that the formula gives for v as fp32 holds it,
+    |u| of the order of lr.  Roundings: of m, the step size, its product, the root, its
+    factor and the reciprocal, 2^-22 each at most, 6 of them; of p 2^-24, of keep p 2^-24.
+    In 8 bits a root's code is then off by 2^-4 of itself or 2^-10 of its scale, or at the
+    least code; its scale by 2^-22."""
+    mf, g, n = cuda_lib, gen(17), 2048
+    lr, b1, b2 = 1e-2, 0.9, 0.95
+    grad = normal(g, n, dtype=F32) * 10.0 ** (-21.5 + 3 * torch.rand(n, generator=g, device="cuda"))
+    grad[::11] = 0
+    p = [normal(g, n, dtype=F32)]
+    p0, state = p[0].double(), mf.adamw_state(p, bits)
+    mf.adamw_step(p, [grad], step=1, lr=lr, betas=(b1, b2), eps=0.0, weight_decay=0.0, **state)
+    # as fp32 rounds them; the factors 1 - beta are rounded from 64 bits
+    v = ((grad * grad).double() * torch.tensor(1 - b2).double().cuda()).float().double()
+    m = grad.double() * (1 - b1)
+    on = v > 0                          # a square may be 0: 0 / 0, m / 0
+    assert on.sum() > n // 2 and (v[on] < 2.0 ** -126).sum() > n // 4
+    u = lr / (1 - b1) * m / (v / (1 - b2)).sqrt()
+    tol = 6 * 2.0 ** -22 * u.abs() + 2 * 2.0 ** -24 * (p0.abs() + u.abs())
+    T_.check(p[0][on], ((p0 - u)[on], tol[on]), "param")
+    assert not torch.isfinite(p[0][~on]).any()
+    if bits == 8:
+        scale = v.sqrt().view(-1, 256).amax(1) / 448
+        T_.check(state["exp_avg_sq_scale"][0], (scale, 2.0 ** -22 * scale), "scale")
+        code, want = state["exp_avg_sq"][0].double(), v.sqrt() / scale.repeat_interleave(256)
+        least = torch.where(on & (want < 2.0 ** -9), 2.0 ** -9, want)
+        T_.check(code, (least, 2.0 ** -4 * want * (1 + 2.0 ** -20) + 2.0 ** -10), "codes")
+        assert (code[on] > 0).all() and not code[~on].any()
+
+
 # ---------------------------------------------------------- all together
 
 
