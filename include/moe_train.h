@@ -231,7 +231,10 @@ moef_status moe_expert_linear_backward(const void *dout, const void *x, int64_t 
  * fp32 number (a scaled gradient above 1.8e19 can) is infinite, and the value moves by
  * its decay alone: for good with fp32 states, while 8 bits store a sqrt(v) of 2^64
  * (1 - 2^-20) at most, which decays again.  A gradient that is not
- * finite leaves its value's states not finite (8 bits: those of its 256).
+ * finite leaves its value and its fp32 states not finite.  With 8 bits, NaN is its own
+ * value's alone in both states; an infinite one makes all 256 values of exp_avg NaN
+ * (their scale is infinite), while its sqrt(v) is stored as the largest above, beside
+ * which the block's other roots keep the least code above 0.
  * MOEF_ERR_ARG for lr, eps or weight_decay negative or not finite, a beta
  * outside [0, 1), step < 1 without device_step, or state_bits other than 8
  * and 32.  tensors may be NULL with n = 0.

@@ -831,6 +831,33 @@ def test_adamw_squares_below_the_normal_range(cuda_lib, bits):
         assert (code[on] > 0).all() and not code[~on].any()
 
 
+def test_adamw_not_finite_in_8_bits(cuda_lib):
+    """All 256 values of both states beside a gradient that is not finite: NaN stays with
+    its value; an infinite one takes exp_avg's block, and leaves exp_avg_sq's other roots
+    the least code."""
+    mf = cuda_lib
+    clean = adamw_inputs(mf, (1024,), 8, True, BF16, F32, False)
+    dirty = adamw_inputs(mf, (1024,), 8, True, BF16, F32, False)
+    clean[1][0][[300, 600]] = 0     # the blocks' largest are others
+    dirty[1][0][300], dirty[1][0][600] = NAN, -float("inf")
+    for inputs in (clean, dirty):
+        mf.adamw_step(*inputs[:2], step=1, **inputs[2])
+    at = torch.arange(1024, device="cuda")
+    nan, inf = at == 300, (at >= 512) & (at < 768)
+    m0, m = clean[2]["exp_avg"][0].float(), dirty[2]["exp_avg"][0].float()
+    v0, v = clean[2]["exp_avg_sq"][0].float(), dirty[2]["exp_avg_sq"][0].float()
+    assert torch.isnan(m[nan | inf]).all() and torch.equal(m[~(nan | inf)], m0[~(nan | inf)])
+    assert torch.isnan(v[nan]).all() and torch.equal(v[~(nan | inf)], v0[~(nan | inf)])
+    assert v[600] == 448 and (v[inf & (at != 600)] == 2.0 ** -9 * (v0[inf & (at != 600)] > 0)).all()
+    for key in ("exp_avg_scale", "exp_avg_sq_scale"):
+        a, b = clean[2][key][0], dirty[2][key][0]
+        assert torch.equal(a[[0, 1, 3]], b[[0, 1, 3]])
+        assert torch.isinf(b[2]) if key == "exp_avg_scale" else torch.isfinite(b[2])
+    p0, p = clean[2]["masters"][0], dirty[2]["masters"][0]
+    own = nan | (at == 600)
+    assert torch.isnan(p[own]).all() and torch.equal(p[~own], p0[~own])
+
+
 # ---------------------------------------------------------- all together
 
 
