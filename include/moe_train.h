@@ -60,7 +60,7 @@ extern "C" {
  *   dweights       fp32 [T, K] or NULL
  *   dshared, dresidual  bf16 [T, H], each or NULL (equal values without dout)
  *   dgamma         bf16 [H] or NULL; needs dnorm_out
- *                  (at least one output non-NULL)
+ *                  (at least one output non-NULL when T > 0)
  *   workspace      moe_finalize_backward_workspace_bytes(T, H) bytes with
  *                  dgamma, 16-byte aligned, contents irrelevant; may be NULL
  *                  without dgamma or when that is 0 (up to 32 tokens, 16
@@ -158,7 +158,7 @@ moef_status moe_expert_linear_save(const void *x, int64_t T, const int32_t *row_
  *                  left as they were
  *   dweight        bf16 [E, 2I, H] ([E, N, K]) or NULL; zeros for an expert
  *                  without rows
- *   dbias          bf16 [E, 2I] ([E, N]) or NULL          (at least one non-NULL)
+ *   dbias          bf16 [E, 2I] ([E, N]) or NULL          (at least one non-NULL when P > 0)
  *   workspace      moe_expert_backward_workspace_bytes(P, cols, inputs) bytes,
  *                  16-byte aligned (NULL when that is 0): cols the width of dz
  *                  (2I, or N), 0 when dout is dz and lies so that it can be

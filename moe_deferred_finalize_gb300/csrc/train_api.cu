@@ -53,7 +53,7 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
         return MOEF_ERR_SHAPE;
     if (act < MOEF_ACT_NONE || act > MOEF_ACT_RELU) return MOEF_ERR_ARG;
     if (!row_token && T != P) return MOEF_ERR_SHAPE;
-    if (!dx && !dweight && !dbias) return MOEF_ERR_NULL;
+    if (P > 0 && !dx && !dweight && !dbias) return MOEF_ERR_NULL;     // P = 0: dx of no rows
     const bool needs_preact = gated || act != MOEF_ACT_NONE;
     if (!needs_preact && preact) return MOEF_ERR_ARG;
     const int cols = gated ? 2 * n : n;
@@ -149,8 +149,8 @@ moef_status moe_finalize_backward(const void *permuted_out, int64_t P, const int
     if (T < 0 || K < 1 || K > MOEF_MAX_K || !valid_hidden(H)) return MOEF_ERR_SHAPE;
     if (wkind != MOEF_W_FP32 && wkind != MOEF_W_BF16 && wkind != MOEF_W_PACKED_TOPK)
         return MOEF_ERR_ARG;
-    if (!drows && !dweights && !dshared && !dresidual && !dgamma) return MOEF_ERR_NULL;
     if (T > 0) {
+        if (!drows && !dweights && !dshared && !dresidual && !dgamma) return MOEF_ERR_NULL;
         if (P < 1) return MOEF_ERR_SHAPE;
         if (!idx_map || (drows && !weights) || (dweights && !permuted_out)) return MOEF_ERR_NULL;
         if (!dout && !dresidual_out && !dnorm_out) return MOEF_ERR_NULL;

@@ -1036,6 +1036,36 @@ def test_threads_with_streams_of_their_own(cuda_lib):
     assert mf.lost_waits() == 0
 
 
+@pytest.mark.parametrize("fast", [True, False])
+def test_batches_of_nothing(cuda_lib, monkeypatch, fast):
+    """No tokens and no rows: outputs of no elements, gradients of weights that are zeros."""
+    mf = cuda_lib
+    from moe_deferred_finalize_gb300 import _abi
+    if not fast:
+        monkeypatch.setattr(_abi, "_FAST", None)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    e, wide = (torch.empty((0, n), dtype=BF16, device="cuda") for n in (64, 128))
+    idx, w = torch.empty((0, 2), **i32), torch.empty((0, 2), device="cuda")
+    for kw in ({}, dict(want_dweights=False), dict(dresidual_out=e)):
+        res = mf.moe_finalize_backward(e, idx, w, "fp32", e, **kw)
+        assert res and all(v.shape[0] == 0 for v in res.values())
+    res = mf.moe_finalize_backward(e, idx, w, "fp32", dnorm_out=e, residual_out=e,
+                                   gamma=torch.ones(64, dtype=BF16, device="cuda"))
+    assert not res["dgamma"].any()
+    assert mf.unpermute_tokens(e, idx, add=(e, e)).shape == (0, 64)
+    assert mf.topk_route_backward(w, w, idx, 4, "softmax").shape == (0, 4)
+    offsets, counts = torch.zeros(4, **i32), torch.zeros(3, **i32)
+    weight = torch.ones((3, 128, 64), dtype=BF16, device="cuda")
+    for want in ({}, dict(want_dweight=False), dict(want_dx=False, want_dbias=True)):
+        for row_token in (None, torch.empty(0, **i32)):
+            for res in (mf.expert_gated_ffn_backward(e, e, row_token, offsets, counts, weight,
+                                                     wide, **want),
+                        mf.expert_linear_backward(wide, e, offsets, counts, weight,
+                                                  row_token=row_token, **want)):
+                assert not any(v.any() for v in res.values())
+                assert "dx" not in res or res["dx"].shape == (0, 64)
+
+
 def test_two_streams_at_once(cuda_lib):
     """Calls on a given stream, beside others on the current one."""
     mf = cuda_lib

@@ -65,6 +65,19 @@ def test_finalize_backward_argument_errors(lib):
     assert call(f, FINALIZE, H=32768 + 8, dout=HALF, ws_bytes=1 << 40) == E_SHAPE
 
 
+def test_batches_of_nothing(lib):
+    """Arrays without elements may have no address: without tokens and rows, outputs of
+    none are not missing ones."""
+    f = lib.moe_finalize_backward
+    none = dict(drows=NULL, dweights=NULL, dshared=NULL, dresidual=NULL, dgamma=NULL)
+    assert call(f, FINALIZE, **none, T=0) == call(f, FINALIZE, **none, T=0, P=0) == OK
+    assert call(f, FINALIZE, **none, T=1) == E_NULL
+    none = dict(dx=NULL, dw=NULL, db=NULL)
+    for f in (lib.moe_expert_gated_ffn_backward, lib.moe_expert_linear_backward):
+        assert call(f, EXPERT, **none, T=0, P=0) == call(f, EXPERT, **none, P=0) == OK
+        assert call(f, EXPERT, **none, T=0) == call(f, EXPERT, **none) == E_NULL
+
+
 def test_finalize_backward_workspace(lib):
     size = lib.moe_finalize_backward_workspace_bytes
     assert size(0, 8) == size(4, 0) == size(-1, 8) == 0
