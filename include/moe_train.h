@@ -235,7 +235,7 @@ moef_status moe_expert_linear_backward(const void *dout, const void *x, int64_t 
  * value's alone in both states; an infinite one makes all 256 values of exp_avg NaN
  * (their scale is infinite), while its sqrt(v) is stored as the largest above, beside
  * which the block's other roots keep the least code above 0.
- * MOEF_ERR_ARG for lr, eps or weight_decay negative or not finite, a beta
+ * MOEF_ERR_ARG for lr, eps or weight_decay negative or not finite in fp32, a beta
  * outside [0, 1), step < 1 without device_step, or state_bits other than 8
  * and 32.  tensors may be NULL with n = 0.
  */

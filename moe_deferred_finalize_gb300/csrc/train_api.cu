@@ -1,5 +1,6 @@
 // C ABI of the MoE layer's training side (moe_train.h): argument checks and the
 // launches of each entry point.  Host code only.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>
@@ -127,7 +128,8 @@ moef_status expert_backward(const void *dout, const void *x, int64_t T, const in
     return st;
 }
 
-bool not_negative(double v) { return isfinite(v) && v >= 0.0; }
+// A number of the step, which is taken in fp32.
+bool not_negative(double v) { return v >= 0.0 && v <= FLT_MAX; }
 
 }  // namespace
 

@@ -216,6 +216,17 @@ def test_adamw_argument_errors(lib):
         assert step(config={k: HALF}) == E_ALIGN
 
 
+def test_adamw_numbers_past_fp32(lib):
+    """Numbers that are infinite in fp32, which the step is taken in, are refused."""
+    from moe_deferred_finalize_gb300._train import AdamWConfig, AdamWTensor
+    t = (AdamWTensor * 1)(AdamWTensor(param=A, grad=A, exp_avg=A, exp_avg_sq=A, n=0))
+    c = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1, state_bits=32)
+    for k in ("lr", "eps", "weight_decay"):
+        for v, want in ((3.4e38, OK), (3.5e38, E_ARG), (1e300, E_ARG)):
+            config = AdamWConfig(**{**c, k: v})
+            assert lib.moe_adamw_step(t, 1, ctypes.byref(config), NULL) == want, (k, v)
+
+
 # ---------------------------------------------------------------- binding
 
 
