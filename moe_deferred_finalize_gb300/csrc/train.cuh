@@ -36,7 +36,7 @@ struct Unpermute {
     const uint16_t *rows;
     int64_t P;
     const int32_t *idx;
-    const uint16_t *add[2];             // null from the first missing one on
+    const uint16_t *add[2];             // each may be null
     uint16_t *out;
     int T, K, H;
 };

@@ -253,6 +253,17 @@ def test_unpermute(cuda_lib, T, K, E, H, tile, adds, absent, off):
         T_.check(got, ref, "in place")
 
 
+@pytest.mark.parametrize("H", [64, 33])
+def test_unpermute_second_addend_alone(cuda_lib, H):
+    """Either addend may be missing."""
+    mf, g = cuda_lib, gen(H)
+    _, m = routing(mf, g, 20, 3, 8, 4, absent=0.2)
+    rows, add = poisoned(g, m, m["row_token"].numel(), H), normal(g, 20, H)
+    ref = T_.unpermute(rows, m["idx_map"], [add])
+    for adds in ((None, add), (add, None)):
+        T_.check(mf.unpermute_tokens(rows, m["idx_map"], add=adds), ref, "out")
+
+
 def test_unpermute_indices_outside(cuda_lib):
     """Row numbers outside [0, P), the extremes among them, add nothing."""
     mf = cuda_lib
