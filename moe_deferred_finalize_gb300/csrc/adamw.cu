@@ -7,7 +7,7 @@
 // parameters, so that nothing is copied or kept between calls.  256 values are also
 // what an 8-bit state's scale is for, so a warp has a scale's values to itself and
 // finds the largest by shuffles.  396M values: 1.56 ms with fp32 states and master
-// weights (7.1 TB/s), 1.02 ms with 8-bit states (6.3 TB/s; their 75 instructions a
+// weights (7.1 TB/s), 1.03 ms with 8-bit states (6.2 TB/s; their 75 instructions a
 // value keep the SMs' issue two thirds busy).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -20,8 +20,8 @@ namespace moef {
 namespace {
 
 constexpr int kPiece = 256;             // values a warp takes at a time
-constexpr int kAdamThreads = 128;       // 256: 8-bit states 1.06 ms, 512: 1.20
-constexpr int kEightCtas = 12;          // of an SM, with 8-bit states: 10 1.05 ms, 14 1.07
+constexpr int kAdamThreads = 128;       // 8-bit states 1.03 ms, with 256 4 % more, with 512 18 %
+constexpr int kEightCtas = 12;          // of an SM, with 8-bit states: 10 take 3 % more, 14 5 %
 constexpr int kPerCta = kAdamThreads / 32;
 constexpr float kE4m3Max = 448.f, kE4m3Least = 0.001953125f;    // 2^-9
 constexpr int kFewTensors = 48, kManyTensors = 256;             // of a launch
