@@ -7,7 +7,7 @@
 // parameters, so that nothing is copied or kept between calls.  256 values are also
 // what an 8-bit state's scale is for, so a warp has a scale's values to itself and
 // finds the largest by shuffles.  396M values: 1.56 ms with fp32 states and master
-// weights (7.1 TB/s), 1.03 ms with 8-bit states (6.2 TB/s; their 75 instructions a
+// weights (7.1 TB/s), 1.04 ms with 8-bit states (6.1 TB/s; their 75 instructions a
 // value keep the SMs' issue two thirds busy).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -20,7 +20,7 @@ namespace moef {
 namespace {
 
 constexpr int kPiece = 256;             // values a warp takes at a time
-constexpr int kAdamThreads = 128;       // 8-bit states 1.03 ms, with 256 4 % more, with 512 18 %
+constexpr int kAdamThreads = 128;       // 8-bit states 1.04 ms, with 256 4 % more, with 512 18 %
 constexpr int kEightCtas = 12;          // of an SM, with 8-bit states: 10 take 3 % more, 14 5 %
 constexpr int kPerCta = kAdamThreads / 32;
 constexpr float kE4m3Max = 448.f, kE4m3Least = 0.001953125f;    // 2^-9
@@ -125,21 +125,31 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[8]) {
 // method on its residual, which an fma gives exactly (P. Markstein, IBM J. Res. Dev.
 // 34, 1990; the quotient needs y's reciprocal rounded to nearest).  Three and five
 // instructions where the library's functions take about ten each, which 8-bit states
-// are bound by otherwise.  The root is of 2^-126 <= x < 2^127: below that range neither
-// the approximation nor the residual is one.
+// are bound by otherwise.  The root is of 0 and of 2^-126 <= x < 2^127: below that range
+// neither the approximation nor the residual is one.
 __device__ __forceinline__ float rounded_quotient(float x, float y, float reciprocal) {
     const float q = x * reciprocal;
     return fmaf(fmaf(-q, y, x), reciprocal, q);
 }
 __device__ __forceinline__ float rounded_sqrt(float x) {
     float r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(x, 1.17549435e-38f)));      // 0: 0 r
     const float s = x * r;
     return fmaf(fmaf(-s, s, x), 0.5f * r, s);
 }
-__device__ __forceinline__ bool has_rounded_sqrt(float x) {
-    return __float_as_uint(x) - 0x00800000u < 0x7F000000u - 0x00800000u;
-}
+// Which of a lane's values these are, by the least and the largest of their patterns (the
+// least of pattern - 1: 0 is not below the range).  Comparisons of each value take 5 %
+// more time; zeros left to the library's root, 5 to 10 % more where there are any.
+struct RootRange {
+    uint32_t least = 0xFFFFFFFFu, largest = 0;
+    __device__ __forceinline__ void add(float x) {
+        least = min(least, __float_as_uint(x) - 1u);
+        largest = max(largest, __float_as_uint(x));
+    }
+    __device__ __forceinline__ bool usual() const {
+        return least >= 0x00800000u - 1u && largest < 0x7F000000u;
+    }
+};
 // The largest root that is stored, 2^64 (1 - 2^-20): its code and scale give a value
 // whose square is finite, so a v that passed the largest number decays again.
 constexpr float kMostRoot = 0x1.ffffep63f;
@@ -245,19 +255,20 @@ adamw_kernel(const __grid_constant__ Table<N> table, const __grid_constant__ Ada
             load8(static_cast<const float *>(t.exp_avg) + i, m, left, whole);
             load8(static_cast<const float *>(t.exp_avg_sq) + i, v, left, whole);
         }
-        bool usual = true;
+        RootRange range;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             g[k] *= grad_scale;
             m[k] = fmaf(f.rest1, g[k], __fmul_rn(f.beta1, m[k]));
             v[k] = fmaf(f.rest2, __fmul_rn(g[k], g[k]), __fmul_rn(f.beta2, v[k]));
-            usual = usual && has_rounded_sqrt(v[k]);
+            range.add(v[k]);
         }
+        const bool usual = range.usual();
         if constexpr (EIGHT) {          // v becomes its root
             if (usual) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = rounded_sqrt(v[k]);
-            } else {                    // 0, below the normal range, past the largest number, NaN
+            } else {                    // below the normal range, near or past its end, NaN
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = sqrtf(v[k]);
             }
