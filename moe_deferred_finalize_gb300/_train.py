@@ -692,7 +692,7 @@ def adamw_state(params: Sequence[torch.Tensor], bits: int = 32, master: bool = F
 
     res = {"exp_avg": [zeros(p) for p in params], "exp_avg_sq": [zeros(p) for p in params]}
     if master:
-        res["masters"] = [p.float() for p in params]
+        res["masters"] = [p.detach().to(torch.float32, copy=True) for p in params]
     if bits == 8:
         for name in ("exp_avg_scale", "exp_avg_sq_scale"):
             res[name] = [torch.zeros(-(-p.numel() // BLOCK), device=p.device) for p in params]

@@ -271,6 +271,16 @@ def test_adamw_state_on_the_host():
     assert set(s) == {"exp_avg", "exp_avg_sq"} and not s["exp_avg"][0].any()
 
 
+def test_adamw_masters_are_copies_of_their_own():
+    """Of parameters that record gradients too: numbers, not part of a graph."""
+    import moe_deferred_finalize_gb300 as mf
+    for dtype in (BF16, F32):
+        p = torch.nn.Parameter(torch.arange(6, dtype=dtype).view(2, 3))
+        m = mf.adamw_state([p], master=True)["masters"][0]
+        assert m.dtype == F32 and torch.equal(m, p.detach().float())
+        assert not m.requires_grad and m.data_ptr() != p.data_ptr()
+
+
 # ---------------------------------------------------------- given streams
 
 CURRENT, OTHER = 0x70, 0x90     # stream handles
